@@ -438,6 +438,157 @@ size_t harts_attn_bwd_workspace_bytes(const harts_plan *plan, int32_t H);
  * workspace) and HARTS_ESMALLBUF (workspace). */
 int harts_attn_bwd(const harts_plan *plan, const harts_attn_bwd_args *args, harts_stream_t stream);
 
+/* ------------------------------------------------------------------------------ */
+/* Root-mean-square norm with the residual's addition.                            */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * Per compact row (the rows of every layer's norm, and of the one before the vocabulary
+ * projection):
+ *   h = x + residual,  rstd = 1 / sqrt(mean_j h_j^2 + eps),  y_j = h_j rstd weight_j.
+ * h is normalised in fp32 before it is rounded to `dtype` for the residual stream.  The
+ * 8-bit output holds y as e4m3 values with one power-of-two scale (e8m0: 2^(byte - 127))
+ * per 32 channels, the smallest that keeps the block within 448; a block that holds an
+ * infinity gets scale 255 (NaN), a NaN stays one.  h may be x or residual, and y may be x
+ * (rows are read before they are written).
+ */
+typedef struct {
+    int64_t C;               /* rows, >= 0 */
+    int32_t D;               /* channels, 1 .. 16384 */
+    int32_t dtype;           /* harts_dtype of x, residual, h, y */
+    float eps;               /* >= 0 */
+    const void *x;           /* device [C][D], 16-byte aligned (so are residual, h, y, y8) */
+    const void *residual;    /* device [C][D], or NULL */
+    const float *weight;     /* device [D] fp32 */
+    void *h;                 /* device [C][D] output, x + residual; required with a residual,
+                                NULL allowed without */
+    void *y;                 /* device [C][D] output, or NULL */
+    void *y8;                /* device [C][D] e4m3 output, or NULL; D a multiple of 32 */
+    void *y8_scale;          /* device [C][D/32] e8m0 output, given exactly when y8 is */
+    float *rstd;             /* device [C] output, or NULL */
+} harts_rmsnorm_fwd_args;
+
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, no output, negative C, eps),
+ * HARTS_EUNSUPPORTED (dtype, D above 16384, y8 with D not a multiple of 32), HARTS_ECUDA. */
+int harts_rmsnorm_fwd(const harts_rmsnorm_fwd_args *args, harts_stream_t stream);
+
+typedef struct {
+    int64_t C;
+    int32_t D;
+    int32_t dtype;           /* harts_dtype of dy, h, dh, dx */
+    const void *dy;          /* device [C][D] dL/dy, 16-byte aligned (so are h, dh, dx) */
+    const void *h;           /* device [C][D] as the forward wrote it (x where it had no residual) */
+    const void *dh;          /* device [C][D] dL/dh along the residual stream, or NULL */
+    const float *weight;     /* device [D] fp32 */
+    const float *rstd;       /* device [C] from the forward */
+    void *dx;                /* device [C][D] output: dL/dx = dL/dresidual; may be dy or dh */
+    float *dweight;          /* device [D] output (overwritten; zero when C is 0) */
+    void *workspace;         /* device, harts_rmsnorm_bwd_workspace_bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} harts_rmsnorm_bwd_args;
+
+/* Workspace of harts_rmsnorm_bwd: fp32 column sums; 0 for invalid arguments. */
+size_t harts_rmsnorm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype);
+
+/* Backward.  dweight is summed in a fixed order (no atomics).  Errors as the forward, plus
+ * HARTS_ESMALLBUF (workspace). */
+int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *args, harts_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
+/* The gradients' global norm, and clipping.                                      */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * norm = sqrt(sum over all tensors of the squares of their values);
+ * out_i = g_i * (norm > max_norm ? max_norm / norm : 1).
+ * Squares are summed in fp32 within a block's chunks and in fp64 above that, in a fixed
+ * order (no atomics); squares that overflow fp32 are summed again in fp64.  When the norm is
+ * not finite the gradients are passed on unscaled, and the caller sees it in *norm.
+ */
+typedef struct {
+    const void *g;           /* device [n] values, aligned to their type */
+    void *out;               /* device [n] output of harts_grad_clip; g itself (with the same
+                                dtype) scales in place; not read by harts_grad_norm */
+    int64_t n;               /* values, >= 0 (0: pointers are not looked at) */
+    int32_t dtype;           /* harts_dtype of g */
+    int32_t out_dtype;       /* harts_dtype of out */
+} harts_grad_tensor;
+
+/* Workspace for `count` tensors: fp64 partial sums; 0 for invalid arguments. */
+size_t harts_grad_workspace_bytes(int32_t count);
+
+/* tensors: host array of `count` >= 0 descriptors, read before the call returns.
+ * norm: device [1] fp32 output.  workspace: device, 16-byte aligned.
+ * Errors: HARTS_EINVAL (NULL / misaligned pointers, negative sizes, max_norm negative or
+ * NaN, in place with two dtypes), HARTS_EUNSUPPORTED (dtype), HARTS_EOVERFLOW (more than
+ * 2^44 values), HARTS_ESMALLBUF (workspace), HARTS_ECUDA. */
+int harts_grad_norm(const harts_grad_tensor *tensors, int32_t count, float *norm, void *workspace,
+                    size_t workspace_bytes, harts_stream_t stream);
+int harts_grad_clip(const harts_grad_tensor *tensors, int32_t count, float max_norm, float *norm, void *workspace,
+                    size_t workspace_bytes, harts_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
+/* Log-probabilities from hidden rows and the vocabulary weight.                  */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * harts_logprob_* with the vocabulary projection inside: the logits
+ *   z[c][v] = scale * (x[c] . weight[v])
+ * exist tile by tile only.  lse[c] = log sum_v e^z[c][v] and
+ *   logp[s] = z[c(s)][target[s]] - lse[c(s)]
+ * for the same semantic positions (row_ptr, row_sem, target).  A position whose target lies
+ * outside 0 .. V-1 has no label: logp 0, and its dlogp is not used.
+ *   dx[c] = scale sum_v dz[c][v] weight[v],   dweight[v] = scale sum_c dz[c][v] x[c],
+ *   dz[c][v] = sum_{s -> c, target[s] = v} dlogp[s] - (sum_{s -> c} dlogp[s]) e^(z[c][v] - lse[c]).
+ * The backward forms the logits again, one piece of the vocabulary at a time, and holds that
+ * piece's dz in bf16 (each entry formed in fp32 and rounded once); all sums are fp32 and in a
+ * fixed order.  x and weight must be finite: dweight sums over every row, also over rows
+ * without positions (whose dx is zero).
+ */
+typedef struct {
+    int64_t C;               /* compact rows, >= 0 */
+    int32_t V;               /* vocabulary, >= 1 (any) */
+    int32_t D;               /* width of the hidden rows, a multiple of 8 */
+    int32_t dtype;           /* harts_dtype of x, weight, dx, dweight: HARTS_BF16 */
+    float scale;             /* of the logits (1 / temperature), finite */
+    int64_t S;               /* semantic positions, < 2^31 */
+    const void *x;           /* device [C][D], 16-byte aligned */
+    const void *weight;      /* device [V][D], 16-byte aligned */
+    const int32_t *row_ptr;  /* device [C+1]: semantic positions of row c are row_sem[row_ptr[c] ..] */
+    const int32_t *row_sem;  /* device [S] */
+    const int32_t *target;   /* device [S] label of each semantic position */
+    float *lse;              /* device [C]: written by the forward, read by the backward */
+    float *logp;             /* device [S]: written by the forward */
+    int32_t *error;          /* device [1], or NULL: set to 3 if a bounded wait ran out (the
+                                outputs are then incomplete); cleared by the caller */
+    void *workspace;         /* device, harts_linear_logprob_{fwd,bwd}_workspace_bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} harts_linear_logprob_fwd_args;
+
+/* Workspace of the forward: a (max, sum) pair per row and tile; 0 for invalid arguments. */
+size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D);
+
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, scale not finite),
+ * HARTS_EUNSUPPORTED (dtype other than bf16, D not a multiple of 8), HARTS_EOVERFLOW (C, V or
+ * S), HARTS_ESMALLBUF (workspace), HARTS_ECUDA. */
+int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *args, harts_stream_t stream);
+
+typedef struct {
+    harts_linear_logprob_fwd_args fwd;  /* lse as written by the forward; logp unused */
+    const float *dlogp;      /* device [S] dL/dlogp */
+    void *dx;                /* device [C][D] bf16 output (overwritten), 16-byte aligned */
+    void *dweight;           /* device [V][D] bf16 output (overwritten), 16-byte aligned */
+    int32_t piece;           /* vocabulary entries held at a time (rounded down to a multiple of
+                                256, at least 256), or 0: as many as make dz 512 MiB */
+} harts_linear_logprob_bwd_args;
+
+/* Workspace of the backward for a given piece (0: the library's choice); 0 for invalid
+ * arguments.  About 2 C piece bytes of dz, and fp32 sums of dx. */
+size_t harts_linear_logprob_bwd_workspace_bytes(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece);
+
+/* Errors as the forward. */
+int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *args, harts_stream_t stream);
+
 /* Message for the last error on the calling thread ("" if none). */
 const char *harts_last_error(void);
 

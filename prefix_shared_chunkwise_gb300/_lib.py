@@ -26,7 +26,11 @@ EXPORTED = [
     "harts_kda_bwd", "harts_kda_bwd_state", "harts_kda_bwd_grad", "harts_kda_bwd_static",
     "harts_kda_bwd_static_max_bytes", "harts_conv_fwd", "harts_conv_bwd_workspace_bytes",
     "harts_conv_bwd", "harts_plan_semantic_map", "harts_logprob_fwd", "harts_logprob_bwd",
-    "harts_attn_fwd", "harts_attn_bwd_workspace_bytes", "harts_attn_bwd", "harts_last_error",
+    "harts_attn_fwd", "harts_attn_bwd_workspace_bytes", "harts_attn_bwd",
+    "harts_rmsnorm_fwd", "harts_rmsnorm_bwd_workspace_bytes", "harts_rmsnorm_bwd",
+    "harts_grad_workspace_bytes", "harts_grad_norm", "harts_grad_clip",
+    "harts_linear_logprob_fwd_workspace_bytes", "harts_linear_logprob_fwd",
+    "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_last_error",
 ]
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
@@ -100,6 +104,34 @@ class AttnBwdArgs(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class RmsnormFwdArgs(ctypes.Structure):
+    _fields_ = [("C", _i64), ("D", _i32), ("dtype", _i32), ("eps", ctypes.c_float), ("x", _vp),
+                ("residual", _vp), ("weight", _vp), ("h", _vp), ("y", _vp), ("y8", _vp),
+                ("y8_scale", _vp), ("rstd", _vp)]
+
+
+class RmsnormBwdArgs(ctypes.Structure):
+    _fields_ = [("C", _i64), ("D", _i32), ("dtype", _i32), ("dy", _vp), ("h", _vp), ("dh", _vp),
+                ("weight", _vp), ("rstd", _vp), ("dx", _vp), ("dweight", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("g", _vp), ("out", _vp), ("n", _i64), ("dtype", _i32), ("out_dtype", _i32)]
+
+
+class LinearLogprobFwdArgs(ctypes.Structure):
+    _fields_ = [("C", _i64), ("V", _i32), ("D", _i32), ("dtype", _i32), ("scale", ctypes.c_float),
+                ("S", _i64), ("x", _vp), ("weight", _vp), ("row_ptr", _vp), ("row_sem", _vp),
+                ("target", _vp), ("lse", _vp), ("logp", _vp), ("error", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class LinearLogprobBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", LinearLogprobFwdArgs), ("dlogp", _vp), ("dx", _vp), ("dweight", _vp),
+                ("piece", _i32)]
+
+
 _lib = None
 
 
@@ -151,6 +183,27 @@ def lib():
         L.harts_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.harts_attn_bwd.argtypes = [_vp, ctypes.POINTER(AttnBwdArgs), _vp]
         L.harts_attn_bwd.restype = ctypes.c_int
+        _sz = ctypes.c_size_t
+        L.harts_rmsnorm_fwd.argtypes = [ctypes.POINTER(RmsnormFwdArgs), _vp]
+        L.harts_rmsnorm_fwd.restype = ctypes.c_int
+        L.harts_rmsnorm_bwd_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.harts_rmsnorm_bwd_workspace_bytes.restype = _sz
+        L.harts_rmsnorm_bwd.argtypes = [ctypes.POINTER(RmsnormBwdArgs), _vp]
+        L.harts_rmsnorm_bwd.restype = ctypes.c_int
+        L.harts_grad_workspace_bytes.argtypes = [_i32]
+        L.harts_grad_workspace_bytes.restype = _sz
+        L.harts_grad_norm.argtypes = [ctypes.POINTER(GradTensor), _i32, _vp, _vp, _sz, _vp]
+        L.harts_grad_norm.restype = ctypes.c_int
+        L.harts_grad_clip.argtypes = [ctypes.POINTER(GradTensor), _i32, ctypes.c_float, _vp, _vp, _sz, _vp]
+        L.harts_grad_clip.restype = ctypes.c_int
+        L.harts_linear_logprob_fwd_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.harts_linear_logprob_fwd_workspace_bytes.restype = _sz
+        L.harts_linear_logprob_fwd.argtypes = [ctypes.POINTER(LinearLogprobFwdArgs), _vp]
+        L.harts_linear_logprob_fwd.restype = ctypes.c_int
+        L.harts_linear_logprob_bwd_workspace_bytes.argtypes = [_i64, _i32, _i32, _i64, _i32]
+        L.harts_linear_logprob_bwd_workspace_bytes.restype = _sz
+        L.harts_linear_logprob_bwd.argtypes = [ctypes.POINTER(LinearLogprobBwdArgs), _vp]
+        L.harts_linear_logprob_bwd.restype = ctypes.c_int
         L.harts_last_error.argtypes = []
         L.harts_last_error.restype = ctypes.c_char_p
         for fn in ("harts_plan_calls", "harts_plan_get_info", "harts_plan_export",

@@ -10,7 +10,8 @@ import numpy as np
 from . import _lib as L
 
 __all__ = ["Plan", "kda_fwd", "kda_bwd", "conv_fwd", "conv_bwd", "semantic_map", "logprob_fwd",
-           "logprob_bwd", "dtype_code"]
+           "logprob_bwd", "attn_fwd", "attn_bwd", "linear_logprob_fwd", "linear_logprob_bwd",
+           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "dtype_code"]
 
 
 def dtype_code(torch_dtype):
@@ -347,3 +348,212 @@ def attn_bwd(plan: Plan, q, k, v, o, lse, d_o, *, scale=None, dq=None, dk=None, 
     b.workspace, b.workspace_bytes = workspace.data_ptr(), workspace.numel()
     L.check(L.lib().harts_attn_bwd(plan.handle, ctypes.byref(b), _stream(stream)), "harts_attn_bwd")
     return dq, dk, dv
+
+
+def _row_stream(stream, device):
+    """The stream to enqueue on: the given one, or the current one of `device`."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _ready(name, t, shape, dtype, device):
+    """_need, and contiguous: what every buffer of the operators below has to be."""
+    _need(name, t, shape, dtype, None, device)
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None, rstd=None, stream=None):
+    """harts_rmsnorm_fwd: h = x + residual, y = h / sqrt(mean h^2 + eps) * weight per row.
+    x, residual: [C, D] bf16 or fp32; weight: [D] fp32.  Returns (y, h, rstd [C] fp32); h is
+    x itself where there is no residual.  mx8=True returns y as (values [C, D] float8_e4m3fn,
+    scales [C, D/32] float8_e8m0fnu) instead; D is then a multiple of 32.  h may be given as
+    x or residual (in place)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [C, D]")
+    C, D = x.shape
+    dev, f32 = x.device, torch.float32
+    a = L.RmsnormFwdArgs()
+    a.C, a.D, a.dtype, a.eps = C, D, dtype_code(x.dtype), eps
+    _ready("x", x, (C, D), x.dtype, dev)
+    _ready("weight", weight, (D,), f32, dev)
+    _ready("residual", residual, (C, D), x.dtype, dev)
+    if mx8:
+        if D % 32:
+            raise ValueError("mx8 needs D a multiple of 32")
+        if y is None:
+            y = (torch.empty((C, D), dtype=torch.float8_e4m3fn, device=dev),
+                 torch.empty((C, D // 32), dtype=torch.float8_e8m0fnu, device=dev))
+        _ready("y values", y[0], (C, D), torch.float8_e4m3fn, dev)
+        _ready("y scales", y[1], (C, D // 32), torch.float8_e8m0fnu, dev)
+        a.y8, a.y8_scale = y[0].data_ptr(), y[1].data_ptr()
+    else:
+        if y is None:
+            y = torch.empty_like(x)
+        _ready("y", y, (C, D), x.dtype, dev)
+        a.y = y.data_ptr()
+    if residual is not None:
+        if h is None:
+            h = torch.empty_like(x)
+        _ready("h", h, (C, D), x.dtype, dev)
+        a.residual, a.h = residual.data_ptr(), h.data_ptr()
+    else:
+        h = x
+    if rstd is None:
+        rstd = torch.empty(C, dtype=f32, device=dev)
+    _ready("rstd", rstd, (C,), f32, dev)
+    a.x, a.weight, a.rstd = x.data_ptr(), weight.data_ptr(), rstd.data_ptr()
+    L.check(L.lib().harts_rmsnorm_fwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_rmsnorm_fwd")
+    return y, h, rstd
+
+
+def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, workspace=None, stream=None):
+    """harts_rmsnorm_bwd: from dL/dy, the forward's h and rstd, and dL/dh along the residual
+    stream (or None).  Returns (dx [C, D] like h: the gradient of x and of the residual;
+    dweight [D] fp32)."""
+    import torch
+    if h.dim() != 2:
+        raise ValueError(f"h has shape {tuple(h.shape)}, expected [C, D]")
+    C, D = h.shape
+    dev, f32 = h.device, torch.float32
+    if dx is None:
+        dx = torch.empty_like(h)
+    if dweight is None:
+        dweight = torch.empty(D, dtype=f32, device=dev)
+    for n, t in (("dy", dy), ("h", h), ("dh", dh), ("dx", dx)):
+        _ready(n, t, (C, D), h.dtype, dev)
+    _ready("weight", weight, (D,), f32, dev)
+    _ready("rstd", rstd, (C,), f32, dev)
+    _ready("dweight", dweight, (D,), f32, dev)
+    a = L.RmsnormBwdArgs()
+    a.C, a.D, a.dtype = C, D, dtype_code(h.dtype)
+    nb = int(L.lib().harts_rmsnorm_bwd_workspace_bytes(C, D, a.dtype))
+    if workspace is None:
+        workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=dev)
+    _need("workspace", workspace, nbytes=nb, device=dev)
+    a.dy, a.h, a.dh = dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr()
+    a.weight, a.rstd, a.dx, a.dweight = weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr()
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    L.check(L.lib().harts_rmsnorm_bwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_rmsnorm_bwd")
+    return dx, dweight
+
+
+class GradSet:
+    """harts_grad_norm / harts_grad_clip over a fixed list of gradient buffers (bf16 or fp32,
+    contiguous, one device).  The buffers and their addresses are taken once; their values are
+    read at every call.  outs: where clip() writes (same shapes, bf16 or fp32), None: in place."""
+
+    def __init__(self, grads, outs=None):
+        import torch
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
+        self.grads, self.outs = grads, outs
+        self._dev = grads[0].device if grads else torch.empty(0, device="cuda").device
+        self._list = (L.GradTensor * max(len(grads), 1))()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            _ready(f"gradient {i}", g, None, None, self._dev)
+            _ready(f"output {i}", o, tuple(g.shape), None, self._dev)
+            t = self._list[i]
+            t.g, t.out, t.n = g.data_ptr(), o.data_ptr(), g.numel()
+            t.dtype, t.out_dtype = dtype_code(g.dtype), dtype_code(o.dtype)
+        nb = int(L.lib().harts_grad_workspace_bytes(len(grads)))
+        self._ws = torch.empty(nb, dtype=torch.uint8, device=self._dev)
+
+    def norm(self, *, norm=None, stream=None):
+        """The global 2-norm, a 0-dim fp32 tensor."""
+        import torch
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self._dev)
+        _need("norm", norm, None, torch.float32, 4, self._dev)
+        L.check(L.lib().harts_grad_norm(self._list, len(self.grads), norm.data_ptr(), self._ws.data_ptr(),
+                                        self._ws.numel(), _row_stream(stream, self._dev)), "harts_grad_norm")
+        return norm
+
+    def clip(self, max_norm, *, norm=None, stream=None):
+        """outs = grads * min(1, max_norm / norm); returns the norm before clipping."""
+        import torch
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self._dev)
+        _need("norm", norm, None, torch.float32, 4, self._dev)
+        L.check(L.lib().harts_grad_clip(self._list, len(self.grads), float(max_norm), norm.data_ptr(),
+                                        self._ws.data_ptr(), self._ws.numel(), _row_stream(stream, self._dev)),
+                "harts_grad_clip")
+        return norm
+
+
+def _head_args(x, weight, row_ptr, row_sem, target, scale, lse, logp, error):
+    import torch
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x and weight must be [C, D] and [V, D]")
+    (C, D), V, S, dev, i32 = x.shape, weight.shape[0], target.numel(), x.device, torch.int32
+    _ready("x", x, None, None, dev)
+    _ready("weight", weight, (V, D), x.dtype, dev)
+    _ready("row_ptr", row_ptr, (C + 1,), i32, dev)
+    _ready("row_sem", row_sem, (S,), i32, dev)
+    _ready("target", target, (S,), i32, dev)
+    _ready("lse", lse, (C,), torch.float32, dev)
+    _ready("logp", logp, (S,), torch.float32, dev)
+    _need("error", error, None, i32, 4, dev)
+    a = L.LinearLogprobFwdArgs()
+    a.C, a.V, a.D, a.S, a.dtype, a.scale = C, V, D, S, dtype_code(x.dtype), scale
+    a.x, a.weight, a.row_ptr = x.data_ptr(), weight.data_ptr(), row_ptr.data_ptr()
+    a.row_sem, a.target, a.lse = row_sem.data_ptr(), target.data_ptr(), lse.data_ptr()
+    a.logp = None if logp is None else logp.data_ptr()
+    a.error = None if error is None else error.data_ptr()
+    return a
+
+
+def _head_workspace(workspace, nb, dev):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _need("workspace", workspace, nbytes=nb, device=dev)
+    return workspace
+
+
+def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=None, logp=None, error=None,
+                       workspace=None, stream=None):
+    """harts_linear_logprob_fwd: log-probabilities of the semantic positions from hidden rows
+    x [C, D] and the vocabulary weight [V, D] (bf16), without forming the logits in memory.
+    A target outside 0 .. V-1 has no label (logp 0).  Returns (logp [S] fp32, lse [C] fp32).
+    error: int32 device tensor that a bounded wait which ran out sets to 3."""
+    import torch
+    dev = x.device
+    if lse is None:
+        lse = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
+    if logp is None:
+        logp = torch.empty(target.numel(), dtype=torch.float32, device=dev)
+    a = _head_args(x, weight, row_ptr, row_sem, target, scale, lse, logp, error)
+    workspace = _head_workspace(workspace, int(L.lib().harts_linear_logprob_fwd_workspace_bytes(a.C, a.V, a.D)), dev)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    L.check(L.lib().harts_linear_logprob_fwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_linear_logprob_fwd")
+    return logp, lse
+
+
+def linear_logprob_bwd(x, weight, row_ptr, row_sem, target, lse, dlogp, *, scale=1.0, dx=None, dweight=None,
+                       piece=0, error=None, workspace=None, stream=None):
+    """harts_linear_logprob_bwd: returns (dx like x, dweight like weight) from the forward's lse
+    and dL/dlogp [S] fp32.  piece: vocabulary entries whose logit gradients are held at a time
+    (0: the library's choice)."""
+    import torch
+    dev = x.device
+    a = L.LinearLogprobBwdArgs()
+    a.fwd = _head_args(x, weight, row_ptr, row_sem, target, scale, lse, None, error)
+    f = a.fwd
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dweight is None:
+        dweight = torch.empty_like(weight)
+    _ready("dx", dx, tuple(x.shape), x.dtype, dev)
+    _ready("dweight", dweight, tuple(weight.shape), x.dtype, dev)
+    _ready("dlogp", dlogp, (f.S,), torch.float32, dev)
+    a.dlogp, a.dx, a.dweight, a.piece = dlogp.data_ptr(), dx.data_ptr(), dweight.data_ptr(), piece
+    nb = int(L.lib().harts_linear_logprob_bwd_workspace_bytes(f.C, f.V, f.D, f.S, max(piece, 0)))
+    workspace = _head_workspace(workspace, nb, dev)
+    a.fwd.workspace, a.fwd.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    L.check(L.lib().harts_linear_logprob_bwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_linear_logprob_bwd")
+    return dx, dweight

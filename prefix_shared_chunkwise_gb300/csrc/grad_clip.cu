@@ -1,0 +1,357 @@
+// The global norm of many gradient tensors, and clipping by it.
+//
+//   n = sqrt(sum_i sum_j g_ij^2),   out_i = g_i * (n > max_norm ? max_norm / n : 1)
+// Two kernels over the same chunks of all tensors: squares (each block leaves one fp64
+// partial sum), then the scaling, whose blocks each add up the partials in the same fixed
+// order -- a few kilobytes from L2 -- so that the norm needs neither atomics nor a launch of
+// its own.  The scaling walks the chunks backwards: what the first kernel read last is still
+// in L2.  Both kernels only stream: HBM bounds them, two reads and one write of every value
+// for sets larger than L2, one read and one write below that.
+//
+// Squares are summed in fp32 over one block's chunks (16 or so per accumulator and chunk)
+// and in fp64 across threads and blocks.  A block whose fp32 sum is not finite reads its chunks again in
+// fp64: squares overflow fp32 from 1.8e19 on, which bf16 and fp32 values reach.  If the norm
+// itself is not finite the gradients pass through unscaled; the caller sees it in the norm.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "plan_internal.h"
+
+namespace harts {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSet = 512;                   // tensors a launch carries in its parameters
+constexpr int64_t kMaxChunk = 16384;        // values
+constexpr int64_t kMinChunk = 2048;
+constexpr int kPerSm = 4;                   // resident blocks
+
+struct Item {
+    const void *g;
+    void *out;
+    int64_t n;
+    int32_t chunk0;                         // first chunk of the tensor within the launch
+    int32_t kinds;                          // bit 0: g is bf16, bit 1: out is bf16
+};
+
+struct Set {
+    Item item[kSet];
+    int32_t count, chunks, chunk, partials;
+    int32_t first;                          // index of the launch's first partial
+    float max_norm;
+    float *norm;
+    double *part;
+};
+
+__device__ __forceinline__ int find(const Set &s, int32_t c) {
+    int lo = 0, hi = s.count - 1;           // last item whose chunk0 <= c
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (s.item[m].chunk0 <= c) lo = m; else hi = m - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float get(const float *p) { return *p; }
+__device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <typename T> struct Pack { static constexpr int n = 16 / sizeof(T); };
+
+__device__ __forceinline__ void expand(uint4 u, float (&v)[8], const __nv_bfloat16 *) {
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { const float2 f = __bfloat1622float2(p[i]); v[2 * i] = f.x; v[2 * i + 1] = f.y; }
+}
+__device__ __forceinline__ void expand(uint4 u, float (&v)[4], const float *) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+}
+template <int N>
+__device__ __forceinline__ void store_pack(__nv_bfloat16 *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) reinterpret_cast<__nv_bfloat162 *>(p)[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void store_pack(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint4 u;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = u;
+}
+__device__ __forceinline__ void store_pack(__nv_bfloat16 *p, const float (&v)[4]) {
+    uint2 u;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+    h[0] = __floats2bfloat162_rn(v[0], v[1]); h[1] = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) = u;
+}
+template <int N>
+__device__ __forceinline__ void store_pack(float *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// Values before the first 16-byte boundary at or after p.
+template <typename T>
+__device__ __forceinline__ int64_t head_of(const T *p, int64_t n) {
+    const int64_t h = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / static_cast<int64_t>(sizeof(T));
+    return h < n ? h : n;
+}
+
+template <typename T>
+__device__ float squares(const T *g, int64_t n) {
+    constexpr int N = Pack<T>::n;
+    const int t = threadIdx.x;
+    const int64_t head = head_of(g, n);
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    if (t < head) { const float v = get(g + t); s0 = v * v; }
+    const uint4 *q = reinterpret_cast<const uint4 *>(g + head);
+    const int64_t nv = (n - head) / N;
+    for (int64_t i = t; i < nv; i += 4 * kThreads) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            u[k] = i + k * kThreads < nv ? __ldg(q + i + k * kThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float v[N];
+            expand(u[k], v, g);
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                s0 = fmaf(v[j], v[j], s0); s1 = fmaf(v[j + 1], v[j + 1], s1);
+                s2 = fmaf(v[j + 2], v[j + 2], s2); s3 = fmaf(v[j + 3], v[j + 3], s3);
+            }
+        }
+    }
+    const int64_t tail = head + nv * N + t;
+    if (tail < n) { const float v = get(g + tail); s1 = fmaf(v, v, s1); }
+    return (s0 + s1) + (s2 + s3);
+}
+
+template <typename T>
+__device__ double squares64(const T *g, int64_t n) {
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) { const double v = get(g + i); s = fma(v, v, s); }
+    return s;
+}
+
+// Sum over the block in a fixed order; every thread returns it.
+__device__ double block_sum(double v, double *sm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();                        // sm may still be read from an earlier sum
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) s += sm[i];
+    return s;
+}
+
+__global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __grid_constant__ Set s) {
+    __shared__ double sm[kThreads / 32];
+    double sum = 0.0;
+    for (int32_t c = blockIdx.x; c < s.chunks; c += gridDim.x) {
+        const Item &it = s.item[find(s, c)];
+        const int64_t at = static_cast<int64_t>(c - it.chunk0) * s.chunk;
+        const int64_t n = it.n - at < s.chunk ? it.n - at : s.chunk;
+        sum += it.kinds & 1 ? squares(static_cast<const __nv_bfloat16 *>(it.g) + at, n)
+                            : squares(static_cast<const float *>(it.g) + at, n);
+    }
+    sum = block_sum(sum, sm);
+    if (!isfinite(sum)) {
+        sum = 0.0;
+        for (int32_t c = blockIdx.x; c < s.chunks; c += gridDim.x) {
+            const Item &it = s.item[find(s, c)];
+            const int64_t at = static_cast<int64_t>(c - it.chunk0) * s.chunk;
+            const int64_t n = it.n - at < s.chunk ? it.n - at : s.chunk;
+            sum += it.kinds & 1 ? squares64(static_cast<const __nv_bfloat16 *>(it.g) + at, n)
+                                : squares64(static_cast<const float *>(it.g) + at, n);
+        }
+        sum = block_sum(sum, sm);
+    }
+    if (threadIdx.x == 0) s.part[s.first + blockIdx.x] = sum;
+}
+
+__device__ double total_of(const Set &s, double *sm) {
+    double v = 0.0;
+    for (int32_t i = threadIdx.x; i < s.partials; i += kThreads) v += s.part[i];
+    return block_sum(v, sm);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double *part, int32_t partials, float *norm) {
+    __shared__ double sm[kThreads / 32];
+    double v = 0.0;
+    for (int32_t i = threadIdx.x; i < partials; i += kThreads) v += part[i];
+    v = block_sum(v, sm);
+    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(v));
+}
+
+template <typename T, typename U>
+__device__ void scale(const T *g, U *out, int64_t n, float f) {
+    constexpr int N = Pack<T>::n;
+    const int t = threadIdx.x;
+    const int64_t head = head_of(g, n);
+    if (t < head) put(out + t, get(g + t) * f);
+    const uint4 *q = reinterpret_cast<const uint4 *>(g + head);
+    const int64_t nv = (n - head) / N;
+    U *o = out + head;
+    const bool whole = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+    for (int64_t i = t; i < nv; i += 4 * kThreads) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k * kThreads < nv) u[k] = q[i + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k * kThreads >= nv) break;
+            float v[N];
+            expand(u[k], v, g);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] *= f;
+            U *d = o + (i + k * kThreads) * N;
+            if (whole) {
+                store_pack(d, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) put(d + j, v[j]);
+            }
+        }
+    }
+    const int64_t tail = head + nv * N + t;
+    if (tail < n) put(out + tail, get(g + tail) * f);
+}
+
+__global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Set s) {
+    __shared__ double sm[kThreads / 32];
+    const double norm = sqrt(total_of(s, sm));
+    const float f = norm > s.max_norm && isfinite(norm) ? static_cast<float>(s.max_norm / norm) : 1.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && s.first == 0) *s.norm = static_cast<float>(norm);
+    for (int32_t c = s.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+        const Item &it = s.item[find(s, c)];
+        if (f == 1.f && it.out == it.g) continue;           // in place and nothing to scale
+        const int64_t at = static_cast<int64_t>(c - it.chunk0) * s.chunk;
+        const int64_t n = it.n - at < s.chunk ? it.n - at : s.chunk;
+        const __nv_bfloat16 *gb = static_cast<const __nv_bfloat16 *>(it.g) + at;
+        const float *gf = static_cast<const float *>(it.g) + at;
+        __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(it.out) + at;
+        float *of = static_cast<float *>(it.out) + at;
+        switch (it.kinds) {
+            case 0: scale(gf, of, n, f); break;
+            case 1: scale(gb, of, n, f); break;
+            case 2: scale(gf, ob, n, f); break;
+            default: scale(gb, ob, n, f); break;
+        }
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+// Walks the tensors in launches of up to kSet; 0 or an error code.  `sets` receives the
+// number of launches, `total` of values.
+int check(const harts_grad_tensor *t, int32_t count, bool clip, int64_t *total) {
+    if (count < 0 || (count > 0 && !t)) { set_error("count >= 0 and a tensor list required"); return HARTS_EINVAL; }
+    *total = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (t[i].n < 0) { set_error("negative length"); return HARTS_EINVAL; }
+        if (t[i].dtype != HARTS_FP32 && t[i].dtype != HARTS_BF16) { set_error("dtype"); return HARTS_EUNSUPPORTED; }
+        if (t[i].n == 0) continue;
+        if (!t[i].g || (clip && !t[i].out)) { set_error("NULL gradient or output"); return HARTS_EINVAL; }
+        const uintptr_t ga = t[i].dtype == HARTS_BF16 ? 1 : 3;
+        if (reinterpret_cast<uintptr_t>(t[i].g) & ga) { set_error("gradient not aligned to its type"); return HARTS_EINVAL; }
+        if (clip) {
+            if (t[i].out_dtype != HARTS_FP32 && t[i].out_dtype != HARTS_BF16) { set_error("output dtype"); return HARTS_EUNSUPPORTED; }
+            const uintptr_t oa = t[i].out_dtype == HARTS_BF16 ? 1 : 3;
+            if (reinterpret_cast<uintptr_t>(t[i].out) & oa) { set_error("output not aligned to its type"); return HARTS_EINVAL; }
+            if (t[i].out == t[i].g && t[i].out_dtype != t[i].dtype) { set_error("in place needs one dtype"); return HARTS_EINVAL; }
+        }
+        if (t[i].n > (int64_t(1) << 44) - *total) { set_error("more than 2^44 values"); return HARTS_EOVERFLOW; }
+        *total += t[i].n;
+    }
+    return HARTS_OK;
+}
+
+// Values of a chunk: about four chunks a resident block, within limits that keep a chunk a
+// few vectors per thread and the table search rare.
+int32_t chunk_of(int64_t total) {
+    const int64_t want = total / (int64_t(sm_count()) * kPerSm * 4);
+    int64_t c = kMinChunk;
+    while (c < want && c < kMaxChunk) c *= 2;
+    while ((total + c - 1) / c > (int64_t(1) << 30)) c *= 2;
+    return static_cast<int32_t>(c);
+}
+
+int grid_limit() { return sm_count() * kPerSm; }
+
+int run(const harts_grad_tensor *t, int32_t count, bool clip, float max_norm, float *norm, void *ws, size_t ws_bytes,
+        cudaStream_t st) {
+    int64_t total = 0;
+    const int rc = check(t, count, clip, &total);
+    if (rc) return rc;
+    if (!norm) { set_error("NULL norm"); return HARTS_EINVAL; }
+    if (clip && !(max_norm >= 0.f)) { set_error("max_norm must be >= 0"); return HARTS_EINVAL; }
+    if (!ws || ws_bytes < harts_grad_workspace_bytes(count)) { set_error("workspace too small"); return HARTS_ESMALLBUF; }
+    if (reinterpret_cast<uintptr_t>(ws) & 15) { set_error("workspace must be 16-byte aligned"); return HARTS_EINVAL; }
+    const int32_t chunk = chunk_of(total);
+    static thread_local Set s;              // 20 KB: passed by value to each launch
+    s.chunk = chunk; s.max_norm = max_norm; s.norm = norm; s.part = static_cast<double *>(ws);
+    int32_t partials = 0;
+    for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+        int32_t first = 0, i = 0;
+        do {
+            s.count = s.chunks = 0;
+            for (; i < count && s.count < kSet; ++i) {
+                if (t[i].n == 0) continue;
+                const int64_t c = (t[i].n + chunk - 1) / chunk;
+                Item &it = s.item[s.count++];
+                it.g = t[i].g; it.out = t[i].out; it.n = t[i].n; it.chunk0 = s.chunks;
+                it.kinds = (t[i].dtype == HARTS_BF16 ? 1 : 0) | (t[i].out_dtype == HARTS_BF16 ? 2 : 0);
+                s.chunks += static_cast<int32_t>(c);
+            }
+            const int grid = std::max(1, std::min(s.chunks, grid_limit()));
+            s.first = first;
+            s.partials = partials;
+            if (pass == 0) grad_squares_kernel<<<grid, kThreads, 0, st>>>(s);
+            else grad_scale_kernel<<<grid, kThreads, 0, st>>>(s);
+            first += grid;
+        } while (i < count);
+        partials = first;
+    }
+    if (!clip) grad_norm_kernel<<<1, kThreads, 0, st>>>(s.part, partials, norm);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) { set_error(std::string("gradient norm launch: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
+    set_error("");
+    return HARTS_OK;
+}
+
+}  // namespace
+}  // namespace harts
+
+using namespace harts;
+
+extern "C" {
+
+size_t harts_grad_workspace_bytes(int32_t count) {
+    if (count < 0) return 0;
+    const size_t sets = std::max(1, (count + kSet - 1) / kSet);
+    return std::max<size_t>(256, sets * grid_limit() * sizeof(double));
+}
+
+int harts_grad_norm(const harts_grad_tensor *t, int32_t count, float *norm, void *workspace, size_t workspace_bytes,
+                    harts_stream_t stream) {
+    return run(t, count, false, 0.f, norm, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int harts_grad_clip(const harts_grad_tensor *t, int32_t count, float max_norm, float *norm, void *workspace,
+                    size_t workspace_bytes, harts_stream_t stream) {
+    return run(t, count, true, max_norm, norm, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

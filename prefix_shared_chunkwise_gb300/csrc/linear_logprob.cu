@@ -1,0 +1,750 @@
+// Log-probabilities straight from the hidden rows and the vocabulary weight, forward and
+// backward, without keeping the C x V logits.
+//
+//   z[c][v] = scale x_c . w_v,  lse_c = log sum_v e^z[c][v],  logp[s] = z[c(s)][y_s] - lse_c(s)
+//   dz[c][v] = sum_{s -> c, y_s = v} g_s - G_c e^(z[c][v] - lse_c),  G_c = sum_{s -> c} g_s
+//   dx_c = scale sum_v dz[c][v] w_v,    dw_v = scale sum_c dz[c][v] x_c
+// (the compact-to-semantic form of HARTS, page "HARTS ... 精读", section 4.4 and eq. 19, with
+// the vocabulary projection taken into the operator).  Positions whose label lies outside the
+// vocabulary carry no log-probability and no gradient.
+//
+// Forward: one product X W^T whose 128 x N tiles never leave the SM.  A tile's accumulators
+// are reduced in place to one (max, sum of exponentials) per row, 8 bytes instead of N
+// logits; a small kernel joins a row's pairs, and the positions' own logits are formed by
+// dot products of the rows they name (S of them, against C V in the product).
+// Backward, over pieces of the vocabulary: the product again, its epilogue turning logits
+// into scale * dz in bf16; then dX += dZ W and dW = dZ^T X in one launch, with the same tiles.
+// dz is rounded to bf16 because the tensor cores take bf16 operands next to bf16 W and X;
+// every entry, labels' included, is formed in fp32 and rounded once.  Sums are fp32.  dX of
+// several pieces or of a split vocabulary is summed in fp32 (one buffer per split, added to
+// in piece order), so results do not depend on timing.
+//
+// Tile kernel: persistent blocks, one per SM; warp 0 fills a ring of shared-memory stages
+// by TMA, warp 1 issues tcgen05.mma into one of two 256-column accumulators in TMEM, warps
+// 4-7 empty the other one.  All waits are bounded.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "kda_common.cuh"
+#include "tc_primitives.cuh"
+#include "tensor_map.h"
+
+namespace harts {
+namespace {
+
+constexpr int kTM = 128, kTK = 64, kTN = 256;       // tile rows, K step (one 128-byte swizzle row), tile columns
+constexpr int kStages = 4;
+constexpr uint32_t kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2, kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kOutBytes = 4 * 2 * 4096;        // 4 warps x 2 slots of 32 rows x 128 bytes
+constexpr uint32_t kSmem = kStages * kStageBytes + kOutBytes + 1024;
+constexpr int kThreads = 256, kEpiWarp0 = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+enum Mode { kFwd = 0, kDz = 1, kGrad = 2 };
+
+// One product D = op(A) op(B)^T cut into tiles and splits of its K range.
+struct Prod {
+    CUtensorMap a, b, out;
+    int32_t a_mn, b_mn;             // operand stored [K][rows] instead of [rows][K]
+    int32_t a_rows;                 // rows of A's box when stored [rows][K]
+    int32_t m_tiles, n_tiles, splits, n;
+    int32_t k_blocks, k_per;        // steps of 64 in all, per split
+    int32_t b_y0, out_y0;           // row offsets of this piece of the vocabulary in B and the output
+    int32_t rows, cols;             // extent of the output (rows from out_y0 on)
+    int32_t fast_n;                 // tiles that run together share A (walk n first) instead of B
+    int32_t out_f32, out_add;
+};
+
+struct alignas(16) RowInfo { float neg_g, lse2; int32_t count, first; };   // -scale G, lse log2 e, labelled entries
+
+struct Params {
+    Prod prod[2];
+    int32_t n_prod;
+    int32_t *error;
+    float c2;                       // scale * log2 e
+    float2 *part;                   // forward: [C][n_tiles]
+    const RowInfo *rows;            // dz: per compact row
+    const int32_t *ent_y;
+    const float *ent_v;
+    int32_t v0;                     // dz: first vocabulary entry of the piece
+};
+
+struct TileId { int which, mt, nt, split; };
+
+__device__ __forceinline__ bool tile_at(const Params &p, int64_t idx, TileId &t) {
+    int which = 0;
+    int64_t items = static_cast<int64_t>(p.prod[0].m_tiles) * p.prod[0].n_tiles * p.prod[0].splits;
+    if (idx >= items) {
+        if (p.n_prod < 2) return false;
+        idx -= items;
+        which = 1;
+        items = static_cast<int64_t>(p.prod[1].m_tiles) * p.prod[1].n_tiles * p.prod[1].splits;
+        if (idx >= items) return false;
+    }
+    const Prod &q = p.prod[which];
+    const int32_t per = q.m_tiles * q.n_tiles;
+    t.which = which;
+    t.split = static_cast<int>(idx / per);
+    const int32_t r = static_cast<int32_t>(idx - static_cast<int64_t>(t.split) * per);
+    // groups of up to 16 (or 32) tiles along the fast side run against every tile of the other
+    const int32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
+    const int32_t gs = min(fast, 32), g = r / (gs * slow), in = r - g * gs * slow;
+    const int32_t len = min(gs, fast - g * gs);
+    const int32_t f = g * gs + in % len, s = in / len;
+    t.mt = q.fast_n ? s : f;
+    t.nt = q.fast_n ? f : s;
+    return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void store_3d(const void *map, int x, int y, int z, const void *src, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                     :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(src)) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                     :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(src)) : "memory");
+}
+// all but the last committed store of this thread have read their source
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
+__device__ __forceinline__ bool failed(const int *f) { return *reinterpret_cast<const volatile int *>(f) != 0; }
+// True once the phase completed; false, with the block marked, when the wait ran out or
+// another role gave up.
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t phase, int *f) {
+    if (failed(f)) return false;
+    if (tc::mbar_wait(bar, phase)) return true;
+    atomicExch(f, 1);
+    return false;
+}
+
+enum Bar { bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = bAccFull + 2, bDrain = bAccEmpty + 2, bCount };
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smraw[];
+    uint8_t *sm = smraw + ((1024 - (tc::smem_addr(smraw) & 1023)) & 1023);
+    __shared__ uint64_t bars[bCount];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) { tc::mbar_init(&bars[bFull + i], 1); tc::mbar_init(&bars[bEmpty + i], 1); }
+        for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[bAccFull + i], 1); tc::mbar_init(&bars[bAccEmpty + i], 4); }
+        tc::mbar_init(&bars[bDrain], 1);
+        tc::fence_mbar_init();
+        s_fail = 0;
+    }
+    if (warp == 2) { tc::tmem_alloc(&s_tmem, 512); tc::fence_before_sync(); }
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = s_tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;                            // stages filled so far
+            TileId t;
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; ok && tile_at(p, idx, t); idx += gridDim.x) {
+                const Prod &q = p.prod[t.which];
+                const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
+                const int32_t m0 = t.mt * kTM, n0 = t.nt * q.n;
+                const uint32_t bytes = (q.a_mn ? kABytes : q.a_rows * 128u) + q.n * 128u;
+                for (int32_t k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % kStages, use = it / kStages;
+                    if (use > 0 && !wait_or_fail(&bars[bEmpty + s], (use - 1) & 1, &s_fail)) { ok = false; break; }
+                    uint64_t *full = &bars[bFull + s];
+                    uint8_t *a = sm + s * kStageBytes, *b = a + kABytes;
+                    tc::mbar_expect_tx(full, bytes);
+                    if (q.a_mn) {
+                        tc::tma_load_2d(a, &q.a, m0, k * kTK, full);
+                        tc::tma_load_2d(a + 8192, &q.a, m0 + 64, k * kTK, full);
+                    } else {
+                        tc::tma_load_2d(a, &q.a, k * kTK, m0, full);
+                    }
+                    if (q.b_mn) {
+                        for (int j = 0; j < q.n; j += 64) tc::tma_load_2d(b + j * 128, &q.b, n0 + j, q.b_y0 + k * kTK, full);
+                    } else {
+                        tc::tma_load_2d(b, &q.b, k * kTK, q.b_y0 + n0, full);
+                    }
+                }
+            }
+            // Nothing may be in flight into this block's shared memory when it ends: the copies
+            // (after a failure the products may not have waited for them), then the stages'
+            // last release.
+            for (uint32_t s = 0; s < kStages; ++s) {
+                if (it <= s) continue;
+                const uint32_t uses = (it - s + kStages - 1) / kStages;
+                tc::mbar_wait(&bars[bFull + s], (uses - 1) & 1, 1000000000LL);
+                if (ok && !failed(&s_fail)) wait_or_fail(&bars[bEmpty + s], (uses - 1) & 1, &s_fail);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, tile = 0;
+            TileId t;
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; ok && tile_at(p, idx, t); idx += gridDim.x, ++tile) {
+                const Prod &q = p.prod[t.which];
+                const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
+                const uint32_t buf = tile & 1, use = tile >> 1, d = tm + buf * kTN;
+                const uint32_t id = tc::idesc_bf16(kTM, q.n, q.a_mn != 0, q.b_mn != 0);
+                if (use > 0 && !wait_or_fail(&bars[bAccEmpty + buf], (use - 1) & 1, &s_fail)) { ok = false; break; }
+                tc::fence_after_sync();
+                for (int32_t k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_or_fail(&bars[bFull + s], (it / kStages) & 1, &s_fail)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    const uint32_t a = tc::smem_addr(sm + s * kStageBytes), b = a + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kTK / 16; ++kk) {
+                        const uint64_t da = q.a_mn ? tc::desc_sw128_mn(a + kk * 2048, 8192) : tc::desc_sw128(a + kk * 32);
+                        const uint64_t db = q.b_mn ? tc::desc_sw128_mn(b + kk * 2048, 8192) : tc::desc_sw128(b + kk * 32);
+                        tc::mma_bf16(d, da, db, id, (k > k0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::mma_commit(&bars[bEmpty + s]);
+                }
+                if (ok) tc::mma_commit(&bars[bAccFull + buf]);
+            }
+            if (failed(&s_fail)) {                      // let the products in flight end
+                if (p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
+                tc::mma_commit(&bars[bDrain]);
+                tc::mbar_wait(&bars[bDrain], 0, 1000000000LL);
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        const int lg = warp - kEpiWarp0;                // TMEM lanes 32 lg .. 32 lg + 31
+        const uint32_t lane_off = static_cast<uint32_t>(lg * 32) << 16;
+        uint8_t *out = sm + kStages * kStageBytes + lg * 8192;
+        uint32_t tile = 0, slot = 0;
+        TileId t;
+        for (int64_t idx = blockIdx.x; tile_at(p, idx, t); idx += gridDim.x, ++tile) {
+            const Prod &q = p.prod[t.which];
+            const uint32_t buf = tile & 1;
+            if (!__all_sync(0xffffffffu, wait_or_fail(&bars[bAccFull + buf], (tile >> 1) & 1, &s_fail))) break;
+            tc::fence_after_sync();
+            const uint32_t acc = tm + buf * kTN + lane_off;
+            const int32_t n0 = t.nt * q.n, row = t.mt * kTM + lg * 32 + lane;
+            if (MODE == kFwd) {
+                const int32_t nv = min(q.n, q.cols - n0);       // columns that are vocabulary entries
+                float m = -INFINITY, s = 0.f;
+                for (int c = 0; c < nv; c += 32) {
+                    float v[32];
+                    tc::tmem_ld32(acc + c, v);
+                    if (c + 32 <= nv) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i] * p.c2);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) if (c + i < nv) m = fmaxf(m, v[i] * p.c2);
+                    }
+                }
+                for (int c = 0; c < nv; c += 32) {
+                    float v[32], s0 = 0.f, s1 = 0.f;
+                    tc::tmem_ld32(acc + c, v);
+                    if (c + 32 <= nv) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            s0 += ex2(fmaf(v[i], p.c2, -m));
+                            s1 += ex2(fmaf(v[i + 1], p.c2, -m));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) if (c + i < nv) s0 += ex2(fmaf(v[i], p.c2, -m));
+                    }
+                    s += s0 + s1;
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive(&bars[bAccEmpty + buf]);
+                if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
+            } else {
+                RowInfo ri{0.f, 0.f, 0, 0};
+                if (MODE == kDz && row < q.rows) ri = p.rows[row];
+                const int step = q.out_f32 ? 32 : 64;
+                const int32_t y = t.mt * kTM + lg * 32;
+                for (int c = 0; c < q.n; c += step) {
+                    uint8_t *dst = out + slot * 4096;
+                    if (lane == 0) store_wait_read1();
+                    __syncwarp();
+                    if (q.out_f32) {
+                        float v[32];
+                        tc::tmem_ld32(acc + c, v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    } else {
+                        float v[64];
+                        tc::tmem_ld32x2(acc + c, reinterpret_cast<float(&)[32]>(v[0]), acc + c + 32,
+                                        reinterpret_cast<float(&)[32]>(v[32]));
+                        if (MODE == kDz) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) v[i] = ri.neg_g * ex2(fmaf(v[i], p.c2, -ri.lse2));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint4 w;
+                            w.x = tc::pack_bf16(v[8 * j], v[8 * j + 1]); w.y = tc::pack_bf16(v[8 * j + 2], v[8 * j + 3]);
+                            w.z = tc::pack_bf16(v[8 * j + 4], v[8 * j + 5]); w.w = tc::pack_bf16(v[8 * j + 6], v[8 * j + 7]);
+                            *reinterpret_cast<uint4 *>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+                        }
+                        if (MODE == kDz) {              // the row's labels among these 64 columns
+                            const int32_t lo = p.v0 + n0 + c;
+                            for (int32_t e = 0; e < ri.count; ++e) {
+                                const uint32_t j = static_cast<uint32_t>(__ldg(p.ent_y + ri.first + e) - lo);
+                                if (j < 64u)
+                                    *reinterpret_cast<__nv_bfloat16 *>(dst + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) +
+                                                                       (j & 7) * 2) =
+                                        __float2bfloat16_rn(__ldg(p.ent_v + ri.first + e));
+                            }
+                        }
+                    }
+                    if (c + step >= q.n) {              // the accumulator has been read
+                        tc::fence_before_sync();
+                    }
+                    tc::fence_smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (c + step >= q.n) arrive(&bars[bAccEmpty + buf]);
+                        if (y < q.rows && n0 + c < q.cols)
+                            store_3d(&q.out, n0 + c, q.out_y0 + y, t.split, dst, q.out_add != 0);
+                        tc::bulk_commit();
+                    }
+                    slot ^= 1;
+                }
+            }
+        }
+        if (MODE != kFwd && lane == 0) tc::bulk_wait_all();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 2) tc::tmem_dealloc(tm, 512);
+}
+
+// ---- forward: joining the tiles, and the positions' own logits --------------------------
+
+// One warp a row: lse from the row's (max, sum) pairs, which are in units of log 2.
+__global__ void __launch_bounds__(256) head_lse_kernel(const float2 *part, float *lse, int64_t C, int32_t tiles) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (c >= C) return;
+    const float2 *q = part + c * tiles;
+    float m = -INFINITY, s = 0.f;
+    for (int32_t i = lane; i < tiles; i += 32) {
+        const float2 t = q[i];
+        const float n = fmaxf(m, t.x);
+        s = s * exp2f(m - n) + t.y * exp2f(t.x - n);
+        if (m == -INFINITY) s = t.y;
+        m = n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float n = fmaxf(m, m2);
+        const float a = m == -INFINITY ? 0.f : s * exp2f(m - n), b = m2 == -INFINITY ? 0.f : s2 * exp2f(m2 - n);
+        s = a + b;
+        m = n;
+    }
+    if (lane == 0) lse[c] = (m + log2f(s)) * kLn2;
+}
+
+// x_c . w_y over D (a multiple of 8), one warp; every lane returns it.
+__device__ __forceinline__ float row_dot(const __nv_bfloat16 *x, const __nv_bfloat16 *w, int32_t D) {
+    const int lane = threadIdx.x & 31;
+    float s0 = 0.f, s1 = 0.f;
+    for (int32_t i = lane * 8; i < D; i += 256) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + i)), b = __ldg(reinterpret_cast<const uint4 *>(w + i));
+        const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a), *pb = reinterpret_cast<const __nv_bfloat162 *>(&b);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = __bfloat1622float2(pa[k]), v = __bfloat1622float2(pb[k]);
+            s0 = fmaf(u.x, v.x, s0);
+            s1 = fmaf(u.y, v.y, s1);
+        }
+    }
+    float s = s0 + s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+struct SemParams {
+    const __nv_bfloat16 *x, *w;
+    const int32_t *row_ptr, *row_sem, *target;
+    const float *lse, *dlogp;
+    float *logp;
+    RowInfo *rows;
+    int32_t *ent_y;
+    float *ent_v;
+    int64_t C, S;
+    int32_t V, D;
+    float scale;
+};
+
+// One warp a position (the q-th of row_sem): its row by binary search in row_ptr.
+__global__ void __launch_bounds__(256) head_logp_kernel(SemParams p) {
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (q >= p.S) return;
+    int64_t lo = 0, hi = p.C;                       // last row with row_ptr <= q
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (__ldg(p.row_ptr + mid) <= q) lo = mid; else hi = mid;
+    }
+    const int32_t s = __ldg(p.row_sem + q);
+    if (s < 0 || s >= p.S) return;
+    const int32_t y = __ldg(p.target + s);
+    float r = 0.f;
+    if (y >= 0 && y < p.V)
+        r = p.scale * row_dot(p.x + lo * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D) - p.lse[lo];
+    if ((threadIdx.x & 31) == 0) p.logp[s] = r;
+}
+
+// ---- backward: per row, G and the distinct labels with a gradient of their own ----------
+
+// One warp a row.  A label that several positions of the row share gets the sum of their
+// gradients in list order; ent_v is the finished entry scale (sum g - G e^(z - lse)) in fp32,
+// written over the row's softmax term when its tile is formed.
+__global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (c >= p.C) return;
+    const int32_t b = max(0, __ldg(p.row_ptr + c));
+    const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
+    float G = 0.f;
+    int32_t count = 0;
+    auto label = [&](int32_t q, float *g) {
+        const int32_t s = __ldg(p.row_sem + q);
+        if (s < 0 || s >= p.S) return -1;
+        const int32_t y = __ldg(p.target + s);
+        if (y < 0 || y >= p.V) return -1;
+        *g = __ldg(p.dlogp + s);
+        return y;
+    };
+    for (int32_t base = b; base < e; base += 32) {
+        const int32_t q = base + lane;
+        float g = 0.f;
+        const int32_t y = q < e ? label(q, &g) : -1;
+        if (y >= 0) G += g;
+        bool first = y >= 0;
+        float other;
+        for (int32_t t = b; t < q && first; ++t) first = label(t, &other) != y;
+        float sum = 0.f;
+        if (first) {
+            sum = g;
+            for (int32_t t = q + 1; t < e; ++t) {
+                float gt = 0.f;
+                if (label(t, &gt) == y) sum += gt;
+            }
+        }
+        first = first && sum != 0.f;
+        const uint32_t mask = __ballot_sync(0xffffffffu, first);
+        if (first) {
+            const int32_t at = b + count + __popc(mask & ((1u << lane) - 1u));
+            p.ent_y[at] = y;
+            p.ent_v[at] = sum;
+        }
+        count += __popc(mask);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
+    const float lse = p.lse[c];
+    __syncwarp();
+    for (int32_t i = 0; i < count; ++i) {
+        const int32_t y = p.ent_y[b + i];
+        const float z = p.scale * row_dot(p.x + c * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
+        const float v = p.scale * (p.ent_v[b + i] - G * expf(z - lse));
+        __syncwarp();
+        if (lane == 0) p.ent_v[b + i] = v;
+    }
+    if (lane == 0) p.rows[c] = RowInfo{-p.scale * G, lse * kLog2e, count, b};
+}
+
+// dX in bf16 from the splits' fp32 sums, in ascending order.
+__global__ void __launch_bounds__(256) head_dx_kernel(const float *acc, __nv_bfloat16 *dx, int64_t n, int32_t splits) {
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 256 * 8) {
+        float v[8] = {};
+        for (int32_t s = 0; s < splits; ++s) {
+            const float4 *q = reinterpret_cast<const float4 *>(acc + s * n + i);
+            const float4 a = q[0], b = q[1];
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        }
+        uint4 u;
+        u.x = tc::pack_bf16(v[0], v[1]); u.y = tc::pack_bf16(v[2], v[3]);
+        u.z = tc::pack_bf16(v[4], v[5]); u.w = tc::pack_bf16(v[6], v[7]);
+        *reinterpret_cast<uint4 *>(dx + i) = u;
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+int sm_count() {
+    int dev = 0, n = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Tile width of a product with m_tiles row tiles over `cols` columns: the multiple of `unit`
+// up to 256 that leaves the least work on the busiest SM (16 columns stand for a tile's
+// fixed cost).
+int32_t tile_width(int32_t m_tiles, int64_t cols, int32_t unit) {
+    int32_t best = kTN;
+    int64_t cost = INT64_MAX;
+    for (int32_t n = kTN; n >= 64; n -= unit) {
+        const int64_t tiles = int64_t(m_tiles) * ceil_div(cols, n);
+        const int64_t c = (tiles + sm_count() - 1) / sm_count() * (n + 16);
+        if (c < cost) { cost = c; best = n; }
+    }
+    return best;
+}
+
+// [rows][cols] bf16, read in boxes of 64 columns x box_rows.
+bool map_in(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t pitch, int32_t box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    return encode_bf16(m, base, 2, dims, strides, box);
+}
+
+// [layers][rows][cols], written in boxes of 128 bytes x 32 rows.
+bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t cols, int64_t pitch, bool f32) {
+    const cuuint64_t e = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(layers)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * e, static_cast<cuuint64_t>(pitch) * e * rows};
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    auto fn = encode_tiled();
+    return fn && fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides,
+                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_tiles(const Params &p, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    int64_t items = 0;
+    for (int i = 0; i < p.n_prod; ++i) items += int64_t(p.prod[i].m_tiles) * p.prod[i].n_tiles * p.prod[i].splits;
+    const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));
+    head_tile_kernel<MODE><<<grid, kThreads, kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int check(const harts_linear_logprob_fwd_args *a) {
+    if (!a) { set_error("NULL args"); return HARTS_EINVAL; }
+    if (a->dtype != HARTS_BF16) { set_error("hidden rows and weight must be bf16"); return HARTS_EUNSUPPORTED; }
+    if (a->C < 0 || a->S < 0 || a->V < 1 || a->D < 1) { set_error("C, S >= 0 and V, D >= 1 required"); return HARTS_EINVAL; }
+    if (a->D % 8) { set_error("D must be a multiple of 8 (rows start 16-byte aligned)"); return HARTS_EUNSUPPORTED; }
+    if (a->S > 0x7fffffff || a->C > 0x7fffff00 || a->V > 0x7fffff00) { set_error("C, V or S beyond int32 rows"); return HARTS_EOVERFLOW; }
+    if (!std::isfinite(a->scale)) { set_error("scale must be finite"); return HARTS_EINVAL; }
+    if (a->C > 0 && (!a->x || !a->weight || !a->row_ptr || !a->lse)) { set_error("NULL x, weight, row_ptr or lse"); return HARTS_EINVAL; }
+    if (a->S > 0 && (!a->row_sem || !a->target)) { set_error("NULL row_sem or target"); return HARTS_EINVAL; }
+    if (!aligned16(a->x) || !aligned16(a->weight) || !aligned16(a->workspace)) {
+        set_error("x, weight and workspace must be 16-byte aligned");
+        return HARTS_EINVAL;
+    }
+    return HARTS_OK;
+}
+
+int cuda_fail(cudaError_t e, const char *what) {
+    set_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return HARTS_ECUDA;
+}
+
+int32_t fwd_width(int64_t C, int32_t V) { return tile_width(ceil_div(C, kTM), V, 16); }
+
+SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
+    SemParams s{};
+    s.x = static_cast<const __nv_bfloat16 *>(a->x); s.w = static_cast<const __nv_bfloat16 *>(a->weight);
+    s.row_ptr = a->row_ptr; s.row_sem = a->row_sem; s.target = a->target; s.lse = a->lse; s.logp = a->logp;
+    s.C = a->C; s.S = a->S; s.V = a->V; s.D = a->D; s.scale = a->scale;
+    return s;
+}
+
+// How the backward is cut: vocabulary entries a piece, K splits of dX, and where things lie
+// in the workspace.
+struct BwdPlan {
+    int32_t piece, n_pieces, n_dz, n_grad, splits, k_per;
+    bool acc;                       // dX goes through fp32 sums
+    size_t rows, ent_y, ent_v, dz, dx, total;
+};
+
+constexpr size_t kPieceBytes = size_t(512) << 20;     // dZ of one piece, when the caller sets no piece
+
+BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
+    BwdPlan b{};
+    int64_t want = piece > 0 ? piece : static_cast<int64_t>(kPieceBytes / (2 * std::max<int64_t>(C, 1)));
+    want = std::max<int64_t>(kTN, want / kTN * kTN);
+    b.piece = static_cast<int32_t>(std::min<int64_t>(want, (int64_t(V) + 63) / 64 * 64));
+    b.n_pieces = ceil_div(V, b.piece);
+    const int32_t mt = ceil_div(C, kTM);
+    b.n_dz = tile_width(mt, std::min<int32_t>(b.piece, V), 64);
+    b.n_grad = std::min<int32_t>(kTN, (D + 63) / 64 * 64);
+    if (D > kTN) b.n_grad = (ceil_div(D, ceil_div(D, kTN)) + 63) / 64 * 64;
+    const int32_t kb = ceil_div(std::min<int32_t>(b.piece, V), kTK), tiles = mt * ceil_div(D, b.n_grad);
+    // about two rounds of dX tiles over the SMs, each at least 16 steps deep
+    b.splits = std::max(1, std::min({static_cast<int32_t>(ceil_div(2 * sm_count(), tiles)), ceil_div(kb, 16), int32_t(32)}));
+    b.k_per = ceil_div(kb, b.splits);
+    b.splits = ceil_div(kb, b.k_per);
+    b.acc = b.splits > 1 || b.n_pieces > 1;
+    b.rows = 0;
+    b.ent_y = align256(sizeof(RowInfo) * static_cast<size_t>(C));
+    b.ent_v = b.ent_y + align256(4 * static_cast<size_t>(S));
+    b.dz = b.ent_v + align256(4 * static_cast<size_t>(S));
+    b.dx = b.dz + align256(2 * static_cast<size_t>(C) * b.piece);
+    b.total = b.dx + (b.acc ? align256(4 * static_cast<size_t>(C) * D * b.splits) : 0);
+    return b;
+}
+
+}  // namespace
+}  // namespace harts
+
+using namespace harts;
+
+extern "C" {
+
+size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D) {
+    if (C < 0 || V < 1 || D < 1) return 0;
+    return std::max<size_t>(256, sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_width(C, V)));
+}
+
+int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_stream_t stream) {
+    const int rc = check(a);
+    if (rc) return rc;
+    if (a->S > 0 && !a->logp) { set_error("NULL logp"); return HARTS_EINVAL; }
+    if (a->C == 0) { set_error(""); return HARTS_OK; }
+    if (!a->workspace || a->workspace_bytes < harts_linear_logprob_fwd_workspace_bytes(a->C, a->V, a->D)) {
+        set_error("workspace too small");
+        return HARTS_ESMALLBUF;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    Prod &q = p.prod[0];
+    q.m_tiles = ceil_div(a->C, kTM);
+    q.n = fwd_width(a->C, a->V);
+    q.n_tiles = ceil_div(a->V, q.n);
+    q.splits = 1;
+    q.k_blocks = q.k_per = ceil_div(a->D, kTK);
+    q.a_rows = static_cast<int32_t>(std::min<int64_t>(kTM, (a->C + 7) / 8 * 8));
+    q.rows = static_cast<int32_t>(a->C);
+    q.cols = a->V;
+    p.n_prod = 1;
+    p.error = a->error;
+    p.c2 = a->scale * kLog2e;
+    p.part = static_cast<float2 *>(a->workspace);
+    if (!map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows) || !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n)) {
+        set_error("tensor map");
+        return HARTS_ECUDA;
+    }
+    cudaError_t e = launch_tiles<kFwd>(p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
+    head_lse_kernel<<<ceil_div(a->C, 8), 256, 0, st>>>(p.part, a->lse, a->C, q.n_tiles);
+    if (a->S > 0) head_logp_kernel<<<ceil_div(a->S, 8), 256, 0, st>>>(sem_params(a));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
+    set_error("");
+    return HARTS_OK;
+}
+
+size_t harts_linear_logprob_bwd_workspace_bytes(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
+    if (C < 0 || V < 1 || D < 1 || S < 0 || piece < 0) return 0;
+    return std::max<size_t>(256, plan_bwd(C, V, D, S, piece).total);
+}
+
+int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_stream_t stream) {
+    if (!a) { set_error("NULL args"); return HARTS_EINVAL; }
+    const harts_linear_logprob_fwd_args &f = a->fwd;
+    const int rc = check(&f);
+    if (rc) return rc;
+    if (a->piece < 0) { set_error("piece must be >= 0"); return HARTS_EINVAL; }
+    if (f.S > 0 && !a->dlogp) { set_error("NULL dlogp"); return HARTS_EINVAL; }
+    if (!a->dweight || (f.C > 0 && !a->dx)) { set_error("NULL dx or dweight"); return HARTS_EINVAL; }
+    if (!aligned16(a->dx) || !aligned16(a->dweight)) { set_error("dx and dweight must be 16-byte aligned"); return HARTS_EINVAL; }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (f.C == 0) {
+        const cudaError_t e = cudaMemsetAsync(a->dweight, 0, 2 * static_cast<size_t>(f.V) * f.D, st);
+        if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward");
+        set_error("");
+        return HARTS_OK;
+    }
+    const BwdPlan b = plan_bwd(f.C, f.V, f.D, f.S, a->piece);
+    if (!f.workspace || f.workspace_bytes < b.total) { set_error("workspace too small"); return HARTS_ESMALLBUF; }
+    if (reinterpret_cast<uintptr_t>(f.workspace) & 255) { set_error("workspace must be 256-B aligned"); return HARTS_EINVAL; }
+    uint8_t *ws = static_cast<uint8_t *>(f.workspace);
+    void *dz = ws + b.dz;
+    float *acc = reinterpret_cast<float *>(ws + b.dx);
+
+    SemParams s = sem_params(&f);
+    s.dlogp = a->dlogp;
+    s.rows = reinterpret_cast<RowInfo *>(ws + b.rows);
+    s.ent_y = reinterpret_cast<int32_t *>(ws + b.ent_y);
+    s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
+    head_rows_kernel<<<ceil_div(f.C, 8), 256, 0, st>>>(s);
+
+    const int32_t mt = ceil_div(f.C, kTM), C = static_cast<int32_t>(f.C);
+    const int32_t a_rows = static_cast<int32_t>(std::min<int64_t>(kTM, (f.C + 7) / 8 * 8));
+    Params pz, pg;
+    std::memset(&pz, 0, sizeof(pz));
+    std::memset(&pg, 0, sizeof(pg));
+    Prod &z = pz.prod[0], &gx = pg.prod[0], &gw = pg.prod[1];
+    bool ok = map_in(&z.a, f.x, f.C, f.D, f.D, a_rows) && map_in(&z.b, f.weight, f.V, f.D, f.D, b.n_dz) &&
+              map_in(&gx.b, f.weight, f.V, f.D, f.D, 64) && map_in(&gw.b, f.x, f.C, f.D, f.D, 64) &&
+              map_out(&gw.out, a->dweight, 1, f.V, f.D, f.D, false) &&
+              (b.acc ? map_out(&gx.out, acc, b.splits, f.C, f.D, f.D, true) : map_out(&gx.out, a->dx, 1, f.C, f.D, f.D, false));
+    for (int32_t i = 0; ok && i < b.n_pieces; ++i) {
+        const int32_t v0 = i * b.piece, nv = std::min(b.piece, f.V - v0);
+        ok = map_out(&z.out, dz, 1, f.C, nv, b.piece, false) && map_in(&gx.a, dz, f.C, nv, b.piece, a_rows) &&
+             map_in(&gw.a, dz, f.C, nv, b.piece, 64);
+        if (!ok) break;
+        // logits of the piece, as dz
+        z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
+        z.k_blocks = z.k_per = ceil_div(f.D, kTK);
+        z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
+        pz.n_prod = 1; pz.error = f.error; pz.c2 = f.scale * kLog2e;
+        pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0;
+        cudaError_t e = launch_tiles<kDz>(pz, st);
+        if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
+        // dX (first: its tiles are the longest) and dW
+        gx.b_mn = 1; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
+        gx.k_blocks = ceil_div(nv, kTK); gx.k_per = b.k_per; gx.splits = ceil_div(gx.k_blocks, b.k_per);
+        gx.b_y0 = v0; gx.out_y0 = 0; gx.rows = C; gx.cols = f.D; gx.out_f32 = b.acc; gx.out_add = i > 0;
+        gw.a_mn = gw.b_mn = 1; gw.m_tiles = ceil_div(nv, kTM); gw.n = b.n_grad; gw.n_tiles = ceil_div(f.D, b.n_grad);
+        gw.k_blocks = gw.k_per = ceil_div(f.C, kTK); gw.splits = 1;
+        gw.out_y0 = v0; gw.rows = nv; gw.cols = f.D; gw.fast_n = 1;
+        pg.n_prod = 2; pg.error = f.error;
+        e = launch_tiles<kGrad>(pg, st);
+        if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
+    }
+    if (!ok) { set_error("tensor map"); return HARTS_ECUDA; }
+    if (b.acc) {
+        const int64_t n = f.C * f.D;
+        const int grid = static_cast<int>(std::min<int64_t>((n / 8 + 255) / 256, int64_t(sm_count()) * 8));
+        head_dx_kernel<<<grid, 256, 0, st>>>(acc, static_cast<__nv_bfloat16 *>(a->dx), n, b.splits);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
+    set_error("");
+    return HARTS_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,246 @@
+"""GPU parity of harts_linear_logprob_fwd / _bwd against the fp64 oracle (oracle/tail.py) on
+the same bf16 inputs.
+
+Bounds.  u = 2^-23 bounds an fp32 addition on the tensor cores (which may truncate).  A logit
+sums D products: off by e_z = D u |scale| max_v sum_i |x_i w_i|.  lse is off by at most that,
+plus the joined exponentials (8 u) and its rounding (u |lse|); logp by that plus its own dot
+product.  dz = -G p + g carries e_z + e_lse + 8 u in p, and one rounding to bf16 (half a step:
+2^-8); dx adds V terms, dweight C terms: elementwise
+  |d - ref| <= ((2^-8 + 8 u) |dz| + (e_z + e_lse) |G| p) |w| + n u |dz| |w| + 2^-8 |ref|,
+with the sums over |.| formed here in fp64."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import tail
+from prefix_shared_chunkwise_gb300.api import Plan, linear_logprob_bwd, linear_logprob_fwd, semantic_map
+from prefix_shared_chunkwise_gb300.synth import make_tree
+from tests._parity import rel_l2
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from prefix_shared_chunkwise_gb300 import build
+    build.build()
+
+
+def _csr(sem_row, C):
+    row_ptr = np.zeros(C + 1, np.int32)
+    np.add.at(row_ptr, sem_row + 1, 1)
+    return np.cumsum(row_ptr).astype(np.int32), np.argsort(sem_row, kind="stable").astype(np.int32)
+
+
+def _case(C, V, D, S, seed, spread=2.0, labels=None):
+    """Rows without positions, labels shared and distinct within a row, and positions without
+    a label (-1 and V) all occur once S is large enough."""
+    rng = np.random.default_rng(seed)
+    bf = lambda a: torch.as_tensor(a, dtype=torch.float32).to(torch.bfloat16)
+    x, w = bf(rng.standard_normal((C, D))), bf(rng.standard_normal((V, D)) * spread / D ** 0.5)
+    sem_row = rng.integers(0, max(1, C - C // 5), size=S)
+    target = rng.integers(0, V if labels is None else min(V, labels), size=S)
+    target[rng.random(S) < 0.05] = -1
+    target[rng.random(S) < 0.02] = V
+    g = rng.standard_normal(S).astype(np.float32)
+    g[rng.random(S) < 0.1] = 0
+    return x, w, sem_row.astype(np.int64), target.astype(np.int64), g
+
+
+def _dev(a):
+    return torch.as_tensor(a, device="cuda")
+
+
+def _run_fwd(x, w, sem_row, target, scale, **kw):
+    row_ptr, row_sem = _csr(sem_row, x.shape[0])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logp, lse = linear_logprob_fwd(x.cuda(), w.cuda(), _dev(row_ptr), _dev(row_sem), _dev(target.astype(np.int32)),
+                                   scale=scale, error=err, **kw)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    return logp, lse
+
+
+def _errors(x, w, scale, lse):
+    xa, wa = np.abs(x.double().numpy()), np.abs(w.double().numpy())
+    ez = x.shape[1] * U * abs(scale) * (xa @ wa.T).max(axis=1)
+    return ez, ez + 8 * U + U * np.abs(lse)
+
+
+SIZES = [(1, 1, 8, 1), (1, 5, 8, 3), (3, 64, 64, 10), (1, 40_001, 256, 1), (5, 257, 72, 40), (127, 255, 128, 300),
+         (128, 256, 64, 0), (129, 1000, 200, 700), (300, 2049, 1032, 900), (777, 4099, 136, 1000)]
+
+
+@pytest.mark.parametrize("C,V,D,S", SIZES)
+@pytest.mark.parametrize("scale", [1.0, 0.6])
+def test_forward(C, V, D, S, scale):
+    x, w, sem_row, target, _ = _case(C, V, D, S, 1)
+    logp, lse = _run_fwd(x, w, sem_row, target, scale)
+    rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target, scale)
+    ez, el = _errors(x, w, scale, re)
+    assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
+    assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl)) if S else True
+
+
+def _check_bwd(x, w, sem_row, target, g, scale, piece=0):
+    C, V, D = x.shape[0], w.shape[0], x.shape[1]
+    x64, w64 = x.double().numpy(), w.double().numpy()
+    _, re = tail.linear_logprob_fwd(x64, w64, sem_row, target, scale)
+    row_ptr, row_sem = _csr(sem_row, C)
+    args = (x.cuda(), w.cuda(), _dev(row_ptr), _dev(row_sem), _dev(target.astype(np.int32)),
+            _dev(re.astype(np.float32)), _dev(g))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(scale=scale, piece=piece, error=err)
+    dx, dw = linear_logprob_bwd(*args, **kw, dx=torch.full_like(args[0], 7), dweight=torch.full_like(args[1], 7))
+    dx2, dw2 = linear_logprob_bwd(*args, **kw)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)       # no order of additions left open
+    rdx, rdw = tail.linear_logprob_bwd(x64, w64, sem_row, target, g, scale)
+    ez, el = _errors(x, w, scale, re)
+    keep = (target >= 0) & (target < V)
+    G, Ga = np.zeros(C), np.zeros(C)
+    np.add.at(G, sem_row[keep], g[keep].astype(np.float64))
+    np.add.at(Ga, sem_row[keep], np.abs(g[keep]).astype(np.float64))
+    p = np.exp(scale * (x64 @ w64.T) - re[:, None])
+    own = np.zeros((C, V))
+    np.add.at(own, (sem_row[keep], target[keep]), np.abs(g[keep]).astype(np.float64))
+    dz = np.abs(G)[:, None] * p + own                          # |dz| at most
+    off = (2.0 ** -8 + 8 * U) * dz + (ez + el)[:, None] * np.abs(G)[:, None] * p + len(g) * U * (Ga[:, None] * p + own)
+    for got, ref, o, n in ((dx, rdx, abs(scale) * (off @ np.abs(w64)), V), (dw, rdw, abs(scale) * (off.T @ np.abs(x64)), C)):
+        size = abs(scale) * ((dz @ np.abs(w64)) if n == V else (dz.T @ np.abs(x64)))
+        got = got.double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= o + n * U * size + 2.0 ** -8 * np.abs(ref) + 1e-37)
+        if np.linalg.norm(ref) > 0:
+            assert rel_l2(got, ref) <= 1e-2
+    empty = np.setdiff1d(np.arange(C), sem_row[keep])
+    assert np.all(dx.float().cpu().numpy()[empty] == 0)
+
+
+@pytest.mark.parametrize("C,V,D,S", SIZES)
+@pytest.mark.parametrize("scale", [1.0, 0.6])
+def test_backward(C, V, D, S, scale):
+    _check_bwd(*_case(C, V, D, S, 2), scale)
+
+
+@pytest.mark.parametrize("piece", [1, 256, 700, 2048, 100_000])
+def test_backward_in_pieces(piece):
+    _check_bwd(*_case(150, 2049, 136, 400, 3), 0.8, piece)
+
+
+def test_many_positions_on_one_row():
+    """All positions on few rows, with few labels and with many."""
+    for labels in (3, None):
+        x, w, _, target, g = _case(4, 999, 64, 500, 4, labels=labels)
+        sem_row = np.where(np.arange(500) < 450, 2, 0).astype(np.int64)
+        _check_bwd(x, w, sem_row, target, g, 1.0)
+        logp, lse = _run_fwd(x, w, sem_row, target, 1.0)
+        rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target)
+        ez, el = _errors(x, w, 1.0, re)
+        assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl))
+
+
+def test_peaked_rows():
+    """Logits of spread 60: softmax rows close to one-hot, exponentials that underflow."""
+    x, w, sem_row, target, g = _case(40, 700, 128, 100, 5, spread=60.0)
+    logp, lse = _run_fwd(x, w, sem_row, target, 1.0)
+    rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target)
+    ez, el = _errors(x, w, 1.0, re)
+    assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
+    assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl))
+    _check_bwd(x, w, sem_row, target, g, 1.0)
+
+
+def test_gradient_against_differences():
+    """<dx, d> and <dweight, d> against central differences of the forward kernel's
+    sum_s g_s logp[s].  Inputs on a grid of 2^-3 below 4 and steps of 2^-5 are exact in bf16;
+    the third-order term is ~ (step |w|)^2 < 1e-3 of the value, bf16 rounding of the gradient
+    2^-8 of its terms: 2 % of the sum of absolute terms over sqrt(n) is far above both."""
+    rng = np.random.default_rng(6)
+    C, V, D, S, step = 20, 300, 64, 60, 2.0 ** -5
+    grid = lambda a: torch.as_tensor(np.clip(np.round(a * 8) / 8, -3.5, 3.5), dtype=torch.float32)
+    x, w = grid(rng.standard_normal((C, D))), grid(rng.standard_normal((V, D)) * 0.3)
+    sem_row, target = rng.integers(0, C, S), rng.integers(0, V, S)
+    g = rng.standard_normal(S).astype(np.float32)
+    row_ptr, row_sem = _csr(sem_row, C)
+    idx = (_dev(row_ptr), _dev(row_sem), _dev(target.astype(np.int32)))
+    scale = 0.25
+
+    def loss(a, b):
+        logp, lse = linear_logprob_fwd(a.to(torch.bfloat16).cuda(), b.to(torch.bfloat16).cuda(), *idx, scale=scale)
+        return float((logp.double() * _dev(g).double()).sum()), lse
+
+    _, lse = loss(x, w)
+    dx, dw = linear_logprob_bwd(x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda(), *idx, lse, _dev(g), scale=scale)
+    for grad, base, put in ((dx, x, lambda a: (a, w)), (dw, w, lambda a: (x, a))):
+        d = torch.as_tensor(rng.choice([-1.0, 1.0], size=tuple(base.shape)), dtype=torch.float32)
+        num = (loss(*put(base + step * d))[0] - loss(*put(base - step * d))[0]) / (2 * step)
+        terms = grad.double().cpu() * d.double()
+        assert abs(float(terms.sum()) - num) <= 0.02 * float(terms.square().sum().sqrt()) * 3
+
+
+def test_semantic_map_of_a_forest():
+    """A forest's own semantic map at an odd vocabulary: shared rows carry several positions."""
+    parent, seg_len = make_tree("fig1_fp32")
+    pl = Plan(parent, seg_len, 64)
+    sem_row, row_ptr, row_sem = semantic_map(pl)
+    C, S, V, D = pl.info["C"], len(sem_row), 5003, 256
+    x, w, _, target, g = _case(C, V, D, S, 7)
+    _check_bwd(x, w, sem_row.astype(np.int64), target, g, 1.0)
+
+
+def test_large_row_offsets():
+    """A weight whose rows pass 2^31 elements: the last vocabulary entries decide the result."""
+    V, D, C = 600_000, 4096, 3
+    w = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w[-300:] = torch.randn((300, D), generator=g, device="cuda").to(torch.bfloat16)
+    x = torch.randn((C, D), generator=g, device="cuda").to(torch.bfloat16)
+    ptr = torch.arange(C + 1, dtype=torch.int32, device="cuda")
+    tgt = torch.tensor([V - 1, V - 299, 5], dtype=torch.int32, device="cuda")
+    logp, lse = linear_logprob_fwd(x, w, ptr, ptr[:C].clone(), tgt)
+    z = x.double() @ w[-300:].double().t()
+    re = torch.logsumexp(torch.cat([z, torch.zeros((C, 1), dtype=torch.float64, device="cuda") + np.log(V - 300)], 1), 1)
+    rl = torch.stack([z[0, 299], z[1, 1], 0 * z[2, 0]]) - re
+    size = float((x.double().abs() @ w[-300:].double().abs().t()).max())
+    tol = 2 * D * U * size + 20 * U + 4 * U * float(re.abs().max())
+    assert float((lse.double() - re).abs().max()) <= tol and float((logp.double() - rl).abs().max()) <= tol
+    dx, dw = linear_logprob_bwd(x, w, ptr, ptr[:C].clone(), tgt, lse, torch.ones(C, device="cuda"))
+    p = torch.exp(z - re[:, None])
+    dz = -p
+    dz[0, 299] += 1
+    dz[1, 1] += 1
+    assert rel_l2(dw[-300:].double().cpu().numpy(), (dz.t() @ x.double()).cpu().numpy()) <= 1e-2
+    assert rel_l2(dx.double().cpu().numpy(), (dz @ w[-300:].double()).cpu().numpy()) <= 1e-2
+
+
+def test_no_rows_and_stream_and_graph():
+    x, w, sem_row, target, g = _case(70, 500, 64, 90, 8)
+    row_ptr, row_sem = _csr(sem_row, 70)
+    a = (x.cuda(), w.cuda(), _dev(row_ptr), _dev(row_sem), _dev(target.astype(np.int32)))
+    e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    z1 = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logp, lse = linear_logprob_fwd(e, a[1], z1, none, none)
+    dx, dw = linear_logprob_bwd(e, a[1], z1, none, none, lse, logp)
+    assert logp.numel() == 0 and float(dw.float().abs().sum()) == 0
+    logp, lse = linear_logprob_fwd(*a)
+    dx, dw = linear_logprob_bwd(*a, lse, _dev(g))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    l2, e2 = linear_logprob_fwd(*a, stream=st)
+    st.synchronize()
+    assert torch.equal(l2, logp) and torch.equal(e2, lse)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    dx3, dw3, dl = torch.zeros_like(dx), torch.zeros_like(dw), _dev(g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        linear_logprob_bwd(*a, lse, dl, dx=dx3, dweight=dw3, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dx3, dx) and torch.equal(dw3, dw)
