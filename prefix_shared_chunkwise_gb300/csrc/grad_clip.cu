@@ -8,8 +8,8 @@
 // in L2.  Both kernels only stream: HBM bounds them, two reads and one write of every value
 // for sets larger than L2, one read and one write below that.
 //
-// Squares are summed in fp32 over one block's chunks (16 or so per accumulator and chunk)
-// and in fp64 across threads and blocks.  A block whose fp32 sum is not finite reads its chunks again in
+// Squares are summed in fp32 over a thread's share of one chunk (16 per accumulator) and in
+// fp64 across chunks, threads and blocks.  A block whose fp32 sum is not finite reads its chunks again in
 // fp64: squares overflow fp32 from 1.8e19 on, which bf16 and fp32 values reach.  If the norm
 // itself is not finite the gradients pass through unscaled; the caller sees it in the norm.
 #include <cuda_bf16.h>
@@ -138,21 +138,23 @@ __device__ double squares64(const T *g, int64_t n) {
     return s;
 }
 
-// Sum over the block in a fixed order; every thread returns it.
+// Sum over the block in a fixed order; thread 0 returns it.  GB300 has few fp64 units (a
+// warp's addition holds them for ~16 cycles), so fp64 is kept to one addition a thread and
+// chunk, one such sum a block, and one warp for the norm.
 __device__ double block_sum(double v, double *sm) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();                        // sm may still be read from an earlier sum
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += sm[i];
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kThreads / 32; ++i) s += sm[i];
     return s;
 }
 
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __grid_constant__ Set s) {
     __shared__ double sm[kThreads / 32];
+    __shared__ int s_wide;
     double sum = 0.0;
     for (int32_t c = blockIdx.x; c < s.chunks; c += gridDim.x) {
         const Item &it = s.item[find(s, c)];
@@ -162,7 +164,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __
                             : squares(static_cast<const float *>(it.g) + at, n);
     }
     sum = block_sum(sum, sm);
-    if (!isfinite(sum)) {
+    if (threadIdx.x == 0) s_wide = !isfinite(sum);
+    __syncthreads();
+    if (s_wide) {
         sum = 0.0;
         for (int32_t c = blockIdx.x; c < s.chunks; c += gridDim.x) {
             const Item &it = s.item[find(s, c)];
@@ -176,18 +180,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __
     if (threadIdx.x == 0) s.part[s.first + blockIdx.x] = sum;
 }
 
-__device__ double total_of(const Set &s, double *sm) {
+// The norm from the partial sums, by one warp in a fixed order; all lanes return it.
+__device__ double norm_of(const double *part, int32_t partials) {
     double v = 0.0;
-    for (int32_t i = threadIdx.x; i < s.partials; i += kThreads) v += s.part[i];
-    return block_sum(v, sm);
+#pragma unroll 4
+    for (int32_t i = threadIdx.x; i < partials; i += 32) v += part[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return sqrt(v);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double *part, int32_t partials, float *norm) {
-    __shared__ double sm[kThreads / 32];
-    double v = 0.0;
-    for (int32_t i = threadIdx.x; i < partials; i += kThreads) v += part[i];
-    v = block_sum(v, sm);
-    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(v));
+__global__ void __launch_bounds__(32) grad_norm_kernel(const double *part, int32_t partials, float *norm) {
+    const double n = norm_of(part, partials);
+    if (threadIdx.x == 0) *norm = static_cast<float>(n);
 }
 
 template <typename T, typename U>
@@ -226,10 +231,16 @@ __device__ void scale(const T *g, U *out, int64_t n, float f) {
 }
 
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Set s) {
-    __shared__ double sm[kThreads / 32];
-    const double norm = sqrt(total_of(s, sm));
-    const float f = norm > s.max_norm && isfinite(norm) ? static_cast<float>(s.max_norm / norm) : 1.f;
-    if (blockIdx.x == 0 && threadIdx.x == 0 && s.first == 0) *s.norm = static_cast<float>(norm);
+    __shared__ float s_f;
+    if (threadIdx.x < 32) {
+        const double norm = norm_of(s.part, s.partials);
+        if (threadIdx.x == 0) {
+            s_f = norm > s.max_norm && isfinite(norm) ? static_cast<float>(s.max_norm / norm) : 1.f;
+            if (blockIdx.x == 0 && s.first == 0) *s.norm = static_cast<float>(norm);
+        }
+    }
+    __syncthreads();
+    const float f = s_f;
     for (int32_t c = s.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
         const Item &it = s.item[find(s, c)];
         if (f == 1.f && it.out == it.g) continue;           // in place and nothing to scale
@@ -324,7 +335,7 @@ int run(const harts_grad_tensor *t, int32_t count, bool clip, float max_norm, fl
         } while (i < count);
         partials = first;
     }
-    if (!clip) grad_norm_kernel<<<1, kThreads, 0, st>>>(s.part, partials, norm);
+    if (!clip) grad_norm_kernel<<<1, 32, 0, st>>>(s.part, partials, norm);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_error(std::string("gradient norm launch: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
     set_error("");

@@ -33,12 +33,18 @@
 namespace harts {
 namespace {
 
-constexpr int kTM = 128, kTK = 64, kTN = 256;       // tile rows, K step (one 128-byte swizzle row), tile columns
-constexpr int kStages = 4;
-constexpr uint32_t kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K step (one 128-byte swizzle row), tile columns
+constexpr uint32_t kABytes = kTM * kTK * 2;
 constexpr uint32_t kOutBytes = 4 * 2 * 4096;        // 4 warps x 2 slots of 32 rows x 128 bytes
-constexpr uint32_t kSmem = kStages * kStageBytes + kOutBytes + 1024;
+// A block of a pair holds half of the tile's columns in shared memory: stages are smaller,
+// and there are more of them.
+template <int G> struct Ring {
+    static constexpr int stages = G == 2 ? 6 : 4;
+    static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
+    static constexpr uint32_t smem = stages * stage_bytes + kOutBytes + 1024;
+};
 constexpr int kThreads = 256, kEpiWarp0 = 4;
+constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kFwd = 0, kDz = 1, kGrad = 2 };
@@ -47,6 +53,8 @@ enum Mode { kFwd = 0, kDz = 1, kGrad = 2 };
 struct Prod {
     CUtensorMap a, b, out;
     int32_t a_mn, b_mn;             // operand stored [K][rows] instead of [rows][K]
+    int32_t a_panel;                // A is dZ, kept in panels of 64 columns
+    int32_t b_panel;                // B is seen as such panels: one copy for a block's columns
     int32_t a_rows;                 // rows of A's box when stored [rows][K]
     int32_t m_tiles, n_tiles, splits, n;
     int32_t k_blocks, k_per;        // steps of 64 in all, per split
@@ -87,9 +95,9 @@ __device__ __forceinline__ bool tile_at(const Params &p, int64_t idx, TileId &t)
     t.which = which;
     t.split = static_cast<int>(idx / per);
     const int32_t r = static_cast<int32_t>(idx - static_cast<int64_t>(t.split) * per);
-    // groups of up to 16 (or 32) tiles along the fast side run against every tile of the other
+    // groups of tiles along the fast side run against every tile of the other
     const int32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
-    const int32_t gs = min(fast, 32), g = r / (gs * slow), in = r - g * gs * slow;
+    const int32_t gs = min(fast, kGroup), g = r / (gs * slow), in = r - g * gs * slow;
     const int32_t len = min(gs, fast - g * gs);
     const int32_t f = g * gs + in % len, s = in / len;
     t.mt = q.fast_n ? s : f;
@@ -128,114 +136,204 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t phase, int 
     return false;
 }
 
-enum Bar { bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = bAccFull + 2, bDrain = bAccEmpty + 2, bCount };
+// ---- pairs of blocks: the leader (rank 0) issues the products of both, 256 tile rows ----
 
-template <int MODE>
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address of a barrier of this block in the pair's leader
+__device__ __forceinline__ uint32_t leader_addr(const uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_addr(bar)));
+    return a;
+}
+template <int G> __device__ __forceinline__ void pair_alloc(uint32_t *dst) {
+    if constexpr (G == 1) {
+        tc::tmem_alloc(dst, 512);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(tc::smem_addr(dst)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int G> __device__ __forceinline__ void pair_dealloc(uint32_t t) {
+    if constexpr (G == 1) tc::tmem_dealloc(t, 512);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(t) : "memory");
+}
+template <int G> __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if constexpr (G == 1)
+        tc::mma_bf16(d, a, b, id, acc);
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+// Arrive, in every block of the pair, on the barrier at this offset once all products issued
+// so far are done.
+template <int G> __device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    if constexpr (G == 1)
+        tc::mma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     :: "r"(tc::smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// Copy into this block; the bytes count on `bar`, which in a pair lies in the leader.
+template <int G> __device__ __forceinline__ void pair_load(void *dst, const void *map, int x, int y, uint32_t bar) {
+    if constexpr (G == 1)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                     " [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+template <int G> __device__ __forceinline__ void pair_load3(void *dst, const void *map, int x, int y, int z, uint32_t bar) {
+    if constexpr (G == 1)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3, %4}], [%5];"
+                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                     " [%0], [%1, {%2, %3, %4}], [%5];"
+                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+
+template <int G> struct Bar {
+    static constexpr int full = 0, empty = Ring<G>::stages, acc_full = 2 * Ring<G>::stages, acc_empty = acc_full + 2,
+                         drain = acc_empty + 2, count = drain + 1;
+};
+
+template <int MODE, int G>
 __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_constant__ Params p) {
+    using B = Bar<G>;
+    constexpr uint32_t kStages = Ring<G>::stages, kStageBytes = Ring<G>::stage_bytes;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024 - (tc::smem_addr(smraw) & 1023)) & 1023);
-    __shared__ uint64_t bars[bCount];
+    __shared__ uint64_t bars[B::count];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t first = blockIdx.x / G, stride = gridDim.x / G;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { tc::mbar_init(&bars[bFull + i], 1); tc::mbar_init(&bars[bEmpty + i], 1); }
-        for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[bAccFull + i], 1); tc::mbar_init(&bars[bAccEmpty + i], 4); }
-        tc::mbar_init(&bars[bDrain], 1);
+        for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 1); tc::mbar_init(&bars[B::empty + i], 1); }
+        for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[B::acc_full + i], 1); tc::mbar_init(&bars[B::acc_empty + i], 4 * G); }
+        tc::mbar_init(&bars[B::drain], 1);
         tc::fence_mbar_init();
         s_fail = 0;
     }
-    if (warp == 2) { tc::tmem_alloc(&s_tmem, 512); tc::fence_before_sync(); }
+    if (warp == 2) { pair_alloc<G>(&s_tmem); tc::fence_before_sync(); }
     __syncthreads();
+    if (G == 2) cluster_sync();                         // the other block's barriers exist
     tc::fence_after_sync();
     const uint32_t tm = s_tmem;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;                            // stages filled so far
+            uint32_t s = 0, round = 0;                  // next stage, times the ring went round
+            const uint32_t full0 = G == 2 ? leader_addr(&bars[B::full]) : tc::smem_addr(&bars[B::full]);
             TileId t;
             bool ok = true;
-            for (int64_t idx = blockIdx.x; ok && tile_at(p, idx, t); idx += gridDim.x) {
+            for (int64_t idx = first; ok && tile_at(p, idx, t); idx += stride) {
+                // what the loop needs is taken out of the parameters: one thread feeds the tensor
+                // cores, every instruction in it counts
                 const Prod &q = p.prod[t.which];
+                const CUtensorMap *ma = &q.a, *mb = &q.b;
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
-                const int32_t m0 = t.mt * kTM, n0 = t.nt * q.n;
-                const uint32_t bytes = (q.a_mn ? kABytes : q.a_rows * 128u) + q.n * 128u;
+                const int32_t nb = q.n / G;             // columns that this block holds
+                const int32_t m0 = (t.mt * G + rank) * kTM, n0 = t.nt * q.n + rank * nb, y0 = q.b_y0;
+                const int how_a = q.a_panel ? (q.a_mn ? 2 : 1) : 0, how_b = q.b_mn ? (q.b_panel ? 2 : 1) : 0;
+                const uint32_t bytes = ((q.a_mn ? kABytes : q.a_rows * 128u) + nb * 128u) * G;
                 for (int32_t k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % kStages, use = it / kStages;
-                    if (use > 0 && !wait_or_fail(&bars[bEmpty + s], (use - 1) & 1, &s_fail)) { ok = false; break; }
-                    uint64_t *full = &bars[bFull + s];
+                    if (round > 0 && !wait_or_fail(&bars[B::empty + s], (round - 1) & 1, &s_fail)) { ok = false; break; }
+                    const uint32_t full = full0 + s * 8;
                     uint8_t *a = sm + s * kStageBytes, *b = a + kABytes;
-                    tc::mbar_expect_tx(full, bytes);
-                    if (q.a_mn) {
-                        tc::tma_load_2d(a, &q.a, m0, k * kTK, full);
-                        tc::tma_load_2d(a + 8192, &q.a, m0 + 64, k * kTK, full);
-                    } else {
-                        tc::tma_load_2d(a, &q.a, k * kTK, m0, full);
-                    }
-                    if (q.b_mn) {
-                        for (int j = 0; j < q.n; j += 64) tc::tma_load_2d(b + j * 128, &q.b, n0 + j, q.b_y0 + k * kTK, full);
-                    } else {
-                        tc::tma_load_2d(b, &q.b, k * kTK, q.b_y0 + n0, full);
-                    }
+                    if (rank == 0) tc::mbar_expect_tx(&bars[B::full + s], bytes);
+                    if (how_a == 0) pair_load<G>(a, ma, k * kTK, m0, full);
+                    else if (how_a == 1) pair_load3<G>(a, ma, 0, m0, k, full);
+                    else pair_load3<G>(a, ma, 0, k * kTK, m0 / 64, full);
+                    if (how_b == 0) pair_load<G>(b, mb, k * kTK, y0 + n0, full);
+                    else if (how_b == 2) pair_load3<G>(b, mb, 0, y0 + k * kTK, n0 / 64, full);
+                    else for (int j = 0; j < nb; j += 64) pair_load<G>(b + j * 128, mb, n0 + j, y0 + k * kTK, full);
+                    if (++s == kStages) { s = 0; ++round; }
                 }
             }
             // Nothing may be in flight into this block's shared memory when it ends: the copies
             // (after a failure the products may not have waited for them), then the stages'
-            // last release.
+            // last release.  In a pair only the release says so for the second block; after a
+            // failure its wait runs out, long after the last copy.
             for (uint32_t s = 0; s < kStages; ++s) {
                 if (it <= s) continue;
                 const uint32_t uses = (it - s + kStages - 1) / kStages;
-                tc::mbar_wait(&bars[bFull + s], (uses - 1) & 1, 1000000000LL);
-                if (ok && !failed(&s_fail)) wait_or_fail(&bars[bEmpty + s], (uses - 1) & 1, &s_fail);
+                if (rank == 0) tc::mbar_wait(&bars[B::full + s], (uses - 1) & 1, 1000000000LL);
+                if (!tc::mbar_wait(&bars[B::empty + s], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL))
+                    atomicExch(&s_fail, 1);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, tile = 0;
+        if (lane == 0 && rank == 0) {
+            uint32_t s = 0, round = 0, tile = 0;
+            const uint32_t base = tc::smem_addr(sm);
             TileId t;
             bool ok = true;
-            for (int64_t idx = blockIdx.x; ok && tile_at(p, idx, t); idx += gridDim.x, ++tile) {
+            for (int64_t idx = first; ok && tile_at(p, idx, t); idx += stride, ++tile) {
                 const Prod &q = p.prod[t.which];
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
                 const uint32_t buf = tile & 1, use = tile >> 1, d = tm + buf * kTN;
-                const uint32_t id = tc::idesc_bf16(kTM, q.n, q.a_mn != 0, q.b_mn != 0);
-                if (use > 0 && !wait_or_fail(&bars[bAccEmpty + buf], (use - 1) & 1, &s_fail)) { ok = false; break; }
+                const uint32_t id = tc::idesc_bf16(kTM * G, q.n, q.a_mn != 0, q.b_mn != 0);
+                // descriptors of stage 0; 16 columns of K lie 32 bytes apart in an operand stored
+                // by rows and 2 KB apart in one stored by K (descriptors count 16 bytes)
+                const uint64_t da0 = q.a_mn ? tc::desc_sw128_mn(base, 8192) : tc::desc_sw128(base);
+                const uint64_t db0 = q.b_mn ? tc::desc_sw128_mn(base + kABytes, 8192) : tc::desc_sw128(base + kABytes);
+                const uint32_t ka = q.a_mn ? 128 : 2, kb = q.b_mn ? 128 : 2;
+                if (use > 0 && !wait_or_fail(&bars[B::acc_empty + buf], (use - 1) & 1, &s_fail)) { ok = false; break; }
                 tc::fence_after_sync();
-                for (int32_t k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!wait_or_fail(&bars[bFull + s], (it / kStages) & 1, &s_fail)) { ok = false; break; }
+                uint32_t acc = 0;
+                for (int32_t k = k0; k < k1; ++k) {
+                    if (!wait_or_fail(&bars[B::full + s], round & 1, &s_fail)) { ok = false; break; }
                     tc::fence_after_sync();
-                    const uint32_t a = tc::smem_addr(sm + s * kStageBytes), b = a + kABytes;
+                    const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
-                    for (int kk = 0; kk < kTK / 16; ++kk) {
-                        const uint64_t da = q.a_mn ? tc::desc_sw128_mn(a + kk * 2048, 8192) : tc::desc_sw128(a + kk * 32);
-                        const uint64_t db = q.b_mn ? tc::desc_sw128_mn(b + kk * 2048, 8192) : tc::desc_sw128(b + kk * 32);
-                        tc::mma_bf16(d, da, db, id, (k > k0 || kk > 0) ? 1u : 0u);
+                    for (uint32_t kk = 0; kk < kTK / 16; ++kk) {
+                        pair_mma<G>(d, da + kk * ka, db + kk * kb, id, acc);
+                        acc = 1;
                     }
-                    tc::mma_commit(&bars[bEmpty + s]);
+                    pair_commit<G>(&bars[B::empty + s]);
+                    if (++s == kStages) { s = 0; ++round; }
                 }
-                if (ok) tc::mma_commit(&bars[bAccFull + buf]);
+                if (ok) pair_commit<G>(&bars[B::acc_full + buf]);
             }
             if (failed(&s_fail)) {                      // let the products in flight end
-                if (p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
-                tc::mma_commit(&bars[bDrain]);
-                tc::mbar_wait(&bars[bDrain], 0, 1000000000LL);
+                pair_commit<G>(&bars[B::drain]);
+                tc::mbar_wait(&bars[B::drain], 0, 1000000000LL);
             }
         }
     } else if (warp >= kEpiWarp0) {
         const int lg = warp - kEpiWarp0;                // TMEM lanes 32 lg .. 32 lg + 31
         const uint32_t lane_off = static_cast<uint32_t>(lg * 32) << 16;
         uint8_t *out = sm + kStages * kStageBytes + lg * 8192;
+        const uint32_t released = G == 2 ? leader_addr(&bars[B::acc_empty]) : 0;
         uint32_t tile = 0, slot = 0;
         TileId t;
-        for (int64_t idx = blockIdx.x; tile_at(p, idx, t); idx += gridDim.x, ++tile) {
+        for (int64_t idx = first; tile_at(p, idx, t); idx += stride, ++tile) {
             const Prod &q = p.prod[t.which];
             const uint32_t buf = tile & 1;
-            if (!__all_sync(0xffffffffu, wait_or_fail(&bars[bAccFull + buf], (tile >> 1) & 1, &s_fail))) break;
+            if (!__all_sync(0xffffffffu, wait_or_fail(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail))) break;
             tc::fence_after_sync();
             const uint32_t acc = tm + buf * kTN + lane_off;
-            const int32_t n0 = t.nt * q.n, row = t.mt * kTM + lg * 32 + lane;
+            const int32_t n0 = t.nt * q.n, row = (t.mt * G + rank) * kTM + lg * 32 + lane;
             if (MODE == kFwd) {
                 const int32_t nv = min(q.n, q.cols - n0);       // columns that are vocabulary entries
                 float m = -INFINITY, s = 0.f;
@@ -267,13 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive(&bars[bAccEmpty + buf]);
+                if (lane == 0) {
+                    if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
+                }
                 if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
             } else {
                 RowInfo ri{0.f, 0.f, 0, 0};
                 if (MODE == kDz && row < q.rows) ri = p.rows[row];
                 const int step = q.out_f32 ? 32 : 64;
-                const int32_t y = t.mt * kTM + lg * 32;
+                const int32_t y = (t.mt * G + rank) * kTM + lg * 32;
                 for (int c = 0; c < q.n; c += step) {
                     uint8_t *dst = out + slot * 4096;
                     if (lane == 0) store_wait_read1();
@@ -292,6 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                         if (MODE == kDz) {
 #pragma unroll
                             for (int i = 0; i < 64; ++i) v[i] = ri.neg_g * ex2(fmaf(v[i], p.c2, -ri.lse2));
+                            if (n0 + c + 64 > q.cols) {         // past the vocabulary: dX must see zeros
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) if (n0 + c + i >= q.cols) v[i] = 0.f;
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -317,9 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                     tc::fence_smem_to_async();
                     __syncwarp();
                     if (lane == 0) {
-                        if (c + step >= q.n) arrive(&bars[bAccEmpty + buf]);
-                        if (y < q.rows && n0 + c < q.cols)
-                            store_3d(&q.out, n0 + c, q.out_y0 + y, t.split, dst, q.out_add != 0);
+                        if (c + step >= q.n) {
+                            if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
+                        }
+                        if (y < q.rows && n0 + c < q.cols) {
+                            if (MODE == kDz) store_3d(&q.out, 0, y, (n0 + c) / 64, dst, false);
+                            else store_3d(&q.out, n0 + c, q.out_y0 + y, t.split, dst, q.out_add != 0);
+                        }
                         tc::bulk_commit();
                     }
                     slot ^= 1;
@@ -330,8 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     }
     tc::fence_before_sync();
     __syncthreads();
+    if (tid == 0 && failed(&s_fail) && p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
+    if (G == 2) cluster_sync();                         // neither block ends under the other's copies or arrivals
     tc::fence_after_sync();
-    if (warp == 2) tc::tmem_dealloc(tm, 512);
+    if (warp == 2) pair_dealloc<G>(tm);
 }
 
 // ---- forward: joining the tiles, and the positions' own logits --------------------------
@@ -501,15 +611,20 @@ int sm_count() {
 int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Blocks that share a tile: pairs (256 rows) as soon as there are more rows than one block's
+// tile holds; a pair reads each operand row once where two blocks read the columns twice.
+int group_of(int64_t C) { return C > kTM ? 2 : 1; }
+
 // Tile width of a product with m_tiles row tiles over `cols` columns: the multiple of `unit`
-// up to 256 that leaves the least work on the busiest SM (16 columns stand for a tile's
-// fixed cost).
-int32_t tile_width(int32_t m_tiles, int64_t cols, int32_t unit) {
+// up to 256 that leaves the least work on the busiest pair or block (16 columns stand for a
+// tile's fixed cost).
+int32_t tile_width(int32_t m_tiles, int64_t cols, int32_t unit, int G) {
     int32_t best = kTN;
     int64_t cost = INT64_MAX;
+    const int64_t workers = sm_count() / G;
     for (int32_t n = kTN; n >= 64; n -= unit) {
         const int64_t tiles = int64_t(m_tiles) * ceil_div(cols, n);
-        const int64_t c = (tiles + sm_count() - 1) / sm_count() * (n + 16);
+        const int64_t c = (tiles + workers - 1) / workers * (n + 16);
         if (c < cost) { cost = c; best = n; }
     }
     return best;
@@ -521,6 +636,26 @@ bool map_in(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
     return encode_bf16(m, base, 2, dims, strides, box);
+}
+
+// dZ in panels of 64 columns, [panels][C][64]: every box that is written (32 rows), read as
+// rows (dX) or as columns (dW, 64 rows) is one contiguous run.  Row-major, a box's 64 or 128
+// rows lie a whole piece (128 KB) apart each.
+bool map_dz(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_rows, int32_t box_panels) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(C), static_cast<cuuint64_t>((nv + 63) / 64)};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(C) * 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_panels)};
+    return encode_bf16(m, dz, 3, dims, strides, box);
+}
+
+// A row-major [rows][D] operand that is read as columns, in boxes of 64 rows x `cols` columns:
+// as panels of 64 columns where D holds whole ones, else in boxes of one panel.
+bool map_cols(CUtensorMap *m, const void *base, int64_t rows, int64_t D, int32_t cols) {
+    if (D % 64) return map_in(m, base, rows, D, D, 64);
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, 128};
+    const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(cols / 64)};
+    return encode_bf16(m, base, 3, dims, strides, box);
 }
 
 // [layers][rows][cols], written in boxes of 128 bytes x 32 rows.
@@ -536,15 +671,29 @@ bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t c
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
-cudaError_t launch_tiles(const Params &p, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <int MODE, int G>
+cudaError_t launch_group(const Params &p, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<MODE, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Ring<G>::smem);
     if (e != cudaSuccess) return e;
     int64_t items = 0;
     for (int i = 0; i < p.n_prod; ++i) items += int64_t(p.prod[i].m_tiles) * p.prod[i].n_tiles * p.prod[i].splits;
-    const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));
-    head_tile_kernel<MODE><<<grid, kThreads, kSmem, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, sm_count() / G) * G));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<G>::smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = G;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = G == 2 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, head_tile_kernel<MODE, G>, p);
+}
+template <int MODE>
+cudaError_t launch_tiles(const Params &p, int G, cudaStream_t st) {
+    return G == 2 ? launch_group<MODE, 2>(p, st) : launch_group<MODE, 1>(p, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -570,7 +719,10 @@ int cuda_fail(cudaError_t e, const char *what) {
     return HARTS_ECUDA;
 }
 
-int32_t fwd_width(int64_t C, int32_t V) { return tile_width(ceil_div(C, kTM), V, 16); }
+int32_t fwd_width(int64_t C, int32_t V) {
+    const int G = group_of(C);
+    return tile_width(ceil_div(C, kTM * G), V, 16 * G, G);
+}
 
 SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
     SemParams s{};
@@ -596,13 +748,14 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     want = std::max<int64_t>(kTN, want / kTN * kTN);
     b.piece = static_cast<int32_t>(std::min<int64_t>(want, (int64_t(V) + 63) / 64 * 64));
     b.n_pieces = ceil_div(V, b.piece);
-    const int32_t mt = ceil_div(C, kTM);
-    b.n_dz = tile_width(mt, std::min<int32_t>(b.piece, V), 64);
-    b.n_grad = std::min<int32_t>(kTN, (D + 63) / 64 * 64);
-    if (D > kTN) b.n_grad = (ceil_div(D, ceil_div(D, kTN)) + 63) / 64 * 64;
+    const int G = group_of(C);
+    const int32_t mt = ceil_div(C, kTM * G);
+    b.n_dz = tile_width(mt, std::min<int32_t>(b.piece, V), 64, G);
+    const int32_t unit = 64 * G;                        // columns stored [K][columns] come in 64s per block
+    b.n_grad = (ceil_div(D, ceil_div(D, kTN)) + unit - 1) / unit * unit;
     const int32_t kb = ceil_div(std::min<int32_t>(b.piece, V), kTK), tiles = mt * ceil_div(D, b.n_grad);
     // about two rounds of dX tiles over the SMs, each at least 16 steps deep
-    b.splits = std::max(1, std::min({static_cast<int32_t>(ceil_div(2 * sm_count(), tiles)), ceil_div(kb, 16), int32_t(32)}));
+    b.splits = std::max(1, std::min({static_cast<int32_t>(ceil_div(2 * sm_count() / G, tiles)), ceil_div(kb, 16), int32_t(32)}));
     b.k_per = ceil_div(kb, b.splits);
     b.splits = ceil_div(kb, b.k_per);
     b.acc = b.splits > 1 || b.n_pieces > 1;
@@ -640,7 +793,8 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     Params p;
     std::memset(&p, 0, sizeof(p));
     Prod &q = p.prod[0];
-    q.m_tiles = ceil_div(a->C, kTM);
+    const int G = group_of(a->C);
+    q.m_tiles = ceil_div(a->C, kTM * G);
     q.n = fwd_width(a->C, a->V);
     q.n_tiles = ceil_div(a->V, q.n);
     q.splits = 1;
@@ -652,11 +806,11 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     p.error = a->error;
     p.c2 = a->scale * kLog2e;
     p.part = static_cast<float2 *>(a->workspace);
-    if (!map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows) || !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n)) {
+    if (!map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows) || !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n / G)) {
         set_error("tensor map");
         return HARTS_ECUDA;
     }
-    cudaError_t e = launch_tiles<kFwd>(p, st);
+    cudaError_t e = launch_tiles<kFwd>(p, G, st);
     if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
     head_lse_kernel<<<ceil_div(a->C, 8), 256, 0, st>>>(p.part, a->lse, a->C, q.n_tiles);
     if (a->S > 0) head_logp_kernel<<<ceil_div(a->S, 8), 256, 0, st>>>(sem_params(a));
@@ -701,20 +855,20 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
     head_rows_kernel<<<ceil_div(f.C, 8), 256, 0, st>>>(s);
 
-    const int32_t mt = ceil_div(f.C, kTM), C = static_cast<int32_t>(f.C);
+    const int G = group_of(f.C);
+    const int32_t mt = ceil_div(f.C, kTM * G), C = static_cast<int32_t>(f.C);
     const int32_t a_rows = static_cast<int32_t>(std::min<int64_t>(kTM, (f.C + 7) / 8 * 8));
     Params pz, pg;
     std::memset(&pz, 0, sizeof(pz));
     std::memset(&pg, 0, sizeof(pg));
     Prod &z = pz.prod[0], &gx = pg.prod[0], &gw = pg.prod[1];
-    bool ok = map_in(&z.a, f.x, f.C, f.D, f.D, a_rows) && map_in(&z.b, f.weight, f.V, f.D, f.D, b.n_dz) &&
-              map_in(&gx.b, f.weight, f.V, f.D, f.D, 64) && map_in(&gw.b, f.x, f.C, f.D, f.D, 64) &&
+    bool ok = map_in(&z.a, f.x, f.C, f.D, f.D, a_rows) && map_in(&z.b, f.weight, f.V, f.D, f.D, b.n_dz / G) &&
+              map_cols(&gx.b, f.weight, f.V, f.D, b.n_grad / G) && map_cols(&gw.b, f.x, f.C, f.D, b.n_grad / G) &&
               map_out(&gw.out, a->dweight, 1, f.V, f.D, f.D, false) &&
               (b.acc ? map_out(&gx.out, acc, b.splits, f.C, f.D, f.D, true) : map_out(&gx.out, a->dx, 1, f.C, f.D, f.D, false));
     for (int32_t i = 0; ok && i < b.n_pieces; ++i) {
         const int32_t v0 = i * b.piece, nv = std::min(b.piece, f.V - v0);
-        ok = map_out(&z.out, dz, 1, f.C, nv, b.piece, false) && map_in(&gx.a, dz, f.C, nv, b.piece, a_rows) &&
-             map_in(&gw.a, dz, f.C, nv, b.piece, 64);
+        ok = map_dz(&z.out, dz, f.C, nv, 32, 1) && map_dz(&gx.a, dz, f.C, nv, a_rows, 1) && map_dz(&gw.a, dz, f.C, nv, 64, 2);
         if (!ok) break;
         // logits of the piece, as dz
         z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
@@ -722,17 +876,17 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
         pz.n_prod = 1; pz.error = f.error; pz.c2 = f.scale * kLog2e;
         pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0;
-        cudaError_t e = launch_tiles<kDz>(pz, st);
+        cudaError_t e = launch_tiles<kDz>(pz, G, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
         // dX (first: its tiles are the longest) and dW
-        gx.b_mn = 1; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
+        gx.b_mn = 1; gx.a_panel = gw.a_panel = 1; gx.b_panel = gw.b_panel = f.D % 64 == 0; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
         gx.k_blocks = ceil_div(nv, kTK); gx.k_per = b.k_per; gx.splits = ceil_div(gx.k_blocks, b.k_per);
         gx.b_y0 = v0; gx.out_y0 = 0; gx.rows = C; gx.cols = f.D; gx.out_f32 = b.acc; gx.out_add = i > 0;
-        gw.a_mn = gw.b_mn = 1; gw.m_tiles = ceil_div(nv, kTM); gw.n = b.n_grad; gw.n_tiles = ceil_div(f.D, b.n_grad);
+        gw.a_mn = gw.b_mn = 1; gw.m_tiles = ceil_div(nv, kTM * G); gw.n = b.n_grad; gw.n_tiles = ceil_div(f.D, b.n_grad);
         gw.k_blocks = gw.k_per = ceil_div(f.C, kTK); gw.splits = 1;
         gw.out_y0 = v0; gw.rows = nv; gw.cols = f.D; gw.fast_n = 1;
         pg.n_prod = 2; pg.error = f.error;
-        e = launch_tiles<kGrad>(pg, st);
+        e = launch_tiles<kGrad>(pg, G, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     }
     if (!ok) { set_error("tensor map"); return HARTS_ECUDA; }

@@ -291,19 +291,22 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
     }
 }
 
-// dw[j] = sum over the groups' column sums, in ascending order within eight interleaved
-// chains that are then added in order.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *part, float *dw, int32_t D, int32_t groups) {
-    __shared__ float sm[8][33];
+// dw[j] = sum over the groups' column sums: 32 warps take every 32nd group each, in ascending
+// order, and are added in order.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, float *dw, int32_t D, int32_t groups) {
+    __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int32_t col = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (col < D)
-        for (int32_t g = k; g < groups; g += 8) s += part[static_cast<int64_t>(g) * D + col];
+    if (col < D) {
+#pragma unroll 8
+        for (int32_t g = k; g < groups; g += 32) s += part[static_cast<int64_t>(g) * D + col];
+    }
     sm[k][lane] = s;
     __syncthreads();
     if (k == 0 && col < D) {
-        for (int i = 1; i < 8; ++i) s += sm[i][lane];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) s += sm[i][lane];
         dw[col] = s;
     }
 }
@@ -454,7 +457,7 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
         if (s.vec == 4) HARTS_NORM_DISPATCH(launch_bwd, float, 4, 4, p, s, grid, st);
         else HARTS_NORM_DISPATCH(launch_bwd, float, 1, 8, p, s, grid, st);
     }
-    rmsnorm_dw_kernel<<<(a->D + 31) / 32, 256, 0, st>>>(p.part, a->dweight, a->D, static_cast<int32_t>(groups));
+    rmsnorm_dw_kernel<<<(a->D + 31) / 32, 1024, 0, st>>>(p.part, a->dweight, a->D, static_cast<int32_t>(groups));
     return launched("rmsnorm backward launch");
 }
 
