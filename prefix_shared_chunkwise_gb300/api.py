@@ -350,17 +350,23 @@ def attn_bwd(plan: Plan, q, k, v, o, lse, d_o, *, scale=None, dq=None, dk=None, 
     return dq, dk, dv
 
 
-def _row_stream(stream, device):
-    """The stream to enqueue on: the given one, or the current one of `device`."""
+def _stream_on(stream, t):
+    """The raw handle of the given stream, or of the current one of `t`'s device (without
+    building a Stream object: this runs in every call, some of which take a few us)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors are on {t.device}, expected a CUDA device")
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _ready(name, t, shape, dtype, device):
-    """_need, and contiguous: what every buffer of the operators below has to be."""
-    _need(name, t, shape, dtype, None, device)
-    if t is not None and not t.is_contiguous():
+    """_need, and contiguous: what every buffer of the operators below has to be.  None is
+    an absent buffer; a shape or dtype of None is not compared."""
+    if t is None:
+        return
+    if ((shape is not None and t.shape != shape) or (dtype is not None and t.dtype is not dtype)
+            or t.device != device or not t.is_contiguous()):
+        _need(name, t, shape, dtype, None, device)
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -405,7 +411,7 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None
         rstd = torch.empty(C, dtype=f32, device=dev)
     _ready("rstd", rstd, (C,), f32, dev)
     a.x, a.weight, a.rstd = x.data_ptr(), weight.data_ptr(), rstd.data_ptr()
-    L.check(L.lib().harts_rmsnorm_fwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_rmsnorm_fwd")
+    L.check(L.lib().harts_rmsnorm_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_rmsnorm_fwd")
     return y, h, rstd
 
 
@@ -436,7 +442,7 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, workspac
     a.dy, a.h, a.dh = dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr()
     a.weight, a.rstd, a.dx, a.dweight = weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr()
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_rmsnorm_bwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_rmsnorm_bwd")
+    L.check(L.lib().harts_rmsnorm_bwd(ctypes.byref(a), _stream_on(stream, h)), "harts_rmsnorm_bwd")
     return dx, dweight
 
 
@@ -470,7 +476,7 @@ class GradSet:
             norm = torch.empty((), dtype=torch.float32, device=self._dev)
         _need("norm", norm, None, torch.float32, 4, self._dev)
         L.check(L.lib().harts_grad_norm(self._list, len(self.grads), norm.data_ptr(), self._ws.data_ptr(),
-                                        self._ws.numel(), _row_stream(stream, self._dev)), "harts_grad_norm")
+                                        self._ws.numel(), _stream_on(stream, norm)), "harts_grad_norm")
         return norm
 
     def clip(self, max_norm, *, norm=None, stream=None):
@@ -480,7 +486,7 @@ class GradSet:
             norm = torch.empty((), dtype=torch.float32, device=self._dev)
         _need("norm", norm, None, torch.float32, 4, self._dev)
         L.check(L.lib().harts_grad_clip(self._list, len(self.grads), float(max_norm), norm.data_ptr(),
-                                        self._ws.data_ptr(), self._ws.numel(), _row_stream(stream, self._dev)),
+                                        self._ws.data_ptr(), self._ws.numel(), _stream_on(stream, norm)),
                 "harts_grad_clip")
         return norm
 
@@ -530,7 +536,7 @@ def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=No
     a = _head_args(x, weight, row_ptr, row_sem, target, scale, lse, logp, error)
     workspace = _head_workspace(workspace, int(L.lib().harts_linear_logprob_fwd_workspace_bytes(a.C, a.V, a.D)), dev)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_linear_logprob_fwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_linear_logprob_fwd")
+    L.check(L.lib().harts_linear_logprob_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_fwd")
     return logp, lse
 
 
@@ -555,5 +561,5 @@ def linear_logprob_bwd(x, weight, row_ptr, row_sem, target, lse, dlogp, *, scale
     nb = int(L.lib().harts_linear_logprob_bwd_workspace_bytes(f.C, f.V, f.D, f.S, max(piece, 0)))
     workspace = _head_workspace(workspace, nb, dev)
     a.fwd.workspace, a.fwd.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_linear_logprob_bwd(ctypes.byref(a), _row_stream(stream, dev)), "harts_linear_logprob_bwd")
+    L.check(L.lib().harts_linear_logprob_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_bwd")
     return dx, dweight

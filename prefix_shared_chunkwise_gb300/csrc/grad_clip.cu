@@ -18,6 +18,7 @@
 #include <cmath>
 #include <string>
 
+#include "launch_util.h"
 #include "plan_internal.h"
 
 namespace harts {
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __
     __shared__ double sm[kThreads / 32];
     __shared__ int s_wide;
     double sum = 0.0;
+    let_next_start();
     for (int32_t c = blockIdx.x; c < s.chunks; c += gridDim.x) {
         const Item &it = s.item[find(s, c)];
         const int64_t at = static_cast<int64_t>(c - it.chunk0) * s.chunk;
@@ -232,6 +234,7 @@ __device__ void scale(const T *g, U *out, int64_t n, float f) {
 
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Set s) {
     __shared__ float s_f;
+    wait_previous();
     if (threadIdx.x < 32) {
         const double norm = norm_of(s.part, s.partials);
         if (threadIdx.x == 0) {
@@ -257,12 +260,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __gr
             default: scale(gb, ob, n, f); break;
         }
     }
-}
-
-int sm_count() {
-    int dev = 0, n = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
 }
 
 // Walks the tensors in launches of up to kSet; 0 or an error code.  `sets` receives the
@@ -329,8 +326,10 @@ int run(const harts_grad_tensor *t, int32_t count, bool clip, float max_norm, fl
             const int grid = std::max(1, std::min(s.chunks, grid_limit()));
             s.first = first;
             s.partials = partials;
-            if (pass == 0) grad_squares_kernel<<<grid, kThreads, 0, st>>>(s);
-            else grad_scale_kernel<<<grid, kThreads, 0, st>>>(s);
+            // the first scaling is set up while the last squares are summed
+            const cudaError_t e = pass == 0 ? launch(grad_squares_kernel, grid, kThreads, 0, 1, false, st, s)
+                                            : launch(grad_scale_kernel, grid, kThreads, 0, 1, first == 0, st, s);
+            if (e != cudaSuccess) { set_error(std::string("gradient norm launch: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
             first += grid;
         } while (i < count);
         partials = first;

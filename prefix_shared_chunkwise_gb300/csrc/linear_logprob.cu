@@ -27,6 +27,7 @@
 #include <cstring>
 
 #include "kda_common.cuh"
+#include "launch_util.h"
 #include "tc_primitives.cuh"
 #include "tensor_map.h"
 
@@ -69,6 +70,7 @@ struct alignas(16) RowInfo { float neg_g, lse2; int32_t count, first; };   // -s
 struct Params {
     Prod prod[2];
     int32_t n_prod;
+    int32_t extra;                  // see tile_at
     int32_t *error;
     float c2;                       // scale * log2 e
     float2 *part;                   // forward: [C][n_tiles]
@@ -80,19 +82,30 @@ struct Params {
 
 struct TileId { int which, mt, nt, split; };
 
-__device__ __forceinline__ bool tile_at(const Params &p, int64_t idx, TileId &t) {
-    int which = 0;
-    int64_t items = static_cast<int64_t>(p.prod[0].m_tiles) * p.prod[0].n_tiles * p.prod[0].splits;
-    if (idx >= items) {
+// The n-th tile of worker `w` of `workers` (blocks or pairs).  Tiles of the first product go
+// round the workers; those of the second follow, the workers that got one tile less of the
+// first taking `extra` of them before the others join in.
+__device__ __forceinline__ bool tile_at(const Params &p, int64_t n, int64_t w, int64_t workers, TileId &t) {
+    const int64_t x = static_cast<int64_t>(p.prod[0].m_tiles) * p.prod[0].n_tiles * p.prod[0].splits;
+    int64_t idx = w + n * workers;
+    t.which = 0;
+    if (idx >= x) {
         if (p.n_prod < 2) return false;
-        idx -= items;
-        which = 1;
-        items = static_cast<int64_t>(p.prod[1].m_tiles) * p.prod[1].n_tiles * p.prod[1].splits;
-        if (idx >= items) return false;
+        t.which = 1;
+        const int64_t over = x % workers, few = workers - over;      // workers with a tile less, if any
+        int64_t m = n - (x > w ? (x - w + workers - 1) / workers : 0);
+        if (over == 0) {
+            idx = w + m * workers;
+        } else if (w >= over && m < p.extra) {
+            idx = (w - over) + m * few;
+        } else {
+            if (w >= over) m -= p.extra;
+            idx = few * p.extra + w + m * workers;
+        }
+        if (idx >= static_cast<int64_t>(p.prod[1].m_tiles) * p.prod[1].n_tiles * p.prod[1].splits) return false;
     }
-    const Prod &q = p.prod[which];
+    const Prod &q = p.prod[t.which];
     const int32_t per = q.m_tiles * q.n_tiles;
-    t.which = which;
     t.split = static_cast<int>(idx / per);
     const int32_t r = static_cast<int32_t>(idx - static_cast<int64_t>(t.split) * per);
     // groups of tiles along the fast side run against every tile of the other
@@ -224,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     __shared__ int s_fail;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t first = blockIdx.x / G, stride = gridDim.x / G;
+    const int64_t worker = blockIdx.x / G, workers = gridDim.x / G;
 
     if (tid == 0) {
         for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 1); tc::mbar_init(&bars[B::empty + i], 1); }
@@ -237,16 +250,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     __syncthreads();
     if (G == 2) cluster_sync();                         // the other block's barriers exist
     tc::fence_after_sync();
+    let_next_start();
     const uint32_t tm = s_tmem;
 
     if (warp == 0) {
         if (lane == 0) {
+            if (MODE == kGrad) wait_previous();         // dZ is complete
             uint32_t it = 0;                            // stages filled so far
             uint32_t s = 0, round = 0;                  // next stage, times the ring went round
             const uint32_t full0 = G == 2 ? leader_addr(&bars[B::full]) : tc::smem_addr(&bars[B::full]);
             TileId t;
             bool ok = true;
-            for (int64_t idx = first; ok && tile_at(p, idx, t); idx += stride) {
+            for (int64_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
                 // what the loop needs is taken out of the parameters: one thread feeds the tensor
                 // cores, every instruction in it counts
                 const Prod &q = p.prod[t.which];
@@ -288,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             const uint32_t base = tc::smem_addr(sm);
             TileId t;
             bool ok = true;
-            for (int64_t idx = first; ok && tile_at(p, idx, t); idx += stride, ++tile) {
+            for (; ok && tile_at(p, tile, worker, workers, t); ++tile) {
                 const Prod &q = p.prod[t.which];
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
                 const uint32_t buf = tile & 1, use = tile >> 1, d = tm + buf * kTN;
@@ -327,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         const uint32_t released = G == 2 ? leader_addr(&bars[B::acc_empty]) : 0;
         uint32_t tile = 0, slot = 0;
         TileId t;
-        for (int64_t idx = first; tile_at(p, idx, t); idx += stride, ++tile) {
+        if (MODE == kDz) wait_previous();               // rows' terms; the last piece's dZ has been read
+        for (; tile_at(p, tile, worker, workers, t); ++tile) {
             const Prod &q = p.prod[t.which];
             const uint32_t buf = tile & 1;
             if (!__all_sync(0xffffffffu, wait_or_fail(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail))) break;
@@ -446,31 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
 
 // ---- forward: joining the tiles, and the positions' own logits --------------------------
 
-// One warp a row: lse from the row's (max, sum) pairs, which are in units of log 2.
-__global__ void __launch_bounds__(256) head_lse_kernel(const float2 *part, float *lse, int64_t C, int32_t tiles) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (c >= C) return;
-    const float2 *q = part + c * tiles;
-    float m = -INFINITY, s = 0.f;
-    for (int32_t i = lane; i < tiles; i += 32) {
-        const float2 t = q[i];
-        const float n = fmaxf(m, t.x);
-        s = s * exp2f(m - n) + t.y * exp2f(t.x - n);
-        if (m == -INFINITY) s = t.y;
-        m = n;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float n = fmaxf(m, m2);
-        const float a = m == -INFINITY ? 0.f : s * exp2f(m - n), b = m2 == -INFINITY ? 0.f : s2 * exp2f(m2 - n);
-        s = a + b;
-        m = n;
-    }
-    if (lane == 0) lse[c] = (m + log2f(s)) * kLn2;
-}
-
 // x_c . w_y over D (a multiple of 8), one warp; every lane returns it.
 __device__ __forceinline__ float row_dot(const __nv_bfloat16 *x, const __nv_bfloat16 *w, int32_t D) {
     const int lane = threadIdx.x & 31;
@@ -495,31 +486,65 @@ struct SemParams {
     const __nv_bfloat16 *x, *w;
     const int32_t *row_ptr, *row_sem, *target;
     const float *lse, *dlogp;
-    float *logp;
+    float *logp, *lse_out;
+    const float2 *part;             // forward: [C][tiles]
     RowInfo *rows;
     int32_t *ent_y;
     float *ent_v;
     int64_t C, S;
-    int32_t V, D;
+    int32_t V, D, tiles;
     float scale;
 };
 
-// One warp a position (the q-th of row_sem): its row by binary search in row_ptr.
-__global__ void __launch_bounds__(256) head_logp_kernel(SemParams p) {
+// lse of row c from its (max, sum) pairs, which are in units of log 2; one warp, every lane
+// returns it.
+__device__ __forceinline__ float row_lse(const float2 *part, int64_t c, int32_t tiles) {
+    const float2 *q = part + c * tiles;
+    float m = -INFINITY, s = 0.f;
+    for (int32_t i = threadIdx.x & 31; i < tiles; i += 32) {
+        const float2 t = q[i];
+        const float n = fmaxf(m, t.x);
+        s = (m == -INFINITY ? 0.f : s * exp2f(m - n)) + (n == -INFINITY ? t.y : t.y * exp2f(t.x - n));
+        m = n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float n = fmaxf(m, m2);
+        const float a = m == -INFINITY ? s : s * exp2f(m - n), b = m2 == -INFINITY ? s2 : s2 * exp2f(m2 - n);
+        s = a + b;
+        m = n;
+    }
+    return (m + log2f(s)) * kLn2;
+}
+
+// One warp a position (the q-th of row_sem; its row by binary search in row_ptr), then one
+// warp a row.  A position's own logit needs only the inputs: it is formed while the tiles are
+// still being computed.  Every position joins its row's pairs itself -- a few kilobytes, as
+// much as its dot product reads -- so that no position waits for another warp.
+__global__ void __launch_bounds__(256) head_finish_kernel(SemParams p) {
     const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (q >= p.S) return;
+    const int lane = threadIdx.x & 31;
+    if (q >= p.S + p.C) return;
+    if (q >= p.S) {
+        wait_previous();
+        const float lse = row_lse(p.part, q - p.S, p.tiles);
+        if (lane == 0) p.lse_out[q - p.S] = lse;
+        return;
+    }
     int64_t lo = 0, hi = p.C;                       // last row with row_ptr <= q
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) >> 1;
         if (__ldg(p.row_ptr + mid) <= q) lo = mid; else hi = mid;
     }
     const int32_t s = __ldg(p.row_sem + q);
-    if (s < 0 || s >= p.S) return;
-    const int32_t y = __ldg(p.target + s);
+    const int32_t y = s >= 0 && s < p.S ? __ldg(p.target + s) : -1;
+    const bool labelled = y >= 0 && y < p.V;
     float r = 0.f;
-    if (y >= 0 && y < p.V)
-        r = p.scale * row_dot(p.x + lo * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D) - p.lse[lo];
-    if ((threadIdx.x & 31) == 0) p.logp[s] = r;
+    if (labelled) r = p.scale * row_dot(p.x + lo * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
+    wait_previous();
+    if (labelled) r -= row_lse(p.part, lo, p.tiles);
+    if (lane == 0 && s >= 0 && s < p.S) p.logp[s] = r;
 }
 
 // ---- backward: per row, G and the distinct labels with a gradient of their own ----------
@@ -530,6 +555,7 @@ __global__ void __launch_bounds__(256) head_logp_kernel(SemParams p) {
 __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    let_next_start();
     if (c >= p.C) return;
     const int32_t b = max(0, __ldg(p.row_ptr + c));
     const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
@@ -583,12 +609,15 @@ __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
 }
 
 // dX in bf16 from the splits' fp32 sums, in ascending order.
-__global__ void __launch_bounds__(256) head_dx_kernel(const float *acc, __nv_bfloat16 *dx, int64_t n, int32_t splits) {
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < n;
+struct DxParams { const float *acc; __nv_bfloat16 *dx; int64_t n; int32_t splits; };
+__global__ void __launch_bounds__(256) head_dx_kernel(DxParams p) {
+    wait_previous();
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < p.n;
          i += static_cast<int64_t>(gridDim.x) * 256 * 8) {
         float v[8] = {};
-        for (int32_t s = 0; s < splits; ++s) {
-            const float4 *q = reinterpret_cast<const float4 *>(acc + s * n + i);
+#pragma unroll 4
+        for (int32_t s = 0; s < p.splits; ++s) {
+            const float4 *q = reinterpret_cast<const float4 *>(p.acc + s * p.n + i);
             const float4 a = q[0], b = q[1];
             v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
             v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
@@ -596,19 +625,12 @@ __global__ void __launch_bounds__(256) head_dx_kernel(const float *acc, __nv_bfl
         uint4 u;
         u.x = tc::pack_bf16(v[0], v[1]); u.y = tc::pack_bf16(v[2], v[3]);
         u.z = tc::pack_bf16(v[4], v[5]); u.w = tc::pack_bf16(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(dx + i) = u;
+        *reinterpret_cast<uint4 *>(p.dx + i) = u;
     }
 }
 
 // ---- host ---------------------------------------------------------------------------------
 
-int sm_count() {
-    int dev = 0, n = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-}
-
-int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Blocks that share a tile: pairs (256 rows) as soon as there are more rows than one block's
@@ -672,28 +694,25 @@ bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t c
 }
 
 template <int MODE, int G>
-cudaError_t launch_group(const Params &p, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<MODE, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Ring<G>::smem);
+cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(head_tile_kernel<MODE, G>, Ring<G>::smem, done);
     if (e != cudaSuccess) return e;
-    int64_t items = 0;
-    for (int i = 0; i < p.n_prod; ++i) items += int64_t(p.prod[i].m_tiles) * p.prod[i].n_tiles * p.prod[i].splits;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, sm_count() / G) * G));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<G>::smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = G;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = G == 2 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, head_tile_kernel<MODE, G>, p);
+    int64_t items[2] = {0, 0};
+    for (int i = 0; i < p.n_prod; ++i) items[i] = int64_t(p.prod[i].m_tiles) * p.prod[i].n_tiles * p.prod[i].splits;
+    const int64_t workers = std::min<int64_t>(items[0] + items[1], sm_count() / G);
+    p.extra = 0;
+    if (p.n_prod == 2 && items[0] % workers) {
+        // a tile costs its K steps and about three more for its ends
+        const int64_t few = workers - items[0] % workers;
+        const int64_t even = (p.prod[0].k_per + 3 + (p.prod[1].k_per + 3) / 2) / (p.prod[1].k_per + 3);
+        p.extra = static_cast<int32_t>(std::min(even, items[1] / few));
+    }
+    return launch(head_tile_kernel<MODE, G>, workers * G, kThreads, Ring<G>::smem, G, behind, st, p);
 }
 template <int MODE>
-cudaError_t launch_tiles(const Params &p, int G, cudaStream_t st) {
-    return G == 2 ? launch_group<MODE, 2>(p, st) : launch_group<MODE, 1>(p, st);
+cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {
+    return G == 2 ? launch_group<MODE, 2>(p, behind, st) : launch_group<MODE, 1>(p, behind, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -727,7 +746,7 @@ int32_t fwd_width(int64_t C, int32_t V) {
 SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
     SemParams s{};
     s.x = static_cast<const __nv_bfloat16 *>(a->x); s.w = static_cast<const __nv_bfloat16 *>(a->weight);
-    s.row_ptr = a->row_ptr; s.row_sem = a->row_sem; s.target = a->target; s.lse = a->lse; s.logp = a->logp;
+    s.row_ptr = a->row_ptr; s.row_sem = a->row_sem; s.target = a->target; s.lse = s.lse_out = a->lse; s.logp = a->logp;
     s.C = a->C; s.S = a->S; s.V = a->V; s.D = a->D; s.scale = a->scale;
     return s;
 }
@@ -810,11 +829,11 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
         set_error("tensor map");
         return HARTS_ECUDA;
     }
-    cudaError_t e = launch_tiles<kFwd>(p, G, st);
-    if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
-    head_lse_kernel<<<ceil_div(a->C, 8), 256, 0, st>>>(p.part, a->lse, a->C, q.n_tiles);
-    if (a->S > 0) head_logp_kernel<<<ceil_div(a->S, 8), 256, 0, st>>>(sem_params(a));
-    e = cudaGetLastError();
+    SemParams s = sem_params(a);
+    s.part = p.part;
+    s.tiles = q.n_tiles;
+    cudaError_t e = launch_tiles<kFwd>(p, G, false, st);
+    if (e == cudaSuccess) e = launch(head_finish_kernel, (a->S + a->C + 7) / 8, 256, 0, 1, true, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
     set_error("");
     return HARTS_OK;
@@ -853,7 +872,8 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.rows = reinterpret_cast<RowInfo *>(ws + b.rows);
     s.ent_y = reinterpret_cast<int32_t *>(ws + b.ent_y);
     s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
-    head_rows_kernel<<<ceil_div(f.C, 8), 256, 0, st>>>(s);
+    const cudaError_t first = launch(head_rows_kernel, ceil_div(f.C, 8), 256, 0, 1, false, st, s);
+    if (first != cudaSuccess) return cuda_fail(first, "linear log-prob backward launch");
 
     const int G = group_of(f.C);
     const int32_t mt = ceil_div(f.C, kTM * G), C = static_cast<int32_t>(f.C);
@@ -876,7 +896,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
         pz.n_prod = 1; pz.error = f.error; pz.c2 = f.scale * kLog2e;
         pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0;
-        cudaError_t e = launch_tiles<kDz>(pz, G, st);
+        cudaError_t e = launch_tiles<kDz>(pz, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
         // dX (first: its tiles are the longest) and dW
         gx.b_mn = 1; gx.a_panel = gw.a_panel = 1; gx.b_panel = gw.b_panel = f.D % 64 == 0; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
@@ -886,17 +906,16 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         gw.k_blocks = gw.k_per = ceil_div(f.C, kTK); gw.splits = 1;
         gw.out_y0 = v0; gw.rows = nv; gw.cols = f.D; gw.fast_n = 1;
         pg.n_prod = 2; pg.error = f.error;
-        e = launch_tiles<kGrad>(pg, G, st);
+        e = launch_tiles<kGrad>(pg, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     }
     if (!ok) { set_error("tensor map"); return HARTS_ECUDA; }
     if (b.acc) {
-        const int64_t n = f.C * f.D;
-        const int grid = static_cast<int>(std::min<int64_t>((n / 8 + 255) / 256, int64_t(sm_count()) * 8));
-        head_dx_kernel<<<grid, 256, 0, st>>>(acc, static_cast<__nv_bfloat16 *>(a->dx), n, b.splits);
+        const DxParams d{acc, static_cast<__nv_bfloat16 *>(a->dx), f.C * f.D, b.splits};
+        const int64_t blocks = std::min<int64_t>((d.n / 8 + 255) / 256, int64_t(sm_count()) * 8);
+        const cudaError_t e = launch(head_dx_kernel, blocks, 256, 0, 1, true, st, d);
+        if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     set_error("");
     return HARTS_OK;
 }

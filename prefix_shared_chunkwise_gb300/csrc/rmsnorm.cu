@@ -21,6 +21,7 @@
 #include <cstring>
 
 #include "kda_common.cuh"
+#include "launch_util.h"
 
 namespace harts {
 namespace {
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
     float w[NV][VEC], dw[NV][VEC];
     Raw<T, VEC> a[NV], b[NV], e[NV];
     float rstd = 0.f;
+    let_next_start();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int32_t col = (j * R + t) * VEC;
@@ -293,21 +295,23 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
 
 // dw[j] = sum over the groups' column sums: 32 warps take every 32nd group each, in ascending
 // order, and are added in order.
-__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, float *dw, int32_t D, int32_t groups) {
+struct DwParams { const float *part; float *dw; int32_t D, groups; };
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(DwParams p) {
     __shared__ float sm[32][33];
+    wait_previous();
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int32_t col = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (col < D) {
+    if (col < p.D) {
 #pragma unroll 8
-        for (int32_t g = k; g < groups; g += 32) s += part[static_cast<int64_t>(g) * D + col];
+        for (int32_t g = k; g < p.groups; g += 32) s += p.part[static_cast<int64_t>(g) * p.D + col];
     }
     sm[k][lane] = s;
     __syncthreads();
-    if (k == 0 && col < D) {
+    if (k == 0 && col < p.D) {
 #pragma unroll
         for (int i = 1; i < 32; ++i) s += sm[i][lane];
-        dw[col] = s;
+        p.dw[col] = s;
     }
 }
 
@@ -321,12 +325,6 @@ Shape shape_of(int32_t dtype, int32_t D) {
     const int per = s.vec == 1 ? 8 : 16;
     s.r = D <= 32 * per ? 32 : D <= 128 * per ? 128 : D <= 256 * per ? 256 : D <= 512 * per ? 512 : 1024;
     return s;
-}
-
-int sm_count() {
-    int dev = 0, n = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
 }
 
 // Groups of R threads that work at a time, at most: 1,024 threads an SM.
@@ -457,8 +455,12 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
         if (s.vec == 4) HARTS_NORM_DISPATCH(launch_bwd, float, 4, 4, p, s, grid, st);
         else HARTS_NORM_DISPATCH(launch_bwd, float, 1, 8, p, s, grid, st);
     }
-    rmsnorm_dw_kernel<<<(a->D + 31) / 32, 1024, 0, st>>>(p.part, a->dweight, a->D, static_cast<int32_t>(groups));
-    return launched("rmsnorm backward launch");
+    const int ok = launched("rmsnorm backward launch");
+    if (ok) return ok;
+    const DwParams d{p.part, a->dweight, a->D, static_cast<int32_t>(groups)};
+    const cudaError_t e = launch(rmsnorm_dw_kernel, (a->D + 31) / 32, 1024, 0, 1, true, st, d);
+    if (e != cudaSuccess) { set_error(std::string("rmsnorm backward launch: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
+    return HARTS_OK;
 }
 
 }  // extern "C"
