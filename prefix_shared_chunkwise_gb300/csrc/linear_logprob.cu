@@ -58,6 +58,7 @@ struct Prod {
     int32_t b_panel;                // B is seen as such panels: one copy for a block's columns
     int32_t a_rows;                 // rows of A's box when stored [rows][K]
     int32_t m_tiles, n_tiles, splits, n;
+    uint32_t items, per_split;      // tiles times splits, tiles
     int32_t k_blocks, k_per;        // steps of 64 in all, per split
     int32_t b_y0, out_y0;           // row offsets of this piece of the vocabulary in B and the output
     int32_t rows, cols;             // extent of the output (rows from out_y0 on)
@@ -70,9 +71,9 @@ struct alignas(16) RowInfo { float neg_g, lse2; int32_t count, first; };   // -s
 struct Params {
     Prod prod[2];
     int32_t n_prod;
-    int32_t extra;                  // see tile_at
+    uint32_t each0, over, extra;    // see tile_at: tiles of the first product per worker, and what is left
     int32_t *error;
-    float c2;                       // scale * log2 e
+    float c2;                       // scale * log2 e (logit_factor)
     float2 *part;                   // forward: [C][n_tiles]
     const RowInfo *rows;            // dz: per compact row
     const int32_t *ent_y;
@@ -84,35 +85,42 @@ struct TileId { int which, mt, nt, split; };
 
 // The n-th tile of worker `w` of `workers` (blocks or pairs).  Tiles of the first product go
 // round the workers; those of the second follow, the workers that got one tile less of the
-// first taking `extra` of them before the others join in.
-__device__ __forceinline__ bool tile_at(const Params &p, int64_t n, int64_t w, int64_t workers, TileId &t) {
-    const int64_t x = static_cast<int64_t>(p.prod[0].m_tiles) * p.prod[0].n_tiles * p.prod[0].splits;
-    int64_t idx = w + n * workers;
+// first taking `extra` of them before the others join in.  32-bit arithmetic: the threads that
+// feed the tensor cores come through here between two tiles.
+__device__ __forceinline__ bool tile_at(const Params &p, uint32_t n, uint32_t w, uint32_t workers, TileId &t) {
+    uint32_t idx = w + n * workers;
     t.which = 0;
-    if (idx >= x) {
+    if (idx >= p.prod[0].items) {
         if (p.n_prod < 2) return false;
         t.which = 1;
-        const int64_t over = x % workers, few = workers - over;      // workers with a tile less, if any
-        int64_t m = n - (x > w ? (x - w + workers - 1) / workers : 0);
-        if (over == 0) {
+        const uint32_t few = workers - p.over;                       // workers with a tile less, if any
+        uint32_t m = n - p.each0 - (w < p.over ? 1 : 0);
+        if (p.over == 0) {
             idx = w + m * workers;
-        } else if (w >= over && m < p.extra) {
-            idx = (w - over) + m * few;
+        } else if (w >= p.over && m < p.extra) {
+            idx = (w - p.over) + m * few;
         } else {
-            if (w >= over) m -= p.extra;
+            if (w >= p.over) m -= p.extra;
             idx = few * p.extra + w + m * workers;
         }
-        if (idx >= static_cast<int64_t>(p.prod[1].m_tiles) * p.prod[1].n_tiles * p.prod[1].splits) return false;
+        if (idx >= p.prod[1].items) return false;
     }
     const Prod &q = p.prod[t.which];
-    const int32_t per = q.m_tiles * q.n_tiles;
-    t.split = static_cast<int>(idx / per);
-    const int32_t r = static_cast<int32_t>(idx - static_cast<int64_t>(t.split) * per);
-    // groups of tiles along the fast side run against every tile of the other
-    const int32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
-    const int32_t gs = min(fast, kGroup), g = r / (gs * slow), in = r - g * gs * slow;
-    const int32_t len = min(gs, fast - g * gs);
-    const int32_t f = g * gs + in % len, s = in / len;
+    t.split = 0;
+    if (q.splits > 1) {
+        t.split = static_cast<int>(idx / q.per_split);
+        idx -= t.split * q.per_split;
+    }
+    // groups of `group` tiles along the fast side run against every tile of the other
+    const uint32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
+    uint32_t base = 0, len = fast;
+    if (fast > kGroup) {
+        const uint32_t g = idx / (kGroup * slow);
+        idx -= g * kGroup * slow;
+        base = g * kGroup;
+        len = min(static_cast<uint32_t>(kGroup), fast - base);
+    }
+    const uint32_t s = idx / len, f = base + idx - s * len;
     t.mt = q.fast_n ? s : f;
     t.nt = q.fast_n ? f : s;
     return true;
@@ -143,6 +151,7 @@ __device__ __forceinline__ bool failed(const int *f) { return *reinterpret_cast<
 // True once the phase completed; false, with the block marked, when the wait ran out or
 // another role gave up.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t phase, int *f) {
+    if (tc::mbar_try(bar, phase)) return true;
     if (failed(f)) return false;
     if (tc::mbar_wait(bar, phase)) return true;
     atomicExch(f, 1);
@@ -237,10 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     __shared__ int s_fail;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t worker = blockIdx.x / G, workers = gridDim.x / G;
+    const uint32_t worker = blockIdx.x / G, workers = gridDim.x / G;
 
     if (tid == 0) {
-        for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 1); tc::mbar_init(&bars[B::empty + i], 1); }
+        for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 2); tc::mbar_init(&bars[B::empty + i], 1); }
         for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[B::acc_full + i], 1); tc::mbar_init(&bars[B::acc_empty + i], 4 * G); }
         tc::mbar_init(&bars[B::drain], 1);
         tc::fence_mbar_init();
@@ -253,35 +262,38 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     let_next_start();
     const uint32_t tm = s_tmem;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
+        // One thread each for A and B: a copy takes its thread a few hundred cycles, and one
+        // thread for both could not keep up with the 512 cycles of a step's products.
         if (lane == 0) {
+            const bool is_b = warp == 3;
             if (MODE == kGrad) wait_previous();         // dZ is complete
             uint32_t it = 0;                            // stages filled so far
             uint32_t s = 0, round = 0;                  // next stage, times the ring went round
             const uint32_t full0 = G == 2 ? leader_addr(&bars[B::full]) : tc::smem_addr(&bars[B::full]);
             TileId t;
             bool ok = true;
-            for (int64_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
-                // what the loop needs is taken out of the parameters: one thread feeds the tensor
-                // cores, every instruction in it counts
+            for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
+                // what the loop needs is taken out of the parameters once a tile
                 const Prod &q = p.prod[t.which];
-                const CUtensorMap *ma = &q.a, *mb = &q.b;
+                const CUtensorMap *map = is_b ? &q.b : &q.a;
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
                 const int32_t nb = q.n / G;             // columns that this block holds
                 const int32_t m0 = (t.mt * G + rank) * kTM, n0 = t.nt * q.n + rank * nb, y0 = q.b_y0;
-                const int how_a = q.a_panel ? (q.a_mn ? 2 : 1) : 0, how_b = q.b_mn ? (q.b_panel ? 2 : 1) : 0;
-                const uint32_t bytes = ((q.a_mn ? kABytes : q.a_rows * 128u) + nb * 128u) * G;
+                enum { kRows, kPanelRows, kPanelCols, kBoxes };
+                const int how = is_b ? (q.b_mn ? (q.b_panel ? kPanelCols : kBoxes) : kRows)
+                                     : (q.a_panel ? (q.a_mn ? kPanelCols : kPanelRows) : kRows);
+                const int32_t row = is_b ? y0 + n0 : m0, panel = (is_b ? n0 : m0) / 64, ky = is_b ? y0 : 0;
+                const uint32_t bytes = (is_b ? nb * 128u : q.a_mn ? kABytes : q.a_rows * 128u) * G;
                 for (int32_t k = k0; k < k1; ++k, ++it) {
                     if (round > 0 && !wait_or_fail(&bars[B::empty + s], (round - 1) & 1, &s_fail)) { ok = false; break; }
                     const uint32_t full = full0 + s * 8;
-                    uint8_t *a = sm + s * kStageBytes, *b = a + kABytes;
+                    uint8_t *dst = sm + s * kStageBytes + (is_b ? kABytes : 0);
                     if (rank == 0) tc::mbar_expect_tx(&bars[B::full + s], bytes);
-                    if (how_a == 0) pair_load<G>(a, ma, k * kTK, m0, full);
-                    else if (how_a == 1) pair_load3<G>(a, ma, 0, m0, k, full);
-                    else pair_load3<G>(a, ma, 0, k * kTK, m0 / 64, full);
-                    if (how_b == 0) pair_load<G>(b, mb, k * kTK, y0 + n0, full);
-                    else if (how_b == 2) pair_load3<G>(b, mb, 0, y0 + k * kTK, n0 / 64, full);
-                    else for (int j = 0; j < nb; j += 64) pair_load<G>(b + j * 128, mb, n0 + j, y0 + k * kTK, full);
+                    if (how == kRows) pair_load<G>(dst, map, k * kTK, row, full);
+                    else if (how == kPanelCols) pair_load3<G>(dst, map, 0, ky + k * kTK, panel, full);
+                    else if (how == kPanelRows) pair_load3<G>(dst, map, 0, row, k, full);
+                    else for (int j = 0; j < nb; j += 64) pair_load<G>(dst + j * 128, map, n0 + j, ky + k * kTK, full);
                     if (++s == kStages) { s = 0; ++round; }
                 }
             }
@@ -289,11 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             // (after a failure the products may not have waited for them), then the stages'
             // last release.  In a pair only the release says so for the second block; after a
             // failure its wait runs out, long after the last copy.
-            for (uint32_t s = 0; s < kStages; ++s) {
-                if (it <= s) continue;
-                const uint32_t uses = (it - s + kStages - 1) / kStages;
-                if (rank == 0) tc::mbar_wait(&bars[B::full + s], (uses - 1) & 1, 1000000000LL);
-                if (!tc::mbar_wait(&bars[B::empty + s], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL))
+            for (uint32_t i = 0; i < kStages; ++i) {
+                if (it <= i) continue;
+                const uint32_t uses = (it - i + kStages - 1) / kStages;
+                if (rank == 0) tc::mbar_wait(&bars[B::full + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL);
+                if (!tc::mbar_wait(&bars[B::empty + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL))
                     atomicExch(&s_fail, 1);
             }
         }
@@ -633,13 +645,34 @@ __global__ void __launch_bounds__(256) head_dx_kernel(DxParams p) {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Blocks that share a tile: pairs (256 rows) as soon as there are more rows than one block's
-// tile holds; a pair reads each operand row once where two blocks read the columns twice.
-int group_of(int64_t C) { return C > kTM ? 2 : 1; }
+// The forward's cut: blocks that share a tile (pairs: 256 rows) and the tile width, a multiple
+// of 16 columns a block.  The busiest worker's tiles cost their columns and 16 more for their
+// ends; a block alone, which reads its columns from L2 where a pair shares them, takes 1.12 as
+// long (4096 x 157184 x 2048: 1453 us alone, 1287 us in pairs), but wastes less where the rows
+// end early in a tile (300 rows: 174 us alone, 197 us in pairs).
+struct Cut { int group; int32_t width; };
+Cut fwd_cut(int64_t C, int32_t V) {
+    Cut best{1, kTN};
+    double least = 0.0;
+    for (int G = 1; G <= (C > kTM ? 2 : 1); ++G)
+        for (int32_t n = kTN; n >= 64; n -= 16 * G) {
+            const int64_t tiles = int64_t(ceil_div(C, kTM * G)) * ceil_div(V, n), workers = sm_count() / G;
+            const double cost = double((tiles + workers - 1) / workers) * (n + 16) * (G == 1 ? 1.12 : 1.0);
+            if (least == 0.0 || cost < least) { least = cost; best = Cut{G, n}; }
+        }
+    return best;
+}
 
-// Tile width of a product with m_tiles row tiles over `cols` columns: the multiple of `unit`
-// up to 256 that leaves the least work on the busiest pair or block (16 columns stand for a
-// tile's fixed cost).
+// The backward's group: two of its products have C for their rows, the third for its K.  By
+// measurement a block alone takes about 1.2 as long a tile row (640 rows: 866 us alone, 796 us
+// in pairs at V = 157184, D = 2048; 300 rows: 549 and 616).
+int bwd_group(int64_t C) {
+    const int64_t alone = 2 * ((C + 127) / 128 * 128) + C, pairs = 2 * ((C + 255) / 256 * 256) + C;
+    return C <= kTM || 1.2 * double(alone) < double(pairs) ? 1 : 2;
+}
+
+// Tile width over `cols` columns in multiples of `unit`: the least work for the busiest worker,
+// as above.
 int32_t tile_width(int32_t m_tiles, int64_t cols, int32_t unit, int G) {
     int32_t best = kTN;
     int64_t cost = INT64_MAX;
@@ -698,17 +731,23 @@ cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(head_tile_kernel<MODE, G>, Ring<G>::smem, done);
     if (e != cudaSuccess) return e;
-    int64_t items[2] = {0, 0};
-    for (int i = 0; i < p.n_prod; ++i) items[i] = int64_t(p.prod[i].m_tiles) * p.prod[i].n_tiles * p.prod[i].splits;
-    const int64_t workers = std::min<int64_t>(items[0] + items[1], sm_count() / G);
-    p.extra = 0;
-    if (p.n_prod == 2 && items[0] % workers) {
-        // a tile costs its K steps and about three more for its ends
-        const int64_t few = workers - items[0] % workers;
-        const int64_t even = (p.prod[0].k_per + 3 + (p.prod[1].k_per + 3) / 2) / (p.prod[1].k_per + 3);
-        p.extra = static_cast<int32_t>(std::min(even, items[1] / few));
+    int64_t items = 0;
+    for (int i = 0; i < p.n_prod; ++i) {
+        Prod &q = p.prod[i];
+        q.per_split = static_cast<uint32_t>(q.m_tiles) * q.n_tiles;
+        q.items = q.per_split * q.splits;
+        items += q.items;
     }
-    return launch(head_tile_kernel<MODE, G>, workers * G, kThreads, Ring<G>::smem, G, behind, st, p);
+    const uint32_t workers = static_cast<uint32_t>(std::min<int64_t>(items, sm_count() / G));
+    p.each0 = p.prod[0].items / workers;
+    p.over = p.prod[0].items % workers;
+    p.extra = 0;
+    if (p.n_prod == 2 && p.over) {
+        // a tile costs its K steps and about three more for its ends
+        const uint32_t a = p.prod[0].k_per + 3, b = p.prod[1].k_per + 3;
+        p.extra = std::min((a + b / 2) / b, p.prod[1].items / (workers - p.over));
+    }
+    return launch(head_tile_kernel<MODE, G>, int64_t(workers) * G, kThreads, Ring<G>::smem, G, behind, st, p);
 }
 template <int MODE>
 cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {
@@ -723,6 +762,11 @@ int check(const harts_linear_logprob_fwd_args *a) {
     if (a->C < 0 || a->S < 0 || a->V < 1 || a->D < 1) { set_error("C, S >= 0 and V, D >= 1 required"); return HARTS_EINVAL; }
     if (a->D % 8) { set_error("D must be a multiple of 8 (rows start 16-byte aligned)"); return HARTS_EUNSUPPORTED; }
     if (a->S > 0x7fffffff || a->C > 0x7fffff00 || a->V > 0x7fffff00) { set_error("C, V or S beyond int32 rows"); return HARTS_EOVERFLOW; }
+    const int64_t c = a->C / kTM + 1, v = a->V / 64 + 1, d = a->D / 64 + 1;      // tiles are counted in 32 bits
+    if (c * v > 0x3fffffff || (c + v) * d > 0xffffff) {
+        set_error("more tiles than the library counts");
+        return HARTS_EOVERFLOW;
+    }
     if (!std::isfinite(a->scale)) { set_error("scale must be finite"); return HARTS_EINVAL; }
     if (a->C > 0 && (!a->x || !a->weight || !a->row_ptr || !a->lse)) { set_error("NULL x, weight, row_ptr or lse"); return HARTS_EINVAL; }
     if (a->S > 0 && (!a->row_sem || !a->target)) { set_error("NULL row_sem or target"); return HARTS_EINVAL; }
@@ -738,9 +782,13 @@ int cuda_fail(cudaError_t e, const char *what) {
     return HARTS_ECUDA;
 }
 
-int32_t fwd_width(int64_t C, int32_t V) {
-    const int G = group_of(C);
-    return tile_width(ceil_div(C, kTM * G), V, 16 * G, G);
+// scale * log2 e, with the tensor cores' truncation taken back to first order.  An accumulator
+// is cut towards zero at every 16 columns of K, which shrinks a logit by D/16 times a quarter of
+// 2^-24 on average (measured with one vocabulary entry, whose lse is its logit: 0.20 - 0.29 for
+// products of either sign at D = 64 .. 4096, up to 0.9 where all have one sign).  Uncorrected
+// that is the largest error of lse, 1.6e-6 of it at D = 2048.
+float logit_factor(float scale, int32_t D) {
+    return static_cast<float>(double(scale) * 1.4426950408889634 * (1.0 + 0.25 * (D / 16.0) * 0x1p-24));
 }
 
 SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
@@ -754,7 +802,7 @@ SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
 // How the backward is cut: vocabulary entries a piece, K splits of dX, and where things lie
 // in the workspace.
 struct BwdPlan {
-    int32_t piece, n_pieces, n_dz, n_grad, splits, k_per;
+    int32_t group, piece, n_pieces, n_dz, n_grad, splits, k_per;
     bool acc;                       // dX goes through fp32 sums
     size_t rows, ent_y, ent_v, dz, dx, total;
 };
@@ -767,7 +815,7 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     want = std::max<int64_t>(kTN, want / kTN * kTN);
     b.piece = static_cast<int32_t>(std::min<int64_t>(want, (int64_t(V) + 63) / 64 * 64));
     b.n_pieces = ceil_div(V, b.piece);
-    const int G = group_of(C);
+    const int G = b.group = bwd_group(C);
     const int32_t mt = ceil_div(C, kTM * G);
     b.n_dz = tile_width(mt, std::min<int32_t>(b.piece, V), 64, G);
     const int32_t unit = 64 * G;                        // columns stored [K][columns] come in 64s per block
@@ -796,7 +844,7 @@ extern "C" {
 
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D) {
     if (C < 0 || V < 1 || D < 1) return 0;
-    return std::max<size_t>(256, sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_width(C, V)));
+    return std::max<size_t>(256, sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V).width));
 }
 
 int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_stream_t stream) {
@@ -812,9 +860,10 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     Params p;
     std::memset(&p, 0, sizeof(p));
     Prod &q = p.prod[0];
-    const int G = group_of(a->C);
+    const Cut cut = fwd_cut(a->C, a->V);
+    const int G = cut.group;
     q.m_tiles = ceil_div(a->C, kTM * G);
-    q.n = fwd_width(a->C, a->V);
+    q.n = cut.width;
     q.n_tiles = ceil_div(a->V, q.n);
     q.splits = 1;
     q.k_blocks = q.k_per = ceil_div(a->D, kTK);
@@ -823,7 +872,7 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     q.cols = a->V;
     p.n_prod = 1;
     p.error = a->error;
-    p.c2 = a->scale * kLog2e;
+    p.c2 = logit_factor(a->scale, a->D);
     p.part = static_cast<float2 *>(a->workspace);
     if (!map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows) || !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n / G)) {
         set_error("tensor map");
@@ -875,7 +924,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     const cudaError_t first = launch(head_rows_kernel, ceil_div(f.C, 8), 256, 0, 1, false, st, s);
     if (first != cudaSuccess) return cuda_fail(first, "linear log-prob backward launch");
 
-    const int G = group_of(f.C);
+    const int G = b.group;
     const int32_t mt = ceil_div(f.C, kTM * G), C = static_cast<int32_t>(f.C);
     const int32_t a_rows = static_cast<int32_t>(std::min<int64_t>(kTM, (f.C + 7) / 8 * 8));
     Params pz, pg;
@@ -894,7 +943,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
         z.k_blocks = z.k_per = ceil_div(f.D, kTK);
         z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
-        pz.n_prod = 1; pz.error = f.error; pz.c2 = f.scale * kLog2e;
+        pz.n_prod = 1; pz.error = f.error; pz.c2 = logit_factor(f.scale, f.D);
         pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0;
         cudaError_t e = launch_tiles<kDz>(pz, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
