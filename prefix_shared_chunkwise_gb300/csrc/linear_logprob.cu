@@ -21,7 +21,8 @@
 //
 // Tile kernel: persistent blocks, one per SM; warp 0 fills a ring of shared-memory stages
 // by TMA, warp 1 issues tcgen05.mma into one of two 256-column accumulators in TMEM, warps
-// 4-7 empty the other one.  All waits are bounded.
+// 4-7 empty the other one (through shared memory and TMA stores of warps 8-9, where there is
+// output).  All waits are bounded.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -36,19 +37,27 @@ namespace {
 
 constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K step (one 128-byte swizzle row), tile columns
 constexpr uint32_t kABytes = kTM * kTK * 2;
-constexpr uint32_t kOutBytes = 4 * 2 * 4096;        // 4 warps x 2 slots of 32 rows x 128 bytes
-// A block of a pair holds half of the tile's columns in shared memory: stages are smaller,
-// and there are more of them.
-template <int G> struct Ring {
-    static constexpr int stages = G == 2 ? 6 : 4;
-    static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
-    static constexpr uint32_t smem = stages * stage_bytes + kOutBytes + 1024;
-};
-constexpr int kThreads = 256, kEpiWarp0 = 4;
+constexpr uint32_t kSlotBytes = kTM * 128;           // 128 rows x 128 bytes of the output on their way out
+
+constexpr int kThreads = 320, kEpiWarp0 = 4, kStoreWarp0 = 8;
 constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kFwd = 0, kDz = 1, kGrad = 2 };
+
+// Shared memory: stages of both operands and slots of the output.  A block of a pair holds
+// half of the tile's columns: its stages are smaller, and there are more of them.  The forward
+// has no output; dW of few rows is nothing but output, which needs bytes on their way.
+template <int MODE, int G> struct Ring {
+    static constexpr uint32_t slots = MODE == kFwd ? 0 : MODE == kDz ? 2 : 4;
+    static constexpr uint32_t stages = G == 2 ? (MODE == kFwd ? 7 : MODE == kDz ? 6 : 5) : (MODE == kGrad ? 3 : 4);
+    static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
+    static constexpr uint32_t smem = stages * stage_bytes + slots * kSlotBytes + 1024;
+    static_assert(smem <= 227 * 1024 - 512, "shared memory of an SM");
+    // barriers
+    static constexpr uint32_t full = 0, empty = stages, acc_full = 2 * stages, acc_empty = acc_full + 2, drain = acc_empty + 2,
+                              out_full = drain + 1, out_free = out_full + slots, count = out_free + slots;
+};
 
 // One product D = op(A) op(B)^T cut into tiles and splits of its K range.
 struct Prod {
@@ -144,6 +153,7 @@ __device__ __forceinline__ void store_3d(const void *map, int x, int y, int z, c
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
                      :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(src)) : "memory");
 }
+
 // all but the last committed store of this thread have read their source
 __device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
@@ -230,15 +240,10 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 
-template <int G> struct Bar {
-    static constexpr int full = 0, empty = Ring<G>::stages, acc_full = 2 * Ring<G>::stages, acc_empty = acc_full + 2,
-                         drain = acc_empty + 2, count = drain + 1;
-};
-
 template <int MODE, int G>
 __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_constant__ Params p) {
-    using B = Bar<G>;
-    constexpr uint32_t kStages = Ring<G>::stages, kStageBytes = Ring<G>::stage_bytes;
+    using B = Ring<MODE, G>;
+    constexpr uint32_t kStages = B::stages, kStageBytes = B::stage_bytes, kSlots = B::slots;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024 - (tc::smem_addr(smraw) & 1023)) & 1023);
     __shared__ uint64_t bars[B::count];
@@ -251,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     if (tid == 0) {
         for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 2); tc::mbar_init(&bars[B::empty + i], 1); }
         for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[B::acc_full + i], 1); tc::mbar_init(&bars[B::acc_empty + i], 4 * G); }
+        for (int i = 0; i < static_cast<int>(kSlots); ++i) { tc::mbar_init(&bars[B::out_full + i], 4); tc::mbar_init(&bars[B::out_free + i], 1); }
         tc::mbar_init(&bars[B::drain], 1);
         tc::fence_mbar_init();
         s_fail = 0;
@@ -347,22 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 tc::mbar_wait(&bars[B::drain], 0, 1000000000LL);
             }
         }
-    } else if (warp >= kEpiWarp0) {
+    } else if (warp >= kEpiWarp0 && warp < kStoreWarp0) {
         const int lg = warp - kEpiWarp0;                // TMEM lanes 32 lg .. 32 lg + 31
         const uint32_t lane_off = static_cast<uint32_t>(lg * 32) << 16;
-        uint8_t *out = sm + kStages * kStageBytes + lg * 8192;
+        [[maybe_unused]] uint8_t *out = sm + kStages * kStageBytes + lg * 4096;   // this warp's rows of a slot
         const uint32_t released = G == 2 ? leader_addr(&bars[B::acc_empty]) : 0;
-        uint32_t tile = 0, slot = 0;
+        uint32_t tile = 0;
+        [[maybe_unused]] uint32_t groups = 0;                  // groups of 128 bytes of columns so far
         TileId t;
+        bool ok = true;
         if (MODE == kDz) wait_previous();               // rows' terms; the last piece's dZ has been read
-        for (; tile_at(p, tile, worker, workers, t); ++tile) {
+        for (; ok && tile_at(p, tile, worker, workers, t); ++tile) {
             const Prod &q = p.prod[t.which];
             const uint32_t buf = tile & 1;
             if (!__all_sync(0xffffffffu, wait_or_fail(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail))) break;
             tc::fence_after_sync();
             const uint32_t acc = tm + buf * kTN + lane_off;
             const int32_t n0 = t.nt * q.n, row = (t.mt * G + rank) * kTM + lg * 32 + lane;
-            if (MODE == kFwd) {
+            if constexpr (MODE == kFwd) {
                 const int32_t nv = min(q.n, q.cols - n0);       // columns that are vocabulary entries
                 float m = -INFINITY, s = 0.f;
                 for (int c = 0; c < nv; c += 32) {
@@ -397,15 +405,17 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                     if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
                 }
                 if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
-            } else {
+            } else if constexpr (MODE != kFwd) {
                 RowInfo ri{0.f, 0.f, 0, 0};
                 if (MODE == kDz && row < q.rows) ri = p.rows[row];
-                const int step = q.out_f32 ? 32 : 64;
-                const int32_t y = (t.mt * G + rank) * kTM + lg * 32;
-                for (int c = 0; c < q.n; c += step) {
-                    uint8_t *dst = out + slot * 4096;
-                    if (lane == 0) store_wait_read1();
-                    __syncwarp();
+                const int step = q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
+                for (int c = 0; c < end; c += step, ++groups) {
+                    const uint32_t slot = groups % kSlots, use = groups / kSlots;
+                    uint8_t *dst = out + slot * kSlotBytes;
+                    if (use > 0 && !__all_sync(0xffffffffu, wait_or_fail(&bars[B::out_free + slot], (use - 1) & 1, &s_fail))) {
+                        ok = false;
+                        break;
+                    }
                     if (q.out_f32) {
                         float v[32];
                         tc::tmem_ld32(acc + c, v);
@@ -443,26 +453,51 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                             }
                         }
                     }
-                    if (c + step >= q.n) {              // the accumulator has been read
-                        tc::fence_before_sync();
-                    }
+                    if (c + step >= end) tc::fence_before_sync();       // the accumulator has been read
                     tc::fence_smem_to_async();
                     __syncwarp();
                     if (lane == 0) {
-                        if (c + step >= q.n) {
+                        arrive(&bars[B::out_full + slot]);
+                        if (c + step >= end) {
                             if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
                         }
-                        if (y < q.rows && n0 + c < q.cols) {
-                            if (MODE == kDz) store_3d(&q.out, 0, y, (n0 + c) / 64, dst, false);
-                            else store_3d(&q.out, n0 + c, q.out_y0 + y, t.split, dst, q.out_add != 0);
-                        }
-                        tc::bulk_commit();
                     }
-                    slot ^= 1;
                 }
             }
         }
-        if (MODE != kFwd && lane == 0) tc::bulk_wait_all();
+    } else if (warp >= kStoreWarp0) {
+        // Two threads send the slots out in turn, each with all but one of its stores read: a store
+        // takes its thread a few hundred cycles, which the warps that fill the slots need not
+        // wait for.
+        if constexpr (MODE != kFwd) {
+            if (lane == 0) {
+                const uint32_t mine = warp - kStoreWarp0;
+                constexpr uint32_t kLag = kSlots / 2 - 1;       // own stores that may still be read
+                uint32_t groups = 0;
+                TileId t;
+                bool ok = true;
+                for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
+                    const Prod &q = p.prod[t.which];
+                    const int32_t n0 = t.nt * q.n, y = (t.mt * G + rank) * kTM;
+                    const int step = q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
+                    for (int c = 0; c < end; c += step, ++groups) {
+                        if ((groups & 1) != mine) continue;
+                        const uint32_t slot = groups % kSlots;
+                        const uint8_t *src = sm + kStages * kStageBytes + slot * kSlotBytes;
+                        if (!wait_or_fail(&bars[B::out_full + slot], (groups / kSlots) & 1, &s_fail)) { ok = false; break; }
+                        if (y < q.rows) {
+                            if (MODE == kDz) store_3d(&q.out, 0, y, (n0 + c) / 64, src, false);
+                            else store_3d(&q.out, n0 + c, q.out_y0 + y, t.split, src, q.out_add != 0);
+                        }
+                        tc::bulk_commit();
+                        if (kLag == 0) tc::bulk_wait_read(); else store_wait_read1();
+                        if (kLag == 0) arrive(&bars[B::out_free + slot]);
+                        else if (groups >= 2) arrive(&bars[B::out_free + (groups - 2) % kSlots]);
+                    }
+                }
+                tc::bulk_wait_all();
+            }
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -622,22 +657,17 @@ __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
 
 // dX in bf16 from the splits' fp32 sums, in ascending order.
 struct DxParams { const float *acc; __nv_bfloat16 *dx; int64_t n; int32_t splits; };
-__global__ void __launch_bounds__(256) head_dx_kernel(DxParams p) {
+__global__ void __launch_bounds__(128) head_dx_kernel(DxParams p) {
     wait_previous();
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < p.n;
-         i += static_cast<int64_t>(gridDim.x) * 256 * 8) {
-        float v[8] = {};
-#pragma unroll 4
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * 4; i < p.n;
+         i += static_cast<int64_t>(gridDim.x) * 128 * 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int32_t s = 0; s < p.splits; ++s) {
-            const float4 *q = reinterpret_cast<const float4 *>(p.acc + s * p.n + i);
-            const float4 a = q[0], b = q[1];
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+            const float4 a = *reinterpret_cast<const float4 *>(p.acc + s * p.n + i);
+            v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
         }
-        uint4 u;
-        u.x = tc::pack_bf16(v[0], v[1]); u.y = tc::pack_bf16(v[2], v[3]);
-        u.z = tc::pack_bf16(v[4], v[5]); u.w = tc::pack_bf16(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(p.dx + i) = u;
+        *reinterpret_cast<uint2 *>(p.dx + i) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
     }
 }
 
@@ -693,8 +723,8 @@ bool map_in(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
     return encode_bf16(m, base, 2, dims, strides, box);
 }
 
-// dZ in panels of 64 columns, [panels][C][64]: every box that is written (32 rows), read as
-// rows (dX) or as columns (dW, 64 rows) is one contiguous run.  Row-major, a box's 64 or 128
+// dZ in panels of 64 columns, [panels][C][64]: every box that is written, read as rows
+// (dX) or as columns (dW) is one contiguous run, or two.  Row-major, a box's 64 or 128
 // rows lie a whole piece (128 KB) apart each.
 bool map_dz(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_rows, int32_t box_panels) {
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(C), static_cast<cuuint64_t>((nv + 63) / 64)};
@@ -713,12 +743,12 @@ bool map_cols(CUtensorMap *m, const void *base, int64_t rows, int64_t D, int32_t
     return encode_bf16(m, base, 3, dims, strides, box);
 }
 
-// [layers][rows][cols], written in boxes of 128 bytes x 32 rows.
+// [layers][rows][cols], written in boxes of 128 bytes x 128 rows.
 bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t cols, int64_t pitch, bool f32) {
     const cuuint64_t e = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(layers)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * e, static_cast<cuuint64_t>(pitch) * e * rows};
-    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, kTM, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     auto fn = encode_tiled();
     return fn && fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides,
@@ -729,7 +759,7 @@ bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t c
 template <int MODE, int G>
 cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(head_tile_kernel<MODE, G>, Ring<G>::smem, done);
+    const cudaError_t e = allow_smem(head_tile_kernel<MODE, G>, Ring<MODE, G>::smem, done);
     if (e != cudaSuccess) return e;
     int64_t items = 0;
     for (int i = 0; i < p.n_prod; ++i) {
@@ -747,7 +777,7 @@ cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
         const uint32_t a = p.prod[0].k_per + 3, b = p.prod[1].k_per + 3;
         p.extra = std::min((a + b / 2) / b, p.prod[1].items / (workers - p.over));
     }
-    return launch(head_tile_kernel<MODE, G>, int64_t(workers) * G, kThreads, Ring<G>::smem, G, behind, st, p);
+    return launch(head_tile_kernel<MODE, G>, int64_t(workers) * G, kThreads, Ring<MODE, G>::smem, G, behind, st, p);
 }
 template <int MODE>
 cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {
@@ -937,7 +967,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
               (b.acc ? map_out(&gx.out, acc, b.splits, f.C, f.D, f.D, true) : map_out(&gx.out, a->dx, 1, f.C, f.D, f.D, false));
     for (int32_t i = 0; ok && i < b.n_pieces; ++i) {
         const int32_t v0 = i * b.piece, nv = std::min(b.piece, f.V - v0);
-        ok = map_dz(&z.out, dz, f.C, nv, 32, 1) && map_dz(&gx.a, dz, f.C, nv, a_rows, 1) && map_dz(&gw.a, dz, f.C, nv, 64, 2);
+        ok = map_dz(&z.out, dz, f.C, nv, kTM, 1) && map_dz(&gx.a, dz, f.C, nv, a_rows, 1) && map_dz(&gw.a, dz, f.C, nv, 64, 2);
         if (!ok) break;
         // logits of the piece, as dz
         z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
@@ -961,8 +991,8 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     if (!ok) { set_error("tensor map"); return HARTS_ECUDA; }
     if (b.acc) {
         const DxParams d{acc, static_cast<__nv_bfloat16 *>(a->dx), f.C * f.D, b.splits};
-        const int64_t blocks = std::min<int64_t>((d.n / 8 + 255) / 256, int64_t(sm_count()) * 8);
-        const cudaError_t e = launch(head_dx_kernel, blocks, 256, 0, 1, true, st, d);
+        const int64_t blocks = std::min<int64_t>((d.n / 4 + 127) / 128, int64_t(sm_count()) * 16);
+        const cudaError_t e = launch(head_dx_kernel, blocks, 128, 0, 1, true, st, d);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     }
     set_error("");
