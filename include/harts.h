@@ -457,7 +457,7 @@ typedef struct {
     int32_t D;               /* channels, 1 .. 16384 */
     int32_t dtype;           /* harts_dtype of x, residual, h, y */
     float eps;               /* >= 0 */
-    const void *x;           /* device [C][D], 16-byte aligned (so are residual, h, y, y8) */
+    const void *x;           /* device [C][D], 16-byte aligned (so are residual, weight, h, y, y8) */
     const void *residual;    /* device [C][D], or NULL */
     const float *weight;     /* device [D] fp32 */
     void *h;                 /* device [C][D] output, x + residual; required with a residual,
@@ -476,13 +476,15 @@ typedef struct {
     int64_t C;
     int32_t D;
     int32_t dtype;           /* harts_dtype of dy, h, dh, dx */
-    const void *dy;          /* device [C][D] dL/dy, 16-byte aligned (so are h, dh, dx) */
+    const void *dy;          /* device [C][D] dL/dy, 16-byte aligned (so are h, dh, weight, dx) */
     const void *h;           /* device [C][D] as the forward wrote it (x where it had no residual) */
     const void *dh;          /* device [C][D] dL/dh along the residual stream, or NULL */
     const float *weight;     /* device [D] fp32 */
     const float *rstd;       /* device [C] from the forward */
     void *dx;                /* device [C][D] output: dL/dx = dL/dresidual; may be dy or dh */
     float *dweight;          /* device [D] output (overwritten; zero when C is 0) */
+    int32_t *error;          /* device [1], or NULL: set to 3 if a bounded wait ran out; cleared by
+                                the caller */
     void *workspace;         /* device, harts_rmsnorm_bwd_workspace_bytes, 16-byte aligned */
     size_t workspace_bytes;
 } harts_rmsnorm_bwd_args;

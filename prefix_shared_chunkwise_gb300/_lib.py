@@ -112,8 +112,8 @@ class RmsnormFwdArgs(ctypes.Structure):
 
 class RmsnormBwdArgs(ctypes.Structure):
     _fields_ = [("C", _i64), ("D", _i32), ("dtype", _i32), ("dy", _vp), ("h", _vp), ("dh", _vp),
-                ("weight", _vp), ("rstd", _vp), ("dx", _vp), ("dweight", _vp), ("workspace", _vp),
-                ("workspace_bytes", ctypes.c_size_t)]
+                ("weight", _vp), ("rstd", _vp), ("dx", _vp), ("dweight", _vp), ("error", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class GradTensor(ctypes.Structure):

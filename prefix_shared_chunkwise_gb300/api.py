@@ -415,10 +415,10 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None
     return y, h, rstd
 
 
-def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, workspace=None, stream=None):
+def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, error=None, workspace=None, stream=None):
     """harts_rmsnorm_bwd: from dL/dy, the forward's h and rstd, and dL/dh along the residual
     stream (or None).  Returns (dx [C, D] like h: the gradient of x and of the residual;
-    dweight [D] fp32)."""
+    dweight [D] fp32).  error: as linear_logprob_fwd's."""
     import torch
     if h.dim() != 2:
         raise ValueError(f"h has shape {tuple(h.shape)}, expected [C, D]")
@@ -433,6 +433,7 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, workspac
     _ready("weight", weight, (D,), f32, dev)
     _ready("rstd", rstd, (C,), f32, dev)
     _ready("dweight", dweight, (D,), f32, dev)
+    _need("error", error, None, torch.int32, 4, dev)
     a = L.RmsnormBwdArgs()
     a.C, a.D, a.dtype = C, D, dtype_code(h.dtype)
     nb = int(L.lib().harts_rmsnorm_bwd_workspace_bytes(C, D, a.dtype))
@@ -441,6 +442,7 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, workspac
     _need("workspace", workspace, nbytes=nb, device=dev)
     a.dy, a.h, a.dh = dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr()
     a.weight, a.rstd, a.dx, a.dweight = weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr()
+    a.error = None if error is None else error.data_ptr()
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     L.check(L.lib().harts_rmsnorm_bwd(ctypes.byref(a), _stream_on(stream, h)), "harts_rmsnorm_bwd")
     return dx, dweight

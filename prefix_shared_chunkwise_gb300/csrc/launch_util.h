@@ -50,8 +50,9 @@ __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.w
 
 // `behind`: the kernel may be set up before its predecessor in the stream has ended (it waits
 // itself, see wait_previous).
-template <typename F, typename P>
-inline cudaError_t launch(F *kernel, int64_t blocks, int threads, size_t smem, int cluster, bool behind, cudaStream_t st, const P &p) {
+template <typename F, typename... P>
+inline cudaError_t launch(F *kernel, int64_t blocks, int threads, size_t smem, int cluster, bool behind, cudaStream_t st,
+                          const P &...p) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(threads);
@@ -71,7 +72,7 @@ inline cudaError_t launch(F *kernel, int64_t blocks, int threads, size_t smem, i
         c.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         c.val.programmaticStreamSerializationAllowed = 1;
     }
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p...);
 }
 
 inline int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }

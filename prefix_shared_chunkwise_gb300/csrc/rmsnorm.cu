@@ -6,14 +6,15 @@
 // Sums and statistics are fp32; h is normalised before its own rounding to the stream's type,
 // so y carries one rounding.  The backward reads the rounded h that the forward stored.
 //
-// Both directions move every value once and do ~10 operations on it: they are bound by HBM.
-// A row belongs to R threads that keep it in registers between the statistics and the
-// output, so nothing is read twice.  Blocks are persistent: each thread keeps the weights
-// (and, backward, the column sums of dw) of its columns in registers over all its rows --
+// Both directions move every value once and do ~10 operations on it: HBM bounds them.  A row
+// belongs to R threads that keep it in registers between the statistics and the output, so
+// nothing is read twice.  Blocks are persistent: each thread keeps the weights (and, backward,
+// the column sums of dw) of its columns in registers over all its rows where they fit --
 // fp32 weights re-read per row would be as many bytes as two bf16 streams -- and the next
-// row's loads are issued before the current row's reduction, so the barrier of a row costs
-// no memory time.  dw: each group of R threads writes its column sums, a second kernel adds
-// them in ascending order: no atomics, the same bits on every run.
+// row's loads are under way before the current row's reduction: in registers forward and for
+// short rows, by bulk copies into shared memory for longer rows backward.  dw: each group of
+// R threads writes its column sums, a second kernel adds them in ascending order: no atomics,
+// the same bits on every run.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -22,12 +23,15 @@
 
 #include "kda_common.cuh"
 #include "launch_util.h"
+#include "tc_primitives.cuh"
 
 namespace harts {
 namespace {
 
 constexpr int kMaxDim = 16384;      // 1024 threads x 16 values
 constexpr int kMxBlock = 32;        // channels that share a scale
+constexpr int kLongRow = 8192;      // values; longer rows take a kernel of their own backward
+constexpr int kMaxStages = 4;       // rows copied ahead
 
 struct NormFwd {
     const void *x, *res;
@@ -45,6 +49,7 @@ struct NormBwd {
     const float *w, *rstd;
     void *dx;
     float *part;                    // [groups][D]
+    int32_t *error;
     int64_t C;
     int32_t D;
 };
@@ -89,19 +94,40 @@ __device__ __forceinline__ void st(void *p, int64_t i, const float *v) {
     *reinterpret_cast<Raw<T, VEC> *>(static_cast<T *>(p) + i) = r;
 }
 
-// Sum over the R threads of a row; sm is one of two slots used in turn, so that one barrier
-// per row is enough.
+constexpr int block_of(int R) { return R < 128 ? 128 : R; }     // threads of a block
+constexpr int rows_of(int R) { return block_of(R) / R; }        // rows it works on at a time
+// Weights (and dw's sums) of a thread's columns stay in registers up to this many values;
+// beyond, weights come from L1.
+constexpr int kRegValues = 16;
+
+// Sum over the R threads of a row.  sm holds two slots a row, used in turn, so that one barrier
+// per row is enough; rows of a block that has several do not wait for each other.
 template <int R>
 __device__ __forceinline__ float row_sum(float v, float *sm) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (R == 32) return v;
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
+    if constexpr (R == 32) return v;
+    const int in_row = (threadIdx.x % R) >> 5;
+    if ((threadIdx.x & 31) == 0) sm[in_row] = v;
+    if constexpr (R < 128) asm volatile("bar.sync %0, %1;" :: "r"(1 + static_cast<int>(threadIdx.x) / R), "n"(R) : "memory");
+    else __syncthreads();
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < R / 32; ++i) s += sm[i];
     return s;
+}
+
+template <int VEC>
+__device__ __forceinline__ void ld_w(const float *w, int32_t col, float (&v)[VEC]) {
+    if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(w + col + i));
+            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+        }
+    } else {
+        v[0] = __ldg(w + col);
+    }
 }
 
 // One block of 32 channels, spread over 32 / VEC neighbouring lanes, in 8 bits: the scale is
@@ -145,15 +171,15 @@ __device__ __forceinline__ void store_mx(uint8_t *y8, uint8_t *scale8, int64_t r
 }
 
 template <typename T, int VEC, int R, int NV, bool MX>
-__global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_fwd_kernel(NormFwd p) {
-    __shared__ float sm[2][R / 32];
-    constexpr int G = R == 32 ? 4 : 1;                  // rows a block works on at a time
-    const int t = R == 32 ? threadIdx.x & 31 : threadIdx.x;
+__global__ void __launch_bounds__(block_of(R)) rmsnorm_fwd_kernel(NormFwd p) {
+    constexpr bool kKeep = NV * VEC <= kRegValues;
+    __shared__ float sm[2][rows_of(R)][R / 32];
+    const int t = threadIdx.x % R, sub = threadIdx.x / R;
     const int32_t D = p.D;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * G + (R == 32 ? threadIdx.x >> 5 : 0);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_of(R);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * rows_of(R) + sub;
     const float inv_d = 1.f / static_cast<float>(D);
-    float w[NV][VEC];
+    [[maybe_unused]] float w[kKeep ? NV : 1][VEC];
     Raw<T, VEC> x[NV], r[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -163,11 +189,12 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_fwd_kernel(NormFwd 
             if (p.res) r[j] = ld<T, VEC>(p.res, row * D + col);
         }
     }
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int32_t col = (j * R + t) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = col < D ? __ldg(p.w + col + i) : 0.f;
+        for (int j = 0; j < NV; ++j) {
+            const int32_t col = (j * R + t) * VEC;
+            if (col < D) ld_w<VEC>(p.w, col, w[j]);
+        }
     }
     for (int slot = 0; row < p.C; row += step, slot ^= 1) {
         float h[NV][VEC], s = 0.f;
@@ -195,14 +222,21 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_fwd_kernel(NormFwd 
                 if (p.res) r[j] = ld<T, VEC>(p.res, next * D + col);
             }
         }
-        const float rstd = __frsqrt_rn(fmaf(row_sum<R>(s, sm[slot]), inv_d, p.eps));
+        const float rstd = __frsqrt_rn(fmaf(row_sum<R>(s, sm[slot][sub]), inv_d, p.eps));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int32_t col = (j * R + t) * VEC;
             if (col < D) {
+                float v[VEC];
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[i] = w[j][i];
+                } else {
+                    ld_w<VEC>(p.w, col, v);
+                }
                 if (p.h) st<T, VEC>(p.h, row * D + col, h[j]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) h[j][i] = h[j][i] * rstd * w[j][i];
+                for (int i = 0; i < VEC; ++i) h[j][i] = h[j][i] * rstd * v[i];
                 if (p.y) st<T, VEC>(p.y, row * D + col, h[j]);
                 if constexpr (MX) store_mx<VEC>(static_cast<uint8_t *>(p.y8), p.scale8, row, D, col, h[j]);
             }
@@ -212,16 +246,17 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_fwd_kernel(NormFwd 
 }
 
 template <typename T, int VEC, int R, int NV>
-__global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd p) {
-    __shared__ float sm[2][R / 32];
-    constexpr int G = R == 32 ? 4 : 1;
-    const int t = R == 32 ? threadIdx.x & 31 : threadIdx.x;
+__global__ void __launch_bounds__(block_of(R)) rmsnorm_bwd_kernel(NormBwd p) {
+    constexpr bool kKeep = NV * VEC <= kRegValues;
+    __shared__ float sm[2][rows_of(R)][R / 32];
+    const int t = threadIdx.x % R, sub = threadIdx.x / R;
     const int32_t D = p.D;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * G + (R == 32 ? threadIdx.x >> 5 : 0);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_of(R);
+    const int64_t group = static_cast<int64_t>(blockIdx.x) * rows_of(R) + sub;
     int64_t row = group;
     const float inv_d = 1.f / static_cast<float>(D);
-    float w[NV][VEC], dw[NV][VEC];
+    [[maybe_unused]] float w[kKeep ? NV : 1][VEC];
+    float dw[NV][VEC];
     Raw<T, VEC> a[NV], b[NV], e[NV];
     float rstd = 0.f;
     let_next_start();
@@ -238,8 +273,9 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int32_t col = (j * R + t) * VEC;
+        if constexpr (kKeep) if (col < D) ld_w<VEC>(p.w, col, w[j]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) { w[j][i] = col < D ? __ldg(p.w + col + i) : 0.f; dw[j][i] = 0.f; }
+        for (int i = 0; i < VEC; ++i) dw[j][i] = 0.f;
     }
     for (int slot = 0; row < p.C; row += step, slot ^= 1) {
         float g[NV][VEC], n[NV][VEC], d[NV][VEC], s = 0.f;
@@ -248,6 +284,13 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
         for (int j = 0; j < NV; ++j) {
             const int32_t col = (j * R + t) * VEC;
             if (col < D) {
+                float v[VEC];
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[i] = w[j][i];
+                } else {
+                    ld_w<VEC>(p.w, col, v);
+                }
                 unpack(a[j], g[j]);
                 unpack(b[j], n[j]);
                 if (p.dh) unpack(e[j], d[j]);
@@ -255,7 +298,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
                 for (int i = 0; i < VEC; ++i) {
                     n[j][i] *= rs;
                     dw[j][i] = fmaf(g[j][i], n[j][i], dw[j][i]);
-                    g[j][i] *= w[j][i];
+                    g[j][i] *= v[i];
                     s = fmaf(g[j][i], n[j][i], s);
                 }
             }
@@ -271,7 +314,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
                 if (p.dh) e[j] = ld<T, VEC>(p.dh, next * D + col);
             }
         }
-        const float m = row_sum<R>(s, sm[slot]) * inv_d;
+        const float m = row_sum<R>(s, sm[slot][sub]) * inv_d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int32_t col = (j * R + t) * VEC;
@@ -288,9 +331,165 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) rmsnorm_bwd_kernel(NormBwd 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int32_t col = (j * R + t) * VEC;
-        if (col < D)
+        if (col < D) {
+#pragma unroll
             for (int i = 0; i < VEC; ++i) p.part[group * D + col + i] = dw[j][i];
+        }
     }
+}
+
+// ---- backward with rows copied ahead into shared memory ----------------------------------
+// The registers of a backward row (dw's sums, weights, two unpacked streams) leave too few
+// threads for the loads that HBM wants on their way.  Rows of 1 KB and more are copied by
+// cp.async.bulk into a ring of `stages` rows instead, whose bytes in flight do not depend on
+// registers: 65,536 rows of 2,048 bf16 values with dh 5618 -> 6554 GB/s, without 3921 -> 6134.
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(tc::smem_addr(dst)), "l"(src), "r"(bytes), "r"(tc::smem_addr(bar)) : "memory");
+}
+
+template <typename T, int VEC, int R, int NV>
+__global__ void __launch_bounds__(R) rmsnorm_bwd_ring_kernel(NormBwd p, int stages) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float sm[2][R / 32];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int s_fail;
+    const int t = threadIdx.x;
+    const int32_t D = p.D;
+    const int64_t step = gridDim.x;
+    const uint32_t bytes = static_cast<uint32_t>(D) * sizeof(T), stage = bytes * (p.dh ? 3 : 2);
+    const float inv_d = 1.f / static_cast<float>(D);
+    auto fetch = [&](int64_t row, int s) {              // thread 0
+        uint8_t *dst = ring + s * stage;
+        tc::mbar_expect_tx(&full[s], stage);
+        bulk_load(dst, static_cast<const T *>(p.dy) + row * D, bytes, &full[s]);
+        bulk_load(dst + bytes, static_cast<const T *>(p.h) + row * D, bytes, &full[s]);
+        if (p.dh) bulk_load(dst + 2 * bytes, static_cast<const T *>(p.dh) + row * D, bytes, &full[s]);
+    };
+    // A wait that runs out is reported once and never waited for again; the block goes on with
+    // what its shared memory holds, so that its barriers stay matched.
+    auto wait = [&](int s, uint32_t phase) {
+        if (tc::mbar_try(&full[s], phase) || *reinterpret_cast<volatile int *>(&s_fail)) return;
+        if (!tc::mbar_wait(&full[s], phase)) {
+            *reinterpret_cast<volatile int *>(&s_fail) = 1;
+            if (p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
+        }
+    };
+    if (t == 0) {
+        s_fail = 0;
+        for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
+        tc::fence_mbar_init();
+        for (int s = 0; s < stages && blockIdx.x + s * step < p.C; ++s) fetch(blockIdx.x + s * step, s);
+    }
+    let_next_start();
+    float w[NV][VEC], dw[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int32_t col = (j * R + t) * VEC;
+        if (col < D) ld_w<VEC>(p.w, col, w[j]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[j][i] = 0.f;
+    }
+    __syncthreads();
+    int s = 0, slot = 0;
+    uint32_t phase = 0;
+    float next_rs = blockIdx.x < p.C ? __ldg(p.rstd + blockIdx.x) : 0.f;
+    for (int64_t row = blockIdx.x; row < p.C; row += step, slot ^= 1) {
+        const float rs = next_rs;
+        if (row + step < p.C) next_rs = __ldg(p.rstd + row + step);
+        wait(s, phase);
+        const T *buf = reinterpret_cast<const T *>(ring + s * stage);
+        float g[NV][VEC], n[NV][VEC], sum = 0.f;
+        Raw<T, VEC> e[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int32_t col = (j * R + t) * VEC;
+            if (col < D) {
+                unpack(ld<T, VEC>(buf, col), g[j]);
+                unpack(ld<T, VEC>(buf + D, col), n[j]);
+                if (p.dh) e[j] = ld<T, VEC>(buf + 2 * D, col);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    n[j][i] *= rs;
+                    dw[j][i] = fmaf(g[j][i], n[j][i], dw[j][i]);
+                    g[j][i] *= w[j][i];
+                    sum = fmaf(g[j][i], n[j][i], sum);
+                }
+            }
+        }
+        const float m = row_sum<R>(sum, sm[slot]) * inv_d;      // behind its barrier the stage is free
+        if (t == 0 && row + stages * step < p.C) fetch(row + stages * step, s);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int32_t col = (j * R + t) * VEC;
+            if (col < D) {
+                float d[VEC];
+                if (p.dh) unpack(e[j], d);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    g[j][i] = rs * (g[j][i] - n[j][i] * m);
+                    if (p.dh) g[j][i] += d[i];
+                }
+                st<T, VEC>(p.dx, row * D + col, g[j]);
+            }
+        }
+        if (++s == stages) { s = 0; phase ^= 1; }
+    }
+    if (t == 0 && *reinterpret_cast<volatile int *>(&s_fail))       // copies in flight, after a failure
+        for (int i = 0; i < stages; ++i) tc::mbar_wait(&full[i], 0, 100000000LL), tc::mbar_wait(&full[i], 1, 100000000LL);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int32_t col = (j * R + t) * VEC;
+        if (col < D) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) p.part[blockIdx.x * static_cast<int64_t>(D) + col + i] = dw[j][i];
+        }
+    }
+}
+
+// Rows above 8,192 values: a block of 1,024 threads reads them twice, the second time from L2,
+// and keeps dw's sums in shared memory.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(NormBwd p) {
+    extern __shared__ float sdw[];
+    __shared__ float sm[2][32];
+    const int32_t D = p.D;
+    const float inv_d = 1.f / static_cast<float>(D);
+    let_next_start();
+    for (int32_t c = threadIdx.x * VEC; c < D; c += 1024 * VEC)
+        for (int i = 0; i < VEC; ++i) sdw[c + i] = 0.f;
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < p.C; row += gridDim.x, slot ^= 1) {
+        const float rs = __ldg(p.rstd + row);
+        float sum = 0.f;
+        for (int32_t c = threadIdx.x * VEC; c < D; c += 1024 * VEC) {
+            float g[VEC], n[VEC], w[VEC];
+            unpack(ld<T, VEC>(p.dy, row * D + c), g);
+            unpack(ld<T, VEC>(p.h, row * D + c), n);
+            ld_w<VEC>(p.w, c, w);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sum = fmaf(g[i] * w[i], n[i] * rs, sum);
+        }
+        const float m = row_sum<1024>(sum, sm[slot]) * inv_d;
+        for (int32_t c = threadIdx.x * VEC; c < D; c += 1024 * VEC) {
+            float g[VEC], n[VEC], w[VEC], d[VEC];
+            unpack(ld<T, VEC>(p.dy, row * D + c), g);
+            unpack(ld<T, VEC>(p.h, row * D + c), n);
+            if (p.dh) unpack(ld<T, VEC>(p.dh, row * D + c), d);
+            ld_w<VEC>(p.w, c, w);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                n[i] *= rs;
+                sdw[c + i] = fmaf(g[i], n[i], sdw[c + i]);
+                g[i] = rs * (g[i] * w[i] - n[i] * m);
+                if (p.dh) g[i] += d[i];
+            }
+            st<T, VEC>(p.dx, row * D + c, g);
+        }
+    }
+    for (int32_t c = threadIdx.x * VEC; c < D; c += 1024 * VEC)
+        for (int i = 0; i < VEC; ++i) p.part[blockIdx.x * static_cast<int64_t>(D) + c + i] = sdw[c + i];
 }
 
 // dw[j] = sum over the groups' column sums: 32 warps take every 32nd group each, in ascending
@@ -315,51 +514,123 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(DwParams p) {
     }
 }
 
-// Threads of a row: few enough that each keeps up to 16 values (8 of unaligned rows, whose
-// loads are single values), but never under a warp.
-struct Shape { int vec, r; };
-Shape shape_of(int32_t dtype, int32_t D) {
+// Threads of a row (R) and values that each of them keeps.  What counts is that R * values is
+// little above D -- idle threads hold registers that could hold loads -- and how many bytes are
+// on their way.  Measured in GB/s at 2^27 bf16 values, forward with / without a residual:
+//   D = 1024: R 32 x 32 6218 / 5958, 64 x 16 6242 / 4855, 128 x 16 5825 / 4345
+//   D = 4096: R 128 x 32 6242 / 6096, 256 x 16 6473 / 5574, 256 x 32 6019 / 4599
+// so the forward keeps 32 values.  The backward needs registers for dw's sums too:
+//   D = 1024: R 32 x 32 5444, 64 x 16 5405, 128 x 8 5937, 128 x 16 4096
+//   D = 2048: R 64 x 32 5405, 128 x 16 5699, 256 x 8 5510, 256 x 16 4263
+// so it keeps 16, and at least 128 threads beyond a warp.  Rows that are not whole vectors move
+// single values; 8 a thread measured best in both directions (D = 2001: 256 x 8 4723 / 3799
+// forward / backward, 128 x 16 4681 / 3312).
+struct Shape { int vec, r, values; };
+Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     const int full = dtype == HARTS_BF16 ? 8 : 4;
     Shape s;
     s.vec = D % full == 0 ? full : 1;
-    const int per = s.vec == 1 ? 8 : 16;
-    s.r = D <= 32 * per ? 32 : D <= 128 * per ? 128 : D <= 256 * per ? 256 : D <= 512 * per ? 512 : 1024;
+    const int most = s.vec == 1 ? 8 : backward ? 16 : 32;
+    s.r = 32;
+    while (s.r < 1024 && s.r * most < D) s.r = backward && s.vec > 1 && s.r == 32 ? 128 : s.r * 2;
+    s.values = 8;
+    while (s.r * s.values < D) s.values *= 2;
     return s;
 }
 
-// Groups of R threads that work at a time, at most: 1,024 threads an SM.
-int64_t group_limit(const Shape &s) {
-    return static_cast<int64_t>(sm_count()) * (s.r == 32 ? 4 * 8 : std::max(1, 1024 / s.r));
-}
+// Most groups of R threads that are resident at a time, whatever the kernel's registers.
 int64_t groups_of(const Shape &s, int64_t C) {
-    const int64_t g = std::min<int64_t>(C, group_limit(s));
-    return s.r == 32 ? (g + 3) / 4 * 4 : g;
+    const int64_t rows = rows_of(s.r), blocks = std::min<int64_t>((C + rows - 1) / rows, int64_t(sm_count()) * (2048 / block_of(s.r)));
+    return blocks * rows;
 }
 
-template <typename T, int VEC, int R, int NV>
-void launch_fwd(const NormFwd &p, int grid, cudaStream_t st) {
+// Blocks of a persistent kernel: as many as are resident at a time, but no more than have rows.
+template <typename F>
+int grid_of(F *kernel, int R, int64_t C, std::atomic<int> &known) {
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block_of(R), 0) != cudaSuccess || n < 1) n = 1;
+        known.store(n, std::memory_order_relaxed);
+    }
+    const int64_t rows = rows_of(R);
+    return static_cast<int>(std::min<int64_t>((C + rows - 1) / rows, int64_t(sm_count()) * n));
+}
+
+template <typename T, int VEC, int R, int VT>
+cudaError_t launch_fwd(const NormFwd &p, int64_t *, cudaStream_t st) {
+    constexpr int NV = VT / VEC;
     if constexpr (VEC > 1) {
         if (p.y8) {
-            rmsnorm_fwd_kernel<T, VEC, R, NV, true><<<grid, R == 32 ? 128 : R, 0, st>>>(p);
-            return;
+            static std::atomic<int> known{0};
+            auto *k = rmsnorm_fwd_kernel<T, VEC, R, NV, true>;
+            return launch(k, grid_of(k, R, p.C, known), block_of(R), 0, 1, false, st, p);
         }
     }
-    rmsnorm_fwd_kernel<T, VEC, R, NV, false><<<grid, R == 32 ? 128 : R, 0, st>>>(p);
+    static std::atomic<int> known{0};
+    auto *k = rmsnorm_fwd_kernel<T, VEC, R, NV, false>;
+    return launch(k, grid_of(k, R, p.C, known), block_of(R), 0, 1, false, st, p);
 }
-template <typename T, int VEC, int R, int NV>
-void launch_bwd(const NormBwd &p, int grid, cudaStream_t st) {
-    rmsnorm_bwd_kernel<T, VEC, R, NV><<<grid, R == 32 ? 128 : R, 0, st>>>(p);
+template <typename T, int VEC, int R, int VT>
+cudaError_t launch_bwd(const NormBwd &p, int64_t *groups, cudaStream_t st) {
+    static std::atomic<int> known{0};
+    if constexpr (VEC > 1 && R >= 128) {
+        static std::atomic<uint64_t> allowed{0};
+        auto *k = rmsnorm_bwd_ring_kernel<T, VEC, R, VT / VEC>;
+        // 45 KB of rows on their way for each 128 threads
+        const size_t stage = size_t(p.D) * sizeof(T) * (p.dh ? 3 : 2), budget = size_t(45) * 1024 * R / 128;
+        const int stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, budget / stage)));
+        const cudaError_t e = allow_smem(k, 200 * 1024, allowed);       // two stages of 8,192 fp32 values are 192 KB
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, R, stages * stage) != cudaSuccess || n < 1) n = 1;
+        const int64_t grid = std::min<int64_t>(p.C, int64_t(sm_count()) * n);
+        *groups = grid;
+        return launch(k, grid, R, stages * stage, 1, false, st, p, stages);
+    } else {
+        auto *k = rmsnorm_bwd_kernel<T, VEC, R, VT / VEC>;
+        const int grid = grid_of(k, R, p.C, known);
+        *groups = int64_t(grid) * rows_of(R);
+        return launch(k, grid, block_of(R), 0, 1, false, st, p);
+    }
+}
+template <typename T, int VEC>
+cudaError_t launch_bwd_long(const NormBwd &p, int64_t *groups, cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    auto *k = rmsnorm_bwd_long_kernel<T, VEC>;
+    const cudaError_t e = allow_smem(k, kMaxDim * sizeof(float), allowed);
+    if (e != cudaSuccess) return e;
+    *groups = std::min<int64_t>(p.C, sm_count() * 2);
+    return launch(k, *groups, 1024, size_t(p.D) * sizeof(float), 1, false, st, p);
 }
 
-#define HARTS_NORM_DISPATCH(LAUNCH, T, VEC, NV, p, s, grid, st)                                     \
-    do {                                                                                            \
-        if ((s).r == 32) LAUNCH<T, VEC, 32, NV>(p, grid, st);                                       \
-        else if ((s).r == 128) LAUNCH<T, VEC, 128, NV>(p, grid, st);                                \
-        else if ((s).r == 256) LAUNCH<T, VEC, 256, NV>(p, grid, st);                                \
-        else if ((s).r == 512) LAUNCH<T, VEC, 512, NV>(p, grid, st);                                \
-        else if (VEC > 1 || (p).D <= 8192) LAUNCH<T, VEC, 1024, NV>(p, grid, st);                   \
-        else LAUNCH<T, VEC, 1024, VEC == 1 ? 16 : NV>(p, grid, st);                                 \
-    } while (0)
+// The instances that shape_of names.
+#define HARTS_NORM_CASE(LAUNCH, T, VEC, R, VT) \
+    if (s.vec == VEC && s.r == R && s.values == VT) return LAUNCH<T, VEC, R, VT>(p, groups, st);
+#define HARTS_NORM_SINGLE(LAUNCH, T)                                                                                \
+    HARTS_NORM_CASE(LAUNCH, T, 1, 32, 8) HARTS_NORM_CASE(LAUNCH, T, 1, 64, 8) HARTS_NORM_CASE(LAUNCH, T, 1, 128, 8) \
+    HARTS_NORM_CASE(LAUNCH, T, 1, 256, 8) HARTS_NORM_CASE(LAUNCH, T, 1, 512, 8)                                     \
+    HARTS_NORM_CASE(LAUNCH, T, 1, 1024, 8)
+
+template <typename T, int VEC>
+cudaError_t run_fwd(const Shape &s, const NormFwd &p, cudaStream_t st) {
+    int64_t *groups = nullptr;
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 8) HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 16)
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 32) HARTS_NORM_CASE(launch_fwd, T, VEC, 64, 32)
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 128, 32) HARTS_NORM_CASE(launch_fwd, T, VEC, 256, 32)
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 512, 32)
+    HARTS_NORM_SINGLE(launch_fwd, T)
+    HARTS_NORM_CASE(launch_fwd, T, 1, 1024, 16)
+    return cudaErrorInvalidValue;
+}
+template <typename T, int VEC>
+cudaError_t run_bwd(const Shape &s, const NormBwd &p, int64_t *groups, cudaStream_t st) {
+    if (p.D > kLongRow) return s.vec == VEC ? launch_bwd_long<T, VEC>(p, groups, st) : launch_bwd_long<T, 1>(p, groups, st);
+    HARTS_NORM_CASE(launch_bwd, T, VEC, 32, 8) HARTS_NORM_CASE(launch_bwd, T, VEC, 32, 16)
+    HARTS_NORM_CASE(launch_bwd, T, VEC, 128, 8) HARTS_NORM_CASE(launch_bwd, T, VEC, 128, 16)
+    HARTS_NORM_CASE(launch_bwd, T, VEC, 256, 16) HARTS_NORM_CASE(launch_bwd, T, VEC, 512, 16)
+    HARTS_NORM_SINGLE(launch_bwd, T)
+    return cudaErrorInvalidValue;
+}
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -370,11 +641,9 @@ int check_common(int64_t C, int32_t D, int32_t dtype) {
     return HARTS_OK;
 }
 
-int launched(const char *what) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) { set_error(std::string(what) + ": " + cudaGetErrorString(e)); return HARTS_ECUDA; }
-    set_error("");
-    return HARTS_OK;
+int cuda_fail(cudaError_t e, const char *what) {
+    set_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return HARTS_ECUDA;
 }
 
 }  // namespace
@@ -395,30 +664,25 @@ int harts_rmsnorm_fwd(const harts_rmsnorm_fwd_args *a, harts_stream_t stream) {
     if (a->residual && !a->h) { set_error("h is required with a residual"); return HARTS_EINVAL; }
     if ((a->y8 == nullptr) != (a->y8_scale == nullptr)) { set_error("y8 and y8_scale go together"); return HARTS_EINVAL; }
     if (a->y8 && a->D % kMxBlock) { set_error("the 8-bit output needs D a multiple of 32"); return HARTS_EUNSUPPORTED; }
-    if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->h) || !aligned16(a->y) || !aligned16(a->y8)) {
-        set_error("x, residual, h, y and y8 must be 16-byte aligned");
+    if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->h) || !aligned16(a->y) ||
+        !aligned16(a->y8)) {
+        set_error("x, residual, weight, h, y and y8 must be 16-byte aligned");
         return HARTS_EINVAL;
     }
     NormFwd p;
     p.x = a->x; p.res = a->residual; p.w = a->weight; p.h = a->h; p.y = a->y; p.y8 = a->y8;
     p.scale8 = static_cast<uint8_t *>(a->y8_scale); p.rstd = a->rstd; p.C = a->C; p.D = a->D; p.eps = a->eps;
-    const Shape s = shape_of(a->dtype, a->D);
-    const int64_t groups = groups_of(s, a->C);
-    const int grid = static_cast<int>(s.r == 32 ? groups / 4 : groups);
+    const Shape s = shape_of(a->dtype, a->D, false);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a->dtype == HARTS_BF16) {
-        if (s.vec == 8) HARTS_NORM_DISPATCH(launch_fwd, __nv_bfloat16, 8, 2, p, s, grid, st);
-        else HARTS_NORM_DISPATCH(launch_fwd, __nv_bfloat16, 1, 8, p, s, grid, st);
-    } else {
-        if (s.vec == 4) HARTS_NORM_DISPATCH(launch_fwd, float, 4, 4, p, s, grid, st);
-        else HARTS_NORM_DISPATCH(launch_fwd, float, 1, 8, p, s, grid, st);
-    }
-    return launched("rmsnorm forward launch");
+    const cudaError_t e = a->dtype == HARTS_BF16 ? run_fwd<__nv_bfloat16, 8>(s, p, st) : run_fwd<float, 4>(s, p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "rmsnorm forward launch");
+    set_error("");
+    return HARTS_OK;
 }
 
 size_t harts_rmsnorm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype) {
     if (C < 0 || D < 1 || D > kMaxDim || (dtype != HARTS_FP32 && dtype != HARTS_BF16)) return 0;
-    return std::max<size_t>(256, sizeof(float) * static_cast<size_t>(groups_of(shape_of(dtype, D), C)) * D);
+    return std::max<size_t>(256, sizeof(float) * static_cast<size_t>(groups_of(shape_of(dtype, D, true), C)) * D);
 }
 
 int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
@@ -429,13 +693,14 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (a->C == 0) {
         const cudaError_t e = cudaMemsetAsync(a->dweight, 0, sizeof(float) * a->D, st);
-        if (e != cudaSuccess) { set_error(std::string("rmsnorm backward: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
+        if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward");
         set_error("");
         return HARTS_OK;
     }
     if (!a->dy || !a->h || !a->weight || !a->rstd || !a->dx) { set_error("NULL dy, h, weight, rstd or dx"); return HARTS_EINVAL; }
-    if (!aligned16(a->dy) || !aligned16(a->h) || !aligned16(a->dh) || !aligned16(a->dx) || !aligned16(a->workspace)) {
-        set_error("dy, h, dh, dx and workspace must be 16-byte aligned");
+    if (!aligned16(a->dy) || !aligned16(a->h) || !aligned16(a->dh) || !aligned16(a->weight) || !aligned16(a->dx) ||
+        !aligned16(a->workspace)) {
+        set_error("dy, h, dh, weight, dx and workspace must be 16-byte aligned");
         return HARTS_EINVAL;
     }
     if (!a->workspace || a->workspace_bytes < harts_rmsnorm_bwd_workspace_bytes(a->C, a->D, a->dtype)) {
@@ -444,22 +709,15 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
     }
     NormBwd p;
     p.dy = a->dy; p.h = a->h; p.dh = a->dh; p.w = a->weight; p.rstd = a->rstd; p.dx = a->dx;
-    p.part = static_cast<float *>(a->workspace); p.C = a->C; p.D = a->D;
-    const Shape s = shape_of(a->dtype, a->D);
-    const int64_t groups = groups_of(s, a->C);
-    const int grid = static_cast<int>(s.r == 32 ? groups / 4 : groups);
-    if (a->dtype == HARTS_BF16) {
-        if (s.vec == 8) HARTS_NORM_DISPATCH(launch_bwd, __nv_bfloat16, 8, 2, p, s, grid, st);
-        else HARTS_NORM_DISPATCH(launch_bwd, __nv_bfloat16, 1, 8, p, s, grid, st);
-    } else {
-        if (s.vec == 4) HARTS_NORM_DISPATCH(launch_bwd, float, 4, 4, p, s, grid, st);
-        else HARTS_NORM_DISPATCH(launch_bwd, float, 1, 8, p, s, grid, st);
-    }
-    const int ok = launched("rmsnorm backward launch");
-    if (ok) return ok;
+    p.part = static_cast<float *>(a->workspace); p.error = a->error; p.C = a->C; p.D = a->D;
+    int64_t groups = 0;
+    const Shape s = shape_of(a->dtype, a->D, true);
+    cudaError_t e = a->dtype == HARTS_BF16 ? run_bwd<__nv_bfloat16, 8>(s, p, &groups, st) : run_bwd<float, 4>(s, p, &groups, st);
+    if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward launch");
     const DwParams d{p.part, a->dweight, a->D, static_cast<int32_t>(groups)};
-    const cudaError_t e = launch(rmsnorm_dw_kernel, (a->D + 31) / 32, 1024, 0, 1, true, st, d);
-    if (e != cudaSuccess) { set_error(std::string("rmsnorm backward launch: ") + cudaGetErrorString(e)); return HARTS_ECUDA; }
+    e = launch(rmsnorm_dw_kernel, (a->D + 31) / 32, 1024, 0, 1, true, st, d);
+    if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward launch");
+    set_error("");
     return HARTS_OK;
 }
 
