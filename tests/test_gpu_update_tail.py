@@ -1,0 +1,61 @@
+"""The update-tail example: its gradients against the fp64 oracle's chain, and its loss over
+a few clipped steps.
+
+Bounds.  The rows are rounded to bf16 twice on the way down (norm's output, the head's dx) and
+once at the end, dz once; each is off by at most 2^-8 of its value, so a gradient that is a sum
+of many such terms of either sign is off by less than 4 * 2^-8 = 1.6e-2 in relative L2."""
+import os
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import tail as otail
+from tests._parity import rel_l2
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from prefix_shared_chunkwise_gb300 import build
+    build.build()
+
+
+def test_gradients_against_the_oracle():
+    from update_tail import Tail
+    t = Tail("fig1_fp32", 256, 1003, seed=3)
+    loss = t.gradients()
+    norm = t.grads.clip(0.01)
+    torch.cuda.synchronize()
+    assert int(t.error) == 0
+    f64 = lambda a: a.double().cpu().numpy()
+    bf = lambda a: f64(a.to(torch.bfloat16))
+    C, S = t.hidden.shape[0], t.target.numel()
+    ptr, sem = t.row_ptr.cpu().numpy(), t.row_sem.cpu().numpy()
+    sem_row = np.empty(S, np.int64)
+    sem_row[sem] = np.repeat(np.arange(C), np.diff(ptr))
+    y, h, rstd = otail.rmsnorm_fwd(bf(t.hidden), f64(t.residual), f64(t.norm_w), 1e-6)
+    target, g = t.target.cpu().numpy().astype(np.int64), -f64(t.adv) / S
+    logp, _ = otail.linear_logprob_fwd(y, bf(t.head), sem_row, target)
+    assert abs(float(loss) + float((f64(t.adv) * logp).mean())) <= 2.0 ** -8 * abs(float(loss))
+    dx, dhead = otail.linear_logprob_bwd(y, bf(t.head), sem_row, target, g)
+    dh, dnorm = otail.rmsnorm_bwd(dx, h, f64(t.norm_w), rstd)
+    for got, ref in ((t.d_hidden, dh), (t.d_head, dhead), (t.d_norm, dnorm)):
+        assert rel_l2(f64(got), ref) <= 1.6e-2
+    n, clipped = otail.grad_clip([dh, dhead, dnorm], 0.01)
+    assert abs(float(norm) - n) <= 1.6e-2 * n
+    for got, ref in zip(t.clipped, clipped):
+        assert rel_l2(f64(got), ref) <= 3.2e-2
+
+
+def test_loss_goes_down():
+    from update_tail import main
+    losses = main(["--steps", "12", "--dim", "264", "--vocab", "777"])
+    assert losses[-1] < losses[0] and all(np.isfinite(losses))
