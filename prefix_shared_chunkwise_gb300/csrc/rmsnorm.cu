@@ -12,9 +12,9 @@
 // the column sums of dw) of its columns in registers over all its rows where they fit --
 // fp32 weights re-read per row would be as many bytes as two bf16 streams -- and the next
 // row's loads are under way before the current row's reduction: in registers forward and for
-// short rows, by bulk copies into shared memory for longer rows backward.  dw: each group of
-// R threads writes its column sums, a second kernel adds them in ascending order: no atomics,
-// the same bits on every run.
+// short rows, by bulk copies into shared memory for longer rows backward.  dw: each block
+// writes its column sums, a second kernel adds them in ascending order: no atomics, the same
+// bits on every run.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -101,12 +101,18 @@ constexpr int rows_of(int R) { return block_of(R) / R; }        // rows it works
 constexpr int kRegValues = 16;
 
 // Sum over the R threads of a row.  sm holds two slots a row, used in turn, so that one barrier
-// per row is enough; rows of a block that has several do not wait for each other.
+// per row is enough; rows of a block (or of a warp, under 32 threads a row) do not wait for each
+// other.
+template <int R>
+__device__ __forceinline__ uint32_t row_lanes() {
+    if constexpr (R >= 32) return 0xffffffffu;
+    else return ((1u << R) - 1u) << ((threadIdx.x & 31) & ~(R - 1));
+}
 template <int R>
 __device__ __forceinline__ float row_sum(float v, float *sm) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (R == 32) return v;
+    for (int o = (R < 32 ? R : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(row_lanes<R>(), v, o);
+    if constexpr (R <= 32) return v;
     const int in_row = (threadIdx.x % R) >> 5;
     if ((threadIdx.x & 31) == 0) sm[in_row] = v;
     if constexpr (R < 128) asm volatile("bar.sync %0, %1;" :: "r"(1 + static_cast<int>(threadIdx.x) / R), "n"(R) : "memory");
@@ -173,7 +179,7 @@ __device__ __forceinline__ void store_mx(uint8_t *y8, uint8_t *scale8, int64_t r
 template <typename T, int VEC, int R, int NV, bool MX>
 __global__ void __launch_bounds__(block_of(R)) rmsnorm_fwd_kernel(NormFwd p) {
     constexpr bool kKeep = NV * VEC <= kRegValues;
-    __shared__ float sm[2][rows_of(R)][R / 32];
+    __shared__ float sm[2][rows_of(R)][R < 32 ? 1 : R / 32];
     const int t = threadIdx.x % R, sub = threadIdx.x / R;
     const int32_t D = p.D;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows_of(R);
@@ -248,12 +254,11 @@ __global__ void __launch_bounds__(block_of(R)) rmsnorm_fwd_kernel(NormFwd p) {
 template <typename T, int VEC, int R, int NV>
 __global__ void __launch_bounds__(block_of(R)) rmsnorm_bwd_kernel(NormBwd p) {
     constexpr bool kKeep = NV * VEC <= kRegValues;
-    __shared__ float sm[2][rows_of(R)][R / 32];
+    __shared__ float sm[2][rows_of(R)][R < 32 ? 1 : R / 32];
     const int t = threadIdx.x % R, sub = threadIdx.x / R;
     const int32_t D = p.D;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows_of(R);
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * rows_of(R) + sub;
-    int64_t row = group;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * rows_of(R) + sub;
     const float inv_d = 1.f / static_cast<float>(D);
     [[maybe_unused]] float w[kKeep ? NV : 1][VEC];
     float dw[NV][VEC];
@@ -328,12 +333,28 @@ __global__ void __launch_bounds__(block_of(R)) rmsnorm_bwd_kernel(NormBwd p) {
             }
         }
     }
+    // the rows of a block leave one sum, added in ascending order
+    constexpr int kRows = rows_of(R);
+    __shared__ float all[kRows > 1 ? kRows : 1][kRows > 1 ? R * NV * VEC : 1];
+    float *part = p.part + blockIdx.x * static_cast<int64_t>(D);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int32_t col = (j * R + t) * VEC;
         if (col < D) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) p.part[group * D + col + i] = dw[j][i];
+            for (int i = 0; i < VEC; ++i) {
+                if constexpr (kRows > 1) all[sub][col + i] = dw[j][i];
+                else part[col + i] = dw[j][i];
+            }
+        }
+    }
+    if constexpr (kRows > 1) {
+        __syncthreads();
+        for (int32_t c = threadIdx.x; c < D; c += block_of(R)) {
+            float v = all[0][c];
+#pragma unroll
+            for (int k = 1; k < kRows; ++k) v += all[k][c];
+            part[c] = v;
         }
     }
 }
@@ -522,7 +543,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(DwParams p) {
 // so the forward keeps 32 values.  The backward needs registers for dw's sums too:
 //   D = 1024: R 32 x 32 5444, 64 x 16 5405, 128 x 8 5937, 128 x 16 4096
 //   D = 2048: R 64 x 32 5405, 128 x 16 5699, 256 x 8 5510, 256 x 16 4263
-// so it keeps 16, and at least 128 threads beyond a warp.  Rows that are not whole vectors move
+// so it keeps 16, and at least 128 threads beyond a warp.  Short rows share a warp.  Rows that are not whole vectors move
 // single values; 8 a thread measured best in both directions (D = 2001: 256 x 8 4723 / 3799
 // forward / backward, 128 x 16 4681 / 3312).
 struct Shape { int vec, r, values; };
@@ -531,17 +552,17 @@ Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     Shape s;
     s.vec = D % full == 0 ? full : 1;
     const int most = s.vec == 1 ? 8 : backward ? 16 : 32;
-    s.r = 32;
+    s.r = s.vec == 1 ? 32 : 8;
     while (s.r < 1024 && s.r * most < D) s.r = backward && s.vec > 1 && s.r == 32 ? 128 : s.r * 2;
     s.values = 8;
     while (s.r * s.values < D) s.values *= 2;
     return s;
 }
 
-// Most groups of R threads that are resident at a time, whatever the kernel's registers.
-int64_t groups_of(const Shape &s, int64_t C) {
-    const int64_t rows = rows_of(s.r), blocks = std::min<int64_t>((C + rows - 1) / rows, int64_t(sm_count()) * (2048 / block_of(s.r)));
-    return blocks * rows;
+// Most blocks that are resident at a time, whatever the kernel's registers.
+int64_t blocks_of(const Shape &s, int64_t C) {
+    const int64_t rows = rows_of(s.r);
+    return std::min<int64_t>((C + rows - 1) / rows, int64_t(sm_count()) * (2048 / block_of(s.r)));
 }
 
 // Blocks of a persistent kernel: as many as are resident at a time, but no more than have rows.
@@ -589,7 +610,7 @@ cudaError_t launch_bwd(const NormBwd &p, int64_t *groups, cudaStream_t st) {
     } else {
         auto *k = rmsnorm_bwd_kernel<T, VEC, R, VT / VEC>;
         const int grid = grid_of(k, R, p.C, known);
-        *groups = int64_t(grid) * rows_of(R);
+        *groups = grid;
         return launch(k, grid, block_of(R), 0, 1, false, st, p);
     }
 }
@@ -614,7 +635,8 @@ cudaError_t launch_bwd_long(const NormBwd &p, int64_t *groups, cudaStream_t st) 
 template <typename T, int VEC>
 cudaError_t run_fwd(const Shape &s, const NormFwd &p, cudaStream_t st) {
     int64_t *groups = nullptr;
-    HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 8) HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 16)
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 8, 8) HARTS_NORM_CASE(launch_fwd, T, VEC, 8, 16)
+    HARTS_NORM_CASE(launch_fwd, T, VEC, 8, 32) HARTS_NORM_CASE(launch_fwd, T, VEC, 16, 32)
     HARTS_NORM_CASE(launch_fwd, T, VEC, 32, 32) HARTS_NORM_CASE(launch_fwd, T, VEC, 64, 32)
     HARTS_NORM_CASE(launch_fwd, T, VEC, 128, 32) HARTS_NORM_CASE(launch_fwd, T, VEC, 256, 32)
     HARTS_NORM_CASE(launch_fwd, T, VEC, 512, 32)
@@ -625,7 +647,8 @@ cudaError_t run_fwd(const Shape &s, const NormFwd &p, cudaStream_t st) {
 template <typename T, int VEC>
 cudaError_t run_bwd(const Shape &s, const NormBwd &p, int64_t *groups, cudaStream_t st) {
     if (p.D > kLongRow) return s.vec == VEC ? launch_bwd_long<T, VEC>(p, groups, st) : launch_bwd_long<T, 1>(p, groups, st);
-    HARTS_NORM_CASE(launch_bwd, T, VEC, 32, 8) HARTS_NORM_CASE(launch_bwd, T, VEC, 32, 16)
+    HARTS_NORM_CASE(launch_bwd, T, VEC, 8, 8) HARTS_NORM_CASE(launch_bwd, T, VEC, 8, 16)
+    HARTS_NORM_CASE(launch_bwd, T, VEC, 16, 16) HARTS_NORM_CASE(launch_bwd, T, VEC, 32, 16)
     HARTS_NORM_CASE(launch_bwd, T, VEC, 128, 8) HARTS_NORM_CASE(launch_bwd, T, VEC, 128, 16)
     HARTS_NORM_CASE(launch_bwd, T, VEC, 256, 16) HARTS_NORM_CASE(launch_bwd, T, VEC, 512, 16)
     HARTS_NORM_SINGLE(launch_bwd, T)
@@ -682,7 +705,7 @@ int harts_rmsnorm_fwd(const harts_rmsnorm_fwd_args *a, harts_stream_t stream) {
 
 size_t harts_rmsnorm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype) {
     if (C < 0 || D < 1 || D > kMaxDim || (dtype != HARTS_FP32 && dtype != HARTS_BF16)) return 0;
-    return std::max<size_t>(256, sizeof(float) * static_cast<size_t>(groups_of(shape_of(dtype, D, true), C)) * D);
+    return std::max<size_t>(256, sizeof(float) * static_cast<size_t>(blocks_of(shape_of(dtype, D, true), C)) * D);
 }
 
 int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {

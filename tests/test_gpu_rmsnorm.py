@@ -89,6 +89,29 @@ def test_backward(dtype, residual, C, D):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)          # no order of additions left open
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("C,D", [(1, 64), (7, 40), (33, 64), (1000, 128), (129, 96), (5, 256), (1003, 200), (77, 512),
+                                 (2, 2048), (500, 2048), (9, 4096), (5, 8192), (3, 12288), (6, 9000)])
+def test_short_and_long_rows(dtype, C, D):
+    """Several rows a warp or a block, rows copied ahead, rows read twice; C below and above
+    what a block works on at a time."""
+    td, r = DT[dtype]
+    x, res, w = _rand((C, D), td, 1), _rand((C, D), td, 2), _rand((D,), torch.float32, 3)
+    _, h, rstd = _check_fwd(x, res, w, dtype)
+    dy, dh = _rand((C, D), td, 4), _rand((C, D), td, 5)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for d in (None, dh):
+        dx, dw = rmsnorm_bwd(dy, h, w, rstd, d, error=err)
+        torch.cuda.synchronize()
+        rdx, rdw = tail.rmsnorm_bwd(_np(dy), _np(h), _np(w), _np(rstd), None if d is None else _np(d))
+        rs = _np(rstd)[:, None]
+        n, t = _np(h) * rs, _np(dy) * _np(w)
+        size = rs * (np.abs(t) + np.abs(n) * np.abs(t * n).mean(axis=1, keepdims=True)) + (0 if d is None else np.abs(_np(d)))
+        assert np.all(np.abs(_np(dx) - rdx) <= r * np.abs(rdx) + (D / 32 + 16) * U * size)
+        assert np.all(np.abs(_np(dw) - rdw) <= (C + 16) * U * np.abs(_np(dy) * n).sum(axis=0))
+    assert int(err) == 0
+
+
 def test_backward_against_differences():
     """dL/dx of L = <y, dy> + <h, dh> in fp32 against central differences of the forward
     kernel along one direction.  Step 2^-6: the third-order term is about rstd^2 step^2 / 2, 6e-5,
