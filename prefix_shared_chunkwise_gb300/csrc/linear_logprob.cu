@@ -444,8 +444,16 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                         }
                         if (MODE == kDz) {              // the row's labels among these 64 columns
                             const int32_t lo = p.v0 + n0 + c;
-                            for (int32_t e = 0; e < ri.count; ++e) {
-                                const uint32_t j = static_cast<uint32_t>(__ldg(p.ent_y + ri.first + e) - lo);
+                            int32_t e = 0;
+                            for (int32_t len = ri.count > 8 ? ri.count : 0; len > 0;) {     // first label >= lo
+                                const int32_t half = len >> 1;
+                                if (__ldg(p.ent_y + ri.first + e + half) < lo) { e += half + 1; len -= half + 1; }
+                                else len = half;
+                            }
+                            for (; e < ri.count; ++e) {
+                                const int32_t y = __ldg(p.ent_y + ri.first + e);
+                                if (y >= lo + 64) break;
+                                const uint32_t j = static_cast<uint32_t>(y - lo);
                                 if (j < 64u)
                                     *reinterpret_cast<__nv_bfloat16 *>(dst + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) +
                                                                        (j & 7) * 2) =
@@ -536,8 +544,8 @@ struct SemParams {
     float *logp, *lse_out;
     const float2 *part;             // forward: [C][tiles]
     RowInfo *rows;
-    int32_t *ent_y;
-    float *ent_v;
+    int32_t *ent_y, *raw_y;
+    float *ent_v, *raw_v;
     int64_t C, S;
     int32_t V, D, tiles;
     float scale;
@@ -596,9 +604,12 @@ __global__ void __launch_bounds__(256) head_finish_kernel(SemParams p) {
 
 // ---- backward: per row, G and the distinct labels with a gradient of their own ----------
 
-// One warp a row.  A label that several positions of the row share gets the sum of their
-// gradients in list order; ent_v is the finished entry scale (sum g - G e^(z - lse)) in fp32,
-// written over the row's softmax term when its tile is formed.
+// One warp a row.  Its positions are taken 32 at a time: lanes with one label are added in
+// position order, and their sum to the label's entry in (raw_y, raw_v), found among the entries
+// so far; a row's positions mostly share few labels.  Entries whose gradients do not cancel are
+// then put in label order, so that a tile finds its own among many, and finished:
+// ent_v = scale (sum g - G e^(z - lse)) in fp32, written over the row's softmax term when the
+// tile is formed.  Rows with d distinct labels cost d^2 / 32 steps and d dot products.
 __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -607,44 +618,59 @@ __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
     const int32_t b = max(0, __ldg(p.row_ptr + c));
     const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
     float G = 0.f;
-    int32_t count = 0;
-    auto label = [&](int32_t q, float *g) {
-        const int32_t s = __ldg(p.row_sem + q);
-        if (s < 0 || s >= p.S) return -1;
-        const int32_t y = __ldg(p.target + s);
-        if (y < 0 || y >= p.V) return -1;
-        *g = __ldg(p.dlogp + s);
-        return y;
-    };
+    int32_t found = 0;
     for (int32_t base = b; base < e; base += 32) {
-        const int32_t q = base + lane;
+        int32_t y = -1;
         float g = 0.f;
-        const int32_t y = q < e ? label(q, &g) : -1;
-        if (y >= 0) G += g;
-        bool first = y >= 0;
-        float other;
-        for (int32_t t = b; t < q && first; ++t) first = label(t, &other) != y;
-        float sum = 0.f;
-        if (first) {
-            sum = g;
-            for (int32_t t = q + 1; t < e; ++t) {
-                float gt = 0.f;
-                if (label(t, &gt) == y) sum += gt;
+        if (base + lane < e) {
+            const int32_t s = __ldg(p.row_sem + base + lane);
+            if (s >= 0 && s < p.S) {
+                y = __ldg(p.target + s);
+                if (y < 0 || y >= p.V) y = -1;
+                else g = __ldg(p.dlogp + s);
             }
         }
-        first = first && sum != 0.f;
-        const uint32_t mask = __ballot_sync(0xffffffffu, first);
-        if (first) {
-            const int32_t at = b + count + __popc(mask & ((1u << lane) - 1u));
-            p.ent_y[at] = y;
-            p.ent_v[at] = sum;
+        G += g;
+        const uint32_t same = __match_any_sync(0xffffffffu, y);
+        const bool leads = y >= 0 && lane == __ffs(same) - 1;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const float gi = __shfl_sync(0xffffffffu, g, i);
+            if (same >> i & 1u) sum += gi;
         }
-        count += __popc(mask);
+        int32_t at = -1;
+        for (int32_t k = 0; k < found; ++k)
+            if (p.raw_y[b + k] == y) at = k;
+        const bool fresh = leads && at < 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, fresh);
+        if (fresh) {
+            const int32_t k = b + found + __popc(mask & ((1u << lane) - 1u));
+            p.raw_y[k] = y;
+            p.raw_v[k] = sum;
+        } else if (leads) {
+            p.raw_v[b + at] += sum;
+        }
+        found += __popc(mask);
+        __syncwarp();
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
-    const float lse = p.lse[c];
+    int32_t count = 0;
+    for (int32_t base = 0; base < found; base += 32) {
+        const int32_t k = base + lane;
+        const int32_t y = k < found ? p.raw_y[b + k] : -1;
+        const float v = k < found ? p.raw_v[b + k] : 0.f;
+        int32_t before = 0;
+        for (int32_t j = 0; j < found; ++j) before += p.raw_v[b + j] != 0.f && p.raw_y[b + j] < y;
+        if (v != 0.f) {
+            p.ent_y[b + before] = y;
+            p.ent_v[b + before] = v;
+        }
+        count += __popc(__ballot_sync(0xffffffffu, v != 0.f));
+    }
     __syncwarp();
+    const float lse = p.lse[c];
     for (int32_t i = 0; i < count; ++i) {
         const int32_t y = p.ent_y[b + i];
         const float z = p.scale * row_dot(p.x + c * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
@@ -834,7 +860,7 @@ SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
 struct BwdPlan {
     int32_t group, piece, n_pieces, n_dz, n_grad, splits, k_per;
     bool acc;                       // dX goes through fp32 sums
-    size_t rows, ent_y, ent_v, dz, dx, total;
+    size_t rows, ent_y, ent_v, raw_y, raw_v, dz, dx, total;
 };
 
 constexpr size_t kPieceBytes = size_t(512) << 20;     // dZ of one piece, when the caller sets no piece
@@ -859,7 +885,9 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     b.rows = 0;
     b.ent_y = align256(sizeof(RowInfo) * static_cast<size_t>(C));
     b.ent_v = b.ent_y + align256(4 * static_cast<size_t>(S));
-    b.dz = b.ent_v + align256(4 * static_cast<size_t>(S));
+    b.raw_y = b.ent_v + align256(4 * static_cast<size_t>(S));
+    b.raw_v = b.raw_y + align256(4 * static_cast<size_t>(S));
+    b.dz = b.raw_v + align256(4 * static_cast<size_t>(S));
     b.dx = b.dz + align256(2 * static_cast<size_t>(C) * b.piece);
     b.total = b.dx + (b.acc ? align256(4 * static_cast<size_t>(C) * D * b.splits) : 0);
     return b;
@@ -951,6 +979,8 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.rows = reinterpret_cast<RowInfo *>(ws + b.rows);
     s.ent_y = reinterpret_cast<int32_t *>(ws + b.ent_y);
     s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
+    s.raw_y = reinterpret_cast<int32_t *>(ws + b.raw_y);
+    s.raw_v = reinterpret_cast<float *>(ws + b.raw_v);
     const cudaError_t first = launch(head_rows_kernel, ceil_div(f.C, 8), 256, 0, 1, false, st, s);
     if (first != cudaSuccess) return cuda_fail(first, "linear log-prob backward launch");
 

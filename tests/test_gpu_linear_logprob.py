@@ -145,6 +145,29 @@ def test_many_positions_on_one_row():
         assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl))
 
 
+@pytest.mark.parametrize("labels", [1, 40, None])
+def test_thousands_of_positions_on_one_row(labels):
+    """3,000 positions of one row with one label, with 40 and with hundreds of distinct ones:
+    shared labels add up, distinct ones are found by the tiles they lie in."""
+    rng = np.random.default_rng(9)
+    x, w, _, _, _ = _case(3, 5003, 64, 1, 9)
+    S = 3100
+    sem_row = np.where(np.arange(S) < 3000, 1, 2).astype(np.int64)
+    target = rng.integers(0, 5003 if labels is None else labels, size=S)
+    target[::50] = -1
+    g = rng.standard_normal(S).astype(np.float32)
+    _check_bwd(x, w, sem_row, target, g, 1.0)
+
+
+def test_gradients_that_cancel():
+    """Positions of one label whose gradients cancel, and rows whose G is zero."""
+    x, w, _, _, _ = _case(4, 300, 64, 1, 10)
+    sem_row = np.array([0, 0, 1, 1, 2, 2, 2], np.int64)
+    target = np.array([5, 5, 7, 9, 250, 3, 3], np.int64)
+    g = np.array([1.5, -1.5, 2.0, -2.0, 1.0, 0.5, -0.5], np.float32)
+    _check_bwd(x, w, sem_row, target, g, 1.0)
+
+
 def test_peaked_rows():
     """Logits of spread 60: softmax rows close to one-hot, exponentials that underflow."""
     x, w, sem_row, target, g = _case(40, 700, 128, 100, 5, spread=60.0)
