@@ -353,21 +353,22 @@ def attn_bwd(plan: Plan, q, k, v, o, lse, d_o, *, scale=None, dq=None, dk=None, 
 def _stream_on(stream, t):
     """The raw handle of the given stream, or of the current one of `t`'s device (without
     building a Stream object: this runs in every call, some of which take a few us)."""
-    import torch
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"tensors are on {t.device}, expected a CUDA device")
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ready(name, t, shape, dtype, device):
-    """_need, and contiguous: what every buffer of the operators below has to be.  None is
-    an absent buffer; a shape or dtype of None is not compared."""
-    if t is None:
+    """_need, and contiguous: what every buffer that a caller gives to the operators below has
+    to be.  None is an absent buffer; a shape of None is not compared."""
+    if t is None or (t.dtype is dtype and t.device == device and t.is_contiguous()
+                     and (shape is None or t.shape == shape)):
         return
-    if ((shape is not None and t.shape != shape) or (dtype is not None and t.dtype is not dtype)
-            or t.device != device or not t.is_contiguous()):
-        _need(name, t, shape, dtype, None, device)
-        raise ValueError(f"{name} must be contiguous")
+    _need(name, t, shape, dtype, None, device)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None, rstd=None, stream=None):
@@ -375,42 +376,47 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None
     x, residual: [C, D] bf16 or fp32; weight: [D] fp32.  Returns (y, h, rstd [C] fp32); h is
     x itself where there is no residual.  mx8=True returns y as (values [C, D] float8_e4m3fn,
     scales [C, D/32] float8_e8m0fnu) instead; D is then a multiple of 32.  h may be given as
-    x or residual (in place)."""
+    x or residual, y as x (in place)."""
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [C, D]")
-    C, D = x.shape
-    dev, f32 = x.device, torch.float32
-    a = L.RmsnormFwdArgs()
-    a.C, a.D, a.dtype, a.eps = C, D, dtype_code(x.dtype), eps
-    _ready("x", x, (C, D), x.dtype, dev)
+    shape, dt, dev, f32 = x.shape, x.dtype, x.device, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"x has shape {tuple(shape)}, expected [C, D]")
+    C, D = shape
+    code = dtype_code(dt)
+    _ready("x", x, None, dt, dev)
     _ready("weight", weight, (D,), f32, dev)
-    _ready("residual", residual, (C, D), x.dtype, dev)
+    y_ptr = q_ptr = scale_ptr = res_ptr = h_ptr = None
     if mx8:
         if D % 32:
             raise ValueError("mx8 needs D a multiple of 32")
         if y is None:
-            y = (torch.empty((C, D), dtype=torch.float8_e4m3fn, device=dev),
+            y = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
                  torch.empty((C, D // 32), dtype=torch.float8_e8m0fnu, device=dev))
-        _ready("y values", y[0], (C, D), torch.float8_e4m3fn, dev)
-        _ready("y scales", y[1], (C, D // 32), torch.float8_e8m0fnu, dev)
-        a.y8, a.y8_scale = y[0].data_ptr(), y[1].data_ptr()
+        else:
+            _ready("y values", y[0], shape, torch.float8_e4m3fn, dev)
+            _ready("y scales", y[1], (C, D // 32), torch.float8_e8m0fnu, dev)
+        q_ptr, scale_ptr = y[0].data_ptr(), y[1].data_ptr()
     else:
         if y is None:
             y = torch.empty_like(x)
-        _ready("y", y, (C, D), x.dtype, dev)
-        a.y = y.data_ptr()
+        else:
+            _ready("y", y, shape, dt, dev)
+        y_ptr = y.data_ptr()
     if residual is not None:
+        _ready("residual", residual, shape, dt, dev)
         if h is None:
             h = torch.empty_like(x)
-        _ready("h", h, (C, D), x.dtype, dev)
-        a.residual, a.h = residual.data_ptr(), h.data_ptr()
+        else:
+            _ready("h", h, shape, dt, dev)
+        res_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
     else:
         h = x
     if rstd is None:
         rstd = torch.empty(C, dtype=f32, device=dev)
-    _ready("rstd", rstd, (C,), f32, dev)
-    a.x, a.weight, a.rstd = x.data_ptr(), weight.data_ptr(), rstd.data_ptr()
+    else:
+        _ready("rstd", rstd, (C,), f32, dev)
+    a = L.RmsnormFwdArgs(C, D, code, eps, x.data_ptr(), res_ptr, weight.data_ptr(), h_ptr, y_ptr, q_ptr, scale_ptr,
+                         rstd.data_ptr())
     L.check(L.lib().harts_rmsnorm_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_rmsnorm_fwd")
     return y, h, rstd
 
@@ -420,32 +426,42 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, error=No
     stream (or None).  Returns (dx [C, D] like h: the gradient of x and of the residual;
     dweight [D] fp32).  error: as linear_logprob_fwd's."""
     import torch
-    if h.dim() != 2:
-        raise ValueError(f"h has shape {tuple(h.shape)}, expected [C, D]")
-    C, D = h.shape
-    dev, f32 = h.device, torch.float32
-    if dx is None:
-        dx = torch.empty_like(h)
-    if dweight is None:
-        dweight = torch.empty(D, dtype=f32, device=dev)
-    for n, t in (("dy", dy), ("h", h), ("dh", dh), ("dx", dx)):
-        _ready(n, t, (C, D), h.dtype, dev)
+    shape, dt, dev, f32 = h.shape, h.dtype, h.device, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"h has shape {tuple(shape)}, expected [C, D]")
+    C, D = shape
+    code = dtype_code(dt)
+    _ready("h", h, None, dt, dev)
+    _ready("dy", dy, shape, dt, dev)
+    _ready("dh", dh, shape, dt, dev)
     _ready("weight", weight, (D,), f32, dev)
     _ready("rstd", rstd, (C,), f32, dev)
-    _ready("dweight", dweight, (D,), f32, dev)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _ready("dx", dx, shape, dt, dev)
+    if dweight is None:
+        dweight = torch.empty(D, dtype=f32, device=dev)
+    else:
+        _ready("dweight", dweight, (D,), f32, dev)
     _need("error", error, None, torch.int32, 4, dev)
-    a = L.RmsnormBwdArgs()
-    a.C, a.D, a.dtype = C, D, dtype_code(h.dtype)
-    nb = int(L.lib().harts_rmsnorm_bwd_workspace_bytes(C, D, a.dtype))
-    if workspace is None:
-        workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=dev)
-    _need("workspace", workspace, nbytes=nb, device=dev)
-    a.dy, a.h, a.dh = dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr()
-    a.weight, a.rstd, a.dx, a.dweight = weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr()
-    a.error = None if error is None else error.data_ptr()
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_rmsnorm_bwd(ctypes.byref(a), _stream_on(stream, h)), "harts_rmsnorm_bwd")
+    lib = L.lib()
+    nb = lib.harts_rmsnorm_bwd_workspace_bytes(C, D, code)
+    workspace, nb = _workspace(workspace, nb, dev)
+    a = L.RmsnormBwdArgs(C, D, code, dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr(),
+                         weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+                         None if error is None else error.data_ptr(), workspace.data_ptr(), nb)
+    L.check(lib.harts_rmsnorm_bwd(ctypes.byref(a), _stream_on(stream, h)), "harts_rmsnorm_bwd")
     return dx, dweight
+
+
+def _workspace(workspace, nb, dev):
+    """The caller's workspace, or one of `nb` bytes; and its size."""
+    if workspace is None:
+        import torch
+        return torch.empty(max(nb, 256), dtype=torch.uint8, device=dev), max(nb, 256)
+    _need("workspace", workspace, nbytes=nb, device=dev)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 class GradSet:
@@ -463,64 +479,48 @@ class GradSet:
         self._dev = grads[0].device if grads else torch.empty(0, device="cuda").device
         self._list = (L.GradTensor * max(len(grads), 1))()
         for i, (g, o) in enumerate(zip(grads, outs)):
-            _ready(f"gradient {i}", g, None, None, self._dev)
-            _ready(f"output {i}", o, tuple(g.shape), None, self._dev)
+            _ready(f"gradient {i}", g, None, g.dtype, self._dev)
+            _ready(f"output {i}", o, g.shape, o.dtype, self._dev)
             t = self._list[i]
             t.g, t.out, t.n = g.data_ptr(), o.data_ptr(), g.numel()
             t.dtype, t.out_dtype = dtype_code(g.dtype), dtype_code(o.dtype)
-        nb = int(L.lib().harts_grad_workspace_bytes(len(grads)))
-        self._ws = torch.empty(nb, dtype=torch.uint8, device=self._dev)
+        self._ws, self._nb = _workspace(None, L.lib().harts_grad_workspace_bytes(len(grads)), self._dev)
+
+    def _norm(self, norm):
+        import torch
+        if norm is None:
+            return torch.empty((), dtype=torch.float32, device=self._dev)
+        _need("norm", norm, None, torch.float32, 4, self._dev)
+        return norm
 
     def norm(self, *, norm=None, stream=None):
         """The global 2-norm, a 0-dim fp32 tensor."""
-        import torch
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self._dev)
-        _need("norm", norm, None, torch.float32, 4, self._dev)
-        L.check(L.lib().harts_grad_norm(self._list, len(self.grads), norm.data_ptr(), self._ws.data_ptr(),
-                                        self._ws.numel(), _stream_on(stream, norm)), "harts_grad_norm")
+        norm = self._norm(norm)
+        L.check(L.lib().harts_grad_norm(self._list, len(self.grads), norm.data_ptr(), self._ws.data_ptr(), self._nb,
+                                        _stream_on(stream, norm)), "harts_grad_norm")
         return norm
 
     def clip(self, max_norm, *, norm=None, stream=None):
         """outs = grads * min(1, max_norm / norm); returns the norm before clipping."""
-        import torch
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self._dev)
-        _need("norm", norm, None, torch.float32, 4, self._dev)
-        L.check(L.lib().harts_grad_clip(self._list, len(self.grads), float(max_norm), norm.data_ptr(),
-                                        self._ws.data_ptr(), self._ws.numel(), _stream_on(stream, norm)),
-                "harts_grad_clip")
+        norm = self._norm(norm)
+        L.check(L.lib().harts_grad_clip(self._list, len(self.grads), max_norm, norm.data_ptr(), self._ws.data_ptr(),
+                                        self._nb, _stream_on(stream, norm)), "harts_grad_clip")
         return norm
 
 
-def _head_args(x, weight, row_ptr, row_sem, target, scale, lse, logp, error):
+def _head_checks(x, weight, row_ptr, row_sem, target, error):
+    """(C, V, D, S) of the operands that forward and backward share."""
     import torch
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x and weight must be [C, D] and [V, D]")
-    (C, D), V, S, dev, i32 = x.shape, weight.shape[0], target.numel(), x.device, torch.int32
-    _ready("x", x, None, None, dev)
-    _ready("weight", weight, (V, D), x.dtype, dev)
+    (C, D), V, S, dt, dev, i32 = x.shape, weight.shape[0], target.numel(), x.dtype, x.device, torch.int32
+    _ready("x", x, None, dt, dev)
+    _ready("weight", weight, (V, D), dt, dev)
     _ready("row_ptr", row_ptr, (C + 1,), i32, dev)
     _ready("row_sem", row_sem, (S,), i32, dev)
     _ready("target", target, (S,), i32, dev)
-    _ready("lse", lse, (C,), torch.float32, dev)
-    _ready("logp", logp, (S,), torch.float32, dev)
     _need("error", error, None, i32, 4, dev)
-    a = L.LinearLogprobFwdArgs()
-    a.C, a.V, a.D, a.S, a.dtype, a.scale = C, V, D, S, dtype_code(x.dtype), scale
-    a.x, a.weight, a.row_ptr = x.data_ptr(), weight.data_ptr(), row_ptr.data_ptr()
-    a.row_sem, a.target, a.lse = row_sem.data_ptr(), target.data_ptr(), lse.data_ptr()
-    a.logp = None if logp is None else logp.data_ptr()
-    a.error = None if error is None else error.data_ptr()
-    return a
-
-
-def _head_workspace(workspace, nb, dev):
-    import torch
-    if workspace is None:
-        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
-    _need("workspace", workspace, nbytes=nb, device=dev)
-    return workspace
+    return C, V, D, S
 
 
 def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=None, logp=None, error=None,
@@ -530,15 +530,22 @@ def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=No
     A target outside 0 .. V-1 has no label (logp 0).  Returns (logp [S] fp32, lse [C] fp32).
     error: int32 device tensor that a bounded wait which ran out sets to 3."""
     import torch
-    dev = x.device
+    C, V, D, S = _head_checks(x, weight, row_ptr, row_sem, target, error)
+    dev, f32 = x.device, torch.float32
     if lse is None:
-        lse = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
+        lse = torch.empty(C, dtype=f32, device=dev)
+    else:
+        _ready("lse", lse, (C,), f32, dev)
     if logp is None:
-        logp = torch.empty(target.numel(), dtype=torch.float32, device=dev)
-    a = _head_args(x, weight, row_ptr, row_sem, target, scale, lse, logp, error)
-    workspace = _head_workspace(workspace, int(L.lib().harts_linear_logprob_fwd_workspace_bytes(a.C, a.V, a.D)), dev)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_linear_logprob_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_fwd")
+        logp = torch.empty(S, dtype=f32, device=dev)
+    else:
+        _ready("logp", logp, (S,), f32, dev)
+    lib = L.lib()
+    workspace, nb = _workspace(workspace, lib.harts_linear_logprob_fwd_workspace_bytes(C, V, D), dev)
+    a = L.LinearLogprobFwdArgs(C, V, D, dtype_code(x.dtype), scale, S, x.data_ptr(), weight.data_ptr(),
+                               row_ptr.data_ptr(), row_sem.data_ptr(), target.data_ptr(), lse.data_ptr(),
+                               logp.data_ptr(), None if error is None else error.data_ptr(), workspace.data_ptr(), nb)
+    L.check(lib.harts_linear_logprob_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_fwd")
     return logp, lse
 
 
@@ -548,20 +555,23 @@ def linear_logprob_bwd(x, weight, row_ptr, row_sem, target, lse, dlogp, *, scale
     and dL/dlogp [S] fp32.  piece: vocabulary entries whose logit gradients are held at a time
     (0: the library's choice)."""
     import torch
-    dev = x.device
-    a = L.LinearLogprobBwdArgs()
-    a.fwd = _head_args(x, weight, row_ptr, row_sem, target, scale, lse, None, error)
-    f = a.fwd
+    C, V, D, S = _head_checks(x, weight, row_ptr, row_sem, target, error)
+    dt, dev, f32 = x.dtype, x.device, torch.float32
+    _ready("lse", lse, (C,), f32, dev)
+    _ready("dlogp", dlogp, (S,), f32, dev)
     if dx is None:
         dx = torch.empty_like(x)
+    else:
+        _ready("dx", dx, x.shape, dt, dev)
     if dweight is None:
         dweight = torch.empty_like(weight)
-    _ready("dx", dx, tuple(x.shape), x.dtype, dev)
-    _ready("dweight", dweight, tuple(weight.shape), x.dtype, dev)
-    _ready("dlogp", dlogp, (f.S,), torch.float32, dev)
-    a.dlogp, a.dx, a.dweight, a.piece = dlogp.data_ptr(), dx.data_ptr(), dweight.data_ptr(), piece
-    nb = int(L.lib().harts_linear_logprob_bwd_workspace_bytes(f.C, f.V, f.D, f.S, max(piece, 0)))
-    workspace = _head_workspace(workspace, nb, dev)
-    a.fwd.workspace, a.fwd.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    L.check(L.lib().harts_linear_logprob_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_bwd")
+    else:
+        _ready("dweight", dweight, weight.shape, dt, dev)
+    lib = L.lib()
+    workspace, nb = _workspace(workspace, lib.harts_linear_logprob_bwd_workspace_bytes(C, V, D, S, max(piece, 0)), dev)
+    f = L.LinearLogprobFwdArgs(C, V, D, dtype_code(dt), scale, S, x.data_ptr(), weight.data_ptr(), row_ptr.data_ptr(),
+                               row_sem.data_ptr(), target.data_ptr(), lse.data_ptr(), None,
+                               None if error is None else error.data_ptr(), workspace.data_ptr(), nb)
+    a = L.LinearLogprobBwdArgs(f, dlogp.data_ptr(), dx.data_ptr(), dweight.data_ptr(), piece)
+    L.check(lib.harts_linear_logprob_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_bwd")
     return dx, dweight
