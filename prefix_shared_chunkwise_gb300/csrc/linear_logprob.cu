@@ -62,9 +62,10 @@ template <int MODE, int G> struct Ring {
 // One product D = op(A) op(B)^T cut into tiles and splits of its K range.
 struct Prod {
     CUtensorMap a, b, out;
+    CUtensorMap b_edge;             // B's last columns, where they do not fill a panel
     int32_t a_mn, b_mn;             // operand stored [K][rows] instead of [rows][K]
     int32_t a_panel;                // A is dZ, kept in panels of 64 columns
-    int32_t b_panel;                // B is seen as such panels: one copy for a block's columns
+    int32_t b_whole;                // B stored [K][columns]: columns in whole panels of 64, one copy for a tile of them
     int32_t a_rows;                 // rows of A's box when stored [rows][K]
     int32_t m_tiles, n_tiles, splits, n;
     uint32_t items, per_split;      // tiles times splits, tiles
@@ -224,6 +225,9 @@ template <int G> __device__ __forceinline__ void pair_load(void *dst, const void
                      " [%0], [%1, {%2, %3}], [%4];"
                      :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 template <int G> __device__ __forceinline__ void pair_load3(void *dst, const void *map, int x, int y, int z, uint32_t bar) {
     if constexpr (G == 1)
         asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -261,6 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         tc::fence_mbar_init();
         s_fail = 0;
     }
+    if (warp == 3 && lane < 2 * p.n_prod) {             // the first copies find their descriptors fetched
+        const Prod &q = p.prod[lane >> 1];
+        prefetch_map(lane & 1 ? &q.b : &q.a);
+    }
     if (warp == 2) { pair_alloc<G>(&s_tmem); tc::fence_before_sync(); }
     __syncthreads();
     if (G == 2) cluster_sync();                         // the other block's barriers exist
@@ -273,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         // thread for both could not keep up with the 512 cycles of a step's products.
         if (lane == 0) {
             const bool is_b = warp == 3;
-            if (MODE == kGrad) wait_previous();         // dZ is complete
+            // dZ is complete; the aligned copy of X, where there is one
+            if (MODE == kGrad || (!is_b && p.prod[0].a_panel)) wait_previous();
             uint32_t it = 0;                            // stages filled so far
             uint32_t s = 0, round = 0;                  // next stage, times the ring went round
             const uint32_t full0 = G == 2 ? leader_addr(&bars[B::full]) : tc::smem_addr(&bars[B::full]);
@@ -282,13 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
                 // what the loop needs is taken out of the parameters once a tile
                 const Prod &q = p.prod[t.which];
-                const CUtensorMap *map = is_b ? &q.b : &q.a;
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
                 const int32_t nb = q.n / G;             // columns that this block holds
                 const int32_t m0 = (t.mt * G + rank) * kTM, n0 = t.nt * q.n + rank * nb, y0 = q.b_y0;
                 enum { kRows, kPanelRows, kPanelCols, kBoxes };
-                const int how = is_b ? (q.b_mn ? (q.b_panel ? kPanelCols : kBoxes) : kRows)
+                const int how = is_b ? (q.b_mn ? (n0 + nb <= q.b_whole ? kPanelCols : kBoxes) : kRows)
                                      : (q.a_panel ? (q.a_mn ? kPanelCols : kPanelRows) : kRows);
+                const CUtensorMap *map = is_b ? (how == kBoxes ? &q.b_edge : &q.b) : &q.a;
                 const int32_t row = is_b ? y0 + n0 : m0, panel = (is_b ? n0 : m0) / 64, ky = is_b ? y0 : 0;
                 const uint32_t bytes = (is_b ? nb * 128u : q.a_mn ? kABytes : q.a_rows * 128u) * G;
                 for (int32_t k = k0; k < k1; ++k, ++it) {
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     let_next_start();
-    if (c >= p.C) return;
+    if (c >= p.C) { wait_previous(); return; }
     const int32_t b = max(0, __ldg(p.row_ptr + c));
     const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
     float G = 0.f;
@@ -679,6 +688,23 @@ __global__ void __launch_bounds__(256) head_rows_kernel(SemParams p) {
         if (lane == 0) p.ent_v[b + i] = v;
     }
     if (lane == 0) p.rows[c] = RowInfo{-p.scale * G, lse * kLog2e, count, b};
+    wait_previous();                // who waits for this kernel waits for the copy of X too
+}
+
+// X in panels of 64 columns, [panels][C][64], zero past D: for rows whose pitch is no multiple
+// of 128 bytes.  Each 128-byte row of a box then lies in one line instead of two; the rows are
+// read once a tile of the vocabulary, and misaligned lines bound the product (777 x 32003 x 1032
+// spent 120 K cycles where 66 K went by without copies).
+struct PadParams { const __nv_bfloat16 *x; __nv_bfloat16 *out; int64_t C; int32_t D; };
+__global__ void __launch_bounds__(256) head_pad_kernel(PadParams p) {
+    let_next_start();
+    const int64_t n = p.C * ((p.D + 63) / 64) * 8;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = (i >> 3) % p.C, panel = (i >> 3) / p.C, col = panel * 64 + (i & 7) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (col < p.D) v = __ldg(reinterpret_cast<const uint4 *>(p.x + row * p.D + col));
+        reinterpret_cast<uint4 *>(p.out)[i] = v;
+    }
 }
 
 // dX in bf16 from the splits' fp32 sums, in ascending order.
@@ -749,10 +775,22 @@ bool map_in(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
     return encode_bf16(m, base, 2, dims, strides, box);
 }
 
+// Whether X is copied into aligned panels first: its rows straddle lines, and there are enough
+// of them for several tiles to read each.
+bool pads_x(int64_t C, int32_t D) { return D % 64 != 0 && C > kTM; }
+size_t pad_bytes(int64_t C, int32_t D) {
+    return pads_x(C, D) ? align256(size_t(2) * static_cast<size_t>(C) * ((D + 63) / 64 * 64)) : 0;
+}
+cudaError_t launch_pad(const void *x, void *out, int64_t C, int32_t D, cudaStream_t st) {
+    const PadParams p{static_cast<const __nv_bfloat16 *>(x), static_cast<__nv_bfloat16 *>(out), C, D};
+    const int64_t blocks = std::min<int64_t>((C * ((D + 63) / 64) * 8 + 255) / 256, int64_t(sm_count()) * 8);
+    return launch(head_pad_kernel, blocks, 256, 0, 1, false, st, p);
+}
+
 // dZ in panels of 64 columns, [panels][C][64]: every box that is written, read as rows
-// (dX) or as columns (dW) is one contiguous run, or two.  Row-major, a box's 64 or 128
+// (dX) or as columns (dW) is one contiguous run, or two.  The aligned copy of X is kept so too.  Row-major, a box's 64 or 128
 // rows lie a whole piece (128 KB) apart each.
-bool map_dz(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_rows, int32_t box_panels) {
+bool map_panels(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_rows, int32_t box_panels) {
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(C), static_cast<cuuint64_t>((nv + 63) / 64)};
     const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(C) * 128};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_panels)};
@@ -760,9 +798,11 @@ bool map_dz(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_rows, i
 }
 
 // A row-major [rows][D] operand that is read as columns, in boxes of 64 rows x `cols` columns:
-// as panels of 64 columns where D holds whole ones, else in boxes of one panel.
-bool map_cols(CUtensorMap *m, const void *base, int64_t rows, int64_t D, int32_t cols) {
-    if (D % 64) return map_in(m, base, rows, D, D, 64);
+// the columns that fill panels of 64 as panels, so that one copy brings a tile's; the others
+// (the panel they lie in would reach past the last row's end) in boxes of 64 through `edge`.
+bool map_cols(CUtensorMap *m, CUtensorMap *edge, const void *base, int64_t rows, int64_t D, int32_t cols) {
+    if (D % 64 && !map_in(edge, base, rows, D, D, 64)) return false;
+    if (D < 64) return true;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D / 64)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, 128};
     const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(cols / 64)};
@@ -860,7 +900,7 @@ SemParams sem_params(const harts_linear_logprob_fwd_args *a) {
 struct BwdPlan {
     int32_t group, piece, n_pieces, n_dz, n_grad, splits, k_per;
     bool acc;                       // dX goes through fp32 sums
-    size_t rows, ent_y, ent_v, raw_y, raw_v, dz, dx, total;
+    size_t pad, rows, ent_y, ent_v, raw_y, raw_v, dz, dx, total;
 };
 
 constexpr size_t kPieceBytes = size_t(512) << 20;     // dZ of one piece, when the caller sets no piece
@@ -882,8 +922,9 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     b.k_per = ceil_div(kb, b.splits);
     b.splits = ceil_div(kb, b.k_per);
     b.acc = b.splits > 1 || b.n_pieces > 1;
-    b.rows = 0;
-    b.ent_y = align256(sizeof(RowInfo) * static_cast<size_t>(C));
+    b.pad = 0;
+    b.rows = pad_bytes(C, D);
+    b.ent_y = b.rows + align256(sizeof(RowInfo) * static_cast<size_t>(C));
     b.ent_v = b.ent_y + align256(4 * static_cast<size_t>(S));
     b.raw_y = b.ent_v + align256(4 * static_cast<size_t>(S));
     b.raw_v = b.raw_y + align256(4 * static_cast<size_t>(S));
@@ -902,7 +943,7 @@ extern "C" {
 
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D) {
     if (C < 0 || V < 1 || D < 1) return 0;
-    return std::max<size_t>(256, sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V).width));
+    return std::max<size_t>(256, pad_bytes(C, D) + sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V).width));
 }
 
 int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_stream_t stream) {
@@ -931,15 +972,19 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     p.n_prod = 1;
     p.error = a->error;
     p.c2 = logit_factor(a->scale, a->D);
-    p.part = static_cast<float2 *>(a->workspace);
-    if (!map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows) || !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n / G)) {
+    p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a->workspace) + pad_bytes(a->C, a->D));
+    const bool pad = pads_x(a->C, a->D);
+    q.a_panel = pad;
+    if (!(pad ? map_panels(&q.a, a->workspace, a->C, a->D, q.a_rows, 1) : map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows)) ||
+        !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n / G)) {
         set_error("tensor map");
         return HARTS_ECUDA;
     }
     SemParams s = sem_params(a);
     s.part = p.part;
     s.tiles = q.n_tiles;
-    cudaError_t e = launch_tiles<kFwd>(p, G, false, st);
+    cudaError_t e = pad ? launch_pad(a->x, a->workspace, a->C, a->D, st) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_tiles<kFwd>(p, G, pad, st);
     if (e == cudaSuccess) e = launch(head_finish_kernel, (a->S + a->C + 7) / 8, 256, 0, 1, true, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
     set_error("");
@@ -981,7 +1026,9 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
     s.raw_y = reinterpret_cast<int32_t *>(ws + b.raw_y);
     s.raw_v = reinterpret_cast<float *>(ws + b.raw_v);
-    const cudaError_t first = launch(head_rows_kernel, ceil_div(f.C, 8), 256, 0, 1, false, st, s);
+    const bool pad = pads_x(f.C, f.D);
+    cudaError_t first = pad ? launch_pad(f.x, ws + b.pad, f.C, f.D, st) : cudaSuccess;
+    if (first == cudaSuccess) first = launch(head_rows_kernel, ceil_div(f.C, 8), 256, 0, 1, pad, st, s);
     if (first != cudaSuccess) return cuda_fail(first, "linear log-prob backward launch");
 
     const int G = b.group;
@@ -991,24 +1038,28 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     std::memset(&pz, 0, sizeof(pz));
     std::memset(&pg, 0, sizeof(pg));
     Prod &z = pz.prod[0], &gx = pg.prod[0], &gw = pg.prod[1];
-    bool ok = map_in(&z.a, f.x, f.C, f.D, f.D, a_rows) && map_in(&z.b, f.weight, f.V, f.D, f.D, b.n_dz / G) &&
-              map_cols(&gx.b, f.weight, f.V, f.D, b.n_grad / G) && map_cols(&gw.b, f.x, f.C, f.D, b.n_grad / G) &&
+    void *xp = ws + b.pad;
+    bool ok = (pad ? map_panels(&z.a, xp, f.C, f.D, a_rows, 1) : map_in(&z.a, f.x, f.C, f.D, f.D, a_rows)) && map_in(&z.b, f.weight, f.V, f.D, f.D, b.n_dz / G) &&
+              map_cols(&gx.b, &gx.b_edge, f.weight, f.V, f.D, b.n_grad / G) &&
+              (pad ? map_panels(&gw.b, xp, f.C, f.D, 64, b.n_grad / G / 64)
+                   : map_cols(&gw.b, &gw.b_edge, f.x, f.C, f.D, b.n_grad / G)) &&
               map_out(&gw.out, a->dweight, 1, f.V, f.D, f.D, false) &&
               (b.acc ? map_out(&gx.out, acc, b.splits, f.C, f.D, f.D, true) : map_out(&gx.out, a->dx, 1, f.C, f.D, f.D, false));
     for (int32_t i = 0; ok && i < b.n_pieces; ++i) {
         const int32_t v0 = i * b.piece, nv = std::min(b.piece, f.V - v0);
-        ok = map_dz(&z.out, dz, f.C, nv, kTM, 1) && map_dz(&gx.a, dz, f.C, nv, a_rows, 1) && map_dz(&gw.a, dz, f.C, nv, 64, 2);
+        ok = map_panels(&z.out, dz, f.C, nv, kTM, 1) && map_panels(&gx.a, dz, f.C, nv, a_rows, 1) && map_panels(&gw.a, dz, f.C, nv, 64, 2);
         if (!ok) break;
         // logits of the piece, as dz
         z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
         z.k_blocks = z.k_per = ceil_div(f.D, kTK);
-        z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
+        z.a_panel = pad; z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
         pz.n_prod = 1; pz.error = f.error; pz.c2 = logit_factor(f.scale, f.D);
         pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0;
         cudaError_t e = launch_tiles<kDz>(pz, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
         // dX (first: its tiles are the longest) and dW
-        gx.b_mn = 1; gx.a_panel = gw.a_panel = 1; gx.b_panel = gw.b_panel = f.D % 64 == 0; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
+        gx.b_mn = 1; gx.a_panel = gw.a_panel = 1; gx.b_whole = f.D % 64 ? f.D / 64 * 64 : INT32_MAX;
+        gw.b_whole = pad ? INT32_MAX : gx.b_whole; gx.a_rows = a_rows; gx.m_tiles = mt; gx.n = b.n_grad; gx.n_tiles = ceil_div(f.D, b.n_grad);
         gx.k_blocks = ceil_div(nv, kTK); gx.k_per = b.k_per; gx.splits = ceil_div(gx.k_blocks, b.k_per);
         gx.b_y0 = v0; gx.out_y0 = 0; gx.rows = C; gx.cols = f.D; gx.out_f32 = b.acc; gx.out_add = i > 0;
         gw.a_mn = gw.b_mn = 1; gw.m_tiles = ceil_div(nv, kTM * G); gw.n = b.n_grad; gw.n_tiles = ceil_div(f.D, b.n_grad);
