@@ -21,8 +21,8 @@
 //
 // Tile kernel: persistent blocks, one per SM; warp 0 fills a ring of shared-memory stages
 // by TMA, warp 1 issues tcgen05.mma into one of two 256-column accumulators in TMEM, warps
-// 4-7 empty the other one (through shared memory and TMA stores of warps 8-9, where there is
-// output).  All waits are bounded.
+// 4-11 empty the other one, two warps for each 32 rows taking columns in turn (through shared
+// memory and TMA stores of warps 12-13, where there is output).  All waits are bounded.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -39,7 +39,7 @@ constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K st
 constexpr uint32_t kABytes = kTM * kTK * 2;
 constexpr uint32_t kSlotBytes = kTM * 128;           // 128 rows x 128 bytes of the output on their way out
 
-constexpr int kThreads = 320, kEpiWarp0 = 4, kStoreWarp0 = 8;
+constexpr int kThreads = 448, kEpiWarp0 = 4, kStoreWarp0 = 12;    // eight epilogue warps: two for each 32 TMEM lanes
 constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -53,10 +53,11 @@ template <int MODE, int G> struct Ring {
     static constexpr uint32_t stages = G == 2 ? (MODE == kFwd ? 7 : MODE == kDz ? 6 : 5) : (MODE == kGrad ? 3 : 4);
     static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
     static constexpr uint32_t smem = stages * stage_bytes + slots * kSlotBytes + 1024;
-    static_assert(smem <= 227 * 1024 - 512, "shared memory of an SM");
+    static_assert(smem + kTM * 8 <= 227 * 1024 - 512, "shared memory of an SM");
     // barriers
     static constexpr uint32_t full = 0, empty = stages, acc_full = 2 * stages, acc_empty = acc_full + 2, drain = acc_empty + 2,
-                              out_full = drain + 1, out_free = out_full + slots, count = out_free + slots;
+                              out_full = drain + 1, out_free = out_full + slots, pair_full = out_free + slots,
+                              pair_free = pair_full + 4, count = pair_free + 4;
 };
 
 // One product D = op(A) op(B)^T cut into tiles and splits of its K range.
@@ -253,14 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     __shared__ uint64_t bars[B::count];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
+    __shared__ float2 s_pair[MODE == kFwd ? kTM : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
     const uint32_t worker = blockIdx.x / G, workers = gridDim.x / G;
 
     if (tid == 0) {
         for (uint32_t i = 0; i < kStages; ++i) { tc::mbar_init(&bars[B::full + i], 2); tc::mbar_init(&bars[B::empty + i], 1); }
-        for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[B::acc_full + i], 1); tc::mbar_init(&bars[B::acc_empty + i], 4 * G); }
+        for (int i = 0; i < 2; ++i) { tc::mbar_init(&bars[B::acc_full + i], 1); tc::mbar_init(&bars[B::acc_empty + i], 8 * G); }
         for (int i = 0; i < static_cast<int>(kSlots); ++i) { tc::mbar_init(&bars[B::out_full + i], 4); tc::mbar_init(&bars[B::out_free + i], 1); }
+        for (int i = 0; i < 4; ++i) { tc::mbar_init(&bars[B::pair_full + i], 1); tc::mbar_init(&bars[B::pair_free + i], 1); }
         tc::mbar_init(&bars[B::drain], 1);
         tc::fence_mbar_init();
         s_fail = 0;
@@ -363,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             }
         }
     } else if (warp >= kEpiWarp0 && warp < kStoreWarp0) {
-        const int lg = warp - kEpiWarp0;                // TMEM lanes 32 lg .. 32 lg + 31
+        const int lg = (warp - kEpiWarp0) & 3;          // TMEM lanes 32 lg .. 32 lg + 31
+        const int half = (warp - kEpiWarp0) >> 2;       // of the two warps that share them
         const uint32_t lane_off = static_cast<uint32_t>(lg * 32) << 16;
         [[maybe_unused]] uint8_t *out = sm + kStages * kStageBytes + lg * 4096;   // this warp's rows of a slot
         const uint32_t released = G == 2 ? leader_addr(&bars[B::acc_empty]) : 0;
@@ -382,18 +386,23 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             if constexpr (MODE == kFwd) {
                 const int32_t nv = min(q.n, q.cols - n0);       // columns that are vocabulary entries
                 float m = -INFINITY, s = 0.f;
-                for (int c = 0; c < nv; c += 32) {
+                for (int c = half * 32; c < nv; c += 64) {
                     float v[32];
                     tc::tmem_ld32(acc + c, v);
+                    float m1 = -INFINITY;
                     if (c + 32 <= nv) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i] * p.c2);
+                        for (int i = 0; i < 32; i += 2) {
+                            m = fmaxf(m, v[i] * p.c2);
+                            m1 = fmaxf(m1, v[i + 1] * p.c2);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) if (c + i < nv) m = fmaxf(m, v[i] * p.c2);
                     }
+                    m = fmaxf(m, m1);
                 }
-                for (int c = 0; c < nv; c += 32) {
+                for (int c = half * 32; c < nv; c += 64) {
                     float v[32], s0 = 0.f, s1 = 0.f;
                     tc::tmem_ld32(acc + c, v);
                     if (c + 32 <= nv) {
@@ -413,12 +422,29 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 if (lane == 0) {
                     if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
                 }
-                if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
+                // the two warps' pairs become one: the second hands its over, the first joins them
+                float2 *pair = s_pair + lg * 32 + lane;
+                uint64_t *give = &bars[B::pair_full + lg], *back = &bars[B::pair_free + lg];
+                if (half == 1) {
+                    if (tile > 0 && !__all_sync(0xffffffffu, wait_or_fail(back, (tile - 1) & 1, &s_fail))) break;
+                    *pair = make_float2(m, s);
+                    __syncwarp();
+                    if (lane == 0) arrive(give);
+                } else {
+                    if (!__all_sync(0xffffffffu, wait_or_fail(give, tile & 1, &s_fail))) break;
+                    const float2 o = *pair;
+                    __syncwarp();
+                    if (lane == 0) arrive(back);
+                    const float n = fmaxf(m, o.x);
+                    if (nv > 32) { s = s * ex2(m - n) + o.y * ex2(o.x - n); m = n; }
+                    if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
+                }
             } else if constexpr (MODE != kFwd) {
                 RowInfo ri{0.f, 0.f, 0, 0};
                 if (MODE == kDz && row < q.rows) ri = p.rows[row];
                 const int step = q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
                 for (int c = 0; c < end; c += step, ++groups) {
+                    if ((groups & 1) != static_cast<uint32_t>(half)) continue;
                     const uint32_t slot = groups % kSlots, use = groups / kSlots;
                     uint8_t *dst = out + slot * kSlotBytes;
                     if (use > 0 && !__all_sync(0xffffffffu, wait_or_fail(&bars[B::out_free + slot], (use - 1) & 1, &s_fail))) {
@@ -470,15 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                             }
                         }
                     }
-                    if (c + step >= end) tc::fence_before_sync();       // the accumulator has been read
                     tc::fence_smem_to_async();
                     __syncwarp();
-                    if (lane == 0) {
-                        arrive(&bars[B::out_full + slot]);
-                        if (c + step >= end) {
-                            if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
-                        }
-                    }
+                    if (lane == 0) arrive(&bars[B::out_full + slot]);
+                }
+                tc::fence_before_sync();                // the accumulator has been read
+                __syncwarp();
+                if (lane == 0) {
+                    if (G == 2) arrive_at(released + buf * 8); else arrive(&bars[B::acc_empty + buf]);
                 }
             }
         }
