@@ -170,6 +170,11 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t phase, int 
     return false;
 }
 
+// The same for a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f) {
+    return __all_sync(0xffffffffu, wait_or_fail(bar, phase, f)) != 0;
+}
+
 // ---- pairs of blocks: the leader (rank 0) issues the products of both, 256 tile rows ----
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -198,22 +203,36 @@ template <int G> __device__ __forceinline__ void pair_dealloc(uint32_t t) {
     if constexpr (G == 1) tc::tmem_dealloc(t, 512);
     else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(t) : "memory");
 }
-template <int G> __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// One lane of the warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on;
+}
+// The whole warp comes through these two, with the same operands in every lane (which the
+// compiler then keeps in uniform registers, where the instruction wants them); the lane with
+// `on` set issues.
+template <int G> __device__ __forceinline__ void pair_mma(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     if constexpr (G == 1)
-        tc::mma_bf16(d, a, b, id, acc);
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on) : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on) : "memory");
 }
 // Arrive, in every block of the pair, on the barrier at this offset once all products issued
 // so far are done.
-template <int G> __device__ __forceinline__ void pair_commit(uint64_t *bar) {
+template <int G> __device__ __forceinline__ void pair_commit(uint32_t on, uint64_t *bar) {
     if constexpr (G == 1)
-        tc::mma_commit(bar);
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                     :: "r"(tc::smem_addr(bar)), "r"(on) : "memory");
     else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     :: "r"(tc::smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+                     :: "r"(tc::smem_addr(bar)), "h"(static_cast<uint16_t>(3)), "r"(on) : "memory");
 }
 // Copy into this block; the bytes count on `bar`, which in a pair lies in the leader.
 template <int G> __device__ __forceinline__ void pair_load(void *dst, const void *map, int x, int y, uint32_t bar) {
@@ -328,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const uint32_t on = elect_lane();
             uint32_t s = 0, round = 0, tile = 0;
             const uint32_t base = tc::smem_addr(sm);
             TileId t;
@@ -343,25 +363,25 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 const uint64_t da0 = q.a_mn ? tc::desc_sw128_mn(base, 8192) : tc::desc_sw128(base);
                 const uint64_t db0 = q.b_mn ? tc::desc_sw128_mn(base + kABytes, 8192) : tc::desc_sw128(base + kABytes);
                 const uint32_t ka = q.a_mn ? 128 : 2, kb = q.b_mn ? 128 : 2;
-                if (use > 0 && !wait_or_fail(&bars[B::acc_empty + buf], (use - 1) & 1, &s_fail)) { ok = false; break; }
+                if (use > 0 && !warp_wait(&bars[B::acc_empty + buf], (use - 1) & 1, &s_fail)) { ok = false; break; }
                 tc::fence_after_sync();
                 uint32_t acc = 0;
                 for (int32_t k = k0; k < k1; ++k) {
-                    if (!wait_or_fail(&bars[B::full + s], round & 1, &s_fail)) { ok = false; break; }
+                    if (!warp_wait(&bars[B::full + s], round & 1, &s_fail)) { ok = false; break; }
                     tc::fence_after_sync();
                     const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
                     for (uint32_t kk = 0; kk < kTK / 16; ++kk) {
-                        pair_mma<G>(d, da + kk * ka, db + kk * kb, id, acc);
+                        pair_mma<G>(on, d, da + kk * ka, db + kk * kb, id, acc);
                         acc = 1;
                     }
-                    pair_commit<G>(&bars[B::empty + s]);
+                    pair_commit<G>(on, &bars[B::empty + s]);
                     if (++s == kStages) { s = 0; ++round; }
                 }
-                if (ok) pair_commit<G>(&bars[B::acc_full + buf]);
+                if (ok) pair_commit<G>(on, &bars[B::acc_full + buf]);
             }
             if (failed(&s_fail)) {                      // let the products in flight end
-                pair_commit<G>(&bars[B::drain]);
+                pair_commit<G>(on, &bars[B::drain]);
                 tc::mbar_wait(&bars[B::drain], 0, 1000000000LL);
             }
         }
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         for (; ok && tile_at(p, tile, worker, workers, t); ++tile) {
             const Prod &q = p.prod[t.which];
             const uint32_t buf = tile & 1;
-            if (!__all_sync(0xffffffffu, wait_or_fail(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail))) break;
+            if (!warp_wait(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail)) break;
             tc::fence_after_sync();
             const uint32_t acc = tm + buf * kTN + lane_off;
             const int32_t n0 = t.nt * q.n, row = (t.mt * G + rank) * kTM + lg * 32 + lane;
@@ -426,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 float2 *pair = s_pair + lg * 32 + lane;
                 uint64_t *give = &bars[B::pair_full + lg], *back = &bars[B::pair_free + lg];
                 if (half == 1) {
-                    if (tile > 0 && !__all_sync(0xffffffffu, wait_or_fail(back, (tile - 1) & 1, &s_fail))) break;
+                    if (tile > 0 && !warp_wait(back, (tile - 1) & 1, &s_fail)) break;
                     *pair = make_float2(m, s);
                     __syncwarp();
                     if (lane == 0) arrive(give);
                 } else {
-                    if (!__all_sync(0xffffffffu, wait_or_fail(give, tile & 1, &s_fail))) break;
+                    if (!warp_wait(give, tile & 1, &s_fail)) break;
                     const float2 o = *pair;
                     __syncwarp();
                     if (lane == 0) arrive(back);
@@ -447,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                     if ((groups & 1) != static_cast<uint32_t>(half)) continue;
                     const uint32_t slot = groups % kSlots, use = groups / kSlots;
                     uint8_t *dst = out + slot * kSlotBytes;
-                    if (use > 0 && !__all_sync(0xffffffffu, wait_or_fail(&bars[B::out_free + slot], (use - 1) & 1, &s_fail))) {
+                    if (use > 0 && !warp_wait(&bars[B::out_free + slot], (use - 1) & 1, &s_fail)) {
                         ok = false;
                         break;
                     }
