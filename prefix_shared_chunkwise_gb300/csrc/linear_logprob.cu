@@ -234,31 +234,42 @@ template <int G> __device__ __forceinline__ void pair_commit(uint32_t on, uint64
                      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
                      :: "r"(tc::smem_addr(bar)), "h"(static_cast<uint16_t>(3)), "r"(on) : "memory");
 }
-// Copy into this block; the bytes count on `bar`, which in a pair lies in the leader.
-template <int G> __device__ __forceinline__ void pair_load(void *dst, const void *map, int x, int y, uint32_t bar) {
+// Copies into this block, issued by the lane with `on` set; the bytes count on `bar`, which in
+// a pair lies in the leader.
+template <int G> __device__ __forceinline__ void pair_load(uint32_t on, uint32_t dst, const void *map, int x, int y, uint32_t bar) {
     if constexpr (G == 1)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%2, %3}], [%4];"
-                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on) : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-                     " [%0], [%1, {%2, %3}], [%4];"
-                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                     " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on) : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-template <int G> __device__ __forceinline__ void pair_load3(void *dst, const void *map, int x, int y, int z, uint32_t bar) {
+template <int G>
+__device__ __forceinline__ void pair_load3(uint32_t on, uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
     if constexpr (G == 1)
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%2, %3, %4}], [%5];"
-                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+                     "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)
                      : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-                     " [%0], [%1, {%2, %3, %4}], [%5];"
-                     :: "r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+                     "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                     " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)
                      : "memory");
+}
+// The bytes that a phase of this block's barrier waits for, counted once.
+__device__ __forceinline__ void expect(uint32_t on, uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes), "r"(on) : "memory");
 }
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
@@ -299,52 +310,51 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     const uint32_t tm = s_tmem;
 
     if (warp == 0 || warp == 3) {
-        // One thread each for A and B: a copy takes its thread a few hundred cycles, and one
-        // thread for both could not keep up with the 512 cycles of a step's products.
-        if (lane == 0) {
-            const bool is_b = warp == 3;
-            // dZ is complete; the aligned copy of X, where there is one
-            if (MODE == kGrad || (!is_b && p.prod[0].a_panel)) wait_previous();
-            uint32_t it = 0;                            // stages filled so far
-            uint32_t s = 0, round = 0;                  // next stage, times the ring went round
-            const uint32_t full0 = G == 2 ? leader_addr(&bars[B::full]) : tc::smem_addr(&bars[B::full]);
-            TileId t;
-            bool ok = true;
-            for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
-                // what the loop needs is taken out of the parameters once a tile
-                const Prod &q = p.prod[t.which];
-                const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
-                const int32_t nb = q.n / G;             // columns that this block holds
-                const int32_t m0 = (t.mt * G + rank) * kTM, n0 = t.nt * q.n + rank * nb, y0 = q.b_y0;
-                enum { kRows, kPanelRows, kPanelCols, kBoxes };
-                const int how = is_b ? (q.b_mn ? (n0 + nb <= q.b_whole ? kPanelCols : kBoxes) : kRows)
-                                     : (q.a_panel ? (q.a_mn ? kPanelCols : kPanelRows) : kRows);
-                const CUtensorMap *map = is_b ? (how == kBoxes ? &q.b_edge : &q.b) : &q.a;
-                const int32_t row = is_b ? y0 + n0 : m0, panel = (is_b ? n0 : m0) / 64, ky = is_b ? y0 : 0;
-                const uint32_t bytes = (is_b ? nb * 128u : q.a_mn ? kABytes : q.a_rows * 128u) * G;
-                for (int32_t k = k0; k < k1; ++k, ++it) {
-                    if (round > 0 && !wait_or_fail(&bars[B::empty + s], (round - 1) & 1, &s_fail)) { ok = false; break; }
-                    const uint32_t full = full0 + s * 8;
-                    uint8_t *dst = sm + s * kStageBytes + (is_b ? kABytes : 0);
-                    if (rank == 0) tc::mbar_expect_tx(&bars[B::full + s], bytes);
-                    if (how == kRows) pair_load<G>(dst, map, k * kTK, row, full);
-                    else if (how == kPanelCols) pair_load3<G>(dst, map, 0, ky + k * kTK, panel, full);
-                    else if (how == kPanelRows) pair_load3<G>(dst, map, 0, row, k, full);
-                    else for (int j = 0; j < nb; j += 64) pair_load<G>(dst + j * 128, map, n0 + j, ky + k * kTK, full);
-                    if (++s == kStages) { s = 0; ++round; }
-                }
+        // One warp each for A and B, whole like the issuing one: a copy by a lone thread, or both
+        // operands' by one warp, could not keep up with the 512 cycles of a step's products.
+        const bool is_b = warp == 3;
+        const uint32_t on = elect_lane(), arms = rank == 0 ? on : 0;
+        // dZ is complete; the aligned copy of X, where there is one
+        if (MODE == kGrad || (!is_b && p.prod[0].a_panel)) wait_previous();
+        uint32_t it = 0;                                // stages filled so far
+        uint32_t s = 0, round = 0;                      // next stage, times the ring went round
+        const uint32_t own0 = tc::smem_addr(&bars[B::full]), full0 = G == 2 ? leader_addr(&bars[B::full]) : own0;
+        const uint32_t dst0 = tc::smem_addr(sm) + (is_b ? kABytes : 0);
+        TileId t;
+        bool ok = true;
+        for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
+            // what the loop needs is taken out of the parameters once a tile
+            const Prod &q = p.prod[t.which];
+            const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
+            const int32_t nb = q.n / G;                 // columns that this block holds
+            const int32_t m0 = (t.mt * G + rank) * kTM, n0 = t.nt * q.n + rank * nb, y0 = q.b_y0;
+            enum { kRows, kPanelRows, kPanelCols, kBoxes };
+            const int how = is_b ? (q.b_mn ? (n0 + nb <= q.b_whole ? kPanelCols : kBoxes) : kRows)
+                                 : (q.a_panel ? (q.a_mn ? kPanelCols : kPanelRows) : kRows);
+            const CUtensorMap *map = is_b ? (how == kBoxes ? &q.b_edge : &q.b) : &q.a;
+            const int32_t row = is_b ? y0 + n0 : m0, panel = (is_b ? n0 : m0) / 64, ky = is_b ? y0 : 0;
+            const uint32_t bytes = (is_b ? nb * 128u : q.a_mn ? kABytes : q.a_rows * 128u) * G;
+            for (int32_t k = k0; k < k1; ++k, ++it) {
+                if (round > 0 && !warp_wait(&bars[B::empty + s], (round - 1) & 1, &s_fail)) { ok = false; break; }
+                const uint32_t full = full0 + s * 8, dst = dst0 + s * kStageBytes;
+                expect(arms, own0 + s * 8, bytes);
+                if (how == kRows) pair_load<G>(on, dst, map, k * kTK, row, full);
+                else if (how == kPanelCols) pair_load3<G>(on, dst, map, 0, ky + k * kTK, panel, full);
+                else if (how == kPanelRows) pair_load3<G>(on, dst, map, 0, row, k, full);
+                else for (int j = 0; j < nb; j += 64) pair_load<G>(on, dst + j * 128, map, n0 + j, ky + k * kTK, full);
+                if (++s == kStages) { s = 0; ++round; }
             }
-            // Nothing may be in flight into this block's shared memory when it ends: the copies
-            // (after a failure the products may not have waited for them), then the stages'
-            // last release.  In a pair only the release says so for the second block; after a
-            // failure its wait runs out, long after the last copy.
-            for (uint32_t i = 0; i < kStages; ++i) {
-                if (it <= i) continue;
-                const uint32_t uses = (it - i + kStages - 1) / kStages;
-                if (rank == 0) tc::mbar_wait(&bars[B::full + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL);
-                if (!tc::mbar_wait(&bars[B::empty + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL))
-                    atomicExch(&s_fail, 1);
-            }
+        }
+        // Nothing may be in flight into this block's shared memory when it ends: the copies (after
+        // a failure the products may not have waited for them), then the stages' last release.
+        // In a pair only the release says so for the second block; after a failure its wait runs
+        // out, long after the last copy.
+        for (uint32_t i = 0; i < kStages; ++i) {
+            if (it <= i) continue;
+            const uint32_t uses = (it - i + kStages - 1) / kStages;
+            if (rank == 0) tc::mbar_wait(&bars[B::full + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL);
+            if (!tc::mbar_wait(&bars[B::empty + i], (uses - 1) & 1, failed(&s_fail) ? 100000000LL : 4000000000LL))
+                atomicExch(&s_fail, 1);
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -772,11 +782,15 @@ __global__ void __launch_bounds__(128) head_dx_kernel(DxParams p) {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// What a tile costs, in columns: a step of K takes a pair two cycles a column, but no less than
+// its copies and barriers do (430 - 450 cycles below 220 columns); 16 more for the tile's ends.
+int32_t tile_cost(int32_t n) { return std::max(n, 220) + 16; }
+
 // The forward's cut: blocks that share a tile (pairs: 256 rows) and the tile width, a multiple
-// of 16 columns a block.  The busiest worker's tiles cost their columns and 16 more for their
-// ends; a block alone, which reads its columns from L2 where a pair shares them, takes 1.12 as
-// long (4096 x 157184 x 2048: 1453 us alone, 1287 us in pairs), but wastes less where the rows
-// end early in a tile (300 rows: 174 us alone, 197 us in pairs).
+// of 16 columns a block, by the busiest worker's tiles.  A block alone, which reads its columns
+// from L2 where a pair shares them, takes 1.12 as long (4096 x 157184 x 2048: 1453 us alone,
+// 1287 us in pairs), but wastes less where the rows end early in a tile (300 rows: 174 us
+// alone, 197 us in pairs).
 struct Cut { int group; int32_t width; };
 Cut fwd_cut(int64_t C, int32_t V) {
     Cut best{1, kTN};
@@ -784,7 +798,7 @@ Cut fwd_cut(int64_t C, int32_t V) {
     for (int G = 1; G <= (C > kTM ? 2 : 1); ++G)
         for (int32_t n = kTN; n >= 64; n -= 16 * G) {
             const int64_t tiles = int64_t(ceil_div(C, kTM * G)) * ceil_div(V, n), workers = sm_count() / G;
-            const double cost = double((tiles + workers - 1) / workers) * (n + 16) * (G == 1 ? 1.12 : 1.0);
+            const double cost = double((tiles + workers - 1) / workers) * tile_cost(n) * (G == 1 ? 1.12 : 1.0);
             if (least == 0.0 || cost < least) { least = cost; best = Cut{G, n}; }
         }
     return best;
@@ -806,7 +820,7 @@ int32_t tile_width(int32_t m_tiles, int64_t cols, int32_t unit, int G) {
     const int64_t workers = sm_count() / G;
     for (int32_t n = kTN; n >= 64; n -= unit) {
         const int64_t tiles = int64_t(m_tiles) * ceil_div(cols, n);
-        const int64_t c = (tiles + workers - 1) / workers * (n + 16);
+        const int64_t c = (tiles + workers - 1) / workers * tile_cost(n);
         if (c < cost) { cost = c; best = n; }
     }
     return best;
