@@ -543,9 +543,9 @@ int harts_grad_clip(const harts_grad_tensor *tensors, int32_t count, float max_n
  *   dx[c] = scale sum_v dz[c][v] weight[v],   dweight[v] = scale sum_c dz[c][v] x[c],
  *   dz[c][v] = sum_{s -> c, target[s] = v} dlogp[s] - (sum_{s -> c} dlogp[s]) e^(z[c][v] - lse[c]).
  * The backward forms the logits again, one piece of the vocabulary at a time, and holds that
- * piece's dz in bf16 (each entry formed in fp32 and rounded once); all sums are fp32 and in a
- * fixed order.  x and weight must be finite: dweight sums over every row, also over rows
- * without positions (whose dx is zero).
+ * piece's dz in bf16 (each entry formed in fp32 and rounded once; up to 32 rows in two bf16
+ * terms); all sums are fp32 and in a fixed order.  x and weight must be finite: dweight sums
+ * over every row, also over rows without positions (whose dx is zero).
  */
 typedef struct {
     int64_t C;               /* compact rows, >= 0 */
@@ -567,7 +567,8 @@ typedef struct {
     size_t workspace_bytes;
 } harts_linear_logprob_fwd_args;
 
-/* Workspace of the forward: a (max, sum) pair per row and tile; 0 for invalid arguments. */
+/* Workspace of the forward: a (max, sum) pair per row and tile, and a copy of x where D is no
+ * multiple of 64; 0 for invalid arguments. */
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D);
 
 /* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, scale not finite),
