@@ -4,6 +4,7 @@ this module only marshals pointers and sizes."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 
@@ -361,6 +362,20 @@ def _stream_on(stream, t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _made_on_stream(call):
+    """Runs `call` under the stream it is given, if any, so that the buffers it makes belong to
+    that stream: a workspace made on the current one would be handed out again, as soon as the
+    call returns, to work that does not wait for this stream's kernels."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return run
+
+
 def _ready(name, t, shape, dtype, device):
     """_need, and contiguous: what every buffer that a caller gives to the operators below has
     to be.  None is an absent buffer; a shape of None is not compared."""
@@ -371,6 +386,7 @@ def _ready(name, t, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+@_made_on_stream
 def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None, rstd=None, stream=None):
     """harts_rmsnorm_fwd: h = x + residual, y = h / sqrt(mean h^2 + eps) * weight per row.
     x, residual: [C, D] bf16 or fp32; weight: [D] fp32.  Returns (y, h, rstd [C] fp32); h is
@@ -421,6 +437,7 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None
     return y, h, rstd
 
 
+@_made_on_stream
 def rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, error=None, workspace=None, stream=None):
     """harts_rmsnorm_bwd: from dL/dy, the forward's h and rstd, and dL/dh along the residual
     stream (or None).  Returns (dx [C, D] like h: the gradient of x and of the residual;
@@ -467,7 +484,9 @@ def _workspace(workspace, nb, dev):
 class GradSet:
     """harts_grad_norm / harts_grad_clip over a fixed list of gradient buffers (bf16 or fp32,
     contiguous, one device).  The buffers and their addresses are taken once; their values are
-    read at every call.  outs: where clip() writes (same shapes, bf16 or fp32), None: in place."""
+    read at every call.  outs: where clip() writes (same shapes, bf16 or fp32), None: in place.
+    A set outlives the graphs that its calls were captured into, and its calls run one after
+    another: they share its workspace."""
 
     def __init__(self, grads, outs=None):
         import torch
@@ -485,6 +504,15 @@ class GradSet:
             t.g, t.out, t.n = g.data_ptr(), o.data_ptr(), g.numel()
             t.dtype, t.out_dtype = dtype_code(g.dtype), dtype_code(o.dtype)
         self._ws, self._nb = _workspace(None, L.lib().harts_grad_workspace_bytes(len(grads)), self._dev)
+        self._made_on = _stream_on(None, self._ws)
+
+    def _call_stream(self, stream):
+        """The call's raw stream; the workspace is not handed out again before it is done there."""
+        raw = _stream_on(stream, self._ws)
+        if raw != self._made_on:
+            import torch
+            self._ws.record_stream(torch.cuda.current_stream(self._dev))
+        return raw
 
     def _norm(self, norm):
         import torch
@@ -493,18 +521,20 @@ class GradSet:
         _need("norm", norm, None, torch.float32, 4, self._dev)
         return norm
 
+    @_made_on_stream
     def norm(self, *, norm=None, stream=None):
         """The global 2-norm, a 0-dim fp32 tensor."""
         norm = self._norm(norm)
         L.check(L.lib().harts_grad_norm(self._list, len(self.grads), norm.data_ptr(), self._ws.data_ptr(), self._nb,
-                                        _stream_on(stream, norm)), "harts_grad_norm")
+                                        self._call_stream(stream)), "harts_grad_norm")
         return norm
 
+    @_made_on_stream
     def clip(self, max_norm, *, norm=None, stream=None):
         """outs = grads * min(1, max_norm / norm); returns the norm before clipping."""
         norm = self._norm(norm)
         L.check(L.lib().harts_grad_clip(self._list, len(self.grads), max_norm, norm.data_ptr(), self._ws.data_ptr(),
-                                        self._nb, _stream_on(stream, norm)), "harts_grad_clip")
+                                        self._nb, self._call_stream(stream)), "harts_grad_clip")
         return norm
 
 
@@ -523,6 +553,7 @@ def _head_checks(x, weight, row_ptr, row_sem, target, error):
     return C, V, D, S
 
 
+@_made_on_stream
 def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=None, logp=None, error=None,
                        workspace=None, stream=None):
     """harts_linear_logprob_fwd: log-probabilities of the semantic positions from hidden rows
@@ -549,6 +580,7 @@ def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=No
     return logp, lse
 
 
+@_made_on_stream
 def linear_logprob_bwd(x, weight, row_ptr, row_sem, target, lse, dlogp, *, scale=1.0, dx=None, dweight=None,
                        piece=0, error=None, workspace=None, stream=None):
     """harts_linear_logprob_bwd: returns (dx like x, dweight like weight) from the forward's lse

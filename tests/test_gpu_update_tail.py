@@ -59,3 +59,41 @@ def test_loss_goes_down():
     from update_tail import main
     losses = main(["--steps", "12", "--dim", "264", "--vocab", "777"])
     assert losses[-1] < losses[0] and all(np.isfinite(losses))
+
+
+def test_buffers_of_a_call_belong_to_its_stream():
+    """Calls on a second stream that is still busy, their workspaces dropped at once: what the
+    current stream then allocates and fills must not reach them.  Same kernels in the same order
+    of sums: results are equal to the bit."""
+    from prefix_shared_chunkwise_gb300.api import GradSet, linear_logprob_bwd, linear_logprob_fwd, rmsnorm_bwd, rmsnorm_fwd
+    gen = torch.Generator().manual_seed(5)
+    rnd = lambda *shape: torch.randn(*shape, generator=gen)
+    C, V, D = 200, 1500, 136
+    x, w = rnd(C, D).bfloat16().cuda(), (0.1 * rnd(V, D)).bfloat16().cuda()
+    ptr = torch.arange(C + 1, dtype=torch.int32).cuda()
+    sem = torch.randperm(C, generator=gen).int().cuda()
+    target, dlogp = torch.randint(0, V, (C,), generator=gen).int().cuda(), rnd(C).cuda()
+    weight, dy = rnd(D).cuda(), rnd(C, D).bfloat16().cuda()
+    grads = [rnd(70001).cuda(), rnd(513).bfloat16().cuda()]
+
+    def calls(stream):
+        clipped = [torch.zeros_like(g) for g in grads]
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+        logp, lse = linear_logprob_fwd(x, w, ptr, sem, target, stream=stream)
+        dx, dw = linear_logprob_bwd(x, w, ptr, sem, target, lse, dlogp, stream=stream)
+        y, h, rstd = rmsnorm_fwd(x, weight, dy, stream=stream)
+        dn, dweight = rmsnorm_bwd(dy, h, weight, rstd, stream=stream)
+        norm = GradSet(grads, clipped).clip(0.5, stream=stream)
+        junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda")
+                for n in (256, 4096, 1 << 16, 1 << 18, 1 << 20, 1 << 22) for _ in range(8)]
+        torch.cuda.synchronize()
+        del junk
+        return [logp, lse, dx, dw, y, h, rstd, dn, dweight, norm, *clipped]
+
+    here = calls(None)
+    there = calls(torch.cuda.Stream())
+    for a, b in zip(here, there):
+        assert torch.equal(a, b)
