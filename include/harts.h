@@ -567,7 +567,7 @@ typedef struct {
     size_t workspace_bytes;
 } harts_linear_logprob_fwd_args;
 
-/* Workspace of the forward: a (max, sum) pair per row and tile, and a copy of x where D is no
+/* Workspace of the forward: a (max, sum) pair and the maximum's column per row and tile, and a copy of x where D is no
  * multiple of 64; 0 for invalid arguments. */
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D);
 

@@ -9,21 +9,25 @@
 // vocabulary carry no log-probability and no gradient.
 //
 // Forward: one product X W^T whose 128 x N tiles never leave the SM.  A tile's accumulators
-// are reduced in place to one (max, sum of exponentials) per row, 8 bytes instead of N
-// logits; a small kernel joins a row's pairs, and the positions' own logits are formed by
-// dot products of the rows they name (S of them, against C V in the product).
+// are reduced in place to one (max, sum of exponentials) per row and the maximum's column, 9
+// bytes instead of N logits; a small kernel joins a row's pairs, and the positions' own logits,
+// like each row's largest, are formed by dot products (S + C of them, against C V in the product).
 // Backward, over pieces of the vocabulary: the product again, its epilogue turning logits
 // into scale * dz in bf16; then dX += dZ W and dW = dZ^T X in one launch, with the same tiles.
 // dz is rounded to bf16 because the tensor cores take bf16 operands next to bf16 W and X;
-// every entry, labels' included, is formed in fp32 and rounded once (up to 32 rows it is kept in
-// two bf16 terms).  Sums are fp32.  dX of
-// several pieces or of a split vocabulary is summed in fp32 (one buffer per split, added to
-// in piece order), so results do not depend on timing.
+// every entry, labels' included, is formed in fp32 and rounded once (up to 32 rows it is kept
+// in two bf16 terms).  Sums are fp32.  dX of several pieces or of a split vocabulary is summed
+// in fp32 (one buffer per split, added to in piece order), so results do not depend on timing.
 //
-// Tile kernel: persistent blocks, one per SM; warp 0 fills a ring of shared-memory stages
-// by TMA, warp 1 issues tcgen05.mma into one of two 256-column accumulators in TMEM, warps
-// 4-11 empty the other one, two warps for each 32 rows taking columns in turn (through shared
-// memory and TMA stores of warps 12-13, where there is output).  All waits are bounded.
+// Tile kernel: persistent blocks, one per SM, in pairs where there are rows for it; warps 0 and
+// 3 fill a ring of shared-memory stages with A and B by TMA, warp 1 issues tcgen05.mma into one
+// of two 256-column accumulators in TMEM, warps 4-11 empty the other one, two warps for each 32
+// rows taking columns in turn (through shared memory and TMA stores of warps 12-13, where there
+// is output).  All waits are bounded.
+//
+// Many rows are bound by the tensor cores, under the power limit: 4,096 x 157,184 x 2,048 takes
+// 1.48 ms forward (1.78 PFLOP/s) and 4.6 ms backward (1.72), at 92 - 95 % of the tensor pipe's
+// cycles.  Few rows are bound by reading W: 1 row takes 107 us (6.0 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -55,7 +59,7 @@ template <int MODE, int G> struct Ring {
     static constexpr uint32_t stages = G == 2 ? (MODE == kFwd ? 7 : MODE == kDz ? 6 : 5) : (MODE == kGrad ? 3 : 4);
     static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
     static constexpr uint32_t smem = stages * stage_bytes + slots * kSlotBytes + 1024;
-    static_assert(smem + kTM * 8 <= 227 * 1024 - 512, "shared memory of an SM");
+    static_assert(smem + kTM * 9 <= 227 * 1024 - 384, "shared memory of an SM");
     // barriers
     static constexpr uint32_t full = 0, empty = stages, acc_full = 2 * stages, acc_empty = acc_full + 2, drain = acc_empty + 2,
                               out_full = drain + 1, out_free = out_full + slots, pair_full = out_free + slots,
@@ -87,7 +91,8 @@ struct Params {
     uint32_t each0, over, extra;    // see tile_at: tiles of the first product per worker, and what is left
     int32_t *error;
     float c2;                       // scale * log2 e (logit_factor)
-    float2 *part;                   // forward: [C][n_tiles]
+    float2 *part;                   // forward: [C][n_tiles] accumulator of the largest logit; the sum
+    uint8_t *top;                   // forward: [C][n_tiles] column of the tile's maximum
     const RowInfo *rows;            // dz: per compact row
     const int32_t *ent_y;
     const float *ent_v;
@@ -143,6 +148,17 @@ __device__ __forceinline__ bool tile_at(const Params &p, uint32_t n, uint32_t w,
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
@@ -299,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     __shared__ float2 s_pair[MODE == kFwd ? kTM : 1];
+    __shared__ uint8_t s_top[MODE == kFwd ? kTM : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
     const uint32_t worker = blockIdx.x / G, workers = gridDim.x / G;
@@ -430,36 +447,48 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             const int32_t n0 = t.nt * q.n, row = (t.mt * G + rank) * kTM + lg * 32 + lane;
             if constexpr (MODE == kFwd) {
                 const int32_t nv = min(q.n, q.cols - n0);       // columns that are vocabulary entries
-                float m = -INFINITY, s = 0.f;
+                // the accumulators that make the largest logit are the largest, or the smallest
+                float mv = p.c2 < 0.f ? INFINITY : -INFINITY;
                 for (int c = half * 32; c < nv; c += 64) {
                     float v[32];
                     tc::tmem_ld32(acc + c, v);
-                    float m1 = -INFINITY;
-                    if (c + 32 <= nv) {
+                    if (c + 32 > nv) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            m = fmaxf(m, v[i] * p.c2);
-                            m1 = fmaxf(m1, v[i + 1] * p.c2);
-                        }
+                        for (int i = 0; i < 32; ++i) if (c + i >= nv) v[i] = mv;
+                    }
+                    float m1 = mv;
+                    if (p.c2 < 0.f) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) { mv = min3(mv, v[i], v[i + 1]); m1 = min3(m1, v[i + 2], v[i + 3]); }
+                        mv = fminf(mv, m1);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) if (c + i < nv) m = fmaxf(m, v[i] * p.c2);
+                        for (int i = 0; i < 32; i += 4) { mv = max3(mv, v[i], v[i + 1]); m1 = max3(m1, v[i + 2], v[i + 3]); }
+                        mv = fmaxf(mv, m1);
                     }
-                    m = fmaxf(m, m1);
                 }
+                float m = half * 32 < nv ? mv * p.c2 : -INFINITY, s = 0.f;
+                int32_t top = 0;                                // column of the maximum
                 for (int c = half * 32; c < nv; c += 64) {
                     float v[32], s0 = 0.f, s1 = 0.f;
                     tc::tmem_ld32(acc + c, v);
+                    int32_t at = -1;
                     if (c + 32 <= nv) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             s0 += ex2(fmaf(v[i], p.c2, -m));
                             s1 += ex2(fmaf(v[i + 1], p.c2, -m));
                         }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) at = v[i] == mv ? i : at;
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) if (c + i < nv) s0 += ex2(fmaf(v[i], p.c2, -m));
+                        for (int i = 0; i < 32; ++i) if (c + i < nv) {
+                            s0 += ex2(fmaf(v[i], p.c2, -m));
+                            at = v[i] == mv ? i : at;
+                        }
                     }
+                    if (at >= 0) top = c + at;
                     s += s0 + s1;
                 }
                 tc::fence_before_sync();
@@ -472,17 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 uint64_t *give = &bars[B::pair_full + lg], *back = &bars[B::pair_free + lg];
                 if (half == 1) {
                     if (tile > 0 && !warp_wait(back, (tile - 1) & 1, &s_fail)) break;
-                    *pair = make_float2(m, s);
+                    *pair = make_float2(mv, s);
+                    s_top[lg * 32 + lane] = static_cast<uint8_t>(top);
                     __syncwarp();
                     if (lane == 0) arrive(give);
                 } else {
                     if (!warp_wait(give, tile & 1, &s_fail)) break;
                     const float2 o = *pair;
+                    const int32_t o_top = s_top[lg * 32 + lane];
                     __syncwarp();
                     if (lane == 0) arrive(back);
-                    const float n = fmaxf(m, o.x);
-                    if (nv > 32) { s = s * ex2(m - n) + o.y * ex2(o.x - n); m = n; }
-                    if (row < q.rows) p.part[static_cast<int64_t>(row) * q.n_tiles + t.nt] = make_float2(m, s);
+                    if (nv > 32) {
+                        const float om = o.x * p.c2, n = fmaxf(m, om);
+                        s = s * ex2(m - n) + o.y * ex2(om - n);
+                        if (om > m) { mv = o.x; top = o_top; }
+                    }
+                    if (row < q.rows) {
+                        const int64_t at = static_cast<int64_t>(row) * q.n_tiles + t.nt;
+                        p.part[at] = make_float2(mv, s);
+                        p.top[at] = static_cast<uint8_t>(top);
+                    }
                 }
             } else if constexpr (MODE != kFwd) {
                 RowInfo ri{0.f, 0.f, 0, 0};
@@ -602,20 +640,32 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
 
 // ---- forward: joining the tiles, and the positions' own logits --------------------------
 
-// x_c . w_y over D (a multiple of 8), one warp; every lane returns it.
+__device__ __forceinline__ void add_products(const uint4 &a, const uint4 &b, float &s0, float &s1) {
+    const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a), *pb = reinterpret_cast<const __nv_bfloat162 *>(&b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 u = __bfloat1622float2(pa[k]), v = __bfloat1622float2(pb[k]);
+        s0 = fmaf(u.x, v.x, s0);
+        s1 = fmaf(u.y, v.y, s1);
+    }
+}
+
+// x_c . w_y over D (a multiple of 8), one warp; every lane returns it.  Four loads of either row
+// at a time: a single one waits for memory as long.
 __device__ __forceinline__ float row_dot(const __nv_bfloat16 *x, const __nv_bfloat16 *w, int32_t D) {
     const int lane = threadIdx.x & 31;
+    constexpr int kAtOnce = 4;
+    const uint4 *px = reinterpret_cast<const uint4 *>(x), *pw = reinterpret_cast<const uint4 *>(w);
     float s0 = 0.f, s1 = 0.f;
-    for (int32_t i = lane * 8; i < D; i += 256) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + i)), b = __ldg(reinterpret_cast<const uint4 *>(w + i));
-        const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a), *pb = reinterpret_cast<const __nv_bfloat162 *>(&b);
+    int32_t i = lane;
+    for (; i + 32 * (kAtOnce - 1) < D / 8; i += 32 * kAtOnce) {
+        uint4 a[kAtOnce], b[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 u = __bfloat1622float2(pa[k]), v = __bfloat1622float2(pb[k]);
-            s0 = fmaf(u.x, v.x, s0);
-            s1 = fmaf(u.y, v.y, s1);
-        }
+        for (int j = 0; j < kAtOnce; ++j) { a[j] = __ldg(px + i + j * 32); b[j] = __ldg(pw + i + j * 32); }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) add_products(a[j], b[j], s0, s1);
     }
+    for (; i < D / 8; i += 32) add_products(__ldg(px + i), __ldg(pw + i), s0, s1);
     float s = s0 + s1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -628,63 +678,120 @@ struct SemParams {
     const float *lse, *dlogp;
     float *logp, *lse_out;
     const float2 *part;             // forward: [C][tiles]
+    const uint8_t *top;
     RowInfo *rows;
     int32_t *ent_y, *raw_y;
     float *ent_v, *raw_v;
     int64_t C, S;
-    int32_t V, D, tiles;
-    float scale;
+    int32_t V, D, tiles, width;     // tiles of `width` columns
+    float scale, c2;                // c2: as the tiles'
 };
 
-// lse of row c from its (max, sum) pairs, which are in units of log 2; one warp, every lane
-// returns it.
-__device__ __forceinline__ float row_lse(const float2 *part, int64_t c, int32_t tiles) {
-    const float2 *q = part + c * tiles;
-    float m = -INFINITY, s = 0.f;
-    for (int32_t i = threadIdx.x & 31; i < tiles; i += 32) {
-        const float2 t = q[i];
-        const float n = fmaxf(m, t.x);
-        s = (m == -INFINITY ? 0.f : s * exp2f(m - n)) + (n == -INFINITY ? t.y : t.y * exp2f(t.x - n));
-        m = n;
+// The positions' own logits, one warp each (the q-th of row_sem; its row by binary search in
+// row_ptr), into logp.  They need only the inputs and are formed while the tiles are; the first
+// block stays until the tiles are done, so that whoever waits for this kernel finds both.
+__global__ void __launch_bounds__(256) head_labels_kernel(SemParams p) {
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    let_next_start();
+    if (q < p.S) {
+        int64_t lo = 0, hi = p.C;                   // last row with row_ptr <= q
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (__ldg(p.row_ptr + mid) <= q) lo = mid; else hi = mid;
+        }
+        const int32_t s = __ldg(p.row_sem + q);
+        if (s >= 0 && s < p.S) {
+            const int32_t y = __ldg(p.target + s);
+            float z = 0.f;
+            if (y >= 0 && y < p.V) z = p.scale * row_dot(p.x + lo * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
+            if ((threadIdx.x & 31) == 0) p.logp[s] = z;
+        }
+    }
+    if (blockIdx.x == 0) wait_previous();
+}
+
+// Joins a row's pairs (accumulator of the largest logit, sum of 2^(c2 v - c2 max)) to its lse, and takes it from
+// the logits of the row's positions; one block a row.  The row's largest logit is formed again by
+// a dot product: where one entry has most of the probability, as sampled tokens mostly do, its
+// error is lse's, and what the tensor cores truncate from a sum whose terms are mostly of one
+// sign is more than logit_factor gives back.  (1 x 157,184 x 2,048, lse 19.86: off by 1.0e-6 of
+// it, 1.3e-7 with the dot product; a label's logp of -0.0031 by 2.0e-5, 1.6e-7.  4,096 rows: lse
+// and logp off by 1.9e-7 in relative L2 without it, 5.4e-8 with.  It costs 1 us of 106 for that
+// row, 2.5 us of 53 for 777 rows x 32,003 x 1,032, 0.5 % for the 4,096.)
+constexpr int kRowThreads = 128;
+__global__ void __launch_bounds__(kRowThreads) head_finish_kernel(SemParams p) {
+    __shared__ float2 s_max[kRowThreads / 32], s_sum[kRowThreads / 32];
+    const int64_t c = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t b = max(0, __ldg(p.row_ptr + c));
+    const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
+    const float2 *pairs = p.part + c * p.tiles;
+    // this thread's first position, its label and its logit are fetched ahead of what they wait for
+    int32_t s = b + tid < e ? __ldg(p.row_sem + b + tid) : -1;
+    int32_t y = s >= 0 && s < p.S ? __ldg(p.target + s) : -1;
+    wait_previous();
+    float label_z = y >= 0 && y < p.V ? p.logp[s] : 0.f;
+    float m = -INFINITY;
+    int32_t tile = 0;
+#pragma unroll 4
+    for (int32_t i = tid; i < p.tiles; i += kRowThreads) {
+        const float t = pairs[i].x * p.c2;
+        if (t > m) { m = t; tile = i; }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float n = fmaxf(m, m2);
-        const float a = m == -INFINITY ? s : s * exp2f(m - n), b = m2 == -INFINITY ? s2 : s2 * exp2f(m2 - n);
-        s = a + b;
-        m = n;
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+        const int32_t t2 = __shfl_xor_sync(0xffffffffu, tile, o);
+        if (m2 > m || (m2 == m && t2 < tile)) { m = m2; tile = t2; }
     }
-    return (m + log2f(s)) * kLn2;
-}
-
-// One warp a position (the q-th of row_sem; its row by binary search in row_ptr), then one
-// warp a row.  A position's own logit needs only the inputs: it is formed while the tiles are
-// still being computed.  Every position joins its row's pairs itself -- a few kilobytes, as
-// much as its dot product reads -- so that no position waits for another warp.
-__global__ void __launch_bounds__(256) head_finish_kernel(SemParams p) {
-    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (q >= p.S + p.C) return;
-    if (q >= p.S) {
-        wait_previous();
-        const float lse = row_lse(p.part, q - p.S, p.tiles);
-        if (lane == 0) p.lse_out[q - p.S] = lse;
-        return;
+    if (lane == 0) s_max[warp] = make_float2(m, __int_as_float(tile));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i) {
+        const float2 t = s_max[i];
+        const int32_t t2 = __float_as_int(t.y);
+        if (t.x > m || (t.x == m && t2 < tile)) { m = t.x; tile = t2; }
     }
-    int64_t lo = 0, hi = p.C;                       // last row with row_ptr <= q
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(p.row_ptr + mid) <= q) lo = mid; else hi = mid;
+    const int32_t top = min(tile * p.width + p.top[c * p.tiles + tile], p.V - 1);
+    const float own = ex2(fmaf(pairs[tile].x, p.c2, -m));           // its term of the tile's sum: 1 but for m's rounding
+    float sum = 0.f, d0 = 0.f, d1 = 0.f;
+#pragma unroll 4
+    for (int32_t i = tid; i < p.tiles; i += kRowThreads) {
+        const float2 t = pairs[i];
+        sum = fmaf(t.y, ex2(t.x * p.c2 - m), sum);
     }
-    const int32_t s = __ldg(p.row_sem + q);
-    const int32_t y = s >= 0 && s < p.S ? __ldg(p.target + s) : -1;
-    const bool labelled = y >= 0 && y < p.V;
-    float r = 0.f;
-    if (labelled) r = p.scale * row_dot(p.x + lo * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
-    wait_previous();
-    if (labelled) r -= row_lse(p.part, lo, p.tiles);
-    if (lane == 0 && s >= 0 && s < p.S) p.logp[s] = r;
+    const uint4 *px = reinterpret_cast<const uint4 *>(p.x + c * p.D);
+    const uint4 *pw = reinterpret_cast<const uint4 *>(p.w + static_cast<int64_t>(top) * p.D);
+#pragma unroll 2
+    for (int32_t i = tid; i < p.D / 8; i += kRowThreads) add_products(__ldg(px + i), __ldg(pw + i), d0, d1);
+    d0 += d1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+    }
+    if (lane == 0) s_sum[warp] = make_float2(sum, d0);
+    __syncthreads();
+    sum = d0 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i) { sum += s_sum[i].x; d0 += s_sum[i].y; }
+    // lse = z + rest, z the largest logit
+    float z = p.scale * d0, rest;
+    const float off = m - z * kLog2e;
+    if (fabsf(off) < 64.f) {
+        rest = log1pf(fmaxf(sum - own, 0.f) * exp2f(off));
+    } else {                                            // logits that are not finite, or beyond fp32's digits
+        z = m * kLn2;
+        rest = log2f(sum) * kLn2;
+    }
+    if (tid == 0) p.lse_out[c] = z + rest;
+    for (int32_t i = b + tid; i < e;) {
+        if (y >= 0 && y < p.V) p.logp[s] = ((y == top ? z : label_z) - z) - rest;
+        if ((i += kRowThreads) >= e) break;
+        s = __ldg(p.row_sem + i);
+        y = s >= 0 && s < p.S ? __ldg(p.target + s) : -1;
+        label_z = y >= 0 && y < p.V ? p.logp[s] : 0.f;
+    }
 }
 
 // X in panels of 64 columns, [panels][rows][64], zero past D, where its rows straddle lines:
@@ -1044,14 +1151,21 @@ extern "C" {
 
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D) {
     if (C < 0 || V < 1 || D < 1) return 0;
-    return std::max<size_t>(256, (pads_x(C, D) ? pad_bytes(C, D) : 0) + sizeof(float2) * static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V, D).width));
+    const size_t pairs = static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V, D).width);
+    return std::max<size_t>(256, (pads_x(C, D) ? pad_bytes(C, D) : 0) + (sizeof(float2) + 1) * pairs);
 }
 
 int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_stream_t stream) {
     const int rc = check(a);
     if (rc) return rc;
     if (a->S > 0 && !a->logp) { set_error("NULL logp"); return HARTS_EINVAL; }
-    if (a->C == 0) { set_error(""); return HARTS_OK; }
+    if (a->C == 0) {                                    // positions without rows have no label either
+        const cudaError_t e = a->S > 0 ? cudaMemsetAsync(a->logp, 0, 4 * static_cast<size_t>(a->S), reinterpret_cast<cudaStream_t>(stream))
+                                       : cudaSuccess;
+        if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward");
+        set_error("");
+        return HARTS_OK;
+    }
     if (!a->workspace || a->workspace_bytes < harts_linear_logprob_fwd_workspace_bytes(a->C, a->V, a->D)) {
         set_error("workspace too small");
         return HARTS_ESMALLBUF;
@@ -1075,6 +1189,7 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     p.c2 = logit_factor(a->scale, a->D);
     const bool pad = pads_x(a->C, a->D);
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a->workspace) + (pad ? pad_bytes(a->C, a->D) : 0));
+    p.top = reinterpret_cast<uint8_t *>(p.part + a->C * q.n_tiles);
     q.a_panel = pad;
     if (!(pad ? map_panels(&q.a, a->workspace, a->C, a->D, q.a_rows, 1) : map_in(&q.a, a->x, a->C, a->D, a->D, q.a_rows)) ||
         !map_in(&q.b, a->weight, a->V, a->D, a->D, q.n / G)) {
@@ -1084,10 +1199,14 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     SemParams s = sem_params(a);
     s.part = p.part;
     s.tiles = q.n_tiles;
+    s.width = q.n;
+    s.c2 = p.c2;
+    s.top = p.top;
     const PadParams copy{s.x, static_cast<__nv_bfloat16 *>(a->workspace), a->C, a->C, a->D, 0};
     cudaError_t e = pad ? launch(head_pad_kernel, pad_blocks(a->C, a->D), 256, 0, 1, false, st, copy) : cudaSuccess;
     if (e == cudaSuccess) e = launch_tiles<kFwd>(p, G, pad, st);
-    if (e == cudaSuccess) e = launch(head_finish_kernel, (a->S + a->C + 7) / 8, 256, 0, 1, true, st, s);
+    if (e == cudaSuccess && a->S > 0) e = launch(head_labels_kernel, (a->S + 7) / 8, 256, 0, 1, true, st, s);
+    if (e == cudaSuccess) e = launch(head_finish_kernel, a->C, kRowThreads, 0, 1, true, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "linear log-prob forward launch");
     set_error("");
     return HARTS_OK;

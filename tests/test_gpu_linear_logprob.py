@@ -267,3 +267,35 @@ def test_no_rows_and_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(dx3, dx) and torch.equal(dw3, dw)
+
+
+@pytest.mark.parametrize("C,V,D,scale", [(1, 5003, 2048, 1.0), (6, 321, 1032, 1.0), (130, 2050, 512, -0.5), (300, 777, 2048, 1.0)])
+def test_an_entry_with_nearly_all_the_probability(C, V, D, scale):
+    """Rows that lean on one entry v* (the last, one in either half of a tile, any), labelled with
+    it and with another.  Its logit is formed in fp32: with Z = sum |x_i w_i| an error of at most
+    e = (16 D / 1024 + 12) u Z (sixteen products in a row for each 1024, then sums over threads,
+    and the scaling).  The other entries' probabilities, q in all, are off by e_z of the module's
+    bound.  At most 40 additions go onto a sum that holds the largest term (16 in its 32 columns,
+    8 across the tile's halves, 16 across tiles and threads; u / 2 each), and exponentials take
+    4 u.  So lse is off by e + q (e + e_z) + 24 u + u |lse|, and the log-probability of v* by
+    q (e + e_z) + 24 u; without the fp32 product it would be off by what the tensor cores
+    truncate, some 1e-6 of the logit whatever q is.  The other label's logit is an fp32 product
+    too."""
+    rng = np.random.default_rng(C + V)
+    bf = lambda a: torch.as_tensor(a, dtype=torch.float32).to(torch.bfloat16)
+    w = bf(rng.standard_normal((V, D)) * 2 / D ** 0.5)
+    main = rng.integers(0, V, size=C)
+    main[:4] = [V - 1, 0, 37, 250][:C]
+    x = bf(rng.standard_normal((C, D)) + 5 / scale * w.double().numpy()[main])
+    sem_row = np.concatenate([np.arange(C), np.arange(C)])
+    target = np.concatenate([main, (main + 1 + rng.integers(0, V - 1, size=C)) % V])
+    logp, lse = (a.double().cpu().numpy() for a in _run_fwd(x, w, sem_row, target, scale))
+    ref_logp, ref_lse = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target, scale)
+    xa, wa = np.abs(x.double().numpy()), np.abs(w.double().numpy())
+    fp32 = lambda v: (D / 1024 * 16 + 12) * U * abs(scale) * (xa * wa[v]).sum(axis=1)
+    e, (ez, _) = fp32(main), _errors(x, w, scale, ref_lse)
+    q = -np.expm1(ref_logp[:C])
+    assert (np.abs(lse - ref_lse) <= e + q * (e + ez) + 24 * U + U * np.abs(ref_lse)).all()
+    assert (np.abs(logp - ref_logp)[:C] <= q * (e + ez) + 24 * U).all()
+    assert (np.abs(logp - ref_logp)[C:] <= fp32(target[C:]) + e + q * (e + ez) + 24 * U + U * np.abs(ref_logp[C:])).all()
+    assert np.median(q) < 0.05
