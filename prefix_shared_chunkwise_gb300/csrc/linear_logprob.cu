@@ -796,9 +796,9 @@ __global__ void __launch_bounds__(kRowThreads) head_finish_kernel(SemParams p) {
 
 // X in panels of 64 columns, [panels][rows][64], zero past D, where its rows straddle lines:
 // each 128-byte row of a box then lies in one line instead of two; the rows are read once a tile
-// of the vocabulary, and misaligned lines bound the product (777 x 32003 x 1032 spent 120 K
-// cycles where 66 K went by without copies).  For a twin dZ (`fold` 32): rows 0 .. 31 and again,
-// zero past C.
+// of the vocabulary, and misaligned lines bound the product (777 x 32,003 x 1,032 forward: 66.8 us
+// with X as it is, 54.3 us with the copy made first).  For a twin dZ (`fold` 32): rows 0 .. 31 and
+// again, zero past C.
 struct PadParams { const __nv_bfloat16 *x; __nv_bfloat16 *out; int64_t C, rows; int32_t D, fold; };
 __device__ __forceinline__ void pad_rows(const PadParams &p, uint32_t block, uint32_t blocks) {
     const int64_t n = p.rows * ((p.D + 63) / 64) * 8;
@@ -937,8 +937,8 @@ int32_t tile_cost(int32_t n) { return std::max(n, 220) + 16; }
 // The forward's cut: blocks that share a tile (pairs: 256 rows) and the tile width, a multiple
 // of 16 columns a block, by the busiest worker's tiles.  A block alone reads its columns from L2
 // where a pair shares them, and takes 1.2 as long, 1.4 where the weight's rows straddle lines
-// (777 x 32003 x 1032: 59.8 us alone, 49.9 us in pairs), but wastes less where the rows end early
-// in a tile (300 x 157184 x 2048: 164 us alone, 177 us in pairs).
+// (777 x 32,003 x 1,032: 64.2 us alone, 54.3 us in pairs), but wastes less where the rows end early
+// in a tile (300 x 157,184 x 2,048: 179 us alone, 202 us in pairs).
 struct Cut { int group; int32_t width; };
 Cut fwd_cut(int64_t C, int32_t V, int32_t D) {
     Cut best{1, kTN};
@@ -953,9 +953,10 @@ Cut fwd_cut(int64_t C, int32_t V, int32_t D) {
     return best;
 }
 
-// The backward's group: pairs from 257 rows on.  By measurement (alone / pairs, us): 256 x 32003
-// x 1032 96 / 99, 129 rows 86 / 92; 385 rows 151 / 116, 300 x 157184 x 2048 611 / 567.
-int bwd_group(int64_t C) { return C <= 2 * kTM ? 1 : 2; }
+// The backward's group: pairs where their 256 rows are three quarters full.  By measurement (alone /
+// pairs, us): 32,003 x 1,032, 129 rows 81 / 87, 224 90 / 92, 256 102 / 93, 300 119 / 106, 513
+// 157 / 126; 157,184 x 2,048, 129 rows 428 / 423, 192 444 / 436, 224 480 / 449, 300 608 / 592.
+int bwd_group(int64_t C) { return C <= 3 * kTM / 2 ? 1 : 2; }
 
 // Tile width over `cols` columns in multiples of `unit`: the least work for the busiest worker,
 // as above.
@@ -979,9 +980,11 @@ bool map_in(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
     return encode_bf16(m, base, 2, dims, strides, box);
 }
 
-// Whether X is copied into aligned panels first: its rows straddle lines, and there are enough
-// of them for several tiles to read each.
-bool pads_x(int64_t C, int32_t D) { return D % 64 != 0 && C > kTM; }
+// Whether X is copied into aligned panels first: its rows straddle lines, and there are enough of
+// them for several tiles to read each.  By measurement (as they are / copied, us, V = 32,003,
+// D = 1,032): forward 129 rows 29.2 / 29.2, 256 31.0 / 29.1, 385 41.0 / 37.0; backward, where a
+// smaller part of the work reads X, 256 rows 94 / 97, 300 107 / 107, 513 135 / 126.
+bool pads_x(int64_t C, int32_t D, bool backward) { return D % 64 != 0 && C > (backward ? 2 * kTM : kTM); }
 size_t pad_bytes(int64_t rows, int32_t D) { return align256(size_t(2) * static_cast<size_t>(rows) * ((D + 63) / 64 * 64)); }
 int64_t pad_blocks(int64_t rows, int32_t D) {
     return std::min<int64_t>((rows * ((D + 63) / 64) * 8 + 255) / 256, int64_t(sm_count()) * 8);
@@ -1112,7 +1115,8 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     // Up to 32 rows a step of K has room for as many again, which take what bf16 cuts from dZ
     // (against X a second time).  With few rows one label's rounding is a whole row's error,
     // 2.8e-3 against the 1.7e-3 that rounding the result alone gives; over many rows it averages
-    // out.  (64 rows, in two steps: 71 us instead of 59 for 61 x 32003 x 1032.)
+    // out.  31 x 32,003 x 1,032 takes 62.8 us with it and 57.2 us without.  (64 rows, in two
+    // steps: 71 us instead of 59 for 61 rows, for 2.4e-3; not taken.)
     b.twin = C <= kTwin;
     b.dz_rows = b.twin ? 2 * kTwin : static_cast<int32_t>(C);
     int64_t want = piece > 0 ? piece : static_cast<int64_t>(kPieceBytes / (2 * std::max<int64_t>(b.dz_rows, 1)));
@@ -1131,7 +1135,7 @@ BwdPlan plan_bwd(int64_t C, int32_t V, int32_t D, int64_t S, int32_t piece) {
     b.splits = ceil_div(kb, b.k_per);
     b.acc = b.twin || b.splits > 1 || b.n_pieces > 1;
     b.pad = 0;
-    b.rows = b.twin ? pad_bytes(b.dz_rows, D) : pads_x(C, D) ? pad_bytes(C, D) : 0;
+    b.rows = b.twin ? pad_bytes(b.dz_rows, D) : pads_x(C, D, true) ? pad_bytes(C, D) : 0;
     b.ent_y = b.rows + align256(sizeof(RowInfo) * static_cast<size_t>(C));
     b.ent_v = b.ent_y + align256(4 * static_cast<size_t>(S));
     b.raw_y = b.ent_v + align256(4 * static_cast<size_t>(S));
@@ -1152,7 +1156,7 @@ extern "C" {
 size_t harts_linear_logprob_fwd_workspace_bytes(int64_t C, int32_t V, int32_t D) {
     if (C < 0 || V < 1 || D < 1) return 0;
     const size_t pairs = static_cast<size_t>(C) * ceil_div(V, fwd_cut(C, V, D).width);
-    return std::max<size_t>(256, (pads_x(C, D) ? pad_bytes(C, D) : 0) + (sizeof(float2) + 1) * pairs);
+    return std::max<size_t>(256, (pads_x(C, D, false) ? pad_bytes(C, D) : 0) + (sizeof(float2) + 1) * pairs);
 }
 
 int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_stream_t stream) {
@@ -1187,7 +1191,7 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     p.n_prod = 1;
     p.error = a->error;
     p.c2 = logit_factor(a->scale, a->D);
-    const bool pad = pads_x(a->C, a->D);
+    const bool pad = pads_x(a->C, a->D, false);
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a->workspace) + (pad ? pad_bytes(a->C, a->D) : 0));
     p.top = reinterpret_cast<uint8_t *>(p.part + a->C * q.n_tiles);
     q.a_panel = pad;
@@ -1247,7 +1251,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.ent_v = reinterpret_cast<float *>(ws + b.ent_v);
     s.raw_y = reinterpret_cast<int32_t *>(ws + b.raw_y);
     s.raw_v = reinterpret_cast<float *>(ws + b.raw_v);
-    const bool pad = pads_x(f.C, f.D), copies = pad || b.twin;
+    const bool pad = pads_x(f.C, f.D, true), copies = pad || b.twin;
     const PadParams copy{s.x, reinterpret_cast<__nv_bfloat16 *>(ws + b.pad), f.C, b.dz_rows, f.D, b.twin ? kTwin : 0};
     const int64_t row_blocks = ceil_div(f.C, 8);
     const cudaError_t first = launch(head_rows_kernel, row_blocks + (copies ? pad_blocks(b.dz_rows, f.D) : 0), 256, 0, 1,

@@ -299,3 +299,28 @@ def test_an_entry_with_nearly_all_the_probability(C, V, D, scale):
     assert (np.abs(logp - ref_logp)[:C] <= q * (e + ez) + 24 * U).all()
     assert (np.abs(logp - ref_logp)[C:] <= fp32(target[C:]) + e + q * (e + ez) + 24 * U + U * np.abs(ref_logp[C:])).all()
     assert np.median(q) < 0.05
+
+
+@pytest.mark.parametrize("C,V,D,S", [(192, 515, 72, 300), (193, 770, 200, 300), (256, 900, 1032, 400), (257, 513, 136, 400)])
+@pytest.mark.parametrize("scale", [1.0, -0.7])
+def test_rows_around_the_cuts(C, V, D, S, scale):
+    """Row counts on either side of where blocks pair up and where X is copied first; a negative
+    scale turns the largest logit into the smallest accumulator."""
+    test_forward(C, V, D, S, scale)
+    _check_bwd(*_case(C, V, D, S, 6), scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, 1.0])
+def test_equal_logits(scale):
+    """Entries that are all equal, and that differ in one: every one is the largest."""
+    C, V, D = 130, 300, 64
+    x = torch.ones(C, D, dtype=torch.bfloat16)
+    w = torch.full((V, D), 0.125, dtype=torch.bfloat16)
+    w[V - 1] = 0.25
+    sem_row, target = np.arange(C), np.arange(C) * 2
+    target[-1] = V - 1
+    logp, lse = _run_fwd(x, w, sem_row, target, scale)
+    rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target, scale)
+    ez, el = _errors(x, w, scale, re)
+    assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
+    assert np.all(np.abs(logp.cpu().numpy() - rl) <= ez + el + U * np.abs(rl))
