@@ -545,7 +545,8 @@ int harts_grad_clip(const harts_grad_tensor *tensors, int32_t count, float max_n
  * The backward forms the logits again, one piece of the vocabulary at a time, and holds that
  * piece's dz in bf16 (each entry formed in fp32 and rounded once; up to 32 rows in two bf16
  * terms); all sums are fp32 and in a fixed order.  x and weight must be finite: dweight sums
- * over every row, also over rows without positions (whose dx is zero).
+ * over every row, also over rows without positions (whose dx is zero).  Where they are not, lse
+ * is not either: a NaN in weight reaches every row's, one in x its own row's.
  */
 typedef struct {
     int64_t C;               /* compact rows, >= 0 */

@@ -779,7 +779,8 @@ __global__ void __launch_bounds__(kRowThreads) head_finish_kernel(SemParams p) {
     float z = p.scale * d0, rest;
     const float off = m - z * kLog2e;
     if (fabsf(off) < 64.f) {
-        rest = log1pf(fmaxf(sum - own, 0.f) * exp2f(off));
+        const float others = sum - own;                 // a NaN among the logits is in the sum alone, and stays in it
+        rest = log1pf((others < 0.f ? 0.f : others) * exp2f(off));
     } else {                                            // logits that are not finite, or beyond fp32's digits
         z = m * kLn2;
         rest = log2f(sum) * kLn2;

@@ -324,3 +324,34 @@ def test_equal_logits(scale):
     ez, el = _errors(x, w, scale, re)
     assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
     assert np.all(np.abs(logp.cpu().numpy() - rl) <= ez + el + U * np.abs(rl))
+
+
+@pytest.mark.parametrize("C,V,D", [(1, 5, 8), (3, 700, 64), (130, 1003, 136), (300, 2050, 72)])
+@pytest.mark.parametrize("scale", [1.0, -0.5])
+def test_not_finite_values_stay_visible(C, V, D, scale):
+    """A NaN or an infinity in one vocabulary row reaches every row's softmax (an infinity as an
+    infinite or undefined one), a NaN in one hidden row only that row's: lse and the positions'
+    log-probabilities are then not finite, and those of the other rows as without it."""
+    x, w, _, _, _ = _case(C, V, D, 1, 12)
+    sem_row, target = np.arange(C), (np.arange(C) * 7) % V
+    logp, lse = _run_fwd(x, w, sem_row, target, scale)
+    assert torch.isfinite(lse).all() and torch.isfinite(logp).all()
+    for v in {0, V // 2, V - 1}:
+        for bad in (float("nan"), float("inf")):
+            b = w.clone()
+            b[v, D // 2] = bad
+            got_logp, got_lse = _run_fwd(x, b, sem_row, target, scale)
+            if np.isnan(bad):
+                assert torch.isnan(got_lse).all() and torch.isnan(got_logp).all(), v
+            else:                                   # z = -infinity leaves the entry out of the sum
+                z = scale * (x.double() @ b.double().t())
+                ref = torch.logsumexp(z, 1)
+                seen = torch.isfinite(ref)
+                assert not torch.isfinite(got_lse.cpu()[~seen]).any(), v
+                assert torch.isfinite(got_lse.cpu()[seen]).all(), v
+    b = x.clone()
+    b[C // 2, 3] = float("nan")
+    got_logp, got_lse = _run_fwd(b, w, sem_row, target, scale)
+    rest = np.arange(C) != C // 2
+    assert torch.isnan(got_lse[C // 2]) and torch.isnan(got_logp[C // 2])
+    assert torch.equal(got_lse[rest], lse[rest]) and torch.equal(got_logp[rest], logp[rest])
