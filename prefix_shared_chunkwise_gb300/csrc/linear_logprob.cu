@@ -561,21 +561,24 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                             for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
                             store_row(dst + kTwin * 128, lane, v);
                         }
-                        if (MODE == kDz) {              // the row's labels among these 64 columns
+                        // The row's labels among these 64 columns.  Written by the kernel before,
+                        // which this one overlaps: plain loads, the read-only path does not
+                        // see what is written while a kernel runs.
+                        if (MODE == kDz) {
                             const int32_t lo = p.v0 + n0 + c;
                             int32_t e = 0;
                             for (int32_t len = ri.count > 8 ? ri.count : 0; len > 0;) {     // first label >= lo
                                 const int32_t half_len = len >> 1;
-                                if (__ldg(p.ent_y + ri.first + e + half_len) < lo) { e += half_len + 1; len -= half_len + 1; }
+                                if (p.ent_y[ri.first + e + half_len] < lo) { e += half_len + 1; len -= half_len + 1; }
                                 else len = half_len;
                             }
                             for (; e < ri.count; ++e) {
-                                const int32_t y = __ldg(p.ent_y + ri.first + e);
+                                const int32_t y = p.ent_y[ri.first + e];
                                 if (y >= lo + 64) break;
                                 const uint32_t j = static_cast<uint32_t>(y - lo);
                                 if (j < 64u) {
                                     uint8_t *at = dst + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2;
-                                    const float val = __ldg(p.ent_v + ri.first + e);
+                                    const float val = p.ent_v[ri.first + e];
                                     const __nv_bfloat16 top = __float2bfloat16_rn(val);
                                     *reinterpret_cast<__nv_bfloat16 *>(at) = top;
                                     if (p.twin)

@@ -355,3 +355,21 @@ def test_not_finite_values_stay_visible(C, V, D, scale):
     rest = np.arange(C) != C // 2
     assert torch.isnan(got_lse[C // 2]) and torch.isnan(got_logp[C // 2])
     assert torch.equal(got_lse[rest], lse[rest]) and torch.equal(got_logp[rest], logp[rest])
+
+
+@pytest.mark.parametrize("C,V,D", [(20, 2050, 72), (150, 2050, 136), (300, 1003, 72)])
+def test_a_workspace_taken_again_for_other_labels(C, V, D):
+    """Calls one after another in one workspace, each with its own labels and gradients: the bits
+    of calls with a workspace of their own."""
+    row_ptr, row_sem = (_dev(a) for a in _csr(np.arange(3 * C) % C, C))
+    x, w, _, _, _ = _case(C, V, D, 1, 13)
+    x, w = x.cuda(), w.cuda()
+    rng = np.random.default_rng(13)
+    sets = [(_dev(rng.integers(0, V, 3 * C).astype(np.int32)), _dev(rng.standard_normal(3 * C).astype(np.float32)))
+            for _ in range(6)]
+    lse = linear_logprob_fwd(x, w, row_ptr, row_sem, sets[0][0])[1]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    shared = [linear_logprob_bwd(x, w, row_ptr, row_sem, t, lse, g, workspace=ws) for t, g in sets]
+    for (t, g), got in zip(sets, shared):
+        want = linear_logprob_bwd(x, w, row_ptr, row_sem, t, lse, g, workspace=torch.zeros_like(ws))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
