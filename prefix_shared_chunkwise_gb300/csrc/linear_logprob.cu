@@ -339,14 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     tc::fence_after_sync();
     let_next_start();
     const uint32_t tm = s_tmem;
+    // Bounded waits begin once the kernel before this one is done: its time is not theirs, and it
+    // may be any.  dZ's first two tiles, one for each accumulator, are copied and multiplied beside
+    // it where both operands are the call's own; nothing else waits for a barrier until then.
+    const bool ahead = MODE == kDz && !p.prod[0].a_panel;
 
     if (warp == 0 || warp == 3) {
         // One warp each for A and B, whole like the issuing one: a copy by a lone thread, or both
         // operands' by one warp, could not keep up with the 512 cycles of a step's products.
         const bool is_b = warp == 3;
         const uint32_t on = elect_lane(), arms = rank == 0 ? on : 0;
-        // dZ is complete; the aligned copy of X, where there is one
-        if (MODE == kGrad || (!is_b && p.prod[0].a_panel)) wait_previous();
+        // dZ is complete; the aligned copy of X, where there is one (B fills its stages once before)
+        if (MODE == kGrad || (!is_b && !ahead)) wait_previous();
         uint32_t it = 0;                                // stages filled so far
         uint32_t s = 0, round = 0;                      // next stage, times the ring went round
         const uint32_t own0 = tc::smem_addr(&bars[B::full]), full0 = G == 2 ? leader_addr(&bars[B::full]) : own0;
@@ -354,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         TileId t;
         bool ok = true;
         for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
+            if (ahead && n == 2) wait_previous();
             // what the loop needs is taken out of the parameters once a tile
             const Prod &q = p.prod[t.which];
             const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             const int32_t row = is_b ? y0 + n0 : m0, panel = (is_b ? n0 : m0) / 64, ky = is_b ? y0 : 0;
             const uint32_t bytes = (is_b ? nb * 128u : q.a_mn ? kABytes : q.a_rows * 128u) * G;
             for (int32_t k = k0; k < k1; ++k, ++it) {
+                if (it == kStages && !ahead) wait_previous();
                 if (round > 0 && !warp_wait(&bars[B::empty + s], (round - 1) & 1, &s_fail)) { ok = false; break; }
                 const uint32_t full = full0 + s * 8, dst = dst0 + s * kStageBytes;
                 expect(arms, own0 + s * 8, bytes);
@@ -381,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         // a failure the products may not have waited for them), then the stages' last release.
         // In a pair only the release says so for the second block; after a failure its wait runs
         // out, long after the last copy.
+        wait_previous();
         for (uint32_t i = 0; i < kStages; ++i) {
             if (it <= i) continue;
             const uint32_t uses = (it - i + kStages - 1) / kStages;
@@ -395,7 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
             const uint32_t base = tc::smem_addr(sm);
             TileId t;
             bool ok = true;
+            if (!ahead) wait_previous();
             for (; ok && tile_at(p, tile, worker, workers, t); ++tile) {
+                if (ahead && tile == 2) wait_previous();
                 const Prod &q = p.prod[t.which];
                 const int32_t k0 = t.split * q.k_per, k1 = min(q.k_blocks, k0 + q.k_per);
                 const uint32_t buf = tile & 1, use = tile >> 1, d = tm + buf * kTN;
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
         [[maybe_unused]] uint32_t groups = 0;                  // groups of 128 bytes of columns so far
         TileId t;
         bool ok = true;
-        if (MODE == kDz) wait_previous();               // rows' terms; the last piece's dZ has been read
+        wait_previous();                                // dZ: rows' terms; the last piece's dZ has been read
         for (; ok && tile_at(p, tile, worker, workers, t); ++tile) {
             const Prod &q = p.prod[t.which];
             const uint32_t buf = tile & 1;
@@ -610,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
                 uint32_t groups = 0;
                 TileId t;
                 bool ok = true;
+                wait_previous();
                 for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
                     const Prod &q = p.prod[t.which];
                     const int32_t n0 = t.nt * q.n, y = (t.mt * G + rank) * kTM;
