@@ -832,87 +832,247 @@ __global__ void __launch_bounds__(256) head_pad_kernel(PadParams p) {
 
 // ---- backward: per row, G and the distinct labels with a gradient of their own ----------
 
+// Label and gradient of the q-th of row_sem; -1 and 0 where the position has no label.
+__device__ __forceinline__ int32_t label_of(const SemParams &p, int32_t q, float &g) {
+    const int32_t s = __ldg(p.row_sem + q);
+    g = 0.f;
+    if (s < 0 || s >= p.S) return -1;
+    const int32_t y = __ldg(p.target + s);
+    if (y < 0 || y >= p.V) return -1;
+    g = __ldg(p.dlogp + s);
+    return y;
+}
+// (Labels are looked up again from the workspace: whatever it holds, the weight's rows are kept to.)
+__device__ __forceinline__ float finish_entry(const SemParams &p, int64_t c, int32_t y, float sum, float G, float lse) {
+    y = min(max(y, 0), p.V - 1);
+    const float z = p.scale * row_dot(p.x + c * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
+    return p.scale * (sum - G * expf(z - lse));
+}
+
+// Distinct labels of a row that one warp gathers.  By measurement (the backward in us, 157,184 x
+// 2,048, one row in eight of 64 with that many positions, by the warp / by the block): 32 labels
+// 428 / 364, 64 524 / 371, 200 931 / 410; every row of 64: 32 labels 439 / 450, 64 532 / 532,
+// 200 951 / 857, 100 labels in 3,000 positions 888 / 1,033.
+constexpr int kFewLabels = 16;
+constexpr int kRowWarps = 8;
+
+struct SortSpace {
+    int32_t base[256], count[kRowWarps][256], sums[kRowWarps];
+};
+
+// Sum over the block of what the threads before this one hold; `total` of all.
+__device__ __forceinline__ int32_t block_before(int32_t v, SortSpace &sm, int32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t up = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t t = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += t;
+    }
+    if (lane == 31) sm.sums[warp] = up;
+    __syncthreads();
+    int32_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) {
+        if (i < warp) before += sm.sums[i];
+        total += sm.sums[i];
+    }
+    __syncthreads();
+    return before + up - v;
+}
+
+// n pairs by the eight bits of the key from `shift` on, equal ones in the order they had.
+__device__ void radix_pass(const int32_t *y, const float *v, int32_t *to_y, float *to_v, int32_t n, int shift, SortSpace &sm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    sm.base[tid] = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) sm.count[w][tid] = 0;
+    __syncthreads();
+    for (int32_t i = tid; i < n; i += 256) atomicAdd(&sm.base[y[i] >> shift & 255], 1);
+    __syncthreads();
+    int32_t total;
+    const int32_t first = block_before(sm.base[tid], sm, total);
+    sm.base[tid] = first;                               // where this digit's next pair goes
+    for (int32_t from = 0; from < n; from += 256) {
+        const int32_t i = from + tid;
+        const bool on = i < n;
+        const int32_t key = on ? y[i] : 0;
+        const float val = on ? v[i] : 0.f;
+        const int digit = on ? key >> shift & 255 : 256;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        if (on && rank == 0) sm.count[warp][digit] = __popc(same);
+        __syncthreads();
+        int32_t at = sm.base[tid];
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+            const int32_t k = sm.count[w][tid];
+            sm.count[w][tid] = at;
+            at += k;
+        }
+        sm.base[tid] = at;
+        __syncthreads();
+        if (on) {
+            const int32_t dst = min(sm.count[warp][digit] + rank, n - 1);   // rows that overlap would not add up
+            to_y[dst] = key;
+            to_v[dst] = val;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) sm.count[w][tid] = 0;
+        __syncthreads();
+    }
+}
+
+// A row with many distinct labels, by the whole block: its positions are sorted by label (a pass
+// per eight bits of the vocabulary, between the two pairs of arrays), equal labels staying in
+// position order; a warp adds up a label's run and finishes its entry.  Work grows with the
+// positions, and with the labels only by a dot product each.
+__device__ void many_labels(const SemParams &p, int64_t c, float G, SortSpace &sm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t b = max(0, __ldg(p.row_ptr + c));
+    const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S)) - b;
+    const int bits = 32 - __clz(p.V);                   // V stands for no label, and is sorted last
+    int32_t *y0 = p.raw_y + b, *y1 = p.ent_y + b;
+    float *v0 = p.raw_v + b, *v1 = p.ent_v + b;
+    const bool odd = (bits + 7) / 8 & 1;                // the last pass has to end in the raw arrays
+    int32_t *y = odd ? y1 : y0;
+    float *v = odd ? v1 : v0;
+    for (int32_t i = tid; i < n; i += 256) {
+        float g;
+        const int32_t label = label_of(p, b + i, g);
+        y[i] = label < 0 ? p.V : label;
+        v[i] = g;
+    }
+    __syncthreads();
+    for (int shift = 0; shift < bits; shift += 8) {
+        int32_t *to_y = y == y0 ? y1 : y0;
+        float *to_v = v == v0 ? v1 : v0;
+        radix_pass(y, v, to_y, to_v, n, shift, sm);
+        y = to_y;
+        v = to_v;
+    }
+    int32_t found = 0;
+    for (int32_t from = 0; from < n; from += 256) {     // where each label's run begins
+        const int32_t i = from + tid;
+        const bool begins = i < n && y0[i] < p.V && (i == 0 || y0[i - 1] != y0[i]);
+        int32_t total;
+        const int32_t k = found + block_before(begins, sm, total);
+        if (begins) y1[k] = i;
+        found += total;
+    }
+    __syncthreads();
+    const float lse = p.lse[c];
+    for (int32_t k = warp; k < found; k += kRowWarps) {
+        const int32_t from = min(max(y1[k], 0), n - 1), label = y0[from];
+        float sum = 0.f;
+        bool run = true;
+        for (int32_t i = from + lane; run; i += 32) {
+            const bool in = i < n && y0[i] == label;
+            if (in) sum += v0[i];
+            run = __all_sync(0xffffffffu, in);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float e = finish_entry(p, c, label, sum, G, lse);
+        __syncwarp();
+        if (lane == 0) {
+            y1[k] = label;
+            v1[k] = e;
+        }
+    }
+    if (tid == 0) p.rows[c] = RowInfo{-p.scale * G, lse * kLog2e, found, b};
+    __syncthreads();
+}
+
 // One warp a row.  Its positions are taken 32 at a time: lanes with one label are added in
 // position order, and their sum to the label's entry in (raw_y, raw_v), found among the entries
 // so far; a row's positions mostly share few labels.  Entries whose gradients do not cancel are
 // then put in label order, so that a tile finds its own among many, and finished:
 // ent_v = scale (sum g - G e^(z - lse)) in fp32, written over the row's softmax term when the
-// tile is formed.  Rows with d distinct labels cost d^2 / 32 steps and d dot products.
+// tile is formed.  A row that turns out to have more than kFewLabels distinct labels is left to
+// the whole block, which sorts it: the warp's steps grow with d^2, its dot products come one by one.
 // Blocks from `pad_from` on copy X instead, where a copy is wanted.
-__global__ void __launch_bounds__(256) head_rows_kernel(SemParams p, PadParams pad, uint32_t pad_from) {
+__global__ void __launch_bounds__(32 * kRowWarps) head_rows_kernel(SemParams p, PadParams pad, uint32_t pad_from) {
+    __shared__ SortSpace space;
+    __shared__ float row_g[kRowWarps];
+    __shared__ bool many[kRowWarps];
     if (blockIdx.x >= pad_from) {
         let_next_start();
         pad_rows(pad, blockIdx.x - pad_from, gridDim.x - pad_from);
         return;
     }
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kRowWarps, c = c0 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     let_next_start();
-    if (c >= p.C) return;
-    const int32_t b = max(0, __ldg(p.row_ptr + c));
-    const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
     float G = 0.f;
-    int32_t found = 0;
-    for (int32_t base = b; base < e; base += 32) {
-        int32_t y = -1;
-        float g = 0.f;
-        if (base + lane < e) {
-            const int32_t s = __ldg(p.row_sem + base + lane);
-            if (s >= 0 && s < p.S) {
-                y = __ldg(p.target + s);
-                if (y < 0 || y >= p.V) y = -1;
-                else g = __ldg(p.dlogp + s);
-            }
-        }
-        G += g;
-        const uint32_t same = __match_any_sync(0xffffffffu, y);
-        const bool leads = y >= 0 && lane == __ffs(same) - 1;
-        float sum = 0.f;
+    int32_t found = 0, b = 0;
+    if (c < p.C) {
+        b = max(0, __ldg(p.row_ptr + c));
+        const int32_t e = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.row_ptr + c + 1)), p.S));
+        for (int32_t base = b; base < e; base += 32) {
+            int32_t y = -1;
+            float g = 0.f;
+            if (base + lane < e) y = label_of(p, base + lane, g);
+            G += g;
+            if (found > kFewLabels) continue;           // only G is still wanted
+            const uint32_t same = __match_any_sync(0xffffffffu, y);
+            const bool leads = y >= 0 && lane == __ffs(same) - 1;
+            float sum = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-            const float gi = __shfl_sync(0xffffffffu, g, i);
-            if (same >> i & 1u) sum += gi;
+            for (int i = 0; i < 32; ++i) {
+                const float gi = __shfl_sync(0xffffffffu, g, i);
+                if (same >> i & 1u) sum += gi;
+            }
+            int32_t at = -1;
+            for (int32_t k = 0; k < found; ++k)
+                if (p.raw_y[b + k] == y) at = k;
+            const bool fresh = leads && at < 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, fresh);
+            if (fresh) {
+                const int32_t k = b + found + __popc(mask & ((1u << lane) - 1u));
+                p.raw_y[k] = y;
+                p.raw_v[k] = sum;
+            } else if (leads) {
+                p.raw_v[b + at] += sum;
+            }
+            found += __popc(mask);
+            __syncwarp();
         }
-        int32_t at = -1;
-        for (int32_t k = 0; k < found; ++k)
-            if (p.raw_y[b + k] == y) at = k;
-        const bool fresh = leads && at < 0;
-        const uint32_t mask = __ballot_sync(0xffffffffu, fresh);
-        if (fresh) {
-            const int32_t k = b + found + __popc(mask & ((1u << lane) - 1u));
-            p.raw_y[k] = y;
-            p.raw_v[k] = sum;
-        } else if (leads) {
-            p.raw_v[b + at] += sum;
-        }
-        found += __popc(mask);
-        __syncwarp();
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
-    int32_t count = 0;
-    for (int32_t base = 0; base < found; base += 32) {
-        const int32_t k = base + lane;
-        const int32_t y = k < found ? p.raw_y[b + k] : -1;
-        const float v = k < found ? p.raw_v[b + k] : 0.f;
-        int32_t before = 0;
-        for (int32_t j = 0; j < found; ++j) before += p.raw_v[b + j] != 0.f && p.raw_y[b + j] < y;
-        if (v != 0.f) {
-            p.ent_y[b + before] = y;
-            p.ent_v[b + before] = v;
+        for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
+    }
+    if (c < p.C && found <= kFewLabels) {
+        int32_t count = 0;
+        for (int32_t base = 0; base < found; base += 32) {
+            const int32_t k = base + lane;
+            const int32_t y = k < found ? p.raw_y[b + k] : -1;
+            const float v = k < found ? p.raw_v[b + k] : 0.f;
+            int32_t before = 0;
+            for (int32_t j = 0; j < found; ++j) before += p.raw_v[b + j] != 0.f && p.raw_y[b + j] < y;
+            if (v != 0.f) {
+                p.ent_y[b + before] = y;
+                p.ent_v[b + before] = v;
+            }
+            count += __popc(__ballot_sync(0xffffffffu, v != 0.f));
         }
-        count += __popc(__ballot_sync(0xffffffffu, v != 0.f));
-    }
-    __syncwarp();
-    const float lse = p.lse[c];
-    for (int32_t i = 0; i < count; ++i) {
-        const int32_t y = p.ent_y[b + i];
-        const float z = p.scale * row_dot(p.x + c * p.D, p.w + static_cast<int64_t>(y) * p.D, p.D);
-        const float v = p.scale * (p.ent_v[b + i] - G * expf(z - lse));
         __syncwarp();
-        if (lane == 0) p.ent_v[b + i] = v;
+        const float lse = p.lse[c];
+        for (int32_t i = 0; i < count; ++i) {
+            const float v = finish_entry(p, c, p.ent_y[b + i], p.ent_v[b + i], G, lse);
+            __syncwarp();
+            if (lane == 0) p.ent_v[b + i] = v;
+        }
+        if (lane == 0) p.rows[c] = RowInfo{-p.scale * G, lse * kLog2e, count, b};
     }
-    if (lane == 0) p.rows[c] = RowInfo{-p.scale * G, lse * kLog2e, count, b};
+    if (lane == 0) {
+        row_g[threadIdx.x >> 5] = G;
+        many[threadIdx.x >> 5] = found > kFewLabels;
+    }
+    if (!__syncthreads_or(found > kFewLabels)) return;
+    for (int i = 0; i < kRowWarps; ++i)
+        if (many[i]) many_labels(p, c0 + i, row_g[i], space);
 }
 
 // dX in bf16 from the splits' fp32 sums, in ascending order; a twin dZ's second half last.
@@ -1267,8 +1427,8 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     s.raw_v = reinterpret_cast<float *>(ws + b.raw_v);
     const bool pad = pads_x(f.C, f.D, true), copies = pad || b.twin;
     const PadParams copy{s.x, reinterpret_cast<__nv_bfloat16 *>(ws + b.pad), f.C, b.dz_rows, f.D, b.twin ? kTwin : 0};
-    const int64_t row_blocks = ceil_div(f.C, 8);
-    const cudaError_t first = launch(head_rows_kernel, row_blocks + (copies ? pad_blocks(b.dz_rows, f.D) : 0), 256, 0, 1,
+    const int64_t row_blocks = ceil_div(f.C, kRowWarps);
+    const cudaError_t first = launch(head_rows_kernel, row_blocks + (copies ? pad_blocks(b.dz_rows, f.D) : 0), 32 * kRowWarps, 0, 1,
                                      false, st, s, copy, static_cast<uint32_t>(row_blocks));
     if (first != cudaSuccess) return cuda_fail(first, "linear log-prob backward launch");
 

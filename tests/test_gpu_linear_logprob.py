@@ -373,3 +373,67 @@ def test_a_workspace_taken_again_for_other_labels(C, V, D):
     for (t, g), got in zip(sets, shared):
         want = linear_logprob_bwd(x, w, row_ptr, row_sem, t, lse, g, workspace=torch.zeros_like(ws))
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("V", [250, 40_003, 70_001])
+def test_rows_with_many_distinct_labels(V):
+    """Rows on either side of what one warp gathers (16 distinct labels), and one with thousands,
+    each of them once, twice or more; labels of one, two and three bytes.  Gradients of a label that
+    cancel, and positions without a label, among them."""
+    rng = np.random.default_rng(V)
+    D, sem_row, target = 64, [], []
+    for row, (n, labels) in enumerate([(128, 16), (17, 17), (20_000, min(V, 12_000)), (0, 1), (700, 200)]):
+        pool = rng.permutation(V)[:min(V, labels)]
+        y = np.concatenate([pool, rng.choice(pool, max(0, n - len(pool)))])[:max(n, 0)]
+        y = rng.permutation(y)
+        if row == 4:
+            y[::9] = [-1, V][0]
+        sem_row.append(np.full(len(y), row))
+        target.append(y)
+    sem_row, target = np.concatenate(sem_row).astype(np.int64), np.concatenate(target).astype(np.int64)
+    order = rng.permutation(len(sem_row))
+    sem_row, target = sem_row[order], target[order]
+    g = rng.standard_normal(len(sem_row)).astype(np.float32)
+    twice = np.flatnonzero((sem_row == 2) & (target == target[sem_row == 2][0]))
+    if len(twice) > 1:
+        g[twice] = 0
+        g[twice[0]], g[twice[1]] = 1.25, -1.25
+    x, w, _, _, _ = _case(5, V, D, 1, 14)
+    _check_bwd(x, w, sem_row, target, g, 1.0)
+
+
+def test_distinct_labels_of_one_row_cost_what_they_are():
+    """Eight times the distinct labels on one row take about eight times as long (plus what both
+    calls share), not sixty-four; and the limit of the waits is for other things."""
+    V, D = 157_184, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((2, D), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((V, D), generator=gen, device="cuda") * 0.2).to(torch.bfloat16)
+    lse = torch.logsumexp(x.double() @ w.double().t(), 1).float()
+
+    def run(n):
+        ptr = torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda")
+        sem = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        target = torch.randperm(V, generator=gen, device="cuda")[:n + 1].to(torch.int32)
+        g = torch.randn(n + 1, generator=gen, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            dx, dw = linear_logprob_bwd(x, w, ptr, sem, target, lse, g, error=err)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        assert int(err) == 0
+        dz = -torch.exp(x.double() @ w.double().t() - lse.double()[:, None])
+        dz *= torch.stack([g[:n].double().sum(), g[n].double()])[:, None]
+        dz[0].index_add_(0, target[:n].long(), g[:n].double())
+        dz[1, target[n].long()] += g[n].double()
+        for got, ref in ((dx, dz @ w.double()), (dw, dz.t() @ x.double())):
+            assert rel_l2(got.double().cpu().numpy(), ref.cpu().numpy()) <= 2.0 ** -7
+        return best
+
+    small, large = run(16_384), run(131_072)
+    assert large <= 16 * small, (small, large)
