@@ -554,7 +554,7 @@ typedef struct {
     int32_t D;               /* width of the hidden rows, a multiple of 8 */
     int32_t dtype;           /* harts_dtype of x, weight, dx, dweight: HARTS_BF16 */
     float scale;             /* of the logits (1 / temperature), finite */
-    int64_t S;               /* semantic positions, < 2^31 */
+    int64_t S;               /* semantic positions; C, V and S are 2^31 - 256 at most */
     const void *x;           /* device [C][D], 16-byte aligned */
     const void *weight;      /* device [V][D], 16-byte aligned */
     const int32_t *row_ptr;  /* device [C+1]: semantic positions of row c are row_sem[row_ptr[c] ..] */

@@ -1234,7 +1234,8 @@ int check(const harts_linear_logprob_fwd_args *a) {
     if (a->dtype != HARTS_BF16) { set_error("hidden rows and weight must be bf16"); return HARTS_EUNSUPPORTED; }
     if (a->C < 0 || a->S < 0 || a->V < 1 || a->D < 1) { set_error("C, S >= 0 and V, D >= 1 required"); return HARTS_EINVAL; }
     if (a->D % 8) { set_error("D must be a multiple of 8 (rows start 16-byte aligned)"); return HARTS_EUNSUPPORTED; }
-    if (a->S > 0x7fffffff || a->C > 0x7fffff00 || a->V > 0x7fffff00) { set_error("C, V or S beyond int32 rows"); return HARTS_EOVERFLOW; }
+    // the kernels' int32 indices take steps of up to 256 past the last one
+    if (a->S > 0x7fffff00 || a->C > 0x7fffff00 || a->V > 0x7fffff00) { set_error("C, V or S beyond int32 rows"); return HARTS_EOVERFLOW; }
     const int64_t c = a->C / kTM + 1, v = a->V / 64 + 1, d = a->D / 64 + 1;      // tiles are counted in 32 bits
     if (c * v > 0x3fffffff || (c + v) * d > 0xffffff) {
         set_error("more tiles than the library counts");

@@ -149,3 +149,13 @@ def test_python_checks():
         api.GradSet([x], [x[:2]])
     with pytest.raises(ValueError, match="unsupported dtype"):
         api.GradSet([x.half()])
+
+
+def test_linear_logprob_positions_up_to_the_last_step_of_an_index():
+    """The kernels step up to 256 past the last position in 32 bits: 2^31 - 256 is the most.  A
+    count that is taken gets as far as the workspace's size."""
+    def call(S):
+        a = _args(L.LinearLogprobFwdArgs, HEAD, S=S, workspace_bytes=16)
+        return L.lib().harts_linear_logprob_fwd(ctypes.byref(a), None)
+    assert call((1 << 31) - 256) == ESMALLBUF
+    assert call((1 << 31) - 255) == EOVERFLOW and call((1 << 31) - 1) == EOVERFLOW
