@@ -503,9 +503,10 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *args, harts_stream_t stream)
 /*
  * norm = sqrt(sum over all tensors of the squares of their values);
  * out_i = g_i * (norm > max_norm ? max_norm / norm : 1).
- * Squares are summed in fp32 within a block's chunks and in fp64 above that, in a fixed
- * order (no atomics); squares that overflow fp32 are summed again in fp64.  When the norm is
- * not finite the gradients are passed on unscaled, and the caller sees it in *norm.
+ * Squares are summed in fp32 over the 64 bytes that a thread loads at a time and in fp64 from
+ * there on, in a fixed order (no atomics); squares that overflow fp32, or that it holds as zero or
+ * with few bits where there are no larger ones, are summed again in fp64.  When the norm is not
+ * finite the gradients are passed on unscaled, and the caller sees it in *norm.
  */
 typedef struct {
     const void *g;           /* device [n] values, aligned to their type */

@@ -10,8 +10,12 @@
 //
 // Squares are summed in fp32 over the 16 to 32 values that a thread loads at a time and in fp64
 // from there on.  A block whose sum is not finite reads its spans again in fp64: squares overflow
-// fp32 from 1.8e19 on, which bf16 and fp32 values reach.  If the norm itself is not finite the
-// gradients pass through unscaled; the caller sees it in the norm.
+// fp32 from 1.8e19 on, which bf16 and fp32 values reach.  So does
+// one whose sum is below 2^-90 and not one of zeros: a square below 2^-126 loses up to 2^-150,
+// which over the 2^34 values that a block has at most is 2^-26 of such a sum, and more of a
+// smaller one.  (Whether values are zeros is looked at where their squares are: doing so for all
+// of them took 4 % of the sum's time.)  If the norm itself is not finite the gradients pass
+// through unscaled; the caller sees it in the norm.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -79,8 +83,14 @@ __device__ __forceinline__ int64_t head_of(const T *p, int64_t n) {
     return h < n ? h : n;
 }
 
-template <typename T>
-__device__ double squares(const T *g, int64_t n) {
+// The bits of a pack that are set where a value is not zero.
+__device__ __forceinline__ uint32_t magnitude(uint4 u, const __nv_bfloat16 *) { return (u.x | u.y | u.z | u.w) & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t magnitude(uint4 u, const float *) { return (u.x | u.y | u.z | u.w) & 0x7fffffffu; }
+
+// This thread's part of the sum; WIDE: all of it in fp64.  `seen` is set where values are not zero
+// whose fp32 squares are.
+template <bool WIDE, typename T>
+__device__ double squares(const T *g, int64_t n, uint32_t &seen) {
     constexpr int N = Pack<T>::n;
     const int t = threadIdx.x;
     const int64_t head = head_of(g, n);
@@ -89,34 +99,41 @@ __device__ double squares(const T *g, int64_t n) {
     const int64_t nv = (n - head) / N, tail = head + nv * N + t;
     if (t < head || tail < n) {
         const float a = t < head ? get(g + t) : 0.f, b = tail < n ? get(g + tail) : 0.f;
-        sum = fmaf(a, a, b * b);
+        if (WIDE) sum = static_cast<double>(a) * a + static_cast<double>(b) * b;
+        else sum = fmaf(a, a, b * b);
+        seen |= (a != 0.f) | (b != 0.f);
     }
     for (int64_t i = t; i < nv; i += 4 * kThreads) {
         uint4 u[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             u[k] = i + k * kThreads < nv ? __ldg(q + i + k * kThreads) : make_uint4(0, 0, 0, 0);
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float v[N];
-            expand(u[k], v, g);
+            for (int k = 0; k < 4; ++k) {
+                float v[N];
+                expand(u[k], v, g);
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                s0 = fmaf(v[j], v[j], s0); s1 = fmaf(v[j + 1], v[j + 1], s1);
-                s2 = fmaf(v[j + 2], v[j + 2], s2); s3 = fmaf(v[j + 3], v[j + 3], s3);
+                for (int j = 0; j < N; ++j) sum = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), sum);
             }
+        } else {
+            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v[N];
+                expand(u[k], v, g);
+#pragma unroll
+                for (int j = 0; j < N; j += 4) {
+                    s0 = fmaf(v[j], v[j], s0); s1 = fmaf(v[j + 1], v[j + 1], s1);
+                    s2 = fmaf(v[j + 2], v[j + 2], s2); s3 = fmaf(v[j + 3], v[j + 3], s3);
+                }
+            }
+            const float s = (s0 + s1) + (s2 + s3);
+            if (s == 0.f) seen |= magnitude(u[0], g) | magnitude(u[1], g) | magnitude(u[2], g) | magnitude(u[3], g);
+            sum += s;
         }
-        sum += (s0 + s1) + (s2 + s3);
     }
     return sum;
-}
-
-template <typename T>
-__device__ double squares64(const T *g, int64_t n) {
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) { const double v = get(g + i); s = fma(v, v, s); }
-    return s;
 }
 
 // Sum over the block in a fixed order; thread 0 returns it.  GB300 has few fp64 units (a
@@ -146,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __
     __shared__ int s_wide;
     let_next_start();
     double sum = 0.0;
+    uint32_t seen = 0;
     for (int wide = 0; wide < 2; ++wide) {
         sum = 0.0;
         for (int32_t j = blockIdx.x; j < s.spans; j += gridDim.x) {
@@ -157,13 +175,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_squares_kernel(const __
                 const int64_t n = run_of(s, k, c, stop, &at);
                 const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(s.item[k].g) + at;
                 const float *f = static_cast<const float *>(s.item[k].g) + at;
-                if (wide) sum += s.item[k].kinds & 1 ? squares64(b, n) : squares64(f, n);
-                else sum += s.item[k].kinds & 1 ? squares(b, n) : squares(f, n);
+                if (wide) sum += s.item[k].kinds & 1 ? squares<true>(b, n, seen) : squares<true>(f, n, seen);
+                else sum += s.item[k].kinds & 1 ? squares<false>(b, n, seen) : squares<false>(f, n, seen);
                 c = stop;
             }
         }
         sum = block_sum(sum, sm);
-        if (threadIdx.x == 0) s_wide = !isfinite(sum);
+        const int some = __syncthreads_or(seen != 0);
+        if (threadIdx.x == 0) s_wide = !isfinite(sum) || (sum < 0x1p-90 && (sum > 0.0 || some));
         __syncthreads();
         if (!s_wide) break;
     }

@@ -124,3 +124,32 @@ def test_graph_and_stream():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want)) and float(n) == wn
+
+
+@pytest.mark.parametrize("kind", [BF, F32])
+@pytest.mark.parametrize("scale", [1e-19, 1e-20, 1e-25, 1e-35])
+def test_squares_below_fp32(kind, scale):
+    """Values whose squares fp32 holds as zero or with few bits.  The norm's own bound; a clipped
+    value's is its relative one, with half of the type's smallest step (2^-134 bf16, 2^-150 fp32)
+    where it is not normal."""
+    for sizes in ((1,), (5001, 3, 700_001), (100, 0, 40)):
+        grads = _grads(sizes, [kind], 6, scale)
+        if sizes[0] == 100:                         # among zeros, and one tensor of them
+            grads[0][1:] = 0
+            grads[2].zero_()
+        outs = [torch.empty_like(g) for g in grads]
+        full = float(np.sqrt(sum(float(g.double().square().sum()) for g in grads)))
+        norm, ref = tail.grad_clip([g.double().cpu().numpy() for g in grads], 0.25 * full)
+        s = GradSet(grads, outs)
+        got = s.clip(0.25 * full)
+        assert abs(float(s.norm()) - norm) <= 11 * U * norm and abs(float(got) - norm) <= 11 * U * norm
+        half, low = (2.0 ** -8, 2.0 ** -134) if kind == BF else (U, 2.0 ** -150)
+        for o, r in zip(outs, ref):
+            assert np.all(np.abs(o.double().cpu().numpy() - r) <= (half + 14 * U) * np.abs(r) + low)
+
+
+def test_small_values_next_to_large_ones():
+    """A block of tiny values beside one whose squares are ordinary: the norm is the latter's."""
+    grads = [*_grads([300_000], [F32], 7, 1e-30), *_grads([300_000], [BF], 8)]
+    _check(grads, [torch.empty_like(g) for g in grads], 1.0)
+
