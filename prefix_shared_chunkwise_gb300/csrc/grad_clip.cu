@@ -276,8 +276,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __gr
     if (threadIdx.x < 32) {
         const double norm = norm_of(s.part, s.partials);
         if (threadIdx.x == 0) {
-            s_f = norm > s.max_norm && isfinite(norm) ? static_cast<float>(s.max_norm / norm) : 1.f;
-            if (blockIdx.x == 0 && s.first == 0) *s.norm = static_cast<float>(norm);
+            const float told = static_cast<float>(norm);     // what the caller sees decides
+            s_f = norm > s.max_norm && isfinite(told) ? static_cast<float>(s.max_norm / norm) : 1.f;
+            if (blockIdx.x == 0 && s.first == 0) *s.norm = told;
         }
     }
     __syncthreads();

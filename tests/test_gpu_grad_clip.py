@@ -153,3 +153,13 @@ def test_small_values_next_to_large_ones():
     grads = [*_grads([300_000], [F32], 7, 1e-30), *_grads([300_000], [BF], 8)]
     _check(grads, [torch.empty_like(g) for g in grads], 1.0)
 
+
+
+def test_norm_beyond_fp32():
+    """Finite values whose norm fp32 does not hold: *norm is infinite, and the gradients pass
+    unscaled, as with every norm that is not finite."""
+    grads = [torch.full((5000,), 3e38, device="cuda"), torch.ones(9, device="cuda", dtype=BF)]
+    outs = [torch.zeros_like(g) for g in grads]
+    n = GradSet(grads, outs).clip(1.0)
+    torch.cuda.synchronize()
+    assert torch.isinf(n) and all(torch.equal(o, g) for o, g in zip(outs, grads))
