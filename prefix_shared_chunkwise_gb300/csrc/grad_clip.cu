@@ -410,7 +410,7 @@ extern "C" {
 
 size_t harts_grad_workspace_bytes(int32_t count) {
     if (count < 0) return 0;
-    const size_t sets = std::max(1, (count + kSet - 1) / kSet);
+    const size_t sets = std::max<int64_t>(1, (int64_t(count) + kSet - 1) / kSet);
     return std::max<size_t>(256, sets * grid_limit() * sizeof(double));
 }
 

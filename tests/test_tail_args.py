@@ -159,3 +159,12 @@ def test_linear_logprob_positions_up_to_the_last_step_of_an_index():
         return L.lib().harts_linear_logprob_fwd(ctypes.byref(a), None)
     assert call((1 << 31) - 256) == ESMALLBUF
     assert call((1 << 31) - 255) == EOVERFLOW and call((1 << 31) - 1) == EOVERFLOW
+
+
+def test_grad_workspace_of_the_most_tensors():
+    """A partial sum for each block of each launch of 512 tensors, whatever the count."""
+    nb = L.lib().harts_grad_workspace_bytes
+    per = nb(512)
+    assert per > 256 and nb(513) == 2 * per
+    for count in ((1 << 31) - 1, (1 << 31) - 511, 1 << 30):
+        assert nb(count) == (count + 511) // 512 * per
