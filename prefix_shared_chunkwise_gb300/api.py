@@ -28,8 +28,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, t=None):
+    """The raw handle of the given stream, or of the current one.  `t`: a tensor of the call,
+    see _stream_on."""
     import torch
+    if t is not None and t.is_cuda:
+        return ctypes.c_void_p(_stream_on(stream, t))
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -87,14 +91,14 @@ class Plan:
         import torch
         nb = self.device_bytes()
         buf = torch.empty(nb, dtype=torch.uint8, device=device)
-        L.check(L.lib().harts_plan_upload(self._h, _ptr(buf), nb, _stream(stream)),
+        L.check(L.lib().harts_plan_upload(self._h, _ptr(buf), nb, _stream(stream, buf)),
                 "harts_plan_upload")
         self._dev = buf
         return self
 
     def device_error(self, stream=None) -> int:
         code = ctypes.c_int32(0)
-        rc = L.lib().harts_plan_device_error(self._h, _stream(stream), ctypes.byref(code))
+        rc = L.lib().harts_plan_device_error(self._h, _stream(stream, self._dev), ctypes.byref(code))
         if rc not in (0, -7):
             L.check(rc, "harts_plan_device_error")
         return code.value
@@ -163,7 +167,7 @@ def kda_fwd(plan: Plan, q, k, v, g, beta, *, o=None, states=None, final_state=No
     if states is None and info["n_states"] > 0:
         states = torch.empty((info["n_states"], H, dk, dv), dtype=torch.float32, device=dev)
     a = _fwd_args(plan, q, k, v, g, beta, o, states, final_state, h0, chunk_states, scale, kernel)
-    L.check(L.lib().harts_kda_fwd(plan.handle, ctypes.byref(a), _stream(stream)), "harts_kda_fwd")
+    L.check(L.lib().harts_kda_fwd(plan.handle, ctypes.byref(a), _stream(stream, q)), "harts_kda_fwd")
     return o, states, final_state, chunk_states
 
 
@@ -203,7 +207,7 @@ def kda_bwd(plan: Plan, q, k, v, g, beta, d_o, *, states, chunk_states, d_final=
     a.workspace_bytes = 0 if workspace is None else workspace.numel()
     fn = {"all": "harts_kda_bwd", "state": "harts_kda_bwd_state", "grad": "harts_kda_bwd_grad",
           "static": "harts_kda_bwd_static"}[phase]
-    L.check(getattr(L.lib(), fn)(plan.handle, ctypes.byref(a), _stream(stream)), fn)
+    L.check(getattr(L.lib(), fn)(plan.handle, ctypes.byref(a), _stream(stream, q)), fn)
     if dh0 is not None:
         grads["dh0"] = dh0
     return grads
@@ -229,7 +233,7 @@ def conv_fwd(plan: Plan, x, weight, bias=None, *, activation="none", y=None, str
     if y is None:
         y = torch.empty_like(x)
     a = _conv_args(x, weight, bias, y, activation)
-    L.check(L.lib().harts_conv_fwd(plan.handle, ctypes.byref(a), _stream(stream)), "harts_conv_fwd")
+    L.check(L.lib().harts_conv_fwd(plan.handle, ctypes.byref(a), _stream(stream, x)), "harts_conv_fwd")
     return y
 
 
@@ -251,7 +255,7 @@ def conv_bwd(plan: Plan, x, weight, bias, dy, *, activation="none", dx=None, dwe
     b.dy, b.dx, b.dweight = dy.data_ptr(), dx.data_ptr(), dweight.data_ptr()
     b.dbias = None if dbias is None else dbias.data_ptr()
     b.workspace, b.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    L.check(L.lib().harts_conv_bwd(plan.handle, ctypes.byref(b), _stream(stream)), "harts_conv_bwd")
+    L.check(L.lib().harts_conv_bwd(plan.handle, ctypes.byref(b), _stream(stream, x)), "harts_conv_bwd")
     return dx, dweight, dbias
 
 
@@ -287,7 +291,7 @@ def logprob_fwd(logits, row_ptr, row_sem, target, *, lse=None, logp=None, stream
     if logp is None:
         logp = torch.empty(target.numel(), dtype=torch.float32, device=logits.device)
     a = _lp_args(logits, row_ptr, row_sem, target, lse, logp)
-    L.check(L.lib().harts_logprob_fwd(ctypes.byref(a), _stream(stream)), "harts_logprob_fwd")
+    L.check(L.lib().harts_logprob_fwd(ctypes.byref(a), _stream(stream, logits)), "harts_logprob_fwd")
     return logp, lse
 
 
@@ -299,7 +303,7 @@ def logprob_bwd(logits, row_ptr, row_sem, target, lse, dlogp, *, dlogits=None, s
     b = L.LogprobBwdArgs()
     b.fwd = _lp_args(logits, row_ptr, row_sem, target, lse, None)
     b.dlogp, b.dlogits = dlogp.data_ptr(), dlogits.data_ptr()
-    L.check(L.lib().harts_logprob_bwd(ctypes.byref(b), _stream(stream)), "harts_logprob_bwd")
+    L.check(L.lib().harts_logprob_bwd(ctypes.byref(b), _stream(stream, logits)), "harts_logprob_bwd")
     return dlogits
 
 
@@ -316,7 +320,7 @@ def attn_fwd(plan: Plan, q, k, v, *, scale=None, o=None, lse=None, stream=None):
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
     a = _attn_args(q, k, v, o, lse, scale)
-    L.check(L.lib().harts_attn_fwd(plan.handle, ctypes.byref(a), _stream(stream)), "harts_attn_fwd")
+    L.check(L.lib().harts_attn_fwd(plan.handle, ctypes.byref(a), _stream(stream, q)), "harts_attn_fwd")
     return o, lse
 
 
@@ -347,19 +351,23 @@ def attn_bwd(plan: Plan, q, k, v, o, lse, d_o, *, scale=None, dq=None, dk=None, 
         workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=q.device)
     b.d_o, b.dq, b.dk, b.dv = d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
     b.workspace, b.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    L.check(L.lib().harts_attn_bwd(plan.handle, ctypes.byref(b), _stream(stream)), "harts_attn_bwd")
+    L.check(L.lib().harts_attn_bwd(plan.handle, ctypes.byref(b), _stream(stream, q)), "harts_attn_bwd")
     return dq, dk, dv
 
 
 def _stream_on(stream, t):
     """The raw handle of the given stream, or of the current one of `t`'s device (without
-    building a Stream object: this runs in every call, some of which take a few us)."""
+    building a Stream object: this runs in every call, some of which take a few us).  The library
+    launches on the current device: tensors and streams of another one are refused."""
     if not t.is_cuda:
         raise ValueError(f"tensors are on {t.device}, expected a CUDA device")
-    if stream is not None:
-        return stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    dev, now = t.get_device(), torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, tensors are on cuda:{dev}")
+    if dev != now:
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{now} (torch.cuda.device)")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _made_on_stream(call):

@@ -97,3 +97,26 @@ def test_buffers_of_a_call_belong_to_its_stream():
     there = calls(torch.cuda.Stream())
     for a, b in zip(here, there):
         assert torch.equal(a, b)
+
+
+def test_every_entry_point_asks_for_the_current_device(monkeypatch):
+    """With another device current (by its name only: one GPU is enough) no entry point launches."""
+    from prefix_shared_chunkwise_gb300 import api
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, w, i = torch.zeros(4, 64, **bf), torch.zeros(64, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    head, f4, f5 = torch.zeros(10, 64, **bf), torch.zeros(4, device="cuda"), torch.zeros(5, device="cuda")
+    q = torch.zeros(4, 1, 128, **bf)
+    pl = api.Plan(np.array([-1], np.int32), np.array([4], np.int64), 64).upload()
+    grads = api.GradSet([w])
+    calls = [lambda: api.rmsnorm_fwd(x, w), lambda: api.rmsnorm_bwd(x, x, w, f4), lambda: grads.norm(),
+             lambda: grads.clip(1.0), lambda: api.GradSet([w]), lambda: api.linear_logprob_fwd(x, head, i, i, i),
+             lambda: api.linear_logprob_bwd(x, head, i, i, i, f4, f5), lambda: api.logprob_fwd(x, i, i, i),
+             lambda: api.logprob_bwd(x, i, i, i, f4, f5), lambda: api.attn_fwd(pl, q, q, q),
+             lambda: api.attn_bwd(pl, q, q, q, q, f4.view(4, 1), q),
+             lambda: api.conv_fwd(pl, x, torch.zeros(64, 4, device="cuda")),
+             lambda: api.conv_bwd(pl, x, torch.zeros(64, 4, device="cuda"), None, x),
+             lambda: api.kda_fwd(pl, q, q, q, q, q[:, :, 0].contiguous()), lambda: pl.device_error(), lambda: pl.upload()]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            call()

@@ -168,3 +168,39 @@ def test_grad_workspace_of_the_most_tensors():
     assert per > 256 and nb(513) == 2 * per
     for count in ((1 << 31) - 1, (1 << 31) - 511, 1 << 30):
         assert nb(count) == (count + 511) // 512 * per
+
+
+class _Tensor:
+    """What the choice of a stream asks of a tensor, without a GPU."""
+    is_cuda, device = True, "cuda:1"
+
+    def get_device(self):
+        return 1
+
+
+class _Stream:
+    cuda_stream = 77
+
+    def __init__(self, device_index):
+        self.device_index = device_index
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """Kernels start on the current device: with tensors or a stream of another one they would run
+    there, on the wrong GPU's addresses."""
+    from prefix_shared_chunkwise_gb300 import api
+    t, now = _Tensor(), [1]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    for stream_of in (api._stream_on, lambda s, t: api._stream(s, t).value):
+        now[0] = 1
+        assert stream_of(None, t) == 101 and stream_of(_Stream(1), t) == 77
+        with pytest.raises(ValueError, match="stream is on cuda:0"):
+            stream_of(_Stream(0), t)
+        now[0] = 0
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            stream_of(None, t)
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            stream_of(_Stream(1), t)
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        api._stream_on(None, torch.zeros(1))
