@@ -450,7 +450,8 @@ int harts_attn_bwd(const harts_plan *plan, const harts_attn_bwd_args *args, hart
  * 8-bit output holds y as e4m3 values with one power-of-two scale (e8m0: 2^(byte - 127))
  * per 32 channels, the smallest that keeps the block within 448; a block that holds an
  * infinity gets scale 255 (NaN), a NaN stays one.  h may be x or residual, and y may be x
- * (rows are read before they are written).
+ * (rows are read before they are written), but not both x.  The backward wants h: without a
+ * residual and with y over x, give one.
  */
 typedef struct {
     int64_t C;               /* rows, >= 0 */

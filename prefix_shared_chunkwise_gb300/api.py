@@ -397,10 +397,11 @@ def _ready(name, t, shape, dtype, device):
 @_made_on_stream
 def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None, rstd=None, stream=None):
     """harts_rmsnorm_fwd: h = x + residual, y = h / sqrt(mean h^2 + eps) * weight per row.
-    x, residual: [C, D] bf16 or fp32; weight: [D] fp32.  Returns (y, h, rstd [C] fp32); h is
-    x itself where there is no residual.  mx8=True returns y as (values [C, D] float8_e4m3fn,
-    scales [C, D/32] float8_e8m0fnu) instead; D is then a multiple of 32.  h may be given as
-    x or residual, y as x (in place)."""
+    x, residual: [C, D] bf16 or fp32; weight: [D] fp32.  Returns (y, h, rstd [C] fp32).  mx8=True
+    returns y as (values [C, D] float8_e4m3fn, scales [C, D/32] float8_e8m0fnu) instead; D is
+    then a multiple of 32.  h may be given as x or residual, y as x (in place).  Without a
+    residual a given h receives x; with none given, h is x itself, or None where y is written
+    over it (nothing is left for the backward)."""
     import torch
     shape, dt, dev, f32 = x.shape, x.dtype, x.device, torch.float32
     if len(shape) != 2:
@@ -426,14 +427,16 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, mx8=False, y=None, h=None
         else:
             _ready("y", y, shape, dt, dev)
         y_ptr = y.data_ptr()
+    if h is not None:
+        _ready("h", h, shape, dt, dev)
+        h_ptr = h.data_ptr()
     if residual is not None:
         _ready("residual", residual, shape, dt, dev)
         if h is None:
             h = torch.empty_like(x)
-        else:
-            _ready("h", h, shape, dt, dev)
-        res_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
-    else:
+            h_ptr = h.data_ptr()
+        res_ptr = residual.data_ptr()
+    elif h is None and (C == 0 or y_ptr != x.data_ptr()):
         h = x
     if rstd is None:
         rstd = torch.empty(C, dtype=f32, device=dev)

@@ -685,6 +685,7 @@ int harts_rmsnorm_fwd(const harts_rmsnorm_fwd_args *a, harts_stream_t stream) {
     if (!a->x || !a->weight) { set_error("NULL x or weight"); return HARTS_EINVAL; }
     if (!a->y && !a->y8) { set_error("no output: y and y8 are both NULL"); return HARTS_EINVAL; }
     if (a->residual && !a->h) { set_error("h is required with a residual"); return HARTS_EINVAL; }
+    if (a->h && a->h == a->y) { set_error("h and y are one buffer"); return HARTS_EINVAL; }
     if ((a->y8 == nullptr) != (a->y8_scale == nullptr)) { set_error("y8 and y8_scale go together"); return HARTS_EINVAL; }
     if (a->y8 && a->D % kMxBlock) { set_error("the 8-bit output needs D a multiple of 32"); return HARTS_EUNSUPPORTED; }
     if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->h) || !aligned16(a->y) ||

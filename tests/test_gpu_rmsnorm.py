@@ -190,3 +190,29 @@ def test_no_rows_and_in_place_and_stream():
     dx, dw = rmsnorm_bwd(d, h, w, rstd, dh)
     dx2, dw2 = rmsnorm_bwd(d, h, w, rstd, dh, dx=dh)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_h_without_a_residual(dtype):
+    """A given h receives x, and is what the call returns: the backward of a norm in place (y over
+    x) is then the one of a norm that kept x."""
+    td, _ = DT[dtype]
+    x, w, dy = _rand((37, 264), td, 1), _rand((264,), torch.float32, 2), _rand((37, 264), td, 3)
+    y, h, rstd = rmsnorm_fwd(x, w)
+    assert h is x
+    want = rmsnorm_bwd(dy, h, w, rstd)
+    own, keep = x.clone(), torch.full_like(x, 7)
+    y2, h2, rstd2 = rmsnorm_fwd(own, w, h=keep, y=own)
+    torch.cuda.synchronize()
+    assert h2 is keep and torch.equal(keep, x) and torch.equal(y2, y) and y2 is own
+    got = rmsnorm_bwd(dy, h2, w, rstd2)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    (q, s), h3, _ = rmsnorm_fwd(x[:, :256].contiguous(), w[:256].contiguous(), mx8=True, h=keep[:, :256].contiguous())
+    assert torch.equal(h3, x[:, :256])
+    inplace = x.clone()
+    y4, h4, _ = rmsnorm_fwd(inplace, w, y=inplace)                  # nothing left to differentiate from
+    assert h4 is None and torch.equal(y4, y)
+    with pytest.raises(RuntimeError, match="one buffer"):
+        rmsnorm_fwd(x, w, keep, h=own, y=own)
+    none = x[:0]
+    assert rmsnorm_fwd(none, w)[1] is none

@@ -204,3 +204,9 @@ def test_other_devices_are_refused(monkeypatch):
             stream_of(_Stream(1), t)
     with pytest.raises(ValueError, match="expected a CUDA device"):
         api._stream_on(None, torch.zeros(1))
+
+
+def test_rmsnorm_fwd_refuses_one_buffer_for_both_outputs():
+    for residual in (None, P):
+        a = _args(L.RmsnormFwdArgs, NORM, x=2 * P, residual=residual, h=P, y=P)
+        assert L.lib().harts_rmsnorm_fwd(ctypes.byref(a), None) == EINVAL
