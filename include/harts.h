@@ -19,7 +19,9 @@
  *    caller.  The library never allocates device memory and never frees caller memory.
  *  - Work is enqueued on the given stream and returns without synchronising.  Faults
  *    found by the kernels (a bad plan, out-of-range decay) are recorded in the plan's
- *    device error word; harts_plan_device_error() reads it (it synchronises).
+ *    device error word; harts_plan_device_error() reads it (it synchronises).  Calls
+ *    without a plan record theirs in the word that they are given, or in the library's
+ *    own, which harts_device_error() reads.
  *  - All tensors are contiguous, token-major: [rows, H, d].  Rows are compact tokens
  *    in the plan's layout (see harts_plan_arrays.seg_offset).
  *  - A plan is immutable once built; the forward and the backward pass reuse the same
@@ -156,11 +158,16 @@ int harts_plan_device_error(harts_plan *plan, harts_stream_t stream, int32_t *co
 
 void harts_plan_free(harts_plan *plan);
 
+/* The same for the library's own error word on the current device, in which calls without a plan
+ * and without a word of their own record a bounded wait that ran out (code 3: the outputs are
+ * incomplete).  Calls on other streams report there too. */
+int harts_device_error(harts_stream_t stream, int32_t *code);
+
 /* Self-test of the device failure path (for tests of error reporting): one thread waits on
  * a barrier that nothing completes, gives up after max_cycles SM cycles (1 .. 1e8) and
- * records device code 3 (timeout) in the plan's error word, the way every kernel of the
- * library reports a wait that ran out; harts_plan_device_error then returns HARTS_EDEVICE
- * and the context stays usable.  Never traps.  Errors: HARTS_EINVAL, HARTS_ENOPLAN,
+ * records device code 3 (timeout) in the plan's error word (plan NULL: in the library's own),
+ * the way every kernel of the library reports a wait that ran out; harts_plan_device_error
+ * (harts_device_error) then returns HARTS_EDEVICE and the context stays usable.  Never traps.  Errors: HARTS_EINVAL, HARTS_ENOPLAN,
  * HARTS_ECUDA. */
 int harts_selftest_timeout(harts_plan *plan, uint32_t max_cycles, harts_stream_t stream);
 
@@ -484,8 +491,8 @@ typedef struct {
     const float *rstd;       /* device [C] from the forward */
     void *dx;                /* device [C][D] output: dL/dx = dL/dresidual; may be dy or dh */
     float *dweight;          /* device [D] output (overwritten; zero when C is 0) */
-    int32_t *error;          /* device [1], or NULL: set to 3 if a bounded wait ran out; cleared by
-                                the caller */
+    int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out; cleared by the caller.
+                                NULL: the library's own word (harts_device_error) */
     void *workspace;         /* device, harts_rmsnorm_bwd_workspace_bytes, 16-byte aligned */
     size_t workspace_bytes;
 } harts_rmsnorm_bwd_args;
@@ -564,8 +571,9 @@ typedef struct {
     const int32_t *target;   /* device [S] label of each semantic position */
     float *lse;              /* device [C]: written by the forward, read by the backward */
     float *logp;             /* device [S]: written by the forward */
-    int32_t *error;          /* device [1], or NULL: set to 3 if a bounded wait ran out (the
-                                outputs are then incomplete); cleared by the caller */
+    int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out (the outputs are then
+                                incomplete); cleared by the caller.  NULL: the library's own word
+                                (harts_device_error) */
     void *workspace;         /* device, harts_linear_logprob_{fwd,bwd}_workspace_bytes, 256-byte aligned */
     size_t workspace_bytes;
 } harts_linear_logprob_fwd_args;

@@ -30,7 +30,8 @@ EXPORTED = [
     "harts_rmsnorm_fwd", "harts_rmsnorm_bwd_workspace_bytes", "harts_rmsnorm_bwd",
     "harts_grad_workspace_bytes", "harts_grad_norm", "harts_grad_clip",
     "harts_linear_logprob_fwd_workspace_bytes", "harts_linear_logprob_fwd",
-    "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_last_error",
+    "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_device_error",
+    "harts_last_error",
 ]
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
@@ -204,6 +205,8 @@ def lib():
         L.harts_linear_logprob_bwd_workspace_bytes.restype = _sz
         L.harts_linear_logprob_bwd.argtypes = [ctypes.POINTER(LinearLogprobBwdArgs), _vp]
         L.harts_linear_logprob_bwd.restype = ctypes.c_int
+        L.harts_device_error.argtypes = [_vp, ctypes.POINTER(_i32)]
+        L.harts_device_error.restype = ctypes.c_int
         L.harts_last_error.argtypes = []
         L.harts_last_error.restype = ctypes.c_char_p
         for fn in ("harts_plan_calls", "harts_plan_get_info", "harts_plan_export",

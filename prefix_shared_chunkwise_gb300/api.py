@@ -12,7 +12,7 @@ from . import _lib as L
 
 __all__ = ["Plan", "kda_fwd", "kda_bwd", "conv_fwd", "conv_bwd", "semantic_map", "logprob_fwd",
            "logprob_bwd", "attn_fwd", "attn_bwd", "linear_logprob_fwd", "linear_logprob_bwd",
-           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "dtype_code"]
+           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "device_error", "dtype_code"]
 
 
 def dtype_code(torch_dtype):
@@ -108,6 +108,17 @@ class Plan:
 
     def bwd_workspace_bytes(self, H, dk, dv):
         return int(L.lib().harts_kda_bwd_workspace_bytes(self._h, H, dk, dv))
+
+
+def device_error(stream=None) -> int:
+    """harts_device_error: waits for the stream; the code that a call without a plan and without
+    an error word of its own left on the current device (3: a bounded wait ran out, its outputs are
+    incomplete), or 0.  Reading clears it."""
+    code = ctypes.c_int32(0)
+    rc = L.lib().harts_device_error(_stream(stream), ctypes.byref(code))
+    if rc not in (0, -7):
+        L.check(rc, "harts_device_error")
+    return code.value
 
 
 def _need(name, t, shape=None, dtype=None, nbytes=None, device=None):
@@ -570,7 +581,8 @@ def linear_logprob_fwd(x, weight, row_ptr, row_sem, target, *, scale=1.0, lse=No
     """harts_linear_logprob_fwd: log-probabilities of the semantic positions from hidden rows
     x [C, D] and the vocabulary weight [V, D] (bf16), without forming the logits in memory.
     A target outside 0 .. V-1 has no label (logp 0).  Returns (logp [S] fp32, lse [C] fp32).
-    error: int32 device tensor that a bounded wait which ran out sets to 3."""
+    error: int32 device tensor that a bounded wait which ran out sets to 3; None: the library's own
+    word, see device_error()."""
     import torch
     C, V, D, S = _head_checks(x, weight, row_ptr, row_sem, target, error)
     dev, f32 = x.device, torch.float32

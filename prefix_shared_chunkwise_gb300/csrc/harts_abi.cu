@@ -1,8 +1,10 @@
 // C ABI entry points that touch the device: plan upload, forward and backward dispatch.
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
 #include "kda_common.cuh"
+#include "launch_util.h"
 #include "tc_primitives.cuh"
 
 namespace harts {
@@ -105,17 +107,36 @@ namespace {
 
 // The library's bounded-wait failure path, on its own: one thread waits on an mbarrier
 // that nothing completes, gives up after max_cycles and records device code 3 (timeout)
-// in the plan's error word, as every kernel of the library does when a wait runs out.
-__global__ void selftest_timeout_kernel(PlanDev pd, uint32_t max_cycles) {
+// in the plan's error word (`own`: in that one), as every kernel of the library does when a
+// wait runs out.
+__global__ void selftest_timeout_kernel(PlanDev pd, int32_t *own, uint32_t max_cycles) {
     __shared__ uint64_t bar;
     if (threadIdx.x == 0) {
         tc::mbar_init(&bar, 1);
         tc::fence_mbar_init();
-        if (!tc::mbar_wait(&bar, 0, static_cast<long long>(max_cycles))) dev_error(pd, kDevErrTimeout, -1, -1);
+        if (!tc::mbar_wait(&bar, 0, static_cast<long long>(max_cycles))) {
+            if (own) atomicCAS(own, 0, static_cast<int>(kDevErrTimeout));
+            else dev_error(pd, kDevErrTimeout, -1, -1);
+        }
     }
 }
 
+__device__ int32_t g_error_word;
+
 }  // namespace
+
+int32_t *own_error_word() {
+    static std::atomic<int32_t *> known[kMaxDeviceIds];
+    const int dev = current_device();
+    int32_t *p = dev < kMaxDeviceIds ? known[dev].load(std::memory_order_relaxed) : nullptr;
+    if (p) return p;
+    void *at = nullptr;
+    if (cudaGetSymbolAddress(&at, g_error_word) != cudaSuccess) return nullptr;
+    p = static_cast<int32_t *>(at);
+    if (dev < kMaxDeviceIds) known[dev].store(p, std::memory_order_relaxed);
+    return p;
+}
+
 }  // namespace harts
 
 extern "C" {
@@ -179,11 +200,29 @@ int harts_plan_device_error(harts_plan *P, harts_stream_t stream, int32_t *code)
     return HARTS_OK;
 }
 
+int harts_device_error(harts_stream_t stream, int32_t *code) {
+    cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "sync");
+    int32_t *word = own_error_word(), host = 0;
+    if (!word) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
+    e = cudaMemcpy(&host, word, sizeof(host), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, "read error word");
+    if (code) *code = host;
+    if (host != 0) {
+        cudaMemset(word, 0, sizeof(host));
+        set_error("device error " + std::to_string(host));
+        return HARTS_EDEVICE;
+    }
+    set_error("");
+    return HARTS_OK;
+}
+
 int harts_selftest_timeout(harts_plan *P, uint32_t max_cycles, harts_stream_t stream) {
-    if (!P) { set_error("NULL plan"); return HARTS_EINVAL; }
-    if (!P->dev) { set_error("plan not uploaded"); return HARTS_ENOPLAN; }
+    if (P && !P->dev) { set_error("plan not uploaded"); return HARTS_ENOPLAN; }
     if (max_cycles == 0 || max_cycles > 100000000u) { set_error("max_cycles must be in 1 .. 1e8"); return HARTS_EINVAL; }
-    selftest_timeout_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P->view, max_cycles);
+    int32_t *own = P ? nullptr : own_error_word();
+    if (!P && !own) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
+    selftest_timeout_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P ? P->view : PlanDev{}, own, max_cycles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
     set_error("");

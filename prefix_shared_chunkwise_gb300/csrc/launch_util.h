@@ -41,6 +41,10 @@ inline cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done)
     return e;
 }
 
+// The library's own error word on the current device, for calls that are given none
+// (harts_device_error reads it); nullptr where it cannot be had.
+int32_t *own_error_word();
+
 // The kernels of one call overlap at their seams: each allows the next one to be set up as
 // soon as it runs itself, and waits for its predecessor only where it first needs (or
 // overwrites) something of it.  The first kernel of a call is launched without this, so what

@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tile_kernel(const __grid_con
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (tid == 0 && failed(&s_fail) && p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
+    if (tid == 0 && failed(&s_fail)) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
     if (G == 2) cluster_sync();                         // neither block ends under the other's copies or arrivals
     tc::fence_after_sync();
     if (warp == 2) pair_dealloc<G>(tm);
@@ -1364,7 +1364,8 @@ int harts_linear_logprob_fwd(const harts_linear_logprob_fwd_args *a, harts_strea
     q.rows = static_cast<int32_t>(a->C);
     q.cols = a->V;
     p.n_prod = 1;
-    p.error = a->error;
+    p.error = a->error ? a->error : own_error_word();
+    if (!p.error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     p.c2 = logit_factor(a->scale, a->D);
     const bool pad = pads_x(a->C, a->D, false);
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a->workspace) + (pad ? pad_bytes(a->C, a->D) : 0));
@@ -1437,6 +1438,8 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
     const int32_t mt = ceil_div(f.C, kTM * G), C = static_cast<int32_t>(f.C);
     const int32_t a_rows = static_cast<int32_t>(std::min<int64_t>(kTM, (f.C + 7) / 8 * 8));
     const int32_t dz_box = b.twin ? 2 * kTwin : a_rows;
+    int32_t *error = f.error ? f.error : own_error_word();
+    if (!error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     Params pz, pg;
     std::memset(&pz, 0, sizeof(pz));
     std::memset(&pg, 0, sizeof(pg));
@@ -1457,7 +1460,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         z.m_tiles = mt; z.n = b.n_dz; z.n_tiles = ceil_div(nv, b.n_dz); z.splits = 1;
         z.k_blocks = z.k_per = ceil_div(f.D, kTK);
         z.a_panel = pad; z.a_rows = a_rows; z.b_y0 = v0; z.out_y0 = 0; z.rows = C; z.cols = nv;
-        pz.n_prod = 1; pz.error = f.error; pz.c2 = logit_factor(f.scale, f.D);
+        pz.n_prod = 1; pz.error = error; pz.c2 = logit_factor(f.scale, f.D);
         pz.rows = s.rows; pz.ent_y = s.ent_y; pz.ent_v = s.ent_v; pz.v0 = v0; pz.twin = b.twin;
         cudaError_t e = launch_tiles<kDz>(pz, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
@@ -1469,7 +1472,7 @@ int harts_linear_logprob_bwd(const harts_linear_logprob_bwd_args *a, harts_strea
         gw.a_mn = gw.b_mn = 1; gw.m_tiles = ceil_div(nv, kTM * G); gw.n = b.n_grad; gw.n_tiles = ceil_div(f.D, b.n_grad);
         gw.k_blocks = gw.k_per = ceil_div(b.dz_rows, kTK); gw.splits = 1;
         gw.out_y0 = v0; gw.rows = nv; gw.cols = f.D; gw.fast_n = 1;
-        pg.n_prod = 2; pg.error = f.error;
+        pg.n_prod = 2; pg.error = error;
         e = launch_tiles<kGrad>(pg, G, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "linear log-prob backward launch");
     }

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(R) rmsnorm_bwd_ring_kernel(NormBwd p, int stag
         if (tc::mbar_try(&full[s], phase) || *reinterpret_cast<volatile int *>(&s_fail)) return;
         if (!tc::mbar_wait(&full[s], phase)) {
             *reinterpret_cast<volatile int *>(&s_fail) = 1;
-            if (p.error) atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
+            atomicCAS(p.error, 0, static_cast<int>(kDevErrTimeout));
         }
     };
     if (t == 0) {
@@ -733,7 +733,9 @@ int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *a, harts_stream_t stream) {
     }
     NormBwd p;
     p.dy = a->dy; p.h = a->h; p.dh = a->dh; p.w = a->weight; p.rstd = a->rstd; p.dx = a->dx;
-    p.part = static_cast<float *>(a->workspace); p.error = a->error; p.C = a->C; p.D = a->D;
+    p.part = static_cast<float *>(a->workspace); p.C = a->C; p.D = a->D;
+    p.error = a->error ? a->error : own_error_word();
+    if (!p.error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     int64_t groups = 0;
     const Shape s = shape_of(a->dtype, a->D, true);
     cudaError_t e = a->dtype == HARTS_BF16 ? run_bwd<__nv_bfloat16, 8>(s, p, &groups, st) : run_bwd<float, 4>(s, p, &groups, st);

@@ -120,3 +120,48 @@ def test_every_entry_point_asks_for_the_current_device(monkeypatch):
     for call in calls:
         with pytest.raises(ValueError, match="current device is cuda:1"):
             call()
+
+
+def test_a_wait_that_ran_out_is_not_lost_without_an_error_word():
+    """Calls that are given no error word report in the library's own, which says so once."""
+    from prefix_shared_chunkwise_gb300 import _lib, api
+    assert api.device_error() == 0
+    assert _lib.lib().harts_selftest_timeout(None, 2_000_000, torch.cuda.current_stream().cuda_stream) == 0
+    assert api.device_error() == 3 and api.device_error() == 0
+    gen = torch.Generator().manual_seed(6)
+    x, w = torch.randn(70, 256, generator=gen).bfloat16().cuda(), torch.randn(500, 256, generator=gen).bfloat16().cuda()
+    ptr = torch.arange(71, dtype=torch.int32).cuda()
+    logp, lse = api.linear_logprob_fwd(x, w, ptr, ptr[:70].clone(), ptr[:70].clone())
+    api.linear_logprob_bwd(x, w, ptr, ptr[:70].clone(), ptr[:70].clone(), lse, logp)
+    y, h, rstd = api.rmsnorm_fwd(x, torch.ones(256, device="cuda"))
+    api.rmsnorm_bwd(y, h, torch.ones(256, device="cuda"), rstd)
+    assert api.device_error() == 0 and torch.isfinite(lse).all()
+
+
+FIRST_CALL = """
+import sys, torch
+from prefix_shared_chunkwise_gb300.api import device_error, linear_logprob_bwd, linear_logprob_fwd
+gen = torch.Generator().manual_seed(7)
+x, w = torch.randn(70, 72, generator=gen).bfloat16().cuda(), torch.randn(500, 72, generator=gen).bfloat16().cuda()
+ptr = torch.arange(71, dtype=torch.int32).cuda()
+sem, tgt, g = ptr[:70].clone(), ptr[:70].clone(), torch.randn(70, generator=gen).cuda()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    logp, lse = linear_logprob_fwd(x, w, ptr, sem, tgt)
+    dx, dw = linear_logprob_bwd(x, w, ptr, sem, tgt, lse, g)
+graph.replay()
+torch.cuda.synchronize()
+logp2, lse2 = linear_logprob_fwd(x, w, ptr, sem, tgt)
+dx2, dw2 = linear_logprob_bwd(x, w, ptr, sem, tgt, lse2, g)
+same = [torch.equal(a, b) for a, b in ((logp, logp2), (lse, lse2), (dx, dx2), (dw, dw2))]
+sys.exit(0 if all(same) and device_error() == 0 else 1)
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """What a first call looks up (the error word, a kernel's shared memory) it finds in a capture."""
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
