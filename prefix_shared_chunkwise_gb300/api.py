@@ -38,6 +38,20 @@ def _stream(stream, t=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _made_on_stream(call):
+    """Runs `call` under the stream it is given, if any, so that the buffers it makes belong to
+    that stream: a workspace made on the current one would be handed out again, as soon as the
+    call returns, to work that does not wait for this stream's kernels."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return run
+
+
 class Plan:
     """harts_plan_calls + harts_plan_get_info / export / upload / free.
 
@@ -90,7 +104,8 @@ class Plan:
         """Allocate the plan's device tables through torch and upload them."""
         import torch
         nb = self.device_bytes()
-        buf = torch.empty(nb, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):             # None: the current one
+            buf = torch.empty(nb, dtype=torch.uint8, device=device)
         L.check(L.lib().harts_plan_upload(self._h, _ptr(buf), nb, _stream(stream, buf)),
                 "harts_plan_upload")
         self._dev = buf
@@ -164,6 +179,7 @@ def _fwd_args(plan, q, k, v, g, beta, o, states, final_state, h0, chunk_states, 
     return a
 
 
+@_made_on_stream
 def kda_fwd(plan: Plan, q, k, v, g, beta, *, o=None, states=None, final_state=None, h0=None,
             chunk_states=None, scale=1.0, kernel=L.HARTS_KERNEL_AUTO, stream=None):
     """harts_kda_fwd.  Allocates any missing output through torch; returns
@@ -182,6 +198,7 @@ def kda_fwd(plan: Plan, q, k, v, g, beta, *, o=None, states=None, final_state=No
     return o, states, final_state, chunk_states
 
 
+@_made_on_stream
 def kda_bwd(plan: Plan, q, k, v, g, beta, d_o, *, states, chunk_states, d_final=None,
             h0=None, dh0=None, scale=1.0, grads=None, workspace=None,
             kernel=L.HARTS_KERNEL_AUTO, stream=None, phase="all"):
@@ -237,6 +254,7 @@ def _conv_args(x, weight, bias, y, activation):
     return a
 
 
+@_made_on_stream
 def conv_fwd(plan: Plan, x, weight, bias=None, *, activation="none", y=None, stream=None):
     """harts_conv_fwd.  x: [C, ...] compact rows (channels = the rest, flattened);
     weight: [channels, w] fp32; bias: [channels] fp32 or None.  Returns y like x."""
@@ -248,6 +266,7 @@ def conv_fwd(plan: Plan, x, weight, bias=None, *, activation="none", y=None, str
     return y
 
 
+@_made_on_stream
 def conv_bwd(plan: Plan, x, weight, bias, dy, *, activation="none", dx=None, dweight=None, dbias=None,
              workspace=None, stream=None):
     """harts_conv_bwd.  Returns (dx, dweight, dbias); dbias is None when bias is None."""
@@ -294,6 +313,7 @@ def _lp_args(logits, row_ptr, row_sem, target, lse, logp):
     return a
 
 
+@_made_on_stream
 def logprob_fwd(logits, row_ptr, row_sem, target, *, lse=None, logp=None, stream=None):
     """harts_logprob_fwd: returns (logp [S] fp32, lse [C] fp32)."""
     import torch
@@ -306,6 +326,7 @@ def logprob_fwd(logits, row_ptr, row_sem, target, *, lse=None, logp=None, stream
     return logp, lse
 
 
+@_made_on_stream
 def logprob_bwd(logits, row_ptr, row_sem, target, lse, dlogp, *, dlogits=None, stream=None):
     """harts_logprob_bwd: returns dlogits like logits."""
     import torch
@@ -318,6 +339,7 @@ def logprob_bwd(logits, row_ptr, row_sem, target, lse, dlogp, *, dlogits=None, s
     return dlogits
 
 
+@_made_on_stream
 def attn_fwd(plan: Plan, q, k, v, *, scale=None, o=None, lse=None, stream=None):
     """harts_attn_fwd: branch attention over the compact layout.  q, k, v: [C, H, d]
     bf16 (d = 128).  Returns (o [C, H, d] bf16, lse [C, H] fp32)."""
@@ -345,6 +367,7 @@ def _attn_args(q, k, v, o, lse, scale):
     return a
 
 
+@_made_on_stream
 def attn_bwd(plan: Plan, q, k, v, o, lse, d_o, *, scale=None, dq=None, dk=None, dv=None, workspace=None,
              stream=None):
     """harts_attn_bwd: returns (dq, dk, dv) like q, from the forward's o and lse."""
@@ -379,20 +402,6 @@ def _stream_on(stream, t):
     if dev != now:
         raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{now} (torch.cuda.device)")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _made_on_stream(call):
-    """Runs `call` under the stream it is given, if any, so that the buffers it makes belong to
-    that stream: a workspace made on the current one would be handed out again, as soon as the
-    call returns, to work that does not wait for this stream's kernels."""
-    @functools.wraps(call)
-    def run(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        import torch
-        with torch.cuda.stream(stream):
-            return call(*args, stream=stream, **kw)
-    return run
 
 
 def _ready(name, t, shape, dtype, device):
