@@ -1179,7 +1179,7 @@ bool map_panels(CUtensorMap *m, void *dz, int64_t C, int32_t nv, int32_t box_row
 // (the panel they lie in would reach past the last row's end) in boxes of 64 through `edge`.
 bool map_cols(CUtensorMap *m, CUtensorMap *edge, const void *base, int64_t rows, int64_t D, int32_t cols) {
     if (D % 64 && !map_in(edge, base, rows, D, D, 64)) return false;
-    if (D < 64) return true;
+    if (D < 64) { *m = *edge; return true; }            // no whole panel; a map is fetched all the same
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D / 64)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, 128};
     const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(cols / 64)};

@@ -437,3 +437,17 @@ def test_distinct_labels_of_one_row_cost_what_they_are():
 
     small, large = run(16_384), run(131_072)
     assert large <= 16 * small, (small, large)
+
+
+@pytest.mark.parametrize("C,V,D", [(300, 700, 8), (257, 515, 40), (300, 2050, 56), (140, 300, 16), (20, 300, 24)])
+def test_narrow_rows(C, V, D):
+    """Rows narrower than one panel of 64 channels, on blocks alone and on pairs."""
+    case = _case(C, V, D, 2 * C, 17)
+    x, w, sem_row, target, _ = case
+    logp, lse = _run_fwd(x, w, sem_row, target, 1.0)
+    rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target)
+    ez, el = _errors(x, w, 1.0, re)
+    assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
+    assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl))
+    _check_bwd(*case, 1.0)
+    _check_bwd(*case, 1.0, 256)
