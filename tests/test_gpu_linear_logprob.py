@@ -439,6 +439,81 @@ def test_distinct_labels_of_one_row_cost_what_they_are():
     assert large <= 16 * small, (small, large)
 
 
+def _bounds_of_the_forward(x, w, scale, lse, logp):
+    """What errors the forward's rounding makes in relative L2, for sums of products of either sign.
+    The tensor cores cut a running sum at every 16 products.  On average that takes 0.20 - 0.29 of
+    2^-24 of a logit each time, of which the factor on the logits gives 0.25 back; what is left is
+    0.05 D / 16, and a spread that grows with the root of their number.  lse is a mean of logits, to
+    which exponentials and sums add some 8 roundings; a position's own logit is an fp32 sum in chains
+    of D / 64, whose roundings mostly cancel."""
+    D, u = x.shape[1], 2.0 ** -24
+    z = np.abs(scale * (x.double().numpy() @ w.double().numpy().T)).max()
+    rms = lambda a: np.sqrt(np.mean(np.square(a)))
+    e = (0.05 * D / 16 + (D / 16) ** 0.5) * u * z + 8 * u
+    own = ((D / 64) ** 0.5 + 8) * u * z
+    return e / rms(lse) + 2 * u, (e + own) / max(rms(logp), 1e-30) + 2 * u
+
+
+@pytest.mark.parametrize("C,V,D,S", [(1, 40_001, 256, 3), (20, 5003, 1032, 60), (129, 1000, 200, 700), (300, 2049, 1032, 900),
+                                     (777, 4099, 136, 1000), (140, 3001, 2048, 300)])
+@pytest.mark.parametrize("scale", [1.0, -0.625])
+def test_forward_in_relative_l2(C, V, D, S, scale):
+    """Beside the bound on each element, which adds up what could go wrong, one on all of them."""
+    x, w, sem_row, target, _ = _case(C, V, D, S, 15)
+    logp, lse = _run_fwd(x, w, sem_row, target, scale)
+    rl, re = tail.linear_logprob_fwd(x.double().numpy(), w.double().numpy(), sem_row, target, scale)
+    el, ep = _bounds_of_the_forward(x, w, scale, re, rl)
+    assert rel_l2(lse.double().cpu().numpy(), re) <= el
+    assert rel_l2(logp.double().cpu().numpy(), rl) <= ep
+
+
+def _check_lse(x, w, scale, per_step):
+    """lse where every logit is off by at most `per_step` 2^-24 of the largest for each 16 channels,
+    and by the roundings of exponentials and sums."""
+    C, V, D = x.shape[0], w.shape[0], x.shape[1]
+    sem_row, target = np.arange(C), (np.arange(C) * 11) % V
+    logp, lse = _run_fwd(x, w, sem_row, target, scale)
+    x64, w64 = x.double().numpy(), w.double().numpy()
+    rl, re = tail.linear_logprob_fwd(x64, w64, sem_row, target, scale)
+    z = np.abs(scale * (x64 @ w64.T)).max(axis=1)
+    el = per_step * D / 16 * 2.0 ** -24 * z + 24 * U + U * np.abs(re)
+    assert np.all(np.abs(lse.cpu().numpy() - re) <= el)
+    own = (D / 1024 * 16 + 12) * U * abs(scale) * np.array([np.abs(x64[c]) @ np.abs(w64[target[c]]) for c in range(C)])
+    assert np.all(np.abs(logp.cpu().numpy() - rl) <= el + own + U * np.abs(rl))
+
+
+@pytest.mark.parametrize("D", [256, 4096, 16_384])
+def test_logits_that_are_exact(D):
+    """Rows with one channel, and values on a coarse grid: the tensor cores cut nothing, and the
+    factor of 1/4 2^-24 for each 16 channels that expects them to is all there is."""
+    gen = torch.Generator().manual_seed(D)
+    w = (torch.randn(300, D, generator=gen) * 4).bfloat16()
+    x = torch.zeros(140, D)
+    x[torch.arange(140), torch.randint(0, D, (140,), generator=gen)] = 1
+    _check_lse(x.bfloat16(), w, 1.0, 0.25)
+    grid = lambda *s: torch.randint(-2, 3, s, generator=gen).float()
+    _check_lse(grid(20, D).bfloat16(), grid(300, D).bfloat16(), 4 / D ** 0.5, 0.25)
+
+
+@pytest.mark.parametrize("D", [256, 4096, 16_384])
+def test_logits_whose_products_have_one_sign(D):
+    """Running sums that only grow are cut by less than two units of 2^-24 of the last one at every
+    16 channels, less the quarter of one that the factor gives back (which is never more than was
+    taken, but for logits that are exact)."""
+    gen = torch.Generator().manual_seed(D)
+    x, w = torch.rand(140, D, generator=gen).bfloat16(), torch.rand(300, D, generator=gen).bfloat16()
+    for scale in (32 / D, -32 / D):
+        _check_lse(x, w, scale, 2.0)
+
+
+@pytest.mark.parametrize("C,V,D,S", [(20, 2049, 136, 60), (32, 1500, 72, 100), (193, 2049, 136, 500), (300, 1793, 72, 700),
+                                     (520, 2500, 200, 900)])
+@pytest.mark.parametrize("piece", [256, 1024])
+def test_backward_in_pieces_of_other_forms(C, V, D, S, piece):
+    """Several pieces with dZ in two terms (up to 32 rows) and on pairs of blocks (from 193)."""
+    _check_bwd(*_case(C, V, D, S, 16), 0.8, piece)
+
+
 @pytest.mark.parametrize("C,V,D", [(300, 700, 8), (257, 515, 40), (300, 2050, 56), (140, 300, 16), (20, 300, 24)])
 def test_narrow_rows(C, V, D):
     """Rows narrower than one panel of 64 channels, on blocks alone and on pairs."""
@@ -451,3 +526,79 @@ def test_narrow_rows(C, V, D):
     assert np.all(np.abs(logp.cpu().numpy() - rl) <= (ez + el)[sem_row] + U * np.abs(rl))
     _check_bwd(*case, 1.0)
     _check_bwd(*case, 1.0, 256)
+
+
+@pytest.mark.parametrize("C", [1, 31, 32])
+def test_gradients_of_few_rows_are_rounded_once(C):
+    """Rows whose label's dz lies halfway between two bf16 values, the entry that makes nearly all of
+    the gradient.  In two terms dz is off by 2^-17, so that every element is the exact one rounded
+    once: within half a step of bf16, 2^(floor(log2 |ref|) - 8), and what comes before it.  That is
+    the sums (cut once for 16 products, and joined in at most 40 additions), and the softmax terms,
+    whose logits are cut at every 16 of D products of which none is larger than their sum of
+    absolute values.  In one term all elements move by 2^-8 |ref|, between half a step and a whole
+    one: those in the upper half of a power of two leave the bound."""
+    V, D = 5003, 2048
+    gen = torch.Generator().manual_seed(C)
+    x = (torch.randn(C, D, generator=gen) * 0.02).bfloat16()
+    w = torch.randn(V, D, generator=gen).bfloat16()
+    sem_row, target = np.arange(C), (np.arange(C) * 37 + 5) % V
+    x64, w64 = x.double().numpy(), w.double().numpy()
+    xa, wa = np.abs(x64), np.abs(w64)
+    rl, re = tail.linear_logprob_fwd(x64, w64, sem_row, target)
+    g = ((1 + 2.0 ** -8) / (1 - np.exp(rl))).astype(np.float32)
+    row_ptr, row_sem = _csr(sem_row, C)
+    dx, dw = linear_logprob_bwd(x.cuda(), w.cuda(), _dev(row_ptr), _dev(row_sem), _dev(target.astype(np.int32)),
+                                _dev(re.astype(np.float32)), _dev(g))
+    rdx, rdw = tail.linear_logprob_bwd(x64, w64, sem_row, target, g)
+    p = np.abs(g)[:, None] * np.exp(x64 @ w64.T - re[:, None])
+    own = np.zeros((C, V))
+    own[sem_row, target] = np.abs(g)
+    ez = D / 16 * U * (xa @ wa.T).max(axis=1) + 8 * U + U * np.abs(re)
+    off = 2.0 ** -17 * (p + own) + ez[:, None] * p + 8 * U * (p + own)
+    half = lambda ref: np.exp2(np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 8)
+    at = target.tolist()
+    for got, ref, bound in ((dx, rdx, off @ wa + (V / 16 + 40) * U * ((p + own) @ wa)),
+                            (dw[at], rdw[at], (off.T @ xa + (C / 16 + 40) * U * ((p + own).T @ xa))[at])):
+        assert np.all(np.abs(got.double().cpu().numpy() - ref) <= half(ref) + bound)
+        one = np.abs(np.float64(2.0 ** -8) * ref)           # what one term would move every element by
+        assert np.mean(one > half(ref) + bound) > 0.25
+
+
+@pytest.mark.parametrize("C,V,D,piece", [(65_676, 1300, 136, 512), (262_129, 515, 72, 0), (262_129, 520, 64, 256)])
+def test_rows_of_whole_forests(C, V, D, piece):
+    """Row counts of this framework's forests, in one piece and in several, against fp64 on the GPU.
+    The forward in relative L2 as above; gradients by two roundings to bf16 (dz and the result,
+    2^-8 each)."""
+    gen = torch.Generator(device="cuda").manual_seed(C + D)
+    x = torch.randn((C, D), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((V, D), generator=gen, device="cuda") * 2 / D ** 0.5).to(torch.bfloat16)
+    S = 2 * C
+    sem_row = (torch.rand(S, generator=gen, device="cuda").pow(1.5) * C).long().clamp(max=C - 1)
+    target = torch.randint(-1, V, (S,), generator=gen, device="cuda").to(torch.int32)
+    ptr = torch.zeros(C + 1, dtype=torch.int32, device="cuda")
+    ptr[1:] = torch.cumsum(torch.bincount(sem_row, minlength=C), 0)
+    sem = torch.argsort(sem_row, stable=True).to(torch.int32)
+    g = torch.randn(S, generator=gen, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logp, lse = linear_logprob_fwd(x, w, ptr, sem, target, error=err)
+    dx, dw = linear_logprob_bwd(x, w, ptr, sem, target, lse, g, piece=piece, error=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    z = x.double() @ w.double().t()
+    re = torch.logsumexp(z, 1)
+    keep, y = target >= 0, target.long().clamp(min=0)
+    rl = torch.where(keep, z[sem_row, y] - re[sem_row], torch.zeros_like(re[sem_row]))
+    gk = torch.where(keep, g, torch.zeros_like(g)).double()
+    G = torch.zeros(C, dtype=torch.float64, device="cuda").index_add_(0, sem_row, gk)
+    zmax = float(z.abs().max())
+    dz = torch.exp(z - re[:, None]).mul_(-G[:, None])
+    del z
+    dz.index_put_((sem_row, y), gk, accumulate=True)
+    u = 2.0 ** -24
+    e = (0.05 * D / 16 + (D / 16) ** 0.5) * u * zmax + 8 * u
+    own = ((D / 64) ** 0.5 + 8) * u * zmax
+    rel = lambda a, b: float((a.double() - b).norm() / b.norm())
+    assert rel(lse, re) <= e / float(re.square().mean().sqrt()) + 2 * u
+    assert rel(logp, rl) <= (e + own) / float(rl.square().mean().sqrt()) + 2 * u
+    assert rel(dx, dz @ w.double()) <= 2 * 2.0 ** -8
+    assert rel(dw, dz.t() @ x.double()) <= 2 * 2.0 ** -8
