@@ -270,19 +270,28 @@ __device__ __forceinline__ void scale(const T *g, U *out, int64_t n, float f) {
     for (int64_t i = head + nv * N + threadIdx.x; i < n; i += kThreads) put(out + i, get(g + i) * f);
 }
 
+// With a coefficient that fp32 holds with few bits or as zero: value by value, by fp64.
+template <typename T, typename U>
+__device__ void scale64(const T *g, U *out, int64_t n, double f) {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) put(out + i, static_cast<float>(get(g + i) * f));
+}
+
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Set s) {
     __shared__ float s_f;
+    __shared__ double s_f64;
     wait_previous();
     if (threadIdx.x < 32) {
         const double norm = norm_of(s.part, s.partials);
         if (threadIdx.x == 0) {
             const float told = static_cast<float>(norm);     // what the caller sees decides
-            s_f = norm > s.max_norm && isfinite(told) ? static_cast<float>(s.max_norm / norm) : 1.f;
+            s_f64 = norm > s.max_norm && isfinite(told) ? s.max_norm / norm : 1.0;
+            s_f = static_cast<float>(s_f64);
             if (blockIdx.x == 0 && s.first == 0) *s.norm = told;
         }
     }
     __syncthreads();
     const float f = s_f;
+    const bool tiny = f < 0x1p-126f && s_f64 > 0.0;
     for (int32_t j = s.spans - 1 - static_cast<int32_t>(blockIdx.x); j >= 0; j -= gridDim.x) {
         const int32_t begin = j * s.span;
         int32_t end = min(begin + s.span, s.chunks);
@@ -297,6 +306,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __gr
             const float *gf = static_cast<const float *>(it.g) + at;
             __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(it.out) + at;
             float *of = static_cast<float *>(it.out) + at;
+            if (tiny) {
+                switch (it.kinds) {
+                    case 0: scale64(gf, of, n, s_f64); break;
+                    case 1: scale64(gb, of, n, s_f64); break;
+                    case 2: scale64(gf, ob, n, s_f64); break;
+                    default: scale64(gb, ob, n, s_f64); break;
+                }
+                continue;
+            }
             switch (it.kinds) {
                 case 0: scale(gf, of, n, f); break;
                 case 1: scale(gb, of, n, f); break;

@@ -163,3 +163,14 @@ def test_norm_beyond_fp32():
     n = GradSet(grads, outs).clip(1.0)
     torch.cuda.synchronize()
     assert torch.isinf(n) and all(torch.equal(o, g) for o, g in zip(outs, grads))
+
+
+@pytest.mark.parametrize("kind,out", [(F32, F32), (BF, BF), (F32, BF), (BF, F32)])
+def test_coefficients_below_fp32(kind, out):
+    """max_norm / norm that fp32 holds with few bits or as zero, from 2^-120 to 2^-150."""
+    for max_norm, value in ((1e-5, 1e31), (1e-8, 1e31), (1e-12, 3e30), (3e-14, 3e30)):
+        grads = [torch.full((5003,), value, device="cuda", dtype=kind), torch.full((9,), -value, device="cuda", dtype=kind)]
+        _check(grads, [torch.zeros_like(g, dtype=out) for g in grads], max_norm)
+    zero = torch.ones(9, device="cuda", dtype=out)
+    GradSet([torch.full((9,), 1.0, device="cuda", dtype=kind)], [zero]).clip(0.0)
+    assert float(zero.abs().sum()) == 0
