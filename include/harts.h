@@ -456,7 +456,9 @@ int harts_attn_bwd(const harts_plan *plan, const harts_attn_bwd_args *args, hart
  * h is normalised in fp32 before it is rounded to `dtype` for the residual stream.  The
  * 8-bit output holds y as e4m3 values with one power-of-two scale (e8m0: 2^(byte - 127))
  * per 32 channels, the smallest that keeps the block within 448; a block that holds an
- * infinity gets scale 255 (NaN), a NaN stays one.  h may be x or residual, and y may be x
+ * infinity gets scale 255 (NaN), a NaN stays one.  Scales are in row order; a block-scaled
+ * product of the tensor cores wants them rearranged in its own.  Squares are summed in fp32: a
+ * row whose sum overflows gets rstd 0, and zeros for its finite values.  h may be x or residual, and y may be x
  * (rows are read before they are written), but not both x.  The backward wants h: without a
  * residual and with y over x, give one.
  */
@@ -574,7 +576,8 @@ typedef struct {
     int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out (the outputs are then
                                 incomplete); cleared by the caller.  NULL: the library's own word
                                 (harts_device_error) */
-    void *workspace;         /* device, harts_linear_logprob_{fwd,bwd}_workspace_bytes, 256-byte aligned */
+    void *workspace;         /* device, harts_linear_logprob_{fwd,bwd}_workspace_bytes; 16-byte aligned for
+                                the forward, 256-byte for the backward */
     size_t workspace_bytes;
 } harts_linear_logprob_fwd_args;
 

@@ -514,8 +514,10 @@ def _workspace(workspace, nb, dev):
 
 class GradSet:
     """harts_grad_norm / harts_grad_clip over a fixed list of gradient buffers (bf16 or fp32,
-    contiguous, one device).  The buffers and their addresses are taken once; their values are
-    read at every call.  outs: where clip() writes (same shapes, bf16 or fp32), None: in place.
+    contiguous, one device).  The buffers and their addresses are taken once and kept; their values
+    are read at every call.  A program whose gradients are new tensors each step (autograd's after
+    grad = None) needs a new set each step: an old one goes on clipping the buffers it was made of.
+    outs: where clip() writes (same shapes, bf16 or fp32), None: in place.
     A set outlives the graphs that its calls were captured into, and its calls run one after
     another: they share its workspace."""
 

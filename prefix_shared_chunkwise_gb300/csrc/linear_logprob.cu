@@ -26,7 +26,7 @@
 // is output).  All waits are bounded.
 //
 // Many rows are bound by the tensor cores, under the power limit: 4,096 x 157,184 x 2,048 takes
-// 1.48 ms forward (1.78 PFLOP/s) and 4.6 ms backward (1.72), at 92 - 95 % of the tensor pipe's
+// 1.50 ms forward (1.76 PFLOP/s) and 4.65 ms backward (1.70), at 92 - 95 % of the tensor pipe's
 // cycles.  Few rows are bound by reading W: 1 row takes 107 us (6.0 TB/s).
 #include <algorithm>
 #include <cmath>
@@ -1260,7 +1260,9 @@ int cuda_fail(cudaError_t e, const char *what) {
 // is cut towards zero at every 16 columns of K, which shrinks a logit by D/16 times a quarter of
 // 2^-24 on average (measured with one vocabulary entry, whose lse is its logit: 0.20 - 0.29 for
 // products of either sign at D = 64 .. 4096, up to 0.9 where all have one sign).  Uncorrected
-// that is the largest error of lse, 1.6e-6 of it at D = 2048.
+// that is the largest error of lse, 1.6e-6 of it at D = 2048.  Logits that nothing is cut from
+// (one channel a row, values on a coarse grid) are off by the quarter instead: D/16 2^-26 of
+// them, 3.8e-6 at D = 4096.
 float logit_factor(float scale, int32_t D) {
     return static_cast<float>(double(scale) * 1.4426950408889634 * (1.0 + 0.25 * (D / 16.0) * 0x1p-24));
 }
