@@ -343,6 +343,62 @@ size_t harts_conv_bwd_workspace_bytes(const harts_plan *plan, int32_t channels, 
 int harts_conv_bwd(const harts_plan *plan, const harts_conv_bwd_args *args, harts_stream_t stream);
 
 /* ------------------------------------------------------------------------------ */
+/* Gated linear recurrence over the compact layout.                               */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * One state per channel, run once per compact row, from the row before it on its own trajectory
+ * (its segment's, or its parent's last one; the root's initial state at a trajectory's start):
+ *   a = e^g,  h[r] = a h[before r] + x[r]            (HARTS_SCAN_ADD)
+ *             h[r] = a h[before r] + (1 - a) x[r]    (HARTS_SCAN_MIX)
+ * g is the natural-log decay, as KDA's: g <= 0, -inf starts afresh.  States, and what the long
+ * products of decays are made of, are fp32.  All plan modes work; results do not depend on the
+ * rounds, and their bits do not depend on timing.  A forest whose segments are roots of one row each is a
+ * decoding step: h0 holds the states before, final_state those behind.
+ * What is not finite reaches the rows behind it on its trajectories (backward: before it), and no others.
+ */
+#define HARTS_SCAN_ADD 0
+#define HARTS_SCAN_MIX 1
+
+typedef struct {
+    int32_t channels;        /* D: values per row, a positive multiple of 8 */
+    int32_t dtype;           /* harts_dtype of x, g, h, d_h, dx, dg */
+    int32_t form;            /* HARTS_SCAN_ADD or HARTS_SCAN_MIX */
+    const void *x;           /* device [C][D], compact layout, 16-byte aligned (so are g, h) */
+    const void *g;           /* device [C][D] */
+    const float *h0;         /* device [n_roots][D] initial state of every root, or NULL (zero) */
+    void *h;                 /* device [C][D]: written by the forward, read by the backward; not x or g */
+    float *final_state;      /* device [n_seq][D] output: state after every sequence's last row, or NULL */
+    void *workspace;         /* device, harts_scan_workspace_bytes, 16-byte aligned; calls that may run
+                                at the same time have one each */
+    size_t workspace_bytes;
+} harts_scan_fwd_args;
+
+/* Workspace of either direction: the tiles' maps and the states between them; 0 for invalid arguments. */
+size_t harts_scan_workspace_bytes(const harts_plan *plan, int32_t channels, int32_t dtype);
+
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, channels, form), HARTS_EUNSUPPORTED
+ * (dtype), HARTS_ENOPLAN, HARTS_EOVERFLOW (more than 2^31 - 1 tiles), HARTS_ESMALLBUF (workspace),
+ * HARTS_ECUDA.  A bounded wait that runs out records device code 3 in the plan's error word. */
+int harts_scan_fwd(const harts_plan *plan, const harts_scan_fwd_args *args, harts_stream_t stream);
+
+typedef struct {
+    harts_scan_fwd_args fwd; /* h as the forward wrote it; final_state is not used */
+    const void *d_h;         /* device [C][D] dL/dh per compact row, 16-byte aligned (so are dx, dg) */
+    const float *d_final;    /* device [n_seq][D] dL/dfinal_state, or NULL */
+    void *dx;                /* device [C][D] output; dx and dg may be none of the inputs */
+    void *dg;                /* device [C][D] output */
+    float *dh0;              /* device [n_roots][D] output, or NULL */
+} harts_scan_bwd_args;
+
+/* Backward: with lam[r] = d_h[r] + the sum of a[c] lam[c] over the rows c that follow r (+ d_final
+ * at a sequence's end, where it has one),
+ *   dx[r] = lam or (1 - a) lam,   dg[r] = lam a (h[before r], minus x[r] in the mix form),
+ * and dh0 the sum of a lam over a root's first row.  Sums over branches run by ascending segment.
+ * Errors as the forward. */
+int harts_scan_bwd(const harts_plan *plan, const harts_scan_bwd_args *args, harts_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
 /* Compact-to-semantic log-probabilities.                                         */
 /* ------------------------------------------------------------------------------ */
 

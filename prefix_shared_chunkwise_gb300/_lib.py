@@ -14,6 +14,7 @@ HARTS_FP32, HARTS_BF16 = 0, 1
 HARTS_KERNEL_AUTO, HARTS_KERNEL_SIMT, HARTS_KERNEL_TC = 0, 1, 2
 HARTS_PLAN_NODEWISE = 1                       # harts_plan_calls flags
 HARTS_PLAN_NOREPLAY = 2
+HARTS_SCAN_ADD, HARTS_SCAN_MIX = 0, 1
 
 ERRORS = {0: "HARTS_OK", -1: "HARTS_EINVAL", -2: "HARTS_EUNSUPPORTED", -3: "HARTS_EOVERFLOW",
           -4: "HARTS_ESMALLBUF", -5: "HARTS_ECUDA", -6: "HARTS_ETIMEOUT", -7: "HARTS_EDEVICE",
@@ -31,6 +32,7 @@ EXPORTED = [
     "harts_grad_workspace_bytes", "harts_grad_norm", "harts_grad_clip",
     "harts_linear_logprob_fwd_workspace_bytes", "harts_linear_logprob_fwd",
     "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_device_error",
+    "harts_scan_workspace_bytes", "harts_scan_fwd", "harts_scan_bwd",
     "harts_last_error",
 ]
 
@@ -133,6 +135,15 @@ class LinearLogprobBwdArgs(ctypes.Structure):
                 ("piece", _i32)]
 
 
+class ScanFwdArgs(ctypes.Structure):
+    _fields_ = [("channels", _i32), ("dtype", _i32), ("form", _i32), ("x", _vp), ("g", _vp), ("h0", _vp), ("h", _vp),
+                ("final_state", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", ScanFwdArgs), ("d_h", _vp), ("d_final", _vp), ("dx", _vp), ("dg", _vp), ("dh0", _vp)]
+
+
 _lib = None
 
 
@@ -205,6 +216,12 @@ def lib():
         L.harts_linear_logprob_bwd_workspace_bytes.restype = _sz
         L.harts_linear_logprob_bwd.argtypes = [ctypes.POINTER(LinearLogprobBwdArgs), _vp]
         L.harts_linear_logprob_bwd.restype = ctypes.c_int
+        L.harts_scan_workspace_bytes.argtypes = [_vp, _i32, _i32]
+        L.harts_scan_workspace_bytes.restype = _sz
+        L.harts_scan_fwd.argtypes = [_vp, ctypes.POINTER(ScanFwdArgs), _vp]
+        L.harts_scan_fwd.restype = ctypes.c_int
+        L.harts_scan_bwd.argtypes = [_vp, ctypes.POINTER(ScanBwdArgs), _vp]
+        L.harts_scan_bwd.restype = ctypes.c_int
         L.harts_device_error.argtypes = [_vp, ctypes.POINTER(_i32)]
         L.harts_device_error.restype = ctypes.c_int
         L.harts_last_error.argtypes = []

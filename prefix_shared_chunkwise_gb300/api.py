@@ -12,7 +12,7 @@ from . import _lib as L
 
 __all__ = ["Plan", "kda_fwd", "kda_bwd", "conv_fwd", "conv_bwd", "semantic_map", "logprob_fwd",
            "logprob_bwd", "attn_fwd", "attn_bwd", "linear_logprob_fwd", "linear_logprob_bwd",
-           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "device_error", "dtype_code"]
+           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "scan_fwd", "scan_bwd", "device_error", "dtype_code"]
 
 
 def dtype_code(torch_dtype):
@@ -641,3 +641,63 @@ def linear_logprob_bwd(x, weight, row_ptr, row_sem, target, lse, dlogp, *, scale
     a = L.LinearLogprobBwdArgs(f, dlogp.data_ptr(), dx.data_ptr(), dweight.data_ptr(), piece)
     L.check(lib.harts_linear_logprob_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_logprob_bwd")
     return dx, dweight
+
+
+_FORMS = {"add": L.HARTS_SCAN_ADD, "mix": L.HARTS_SCAN_MIX}
+
+
+def _scan_args(plan, x, g, h, h0, final_state, form, workspace):
+    """Checked arguments that both directions share, and the workspace (kept alive by the caller)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [C, D]")
+    if form not in _FORMS:
+        raise ValueError(f"form {form!r} is none of {sorted(_FORMS)}")
+    (C, D), dt, dev, info = x.shape, x.dtype, x.device, plan.info
+    if C != info["C"]:
+        raise ValueError(f"x has {C} rows, the plan {info['C']}")
+    code = dtype_code(dt)
+    _ready("x", x, None, dt, dev)
+    _ready("g", g, x.shape, dt, dev)
+    _ready("h", h, x.shape, dt, dev)
+    _ready("h0", h0, (info["n_roots"], D), torch.float32, dev)
+    _ready("final_state", final_state, (info["n_seq"], D), torch.float32, dev)
+    workspace, nb = _workspace(workspace, L.lib().harts_scan_workspace_bytes(plan.handle, D, code), dev)
+    a = L.ScanFwdArgs(D, code, _FORMS[form], x.data_ptr(), g.data_ptr(), None if h0 is None else h0.data_ptr(),
+                      h.data_ptr(), None if final_state is None else final_state.data_ptr(), workspace.data_ptr(), nb)
+    return a, workspace
+
+
+@_made_on_stream
+def scan_fwd(plan: Plan, x, g, *, form="add", h0=None, h=None, final_state=None, workspace=None, stream=None):
+    """harts_scan_fwd: the gated recurrence h = e^g h_before + x ("add") or e^g h_before + (1 - e^g) x
+    ("mix") per channel over the compact rows, each from the row before it on its trajectory.
+    x, g: [C, D] bf16 or fp32, D a multiple of 8, g <= 0.  h0: [n_roots, D] fp32 states before the roots, or None.
+    final_state: [n_seq, D] fp32, receives the state after each sequence.  Returns h like x."""
+    import torch
+    if h is None:
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    a, workspace = _scan_args(plan, x, g, h, h0, final_state, form, workspace)
+    L.check(L.lib().harts_scan_fwd(plan.handle, ctypes.byref(a), _stream_on(stream, x)), "harts_scan_fwd")
+    return h
+
+
+@_made_on_stream
+def scan_bwd(plan: Plan, x, g, h, d_h, *, form="add", h0=None, d_final=None, dx=None, dg=None, dh0=None,
+             workspace=None, stream=None):
+    """harts_scan_bwd: from the forward's inputs and h, and dL/dh per compact row (d_h, already
+    summed over the trajectories that share the row; d_final: dL/dfinal_state).  Returns (dx, dg)
+    like x; dh0 [n_roots, D] fp32, if given, receives the gradient of h0."""
+    import torch
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx is None else dx
+    dg = torch.empty_like(dx) if dg is None else dg
+    f, workspace = _scan_args(plan, x, g, h, h0, None, form, workspace)
+    dev, f32 = x.device, torch.float32
+    for n, t in (("d_h", d_h), ("dx", dx), ("dg", dg)):
+        _ready(n, t, x.shape, x.dtype, dev)
+    _ready("d_final", d_final, (plan.info["n_seq"], x.shape[1]), f32, dev)
+    _ready("dh0", dh0, (plan.info["n_roots"], x.shape[1]), f32, dev)
+    a = L.ScanBwdArgs(f, d_h.data_ptr(), None if d_final is None else d_final.data_ptr(), dx.data_ptr(), dg.data_ptr(),
+                      None if dh0 is None else dh0.data_ptr())
+    L.check(L.lib().harts_scan_bwd(plan.handle, ctypes.byref(a), _stream_on(stream, x)), "harts_scan_bwd")
+    return dx, dg

@@ -11,7 +11,19 @@ namespace harts {
 // Device view of an uploaded plan: pointers into one int32 image.
 constexpr int kConvMaxW = 8;       // widest short convolution the plan tables serve
 constexpr int kAttnTile = 128;     // query / key rows per branch-attention tile
+constexpr int kScanRows = 128;     // rows per tile of the gated scan
+constexpr int kScanGroup = 32;     // most tiles of one segment whose carries are joined side by side
 constexpr int64_t kAttnMaxRows = int64_t(1) << 27;   // largest ancestor-row table built
+
+// A tile of the gated scan: up to kScanRows rows of one segment.  Up to kScanGroup consecutive
+// tiles of a segment form a group; a group's predecessor is the one before it in its segment, or
+// the last one of the parent segment.
+struct ScanTile {
+    int32_t tile, row0, rows, at;             // index, first row, rows, place in its group
+    int32_t group, count, pred, pred_row;     // tiles of the group; predecessor group and the row before row0, or -1 - root
+    int32_t seq_end, next_begin, next_count;  // sequence that ends with the group (or -1); groups that follow it
+    int32_t pad;
+};
 
 struct PlanDev {
     int32_t *err;                // [4] device error word: code, info, info, info
@@ -52,6 +64,10 @@ struct PlanDev {
     const int32_t *attn_kptr;      // [n_kt+1] query tiles of key tile j: attn_kq[3 * kptr[j] ..]
     const int32_t *attn_kq;        // (sequence, query tile, f): f own rows of the key's sequence visible, -1 causal
     int32_t n_qt, n_kt;
+    // gated scan: one record per tile, predecessors first (forward) and successors first (backward)
+    const struct ScanTile *scan_fwd, *scan_bwd;   // [n_scan]
+    const int32_t *scan_next;      // groups that follow a segment's last group: ScanTile::next_begin ..
+    int32_t n_scan, n_scan_groups, scan_alone;    // scan_alone: no tile follows another one
     int32_t n_rounds, n_seq, n_states, n_roots, n_fold, chunk, n_seg;
     uint32_t flags;                // harts_plan_calls flags (HARTS_PLAN_NOREPLAY: slots inside chunks)
     int64_t R, n_chunks, C;
@@ -65,8 +81,9 @@ struct PlanImage {
         off_state_cptr, off_state_cons, off_root_cptr, off_root_cons, off_replay_idx,
         off_fold_rows, off_fold_ptr, off_fold_occ, off_chunk_seq, off_row_seg, off_seg_row0,
         off_seg_len, off_conv_ctx, off_conv_sptr, off_conv_succ, off_attn_rptr, off_attn_runs,
-        off_attn_mptr, off_attn_mask, off_attn_hp, off_attn_qt, off_attn_kt, off_attn_kptr, off_attn_kq;
-    int32_t n_qt, n_kt;
+        off_attn_mptr, off_attn_mask, off_attn_hp, off_attn_qt, off_attn_kt, off_attn_kptr, off_attn_kq,
+        off_scan_fwd, off_scan_bwd, off_scan_next;
+    int32_t n_qt, n_kt, n_scan, n_scan_groups, scan_alone;
 };
 
 void set_error(const std::string &msg);
