@@ -364,7 +364,7 @@ typedef struct {
     int32_t channels;        /* D: values per row, a positive multiple of 8 */
     int32_t dtype;           /* harts_dtype of x, g, h, d_h, dx, dg */
     int32_t form;            /* HARTS_SCAN_ADD or HARTS_SCAN_MIX */
-    const void *x;           /* device [C][D], compact layout, 16-byte aligned (so are g, h) */
+    const void *x;           /* device [C][D], compact layout, 16-byte aligned (so are the others) */
     const void *g;           /* device [C][D] */
     const float *h0;         /* device [n_roots][D] initial state of every root, or NULL (zero) */
     void *h;                 /* device [C][D]: written by the forward, read by the backward; not x or g */
@@ -384,7 +384,7 @@ int harts_scan_fwd(const harts_plan *plan, const harts_scan_fwd_args *args, hart
 
 typedef struct {
     harts_scan_fwd_args fwd; /* h as the forward wrote it; final_state is not used */
-    const void *d_h;         /* device [C][D] dL/dh per compact row, 16-byte aligned (so are dx, dg) */
+    const void *d_h;         /* device [C][D] dL/dh per compact row, 16-byte aligned (so are the others) */
     const float *d_final;    /* device [n_seq][D] dL/dfinal_state, or NULL */
     void *dx;                /* device [C][D] output; dx and dg may be none of the inputs */
     void *dg;                /* device [C][D] output */

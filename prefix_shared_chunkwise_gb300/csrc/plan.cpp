@@ -567,13 +567,19 @@ void build_image(harts_plan &P) {
     }
     for (size_t t = tiles.size(); t-- > 0;)             // a group comes after its predecessor here too
         if (tiles[t].pred >= 0) height[tiles[t].pred] = std::max(height[tiles[t].pred], height[tiles[t].group] + 1);
+    // Of groups that may run side by side, the first tiles of all come before the second ones: by
+    // then what the tiles of a group publish for the next is long there.
     std::vector<ScanTile> by = tiles;
-    std::stable_sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) { return depth[a.group] < depth[b.group]; });
+    std::sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) {
+        if (depth[a.group] != depth[b.group]) return depth[a.group] < depth[b.group];
+        return a.at != b.at ? a.at < b.at : a.tile < b.tile;
+    });
     constexpr size_t kWords = sizeof(ScanTile) / sizeof(int32_t);
     put(I.off_scan_fwd, reinterpret_cast<const int32_t *>(by.data()), by.size() * kWords);
-    by = tiles;
-    std::sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) {      // a group's last tile first
-        return height[a.group] != height[b.group] ? height[a.group] < height[b.group] : a.tile > b.tile;
+    std::sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) {
+        if (height[a.group] != height[b.group]) return height[a.group] < height[b.group];
+        const int32_t u = a.count - a.at, v = b.count - b.at;
+        return u != v ? u < v : a.tile < b.tile;
     });
     put(I.off_scan_bwd, reinterpret_cast<const int32_t *>(by.data()), by.size() * kWords);
     put(I.off_scan_next, snext.data(), snext.size());

@@ -11,9 +11,9 @@
 // value is read and written once; HBM bounds the work, and the chain of carries must not.  The
 // planner cuts segments into tiles of 128 rows (a fork lies at a tile's end); a block takes a
 // tile of 128 bytes of channels: eight warps of 16 rows each compose their rows' map, a ninth
-// joins the eight and publishes the tile's map; the eight then fetch the maps of the tiles before
-// it in its group, four each (up to 32 of a segment, which need not wait for one another), from
-// which the ninth forms the carry with the state that the group before left.  So a chain waits once for 4,096 rows.  The order in which maps are joined is fixed
+// joins the eight and publishes the tile's map, and forms the carry from the maps of the tiles before
+// it in its group (up to 32 of a segment, which need not wait for one another) and the state that
+// the group before left, both fetched while the rows are still on their way.  So a chain waits once for 4,096 rows.  The order in which maps are joined is fixed
 // by position: no atomics on values, the same bits on every run.  What is published carries its
 // own validity: the workspace starts as all ones, a NaN that no published value has.  Tiles are
 // taken in an order that has predecessors first, by a ticket counter, so that whatever a block
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kWarps = 8, kWarpRows = kScanRows / kWarps;      // consumers
 constexpr int kThreads = 32 * (kWarps + 2);                    // and a warp each for carries and copies
-constexpr int kShare = kScanGroup / kWarps;                    // tiles of a group whose maps one consumer joins
+constexpr int kAtOnce = 8;                                     // maps that are fetched at a time
 constexpr int kBox = 16;                                       // rows of one copy
 constexpr uint32_t kTileBytes = kScanRows * 128;               // of one tensor
 constexpr uint32_t kEmpty = 0xffffffffu;                       // not published yet
@@ -59,50 +59,97 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// e^g for g <= 0, as one number that gives both a and 1 - a with few roundings: a itself, or, from
-// e^(-0.3466) = 2^(-1/2) up, -(1 - a) with its sign bit set.  2^y = 2^n 2^f with |f| <= 1/2 and the
-// series of e^(f ln 2) to its seventh power (the next term is 5e-9).  Memories of a thousand rows
-// multiply a thousand decays: an approximate exponential's 2^-22 would be 2e-4 of the state.
-// Without PRECISE (bf16 results of the add form, which round to 2^-9) that is enough, and a is kept.
-template <bool PRECISE> __device__ __forceinline__ float decay(float g) {
-    if constexpr (!PRECISE) return ex2(g * 1.4426950408889634f);
-    const float z = fmaf(g, 1.4426950408889634f, 12582912.f), n = z - 12582912.f;
-    const float f = fmaf(g, 1.9259629911e-8f, fmaf(g, 1.4426950216293335f, -n));
-    float q = 1.5252733804e-5f;
-    q = fmaf(q, f, 1.5403530394e-4f);
-    q = fmaf(q, f, 1.3333558146e-3f);
-    q = fmaf(q, f, 9.6181291076e-3f);
-    q = fmaf(q, f, 5.5504108665e-2f);
-    q = fmaf(q, f, 2.4022650696e-1f);
-    q = fmaf(q, f, 6.9314718056e-1f);
-    const float t = q * f;
-    const float scale = __int_as_float((__float_as_int(z) - 0x4b400000 + 127) << 23);
-    float a = fmaf(t, scale, scale);
-    if (n == 0.f) a = -fabsf(t);
-    return g < -87.f ? 0.f : a;
+// The channels of a lane, 4 bytes: two of bf16, whose fp32 arithmetic runs on pairs (half as many
+// instructions, which are what the exact decay below would be bound by), or one of fp32.
+using Two = float2;
+__device__ __forceinline__ uint64_t bits_of(Two a) { uint64_t u; memcpy(&u, &a, 8); return u; }
+__device__ __forceinline__ Two two_of(uint64_t u) { Two a; memcpy(&a, &u, 8); return a; }
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
+    return two_of(d);
 }
-template <bool PRECISE> __device__ __forceinline__ float keep_of(float v) {      // a
-    if constexpr (!PRECISE) return v;
-    return __float_as_int(v) < 0 && v == v ? 1.f + v : v;
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(d);
 }
-__device__ __forceinline__ float rest_of(float v) { return __float_as_int(v) < 0 ? -v : 1.f - v; }     // 1 - a
+__device__ __forceinline__ Two add(Two a, Two b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(d);
+}
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+template <typename F> __device__ __forceinline__ Two each(Two a, F f) { return make_float2(f(a.x), f(a.y)); }
+template <typename F> __device__ __forceinline__ float each(float a, F f) { return f(a); }
+template <typename F> __device__ __forceinline__ Two each(Two a, Two b, F f) { return make_float2(f(a.x, b.x), f(a.y, b.y)); }
+template <typename F> __device__ __forceinline__ float each(float a, float b, F f) { return f(a, b); }
 
-template <typename T> struct Lane;                             // the channels of a lane: 4 bytes
+template <typename T> struct Lane;
 template <> struct Lane<__nv_bfloat16> {
+    using V = Two;
     static constexpr int n = 2;
-    __device__ __forceinline__ static void get(const uint8_t *p, float (&v)[2]) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
-        v[0] = f.x; v[1] = f.y;
+    __device__ __forceinline__ static V all(float c) { return make_float2(c, c); }
+    __device__ __forceinline__ static V get(const void *p) {
+        const uint32_t u = *static_cast<const uint32_t *>(p);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
-    __device__ __forceinline__ static void put(void *p, const float (&v)[2]) {
-        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
-    }
+    __device__ __forceinline__ static void put(void *p, V v) { *static_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y); }
+    __device__ __forceinline__ static V load(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+    __device__ __forceinline__ static void store(float *p, V v) { *reinterpret_cast<float2 *>(p) = v; }
 };
 template <> struct Lane<float> {
+    using V = float;
     static constexpr int n = 1;
-    __device__ __forceinline__ static void get(const uint8_t *p, float (&v)[1]) { v[0] = *reinterpret_cast<const float *>(p); }
-    __device__ __forceinline__ static void put(void *p, const float (&v)[1]) { *static_cast<float *>(p) = v[0]; }
+    __device__ __forceinline__ static V all(float c) { return c; }
+    __device__ __forceinline__ static V get(const void *p) { return *static_cast<const float *>(p); }
+    __device__ __forceinline__ static void put(void *p, V v) { *static_cast<float *>(p) = v; }
+    __device__ __forceinline__ static V load(const float *p) { return *p; }
+    __device__ __forceinline__ static void store(float *p, V v) { *p = v; }
 };
+
+// e^g for g <= 0, as one number that gives both a and 1 - a with few roundings.  2^y = 2^n 2^f with
+// |f| <= 1/2 and the series of e^(f ln 2) to its seventh power (the next term is 5e-9); below
+// 2^-126.5, zero.  Memories of a thousand rows multiply a thousand decays: an approximate
+// exponential's 2^-22 would be 2e-4 of the state.  KIND kExact keeps a; kBoth keeps a below
+// 2^(-1/2), and above it -(1 - a), its sign bit set, from the series, as 1 - a would lose what the
+// rounding of a took.  kFast, the hardware's exponential, is for results that are all bf16, which
+// rounds to 2^-9, in the add form.
+enum Kind { kFast, kExact, kBoth };
+template <int KIND, typename T> __device__ __forceinline__ typename Lane<T>::V decay(typename Lane<T>::V g) {
+    using L = Lane<T>;
+    if constexpr (KIND == kFast) return each(mul(g, L::all(1.4426950408889634f)), [](float y) { return ex2(y); });
+    g = each(g, [](float v) {
+        float y;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(v), "f"(-88.f));
+        return y;
+    });
+    const auto z = fma(g, L::all(1.4426950408889634f), L::all(12582912.f));        // its low bits are n
+    const auto n = fma(z, L::all(-1.f), L::all(12582912.f));                       // -n
+    const auto f = fma(g, L::all(1.4426950408889634f), n);
+    auto q = L::all(1.5252733804e-5f);
+    q = fma(q, f, L::all(1.5403530394e-4f));
+    q = fma(q, f, L::all(1.3333558146e-3f));
+    q = fma(q, f, L::all(9.6181291076e-3f));
+    q = fma(q, f, L::all(5.5504108665e-2f));
+    q = fma(q, f, L::all(2.4022650696e-1f));
+    q = fma(q, f, L::all(6.9314718056e-1f));
+    const auto t = mul(q, f);
+    const auto scale = each(z, [](float v) { return __uint_as_float((__float_as_uint(v) << 23) + 0x3f800000u); });
+    const auto a = fma(t, scale, scale);
+    if constexpr (KIND == kExact) return a;
+    return each(t, each(a, z, [](float u, float v) { return v == 12582912.f ? __uint_as_float(0xff800000u) : u; }),
+                [](float d, float u) { return __float_as_uint(u) == 0xff800000u ? -fabsf(d) : u; });
+}
+template <int KIND, typename V> __device__ __forceinline__ V keep_of(V v) {      // a
+    if constexpr (KIND != kBoth) return v;
+    return each(v, [](float u) { return __float_as_int(u) < 0 ? 1.f + u : u; });  // (a NaN stays one)
+}
+template <typename V> __device__ __forceinline__ V rest_of(V v) {                // 1 - a
+    return each(v, [](float u) { return __float_as_int(u) < 0 ? -u : 1.f - u; });
+}
 
 __device__ __forceinline__ uint32_t publishable(float v) { return v == v ? __float_as_uint(v) : 0x7fffffffu; }
 __device__ __forceinline__ void publish(float2 *at, float a, float b) {
@@ -112,6 +159,7 @@ __device__ __forceinline__ void publish(float2 *at, float a, float b) {
 __device__ __forceinline__ void publish(float *at, float v) {
     asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" :: "l"(at), "r"(publishable(v)) : "memory");
 }
+__device__ __forceinline__ void publish(float *at, Two v) { publish(reinterpret_cast<float2 *>(at), v.x, v.y); }
 __device__ __forceinline__ float2 look(const float2 *at) {
     uint64_t u;
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(u) : "l"(at) : "memory");
@@ -127,21 +175,15 @@ __device__ __forceinline__ bool is_there(float2 v) { return is_there(v.x) && is_
 
 __device__ __forceinline__ bool gave_up(const int *f) { return *reinterpret_cast<const volatile int *>(f) != 0; }
 
-// What is published at `at`, waiting for it; zeros once a wait of the block has run out.
-template <typename V> __device__ __forceinline__ V await(const V *at, int *failed) {
-    V v = look(at);
-    if (is_there(v)) return v;
-    const long long t0 = clock64();
-    while (!gave_up(failed)) {
-        v = look(at);
-        if (is_there(v)) return v;
-        if (clock64() - t0 > 4000000000LL) *reinterpret_cast<volatile int *>(failed) = 1;
-    }
-    return V{};
-}
-
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_addr(bar)) : "memory");
+}
+// Whether the phase has completed, without the while that try_wait may stay for.
+__device__ __forceinline__ bool is_done(uint64_t *bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(tc::smem_addr(bar)), "r"(phase) : "memory");
+    return ok != 0;
 }
 // True, for the whole warp, once the phase completed; false when the wait ran out or another role gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f) {
@@ -165,25 +207,27 @@ template <bool BWD, bool MIX> struct Ring {
 
 struct Meta { ScanTile t; int32_t col; };                      // rows 0: the end
 
-template <typename T, bool BWD, bool MIX, bool PRECISE>
+template <typename T, bool BWD, bool MIX, int KIND>
 __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(const __grid_constant__ ScanParams p) {
     using R = Ring<BWD, MIX>;
-    constexpr int CH = Lane<T>::n, kWide = 32 * CH;
+    using L = Lane<T>;
+    using V = typename L::V;
+    constexpr int CH = L::n, kWide = 32 * CH;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((128 - (tc::smem_addr(smraw) & 127)) & 127);
-    __shared__ uint64_t full[R::stages], empty[R::stages];
+    __shared__ uint64_t known[R::stages], full[R::stages], empty[R::stages];
+    __shared__ uint64_t maps_full[2], carry_full[2];           // by tile parity, as what they guard
     __shared__ Meta meta[R::stages];
-    __shared__ float2 s_map[2][kWarps][kWide];                 // the warps' maps, by tile parity
-    __shared__ float2 s_pre[kWarps][kWide];                    // maps of the tiles before this one, each of kShare of them
-    __shared__ float s_carry[kWide];
-    __shared__ uint64_t maps_full, pre_full, carry_full;
+    __shared__ V s_a[2][kWarps][32], s_b[2][kWarps][32], s_carry[2][32];           // the warps' maps, the carry
     __shared__ int s_fail;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < R::stages; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], kWarps + 1); }
-        tc::mbar_init(&maps_full, kWarps);
-        tc::mbar_init(&pre_full, kWarps);
-        tc::mbar_init(&carry_full, 1);
+        for (int s = 0; s < R::stages; ++s) {
+            tc::mbar_init(&known[s], 1);
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], kWarps + 1);
+        }
+        for (int i = 0; i < 2; ++i) { tc::mbar_init(&maps_full[i], kWarps); tc::mbar_init(&carry_full[i], 1); }
         tc::fence_mbar_init();
         s_fail = 0;
     }
@@ -213,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
             const int boxes = (m.t.rows + kBox - 1) / kBox;
             if (lane == 0) {
                 meta[s] = m;
+                arrive(&known[s]);
                 if (m.t.rows) tc::mbar_expect_tx(&full[s], boxes * R::tensors * kBox * 128);
                 else arrive(&full[s]);
             }
@@ -229,211 +274,165 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
         for (uint32_t k = it > R::stages ? it - R::stages : 0; k < it; ++k)
             if (!ended || it - k < R::stages) tc::mbar_wait(&full[k % R::stages], (k / R::stages) & 1);
     } else if (warp == kWarps) {
-        // carries
-        uint32_t uses = 0;
+        // Carries, a tile's ahead of its rows: as soon as it is known which tile it is, the maps
+        // between the group's carry and the tile are joined, in the order of the rows; then comes
+        // whichever is there first, the carry or the tile's own map, which others wait for.
         for (uint32_t it = 0;; ++it) {
-            const int s = it % R::stages;
-            if (!warp_wait(&full[s], (it / R::stages) & 1, &s_fail)) break;
+            const int s = it % R::stages, par = it & 1;
+            if (!warp_wait(&known[s], (it / R::stages) & 1, &s_fail)) break;
             const Meta m = meta[s];
-            if (m.t.rows == 0 || !warp_wait(&maps_full, it & 1, &s_fail)) break;
-            float A[CH], B[CH];
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                A[c] = 1.f; B[c] = 0.f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float2 w = s_map[it & 1][BWD ? kWarps - 1 - k : k][lane * CH + c];
-                    B[c] = fmaf(w.x, B[c], w.y);
-                    A[c] *= w.x;
-                }
-            }
+            if (m.t.rows == 0) break;
             const int64_t ch = m.col + lane * CH;
+            const bool inside = ch < p.D;                      // channels come in eights
             float2 *agg = p.agg + static_cast<int64_t>(m.t.tile) * p.width + ch;
-            if (BWD ? m.t.at > 0 : m.t.at < m.t.count - 1) {
-#pragma unroll
-                for (int c = 0; c < CH; ++c) publish(agg + c, A[c], B[c]);
-            }
-            float v[CH];
-#pragma unroll
-            for (int c = 0; c < CH; ++c) v[c] = 0.f;
-            if (!BWD) {
-                if (m.t.pred >= 0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) v[c] = await(p.inc + static_cast<int64_t>(m.t.pred) * p.width + ch + c, &s_fail);
-                } else if (p.h0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (ch + c < p.D) v[c] = p.h0[static_cast<int64_t>(-1 - m.t.pred) * p.D + ch + c];
-                }
-            } else {
-                for (int k = 0; k < m.t.next_count; ++k) {
-                    const int64_t g = p.next[m.t.next_begin + k];
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) v[c] += await(p.inc + g * p.width + ch + c, &s_fail);
-                }
-                if (p.d_final && m.t.seq_end >= 0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (ch + c < p.D) v[c] += p.d_final[static_cast<int64_t>(m.t.seq_end) * p.D + ch + c];
-                }
-            }
+            V pa = L::all(1.f), pb = L::all(0.f), v = L::all(0.f), A = L::all(1.f), B = L::all(0.f);
+            bool mapped = false, carried = false;
             const int between = BWD ? m.t.count - 1 - m.t.at : m.t.at;
-            if (between > 0) {
-                if (!warp_wait(&pre_full, uses++ & 1, &s_fail)) break;
-                for (int k = BWD ? (m.t.count - 1) / kShare : 0; BWD ? k >= (m.t.at + 1) / kShare : k <= (m.t.at - 1) / kShare; k += BWD ? -1 : 1) {
+            int k = between;                                   // maps still to be joined, the farthest first
+            int left = BWD ? m.t.next_count : m.t.pred >= 0;   // states still to come, in order
+            const long long t0 = clock64();
+            while (!mapped || !carried) {
+                if (!mapped && __all_sync(0xffffffffu, is_done(&maps_full[par], (it >> 1) & 1))) {
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const float2 w = s_pre[k][lane * CH + c];
-                        v[c] = fmaf(w.x, v[c], w.y);
+                    for (int i = 0; i < kWarps; ++i) {
+                        const int w = BWD ? kWarps - 1 - i : i;
+                        B = fma(s_a[par][w][lane], B, s_b[par][w][lane]);
+                        A = mul(s_a[par][w][lane], A);
+                    }
+                    if (BWD ? m.t.at > 0 : m.t.at < m.t.count - 1) {
+                        if constexpr (CH == 2) { publish(agg, A.x, B.x); publish(agg + 1, A.y, B.y); }
+                        else publish(agg, A, B);
+                    }
+                    mapped = true;
+                }
+                V state = L::all(0.f);
+                bool there = false;
+                if (left > 0) {
+                    const int64_t g = BWD ? p.next[m.t.next_begin + m.t.next_count - left] : m.t.pred;
+                    if constexpr (CH == 2) state = look(reinterpret_cast<const float2 *>(p.inc + g * p.width + ch));
+                    else state = look(p.inc + g * p.width + ch);
+                }
+                if (k > 0) {                                   // up to kAtOnce maps, if they are all there
+                    float2 w[kAtOnce][CH];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+                            w[i][c] = k - i > 0 ? look(agg + static_cast<int64_t>(BWD ? k - i : i - k) * p.width + c) : make_float2(1.f, 0.f);
+                    there = true;
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) there = there && is_there(w[i][c]);
+                    if (__all_sync(0xffffffffu, there)) {
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i) {    // (past the last one: a map that changes nothing)
+                            if constexpr (CH == 2) {
+                                const V a = make_float2(w[i][0].x, w[i][CH - 1].x);
+                                pb = fma(a, pb, make_float2(w[i][0].y, w[i][CH - 1].y));
+                                pa = mul(a, pa);
+                            } else {
+                                pb = fma(w[i][0].x, pb, w[i][0].y);
+                                pa = mul(w[i][0].x, pa);
+                            }
+                        }
+                        k -= kAtOnce;
                     }
                 }
-            }
-#pragma unroll
-            for (int c = 0; c < CH; ++c) s_carry[lane * CH + c] = v[c];
-            __syncwarp();
-            if (lane == 0) arrive(&carry_full);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) v[c] = fmaf(A[c], v[c], B[c]);
-            if (!BWD) {
-                if (m.t.at == m.t.count - 1 && m.t.next_count > 0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) publish(p.inc + static_cast<int64_t>(m.t.group) * p.width + ch + c, v[c]);
+                if (left > 0) {
+                    if (__all_sync(0xffffffffu, is_there(state))) { v = add(v, state); --left; }
                 }
-            } else if (m.t.at == 0) {
-                if (m.t.pred >= 0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) publish(p.inc + static_cast<int64_t>(m.t.group) * p.width + ch + c, v[c]);
-                } else if (p.dh0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (ch + c < p.D) p.dh0[static_cast<int64_t>(-1 - m.t.pred) * p.D + ch + c] = v[c];
+                if (!carried && left == 0 && k <= 0) {
+                    if (!BWD && m.t.pred < 0 && p.h0 && inside) v = L::load(p.h0 + static_cast<int64_t>(-1 - m.t.pred) * p.D + ch);
+                    if (BWD && m.t.seq_end >= 0 && p.d_final && inside)
+                        v = add(v, L::load(p.d_final + static_cast<int64_t>(m.t.seq_end) * p.D + ch));
+                    if (between > 0) v = fma(pa, v, pb);
+                    s_carry[par][lane] = v;
+                    __syncwarp();
+                    if (lane == 0) arrive(&carry_full[par]);
+                    carried = true;
                 }
+                if (clock64() - t0 > 4000000000LL) *reinterpret_cast<volatile int *>(&s_fail) = 1;
+                if (__any_sync(0xffffffffu, gave_up(&s_fail))) break;
             }
+            if (!mapped || !carried) break;
+            v = fma(A, v, B);
+            if (BWD ? m.t.at == 0 && m.t.pred >= 0 : m.t.at == m.t.count - 1 && m.t.next_count > 0)
+                publish(p.inc + static_cast<int64_t>(m.t.group) * p.width + ch, v);
+            else if (BWD && m.t.at == 0 && p.dh0 && inside)
+                L::store(p.dh0 + static_cast<int64_t>(-1 - m.t.pred) * p.D + ch, v);
             __syncwarp();
             if (lane == 0) arrive(&empty[s]);
         }
     } else {
         for (uint32_t it = 0;; ++it) {
-            const int s = it % R::stages;
+            const int s = it % R::stages, par = it & 1;
             if (!warp_wait(&full[s], (it / R::stages) & 1, &s_fail)) break;
             const int rows = meta[s].t.rows, row0 = meta[s].t.row0;
             if (rows == 0) break;
             const int mine = min(max(rows - warp * kWarpRows, 0), kWarpRows);
             const uint8_t *src = sm + s * R::stage_bytes + warp * kWarpRows * 128 + lane * 4;
             const int64_t ch = meta[s].col + lane * CH;
-            [[maybe_unused]] float hp[CH] = {};                // state before the tile's first row
+            [[maybe_unused]] V before = L::all(0.f);           // state before the tile's first row
             if (BWD && warp == 0 && ch < p.D) {
                 const int32_t pr = meta[s].t.pred_row;
-                if (pr >= 0) {
-                    Lane<T>::get(reinterpret_cast<const uint8_t *>(static_cast<const T *>(p.h_in) + static_cast<int64_t>(pr) * p.D + ch), hp);
-                } else if (p.h0) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) hp[c] = p.h0[static_cast<int64_t>(-1 - pr) * p.D + ch + c];
-                }
+                if (pr >= 0) before = L::get(static_cast<const T *>(p.h_in) + static_cast<int64_t>(pr) * p.D + ch);
+                else if (p.h0) before = L::load(p.h0 + static_cast<int64_t>(-1 - pr) * p.D + ch);
             }
-            float d[kWarpRows][CH], A[CH], B[CH];
+            V d[kWarpRows], A = L::all(1.f), B = L::all(0.f);
+            auto map_row = [&](int i) {
+                const V u = L::get(src + kTileBytes + i * 128);
+                d[i] = decay<KIND, T>(L::get(src + i * 128));
+                const V a = keep_of<KIND>(d[i]);
+                if (BWD) B = mul(a, add(u, B));
+                else B = fma(a, B, MIX ? mul(rest_of(d[i]), u) : u);
+                A = mul(A, a);
+            };
+            if (mine == kWarpRows) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; }
+                for (int k = 0; k < kWarpRows; ++k) map_row(BWD ? kWarpRows - 1 - k : k);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kWarpRows; ++k) {
-                const int i = BWD ? kWarpRows - 1 - k : k;
-                if (i < mine) {
-                    float g[CH], u[CH];
-                    Lane<T>::get(src + i * 128, g);
-                    Lane<T>::get(src + kTileBytes + i * 128, u);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        d[i][c] = decay<PRECISE>(g[c]);
-                        const float a = keep_of<PRECISE>(d[i][c]);
-                        if (BWD) B[c] = a * (u[c] + B[c]);
-                        else B[c] = fmaf(a, B[c], MIX ? rest_of(d[i][c]) * u[c] : u[c]);
-                        A[c] *= a;
-                    }
-                }
+                for (int k = 0; k < kWarpRows; ++k)
+                    if ((BWD ? kWarpRows - 1 - k : k) < mine) map_row(BWD ? kWarpRows - 1 - k : k);
             }
-#pragma unroll
-            for (int c = 0; c < CH; ++c) s_map[it & 1][warp][lane * CH + c] = make_float2(A[c], B[c]);
+            s_a[par][warp][lane] = A;
+            s_b[par][warp][lane] = B;
             __syncwarp();
-            if (lane == 0) arrive(&maps_full);
-            const ScanTile &t = meta[s].t;
-            if (BWD ? t.at < t.count - 1 : t.at > 0) {
-                // this warp's share of the tiles between the group's carry and this tile
-                const int lo = max(warp * kShare, BWD ? t.at + 1 : 0), hi = min(warp * kShare + kShare, BWD ? t.count : t.at);
-                const float2 *at = p.agg + static_cast<int64_t>(t.tile - t.at) * p.width + meta[s].col + lane * CH;
-                float2 w[kShare][CH];
-#pragma unroll
-                for (int k = 0; k < kShare; ++k) {
-                    const int i = warp * kShare + k;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        w[k][c] = i >= lo && i < hi ? look(at + static_cast<int64_t>(i) * p.width + c) : make_float2(1.f, 0.f);
-                }
-#pragma unroll
-                for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; }
-#pragma unroll
-                for (int k = 0; k < kShare; ++k) {
-                    const int j = BWD ? kShare - 1 - k : k, i = warp * kShare + j;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        if (!is_there(w[j][c])) w[j][c] = await(at + static_cast<int64_t>(i) * p.width + c, &s_fail);
-                        if (i >= lo && i < hi) {
-                            B[c] = fmaf(w[j][c].x, B[c], w[j][c].y);
-                            A[c] *= w[j][c].x;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < CH; ++c) s_pre[warp][lane * CH + c] = make_float2(A[c], B[c]);
-                __syncwarp();
-                if (lane == 0) arrive(&pre_full);
-            }
-            if (!warp_wait(&carry_full, it & 1, &s_fail)) break;
-            float v[CH];
-#pragma unroll
-            for (int c = 0; c < CH; ++c) v[c] = s_carry[lane * CH + c];
-            for (int k = BWD ? kWarps - 1 : 0; k != warp; k += BWD ? -1 : 1) {
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const float2 w = s_map[it & 1][k][lane * CH + c];
-                    v[c] = fmaf(w.x, v[c], w.y);
-                }
-            }
+            if (lane == 0) arrive(&maps_full[par]);
+            if (!warp_wait(&maps_full[par], (it >> 1) & 1, &s_fail) || !warp_wait(&carry_full[par], (it >> 1) & 1, &s_fail)) break;
+            V v = s_carry[par][lane];
+            for (int k = BWD ? kWarps - 1 : 0; k != warp; k += BWD ? -1 : 1) v = fma(s_a[par][k][lane], v, s_b[par][k][lane]);
             if (ch < p.D) {
                 const int64_t at = static_cast<int64_t>(row0 + warp * kWarpRows) * p.D + ch;
-                T *out0 = static_cast<T *>(p.out0) + at, *out1 = static_cast<T *>(p.out1) + at;
-#pragma unroll
-                for (int k = 0; k < kWarpRows; ++k) {
-                    const int i = BWD ? kWarpRows - 1 - k : k;
-                    if (i < mine) {
-                        float u[CH];
-                        Lane<T>::get(src + kTileBytes + i * 128, u);
-                        if constexpr (!BWD) {
-#pragma unroll
-                            for (int c = 0; c < CH; ++c)
-                                v[c] = fmaf(keep_of<PRECISE>(d[i][c]), v[c], MIX ? rest_of(d[i][c]) * u[c] : u[c]);
-                            Lane<T>::put(out0 + static_cast<int64_t>(i) * p.D, v);
-                        } else {
-                            float h[CH], x[CH], dx[CH], dg[CH];
-                            Lane<T>::get(src + 2 * kTileBytes + i * 128, h);
-                            if (MIX) Lane<T>::get(src + 3 * kTileBytes + i * 128, x);
-#pragma unroll
-                            for (int c = 0; c < CH; ++c) {
-                                if (i == 0 && warp == 0) h[c] = hp[c];
-                                const float lam = u[c] + v[c];
-                                v[c] = keep_of<PRECISE>(d[i][c]) * lam;
-                                dx[c] = MIX ? rest_of(d[i][c]) * lam : lam;
-                                dg[c] = v[c] * (MIX ? h[c] - x[c] : h[c]);
-                            }
-                            Lane<T>::put(out0 + static_cast<int64_t>(i) * p.D, dx);
-                            Lane<T>::put(out1 + static_cast<int64_t>(i) * p.D, dg);
-                        }
+                T *out0 = static_cast<T *>(p.out0) + at;
+                [[maybe_unused]] T *out1 = static_cast<T *>(p.out1) + at;
+                auto row = [&](int i) {
+                    const V u = L::get(src + kTileBytes + i * 128);
+                    if constexpr (!BWD) {
+                        v = fma(keep_of<KIND>(d[i]), v, MIX ? mul(rest_of(d[i]), u) : u);
+                        L::put(out0 + static_cast<int64_t>(i) * p.D, v);
+                    } else {
+                        V h = L::get(src + 2 * kTileBytes + i * 128);
+                        if (i == 0 && warp == 0) h = before;
+                        if (MIX) h = fma(L::get(src + (MIX ? 3 : 0) * kTileBytes + i * 128), L::all(-1.f), h);
+                        const V lam = add(u, v);
+                        v = mul(keep_of<KIND>(d[i]), lam);
+                        L::put(out0 + static_cast<int64_t>(i) * p.D, MIX ? mul(rest_of(d[i]), lam) : lam);
+                        L::put(out1 + static_cast<int64_t>(i) * p.D, mul(v, h));
                     }
+                };
+                if (mine == kWarpRows) {
+#pragma unroll
+                    for (int k = 0; k < kWarpRows; ++k) row(BWD ? kWarpRows - 1 - k : k);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kWarpRows; ++k)
+                        if ((BWD ? kWarpRows - 1 - k : k) < mine) row(BWD ? kWarpRows - 1 - k : k);
                 }
                 if (!BWD && p.final_state && meta[s].t.seq_end >= 0 && meta[s].t.at == meta[s].t.count - 1 && mine > 0 &&
-                    rows - warp * kWarpRows <= kWarpRows) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) p.final_state[static_cast<int64_t>(meta[s].t.seq_end) * p.D + ch + c] = v[c];
-                }
+                    rows - warp * kWarpRows <= kWarpRows)
+                    L::store(p.final_state + static_cast<int64_t>(meta[s].t.seq_end) * p.D + ch, v);
             }
             __syncwarp();
             if (lane == 0) arrive(&empty[s]);
@@ -446,28 +445,24 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
 // Every segment a root of one row (a decoding step): row, root and sequence have one number.
 template <typename T, bool BWD, bool MIX>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanParams p, const T *g, const T *u, const T *x, int64_t n) {
-    constexpr int CH = Lane<T>::n;
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * CH;
+    using L = Lane<T>;
+    using V = typename L::V;
+    constexpr int KIND = MIX ? kBoth : kExact;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * L::n;
     if (i >= n) return;
-    float gv[CH], uv[CH], xv[CH], o0[CH], o1[CH];
-    Lane<T>::get(reinterpret_cast<const uint8_t *>(g + i), gv);
-    Lane<T>::get(reinterpret_cast<const uint8_t *>(u + i), uv);
-    if (BWD && MIX) Lane<T>::get(reinterpret_cast<const uint8_t *>(x + i), xv);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const float d = decay<true>(gv[c]), a = keep_of<true>(d), h = p.h0 ? p.h0[i + c] : 0.f;
-        if (!BWD) {
-            o0[c] = fmaf(a, h, MIX ? rest_of(d) * uv[c] : uv[c]);
-            if (p.final_state) p.final_state[i + c] = o0[c];
-        } else {
-            const float lam = uv[c] + (p.d_final ? p.d_final[i + c] : 0.f);
-            o0[c] = MIX ? rest_of(d) * lam : lam;
-            o1[c] = a * lam * (MIX ? h - xv[c] : h);
-            if (p.dh0) p.dh0[i + c] = a * lam;
-        }
+    const V d = decay<KIND, T>(L::get(g + i)), a = keep_of<KIND>(d), in = L::get(u + i);
+    V h = p.h0 ? L::load(p.h0 + i) : L::all(0.f);
+    if constexpr (!BWD) {
+        const V o = fma(a, h, MIX ? mul(rest_of(d), in) : in);
+        L::put(static_cast<T *>(p.out0) + i, o);
+        if (p.final_state) L::store(p.final_state + i, o);
+    } else {
+        const V lam = p.d_final ? add(in, L::load(p.d_final + i)) : in, c = mul(a, lam);
+        if (MIX) h = fma(L::get(x + i), L::all(-1.f), h);
+        L::put(static_cast<T *>(p.out0) + i, MIX ? mul(rest_of(d), lam) : lam);
+        L::put(static_cast<T *>(p.out1) + i, mul(c, h));
+        if (p.dh0) L::store(p.dh0 + i, c);
     }
-    Lane<T>::put(static_cast<T *>(p.out0) + i, o0);
-    if (BWD) Lane<T>::put(static_cast<T *>(p.out1) + i, o1);
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -497,11 +492,11 @@ template <typename T> bool map_rows(CUtensorMap *m, const void *base, int64_t C,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool BWD, bool MIX, bool PRECISE>
+template <typename T, bool BWD, bool MIX, int KIND>
 cudaError_t launch_scan(const ScanParams &p, cudaStream_t st) {
     using R = Ring<BWD, MIX>;
     static std::atomic<uint64_t> done{0};
-    auto *k = scan_kernel<T, BWD, MIX, PRECISE>;
+    auto *k = scan_kernel<T, BWD, MIX, KIND>;
     const cudaError_t e = allow_smem(k, R::smem, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = std::min<int64_t>(p.total, int64_t(sm_count()) * R::blocks);
@@ -524,12 +519,11 @@ cudaError_t run(const harts_plan *P, ScanParams &p, const void *const (&in)[4], 
         if (e != cudaSuccess) return e;
     }
     if constexpr (!MIX && std::is_same<T, __nv_bfloat16>::value)
-        if (!precise) return launch_scan<T, BWD, MIX, false>(p, st);
-    return launch_scan<T, BWD, MIX, true>(p, st);
+        if (!precise) return launch_scan<T, BWD, MIX, kFast>(p, st);
+    return launch_scan<T, BWD, MIX, MIX ? kBoth : kExact>(p, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 int check(const harts_plan *P, const harts_scan_fwd_args *a) {
     if (!P || !a) { set_error("NULL plan or args"); return HARTS_EINVAL; }
@@ -543,7 +537,7 @@ int check(const harts_plan *P, const harts_scan_fwd_args *a) {
         return HARTS_EINVAL;
     }
     if (a->h == a->x || a->h == a->g) { set_error("h may be neither x nor g"); return HARTS_EINVAL; }
-    if (!aligned4(a->h0) || !aligned4(a->final_state)) { set_error("h0 and final_state must be aligned to their type"); return HARTS_EINVAL; }
+    if (!aligned16(a->h0) || !aligned16(a->final_state)) { set_error("h0 and final_state must be 16-byte aligned"); return HARTS_EINVAL; }
     if (P->info.C > (int64_t(1) << 38) / a->channels) { set_error("tensor too large"); return HARTS_EOVERFLOW; }
     if (int64_t(P->image.n_scan) * ceil_div(a->channels, wide_of(a->dtype)) > 0x7fffffff) {
         set_error("more tiles than the library counts");
@@ -626,7 +620,7 @@ int harts_scan_bwd(const harts_plan *P, const harts_scan_bwd_args *a, harts_stre
     const void *const in_use[] = {a->fwd.x, a->fwd.g, a->fwd.h, a->d_h};
     for (const void *q : in_use)
         if (a->dx == q || a->dg == q || a->dx == a->dg) { set_error("dx and dg may be none of the inputs"); return HARTS_EINVAL; }
-    if (!aligned4(a->d_final) || !aligned4(a->dh0)) { set_error("d_final and dh0 must be aligned to their type"); return HARTS_EINVAL; }
+    if (!aligned16(a->d_final) || !aligned16(a->dh0)) { set_error("d_final and dh0 must be 16-byte aligned"); return HARTS_EINVAL; }
     ScanParams p = params_of(P, &a->fwd, true);
     p.h_in = a->fwd.h;
     p.out0 = a->dx;
