@@ -33,16 +33,16 @@ namespace {
 constexpr int kWarps = 8, kWarpRows = kScanRows / kWarps;      // consumers
 constexpr int kThreads = 32 * (kWarps + 2);                    // and a warp each for carries and copies
 constexpr int kAtOnce = 8;                                     // maps that are fetched at a time
-constexpr int kBox = 16;                                       // rows of one copy
+constexpr int kBox = 32;                                       // rows of one copy
 constexpr uint32_t kTileBytes = kScanRows * 128;               // of one tensor
 constexpr uint32_t kEmpty = 0xffffffffu;                       // not published yet
 
 struct ScanParams {
-    CUtensorMap map[4];             // forward g, x; backward g, dh, h, x (mix)
+    CUtensorMap map[3];             // forward g, x; backward g, dh, h
     const ScanTile *tiles;
     const int32_t *next;
     const float *h0, *d_final;
-    const void *h_in;               // backward: h
+    const void *h_in, *x_in;        // backward: h, x
     void *out0, *out1;              // forward h; backward dx, dg
     float *final_state, *dh0;
     uint32_t *ticket;               // nullptr: tiles that wait for nothing are dealt out in turn
@@ -113,11 +113,13 @@ template <> struct Lane<float> {
 // e^g for g <= 0, as one number that gives both a and 1 - a with few roundings.  2^y = 2^n 2^f with
 // |f| <= 1/2 and the series of e^(f ln 2) to its seventh power (the next term is 5e-9); below
 // 2^-126.5, zero.  Memories of a thousand rows multiply a thousand decays: an approximate
-// exponential's 2^-22 would be 2e-4 of the state.  KIND kExact keeps a; kBoth keeps a below
-// 2^(-1/2), and above it -(1 - a), its sign bit set, from the series, as 1 - a would lose what the
-// rounding of a took.  kFast, the hardware's exponential, is for results that are all bf16, which
+// exponential's 2^-22 would be 2e-4 of the state.  kExact keeps a.  kRest keeps 1 - a, which the
+// rounding of an a near 1 would take most digits of: 2^n (1 + t) with t the series gives it as
+// (1 - 2^n) - 2^n t, rounded once; a is then 1 - (1 - a), off by 2^-25 at most.  kBoth, for the mix
+// form's gradients, which have a as a factor, keeps a below 2^(-1/2) and -(1 - a), its sign bit set,
+// from there up.  kFast, the hardware's exponential, is for results that are all bf16, which
 // rounds to 2^-9, in the add form.
-enum Kind { kFast, kExact, kBoth };
+enum Kind { kFast, kExact, kRest, kBoth };
 template <int KIND, typename T> __device__ __forceinline__ typename Lane<T>::V decay(typename Lane<T>::V g) {
     using L = Lane<T>;
     if constexpr (KIND == kFast) return each(mul(g, L::all(1.4426950408889634f)), [](float y) { return ex2(y); });
@@ -129,25 +131,29 @@ template <int KIND, typename T> __device__ __forceinline__ typename Lane<T>::V d
     const auto z = fma(g, L::all(1.4426950408889634f), L::all(12582912.f));        // its low bits are n
     const auto n = fma(z, L::all(-1.f), L::all(12582912.f));                       // -n
     const auto f = fma(g, L::all(1.4426950408889634f), n);
-    auto q = L::all(1.5252733804e-5f);
-    q = fma(q, f, L::all(1.5403530394e-4f));
-    q = fma(q, f, L::all(1.3333558146e-3f));
-    q = fma(q, f, L::all(9.6181291076e-3f));
-    q = fma(q, f, L::all(5.5504108665e-2f));
-    q = fma(q, f, L::all(2.4022650696e-1f));
-    q = fma(q, f, L::all(6.9314718056e-1f));
-    const auto t = mul(q, f);
+    constexpr float sign = KIND == kExact ? 1.f : -1.f;
+    auto q = L::all(sign * 1.5252733804e-5f);
+    q = fma(q, f, L::all(sign * 1.5403530394e-4f));
+    q = fma(q, f, L::all(sign * 1.3333558146e-3f));
+    q = fma(q, f, L::all(sign * 9.6181291076e-3f));
+    q = fma(q, f, L::all(sign * 5.5504108665e-2f));
+    q = fma(q, f, L::all(sign * 2.4022650696e-1f));
+    q = fma(q, f, L::all(sign * 6.9314718056e-1f));
+    const auto t = mul(q, f);                                                      // times the sign
     const auto scale = each(z, [](float v) { return __uint_as_float((__float_as_uint(v) << 23) + 0x3f800000u); });
-    const auto a = fma(t, scale, scale);
-    if constexpr (KIND == kExact) return a;
-    return each(t, each(a, z, [](float u, float v) { return v == 12582912.f ? __uint_as_float(0xff800000u) : u; }),
-                [](float d, float u) { return __float_as_uint(u) == 0xff800000u ? -fabsf(d) : u; });
+    if constexpr (KIND == kExact) return fma(t, scale, scale);
+    const auto rest = fma(t, scale, fma(scale, L::all(-1.f), L::all(1.f)));
+    if constexpr (KIND == kRest) return rest;
+    const auto a = fma(mul(t, L::all(-1.f)), scale, scale);
+    return each(a, rest, [](float u, float r) { return u < 0.70710678f ? u : __uint_as_float(__float_as_uint(r) | 0x80000000u); });
 }
 template <int KIND, typename V> __device__ __forceinline__ V keep_of(V v) {      // a
-    if constexpr (KIND != kBoth) return v;
-    return each(v, [](float u) { return __float_as_int(u) < 0 ? 1.f + u : u; });  // (a NaN stays one)
+    if constexpr (KIND == kRest) return each(v, [](float u) { return 1.f - u; });
+    if constexpr (KIND == kBoth) return each(v, [](float u) { return __float_as_int(u) < 0 ? 1.f + u : u; });
+    return v;
 }
-template <typename V> __device__ __forceinline__ V rest_of(V v) {                // 1 - a
+template <int KIND, typename V> __device__ __forceinline__ V rest_of(V v) {      // 1 - a
+    if constexpr (KIND == kRest) return v;
     return each(v, [](float u) { return __float_as_int(u) < 0 ? -u : 1.f - u; });
 }
 
@@ -198,9 +204,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f)
 // Tensors of a tile, stages of the ring and blocks of an SM: as many bytes on their way as shared
 // memory holds.
 template <bool BWD, bool MIX> struct Ring {
-    static constexpr int tensors = BWD ? (MIX ? 4 : 3) : 2;
-    static constexpr int stages = BWD && MIX ? 3 : 2;
-    static constexpr int blocks = BWD ? (MIX ? 1 : 2) : 3;
+    static constexpr int tensors = BWD ? 3 : 2, stages = 2, blocks = BWD ? 2 : 3;
     static constexpr uint32_t stage_bytes = tensors * kTileBytes;
     static constexpr uint32_t smem = stages * stage_bytes + 128;
 };
@@ -379,13 +383,22 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
                 if (pr >= 0) before = L::get(static_cast<const T *>(p.h_in) + static_cast<int64_t>(pr) * p.D + ch);
                 else if (p.h0) before = L::load(p.h0 + static_cast<int64_t>(-1 - pr) * p.D + ch);
             }
+            // the mix form's x, wanted last and by one thread only, does not go through shared memory,
+            // which has room for two blocks' other tensors
+            [[maybe_unused]] uint32_t xr[BWD && MIX ? kWarpRows : 1];
+            if constexpr (BWD && MIX) {
+                const T *xp = static_cast<const T *>(p.x_in) + static_cast<int64_t>(row0 + warp * kWarpRows) * p.D + ch;
+#pragma unroll
+                for (int i = 0; i < kWarpRows; ++i)
+                    xr[i] = i < mine && ch < p.D ? __ldcs(reinterpret_cast<const uint32_t *>(xp + static_cast<int64_t>(i) * p.D)) : 0u;
+            }
             V d[kWarpRows], A = L::all(1.f), B = L::all(0.f);
             auto map_row = [&](int i) {
                 const V u = L::get(src + kTileBytes + i * 128);
                 d[i] = decay<KIND, T>(L::get(src + i * 128));
                 const V a = keep_of<KIND>(d[i]);
                 if (BWD) B = mul(a, add(u, B));
-                else B = fma(a, B, MIX ? mul(rest_of(d[i]), u) : u);
+                else B = fma(a, B, MIX ? mul(rest_of<KIND>(d[i]), u) : u);
                 A = mul(A, a);
             };
             if (mine == kWarpRows) {
@@ -410,15 +423,15 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
                 auto row = [&](int i) {
                     const V u = L::get(src + kTileBytes + i * 128);
                     if constexpr (!BWD) {
-                        v = fma(keep_of<KIND>(d[i]), v, MIX ? mul(rest_of(d[i]), u) : u);
+                        v = fma(keep_of<KIND>(d[i]), v, MIX ? mul(rest_of<KIND>(d[i]), u) : u);
                         L::put(out0 + static_cast<int64_t>(i) * p.D, v);
                     } else {
                         V h = L::get(src + 2 * kTileBytes + i * 128);
                         if (i == 0 && warp == 0) h = before;
-                        if (MIX) h = fma(L::get(src + (MIX ? 3 : 0) * kTileBytes + i * 128), L::all(-1.f), h);
+                        if (MIX) h = fma(L::get(&xr[MIX ? i : 0]), L::all(-1.f), h);
                         const V lam = add(u, v);
                         v = mul(keep_of<KIND>(d[i]), lam);
-                        L::put(out0 + static_cast<int64_t>(i) * p.D, MIX ? mul(rest_of(d[i]), lam) : lam);
+                        L::put(out0 + static_cast<int64_t>(i) * p.D, MIX ? mul(rest_of<KIND>(d[i]), lam) : lam);
                         L::put(out1 + static_cast<int64_t>(i) * p.D, mul(v, h));
                     }
                 };
@@ -447,19 +460,19 @@ template <typename T, bool BWD, bool MIX>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanParams p, const T *g, const T *u, const T *x, int64_t n) {
     using L = Lane<T>;
     using V = typename L::V;
-    constexpr int KIND = MIX ? kBoth : kExact;
+    constexpr int KIND = !MIX ? kExact : BWD ? kBoth : kRest;
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * L::n;
     if (i >= n) return;
     const V d = decay<KIND, T>(L::get(g + i)), a = keep_of<KIND>(d), in = L::get(u + i);
     V h = p.h0 ? L::load(p.h0 + i) : L::all(0.f);
     if constexpr (!BWD) {
-        const V o = fma(a, h, MIX ? mul(rest_of(d), in) : in);
+        const V o = fma(a, h, MIX ? mul(rest_of<KIND>(d), in) : in);
         L::put(static_cast<T *>(p.out0) + i, o);
         if (p.final_state) L::store(p.final_state + i, o);
     } else {
         const V lam = p.d_final ? add(in, L::load(p.d_final + i)) : in, c = mul(a, lam);
         if (MIX) h = fma(L::get(x + i), L::all(-1.f), h);
-        L::put(static_cast<T *>(p.out0) + i, MIX ? mul(rest_of(d), lam) : lam);
+        L::put(static_cast<T *>(p.out0) + i, MIX ? mul(rest_of<KIND>(d), lam) : lam);
         L::put(static_cast<T *>(p.out1) + i, mul(c, h));
         if (p.dh0) L::store(p.dh0 + i, c);
     }
@@ -520,7 +533,7 @@ cudaError_t run(const harts_plan *P, ScanParams &p, const void *const (&in)[4], 
     }
     if constexpr (!MIX && std::is_same<T, __nv_bfloat16>::value)
         if (!precise) return launch_scan<T, BWD, MIX, kFast>(p, st);
-    return launch_scan<T, BWD, MIX, MIX ? kBoth : kExact>(p, st);
+    return launch_scan<T, BWD, MIX, !MIX ? kExact : BWD ? kBoth : kRest>(p, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -623,6 +636,7 @@ int harts_scan_bwd(const harts_plan *P, const harts_scan_bwd_args *a, harts_stre
     if (!aligned16(a->d_final) || !aligned16(a->dh0)) { set_error("d_final and dh0 must be 16-byte aligned"); return HARTS_EINVAL; }
     ScanParams p = params_of(P, &a->fwd, true);
     p.h_in = a->fwd.h;
+    p.x_in = a->fwd.x;
     p.out0 = a->dx;
     p.out1 = a->dg;
     p.d_final = a->d_final;

@@ -7,7 +7,8 @@ product and sum, one product of decays, and its share of the joins (one in 16 ro
 at most 12 u of a S + |b| in all, S the same recurrence over absolute values, and what a row is off
 by is carried on like the state: E = a E_before + 12 u (a S_before + |b|).  bf16 results of the add
 form take the hardware's exponential, 2^-22 or 4 u, of a product that is off by |g| u: 16 u more, and
-a |g| <= 1/e of them.  The backward's lam goes the same way from the leaves, and dx, dg are products
+a |g| <= 1/e of them.  The mix form's forward takes a from 1 - a, which leaves it off by 2^-25 however
+small it is: u S_before more.  The backward's lam goes the same way from the leaves, and dx, dg are products
 of it with up to four roundings more."""
 import numpy as np
 import pytest
@@ -95,10 +96,11 @@ class Case:
         b = np.abs(-np.expm1(g) * x if mix else x)
         size, before = scan_forest(self.parent, self.len, self.off, b, g, False, None if h0 is None else np.abs(h0))
         step = K[self.dtype] * U
-        err, _ = scan_forest(self.parent, self.len, self.off, step * (np.exp(g) * before + b), g, False)
+        own = U * before if mix else 0.0
+        err, _ = scan_forest(self.parent, self.len, self.off, step * (np.exp(g) * before + b) + own, g, False)
         assert np.all(np.abs(_np(h) - ref) <= self.r * np.abs(ref) + err + 1e-37)
         if self.state:
-            err, _ = scan_forest(self.parent, self.len, self.off, 12 * U * (np.exp(g) * before + b), g, False)
+            err, _ = scan_forest(self.parent, self.len, self.off, 12 * U * (np.exp(g) * before + b) + own, g, False)
             assert np.all(np.abs(_np(final) - ref[self.last]) <= err[self.last] + 1e-37)
         return h
 
