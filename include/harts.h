@@ -563,6 +563,70 @@ size_t harts_rmsnorm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype);
 int harts_rmsnorm_bwd(const harts_rmsnorm_bwd_args *args, harts_stream_t stream);
 
 /* ------------------------------------------------------------------------------ */
+/* The norms around a block, with its gate and the residual's scaled addition.    */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * Per row, between a block's output y and the next block's input n:
+ *   u = y / sqrt(mean_j y_j^2 + eps) * post_weight        (u = y where post_weight is NULL)
+ *   h = residual + scale * act(gate) * u                  (1 for a gate, 0 for a residual that is NULL)
+ *   n = h / sqrt(mean_j h_j^2 + eps) * pre_weight         (none where pre_weight is NULL)
+ * with at least one of the norms.  Without a residual and a second norm this is the gated norm of
+ * an attention's or a recurrence's heads (C rows and heads, D a head's channels).  act is
+ * HARTS_GATE_LINEAR (the gate itself), HARTS_GATE_SILU (z sigmoid(z)) or HARTS_GATE_SIGMOID.
+ * Statistics are fp32; h is normalised before it is rounded to `dtype`.  A row whose sum of squares
+ * overflows gets rstd 0.  h and n may each be y, gate or residual (rows are read before they are
+ * written), but not one buffer.
+ */
+#define HARTS_GATE_LINEAR 0
+#define HARTS_GATE_SILU 1
+#define HARTS_GATE_SIGMOID 2
+
+typedef struct {
+    int64_t C;               /* rows, >= 0 */
+    int32_t D;               /* channels, 1 .. 8192 */
+    int32_t dtype;           /* harts_dtype of y, gate, residual, h, n */
+    int32_t gate_act;        /* HARTS_GATE_*; 0 without a gate */
+    float scale;             /* of the gated block, finite */
+    float eps;               /* >= 0; not used by the backward */
+    const void *y;           /* device [C][D], 16-byte aligned (so are all [C][D] and the weights) */
+    const void *gate;        /* device [C][D], or NULL */
+    const void *residual;    /* device [C][D], or NULL; not used by the backward */
+    const float *post_weight;/* device [D] fp32, or NULL: no norm of y */
+    const float *pre_weight; /* device [D] fp32, or NULL: no n */
+    void *h;                 /* device [C][D]: written by the forward; the backward reads it with a pre_weight */
+    void *n;                 /* device [C][D] output, given exactly when pre_weight is; not used by the backward */
+    float *rstd_post;        /* device [C]: written by the forward (or NULL), read by the backward; with post_weight */
+    float *rstd_pre;         /* device [C]: the same with pre_weight */
+    int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out; cleared by the caller.
+                                NULL: the library's own word (harts_device_error) */
+} harts_block_norm_args;
+
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, no norm, negative C, scale, eps,
+ * gate_act), HARTS_EUNSUPPORTED (dtype, D above 8192), HARTS_ECUDA. */
+int harts_block_norm_fwd(const harts_block_norm_args *args, harts_stream_t stream);
+
+typedef struct {
+    harts_block_norm_args fwd;  /* as for the forward, with what it wrote */
+    const void *d_n;         /* device [C][D] dL/dn, given exactly when pre_weight is */
+    const void *d_h;         /* device [C][D] dL/dh along the residual stream, or NULL (then d_n is there) */
+    void *dy;                /* device [C][D] output; the outputs may each be an input, but not one buffer */
+    void *dresidual;         /* device [C][D] output: the whole gradient of h, or NULL */
+    void *dgate;             /* device [C][D] output, or NULL */
+    float *dpost_weight;     /* device [D] output with post_weight (overwritten; zero when C is 0) */
+    float *dpre_weight;      /* device [D] output with pre_weight */
+    void *workspace;         /* device, harts_block_norm_bwd_workspace_bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} harts_block_norm_bwd_args;
+
+/* Workspace of the backward: fp32 column sums; 0 for invalid arguments. */
+size_t harts_block_norm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype);
+
+/* Backward.  The weights' gradients are summed in a fixed order (no atomics).  Errors as the
+ * forward, plus HARTS_ESMALLBUF (workspace). */
+int harts_block_norm_bwd(const harts_block_norm_bwd_args *args, harts_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
 /* The gradients' global norm, and clipping.                                      */
 /* ------------------------------------------------------------------------------ */
 

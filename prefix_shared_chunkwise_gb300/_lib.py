@@ -15,6 +15,7 @@ HARTS_KERNEL_AUTO, HARTS_KERNEL_SIMT, HARTS_KERNEL_TC = 0, 1, 2
 HARTS_PLAN_NODEWISE = 1                       # harts_plan_calls flags
 HARTS_PLAN_NOREPLAY = 2
 HARTS_SCAN_ADD, HARTS_SCAN_MIX = 0, 1
+HARTS_GATE_LINEAR, HARTS_GATE_SILU, HARTS_GATE_SIGMOID = 0, 1, 2
 
 ERRORS = {0: "HARTS_OK", -1: "HARTS_EINVAL", -2: "HARTS_EUNSUPPORTED", -3: "HARTS_EOVERFLOW",
           -4: "HARTS_ESMALLBUF", -5: "HARTS_ECUDA", -6: "HARTS_ETIMEOUT", -7: "HARTS_EDEVICE",
@@ -33,6 +34,7 @@ EXPORTED = [
     "harts_linear_logprob_fwd_workspace_bytes", "harts_linear_logprob_fwd",
     "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_device_error",
     "harts_scan_workspace_bytes", "harts_scan_fwd", "harts_scan_bwd",
+    "harts_block_norm_fwd", "harts_block_norm_bwd_workspace_bytes", "harts_block_norm_bwd",
     "harts_last_error",
 ]
 
@@ -144,6 +146,17 @@ class ScanBwdArgs(ctypes.Structure):
     _fields_ = [("fwd", ScanFwdArgs), ("d_h", _vp), ("d_final", _vp), ("dx", _vp), ("dg", _vp), ("dh0", _vp)]
 
 
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("C", _i64), ("D", _i32), ("dtype", _i32), ("gate_act", _i32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("y", _vp), ("gate", _vp), ("residual", _vp), ("post_weight", _vp),
+                ("pre_weight", _vp), ("h", _vp), ("n", _vp), ("rstd_post", _vp), ("rstd_pre", _vp), ("error", _vp)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", BlockNormArgs), ("d_n", _vp), ("d_h", _vp), ("dy", _vp), ("dresidual", _vp), ("dgate", _vp),
+                ("dpost_weight", _vp), ("dpre_weight", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -222,6 +235,12 @@ def lib():
         L.harts_scan_fwd.restype = ctypes.c_int
         L.harts_scan_bwd.argtypes = [_vp, ctypes.POINTER(ScanBwdArgs), _vp]
         L.harts_scan_bwd.restype = ctypes.c_int
+        L.harts_block_norm_fwd.argtypes = [ctypes.POINTER(BlockNormArgs), _vp]
+        L.harts_block_norm_fwd.restype = ctypes.c_int
+        L.harts_block_norm_bwd_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.harts_block_norm_bwd_workspace_bytes.restype = _sz
+        L.harts_block_norm_bwd.argtypes = [ctypes.POINTER(BlockNormBwdArgs), _vp]
+        L.harts_block_norm_bwd.restype = ctypes.c_int
         L.harts_device_error.argtypes = [_vp, ctypes.POINTER(_i32)]
         L.harts_device_error.restype = ctypes.c_int
         L.harts_last_error.argtypes = []

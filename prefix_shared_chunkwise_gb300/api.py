@@ -12,7 +12,8 @@ from . import _lib as L
 
 __all__ = ["Plan", "kda_fwd", "kda_bwd", "conv_fwd", "conv_bwd", "semantic_map", "logprob_fwd",
            "logprob_bwd", "attn_fwd", "attn_bwd", "linear_logprob_fwd", "linear_logprob_bwd",
-           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "scan_fwd", "scan_bwd", "device_error", "dtype_code"]
+           "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "scan_fwd", "scan_bwd",
+           "block_norm_fwd", "block_norm_bwd", "device_error", "dtype_code"]
 
 
 def dtype_code(torch_dtype):
@@ -701,3 +702,110 @@ def scan_bwd(plan: Plan, x, g, h, d_h, *, form="add", h0=None, d_final=None, dx=
                       None if dh0 is None else dh0.data_ptr())
     L.check(L.lib().harts_scan_bwd(plan.handle, ctypes.byref(a), _stream_on(stream, x)), "harts_scan_bwd")
     return dx, dg
+
+
+_GATES = {"linear": L.HARTS_GATE_LINEAR, "silu": L.HARTS_GATE_SILU, "sigmoid": L.HARTS_GATE_SIGMOID}
+
+
+def _gate_act(gate, gate_act):
+    if gate is None:
+        return L.HARTS_GATE_LINEAR
+    if gate_act not in _GATES:
+        raise ValueError(f"gate_act {gate_act!r} is none of {sorted(_GATES)}")
+    return _GATES[gate_act]
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+@_made_on_stream
+def block_norm_fwd(y, *, post_weight=None, gate=None, gate_act="silu", scale=1.0, residual=None, pre_weight=None,
+                   eps=1e-6, h=None, n=None, rstd_post=None, rstd_pre=None, error=None, stream=None):
+    """harts_block_norm_fwd: what lies between a block's output y [C, D] (bf16 or fp32) and the next
+    block's input, in one pass: u = rms_norm(y) * post_weight (u = y without one), h = residual +
+    scale * act(gate) * u, n = rms_norm(h) * pre_weight.  Weights are [D] fp32, at least one of them;
+    gate, residual: like y, or None; gate_act: "linear", "silu" or "sigmoid".  Returns (h, n,
+    rstd_post [C] fp32, rstd_pre [C] fp32), None for what there is none of.  h and n may each be
+    given as y, gate or residual (in place).  error: as linear_logprob_fwd's."""
+    import torch
+    shape, dt, dev, f32 = y.shape, y.dtype, y.device, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"y has shape {tuple(shape)}, expected [C, D]")
+    C, D = shape
+    code, act = dtype_code(dt), _gate_act(gate, gate_act)
+    _ready("y", y, None, dt, dev)
+    _ready("gate", gate, shape, dt, dev)
+    _ready("residual", residual, shape, dt, dev)
+    _ready("post_weight", post_weight, (D,), f32, dev)
+    _ready("pre_weight", pre_weight, (D,), f32, dev)
+    _need("error", error, None, torch.int32, 4, dev)
+    if h is None:
+        h = torch.empty_like(y)
+    else:
+        _ready("h", h, shape, dt, dev)
+    if pre_weight is None:
+        if n is not None or rstd_pre is not None:
+            raise ValueError("n and rstd_pre go with pre_weight")
+    else:
+        n = torch.empty_like(y) if n is None else n
+        rstd_pre = torch.empty(C, dtype=f32, device=dev) if rstd_pre is None else rstd_pre
+        _ready("n", n, shape, dt, dev)
+        _ready("rstd_pre", rstd_pre, (C,), f32, dev)
+    if post_weight is None:
+        if rstd_post is not None:
+            raise ValueError("rstd_post goes with post_weight")
+    elif rstd_post is None:
+        rstd_post = torch.empty(C, dtype=f32, device=dev)
+    else:
+        _ready("rstd_post", rstd_post, (C,), f32, dev)
+    a = L.BlockNormArgs(C, D, code, act, scale, eps, y.data_ptr(), _at(gate), _at(residual), _at(post_weight),
+                        _at(pre_weight), h.data_ptr(), _at(n), _at(rstd_post), _at(rstd_pre), _at(error))
+    L.check(L.lib().harts_block_norm_fwd(ctypes.byref(a), _stream_on(stream, y)), "harts_block_norm_fwd")
+    return h, n, rstd_post, rstd_pre
+
+
+@_made_on_stream
+def block_norm_bwd(y, h, d_n, d_h=None, *, post_weight=None, gate=None, gate_act="silu", scale=1.0, pre_weight=None,
+                   rstd_post=None, rstd_pre=None, dy=None, dresidual=None, dgate=None, dpost_weight=None,
+                   dpre_weight=None, error=None, workspace=None, stream=None):
+    """harts_block_norm_bwd: from the forward's inputs, its h (only read with a pre_weight) and rstds,
+    dL/dn (d_n, None without a pre_weight) and dL/dh along the residual stream (d_h, or None).
+    Returns dict(dy, dresidual, dgate, dpost_weight, dpre_weight), None for what there is none of.
+    dresidual is the whole gradient of h; without a pre_weight that is d_h, and None is returned
+    unless a buffer is given."""
+    import torch
+    shape, dt, dev, f32 = y.shape, y.dtype, y.device, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"y has shape {tuple(shape)}, expected [C, D]")
+    C, D = shape
+    code, act = dtype_code(dt), _gate_act(gate, gate_act)
+    _ready("y", y, None, dt, dev)
+    for name, t in (("h", h), ("d_n", d_n), ("d_h", d_h), ("gate", gate)):
+        _ready(name, t, shape, dt, dev)
+    _ready("post_weight", post_weight, (D,), f32, dev)
+    _ready("pre_weight", pre_weight, (D,), f32, dev)
+    _ready("rstd_post", rstd_post, (C,), f32, dev)
+    _ready("rstd_pre", rstd_pre, (C,), f32, dev)
+    _need("error", error, None, torch.int32, 4, dev)
+    dy = torch.empty_like(y) if dy is None else dy
+    if dresidual is None and pre_weight is not None:
+        dresidual = torch.empty_like(y)
+    if dgate is None and gate is not None:
+        dgate = torch.empty_like(y)
+    if dpost_weight is None and post_weight is not None:
+        dpost_weight = torch.empty(D, dtype=f32, device=dev)
+    if dpre_weight is None and pre_weight is not None:
+        dpre_weight = torch.empty(D, dtype=f32, device=dev)
+    for name, t in (("dy", dy), ("dresidual", dresidual), ("dgate", dgate)):
+        _ready(name, t, shape, dt, dev)
+    _ready("dpost_weight", dpost_weight, (D,), f32, dev)
+    _ready("dpre_weight", dpre_weight, (D,), f32, dev)
+    lib = L.lib()
+    workspace, nb = _workspace(workspace, lib.harts_block_norm_bwd_workspace_bytes(C, D, code), dev)
+    f = L.BlockNormArgs(C, D, code, act, scale, 0.0, y.data_ptr(), _at(gate), None, _at(post_weight), _at(pre_weight),
+                        _at(y if h is None and pre_weight is None else h), None, _at(rstd_post), _at(rstd_pre), _at(error))
+    a = L.BlockNormBwdArgs(f, _at(d_n), _at(d_h), dy.data_ptr(), _at(dresidual), _at(dgate), _at(dpost_weight),
+                           _at(dpre_weight), workspace.data_ptr(), nb)
+    L.check(lib.harts_block_norm_bwd(ctypes.byref(a), _stream_on(stream, y)), "harts_block_norm_bwd")
+    return dict(dy=dy, dresidual=dresidual, dgate=dgate, dpost_weight=dpost_weight, dpre_weight=dpre_weight)

@@ -28,10 +28,13 @@
 
 #include "kda_common.cuh"
 #include "launch_util.h"
+#include "rows.cuh"
 #include "tc_primitives.cuh"
 
 namespace harts {
 namespace {
+
+using namespace rows;
 
 constexpr int kMaxDim = 16384;      // 1024 threads x 16 values
 constexpr int kMxBlock = 32;        // channels that share a scale
@@ -59,87 +62,9 @@ struct NormBwd {
     int32_t D;
 };
 
-template <typename T, int VEC> struct Raw;      // VEC values of T as they lie in memory
-template <> struct Raw<__nv_bfloat16, 8> { uint4 u; };
-template <> struct Raw<float, 4> { float4 u; };
-template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 u; };
-template <> struct Raw<float, 1> { float u; };
-
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8> &r, float *v) {
-    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&r.u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(p[i]);
-        v[2 * i] = f.x; v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void unpack(const Raw<float, 4> &r, float *v) {
-    v[0] = r.u.x; v[1] = r.u.y; v[2] = r.u.z; v[3] = r.u.w;
-}
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 1> &r, float *v) { v[0] = __bfloat162float(r.u); }
-__device__ __forceinline__ void unpack(const Raw<float, 1> &r, float *v) { v[0] = r.u; }
-
-__device__ __forceinline__ void pack(Raw<__nv_bfloat16, 8> &r, const float *v) {
-    __nv_bfloat162 *p = reinterpret_cast<__nv_bfloat162 *>(&r.u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-}
-__device__ __forceinline__ void pack(Raw<float, 4> &r, const float *v) { r.u = make_float4(v[0], v[1], v[2], v[3]); }
-__device__ __forceinline__ void pack(Raw<__nv_bfloat16, 1> &r, const float *v) { r.u = __float2bfloat16_rn(v[0]); }
-__device__ __forceinline__ void pack(Raw<float, 1> &r, const float *v) { r.u = v[0]; }
-
-template <typename T, int VEC>
-__device__ __forceinline__ Raw<T, VEC> ld(const void *p, int64_t i) {
-    return *reinterpret_cast<const Raw<T, VEC> *>(static_cast<const T *>(p) + i);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void st(void *p, int64_t i, const float *v) {
-    Raw<T, VEC> r;
-    pack(r, v);
-    *reinterpret_cast<Raw<T, VEC> *>(static_cast<T *>(p) + i) = r;
-}
-
-constexpr int block_of(int R) { return R < 128 ? 128 : R; }     // threads of a block
-constexpr int rows_of(int R) { return block_of(R) / R; }        // rows it works on at a time
 // Weights (and dw's sums) of a thread's columns stay in registers up to this many values;
 // beyond, weights come from L1.
 constexpr int kRegValues = 16;
-
-// Sum over the R threads of a row.  sm holds two slots a row, used in turn, so that one barrier
-// per row is enough; rows of a block (or of a warp, under 32 threads a row) do not wait for each
-// other.
-template <int R>
-__device__ __forceinline__ uint32_t row_lanes() {
-    if constexpr (R >= 32) return 0xffffffffu;
-    else return ((1u << R) - 1u) << ((threadIdx.x & 31) & ~(R - 1));
-}
-template <int R>
-__device__ __forceinline__ float row_sum(float v, float *sm) {
-#pragma unroll
-    for (int o = (R < 32 ? R : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(row_lanes<R>(), v, o);
-    if constexpr (R <= 32) return v;
-    const int in_row = (threadIdx.x % R) >> 5;
-    if ((threadIdx.x & 31) == 0) sm[in_row] = v;
-    if constexpr (R < 128) asm volatile("bar.sync %0, %1;" :: "r"(1 + static_cast<int>(threadIdx.x) / R), "n"(R) : "memory");
-    else __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < R / 32; ++i) s += sm[i];
-    return s;
-}
-
-template <int VEC>
-__device__ __forceinline__ void ld_w(const float *w, int32_t col, float (&v)[VEC]) {
-    if constexpr (VEC >= 4) {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(w + col + i));
-            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-        }
-    } else {
-        v[0] = __ldg(w + col);
-    }
-}
 
 // One block of 32 channels, spread over 32 / VEC neighbouring lanes, in 8 bits: the scale is
 // the smallest power of two 2^e with amax <= 448 2^e (448 = 1.75 * 2^8 is e4m3's largest), so
@@ -369,11 +294,6 @@ __global__ void __launch_bounds__(block_of(R)) rmsnorm_bwd_kernel(NormBwd p) {
 // threads for the loads that HBM wants on their way.  Rows of 1 KB and more are copied by
 // cp.async.bulk into a ring of `stages` rows instead, whose bytes in flight do not depend on
 // registers: 65,536 rows of 2,048 bf16 values with dh 5618 -> 6554 GB/s, without 3921 -> 6134.
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(tc::smem_addr(dst)), "l"(src), "r"(bytes), "r"(tc::smem_addr(bar)) : "memory");
-}
 
 template <typename T, int VEC, int R, int NV>
 __global__ void __launch_bounds__(R) rmsnorm_bwd_ring_kernel(NormBwd p, int stages) {
