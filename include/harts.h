@@ -661,6 +661,65 @@ int harts_grad_clip(const harts_grad_tensor *tensors, int32_t count, float max_n
                     size_t workspace_bytes, harts_stream_t stream);
 
 /* ------------------------------------------------------------------------------ */
+/* Matrix product with bias, activation and residual in its epilogue.             */
+/* ------------------------------------------------------------------------------ */
+
+/*
+ * A projection of compact rows:
+ *   z = x weight^T + bias,   y = act(z) + residual
+ * act is HARTS_ACT_NONE, HARTS_ACT_SILU (z sigmoid(z)) or HARTS_ACT_GELU (z Phi(z), Phi the normal
+ * distribution's; not its tanh approximation).  Sums, bias, activation and residual are fp32, rounded
+ * once.  z may be kept in bf16 for the gradient; act is taken of the unrounded one.
+ */
+#define HARTS_ACT_NONE 0
+#define HARTS_ACT_SILU 1
+#define HARTS_ACT_GELU 2
+
+typedef struct {
+    int64_t C;               /* rows, >= 0 */
+    int32_t K;               /* width of x, a multiple of 8 */
+    int32_t N;               /* width of y, a multiple of 8 */
+    int32_t dtype;           /* harts_dtype of all but bias and dbias: HARTS_BF16 */
+    int32_t activation;      /* HARTS_ACT_* */
+    const void *x;           /* device [C][K], 16-byte aligned (so are the others) */
+    const void *weight;      /* device [N][K] */
+    const float *bias;       /* device [N] fp32, or NULL; not used by the backward */
+    const void *residual;    /* device [C][N], or NULL; not used by the backward (its gradient is d_y) */
+    void *y;                 /* device [C][N] output; may be residual; not used by the backward */
+    void *z;                 /* device [C][N]: output of the forward, or NULL; read by the backward where there
+                                is an activation */
+    int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out; cleared by the caller.
+                                NULL: the library's own word (harts_device_error) */
+    void *workspace;         /* device, harts_linear_{fwd,bwd}_workspace_bytes; 256-byte aligned for the backward */
+    size_t workspace_bytes;
+} harts_linear_args;
+
+/* Workspace of the forward: fp32 pieces of the sums where there are few tiles; 0 for invalid arguments. */
+size_t harts_linear_fwd_workspace_bytes(int64_t C, int32_t K, int32_t N);
+
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, activation, y or z over x or one
+ * another), HARTS_EUNSUPPORTED (dtype other than bf16, K or N not a multiple of 8), HARTS_EOVERFLOW (more
+ * than 2^24 tiles), HARTS_ESMALLBUF (workspace), HARTS_ECUDA. */
+int harts_linear_fwd(const harts_linear_args *args, harts_stream_t stream);
+
+typedef struct {
+    harts_linear_args fwd;   /* x, weight; z as the forward kept it */
+    const void *d_y;         /* device [C][N] dL/dy, 16-byte aligned (so are the outputs) */
+    void *dx;                /* device [C][K] bf16 output, or NULL; dx and dweight may be none of the inputs */
+    void *dweight;           /* device [N][K] bf16 output, or NULL (overwritten; zero when C is 0) */
+    float *dbias;            /* device [N] fp32 output, or NULL */
+} harts_linear_bwd_args;
+
+/* Workspace of the backward: dz in bf16 where there is an activation, column sums where dbias is wanted,
+ * fp32 pieces of the sums where there are few tiles; 0 for invalid arguments. */
+size_t harts_linear_bwd_workspace_bytes(int64_t C, int32_t K, int32_t N, int32_t activation, int32_t with_bias);
+
+/* Backward: dz = d_y act'(z) (each entry formed in fp32; held in bf16 for the products, unrounded for
+ * dbias), dx = dz weight, dweight = dz^T x, dbias = sum over rows of dz; all sums fp32 and in a fixed
+ * order.  x, weight and dz must be finite for dx and dweight to be.  Errors as the forward. */
+int harts_linear_bwd(const harts_linear_bwd_args *args, harts_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
 /* Log-probabilities from hidden rows and the vocabulary weight.                  */
 /* ------------------------------------------------------------------------------ */
 

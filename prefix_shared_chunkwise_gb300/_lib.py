@@ -15,6 +15,7 @@ HARTS_KERNEL_AUTO, HARTS_KERNEL_SIMT, HARTS_KERNEL_TC = 0, 1, 2
 HARTS_PLAN_NODEWISE = 1                       # harts_plan_calls flags
 HARTS_PLAN_NOREPLAY = 2
 HARTS_SCAN_ADD, HARTS_SCAN_MIX = 0, 1
+HARTS_ACT_NONE, HARTS_ACT_SILU, HARTS_ACT_GELU = 0, 1, 2
 HARTS_GATE_LINEAR, HARTS_GATE_SILU, HARTS_GATE_SIGMOID = 0, 1, 2
 
 ERRORS = {0: "HARTS_OK", -1: "HARTS_EINVAL", -2: "HARTS_EUNSUPPORTED", -3: "HARTS_EOVERFLOW",
@@ -35,6 +36,7 @@ EXPORTED = [
     "harts_linear_logprob_bwd_workspace_bytes", "harts_linear_logprob_bwd", "harts_device_error",
     "harts_scan_workspace_bytes", "harts_scan_fwd", "harts_scan_bwd",
     "harts_block_norm_fwd", "harts_block_norm_bwd_workspace_bytes", "harts_block_norm_bwd",
+    "harts_linear_fwd_workspace_bytes", "harts_linear_fwd", "harts_linear_bwd_workspace_bytes", "harts_linear_bwd",
     "harts_last_error",
 ]
 
@@ -157,6 +159,16 @@ class BlockNormBwdArgs(ctypes.Structure):
                 ("dpost_weight", _vp), ("dpre_weight", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("C", _i64), ("K", _i32), ("N", _i32), ("dtype", _i32), ("activation", _i32), ("x", _vp), ("weight", _vp),
+                ("bias", _vp), ("residual", _vp), ("y", _vp), ("z", _vp), ("error", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", LinearArgs), ("d_y", _vp), ("dx", _vp), ("dweight", _vp), ("dbias", _vp)]
+
+
 _lib = None
 
 
@@ -241,6 +253,14 @@ def lib():
         L.harts_block_norm_bwd_workspace_bytes.restype = _sz
         L.harts_block_norm_bwd.argtypes = [ctypes.POINTER(BlockNormBwdArgs), _vp]
         L.harts_block_norm_bwd.restype = ctypes.c_int
+        L.harts_linear_fwd_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.harts_linear_fwd_workspace_bytes.restype = _sz
+        L.harts_linear_fwd.argtypes = [ctypes.POINTER(LinearArgs), _vp]
+        L.harts_linear_fwd.restype = ctypes.c_int
+        L.harts_linear_bwd_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
+        L.harts_linear_bwd_workspace_bytes.restype = _sz
+        L.harts_linear_bwd.argtypes = [ctypes.POINTER(LinearBwdArgs), _vp]
+        L.harts_linear_bwd.restype = ctypes.c_int
         L.harts_device_error.argtypes = [_vp, ctypes.POINTER(_i32)]
         L.harts_device_error.restype = ctypes.c_int
         L.harts_last_error.argtypes = []

@@ -13,7 +13,7 @@ from . import _lib as L
 __all__ = ["Plan", "kda_fwd", "kda_bwd", "conv_fwd", "conv_bwd", "semantic_map", "logprob_fwd",
            "logprob_bwd", "attn_fwd", "attn_bwd", "linear_logprob_fwd", "linear_logprob_bwd",
            "rmsnorm_fwd", "rmsnorm_bwd", "GradSet", "scan_fwd", "scan_bwd",
-           "block_norm_fwd", "block_norm_bwd", "device_error", "dtype_code"]
+           "block_norm_fwd", "block_norm_bwd", "linear_fwd", "linear_bwd", "device_error", "dtype_code"]
 
 
 def dtype_code(torch_dtype):
@@ -809,3 +809,74 @@ def block_norm_bwd(y, h, d_n, d_h=None, *, post_weight=None, gate=None, gate_act
                            _at(dpre_weight), workspace.data_ptr(), nb)
     L.check(lib.harts_block_norm_bwd(ctypes.byref(a), _stream_on(stream, y)), "harts_block_norm_bwd")
     return dict(dy=dy, dresidual=dresidual, dgate=dgate, dpost_weight=dpost_weight, dpre_weight=dpre_weight)
+
+
+_ACTS = {"none": L.HARTS_ACT_NONE, "silu": L.HARTS_ACT_SILU, "gelu": L.HARTS_ACT_GELU}
+
+
+def _linear_sizes(x, weight, activation, error):
+    import torch
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x and weight must be [C, K] and [N, K]")
+    if activation not in _ACTS:
+        raise ValueError(f"activation {activation!r} is none of {sorted(_ACTS)}")
+    (C, K), N = x.shape, weight.shape[0]
+    _ready("x", x, None, x.dtype, x.device)
+    _ready("weight", weight, (N, K), x.dtype, x.device)
+    _need("error", error, None, torch.int32, 4, x.device)
+    return C, K, N
+
+
+@_made_on_stream
+def linear_fwd(x, weight, bias=None, residual=None, *, activation="none", keep_z=False, y=None, z=None, error=None,
+               workspace=None, stream=None):
+    """harts_linear_fwd: y = act(x weight^T + bias) + residual, in one pass.  x [C, K], weight [N, K],
+    residual [C, N] bf16, bias [N] fp32; K and N multiples of 8; activation "none", "silu" or "gelu" (by the
+    normal distribution).  Returns (y [C, N] bf16, z): z is x weight^T + bias in bf16 with keep_z=True (what
+    linear_bwd wants where there is an activation), else None.  y may be given as residual.  error: as
+    linear_logprob_fwd's."""
+    import torch
+    C, K, N = _linear_sizes(x, weight, activation, error)
+    dt, dev = x.dtype, x.device
+    code = dtype_code(dt)
+    _ready("bias", bias, (N,), torch.float32, dev)
+    _ready("residual", residual, (C, N), dt, dev)
+    y = torch.empty((C, N), dtype=dt, device=dev) if y is None else y
+    _ready("y", y, (C, N), dt, dev)
+    if z is None and keep_z:
+        z = torch.empty((C, N), dtype=dt, device=dev)
+    _ready("z", z, (C, N), dt, dev)
+    lib = L.lib()
+    workspace, nb = _workspace(workspace, lib.harts_linear_fwd_workspace_bytes(C, K, N), dev)
+    a = L.LinearArgs(C, K, N, code, _ACTS[activation], x.data_ptr(), weight.data_ptr(), _at(bias), _at(residual),
+                     y.data_ptr(), _at(z), _at(error), workspace.data_ptr(), nb)
+    L.check(lib.harts_linear_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_fwd")
+    return y, z
+
+
+@_made_on_stream
+def linear_bwd(x, weight, d_y, z=None, *, activation="none", with_bias=False, dx=None, dweight=None, dbias=None,
+               error=None, workspace=None, stream=None):
+    """harts_linear_bwd: from dL/dy and, where there is an activation, the z that linear_fwd kept.
+    Returns (dx like x, dweight like weight, dbias [N] fp32 or None without with_bias=True).  The
+    residual's gradient is d_y."""
+    import torch
+    C, K, N = _linear_sizes(x, weight, activation, error)
+    dt, dev = x.dtype, x.device
+    code = dtype_code(dt)
+    _ready("d_y", d_y, (C, N), dt, dev)
+    _ready("z", z, (C, N), dt, dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    dweight = torch.empty_like(weight) if dweight is None else dweight
+    if dbias is None and with_bias:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+    _ready("dx", dx, (C, K), dt, dev)
+    _ready("dweight", dweight, (N, K), dt, dev)
+    _ready("dbias", dbias, (N,), torch.float32, dev)
+    lib, act = L.lib(), _ACTS[activation]
+    workspace, nb = _workspace(workspace, lib.harts_linear_bwd_workspace_bytes(C, K, N, act, dbias is not None), dev)
+    f = L.LinearArgs(C, K, N, code, act, x.data_ptr(), weight.data_ptr(), None, None, None, _at(z), _at(error),
+                     workspace.data_ptr(), nb)
+    a = L.LinearBwdArgs(f, d_y.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _at(dbias))
+    L.check(lib.harts_linear_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_bwd")
+    return dx, dweight, dbias

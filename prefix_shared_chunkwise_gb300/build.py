@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_harts.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["plan.cpp", "harts_abi.cu", "kda_simt.cu", "kda_noreplay.cu", "kda_seq.cu", "kda_grad.cu", "conv.cu", "logprob.cu", "attn.cu",
-           "rmsnorm.cu", "grad_clip.cu", "linear_logprob.cu", "scan.cu", "block_norm.cu"]
+           "rmsnorm.cu", "grad_clip.cu", "linear_logprob.cu", "scan.cu", "block_norm.cu", "linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
