@@ -21,16 +21,19 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "launch_util.h"
 #include "rows.cuh"
 #include "tc_primitives.cuh"
+#include "two.cuh"
 
 namespace harts {
 namespace {
 
 using namespace rows;
+using namespace two;
 
 constexpr int kMaxDim = 8192;       // 1024 threads x 8 values
 constexpr int kMaxStages = 4;       // rows copied ahead
@@ -57,39 +60,112 @@ struct Bwd {
     float scale;
 };
 
-// sigmoid(z) and sigmoid(-z), both from e^-|z|, which neither overflows nor is lost in a 1.
-__device__ __forceinline__ float sigmoid(float z, float &other) {
-    const float t = __expf(-fabsf(z)), big = __fdividef(1.f, 1.f + t), small = t * big;
-    other = z < 0.f ? big : small;
-    return z < 0.f ? small : big;
+// A thread's values of one vector: pairs, or a single one.
+template <int VEC> struct Vals {
+    using E = typename std::conditional<VEC == 1, float, Two>::type;
+    static constexpr int n = VEC == 1 ? 1 : VEC / 2;
+    E e[n];
+};
+template <int VEC> __device__ __forceinline__ typename Vals<VEC>::E all(float c) {
+    if constexpr (VEC == 1) return c;
+    else return make_float2(c, c);
 }
-__device__ __forceinline__ float gate_of(float z, int act, float &slope) {
-    slope = 1.f;
-    if (act == HARTS_GATE_LINEAR) return z;
-    float rest;
-    const float q = sigmoid(z, rest);
-    slope = act == HARTS_GATE_SILU ? q * fmaf(z, rest, 1.f) : q * rest;
-    return act == HARTS_GATE_SILU ? z * q : q;
+template <typename T, int VEC> __device__ __forceinline__ void open(const Raw<T, VEC> &r, Vals<VEC> &v) {
+    if constexpr (sizeof(T) == 2 && VEC == 8) {
+        const uint32_t *u = &r.u.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.e[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    } else {
+        unpack(r, reinterpret_cast<float *>(v.e));
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ void put(void *p, int64_t i, const Vals<VEC> &v) {
+    st<T, VEC>(p, i, reinterpret_cast<const float *>(v.e));
 }
 
-// Rows of a block on their way into shared memory: the N tensors that are there, row after row.
-// Thread 0 fetches; a wait that runs out is reported once and never waited for again, and the block
-// goes on with what its shared memory holds, so that its barriers stay matched.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// sigmoid(z) and sigmoid(-z).  For bf16 streams, where instructions are what the kernels are short
+// of, by e^-z, which ends at 2^126: a gate below e^-87 counts as e^-87.  For fp32 by e^-|z|, which
+// neither overflows nor is lost in a 1.
+template <typename T, typename E> __device__ __forceinline__ E sigmoid(E z, E &other) {
+    if constexpr (sizeof(T) == 2) {
+        const E e = each(z, [](float v) {
+            float a;
+            asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(v * -1.44269504f), "f"(126.f));
+            return ex2(a);
+        });
+        const E q = each(e, [](float v) { return rcp(1.f + v); });
+        other = mul(e, q);
+        return q;
+    } else {
+        const E t = each(z, [](float v) { return __expf(-fabsf(v)); });
+        const E big = each(t, [](float v) { return __fdividef(1.f, 1.f + v); }), small = mul(t, big);
+        other = each(z, big, small, [](float v, float b, float s) { return v < 0.f ? b : s; });
+        return each(z, big, small, [](float v, float b, float s) { return v < 0.f ? s : b; });
+    }
+}
+// A gate's value, and its slope.
+template <typename T, int VEC> __device__ __forceinline__ void open_gate(Vals<VEC> &z, int act) {
+    if (act == HARTS_GATE_LINEAR) return;
+    const bool silu = act == HARTS_GATE_SILU;
+#pragma unroll
+    for (int i = 0; i < Vals<VEC>::n; ++i) {
+        typename Vals<VEC>::E rest;
+        const auto q = sigmoid<T>(z.e[i], rest);
+        z.e[i] = silu ? mul(z.e[i], q) : q;
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ void open_gate(Vals<VEC> &z, Vals<VEC> &slope, int act) {
+    const bool silu = act == HARTS_GATE_SILU;
+#pragma unroll
+    for (int i = 0; i < Vals<VEC>::n; ++i) {
+        typename Vals<VEC>::E rest;
+        const auto q = sigmoid<T>(z.e[i], rest);
+        slope.e[i] = mul(q, silu ? fma(z.e[i], rest, all<VEC>(1.f)) : rest);
+        z.e[i] = silu ? mul(z.e[i], q) : q;
+    }
+}
+
+// The R threads of a row, or the warp that several rows share, are a team: it takes its rows, or
+// twice as many where they are short, at a time, which lie one behind another in memory, and has them copied ahead into a ring of
+// its own, without a look at other teams.
+template <int R, int VALUES> struct Team {
+    static constexpr int threads = R < 32 ? 32 : R, side = threads / R;        // rows side by side
+    static constexpr int batch = R <= 32 && VALUES <= 8 ? 2 : 1, rows = side * batch, count = block_of(R) / threads;
+};
+
+// The N tensors' rows on their way, one tensor behind another.  The team's first thread fetches; a
+// wait that runs out is reported once and never waited for again, and the block goes on with what
+// its shared memory holds, so that its barriers stay matched.
 template <typename T, int N> struct Ahead {
     uint8_t *mem;
     uint64_t *full;
     int *fail;
-    uint32_t bytes, stage;
+    uint32_t tensor, stage;         // bytes of a stage and of one tensor in it
     int stages, s;
     uint32_t phase;
-    __device__ __forceinline__ void fetch(const void *const (&in)[N], int64_t row, int32_t D, int slot) {
+    __device__ __forceinline__ void fetch(const void *const (&in)[N], int64_t row, int rows, int64_t C, int32_t D, int slot) {
+        if (row >= C) return;
+        const uint32_t bytes = static_cast<uint32_t>(C - row < rows ? C - row : rows) * D * sizeof(T);
         uint8_t *dst = mem + slot * stage;
-        tc::mbar_expect_tx(&full[slot], stage);
+        uint32_t total = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) total += in[i] ? bytes : 0;
+        tc::mbar_expect_tx(&full[slot], total);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (!in[i]) continue;
             bulk_load(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
-            dst += bytes;
+            dst += tensor;
         }
     }
     __device__ __forceinline__ void wait(int32_t *error) {
@@ -106,334 +182,394 @@ template <typename T, int N> struct Ahead {
     }
 };
 
-template <typename T, int N>
-__device__ __forceinline__ Ahead<T, N> begin_ahead(const void *const (&in)[N], int32_t D, int stages, uint8_t *mem, uint64_t *full,
-                                                   int *fail, int64_t C) {
-    Ahead<T, N> a;
-    a.mem = mem; a.full = full; a.fail = fail; a.stages = stages; a.s = 0; a.phase = 0;
-    a.bytes = static_cast<uint32_t>(D) * sizeof(T);
-    a.stage = 0;
+// Weights of a thread's columns: in its registers, or (KEEP false) from shared memory.
+template <int NV, int VEC, bool KEEP> struct Weights {
+    Vals<VEC> kept[KEEP ? NV : 1];
+    __device__ __forceinline__ void take(const float *w, float *sh, int R, int t, int32_t D) {
+        if (!w) return;
+        if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.stage += in[i] ? a.bytes : 0;
-    if (threadIdx.x == 0) {
-        *fail = 0;
-        for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
-        tc::fence_mbar_init();
-        for (int s = 0; s < stages; ++s)
-            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < C) a.fetch(in, blockIdx.x + static_cast<int64_t>(s) * gridDim.x, D, s);
+            for (int j = 0; j < NV; ++j)
+                if ((j * R + t) * VEC < D) ld_w<VEC>(w, (j * R + t) * VEC, *reinterpret_cast<float (*)[VEC]>(kept[j].e));
+        } else {
+            for (int32_t c = threadIdx.x; c < D; c += blockDim.x) sh[c] = w[c];
+        }
     }
-    __syncthreads();
-    return a;
-}
+    __device__ __forceinline__ Vals<VEC> get(const float *sh, int j, int32_t col) const {
+        Vals<VEC> v;
+        if constexpr (KEEP) v = kept[j];
+        else
+#pragma unroll
+        for (int i = 0; i < Vals<VEC>::n; i += 2)            // vectors hold four values, or eight
+            *reinterpret_cast<float4 *>(&v.e[i]) = *reinterpret_cast<const float4 *>(sh + col + 2 * i);
+        return v;
+    }
+};
 
-// RING: a block works on one row at a time, which has been copied into shared memory.
-template <typename T, int VEC, int R, int NV, bool RING>
-__global__ void __launch_bounds__(block_of(R)) block_norm_fwd_kernel(const Fwd p, int stages) {
-    constexpr bool kKeep = R <= 512;
+// Blocks of an SM that registers are shared out for: by the values that a thread keeps.
+constexpr int fwd_blocks(int R, int values, bool ring) { return ring ? std::max(1, (values <= 8 ? 768 : 512) / block_of(R)) : 1; }
+constexpr int bwd_blocks(int R, bool ring) { return ring ? std::max(1, 512 / block_of(R)) : 1; }
+
+// What there is beside y: known where it is what surrounds a block, or a head's gated norm, and
+// looked up otherwise.
+enum Kind { kAny, kBlock, kHead };
+
+// RING: rows come through shared memory; otherwise (rows that are not whole vectors) the next one
+// is loaded into registers ahead.
+template <typename T, int VEC, int R, int NV, bool RING, bool KEEP, int KIND>
+__global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) block_norm_fwd_kernel(const Fwd p, int stages) {
+    using M = Team<R, NV * VEC>;
+    constexpr int kBatch = RING ? M::batch : 1, kTeamRows = M::side * kBatch;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float sm[2][2][rows_of(R)][R < 32 ? 1 : R / 32];
-    __shared__ uint64_t full[RING ? kMaxStages : 1];
+    __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
     __shared__ int s_fail;
-    const int t = threadIdx.x % R, sub = threadIdx.x / R;
+    const bool post = KIND != kAny || p.w1, gated = KIND != kAny || p.in[1];
+    const bool pre = KIND == kBlock || (KIND == kAny && p.w2), added = KIND == kBlock || (KIND == kAny && p.in[2]);
+    auto there = [&](int i) { return i == 0 || (i == 1 ? gated : added); };
+    const int t = threadIdx.x % R, sub = threadIdx.x / R, team = threadIdx.x / M::threads, tt = threadIdx.x % M::threads;
     const int32_t D = p.D;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_of(R);
-    int64_t row = static_cast<int64_t>(blockIdx.x) * rows_of(R) + sub;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * M::count * kTeamRows;
+    int64_t row0 = (static_cast<int64_t>(blockIdx.x) * M::count + team) * kTeamRows;
     const float inv_d = 1.f / static_cast<float>(D);
     Raw<T, VEC> a[3][NV];
     [[maybe_unused]] Ahead<T, 3> ahead;
-    if constexpr (RING) ahead = begin_ahead<T, 3>(p.in, D, stages, ring, full, &s_fail, p.C);
+    float *sh = reinterpret_cast<float *>(ring);
+    Weights<NV, VEC, KEEP> w1, w2;
+    w1.take(p.w1, sh, R, t, D);
+    w2.take(p.w2, sh + D, R, t, D);
     auto load = [&](int64_t r) {                                // without a ring: a row's values into registers
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int32_t col = (j * R + t) * VEC;
             if (col < D && r < p.C) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) if (p.in[i]) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
+                for (int i = 0; i < 3; ++i) if (there(i)) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
             }
         }
     };
-    if constexpr (!RING) load(row);
-    [[maybe_unused]] float w1[kKeep ? NV : 1][VEC], w2[kKeep ? NV : 1][VEC];
-    if constexpr (kKeep) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col < D && p.w1) ld_w<VEC>(p.w1, col, w1[j]);
-            if (col < D && p.w2) ld_w<VEC>(p.w2, col, w2[j]);
+    if constexpr (RING) {
+        ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
+        ahead.stage = ahead.tensor * (1 + gated + added);
+        ahead.mem = ring + (KEEP ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+        ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
+        if (threadIdx.x == 0) s_fail = 0;
+        if (tt == 0) {
+            for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
+            tc::fence_mbar_init();
+            for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, kTeamRows, p.C, D, s);
         }
+    } else {
+        load(row0 + tt / R);
     }
-    auto weights = [&](const float *w, float (&kept)[kKeep ? NV : 1][VEC], int j, int32_t col, float (&v)[VEC]) {
-        if constexpr (kKeep) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = kept[j][i];
-        } else {
-            ld_w<VEC>(w, col, v);
-        }
-    };
-    for (int slot = 0; row < p.C; row += step, slot ^= 1) {
-        if constexpr (RING) {
-            ahead.wait(p.error);
-            const T *buf = reinterpret_cast<const T *>(ring + ahead.s * ahead.stage);
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                if (!p.in[i]) continue;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int32_t col = (j * R + t) * VEC;
-                    if (col < D) a[i][j] = ld<T, VEC>(buf, col);
-                }
-                buf += D;
-            }
-        }
-        float v[NV][VEC], g[NV][VEC], s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if ((j * R + t) * VEC >= D) continue;
-            unpack(a[0][j], v[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s = fmaf(v[j][i], v[j][i], s);
-            if (p.in[1]) {
-                unpack(a[1][j], g[j]);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float slope;
-                    g[j][i] = gate_of(g[j][i], p.act, slope);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) g[j][i] = 1.f;
-            }
-        }
-        // behind a sum's barrier the stage is free; residuals are taken out of it before
-        Raw<T, VEC> res[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) res[j] = a[2][j];
-        auto free_stage = [&] {
+    __syncthreads();
+    for (int slot = 0; row0 < p.C; row0 += step) {
+        if constexpr (RING) ahead.wait(p.error);
+#pragma unroll 1
+        for (int batch = 0; batch < kBatch; ++batch, slot ^= 1) {
+            const int in_stage = batch * M::side + tt / R;
+            const int64_t row = row0 + in_stage;
+            const bool on = row < p.C;
             if constexpr (RING) {
-                if (t == 0 && row + stages * step < p.C) ahead.fetch(p.in, row + stages * step, D, ahead.s);
-            } else {
-                load(row + step);
+                const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (!there(i)) continue;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int32_t col = (j * R + t) * VEC;
+                        if (col < D) a[i][j] = ld<T, VEC>(buf, col);
+                    }
+                    buf += ahead.tensor / sizeof(T);
+                }
             }
-        };
-        float r1 = 1.f;
-        if (p.w1) {
-            r1 = __frsqrt_rn(fmaf(row_sum<R>(s, sm[slot][0][sub]), inv_d, p.eps));
-            free_stage();
-            if (t == 0 && p.r1) p.r1[row] = r1;
-        }
-        s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col >= D) continue;
-            if (p.w1) {
-                float w[VEC];
-                weights(p.w1, w1, j, col, w);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * r1 * w[i];
+            // behind a sum's barrier, or the warp's own, the stage is free
+            auto free_stage = [&] {
+                if constexpr (RING) {
+                    if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, kTeamRows, p.C, D, ahead.s);
+                }
+            };
+            if constexpr (RING && R <= 32) {
+                __syncwarp();
+                free_stage();
             }
+            Vals<VEC> v[NV], g[NV];
+            Raw<T, VEC> res[NV];
+            auto s = all<VEC>(0.f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * g[j][i] * p.scale;
-            if (p.in[2]) {
-                float x[VEC];
-                unpack(res[j], x);
+            for (int j = 0; j < NV; ++j) {
+                res[j] = a[2][j];
+                if ((j * R + t) * VEC >= D) continue;
+                open(a[0][j], v[j]);
+                if (post) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j][i] += x[i];
+                    for (int i = 0; i < Vals<VEC>::n; ++i) s = fma(v[j].e[i], v[j].e[i], s);
+                }
+                if (gated) {
+                    open(a[1][j], g[j]);
+                    open_gate<T, VEC>(g[j], p.act);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s = fmaf(v[j][i], v[j][i], s);
-            st<T, VEC>(p.h, row * D + col, v[j]);
-        }
-        if (p.w2) {
-            const float r2 = __frsqrt_rn(fmaf(row_sum<R>(s, sm[slot][1][sub]), inv_d, p.eps));
-            if (!p.w1) free_stage();
-            if (t == 0 && p.r2) p.r2[row] = r2;
+            float factor = p.scale;
+            if (post) {
+                const float r1 = __frsqrt_rn(fmaf(row_sum<R>(total(s), sm[slot][0][sub]), inv_d, p.eps));
+                factor *= r1;
+                if constexpr (!RING) load(row + step);
+                else if constexpr (R > 32) free_stage();
+                if (t == 0 && p.r1 && on) p.r1[row] = r1;
+            }
+            s = all<VEC>(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int32_t col = (j * R + t) * VEC;
                 if (col >= D) continue;
-                float w[VEC];
-                weights(p.w2, w2, j, col, w);
+                if (post) {
+                    const Vals<VEC> w = w1.get(sh, j, col);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * r2 * w[i];
-                st<T, VEC>(p.n, row * D + col, v[j]);
+                    for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(v[j].e[i], w.e[i]);
+                }
+                if (gated) {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(v[j].e[i], g[j].e[i]);
+                }
+                if (added) {
+                    Vals<VEC> x;
+                    open(res[j], x);
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = fma(v[j].e[i], all<VEC>(factor), x.e[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(v[j].e[i], all<VEC>(factor));
+                }
+                if (pre) {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) s = fma(v[j].e[i], v[j].e[i], s);
+                }
+                if (on) put<T, VEC>(p.h, row * D + col, v[j]);
+            }
+            if (pre) {
+                const float r2 = __frsqrt_rn(fmaf(row_sum<R>(total(s), sm[slot][1][sub]), inv_d, p.eps));
+                if (!post) {
+                    if constexpr (!RING) load(row + step);
+                    else if constexpr (R > 32) free_stage();
+                }
+                if (t == 0 && p.r2 && on) p.r2[row] = r2;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int32_t col = (j * R + t) * VEC;
+                    if (col >= D) continue;
+                    const Vals<VEC> w = w2.get(sh + D, j, col);
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(mul(v[j].e[i], all<VEC>(r2)), w.e[i]);
+                    if (on) put<T, VEC>(p.n, row * D + col, v[j]);
+                }
             }
         }
         if constexpr (RING) ahead.next();
     }
-    if constexpr (RING) if (t == 0) ahead.drain();
+    if constexpr (RING) if (tt == 0) ahead.drain();
 }
 
-template <typename T, int VEC, int R, int NV, bool RING>
-__global__ void __launch_bounds__(block_of(R)) block_norm_bwd_kernel(const Bwd p, int stages) {
-    constexpr bool kKeep = R <= 512;
+template <typename T, int VEC, int R, int NV, bool RING, bool KEEP, int KIND>
+__global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_bwd_kernel(const Bwd p, int stages) {
+    using M = Team<R, NV * VEC>;
     constexpr int kRows = rows_of(R);
+    constexpr int kBatch = RING ? M::batch : 1, kTeamRows = M::side * kBatch;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float sm[2][2][kRows][R < 32 ? 1 : R / 32];
-    __shared__ uint64_t full[RING ? kMaxStages : 1];
+    __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
     __shared__ int s_fail;
-    const int t = threadIdx.x % R, sub = threadIdx.x / R;
+    const bool post = KIND != kAny || p.w1, gated = KIND != kAny || p.in[1];
+    const bool pre = KIND == kBlock || (KIND == kAny && p.w2), along = KIND != kAny || p.in[4];
+    auto there = [&](int i) { return i == 0 || (i == 1 ? gated : i == 4 ? along : pre); };
+    const int t = threadIdx.x % R, sub = threadIdx.x / R, team = threadIdx.x / M::threads, tt = threadIdx.x % M::threads;
     const int32_t D = p.D;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * M::count * kTeamRows;
+    int64_t row0 = (static_cast<int64_t>(blockIdx.x) * M::count + team) * kTeamRows;
     const float inv_d = 1.f / static_cast<float>(D);
     let_next_start();
     Raw<T, VEC> a[5][NV];
     [[maybe_unused]] Ahead<T, 5> ahead;
-    if constexpr (RING) ahead = begin_ahead<T, 5>(p.in, D, stages, ring, full, &s_fail, p.C);
-    float next1 = 0.f, next2 = 0.f;
+    float *sh = reinterpret_cast<float *>(ring);
+    Weights<NV, VEC, KEEP> w1, w2;
+    w1.take(p.w1, sh, R, t, D);
+    w2.take(p.w2, sh + D, R, t, D);
+    Vals<VEC> dw1[NV], dw2[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < Vals<VEC>::n; ++i) dw1[j].e[i] = dw2[j].e[i] = all<VEC>(0.f);
+    }
     auto load = [&](int64_t r) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int32_t col = (j * R + t) * VEC;
+            if (col < D && r < p.C) {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) if (there(i)) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
+            }
+        }
+    };
+    float next1 = 0.f, next2 = 0.f;
+    auto load_roots = [&](int64_t r) {
         if (r >= p.C) return;
-        if (p.w1) next1 = __ldg(p.r1 + r);
-        if (p.w2) next2 = __ldg(p.r2 + r);
-        if constexpr (!RING) {
+        if (post) next1 = __ldg(p.r1 + r);
+        if (pre) next2 = __ldg(p.r2 + r);
+    };
+    if constexpr (RING) {
+        ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
+        ahead.stage = ahead.tensor * (1 + gated + 2 * pre + along);
+        ahead.mem = ring + (KEEP ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+        ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
+        if (threadIdx.x == 0) s_fail = 0;
+        if (tt == 0) {
+            for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
+            tc::fence_mbar_init();
+            for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, kTeamRows, p.C, D, s);
+        }
+    } else {
+        load(row0 + tt / R);
+    }
+    load_roots(row0 + tt / R);
+    __syncthreads();
+    for (int slot = 0; row0 < p.C; row0 += step) {
+        if constexpr (RING) ahead.wait(p.error);
+#pragma unroll 1
+        for (int batch = 0; batch < kBatch; ++batch, slot ^= 1) {
+            const int in_stage = batch * M::side + tt / R;
+            const int64_t row = row0 + in_stage;
+            const bool on = row < p.C;
+            const float r1 = next1, r2 = next2;
+            load_roots(batch < kBatch - 1 ? row + M::side : row0 + step + tt / R);
+            if constexpr (RING) {
+                const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D;
+#pragma unroll
+                for (int i = 0; i < 5; ++i) {
+                    if (!there(i)) continue;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int32_t col = (j * R + t) * VEC;
+                        if (col < D) a[i][j] = ld<T, VEC>(buf, col);
+                    }
+                    buf += ahead.tensor / sizeof(T);
+                }
+            }
+            auto free_stage = [&] {
+                if constexpr (RING) {
+                    if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, kTeamRows, p.C, D, ahead.s);
+                }
+            };
+            if constexpr (RING && R <= 32) {
+                __syncwarp();
+                free_stage();
+                if (!on) continue;                              // rows of a warp do not wait for each other from here on
+            }
+            Raw<T, VEC> y[NV], g[NV];
+            Vals<VEC> d[NV], n[NV], f[NV];
+            auto s = all<VEC>(0.f);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                y[j] = a[0][j];
+                g[j] = a[1][j];
+                const int32_t col = (j * R + t) * VEC;
+                if (col >= D) continue;
+                if (along) {
+                    open(a[4][j], d[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = all<VEC>(0.f);
+                }
+                if (pre) {
+                    const Vals<VEC> w = w2.get(sh + D, j, col);
+                    open(a[2][j], f[j]);
+                    open(a[3][j], n[j]);
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) {
+                        n[j].e[i] = mul(n[j].e[i], all<VEC>(r2));
+                        dw2[j].e[i] = fma(f[j].e[i], n[j].e[i], dw2[j].e[i]);
+                        f[j].e[i] = mul(f[j].e[i], w.e[i]);
+                        s = fma(f[j].e[i], n[j].e[i], s);
+                    }
+                }
+            }
+            if (pre) {
+                const float m = row_sum<R>(total(s), sm[slot][0][sub]) * inv_d * -r2;
+                if constexpr (!RING) load(row + step);
+                else if constexpr (R > 32) free_stage();
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i)
+                        d[j].e[i] = fma(all<VEC>(r2), f[j].e[i], fma(n[j].e[i], all<VEC>(m), d[j].e[i]));
+                }
+            }
+            s = all<VEC>(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int32_t col = (j * R + t) * VEC;
-                if (col < D) {
+                if (col >= D) continue;
+                if (p.dres && on) put<T, VEC>(p.dres, row * D + col, d[j]);
+                Vals<VEC> w;
+                if (post) w = w1.get(sh, j, col);
+                open(y[j], n[j]);
 #pragma unroll
-                    for (int i = 0; i < 5; ++i) if (p.in[i]) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
+                for (int i = 0; i < Vals<VEC>::n; ++i) {
+                    d[j].e[i] = mul(d[j].e[i], all<VEC>(p.scale));
+                    if (post) n[j].e[i] = mul(n[j].e[i], all<VEC>(r1));
+                }
+                if (gated) {
+                    Vals<VEC> z, out;
+                    open(g[j], z);
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) {
+                        out.e[i] = mul(d[j].e[i], n[j].e[i]);
+                        if (post) out.e[i] = mul(out.e[i], w.e[i]);
+                    }
+                    if (p.act != HARTS_GATE_LINEAR) {
+                        Vals<VEC> slope;
+                        open_gate<T, VEC>(z, slope, p.act);
+#pragma unroll
+                        for (int i = 0; i < Vals<VEC>::n; ++i) out.e[i] = mul(out.e[i], slope.e[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = mul(d[j].e[i], z.e[i]);
+                    if (p.dgate && on) put<T, VEC>(p.dgate, row * D + col, out);
+                }
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) {
+                        dw1[j].e[i] = fma(d[j].e[i], n[j].e[i], dw1[j].e[i]);
+                        d[j].e[i] = mul(d[j].e[i], w.e[i]);
+                        s = fma(d[j].e[i], n[j].e[i], s);
+                    }
                 }
             }
-        }
-    };
-    load(row);
-    [[maybe_unused]] float w1[kKeep ? NV : 1][VEC], w2[kKeep ? NV : 1][VEC];
-    float dw1[NV][VEC], dw2[NV][VEC];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int32_t col = (j * R + t) * VEC;
-        if constexpr (kKeep) {
-            if (col < D && p.w1) ld_w<VEC>(p.w1, col, w1[j]);
-            if (col < D && p.w2) ld_w<VEC>(p.w2, col, w2[j]);
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dw1[j][i] = dw2[j][i] = 0.f;
-    }
-    auto weights = [&](const float *w, float (&kept)[kKeep ? NV : 1][VEC], int j, int32_t col, float (&v)[VEC]) {
-        if constexpr (kKeep) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = kept[j][i];
-        } else {
-            ld_w<VEC>(w, col, v);
-        }
-    };
-    for (int slot = 0; row < p.C; row += step, slot ^= 1) {
-        const float r1 = next1, r2 = next2;
-        if constexpr (RING) {
-            ahead.wait(p.error);
-            const T *buf = reinterpret_cast<const T *>(ring + ahead.s * ahead.stage);
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                if (!p.in[i]) continue;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int32_t col = (j * R + t) * VEC;
-                    if (col < D) a[i][j] = ld<T, VEC>(buf, col);
-                }
-                buf += D;
-            }
-        }
-        Raw<T, VEC> y[NV], g[NV];
-        float d[NV][VEC], n[NV][VEC], f[NV][VEC], s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            y[j] = a[0][j];
-            g[j] = a[1][j];
-            const int32_t col = (j * R + t) * VEC;
-            if (col >= D) continue;
-            if (p.in[4]) {
-                unpack(a[4][j], d[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) d[j][i] = 0.f;
-            }
-            if (p.w2) {
-                float w[VEC];
-                weights(p.w2, w2, j, col, w);
-                unpack(a[2][j], f[j]);
-                unpack(a[3][j], n[j]);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    n[j][i] *= r2;
-                    dw2[j][i] = fmaf(f[j][i], n[j][i], dw2[j][i]);
-                    f[j][i] *= w[i];
-                    s = fmaf(f[j][i], n[j][i], s);
+            float m = 0.f;
+            if (post) {
+                m = -row_sum<R>(total(s), sm[slot][1][sub]) * inv_d;
+                if (!pre) {
+                    if constexpr (!RING) load(row + step);
+                    else if constexpr (R > 32) free_stage();
                 }
             }
-        }
-        auto free_stage = [&] {
-            if constexpr (RING) {
-                if (t == 0 && row + stages * step < p.C) ahead.fetch(p.in, row + stages * step, D, ahead.s);
-            }
-            load(row + step);
-        };
-        if (p.w2) {
-            const float m = row_sum<R>(s, sm[slot][0][sub]) * inv_d;
-            free_stage();
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
+                const int32_t col = (j * R + t) * VEC;
+                if (col >= D) continue;
+                if (post) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) d[j][i] = fmaf(r2, f[j][i] - n[j][i] * m, d[j][i]);
-            }
-        }
-        s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col >= D) continue;
-            if (p.dres) st<T, VEC>(p.dres, row * D + col, d[j]);
-            float w[VEC];
-            if (p.w1) weights(p.w1, w1, j, col, w);
-            unpack(y[j], n[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                d[j][i] *= p.scale;
-                if (p.w1) n[j][i] *= r1;
-            }
-            if (p.in[1]) {
-                float z[VEC];
-                unpack(g[j], z);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float slope;
-                    const float value = gate_of(z[i], p.act, slope);
-                    z[i] = d[j][i] * (p.w1 ? n[j][i] * w[i] : n[j][i]) * slope;
-                    d[j][i] *= value;
+                    for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = mul(all<VEC>(r1), fma(n[j].e[i], all<VEC>(m), d[j].e[i]));
                 }
-                if (p.dgate) st<T, VEC>(p.dgate, row * D + col, z);
+                if (on) put<T, VEC>(p.dy, row * D + col, d[j]);
             }
-            if (p.w1) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    dw1[j][i] = fmaf(d[j][i], n[j][i], dw1[j][i]);
-                    d[j][i] *= w[i];
-                    s = fmaf(d[j][i], n[j][i], s);
-                }
-            }
-        }
-        float m = 0.f;
-        if (p.w1) {
-            m = row_sum<R>(s, sm[slot][1][sub]) * inv_d;
-            if (!p.w2) free_stage();
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col >= D) continue;
-            if (p.w1) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) d[j][i] = r1 * (d[j][i] - n[j][i] * m);
-            }
-            st<T, VEC>(p.dy, row * D + col, d[j]);
         }
         if constexpr (RING) ahead.next();
     }
-    if constexpr (RING) if (t == 0) ahead.drain();
+    if constexpr (RING) if (tt == 0) ahead.drain();
     // the rows of a block leave one sum of either weight, added in ascending order
     __shared__ float all[kRows > 1 ? kRows : 1][kRows > 1 ? R * NV * VEC : 1];
     for (int which = 0; which < 2; ++which) {
-        if (!(which ? p.w2 : p.w1)) continue;
+        if (!(which ? pre : post)) continue;
         float *part = p.part + blockIdx.x * (2 * static_cast<int64_t>(D)) + which * D;
         if constexpr (kRows > 1) __syncthreads();
 #pragma unroll
@@ -442,7 +578,7 @@ __global__ void __launch_bounds__(block_of(R)) block_norm_bwd_kernel(const Bwd p
             if (col >= D) continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float v = which ? dw2[j][i] : dw1[j][i];
+                const float v = reinterpret_cast<const float *>(which ? dw2[j].e : dw1[j].e)[i];
                 if constexpr (kRows > 1) all[sub][col + i] = v;
                 else part[col + i] = v;
             }
@@ -483,23 +619,19 @@ __global__ void __launch_bounds__(1024) block_norm_dw_kernel(const Dw p) {
     }
 }
 
-// Threads of a row and values that each of them keeps: eight, which leaves the registers of the
-// backward (two sums and two weights a column) for two blocks of 256 threads an SM, and sixteen
-// where a warp would not do otherwise.  Rows that are not whole vectors move single values.
-struct Shape { int vec, r, values; bool ring; };
-Shape shape_of(int32_t dtype, int32_t D) {
+// Threads of a row and values that each of them keeps.  Rows that are not whole vectors move single
+// values.
+struct Shape { int vec, r, values; };
+Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     const int full = dtype == HARTS_BF16 ? 8 : 4;
-    Shape s{D % full == 0 ? full : 1, 8, 8, false};
+    Shape s{D % full == 0 ? full : 1, 8, 8};
     if (s.vec == 1) {
         s.r = D <= 256 ? 32 : D <= 2048 ? 256 : 1024;
-    } else if (D <= 512) {
-        while (s.r < 32 && s.r * 8 < D) s.r *= 2;
-        if (s.r * 8 < D) s.values = 16;
-    } else {
-        s.ring = true;
-        s.r = 128;
-        while (s.r * 8 < D) s.r *= 2;
+        return s;
     }
+    while (s.r < 16 && s.r * 8 < D) s.r *= 2;
+    if (s.r * 8 < D && !backward) s.values = 16;
+    while (s.r * s.values < D) s.r *= 2;
     return s;
 }
 
@@ -508,54 +640,75 @@ int64_t blocks_of(const Shape &s, int64_t C) {
     return std::min<int64_t>((C + rows_of(s.r) - 1) / rows_of(s.r), int64_t(sm_count()) * (2048 / block_of(s.r)));
 }
 
-// Resident blocks of a persistent kernel, and the rows that each of them has on its way.
-template <typename T, int R, bool RING, typename K, typename P>
-cudaError_t launch_rows(K *kernel, const P &p, int tensors, size_t budget, std::atomic<uint64_t> &allowed, std::atomic<int> &known,
-                        int64_t *groups, cudaStream_t st) {
-    int stages = 1, n = known.load(std::memory_order_relaxed);
+// Resident blocks of a persistent kernel, and the rows that each of them has on its way: `budget`
+// bytes an SM.
+template <typename T, int R, int VT, bool RING, bool KEEP, typename K, typename P>
+cudaError_t launch_rows(K *kernel, const P &p, int tensors, std::atomic<uint64_t> &allowed, std::atomic<int> &regs_fit, int64_t *groups, cudaStream_t st) {
+    constexpr size_t kSmem = size_t(200) * 1024;
+    using M = Team<R, VT>;
+    int stages = 1, n = regs_fit.load(std::memory_order_relaxed);
+    if (n == 0) {                                        // blocks that registers leave room for
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block_of(R), 0) != cudaSuccess || n < 1) n = 1;
+        regs_fit.store(n, std::memory_order_relaxed);
+    }
     size_t smem = 0;
     if (RING) {
-        const size_t stage = size_t(p.D) * sizeof(T) * tensors;
-        stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(1, budget / stage)));
-        smem = stages * stage;
-        const cudaError_t e = allow_smem(kernel, 200 * 1024, allowed);
+        const size_t weights = KEEP ? 0 : (2 * size_t(p.D) * sizeof(float) + 127) / 128 * 128;
+        const size_t stage = size_t(p.D) * sizeof(T) * tensors * M::rows * M::count;
+        while (n > 1 && n * (weights + 2 * stage) > kSmem) --n;
+        stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(1, (kSmem / n - weights) / stage)));
+        smem = weights + stages * stage;
+        const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and weights: 224 KB
         if (e != cudaSuccess) return e;
-    }
-    if (n == 0 || RING) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block_of(R), smem) != cudaSuccess || n < 1) n = 1;
-        if (!RING) known.store(n, std::memory_order_relaxed);
     }
     const int64_t rows = rows_of(R), grid = std::min<int64_t>((p.C + rows - 1) / rows, int64_t(sm_count()) * n);
     *groups = grid;
     return launch(kernel, grid, block_of(R), smem, 1, false, st, p, stages);
 }
 
-template <typename T, int VEC, int R, int VT, bool RING>
-cudaError_t launch_one(const Fwd &p, int tensors, int64_t *groups, cudaStream_t st) {
+template <typename T, int VEC, int R, int VT, int KIND>
+cudaError_t launch_kind(const Fwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
-    static std::atomic<int> known{0};
-    return launch_rows<T, R, RING>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, RING>, p, tensors, std::min<size_t>(size_t(48) * 1024 * R / 256, 200 * 1024),
-                                   allowed, known, groups, st);
+    static std::atomic<int> fit{0};
+    constexpr bool ring = VEC > 1;
+    return launch_rows<T, R, VT, ring, true>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, ring, true, KIND>, p, tensors, allowed, fit, groups, st);
 }
-template <typename T, int VEC, int R, int VT, bool RING>
-cudaError_t launch_one(const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
+template <typename T, int VEC, int R, int VT, int KIND>
+cudaError_t launch_kind(const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
-    static std::atomic<int> known{0};
-    return launch_rows<T, R, RING>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, RING>, p, tensors, std::min<size_t>(size_t(100) * 1024 * R / 256, 200 * 1024),
-                                   allowed, known, groups, st);
+    static std::atomic<int> fit{0};
+    constexpr bool ring = VEC > 1, keep = !ring;
+    return launch_rows<T, R, VT, ring, keep>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, ring, keep, KIND>, p, tensors, allowed, fit, groups, st);
+}
+Kind kind_of(const Fwd &p) {
+    return !p.w1 || !p.in[1] ? kAny : p.w2 && p.in[2] ? kBlock : !p.w2 && !p.in[2] ? kHead : kAny;
+}
+Kind kind_of(const Bwd &p) { return !p.w1 || !p.in[1] || !p.in[4] ? kAny : p.w2 ? kBlock : kHead; }
+template <typename T, int VEC, int R, int VT, typename P>
+cudaError_t launch_one(const P &p, int tensors, int64_t *groups, cudaStream_t st) {
+    if constexpr (VEC > 1) {
+        const Kind k = kind_of(p);
+        if (k == kBlock) return launch_kind<T, VEC, R, VT, kBlock>(p, tensors, groups, st);
+        if (k == kHead) return launch_kind<T, VEC, R, VT, kHead>(p, tensors, groups, st);
+    }
+    return launch_kind<T, VEC, R, VT, kAny>(p, tensors, groups, st);
 }
 
 // The instances that shape_of names.
-template <typename T, int VEC, typename P>
-cudaError_t run(const Shape &s, const P &p, int tensors, int64_t *groups, cudaStream_t st) {
-#define HARTS_CASE(V, R, VT, RING) \
-    if (s.vec == V && s.r == R && s.values == VT && s.ring == RING) return launch_one<T, V, R, VT, RING>(p, tensors, groups, st);
-    HARTS_CASE(VEC, 8, 8, false) HARTS_CASE(VEC, 16, 8, false) HARTS_CASE(VEC, 32, 8, false) HARTS_CASE(VEC, 32, 16, false)
-    HARTS_CASE(VEC, 128, 8, true) HARTS_CASE(VEC, 256, 8, true) HARTS_CASE(VEC, 512, 8, true) HARTS_CASE(VEC, 1024, 8, true)
-    HARTS_CASE(1, 32, 8, false) HARTS_CASE(1, 256, 8, false) HARTS_CASE(1, 1024, 8, false)
-#undef HARTS_CASE
+#define HARTS_CASE(V, R, VT) if (s.vec == V && s.r == R && s.values == VT) return launch_one<T, V, R, VT>(p, tensors, groups, st);
+template <typename T, int VEC> cudaError_t run(const Shape &s, const Fwd &p, int tensors, int64_t *groups, cudaStream_t st) {
+    HARTS_CASE(VEC, 8, 8) HARTS_CASE(VEC, 16, 8) HARTS_CASE(VEC, 16, 16) HARTS_CASE(VEC, 32, 16) HARTS_CASE(VEC, 64, 16)
+    HARTS_CASE(VEC, 128, 16) HARTS_CASE(VEC, 256, 16) HARTS_CASE(VEC, 512, 16)
+    HARTS_CASE(1, 32, 8) HARTS_CASE(1, 256, 8) HARTS_CASE(1, 1024, 8)
     return cudaErrorInvalidValue;
 }
+template <typename T, int VEC> cudaError_t run(const Shape &s, const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
+    HARTS_CASE(VEC, 8, 8) HARTS_CASE(VEC, 16, 8) HARTS_CASE(VEC, 32, 8) HARTS_CASE(VEC, 64, 8)
+    HARTS_CASE(VEC, 128, 8) HARTS_CASE(VEC, 256, 8) HARTS_CASE(VEC, 512, 8) HARTS_CASE(VEC, 1024, 8)
+    HARTS_CASE(1, 32, 8) HARTS_CASE(1, 256, 8) HARTS_CASE(1, 1024, 8)
+    return cudaErrorInvalidValue;
+}
+#undef HARTS_CASE
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -610,7 +763,7 @@ int harts_block_norm_fwd(const harts_block_norm_args *a, harts_stream_t stream) 
     if (!p.error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     int64_t groups = 0;
     const int tensors = 1 + (a->gate != nullptr) + (a->residual != nullptr);
-    const Shape s = shape_of(a->dtype, a->D);
+    const Shape s = shape_of(a->dtype, a->D, false);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = a->dtype == HARTS_BF16 ? run<__nv_bfloat16, 8>(s, p, tensors, &groups, st) : run<float, 4>(s, p, tensors, &groups, st);
     if (e != cudaSuccess) return cuda_fail(e, "block norm forward launch");
@@ -620,7 +773,7 @@ int harts_block_norm_fwd(const harts_block_norm_args *a, harts_stream_t stream) 
 
 size_t harts_block_norm_bwd_workspace_bytes(int64_t C, int32_t D, int32_t dtype) {
     if (C < 0 || D < 1 || D > kMaxDim || (dtype != HARTS_FP32 && dtype != HARTS_BF16)) return 0;
-    return std::max<size_t>(256, 2 * sizeof(float) * static_cast<size_t>(blocks_of(shape_of(dtype, D), C)) * D);
+    return std::max<size_t>(256, 2 * sizeof(float) * static_cast<size_t>(blocks_of(shape_of(dtype, D, true), C)) * D);
 }
 
 int harts_block_norm_bwd(const harts_block_norm_bwd_args *b, harts_stream_t stream) {
@@ -665,7 +818,7 @@ int harts_block_norm_bwd(const harts_block_norm_bwd_args *b, harts_stream_t stre
     int tensors = 0;
     for (const void *q : p.in) tensors += q != nullptr;
     int64_t groups = 0;
-    const Shape s = shape_of(a->dtype, a->D);
+    const Shape s = shape_of(a->dtype, a->D, true);
     cudaError_t e = a->dtype == HARTS_BF16 ? run<__nv_bfloat16, 8>(s, p, tensors, &groups, st) : run<float, 4>(s, p, tensors, &groups, st);
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward launch");
     const Dw d{p.part, a->post_weight ? b->dpost_weight : nullptr, a->pre_weight ? b->dpre_weight : nullptr, a->D, static_cast<int32_t>(groups)};

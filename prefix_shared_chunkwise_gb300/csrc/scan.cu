@@ -26,9 +26,12 @@
 #include "launch_util.h"
 #include "tc_primitives.cuh"
 #include "tensor_map.h"
+#include "two.cuh"
 
 namespace harts {
 namespace {
+
+using namespace two;
 
 constexpr int kWarps = 8, kWarpRows = kScanRows / kWarps;      // consumers
 constexpr int kThreads = 32 * (kWarps + 2);                    // and a warp each for carries and copies
@@ -61,32 +64,6 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The channels of a lane, 4 bytes: two of bf16, whose fp32 arithmetic runs on pairs (half as many
 // instructions, which are what the exact decay below would be bound by), or one of fp32.
-using Two = float2;
-__device__ __forceinline__ uint64_t bits_of(Two a) { uint64_t u; memcpy(&u, &a, 8); return u; }
-__device__ __forceinline__ Two two_of(uint64_t u) { Two a; memcpy(&a, &u, 8); return a; }
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
-    return two_of(d);
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
-    return two_of(d);
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
-    return two_of(d);
-}
-__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ float mul(float a, float b) { return a * b; }
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-template <typename F> __device__ __forceinline__ Two each(Two a, F f) { return make_float2(f(a.x), f(a.y)); }
-template <typename F> __device__ __forceinline__ float each(float a, F f) { return f(a); }
-template <typename F> __device__ __forceinline__ Two each(Two a, Two b, F f) { return make_float2(f(a.x, b.x), f(a.y, b.y)); }
-template <typename F> __device__ __forceinline__ float each(float a, float b, F f) { return f(a, b); }
-
 template <typename T> struct Lane;
 template <> struct Lane<__nv_bfloat16> {
     using V = Two;
