@@ -36,7 +36,7 @@ using namespace rows;
 using namespace two;
 
 constexpr int kMaxDim = 8192;       // 1024 threads x 8 values
-constexpr int kMaxStages = 4;       // rows copied ahead
+constexpr int kMaxStages = 2;       // rows copied ahead
 
 struct Fwd {
     const void *in[3];              // y; gate; residual
@@ -146,7 +146,7 @@ template <int R, int VALUES> struct Team {
 // The N tensors' rows on their way, one tensor behind another.  The team's first thread fetches; a
 // wait that runs out is reported once and never waited for again, and the block goes on with what
 // its shared memory holds, so that its barriers stay matched.
-template <typename T, int N> struct Ahead {
+template <typename T, int N, bool ONCE> struct Ahead {
     uint8_t *mem;
     uint64_t *full;
     int *fail;
@@ -164,7 +164,8 @@ template <typename T, int N> struct Ahead {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (!in[i]) continue;
-            bulk_load(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
+            if (ONCE) bulk_load_once(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
+            else bulk_load(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
             dst += tensor;
         }
     }
@@ -182,26 +183,29 @@ template <typename T, int N> struct Ahead {
     }
 };
 
-// Weights of a thread's columns: in its registers, or (KEEP false) from shared memory.
-template <int NV, int VEC, bool KEEP> struct Weights {
-    Vals<VEC> kept[KEEP ? NV : 1];
+// Weights of a thread's columns: in its registers, from shared memory, or from where they are.
+enum Place { kRegs, kShared, kMemory };
+template <int NV, int VEC, int PLACE> struct Weights {
+    Vals<VEC> kept[PLACE == kRegs ? NV : 1];
+    const float *from;
     __device__ __forceinline__ void take(const float *w, float *sh, int R, int t, int32_t D) {
+        from = PLACE == kShared ? sh : w;
         if (!w) return;
-        if constexpr (KEEP) {
+        if constexpr (PLACE == kRegs) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if ((j * R + t) * VEC < D) ld_w<VEC>(w, (j * R + t) * VEC, *reinterpret_cast<float (*)[VEC]>(kept[j].e));
-        } else {
+        } else if constexpr (PLACE == kShared) {
             for (int32_t c = threadIdx.x; c < D; c += blockDim.x) sh[c] = w[c];
         }
     }
-    __device__ __forceinline__ Vals<VEC> get(const float *sh, int j, int32_t col) const {
+    __device__ __forceinline__ Vals<VEC> get(int j, int32_t col) const {
         Vals<VEC> v;
-        if constexpr (KEEP) v = kept[j];
+        if constexpr (PLACE == kRegs) v = kept[j];
         else
 #pragma unroll
         for (int i = 0; i < Vals<VEC>::n; i += 2)            // vectors hold four values, or eight
-            *reinterpret_cast<float4 *>(&v.e[i]) = *reinterpret_cast<const float4 *>(sh + col + 2 * i);
+            *reinterpret_cast<float4 *>(&v.e[i]) = *reinterpret_cast<const float4 *>(from + col + 2 * i);
         return v;
     }
 };
@@ -210,13 +214,13 @@ template <int NV, int VEC, bool KEEP> struct Weights {
 constexpr int fwd_blocks(int R, int values, bool ring) { return ring ? std::max(1, (values <= 8 ? 768 : 512) / block_of(R)) : 1; }
 constexpr int bwd_blocks(int R, bool ring) { return ring ? std::max(1, 512 / block_of(R)) : 1; }
 
-// What there is beside y: known where it is what surrounds a block, or a head's gated norm, and
-// looked up otherwise.
-enum Kind { kAny, kBlock, kHead };
+// What there is beside y: known where it is what surrounds a block, with a gate or without, or a
+// head's gated norm, and looked up otherwise.
+enum Kind { kAny, kBlock, kHead, kUngated };
 
 // RING: rows come through shared memory; otherwise (rows that are not whole vectors) the next one
 // is loaded into registers ahead.
-template <typename T, int VEC, int R, int NV, bool RING, bool KEEP, int KIND>
+template <typename T, int VEC, int R, int NV, bool RING, int PLACE, int KIND>
 __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) block_norm_fwd_kernel(const Fwd p, int stages) {
     using M = Team<R, NV * VEC>;
     constexpr int kBatch = RING ? M::batch : 1, kTeamRows = M::side * kBatch;
@@ -224,8 +228,9 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
     __shared__ float sm[2][2][rows_of(R)][R < 32 ? 1 : R / 32];
     __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
     __shared__ int s_fail;
-    const bool post = KIND != kAny || p.w1, gated = KIND != kAny || p.in[1];
-    const bool pre = KIND == kBlock || (KIND == kAny && p.w2), added = KIND == kBlock || (KIND == kAny && p.in[2]);
+    constexpr bool block = KIND == kBlock || KIND == kUngated;
+    const bool post = KIND != kAny || p.w1, gated = KIND == kBlock || KIND == kHead || (KIND == kAny && p.in[1]);
+    const bool pre = block || (KIND == kAny && p.w2), added = block || (KIND == kAny && p.in[2]);
     auto there = [&](int i) { return i == 0 || (i == 1 ? gated : added); };
     const int t = threadIdx.x % R, sub = threadIdx.x / R, team = threadIdx.x / M::threads, tt = threadIdx.x % M::threads;
     const int32_t D = p.D;
@@ -233,9 +238,9 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
     int64_t row0 = (static_cast<int64_t>(blockIdx.x) * M::count + team) * kTeamRows;
     const float inv_d = 1.f / static_cast<float>(D);
     Raw<T, VEC> a[3][NV];
-    [[maybe_unused]] Ahead<T, 3> ahead;
+    [[maybe_unused]] Ahead<T, 3, (R > 32)> ahead;
     float *sh = reinterpret_cast<float *>(ring);
-    Weights<NV, VEC, KEEP> w1, w2;
+    Weights<NV, VEC, PLACE> w1, w2;
     w1.take(p.w1, sh, R, t, D);
     w2.take(p.w2, sh + D, R, t, D);
     auto load = [&](int64_t r) {                                // without a ring: a row's values into registers
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
     if constexpr (RING) {
         ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
         ahead.stage = ahead.tensor * (1 + gated + added);
-        ahead.mem = ring + (KEEP ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+        ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
         ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
         if (threadIdx.x == 0) s_fail = 0;
         if (tt == 0) {
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
                 const int32_t col = (j * R + t) * VEC;
                 if (col >= D) continue;
                 if (post) {
-                    const Vals<VEC> w = w1.get(sh, j, col);
+                    const Vals<VEC> w = w1.get(j, col);
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(v[j].e[i], w.e[i]);
                 }
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
                 for (int j = 0; j < NV; ++j) {
                     const int32_t col = (j * R + t) * VEC;
                     if (col >= D) continue;
-                    const Vals<VEC> w = w2.get(sh + D, j, col);
+                    const Vals<VEC> w = w2.get(j, col);
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(mul(v[j].e[i], all<VEC>(r2)), w.e[i]);
                     if (on) put<T, VEC>(p.n, row * D + col, v[j]);
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
     if constexpr (RING) if (tt == 0) ahead.drain();
 }
 
-template <typename T, int VEC, int R, int NV, bool RING, bool KEEP, int KIND>
+template <typename T, int VEC, int R, int NV, bool RING, int PLACE, int KIND>
 __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_bwd_kernel(const Bwd p, int stages) {
     using M = Team<R, NV * VEC>;
     constexpr int kRows = rows_of(R);
@@ -379,8 +384,9 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
     __shared__ float sm[2][2][kRows][R < 32 ? 1 : R / 32];
     __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
     __shared__ int s_fail;
-    const bool post = KIND != kAny || p.w1, gated = KIND != kAny || p.in[1];
-    const bool pre = KIND == kBlock || (KIND == kAny && p.w2), along = KIND != kAny || p.in[4];
+    constexpr bool block = KIND == kBlock || KIND == kUngated;
+    const bool post = KIND != kAny || p.w1, gated = KIND == kBlock || KIND == kHead || (KIND == kAny && p.in[1]);
+    const bool pre = block || (KIND == kAny && p.w2), along = KIND != kAny || p.in[4];
     auto there = [&](int i) { return i == 0 || (i == 1 ? gated : i == 4 ? along : pre); };
     const int t = threadIdx.x % R, sub = threadIdx.x / R, team = threadIdx.x / M::threads, tt = threadIdx.x % M::threads;
     const int32_t D = p.D;
@@ -389,17 +395,32 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
     const float inv_d = 1.f / static_cast<float>(D);
     let_next_start();
     Raw<T, VEC> a[5][NV];
-    [[maybe_unused]] Ahead<T, 5> ahead;
+    [[maybe_unused]] Ahead<T, 5, false> ahead;
     float *sh = reinterpret_cast<float *>(ring);
-    Weights<NV, VEC, KEEP> w1, w2;
+    Weights<NV, VEC, PLACE> w1, w2;
     w1.take(p.w1, sh, R, t, D);
     w2.take(p.w2, sh + D, R, t, D);
-    Vals<VEC> dw1[NV], dw2[NV];
+    // the weights' gradients of a thread's columns: registers, but shared memory where 64 of them
+    // are all that a thread has (then the weights stay where they are)
+    constexpr bool kSums = PLACE == kMemory;
+    Vals<VEC> dw1[kSums ? 1 : NV], dw2[kSums ? 1 : NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < (kSums ? 1 : NV); ++j) {
 #pragma unroll
         for (int i = 0; i < Vals<VEC>::n; ++i) dw1[j].e[i] = dw2[j].e[i] = all<VEC>(0.f);
     }
+    if constexpr (kSums)
+        for (int32_t c = threadIdx.x; c < 2 * D; c += blockDim.x) sh[c] = 0.f;
+    auto add_dw = [&](Vals<VEC> *dw, int which, int j, int32_t col, const Vals<VEC> &a, const Vals<VEC> &b) {
+        if constexpr (kSums) {
+            auto *at = reinterpret_cast<typename Vals<VEC>::E *>(sh + which * D + col);
+#pragma unroll
+            for (int i = 0; i < Vals<VEC>::n; ++i) at[i] = fma(a.e[i], b.e[i], at[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Vals<VEC>::n; ++i) dw[j].e[i] = fma(a.e[i], b.e[i], dw[j].e[i]);
+        }
+    };
     auto load = [&](int64_t r) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -419,7 +440,7 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
     if constexpr (RING) {
         ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
         ahead.stage = ahead.tensor * (1 + gated + 2 * pre + along);
-        ahead.mem = ring + (KEEP ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+        ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
         ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
         if (threadIdx.x == 0) s_fail = 0;
         if (tt == 0) {
@@ -480,13 +501,14 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
                     for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = all<VEC>(0.f);
                 }
                 if (pre) {
-                    const Vals<VEC> w = w2.get(sh + D, j, col);
+                    const Vals<VEC> w = w2.get(j, col);
                     open(a[2][j], f[j]);
                     open(a[3][j], n[j]);
 #pragma unroll
+                    for (int i = 0; i < Vals<VEC>::n; ++i) n[j].e[i] = mul(n[j].e[i], all<VEC>(r2));
+                    add_dw(dw2, 1, j, col, f[j], n[j]);
+#pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) {
-                        n[j].e[i] = mul(n[j].e[i], all<VEC>(r2));
-                        dw2[j].e[i] = fma(f[j].e[i], n[j].e[i], dw2[j].e[i]);
                         f[j].e[i] = mul(f[j].e[i], w.e[i]);
                         s = fma(f[j].e[i], n[j].e[i], s);
                     }
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
                 if (col >= D) continue;
                 if (p.dres && on) put<T, VEC>(p.dres, row * D + col, d[j]);
                 Vals<VEC> w;
-                if (post) w = w1.get(sh, j, col);
+                if (post) w = w1.get(j, col);
                 open(y[j], n[j]);
 #pragma unroll
                 for (int i = 0; i < Vals<VEC>::n; ++i) {
@@ -536,9 +558,9 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
                     if (p.dgate && on) put<T, VEC>(p.dgate, row * D + col, out);
                 }
                 if (post) {
+                    add_dw(dw1, 0, j, col, d[j], n[j]);
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) {
-                        dw1[j].e[i] = fma(d[j].e[i], n[j].e[i], dw1[j].e[i]);
                         d[j].e[i] = mul(d[j].e[i], w.e[i]);
                         s = fma(d[j].e[i], n[j].e[i], s);
                     }
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             if (col >= D) continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float v = reinterpret_cast<const float *>(which ? dw2[j].e : dw1[j].e)[i];
+                const float v = kSums ? sh[which * D + col + i] : reinterpret_cast<const float *>(which ? dw2[kSums ? 0 : j].e : dw1[kSums ? 0 : j].e)[i];
                 if constexpr (kRows > 1) all[sub][col + i] = v;
                 else part[col + i] = v;
             }
@@ -642,8 +664,8 @@ int64_t blocks_of(const Shape &s, int64_t C) {
 
 // Resident blocks of a persistent kernel, and the rows that each of them has on its way: `budget`
 // bytes an SM.
-template <typename T, int R, int VT, bool RING, bool KEEP, typename K, typename P>
-cudaError_t launch_rows(K *kernel, const P &p, int tensors, std::atomic<uint64_t> &allowed, std::atomic<int> &regs_fit, int64_t *groups, cudaStream_t st) {
+template <typename T, int R, int VT, bool RING, int PLACE, typename K, typename P>
+cudaError_t launch_rows(K *kernel, const P &p, int tensors, size_t most, std::atomic<uint64_t> &allowed, std::atomic<int> &regs_fit, int64_t *groups, cudaStream_t st) {
     constexpr size_t kSmem = size_t(200) * 1024;
     using M = Team<R, VT>;
     int stages = 1, n = regs_fit.load(std::memory_order_relaxed);
@@ -653,10 +675,10 @@ cudaError_t launch_rows(K *kernel, const P &p, int tensors, std::atomic<uint64_t
     }
     size_t smem = 0;
     if (RING) {
-        const size_t weights = KEEP ? 0 : (2 * size_t(p.D) * sizeof(float) + 127) / 128 * 128;
+        const size_t weights = PLACE == kRegs ? 0 : (2 * size_t(p.D) * sizeof(float) + 127) / 128 * 128;
         const size_t stage = size_t(p.D) * sizeof(T) * tensors * M::rows * M::count;
         while (n > 1 && n * (weights + 2 * stage) > kSmem) --n;
-        stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(1, (kSmem / n - weights) / stage)));
+        stages = static_cast<int>(std::min<size_t>(most, std::max<size_t>(1, (kSmem / n - std::min(weights, kSmem / n)) / stage)));
         smem = weights + stages * stage;
         const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and weights: 224 KB
         if (e != cudaSuccess) return e;
@@ -671,25 +693,31 @@ cudaError_t launch_kind(const Fwd &p, int tensors, int64_t *groups, cudaStream_t
     static std::atomic<uint64_t> allowed{0};
     static std::atomic<int> fit{0};
     constexpr bool ring = VEC > 1;
-    return launch_rows<T, R, VT, ring, true>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, ring, true, KIND>, p, tensors, allowed, fit, groups, st);
+    return launch_rows<T, R, VT, ring, kRegs>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, ring, kRegs, KIND>, p, tensors, R <= 32 && VT > 8 ? 1 : kMaxStages, allowed, fit, groups, st);
 }
 template <typename T, int VEC, int R, int VT, int KIND>
 cudaError_t launch_kind(const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     static std::atomic<int> fit{0};
-    constexpr bool ring = VEC > 1, keep = !ring;
-    return launch_rows<T, R, VT, ring, keep>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, ring, keep, KIND>, p, tensors, allowed, fit, groups, st);
+    constexpr bool ring = VEC > 1;
+    constexpr int place = !ring ? kRegs : R < 1024 ? kShared : kMemory;
+    return launch_rows<T, R, VT, ring, place>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, ring, place, KIND>, p, tensors, kMaxStages, allowed, fit, groups, st);
 }
 Kind kind_of(const Fwd &p) {
-    return !p.w1 || !p.in[1] ? kAny : p.w2 && p.in[2] ? kBlock : !p.w2 && !p.in[2] ? kHead : kAny;
+    if (!p.w1 || (p.w2 == nullptr) != (p.in[2] == nullptr)) return kAny;
+    return p.w2 ? (p.in[1] ? kBlock : kUngated) : p.in[1] ? kHead : kAny;
 }
-Kind kind_of(const Bwd &p) { return !p.w1 || !p.in[1] || !p.in[4] ? kAny : p.w2 ? kBlock : kHead; }
+Kind kind_of(const Bwd &p) {
+    if (!p.w1 || !p.in[4]) return kAny;
+    return p.w2 ? (p.in[1] ? kBlock : kUngated) : p.in[1] ? kHead : kAny;
+}
 template <typename T, int VEC, int R, int VT, typename P>
 cudaError_t launch_one(const P &p, int tensors, int64_t *groups, cudaStream_t st) {
     if constexpr (VEC > 1) {
         const Kind k = kind_of(p);
         if (k == kBlock) return launch_kind<T, VEC, R, VT, kBlock>(p, tensors, groups, st);
         if (k == kHead) return launch_kind<T, VEC, R, VT, kHead>(p, tensors, groups, st);
+        if (k == kUngated) return launch_kind<T, VEC, R, VT, kUngated>(p, tensors, groups, st);
     }
     return launch_kind<T, VEC, R, VT, kAny>(p, tensors, groups, st);
 }

@@ -94,5 +94,13 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  :: "r"(tc::smem_addr(dst)), "l"(src), "r"(bytes), "r"(tc::smem_addr(bar)) : "memory");
 }
 
+// The same for what nobody reads again: it leaves L2 first, and does not drive out what is on its way to memory.
+__device__ __forceinline__ void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                 :: "r"(tc::smem_addr(dst)), "l"(src), "r"(bytes), "r"(tc::smem_addr(bar)), "l"(policy) : "memory");
+}
+
 }  // namespace rows
 }  // namespace harts
