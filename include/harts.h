@@ -374,7 +374,8 @@ typedef struct {
     size_t workspace_bytes;
 } harts_scan_fwd_args;
 
-/* Workspace of either direction: the tiles' maps and the states between them; 0 for invalid arguments. */
+/* Workspace of either direction: the tiles' maps and the states between them; 0 where no segment follows
+ * another and none is longer than 128 rows (workspace may be NULL then), and for invalid arguments. */
 size_t harts_scan_workspace_bytes(const harts_plan *plan, int32_t channels, int32_t dtype);
 
 /* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, channels, form), HARTS_EUNSUPPORTED
@@ -694,7 +695,8 @@ typedef struct {
     size_t workspace_bytes;
 } harts_linear_args;
 
-/* Workspace of the forward: fp32 pieces of the sums where there are few tiles; 0 for invalid arguments. */
+/* Workspace of the forward: fp32 pieces of the sums where there are few tiles; 0 where there are none (workspace
+ * may be NULL then), and for invalid arguments. */
 size_t harts_linear_fwd_workspace_bytes(int64_t C, int32_t K, int32_t N);
 
 /* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, activation, y or z over x or one
@@ -711,7 +713,7 @@ typedef struct {
 } harts_linear_bwd_args;
 
 /* Workspace of the backward: dz in bf16 where there is an activation, column sums where dbias is wanted,
- * fp32 pieces of the sums where there are few tiles; 0 for invalid arguments. */
+ * fp32 pieces of the sums where there are few tiles; 0 where there is none of it, and for invalid arguments. */
 size_t harts_linear_bwd_workspace_bytes(int64_t C, int32_t K, int32_t N, int32_t activation, int32_t with_bias);
 
 /* Backward: dz = d_y act'(z) (each entry formed in fp32; held in bf16 for the products, unrounded for

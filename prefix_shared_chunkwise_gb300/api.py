@@ -513,6 +513,14 @@ def _workspace(workspace, nb, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _scratch(workspace, nb, dev):
+    """The same for operators that may need none: (workspace to be kept, its address or None, its size)."""
+    if nb == 0 and workspace is None:
+        return None, None, 0
+    workspace, nb = _workspace(workspace, nb, dev)
+    return workspace, workspace.data_ptr(), nb
+
+
 class GradSet:
     """harts_grad_norm / harts_grad_clip over a fixed list of gradient buffers (bf16 or fp32,
     contiguous, one device).  The buffers and their addresses are taken once and kept; their values
@@ -663,9 +671,9 @@ def _scan_args(plan, x, g, h, h0, final_state, form, workspace):
     _ready("h", h, x.shape, dt, dev)
     _ready("h0", h0, (info["n_roots"], D), torch.float32, dev)
     _ready("final_state", final_state, (info["n_seq"], D), torch.float32, dev)
-    workspace, nb = _workspace(workspace, L.lib().harts_scan_workspace_bytes(plan.handle, D, code), dev)
+    workspace, ws, nb = _scratch(workspace, L.lib().harts_scan_workspace_bytes(plan.handle, D, code), dev)
     a = L.ScanFwdArgs(D, code, _FORMS[form], x.data_ptr(), g.data_ptr(), None if h0 is None else h0.data_ptr(),
-                      h.data_ptr(), None if final_state is None else final_state.data_ptr(), workspace.data_ptr(), nb)
+                      h.data_ptr(), None if final_state is None else final_state.data_ptr(), ws, nb)
     return a, workspace
 
 
@@ -748,10 +756,14 @@ def block_norm_fwd(y, *, post_weight=None, gate=None, gate_act="silu", scale=1.0
         if n is not None or rstd_pre is not None:
             raise ValueError("n and rstd_pre go with pre_weight")
     else:
-        n = torch.empty_like(y) if n is None else n
-        rstd_pre = torch.empty(C, dtype=f32, device=dev) if rstd_pre is None else rstd_pre
-        _ready("n", n, shape, dt, dev)
-        _ready("rstd_pre", rstd_pre, (C,), f32, dev)
+        if n is None:
+            n = torch.empty_like(y)
+        else:
+            _ready("n", n, shape, dt, dev)
+        if rstd_pre is None:
+            rstd_pre = torch.empty(C, dtype=f32, device=dev)
+        else:
+            _ready("rstd_pre", rstd_pre, (C,), f32, dev)
     if post_weight is None:
         if rstd_post is not None:
             raise ValueError("rstd_post goes with post_weight")
@@ -841,15 +853,18 @@ def linear_fwd(x, weight, bias=None, residual=None, *, activation="none", keep_z
     code = dtype_code(dt)
     _ready("bias", bias, (N,), torch.float32, dev)
     _ready("residual", residual, (C, N), dt, dev)
-    y = torch.empty((C, N), dtype=dt, device=dev) if y is None else y
-    _ready("y", y, (C, N), dt, dev)
-    if z is None and keep_z:
+    if y is None:
+        y = torch.empty((C, N), dtype=dt, device=dev)
+    else:
+        _ready("y", y, (C, N), dt, dev)
+    if z is not None:
+        _ready("z", z, (C, N), dt, dev)
+    elif keep_z:
         z = torch.empty((C, N), dtype=dt, device=dev)
-    _ready("z", z, (C, N), dt, dev)
     lib = L.lib()
-    workspace, nb = _workspace(workspace, lib.harts_linear_fwd_workspace_bytes(C, K, N), dev)
+    workspace, ws, nb = _scratch(workspace, lib.harts_linear_fwd_workspace_bytes(C, K, N), dev)
     a = L.LinearArgs(C, K, N, code, _ACTS[activation], x.data_ptr(), weight.data_ptr(), _at(bias), _at(residual),
-                     y.data_ptr(), _at(z), _at(error), workspace.data_ptr(), nb)
+                     y.data_ptr(), _at(z), _at(error), ws, nb)
     L.check(lib.harts_linear_fwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_fwd")
     return y, z
 
@@ -874,9 +889,8 @@ def linear_bwd(x, weight, d_y, z=None, *, activation="none", with_bias=False, dx
     _ready("dweight", dweight, (N, K), dt, dev)
     _ready("dbias", dbias, (N,), torch.float32, dev)
     lib, act = L.lib(), _ACTS[activation]
-    workspace, nb = _workspace(workspace, lib.harts_linear_bwd_workspace_bytes(C, K, N, act, dbias is not None), dev)
-    f = L.LinearArgs(C, K, N, code, act, x.data_ptr(), weight.data_ptr(), None, None, None, _at(z), _at(error),
-                     workspace.data_ptr(), nb)
+    workspace, ws, nb = _scratch(workspace, lib.harts_linear_bwd_workspace_bytes(C, K, N, act, dbias is not None), dev)
+    f = L.LinearArgs(C, K, N, code, act, x.data_ptr(), weight.data_ptr(), None, None, None, _at(z), _at(error), ws, nb)
     a = L.LinearBwdArgs(f, d_y.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _at(dbias))
     L.check(lib.harts_linear_bwd(ctypes.byref(a), _stream_on(stream, x)), "harts_linear_bwd")
     return dx, dweight, dbias

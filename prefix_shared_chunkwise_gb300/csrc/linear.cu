@@ -15,29 +15,32 @@
 // shared-memory stages with either operand by TMA, warp 1 issues tcgen05.mma into one of two
 // 256-column accumulators in TMEM, warps 4-11 empty the other one, and two threads send the
 // finished columns out.  Where there are fewer tiles than SMs, the sum is cut into pieces, whose
-// fp32 results a small kernel joins in order before the epilogue.  Up to eight rows, where
+// fp32 results a small kernel joins in order before the epilogue.  For one row or two, where
 // reading w is all, warps form dot products instead.  All waits are bounded.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "launch_util.h"
 #include "tc_primitives.cuh"
 #include "tensor_map.h"
 #include "tile_pairs.cuh"
+#include "two.cuh"
 
 namespace harts {
 namespace {
 
 using namespace pairs;
+using namespace two;
 
 constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K step (one 128-byte swizzle row), tile columns
 constexpr uint32_t kABytes = kTM * kTK * 2;
 constexpr uint32_t kSlots = 4, kSlotBytes = kTM * 128;          // 128 rows x 128 bytes of output on their way out
 constexpr int kThreads = 448, kEpiWarp0 = 4, kStoreWarp0 = 12;  // eight epilogue warps: two for each 32 TMEM lanes
 constexpr int kGroup = 16;                          // tiles along the fast side that run together
-constexpr int kDotRows = 8;                         // most rows that are done by dot products
+constexpr int kDotRows = 2;                         // most rows that are done by dot products
 
 template <int G> struct Ring {
     static constexpr uint32_t stages = G == 2 ? 5 : 3;
@@ -68,7 +71,6 @@ struct Prod {
 struct Epilogue {
     const float *bias;
     const __nv_bfloat16 *res;
-    int32_t act;
 };
 
 struct Params {
@@ -136,82 +138,76 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+__device__ __forceinline__ Two both(float c) { return make_float2(c, c); }
+
 // Phi(z) and the density at z, up to a factor.  With x = |z| / sqrt 2, Phi(-|z|) = e^(-x^2) E(x) / 2
 // where E(x) = e^(x^2) erfc(x) is smooth: t P(t), t = 1 / (1 + 3/8 x), P of degree 6 fitted to it over
 // 0 .. 10 with least relative error (6.4e-7, against bf16's 2^-9).  One exponential serves both, and
 // the far tail keeps its digits.
-__device__ __forceinline__ float normal(float z, float &density) {
-    const float x = fabsf(z), t = rcp(fmaf(x, 0.375f * 0.70710678f, 1.f));
-    density = ex2(z * z * -0.72134752f);
-    float q = -0.13509675f;
-    q = fmaf(q, t, 0.38794115f);
-    q = fmaf(q, t, -0.12960255f);
-    q = fmaf(q, t, 0.28306571f);
-    q = fmaf(q, t, 0.16666285f);
-    q = fmaf(q, t, 0.21568952f);
-    q = fmaf(q, t, 0.21133942f);
-    const float tail = 0.5f * density * (q * t);
-    return z < 0.f ? tail : 1.f - tail;
+__device__ __forceinline__ Two normal(Two z, Two &density) {
+    const Two t = each(z, [](float v) { return rcp(fmaf(fabsf(v), 0.375f * 0.70710678f, 1.f)); });
+    density = each(mul(z, z), [](float v) { return ex2(v * -0.72134752f); });
+    Two q = both(-0.13509675f);
+    q = fma(q, t, both(0.38794115f));
+    q = fma(q, t, both(-0.12960255f));
+    q = fma(q, t, both(0.28306571f));
+    q = fma(q, t, both(0.16666285f));
+    q = fma(q, t, both(0.21568952f));
+    q = fma(q, t, both(0.21133942f));
+    const Two tail = mul(mul(density, both(0.5f)), mul(q, t));
+    return each(z, tail, [](float v, float a) { return v < 0.f ? a : 1.f - a; });
 }
-__device__ __forceinline__ float act_of(float z, int act) {
-    if (act == HARTS_ACT_SILU) return z * rcp(1.f + ex2(z * -1.44269504f));
-    if (act == HARTS_ACT_GELU) {
-        float density;
-        return z * normal(z, density);
+__device__ __forceinline__ Two sigmoid(Two z) { return each(z, [](float v) { return rcp(1.f + ex2(v * -1.44269504f)); }); }
+template <int ACT> __device__ __forceinline__ Two act_of(Two z) {
+    if constexpr (ACT == HARTS_ACT_SILU) return mul(z, sigmoid(z));
+    if constexpr (ACT == HARTS_ACT_GELU) {
+        Two density;
+        return mul(z, normal(z, density));
     }
     return z;
 }
-__device__ __forceinline__ float slope_of(float z, int act) {
-    if (act == HARTS_ACT_SILU) {
-        const float q = rcp(1.f + ex2(z * -1.44269504f));
-        return q * fmaf(z, 1.f - q, 1.f);
+template <int ACT> __device__ __forceinline__ Two slope_of(Two z) {
+    if constexpr (ACT == HARTS_ACT_SILU) {
+        const Two q = sigmoid(z);
+        return mul(q, fma(z, fma(q, both(-1.f), both(1.f)), both(1.f)));
     }
-    if (act == HARTS_ACT_GELU) {
-        float density;
-        const float phi = normal(z, density);
-        return fmaf(z * 0.39894228f, density, phi);
+    if constexpr (ACT == HARTS_ACT_GELU) {
+        Two density;
+        const Two phi = normal(z, density);
+        return fma(mul(z, both(0.39894228f)), density, phi);
     }
-    return 1.f;
+    return both(1.f);
 }
+__device__ __forceinline__ Two open(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// Eight columns from `col` of one row: z with its bias, and y.  `col` and N are multiples of 8.
-__device__ __forceinline__ void finish8(const Epilogue &e, int64_t at, int32_t col, float (&z)[8], float (&y)[8]) {
-    if (e.bias) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(e.bias + col)), b = __ldg(reinterpret_cast<const float4 *>(e.bias + col) + 1);
-        z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
-        z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+// Eight columns from `col` of one row (the residual's at `res`): z with its bias, and y.  Columns
+// come in eights.
+struct Eight { Two v[4]; };
+template <int ACT> __device__ __forceinline__ void finish8(const float *bias, const uint4 *res, int32_t col, Eight &z, Eight &y) {
+    if (bias) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(bias + col)), b = __ldg(reinterpret_cast<const float4 *>(bias + col) + 1);
+        z.v[0] = add(z.v[0], make_float2(a.x, a.y)); z.v[1] = add(z.v[1], make_float2(a.z, a.w));
+        z.v[2] = add(z.v[2], make_float2(b.x, b.y)); z.v[3] = add(z.v[3], make_float2(b.z, b.w));
     }
-    if (e.act == HARTS_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = act_of(z[i], HARTS_ACT_GELU);
-    } else if (e.act == HARTS_ACT_SILU) {
+    for (int i = 0; i < 4; ++i) y.v[i] = act_of<ACT>(z.v[i]);
+    if (res) {
+        const uint32_t *u = &res->x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = act_of(z[i], HARTS_ACT_SILU);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = z[i];
-    }
-    if (e.res) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(e.res + at);
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(h[i]);
-            y[2 * i] += f.x;
-            y[2 * i + 1] += f.y;
-        }
+        for (int i = 0; i < 4; ++i) y.v[i] = add(y.v[i], open(u[i]));
     }
 }
-__device__ __forceinline__ uint4 pack8(const float *v) {
-    return make_uint4(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]), tc::pack_bf16(v[4], v[5]), tc::pack_bf16(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const Eight &e) {
+    return make_uint4(tc::pack_bf16(e.v[0].x, e.v[0].y), tc::pack_bf16(e.v[1].x, e.v[1].y), tc::pack_bf16(e.v[2].x, e.v[2].y), tc::pack_bf16(e.v[3].x, e.v[3].y));
 }
 
 // ---- tiles ------------------------------------------------------------------------------
 
-// FWD: bias, activation and residual go into the output; otherwise it is the product, or a piece of it.
-template <bool FWD, int G>
+// ACT >= 0: bias, that activation and residual go into the output; otherwise it is the product, or a piece of it.
+template <int ACT, int G>
 __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_constant__ Params p) {
     using B = Ring<G>;
+    constexpr bool FWD = ACT >= 0;
     constexpr uint32_t kStages = B::stages, kStageBytes = B::stage_bytes;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024 - (tc::smem_addr(smraw) & 1023)) & 1023);
@@ -348,6 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
             const uint32_t buf = tile & 1;
             const uint32_t acc = tm + buf * kTN + lane_off;
             const int32_t n0 = t.nt * q.n, row = (t.mt * G + rank) * kTM + lg * 32 + lane;
+            if constexpr (FWD) {
+                // what the tile's end will read is brought near while its products are formed: each
+                // lane's row of the residual to L2, the bias to L1
+                if (p.ep.res && row < q.rows)
+                    for (int c = half * 64; c < q.n && n0 + c < q.cols; c += 128)
+                        asm volatile("prefetch.global.L2 [%0];" :: "l"(p.ep.res + static_cast<int64_t>(row) * q.cols + n0 + c));
+                if (p.ep.bias && lane * 32 < q.n && n0 + lane * 32 < q.cols)
+                    asm volatile("prefetch.global.L1 [%0];" :: "l"(p.ep.bias + n0 + lane * 32));
+            }
             if (!warp_wait(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail)) break;
             tc::fence_after_sync();
             const int step = !FWD && q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
@@ -363,33 +368,43 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
                     for (int j = 0; j < 8; ++j)
                         *reinterpret_cast<float4 *>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else {
-                    float v[64];
-                    tc::tmem_ld32x2(acc + c, reinterpret_cast<float(&)[32]>(v[0]), acc + c + 32, reinterpret_cast<float(&)[32]>(v[32]));
-                    if constexpr (FWD) {
-                        uint8_t *z_dst = dst;
-                        uint32_t z_slot = slot;
-                        if (p.keep) {
-                            if (!slot_for(slot)) { ok = false; break; }
-                            dst = out + slot * kSlotBytes;
-                        }
-                        const int64_t at = static_cast<int64_t>(row) * q.cols + n0 + c;
-                        Epilogue e = p.ep;
-                        if (row >= q.rows) e.res = nullptr;
+                } else if constexpr (FWD) {
+                    uint8_t *z_dst = dst;
+                    const uint32_t z_slot = slot;
+                    if (p.keep) {
+                        if (!slot_for(slot)) { ok = false; break; }
+                        dst = out + slot * kSlotBytes;
+                    }
+                    // 32 columns at a time: what is unrolled is fetched anew by every launch
+#pragma unroll 1
+                    for (int h = 0; h < 64; h += 32) {
+                        const int32_t col = n0 + c + h;
+                        const __nv_bfloat16 *res = p.ep.res ? p.ep.res + static_cast<int64_t>(row) * q.cols + col : nullptr;
+                        uint4 r[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (n0 + c + 8 * j >= q.cols) break;
-                            float y[8];
-                            float(&z)[8] = reinterpret_cast<float(&)[8]>(v[8 * j]);
-                            finish8(e, at + 8 * j, n0 + c + 8 * j, z, y);
-                            const uint32_t chunk = lane * 128 + ((j ^ (lane & 7)) << 4);
+                        for (int j = 0; j < 4; ++j) {
+                            r[j] = make_uint4(0, 0, 0, 0);
+                            if (res && row < q.rows && col + 8 * j < q.cols) r[j] = *reinterpret_cast<const uint4 *>(res + 8 * j);
+                        }
+                        float v[32];
+                        tc::tmem_ld32(acc + c + h, v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (col + 8 * j >= q.cols) break;
+                            Eight z, y;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) z.v[i] = make_float2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                            finish8<FWD ? ACT : 0>(p.ep.bias, p.ep.res ? &r[j] : nullptr, col + 8 * j, z, y);
+                            const uint32_t chunk = lane * 128 + (((h / 8 + j) ^ (lane & 7)) << 4);
                             if (p.keep) *reinterpret_cast<uint4 *>(z_dst + chunk) = pack8(z);
                             *reinterpret_cast<uint4 *>(dst + chunk) = pack8(y);
                         }
-                        if (p.keep) send(z_slot);
-                    } else {
-                        store_row(dst, lane, v);
                     }
+                    if (p.keep) send(z_slot);
+                } else {
+                    float v[64];
+                    tc::tmem_ld32x2(acc + c, reinterpret_cast<float(&)[32]>(v[0]), acc + c + 32, reinterpret_cast<float(&)[32]>(v[32]));
+                    store_row(dst, lane, v);
                 }
                 send(slot);
             }
@@ -448,56 +463,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
 // Eight columns a thread: the pieces of up to two outputs in order, then the epilogue.
 struct JoinOne { const float *part; __nv_bfloat16 *y, *z; int64_t values; int32_t cols, splits; };
 struct Join { JoinOne of[2]; Epilogue ep; int64_t blocks0; };
+template <int ACT>
 __global__ void __launch_bounds__(128) linear_join_kernel(const Join p) {
     wait_previous();
     const int which = blockIdx.x >= p.blocks0;
     const JoinOne &o = p.of[which];
     const int64_t at = ((blockIdx.x - (which ? p.blocks0 : 0)) * 128 + threadIdx.x) * 8;
     if (at >= o.values) return;
-    float z[8] = {}, y[8];
+    Eight z, y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z.v[i] = both(0.f);
+#pragma unroll 4
     for (int s = 0; s < o.splits; ++s) {
         const float4 *q = reinterpret_cast<const float4 *>(o.part + s * o.values + at);
         const float4 a = q[0], b = q[1];
-        z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
-        z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+        z.v[0] = add(z.v[0], make_float2(a.x, a.y)); z.v[1] = add(z.v[1], make_float2(a.z, a.w));
+        z.v[2] = add(z.v[2], make_float2(b.x, b.y)); z.v[3] = add(z.v[3], make_float2(b.z, b.w));
     }
-    finish8(p.ep, at, static_cast<int32_t>(at % o.cols), z, y);
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (p.ep.res) r = *reinterpret_cast<const uint4 *>(p.ep.res + at);
+    finish8<ACT>(p.ep.bias, p.ep.res ? &r : nullptr, static_cast<int32_t>(at % o.cols), z, y);
     if (o.z) *reinterpret_cast<uint4 *>(o.z + at) = pack8(z);
     *reinterpret_cast<uint4 *>(o.y + at) = pack8(y);
 }
 
 // ---- few rows ---------------------------------------------------------------------------
 
-// Dot products of up to R rows with a warp's two rows of w; x comes from L1.
-struct DotParams { const __nv_bfloat16 *x, *w; __nv_bfloat16 *y, *z; Epilogue ep; int32_t rows, K, N; };
-template <int R>
+// Dot products of R rows with a warp's two rows of w; x comes from L1.  (8,192 x 2,048 from L2: one row 4.2 us, two
+// 6.2, three 10.6, where the tiles take 9.7.)
+struct DotParams { const __nv_bfloat16 *x, *w; __nv_bfloat16 *y, *z; Epilogue ep; int32_t K, N; };
+template <int R, int ACT>
 __global__ void __launch_bounds__(256) linear_dot_kernel(const DotParams p) {
     const int lane = threadIdx.x & 31;
     const int32_t n0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 2;
     if (n0 >= p.N) return;
     const uint4 *w0 = reinterpret_cast<const uint4 *>(p.w + static_cast<int64_t>(n0) * p.K), *w1 = w0 + p.K / 8;   // N is even
-    float acc[2][R] = {};
+    Two acc[2][R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[0][r] = acc[1][r] = both(0.f);
     const int32_t chunks = p.K / 8;
-    auto add = [&](const uint4 &a, const uint4 &b, int32_t i) {
-        float fa[8], fb[8];
+    auto take = [&](const uint4 &a, const uint4 &b, int32_t i) {
         const uint32_t *ua = &a.x, *ub = &b.x;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            fa[2 * k] = __uint_as_float(ua[k] << 16); fa[2 * k + 1] = __uint_as_float(ua[k] & 0xffff0000u);
-            fb[2 * k] = __uint_as_float(ub[k] << 16); fb[2 * k + 1] = __uint_as_float(ub[k] & 0xffff0000u);
-        }
-#pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (r >= p.rows) break;
             const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(r) * p.K) + i);
             const uint32_t *ux = &x.x;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float lo = __uint_as_float(ux[k] << 16), hi = __uint_as_float(ux[k] & 0xffff0000u);
-                acc[0][r] = fmaf(fa[2 * k], lo, acc[0][r]);
-                acc[1][r] = fmaf(fb[2 * k], lo, acc[1][r]);
-                acc[0][r] = fmaf(fa[2 * k + 1], hi, acc[0][r]);
-                acc[1][r] = fmaf(fb[2 * k + 1], hi, acc[1][r]);
+                acc[0][r] = fma(open(ua[k]), open(ux[k]), acc[0][r]);
+                acc[1][r] = fma(open(ub[k]), open(ux[k]), acc[1][r]);
             }
         }
     };
@@ -508,26 +522,25 @@ __global__ void __launch_bounds__(256) linear_dot_kernel(const DotParams p) {
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) { a[j] = __ldg(w0 + i + 32 * j); b[j] = __ldg(w1 + i + 32 * j); }
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) add(a[j], b[j], i + 32 * j);
+        for (int j = 0; j < kAtOnce; ++j) take(a[j], b[j], i + 32 * j);
     }
-    for (; i < chunks; i += 32) add(__ldg(w0 + i), __ldg(w1 + i), i);
+    for (; i < chunks; i += 32) take(__ldg(w0 + i), __ldg(w1 + i), i);
     float mine = 0.f;                                   // lane 2 r + c: row r, column c
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float v = acc[c][r];
+            float v = total(acc[c][r]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane == 2 * r + c) mine = v;
         }
-    const int r = lane >> 1;
-    if (r >= p.rows) return;
+    if (lane >= 2 * R) return;
     const int32_t col = n0 + (lane & 1);
-    const int64_t at = static_cast<int64_t>(r) * p.N + col;
+    const int64_t at = static_cast<int64_t>(lane >> 1) * p.N + col;
     if (p.ep.bias) mine += __ldg(p.ep.bias + col);
     if (p.z) p.z[at] = __float2bfloat16_rn(mine);
-    float y = act_of(mine, p.ep.act);
+    float y = act_of<ACT>(both(mine)).x;
     if (p.ep.res) y += __bfloat162float(p.ep.res[at]);
     p.y[at] = __float2bfloat16_rn(y);
 }
@@ -536,41 +549,48 @@ __global__ void __launch_bounds__(256) linear_dot_kernel(const DotParams p) {
 
 // A block takes 256 columns, eight a thread, of `per` rows; its eight warps' column sums are added
 // in order and leave one row of sums, which the second kernel adds in order.
-struct DzParams { const __nv_bfloat16 *dy, *z; __nv_bfloat16 *dz; float *part; int64_t C; int32_t N, act, per; };
+struct DzParams { const __nv_bfloat16 *dy, *z; __nv_bfloat16 *dz; float *part; int64_t C; int32_t N, per; };
+template <int ACT>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const DzParams p) {
+    constexpr bool kCurved = ACT != HARTS_ACT_NONE;
+    constexpr int kAtOnce = 4;                          // rows that a warp loads at a time
     __shared__ float sm[8][256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t strips = (p.N + 255) / 256, strip = blockIdx.x % strips, chunk = blockIdx.x / strips;
     const int32_t col = strip * 256 + lane * 8;
     let_next_start();
-    float s[8] = {};
-    if (col < p.N) {
-        const int64_t r0 = static_cast<int64_t>(chunk) * p.per, r1 = min(p.C, r0 + p.per);
-#pragma unroll 2
-        for (int64_t r = r0 + warp; r < r1; r += 8) {
-            const int64_t at = r * p.N + col;
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p.dy + at));
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (p.z) v = __ldg(reinterpret_cast<const uint4 *>(p.z + at));
-            const uint32_t *pu = &u.x, *pv = &v.x;
-            float d[8];
+    Eight s;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                d[2 * k] = __uint_as_float(pu[k] << 16);
-                d[2 * k + 1] = __uint_as_float(pu[k] & 0xffff0000u);
-                if (p.z) {
-                    d[2 * k] *= slope_of(__uint_as_float(pv[k] << 16), p.act);
-                    d[2 * k + 1] *= slope_of(__uint_as_float(pv[k] & 0xffff0000u), p.act);
-                }
+    for (int k = 0; k < 4; ++k) s.v[k] = both(0.f);
+    if (col < p.N) {
+        const int64_t r0 = static_cast<int64_t>(chunk) * p.per + warp, r1 = min(p.C, static_cast<int64_t>(chunk + 1) * p.per);
+        for (int64_t r = r0; r < r1; r += 8 * kAtOnce) {
+            uint4 u[kAtOnce], v[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (r + 8 * j >= r1) continue;
+                const int64_t at = (r + 8 * j) * p.N + col;
+                u[j] = __ldg(reinterpret_cast<const uint4 *>(p.dy + at));
+                if (kCurved) v[j] = __ldg(reinterpret_cast<const uint4 *>(p.z + at));
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] += d[k];
-            if (p.z) *reinterpret_cast<uint4 *>(p.dz + at) = pack8(d);
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (r + 8 * j >= r1) continue;
+                const uint32_t *pu = &u[j].x, *pv = &v[j].x;
+                Eight d;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    d.v[k] = open(pu[k]);
+                    if (kCurved) d.v[k] = mul(d.v[k], slope_of<ACT>(open(pv[k])));
+                    s.v[k] = add(s.v[k], d.v[k]);
+                }
+                if (kCurved) *reinterpret_cast<uint4 *>(p.dz + (r + 8 * j) * p.N + col) = pack8(d);
+            }
         }
     }
     if (!p.part) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sm[warp][lane * 8 + k] = s[k];
+    for (int k = 0; k < 4; ++k) { sm[warp][lane * 8 + 2 * k] = s.v[k].x; sm[warp][lane * 8 + 2 * k + 1] = s.v[k].y; }
     __syncthreads();
     const int32_t c = strip * 256 + threadIdx.x;
     if (c < p.N) {
@@ -612,7 +632,8 @@ struct Cut { int G; int32_t n, splits, k_per; };
 // a step of 64 takes two cycles a column, no less than its copies and barriers (430 - 450), and in
 // single blocks 1.2 as long, as each reads its columns alone; a tile's ends cost about three steps.
 // Columns leave in 64s, and an operand read by columns comes in 64s per block.
-// Pieces cost their fp32 sums, written and read again at some 3,500 bytes a cycle, and a launch.
+// Pieces cost their fp32 sums, written and read again at some 3,500 bytes a cycle, a launch, and the caller a
+// workspace.
 Cut cut_of(int64_t M, int64_t N, int32_t kb, bool by_columns, int32_t outputs, int groups = 2) {
     Cut best{1, kTN, 1, kb};
     double least = 0.0;
@@ -625,7 +646,7 @@ Cut cut_of(int64_t M, int64_t N, int32_t kb, bool by_columns, int32_t outputs, i
                 if (used != s) continue;
                 const double step = 2.0 * std::max(n, 220) * (G == 1 ? 1.2 : 1.0);
                 double cost = double((tiles * s + workers - 1) / workers) * (per + 3) * step;
-                if (s > 1) cost += 5000.0 + double(M) * N * (8 * s + 2 * outputs) / 3500.0;
+                if (s > 1) cost += 9000.0 + double(M) * N * (8 * s + 2 * outputs) / 3500.0;
                 if (least == 0.0 || cost < least) { least = cost; best = Cut{G, n, s, per}; }
             }
         }
@@ -681,10 +702,10 @@ bool make_prod(Prod &q, const Cut &c, int64_t M, int64_t N, int64_t S, const voi
            map_out(&q.out, part ? static_cast<void *>(part) : out, part ? c.splits : 1, M, N, part != nullptr);
 }
 
-template <bool FWD, int G>
+template <int ACT, int G>
 cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(linear_tile_kernel<FWD, G>, Ring<G>::smem, done);
+    const cudaError_t e = allow_smem(linear_tile_kernel<ACT, G>, Ring<G>::smem, done);
     if (e != cudaSuccess) return e;
     int64_t items = 0;
     for (int i = 0; i < p.n_prod; ++i) {
@@ -702,11 +723,17 @@ cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
         const uint32_t a = p.prod[0].k_per + 3, b = p.prod[1].k_per + 3;
         p.extra = std::min((a + b / 2) / b, p.prod[1].items / (workers - p.over));
     }
-    return launch(linear_tile_kernel<FWD, G>, int64_t(workers) * G, kThreads, Ring<G>::smem, G, behind, st, p);
+    return launch(linear_tile_kernel<ACT, G>, int64_t(workers) * G, kThreads, Ring<G>::smem, G, behind, st, p);
 }
-template <bool FWD>
-cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {
-    return G == 2 ? launch_group<FWD, 2>(p, behind, st) : launch_group<FWD, 1>(p, behind, st);
+template <int ACT> cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {
+    return G == 2 ? launch_group<ACT, 2>(p, behind, st) : launch_group<ACT, 1>(p, behind, st);
+}
+
+// Calls f with the activation as a constant.
+template <typename F> cudaError_t with_act(int32_t act, F &&f) {
+    if (act == HARTS_ACT_SILU) return f(std::integral_constant<int, HARTS_ACT_SILU>{});
+    if (act == HARTS_ACT_GELU) return f(std::integral_constant<int, HARTS_ACT_GELU>{});
+    return f(std::integral_constant<int, HARTS_ACT_NONE>{});
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -759,7 +786,7 @@ BwdPlan plan_bwd(int64_t C, int32_t K, int32_t N, int32_t act, bool bias) {
     b.sums = act != HARTS_ACT_NONE ? align256(2 * size_t(C) * N) : 0;
     b.part_x = b.sums + (bias ? align256(4 * size_t(b.chunks) * N) : 0);
     b.part_w = b.part_x + (b.dx.splits > 1 ? align256(4 * size_t(C) * K * b.dx.splits) : 0);
-    b.total = std::max<size_t>(256, b.part_w + (b.dw.splits > 1 ? align256(4 * size_t(N) * K * b.dw.splits) : 0));
+    b.total = b.part_w + (b.dw.splits > 1 ? align256(4 * size_t(N) * K * b.dw.splits) : 0);
     return b;
 }
 
@@ -772,9 +799,9 @@ extern "C" {
 
 size_t harts_linear_fwd_workspace_bytes(int64_t C, int32_t K, int32_t N) {
     if (!sizes_ok(C, K, N)) return 0;
-    if (by_dots(C)) return 256;
+    if (by_dots(C)) return 0;
     const Cut c = fwd_cut(C, K, N);
-    return c.splits > 1 ? align256(4 * size_t(C) * N * c.splits) : 256;
+    return c.splits > 1 ? align256(4 * size_t(C) * N * c.splits) : 0;
 }
 
 int harts_linear_fwd(const harts_linear_args *a, harts_stream_t stream) {
@@ -785,25 +812,25 @@ int harts_linear_fwd(const harts_linear_args *a, harts_stream_t stream) {
     if (a->y == a->z) { set_error("y and z are one buffer"); return HARTS_EINVAL; }
     if (a->y == a->x || a->z == a->x) { set_error("y and z may not be x"); return HARTS_EINVAL; }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const Epilogue ep{a->bias, static_cast<const __nv_bfloat16 *>(a->residual), a->activation};
+    const Epilogue ep{a->bias, static_cast<const __nv_bfloat16 *>(a->residual)};
     const int32_t C = static_cast<int32_t>(a->C);
     __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a->y), *z = static_cast<__nv_bfloat16 *>(a->z);
     if (by_dots(C)) {
-        const DotParams d{static_cast<const __nv_bfloat16 *>(a->x), static_cast<const __nv_bfloat16 *>(a->weight), y, z, ep, C, a->K, a->N};
+        const DotParams d{static_cast<const __nv_bfloat16 *>(a->x), static_cast<const __nv_bfloat16 *>(a->weight), y, z, ep, a->K, a->N};
         const int64_t blocks = (a->N / 2 + 7) / 8;
-        const cudaError_t e = C == 1 ? launch(linear_dot_kernel<1>, blocks, 256, 0, 1, false, st, d)
-                              : C == 2 ? launch(linear_dot_kernel<2>, blocks, 256, 0, 1, false, st, d)
-                              : C <= 4 ? launch(linear_dot_kernel<4>, blocks, 256, 0, 1, false, st, d)
-                                       : launch(linear_dot_kernel<8>, blocks, 256, 0, 1, false, st, d);
+        const cudaError_t e = with_act(a->activation, [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
+            return C == 1 ? launch(linear_dot_kernel<1, kAct>, blocks, 256, 0, 1, false, st, d) : launch(linear_dot_kernel<2, kAct>, blocks, 256, 0, 1, false, st, d);
+        });
         if (e != cudaSuccess) return cuda_fail(e, "linear forward launch");
         set_error("");
         return HARTS_OK;
     }
-    if (!a->workspace || a->workspace_bytes < harts_linear_fwd_workspace_bytes(a->C, a->K, a->N)) {
+    const Cut c = fwd_cut(a->C, a->K, a->N);
+    if (c.splits > 1 && (!a->workspace || a->workspace_bytes < align256(4 * size_t(a->C) * a->N * c.splits))) {
         set_error("workspace too small");
         return HARTS_ESMALLBUF;
     }
-    const Cut c = fwd_cut(a->C, a->K, a->N);
     float *part = c.splits > 1 ? static_cast<float *>(a->workspace) : nullptr;
     Params p;
     std::memset(&p, 0, sizeof(p));
@@ -817,13 +844,14 @@ int harts_linear_fwd(const harts_linear_args *a, harts_stream_t stream) {
         if (z) ok = ok && map_out(&p.prod[0].keep, z, 1, a->C, a->N, false);
     }
     if (!ok) { set_error("tensor map"); return HARTS_ECUDA; }
-    cudaError_t e = part ? launch_tiles<false>(p, c.G, false, st) : launch_tiles<true>(p, c.G, false, st);
+    cudaError_t e = part ? launch_tiles<-1>(p, c.G, false, st)
+                         : with_act(a->activation, [&](auto act) { return launch_tiles<decltype(act)::value>(p, c.G, false, st); });
     if (e == cudaSuccess && part) {
         Join j{};
         j.of[0] = JoinOne{part, y, z, a->C * a->N, a->N, c.splits};
         j.ep = ep;
         j.blocks0 = (j.of[0].values / 8 + 127) / 128;
-        e = launch(linear_join_kernel, j.blocks0, 128, 0, 1, true, st, j);
+        e = with_act(a->activation, [&](auto act) { return launch(linear_join_kernel<decltype(act)::value>, j.blocks0, 128, 0, 1, true, st, j); });
     }
     if (e != cudaSuccess) return cuda_fail(e, "linear forward launch");
     set_error("");
@@ -832,7 +860,7 @@ int harts_linear_fwd(const harts_linear_args *a, harts_stream_t stream) {
 
 size_t harts_linear_bwd_workspace_bytes(int64_t C, int32_t K, int32_t N, int32_t activation, int32_t with_bias) {
     if (!sizes_ok(C, K, N) || activation < HARTS_ACT_NONE || activation > HARTS_ACT_GELU) return 0;
-    return C == 0 ? 256 : plan_bwd(C, K, N, activation, with_bias != 0).total;
+    return C == 0 ? 0 : plan_bwd(C, K, N, activation, with_bias != 0).total;
 }
 
 int harts_linear_bwd(const harts_linear_bwd_args *b, harts_stream_t stream) {
@@ -861,7 +889,7 @@ int harts_linear_bwd(const harts_linear_bwd_args *b, harts_stream_t stream) {
         if ((b->dx && b->dx == q) || (b->dweight && b->dweight == q)) { set_error("dx and dweight may be none of the inputs"); return HARTS_EINVAL; }
     if (b->dx && b->dx == b->dweight) { set_error("two outputs in one buffer"); return HARTS_EINVAL; }
     const BwdPlan w = plan_bwd(a->C, a->K, a->N, a->activation, b->dbias != nullptr);
-    if (!a->workspace || a->workspace_bytes < w.total) { set_error("workspace too small"); return HARTS_ESMALLBUF; }
+    if (w.total && (!a->workspace || a->workspace_bytes < w.total)) { set_error("workspace too small"); return HARTS_ESMALLBUF; }
     if (reinterpret_cast<uintptr_t>(a->workspace) % 256) { set_error("workspace must be 256-byte aligned"); return HARTS_EINVAL; }
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     Params p;
@@ -888,19 +916,21 @@ int harts_linear_bwd(const harts_linear_bwd_args *b, harts_stream_t stream) {
     if (b->dbias || (curved && p.n_prod)) {
         const DzParams d{static_cast<const __nv_bfloat16 *>(b->d_y), curved ? static_cast<const __nv_bfloat16 *>(a->z) : nullptr,
                          reinterpret_cast<__nv_bfloat16 *>(ws), b->dbias ? reinterpret_cast<float *>(ws + w.sums) : nullptr,
-                         a->C, a->N, a->activation, w.per};
-        e = launch(linear_dz_kernel, int64_t(ceil_div(a->N, 256)) * w.chunks, 256, 0, 1, false, st, d);
+                         a->C, a->N, w.per};
+        e = with_act(a->activation, [&](auto act) {
+            return launch(linear_dz_kernel<decltype(act)::value>, int64_t(ceil_div(a->N, 256)) * w.chunks, 256, 0, 1, false, st, d);
+        });
         behind = true;
         if (e == cudaSuccess && b->dbias) {
             const DbParams s{reinterpret_cast<const float *>(ws + w.sums), b->dbias, a->N, w.chunks};
             e = launch(linear_db_kernel, ceil_div(a->N, 32), 1024, 0, 1, true, st, s);
         }
     }
-    if (e == cudaSuccess && p.n_prod) e = launch_tiles<false>(p, w.dx.G, behind, st);
+    if (e == cudaSuccess && p.n_prod) e = launch_tiles<-1>(p, w.dx.G, behind, st);
     if (e == cudaSuccess && joins) {
         int64_t blocks[2] = {(j.of[0].values / 8 + 127) / 128, joins > 1 ? (j.of[1].values / 8 + 127) / 128 : 0};
         j.blocks0 = blocks[0];
-        e = launch(linear_join_kernel, blocks[0] + blocks[1], 128, 0, 1, true, st, j);
+        e = launch(linear_join_kernel<HARTS_ACT_NONE>, blocks[0] + blocks[1], 128, 0, 1, true, st, j);
     }
     if (e != cudaSuccess) return cuda_fail(e, "linear backward launch");
     set_error("");

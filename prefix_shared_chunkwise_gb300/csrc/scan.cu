@@ -465,7 +465,7 @@ struct Space { size_t inc, agg, total; };       // behind 256 bytes with the tic
 Space space_of(const harts_plan *P, int32_t D, int32_t dtype) {
     const size_t width = size_t(ceil_div(D, wide_of(dtype))) * wide_of(dtype);
     Space s{};
-    if (P->image.scan_alone) { s.total = 256; return s; }
+    if (P->image.scan_alone) return s;
     s.inc = 256;
     s.agg = s.inc + align256(4 * width * P->image.n_scan_groups);
     s.total = s.agg + align256(8 * width * P->image.n_scan);
@@ -533,7 +533,8 @@ int check(const harts_plan *P, const harts_scan_fwd_args *a) {
         set_error("more tiles than the library counts");
         return HARTS_EOVERFLOW;
     }
-    if (!a->workspace || a->workspace_bytes < space_of(P, a->channels, a->dtype).total) {
+    const size_t need = space_of(P, a->channels, a->dtype).total;
+    if (need && (!a->workspace || a->workspace_bytes < need)) {
         set_error("workspace too small");
         return HARTS_ESMALLBUF;
     }
