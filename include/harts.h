@@ -368,7 +368,8 @@ typedef struct {
     const void *g;           /* device [C][D] */
     const float *h0;         /* device [n_roots][D] initial state of every root, or NULL (zero) */
     void *h;                 /* device [C][D]: written by the forward, read by the backward; not x or g */
-    float *final_state;      /* device [n_seq][D] output: state after every sequence's last row, or NULL */
+    float *final_state;      /* device [n_seq][D] output: state after every sequence's last row, or NULL;
+                                may be h0 in a decoding step (a plan of single rows) */
     void *workspace;         /* device, harts_scan_workspace_bytes, 16-byte aligned; calls that may run
                                 at the same time have one each */
     size_t workspace_bytes;
@@ -389,7 +390,7 @@ typedef struct {
     const float *d_final;    /* device [n_seq][D] dL/dfinal_state, or NULL */
     void *dx;                /* device [C][D] output; dx and dg may be none of the inputs */
     void *dg;                /* device [C][D] output */
-    float *dh0;              /* device [n_roots][D] output, or NULL */
+    float *dh0;              /* device [n_roots][D] output, or NULL; not h0, d_final only in a decoding step */
 } harts_scan_bwd_args;
 
 /* Backward: with lam[r] = d_h[r] + the sum of a[c] lam[c] over the rows c that follow r (+ d_final

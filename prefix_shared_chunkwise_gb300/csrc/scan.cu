@@ -517,7 +517,6 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 int check(const harts_plan *P, const harts_scan_fwd_args *a) {
     if (!P || !a) { set_error("NULL plan or args"); return HARTS_EINVAL; }
-    if (!P->dev) { set_error("plan not uploaded (harts_plan_upload)"); return HARTS_ENOPLAN; }
     if (a->dtype != HARTS_FP32 && a->dtype != HARTS_BF16) { set_error("dtype"); return HARTS_EUNSUPPORTED; }
     if (a->channels < 8 || a->channels % 8) { set_error("channels must be a positive multiple of 8"); return HARTS_EINVAL; }
     if (a->form != HARTS_SCAN_ADD && a->form != HARTS_SCAN_MIX) { set_error("form must be 0 (add) or 1 (mix)"); return HARTS_EINVAL; }
@@ -528,11 +527,21 @@ int check(const harts_plan *P, const harts_scan_fwd_args *a) {
     }
     if (a->h == a->x || a->h == a->g) { set_error("h may be neither x nor g"); return HARTS_EINVAL; }
     if (!aligned16(a->h0) || !aligned16(a->final_state)) { set_error("h0 and final_state must be 16-byte aligned"); return HARTS_EINVAL; }
+    if (a->final_state && a->final_state == a->h0 && !one_step(P)) {
+        set_error("final_state may be h0 only in a plan of single rows");
+        return HARTS_EINVAL;
+    }
     if (P->info.C > (int64_t(1) << 38) / a->channels) { set_error("tensor too large"); return HARTS_EOVERFLOW; }
     if (int64_t(P->image.n_scan) * ceil_div(a->channels, wide_of(a->dtype)) > 0x7fffffff) {
         set_error("more tiles than the library counts");
         return HARTS_EOVERFLOW;
     }
+    return HARTS_OK;
+}
+
+// What comes last: the plan's tables, and the workspace.
+int check_space(const harts_plan *P, const harts_scan_fwd_args *a) {
+    if (!P->dev) { set_error("plan not uploaded (harts_plan_upload)"); return HARTS_ENOPLAN; }
     const size_t need = space_of(P, a->channels, a->dtype).total;
     if (need && (!a->workspace || a->workspace_bytes < need)) {
         set_error("workspace too small");
@@ -590,7 +599,8 @@ size_t harts_scan_workspace_bytes(const harts_plan *P, int32_t channels, int32_t
 }
 
 int harts_scan_fwd(const harts_plan *P, const harts_scan_fwd_args *a, harts_stream_t stream) {
-    const int rc = check(P, a);
+    int rc = check(P, a);
+    if (!rc) rc = check_space(P, a);
     if (rc) return rc;
     ScanParams p = params_of(P, a, false);
     p.out0 = a->h;
@@ -604,7 +614,7 @@ int harts_scan_fwd(const harts_plan *P, const harts_scan_fwd_args *a, harts_stre
 
 int harts_scan_bwd(const harts_plan *P, const harts_scan_bwd_args *a, harts_stream_t stream) {
     if (!a) { set_error("NULL args"); return HARTS_EINVAL; }
-    const int rc = check(P, &a->fwd);
+    int rc = check(P, &a->fwd);
     if (rc) return rc;
     if (!a->d_h || !a->dx || !a->dg) { set_error("NULL d_h, dx or dg"); return HARTS_EINVAL; }
     if (!aligned16(a->d_h) || !aligned16(a->dx) || !aligned16(a->dg)) { set_error("d_h, dx and dg must be 16-byte aligned"); return HARTS_EINVAL; }
@@ -612,6 +622,13 @@ int harts_scan_bwd(const harts_plan *P, const harts_scan_bwd_args *a, harts_stre
     for (const void *q : in_use)
         if (a->dx == q || a->dg == q || a->dx == a->dg) { set_error("dx and dg may be none of the inputs"); return HARTS_EINVAL; }
     if (!aligned16(a->d_final) || !aligned16(a->dh0)) { set_error("d_final and dh0 must be 16-byte aligned"); return HARTS_EINVAL; }
+    if (a->dh0 && a->dh0 == a->d_final && !one_step(P)) {
+        set_error("dh0 may be d_final only in a plan of single rows");
+        return HARTS_EINVAL;
+    }
+    if (a->dh0 && a->dh0 == a->fwd.h0) { set_error("dh0 may not be h0"); return HARTS_EINVAL; }
+    rc = check_space(P, &a->fwd);
+    if (rc) return rc;
     ScanParams p = params_of(P, &a->fwd, true);
     p.h_in = a->fwd.h;
     p.x_in = a->fwd.x;
