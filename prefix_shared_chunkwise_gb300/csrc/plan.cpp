@@ -532,6 +532,7 @@ void build_image(harts_plan &P) {
     // before it in either order.
     std::vector<ScanTile> tiles;
     std::vector<int32_t> gfirst(n + 1, 0), depth, height, snext;
+    std::vector<int64_t> behind(n, 0);                  // rows from the root to a segment's end
     for (int32_t v = 0; v < n; ++v)
         gfirst[v + 1] = gfirst[v] + static_cast<int32_t>((P.seg_len[v] + kScanRows * kScanGroup - 1) / (kScanRows * kScanGroup));
     const int32_t n_groups = gfirst[n];
@@ -542,6 +543,7 @@ void build_image(harts_plan &P) {
         const int32_t u = P.parent[v], root_id = u < 0 ? root_no++ : 0;
         const int64_t count = (P.seg_len[v] + kScanRows - 1) / kScanRows;
         alone = alone && u < 0 && count == 1;
+        behind[v] = P.seg_len[v] + (u < 0 ? 0 : behind[u]);
         for (int64_t t = 0; t < count; ++t) {
             ScanTile s{};
             s.tile = static_cast<int32_t>(tiles.size());
@@ -586,6 +588,7 @@ void build_image(harts_plan &P) {
     I.n_scan = static_cast<int32_t>(tiles.size());
     I.n_scan_groups = n_groups;
     I.scan_alone = alone;
+    I.scan_longest = *std::max_element(behind.begin(), behind.end());
     while (w.size() % 64) w.push_back(0);
 }
 

@@ -84,6 +84,7 @@ struct PlanImage {
         off_attn_mptr, off_attn_mask, off_attn_hp, off_attn_qt, off_attn_kt, off_attn_kptr, off_attn_kq,
         off_scan_fwd, off_scan_bwd, off_scan_next;
     int32_t n_qt, n_kt, n_scan, n_scan_groups, scan_alone;
+    int64_t scan_longest;          // rows of the longest trajectory
 };
 
 void set_error(const std::string &msg);

@@ -247,3 +247,21 @@ def test_captured_and_on_another_stream():
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(want, out))
     assert c.plan.device_error() == 0
+
+
+def test_slow_decays_over_a_long_trajectory():
+    """x = 1 and a decay per channel that stays: h_t = (1 - a^(t+1)) / (1 - a).  A row adds half a u for a
+    (a rounded number below 1), one for the product of decays and as much for the sum, of which 1 in 16, 1 in
+    128 and 1 in 4,096 rows have more: 1.7 u in all, once for every row that a term is old."""
+    T, D = 131_072, 64
+    plan = Plan([-1], [T], 64).upload()
+    g = -torch.exp(torch.linspace(-4, -15, D)).bfloat16()
+    x = torch.ones(T, D, dtype=torch.bfloat16, device="cuda")
+    h = scan_fwd(plan, x, g.cuda().expand(T, D).contiguous())
+    torch.cuda.synchronize()
+    assert plan.device_error() == 0
+    n, lg = np.arange(1, T + 1)[:, None], _np(g)[None]
+    ref = np.expm1(n * lg) / np.expm1(lg)
+    a = np.exp(lg)
+    age = a / -np.expm1(lg) - n * np.exp(n * lg) / -np.expm1(n * lg)        # of a term, by its share of the sum
+    assert np.all(np.abs(_np(h) - ref) <= (2.0 ** -8 + 1.7 * U * (age + 1)) * ref)
