@@ -527,68 +527,72 @@ void build_image(harts_plan &P) {
 
     // ---- gated scan -------------------------------------------------------------------
     // Tiles of kScanRows rows of one segment, so that a fork always lies at a tile's end, in
-    // groups of kScanGroup.  Forward by the number of groups before a tile, backward by the most
+    // groups of `group` tiles.  Forward by the number of groups before a tile, backward by the most
     // groups behind it: what a tile waits for (in its group: the tiles on the way to it) comes
     // before it in either order.
-    std::vector<ScanTile> tiles;
-    std::vector<int32_t> gfirst(n + 1, 0), depth, height, snext;
     std::vector<int64_t> behind(n, 0);                  // rows from the root to a segment's end
-    for (int32_t v = 0; v < n; ++v)
-        gfirst[v + 1] = gfirst[v] + static_cast<int32_t>((P.seg_len[v] + kScanRows * kScanGroup - 1) / (kScanRows * kScanGroup));
-    const int32_t n_groups = gfirst[n];
-    depth.assign(n_groups, 0);
-    height.assign(n_groups, 0);
     bool alone = true;
-    for (int32_t v = 0, root_no = 0; v < n; ++v) {
-        const int32_t u = P.parent[v], root_id = u < 0 ? root_no++ : 0;
-        const int64_t count = (P.seg_len[v] + kScanRows - 1) / kScanRows;
-        alone = alone && u < 0 && count == 1;
-        behind[v] = P.seg_len[v] + (u < 0 ? 0 : behind[u]);
-        for (int64_t t = 0; t < count; ++t) {
-            ScanTile s{};
-            s.tile = static_cast<int32_t>(tiles.size());
-            s.row0 = static_cast<int32_t>(P.seg_offset[v] + t * kScanRows);
-            s.rows = static_cast<int32_t>(std::min<int64_t>(kScanRows, P.seg_len[v] - t * kScanRows));
-            s.at = static_cast<int32_t>(t % kScanGroup);
-            s.group = gfirst[v] + static_cast<int32_t>(t / kScanGroup);
-            s.count = static_cast<int32_t>(std::min<int64_t>(kScanGroup, count - (t - s.at)));
-            const int32_t outer = u < 0 ? -1 - root_id : 0;
-            s.pred = t >= kScanGroup ? s.group - 1 : u < 0 ? outer : gfirst[u + 1] - 1;
-            s.pred_row = t > 0 ? s.row0 - 1 : u < 0 ? outer : static_cast<int32_t>(P.seg_offset[u] + P.seg_len[u] - 1);
-            const bool last = s.group == gfirst[v + 1] - 1;
-            s.seq_end = last && P.seg_ctop[v] < 0 ? P.seg_seq[v] : -1;
-            s.next_begin = static_cast<int32_t>(snext.size());
-            s.next_count = last ? kptr[v + 1] - kptr[v] : 1;
-            if (s.pred >= 0) depth[s.group] = depth[s.pred] + 1;
-            if (s.at == s.count - 1) {
-                if (last) for (int32_t j = kptr[v]; j < kptr[v + 1]; ++j) snext.push_back(gfirst[kids[j]]);
-                else snext.push_back(s.group + 1);
-            }
-            tiles.push_back(s);
-        }
+    for (int32_t v = 0; v < n; ++v) {
+        alone = alone && P.parent[v] < 0 && P.seg_len[v] <= kScanRows;
+        behind[v] = P.seg_len[v] + (P.parent[v] < 0 ? 0 : behind[P.parent[v]]);
     }
-    for (size_t t = tiles.size(); t-- > 0;)             // a group comes after its predecessor here too
-        if (tiles[t].pred >= 0) height[tiles[t].pred] = std::max(height[tiles[t].pred], height[tiles[t].group] + 1);
-    // Of groups that may run side by side, the first tiles of all come before the second ones: by
-    // then what the tiles of a group publish for the next is long there.
-    std::vector<ScanTile> by = tiles;
-    std::sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) {
-        if (depth[a.group] != depth[b.group]) return depth[a.group] < depth[b.group];
-        return a.at != b.at ? a.at < b.at : a.tile < b.tile;
-    });
-    constexpr size_t kWords = sizeof(ScanTile) / sizeof(int32_t);
-    put(I.off_scan_fwd, reinterpret_cast<const int32_t *>(by.data()), by.size() * kWords);
-    std::sort(by.begin(), by.end(), [&](const ScanTile &a, const ScanTile &b) {
-        if (height[a.group] != height[b.group]) return height[a.group] < height[b.group];
-        const int32_t u = a.count - a.at, v = b.count - b.at;
-        return u != v ? u < v : a.tile < b.tile;
-    });
-    put(I.off_scan_bwd, reinterpret_cast<const int32_t *>(by.data()), by.size() * kWords);
-    put(I.off_scan_next, snext.data(), snext.size());
-    I.n_scan = static_cast<int32_t>(tiles.size());
-    I.n_scan_groups = n_groups;
     I.scan_alone = alone;
     I.scan_longest = *std::max_element(behind.begin(), behind.end());
+    for (int cut = 0; cut < 2; ++cut) {
+        const int group = kScanGroups[cut];
+        std::vector<ScanTile> tiles;
+        std::vector<int32_t> gfirst(n + 1, 0), depth, height, snext;
+        for (int32_t v = 0; v < n; ++v)
+            gfirst[v + 1] = gfirst[v] + static_cast<int32_t>((P.seg_len[v] + kScanRows * group - 1) / (kScanRows * group));
+        const int32_t n_groups = gfirst[n];
+        depth.assign(n_groups, 0);
+        height.assign(n_groups, 0);
+        for (int32_t v = 0, root_no = 0; v < n; ++v) {
+            const int32_t u = P.parent[v], root_id = u < 0 ? root_no++ : 0;
+            const int64_t count = (P.seg_len[v] + kScanRows - 1) / kScanRows;
+            for (int64_t t = 0; t < count; ++t) {
+                ScanTile s{};
+                s.tile = static_cast<int32_t>(tiles.size());
+                s.row0 = static_cast<int32_t>(P.seg_offset[v] + t * kScanRows);
+                s.rows = static_cast<int32_t>(std::min<int64_t>(kScanRows, P.seg_len[v] - t * kScanRows));
+                s.at = static_cast<int32_t>(t % group);
+                s.group = gfirst[v] + static_cast<int32_t>(t / group);
+                s.count = static_cast<int32_t>(std::min<int64_t>(group, count - (t - s.at)));
+                const int32_t outer = u < 0 ? -1 - root_id : 0;
+                s.pred = t >= group ? s.group - 1 : u < 0 ? outer : gfirst[u + 1] - 1;
+                s.pred_row = t > 0 ? s.row0 - 1 : u < 0 ? outer : static_cast<int32_t>(P.seg_offset[u] + P.seg_len[u] - 1);
+                const bool last = s.group == gfirst[v + 1] - 1;
+                s.seq_end = last && P.seg_ctop[v] < 0 ? P.seg_seq[v] : -1;
+                s.next_begin = static_cast<int32_t>(snext.size());
+                s.next_count = last ? kptr[v + 1] - kptr[v] : 1;
+                if (s.pred >= 0) depth[s.group] = depth[s.pred] + 1;
+                if (s.at == s.count - 1) {
+                    if (last) for (int32_t j = kptr[v]; j < kptr[v + 1]; ++j) snext.push_back(gfirst[kids[j]]);
+                    else snext.push_back(s.group + 1);
+                }
+                tiles.push_back(s);
+            }
+        }
+        for (size_t t = tiles.size(); t-- > 0;)         // a group comes after its predecessor here too
+            if (tiles[t].pred >= 0) height[tiles[t].pred] = std::max(height[tiles[t].pred], height[tiles[t].group] + 1);
+        constexpr size_t kWords = sizeof(ScanTile) / sizeof(int32_t);
+        I.n_scan = static_cast<int32_t>(tiles.size());
+        I.n_scan_groups[cut] = n_groups;
+        put(I.off_scan_next[cut], snext.data(), snext.size());
+        // Of groups that may run side by side, the first tiles of all come before the second ones: by
+        // then what the tiles of a group publish for the next is long there.
+        std::sort(tiles.begin(), tiles.end(), [&](const ScanTile &a, const ScanTile &b) {
+            if (depth[a.group] != depth[b.group]) return depth[a.group] < depth[b.group];
+            return a.at != b.at ? a.at < b.at : a.tile < b.tile;
+        });
+        put(I.off_scan_fwd[cut], reinterpret_cast<const int32_t *>(tiles.data()), tiles.size() * kWords);
+        std::sort(tiles.begin(), tiles.end(), [&](const ScanTile &a, const ScanTile &b) {
+            if (height[a.group] != height[b.group]) return height[a.group] < height[b.group];
+            const int32_t u = a.count - a.at, v = b.count - b.at;
+            return u != v ? u < v : a.tile < b.tile;
+        });
+        put(I.off_scan_bwd[cut], reinterpret_cast<const int32_t *>(tiles.data()), tiles.size() * kWords);
+    }
     while (w.size() % 64) w.push_back(0);
 }
 

@@ -11,13 +11,14 @@
 // value is read and written once; HBM bounds the work, and the chain of carries must not.  The
 // planner cuts segments into tiles of 128 rows (a fork lies at a tile's end); a block takes a
 // tile of 128 bytes of channels: eight warps of 16 rows each compose their rows' map, a ninth
-// joins the eight and publishes the tile's map, and forms the carry from the maps of the tiles before
-// it in its group (up to 32 of a segment, which need not wait for one another) and the state that
-// the group before left, both fetched while the rows are still on their way.  So a chain waits once for 4,096 rows.  The order in which maps are joined is fixed
-// by position: no atomics on values, the same bits on every run.  What is published carries its
-// own validity: the workspace starts as all ones, a NaN that no published value has.  Tiles are
-// taken in an order that has predecessors first, by a ticket counter, so that whatever a block
-// waits for is in the hands of a running one; every wait is bounded all the same.
+// joins the eight and forms the carry, from the maps that the tiles before it in its group published
+// (16 or 32 tiles of a segment, which need not wait for one another) and the state that the group before
+// left, both fetched while the rows are still on their way: a chain waits once for 2,048 or 4,096 rows,
+// about 1 us.  The order in which maps are joined is fixed by position: no atomics on values, the same
+// bits on every run.  What is published carries its own validity: the workspace starts as all ones, a NaN
+// that no published value has.  Tiles are taken in an order that has predecessors first, by a ticket
+// counter, so that whatever a block waits for is in the hands of a running one; every wait is bounded all
+// the same.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -183,36 +184,49 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f)
 }
 
 // Tensors of a tile, stages of the ring and blocks of an SM: as many bytes on their way as shared
-// memory holds.
-template <bool BWD, bool MIX> struct Ring {
-    static constexpr int tensors = BWD ? 3 : 2, stages = 2, blocks = BWD ? 2 : 3;
+// memory holds.  AHEAD: a tile's map is composed, and published, before the results of the tile
+// before it in the block, whose carry may be long in coming: on long trajectories all blocks would
+// otherwise compose and then wait together.  That takes the registers of two tiles' decays, so a third
+// block's, and does nothing for tiles that need not wait: the forward takes it where the longest trajectory has
+// kAheadRows rows.  (bf16, mix form: one of 131,072 rows of 1,024 channels 192 us, 339 without; 4 of
+// 16,384 rows of 2,048 channels 170 and 202, 8 of 8,192 rows 168 and 177, 16 of 4,200 rows 172 and 169,
+// 16 chains of 40 segments of 200 rows 215 and 197.)
+constexpr int64_t kAheadRows = 8192;
+// Up to so many tiles across, the chain of carries is all there is, and the longer groups are
+// taken forward too.  (131,072 rows, bf16, mix: 64 channels 35 us, 54 in groups of 16; 128: 49 and 72; 256:
+// 79 and 76; 1,024: 221 and 192.  Backward, 1,024 channels: 345 and 394.)
+constexpr int32_t kNarrow = 2;
+template <bool BWD, bool AHEAD> struct Ring {
+    static constexpr int tensors = BWD ? 3 : 2, stages = AHEAD ? 3 : 2, blocks = BWD || AHEAD ? 2 : 3;
     static constexpr uint32_t stage_bytes = tensors * kTileBytes;
     static constexpr uint32_t smem = stages * stage_bytes + 128;
 };
 
 struct Meta { ScanTile t; int32_t col; };                      // rows 0: the end
 
-template <typename T, bool BWD, bool MIX, int KIND>
-__global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(const __grid_constant__ ScanParams p) {
-    using R = Ring<BWD, MIX>;
+template <typename T, bool BWD, bool MIX, int KIND, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kernel(const __grid_constant__ ScanParams p) {
+    using R = Ring<BWD, AHEAD>;
     using L = Lane<T>;
     using V = typename L::V;
     constexpr int CH = L::n, kWide = 32 * CH;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((128 - (tc::smem_addr(smraw) & 127)) & 127);
     __shared__ uint64_t known[R::stages], full[R::stages], empty[R::stages];
-    __shared__ uint64_t maps_full[2], carry_full[2];           // by tile parity, as what they guard
+    __shared__ uint64_t maps_full[R::stages], carry_full[R::stages];
     __shared__ Meta meta[R::stages];
-    __shared__ V s_a[2][kWarps][32], s_b[2][kWarps][32], s_carry[2][32];           // the warps' maps, the carry
-    __shared__ int s_fail;
+    __shared__ V s_a[R::stages][kWarps][32], s_b[R::stages][kWarps][32], s_carry[R::stages][32];   // the warps' maps, the carry
+    __shared__ int s_fail, s_mapped[R::stages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < R::stages; ++s) {
             tc::mbar_init(&known[s], 1);
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], kWarps + 1);
+            tc::mbar_init(&maps_full[s], kWarps);
+            tc::mbar_init(&carry_full[s], 1);
+            s_mapped[s] = 0;
         }
-        for (int i = 0; i < 2; ++i) { tc::mbar_init(&maps_full[i], kWarps); tc::mbar_init(&carry_full[i], 1); }
         tc::fence_mbar_init();
         s_fail = 0;
     }
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
         // between the group's carry and the tile are joined, in the order of the rows; then comes
         // whichever is there first, the carry or the tile's own map, which others wait for.
         for (uint32_t it = 0;; ++it) {
-            const int s = it % R::stages, par = it & 1;
+            const int s = it % R::stages;
             if (!warp_wait(&known[s], (it / R::stages) & 1, &s_fail)) break;
             const Meta m = meta[s];
             if (m.t.rows == 0) break;
@@ -277,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
             int left = BWD ? m.t.next_count : m.t.pred >= 0;   // states still to come, in order
             const long long t0 = clock64();
             while (!mapped || !carried) {
-                if (!mapped && __all_sync(0xffffffffu, is_done(&maps_full[par], (it >> 1) & 1))) {
+                if (!mapped && __all_sync(0xffffffffu, is_done(&maps_full[s], (it / R::stages) & 1))) {
 #pragma unroll
                     for (int i = 0; i < kWarps; ++i) {
                         const int w = BWD ? kWarps - 1 - i : i;
-                        B = fma(s_a[par][w][lane], B, s_b[par][w][lane]);
-                        A = mul(s_a[par][w][lane], A);
+                        B = fma(s_a[s][w][lane], B, s_b[s][w][lane]);
+                        A = mul(s_a[s][w][lane], A);
                     }
-                    if (BWD ? m.t.at > 0 : m.t.at < m.t.count - 1) {
+                    if (!AHEAD && (BWD ? m.t.at > 0 : m.t.at < m.t.count - 1)) {
                         if constexpr (CH == 2) { publish(agg, A.x, B.x); publish(agg + 1, A.y, B.y); }
                         else publish(agg, A, B);
                     }
@@ -332,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
                     if (BWD && m.t.seq_end >= 0 && p.d_final && inside)
                         v = add(v, L::load(p.d_final + static_cast<int64_t>(m.t.seq_end) * p.D + ch));
                     if (between > 0) v = fma(pa, v, pb);
-                    s_carry[par][lane] = v;
+                    s_carry[s][lane] = v;
                     __syncwarp();
-                    if (lane == 0) arrive(&carry_full[par]);
+                    if (lane == 0) arrive(&carry_full[s]);
                     carried = true;
                 }
                 if (clock64() - t0 > 4000000000LL) *reinterpret_cast<volatile int *>(&s_fail) = 1;
@@ -350,30 +364,28 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
             if (lane == 0) arrive(&empty[s]);
         }
     } else {
-        for (uint32_t it = 0;; ++it) {
-            const int s = it % R::stages, par = it & 1;
-            if (!warp_wait(&full[s], (it / R::stages) & 1, &s_fail)) break;
-            const int rows = meta[s].t.rows, row0 = meta[s].t.row0;
-            if (rows == 0) break;
+        // The tile's rows, 0 behind the last one, -1 where a wait did not end.
+        auto map_tile = [&](uint32_t it, V (&d)[kWarpRows], [[maybe_unused]] V &before, [[maybe_unused]] uint32_t *xr) -> int {
+            const int s = it % R::stages;
+            if (!warp_wait(&full[s], (it / R::stages) & 1, &s_fail)) return -1;
+            const int rows = meta[s].t.rows;
+            if (rows == 0) return 0;
             const int mine = min(max(rows - warp * kWarpRows, 0), kWarpRows);
             const uint8_t *src = sm + s * R::stage_bytes + warp * kWarpRows * 128 + lane * 4;
             const int64_t ch = meta[s].col + lane * CH;
-            [[maybe_unused]] V before = L::all(0.f);           // state before the tile's first row
-            if (BWD && warp == 0 && ch < p.D) {
+            if (BWD && warp == 0 && ch < p.D) {                // state before the tile's first row
                 const int32_t pr = meta[s].t.pred_row;
+                before = L::all(0.f);
                 if (pr >= 0) before = L::get(static_cast<const T *>(p.h_in) + static_cast<int64_t>(pr) * p.D + ch);
                 else if (p.h0) before = L::load(p.h0 + static_cast<int64_t>(-1 - pr) * p.D + ch);
             }
-            // the mix form's x, wanted last and by one thread only, does not go through shared memory,
-            // which has room for two blocks' other tensors
-            [[maybe_unused]] uint32_t xr[BWD && MIX ? kWarpRows : 1];
             if constexpr (BWD && MIX) {
-                const T *xp = static_cast<const T *>(p.x_in) + static_cast<int64_t>(row0 + warp * kWarpRows) * p.D + ch;
+                const T *xp = static_cast<const T *>(p.x_in) + static_cast<int64_t>(meta[s].t.row0 + warp * kWarpRows) * p.D + ch;
 #pragma unroll
                 for (int i = 0; i < kWarpRows; ++i)
                     xr[i] = i < mine && ch < p.D ? __ldcs(reinterpret_cast<const uint32_t *>(xp + static_cast<int64_t>(i) * p.D)) : 0u;
             }
-            V d[kWarpRows], A = L::all(1.f), B = L::all(0.f);
+            V A = L::all(1.f), B = L::all(0.f);
             auto map_row = [&](int i) {
                 const V u = L::get(src + kTileBytes + i * 128);
                 d[i] = decay<KIND, T>(L::get(src + i * 128));
@@ -390,15 +402,42 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
                 for (int k = 0; k < kWarpRows; ++k)
                     if ((BWD ? kWarpRows - 1 - k : k) < mine) map_row(BWD ? kWarpRows - 1 - k : k);
             }
-            s_a[par][warp][lane] = A;
-            s_b[par][warp][lane] = B;
+            s_a[s][warp][lane] = A;
+            s_b[s][warp][lane] = B;
             __syncwarp();
-            if (lane == 0) arrive(&maps_full[par]);
-            if (!warp_wait(&maps_full[par], (it >> 1) & 1, &s_fail) || !warp_wait(&carry_full[par], (it >> 1) & 1, &s_fail)) break;
-            V v = s_carry[par][lane];
-            for (int k = BWD ? kWarps - 1 : 0; k != warp; k += BWD ? -1 : 1) v = fma(s_a[par][k][lane], v, s_b[par][k][lane]);
+            int last = 0;
+            if (lane == 0) {
+                arrive(&maps_full[s]);
+                if (AHEAD) {
+                    __threadfence_block();
+                    last = atomicAdd(&s_mapped[s], 1) == kWarps - 1;
+                    __threadfence_block();
+                    if (last) s_mapped[s] = 0;
+                }
+            }
+            if (AHEAD && __shfl_sync(0xffffffffu, last, 0) && meta[s].t.at < meta[s].t.count - 1) {
+                A = L::all(1.f), B = L::all(0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    B = fma(s_a[s][w][lane], B, s_b[s][w][lane]);
+                    A = mul(s_a[s][w][lane], A);
+                }
+                float2 *agg = p.agg + static_cast<int64_t>(meta[s].t.tile) * p.width + ch;
+                if constexpr (CH == 2) { publish(agg, A.x, B.x); publish(agg + 1, A.y, B.y); }
+                else publish(agg, A, B);
+            }
+            return rows;
+        };
+        auto results = [&](uint32_t it, const V (&d)[kWarpRows], [[maybe_unused]] V before, [[maybe_unused]] const uint32_t *xr) -> bool {
+            const int s = it % R::stages;
+            if (!warp_wait(&maps_full[s], (it / R::stages) & 1, &s_fail) || !warp_wait(&carry_full[s], (it / R::stages) & 1, &s_fail)) return false;
+            const int rows = meta[s].t.rows, mine = min(max(rows - warp * kWarpRows, 0), kWarpRows);
+            const uint8_t *src = sm + s * R::stage_bytes + warp * kWarpRows * 128 + lane * 4;
+            const int64_t ch = meta[s].col + lane * CH;
+            V v = s_carry[s][lane];
+            for (int k = BWD ? kWarps - 1 : 0; k != warp; k += BWD ? -1 : 1) v = fma(s_a[s][k][lane], v, s_b[s][k][lane]);
             if (ch < p.D) {
-                const int64_t at = static_cast<int64_t>(row0 + warp * kWarpRows) * p.D + ch;
+                const int64_t at = static_cast<int64_t>(meta[s].t.row0 + warp * kWarpRows) * p.D + ch;
                 T *out0 = static_cast<T *>(p.out0) + at;
                 [[maybe_unused]] T *out1 = static_cast<T *>(p.out1) + at;
                 auto row = [&](int i) {
@@ -430,6 +469,22 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, MIX>::blocks) scan_kernel(
             }
             __syncwarp();
             if (lane == 0) arrive(&empty[s]);
+            return true;
+        };
+        V d[kWarpRows], before = L::all(0.f);
+        uint32_t xr[BWD && MIX ? kWarpRows : 1];
+        if constexpr (AHEAD) {
+            V next[kWarpRows];
+            int rows = map_tile(0, d, before, xr);
+            for (uint32_t it = 0; rows > 0; ++it) {
+                rows = map_tile(it + 1, next, before, xr);
+                if (rows < 0 || !results(it, d, before, xr)) break;
+#pragma unroll
+                for (int i = 0; i < kWarpRows; ++i) d[i] = next[i];
+            }
+        } else {
+            for (uint32_t it = 0; map_tile(it, d, before, xr) > 0; ++it)
+                if (!results(it, d, before, xr)) break;
         }
     }
     __syncthreads();
@@ -471,7 +526,7 @@ Space space_of(const harts_plan *P, int32_t D, int32_t dtype) {
     Space s{};
     if (P->image.scan_alone) return s;
     s.inc = 256;
-    s.agg = s.inc + align256(4 * width * P->image.n_scan_groups);
+    s.agg = s.inc + align256(4 * width * std::max(P->image.n_scan_groups[0], P->image.n_scan_groups[1]));
     s.total = s.agg + align256(8 * width * P->image.n_scan);
     return s;
 }
@@ -486,11 +541,11 @@ template <typename T> bool map_rows(CUtensorMap *m, const void *base, int64_t C,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool BWD, bool MIX, int KIND>
+template <typename T, bool BWD, bool MIX, int KIND, bool AHEAD>
 cudaError_t launch_scan(const ScanParams &p, cudaStream_t st) {
-    using R = Ring<BWD, MIX>;
+    using R = Ring<BWD, AHEAD>;
     static std::atomic<uint64_t> done{0};
-    auto *k = scan_kernel<T, BWD, MIX, KIND>;
+    auto *k = scan_kernel<T, BWD, MIX, KIND, AHEAD>;
     const cudaError_t e = allow_smem(k, R::smem, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = std::min<int64_t>(p.total, int64_t(sm_count()) * R::blocks);
@@ -506,15 +561,18 @@ cudaError_t run(const harts_plan *P, ScanParams &p, const void *const (&in)[4], 
         return launch(scan_step_kernel<T, BWD, MIX>, (n / Lane<T>::n + 127) / 128, 128, 0, 1, false, st, p, static_cast<const T *>(in[0]),
                       static_cast<const T *>(in[1]), static_cast<const T *>(in[3]), n);
     }
-    for (int i = 0; i < Ring<BWD, MIX>::tensors; ++i)
+    for (int i = 0; i < Ring<BWD, false>::tensors; ++i)
         if (!map_rows<T>(&p.map[i], in[i], C, p.D)) return cudaErrorInvalidValue;
     if (p.ticket) {
         const cudaError_t e = cudaMemsetAsync(ws, 0xff, bytes, st);
         if (e != cudaSuccess) return e;
     }
     if constexpr (!MIX && std::is_same<T, __nv_bfloat16>::value)
-        if (!precise && P->image.scan_longest <= kFastRows) return launch_scan<T, BWD, MIX, kFast>(p, st);
-    return launch_scan<T, BWD, MIX, !MIX ? kExact : BWD ? kBoth : kRest>(p, st);
+        if (!precise && P->image.scan_longest <= kFastRows) return launch_scan<T, BWD, MIX, kFast, false>(p, st);
+    constexpr int KIND = !MIX ? kExact : BWD ? kBoth : kRest;
+    if constexpr (!BWD)
+        if (P->image.scan_longest >= kAheadRows) return launch_scan<T, BWD, MIX, KIND, true>(p, st);
+    return launch_scan<T, BWD, MIX, KIND, false>(p, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -559,8 +617,10 @@ ScanParams params_of(const harts_plan *P, const harts_scan_fwd_args *a, bool bac
     std::memset(&p, 0, sizeof(p));
     const Space s = space_of(P, a->channels, a->dtype);
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
-    p.tiles = backward ? P->view.scan_bwd : P->view.scan_fwd;
-    p.next = P->view.scan_next;
+    p.cols = ceil_div(a->channels, wide_of(a->dtype));
+    const int cut = backward || p.cols <= kNarrow;
+    p.tiles = backward ? P->view.scan_bwd[cut] : P->view.scan_fwd[cut];
+    p.next = P->view.scan_next[cut];
     p.h0 = a->h0;
     if (!P->image.scan_alone) {
         p.ticket = reinterpret_cast<uint32_t *>(ws);
@@ -569,7 +629,6 @@ ScanParams params_of(const harts_plan *P, const harts_scan_fwd_args *a, bool bac
     }
     p.error = P->view.err;
     p.D = a->channels;
-    p.cols = ceil_div(a->channels, wide_of(a->dtype));
     p.width = p.cols * wide_of(a->dtype);
     p.total = static_cast<uint32_t>(P->image.n_scan) * p.cols;
     return p;

@@ -249,6 +249,26 @@ def test_captured_and_on_another_stream():
     assert c.plan.device_error() == 0
 
 
+
+LONG = {
+    "chain": ([-1], [9001]),
+    "forks": ([-1, 0, 0, 1, 1, 4, -1, 6], [5000, 300, 2100, 2048, 4096, 129, 1, 8200]),
+    "short-segments": ([-1] + list(range(89)), [1 + (37 * i) % 200 for i in range(90)]),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("form,state", [("add", False), ("mix", True), ("add", True)])
+@pytest.mark.parametrize("D", [40, 264])
+@pytest.mark.parametrize("forest", sorted(LONG))
+def test_long_trajectories(forest, D, form, state, dtype):
+    c = Case(LONG[forest], D, dtype, form, state)
+    assert sum(c.len) >= 8192
+    h = c.check_forward()
+    c.check_backward(h)
+    assert torch.equal(h.view(torch.uint8), c.forward()[0].view(torch.uint8))
+
+
 def test_slow_decays_over_a_long_trajectory():
     """x = 1 and a decay per channel that stays: h_t = (1 - a^(t+1)) / (1 - a).  A row adds half a u for a
     (a rounded number below 1), one for the product of decays and as much for the sum, of which 1 in 16, 1 in

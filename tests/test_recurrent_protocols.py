@@ -114,6 +114,93 @@ def scan_block(sim, name, tiles, stages, own_map_last=False):
         sim.agent(g)
 
 
+
+def scan_block_ahead(sim, name, tiles, stages=3):
+    """One block of the kernel for long trajectories: a tile's map before the results of the one before
+    it, published by the warp that is last with its rows."""
+    b = lambda kind, i, count=1: sim.bar(f"{name}.{kind}{i}", count)
+    known, full, empty, maps, carry = ([b(k, i, c) for i in range(stages)] for k, c in (
+        ("known", 1), ("full", 1), ("empty", WARPS + 1), ("maps", WARPS), ("carry", 1)))
+    meta, mapped = {}, {}
+
+    def copy():
+        it, drawn = 0, sim.draw()
+        while True:
+            tile = tiles[drawn] if drawn < len(tiles) else None
+            if tile:
+                drawn = sim.draw()
+            s = it % stages
+            if it >= stages:
+                yield ("wait", empty[s], it // stages - 1)
+            meta[it] = tile
+            yield ("write", f"{name}.meta{s}", it)
+            yield ("arrive", known[s], it)
+            if tile is None:
+                yield ("arrive", full[s], it)
+                return
+            yield ("copy", full[s], it, f"{name}.rows{s}", it)
+            it += 1
+
+    def carries():
+        it = 0
+        while True:
+            s = it % stages
+            yield ("wait", known[s], it // stages)
+            yield ("read", f"{name}.meta{s}", it)
+            if meta[it] is None:
+                return
+            index, at, count, group, before = meta[it]
+            for k in range(at):
+                yield ("await", ("map", index - at + k))
+            if before is not None:
+                yield ("await", ("state", before))
+            yield ("write", f"{name}.carry{s}", it)
+            yield ("arrive", carry[s], it)
+            yield ("wait", maps[s], it // stages)
+            for w in range(WARPS):
+                yield ("read", f"{name}.map{s}.{w}", it)
+            if at == count - 1:
+                yield ("publish", ("state", group))
+            yield ("arrive", empty[s], it)
+            it += 1
+
+    def consumer(w):
+        def map_tile(it):
+            s = it % stages
+            yield ("wait", full[s], it // stages)
+            yield ("read", f"{name}.meta{s}", it)
+            if meta[it] is None:
+                return
+            yield ("read", f"{name}.rows{s}", it)
+            yield ("write", f"{name}.map{s}.{w}", it)
+            yield ("arrive", maps[s], it)
+            mapped[it] = mapped.get(it, 0) + 1
+            if mapped[it] == WARPS and meta[it][1] < meta[it][2] - 1:
+                for v in range(WARPS):
+                    yield ("read", f"{name}.map{s}.{v}", it)
+                yield ("publish", ("map", meta[it][0]))
+
+        def results(it):
+            s = it % stages
+            yield ("wait", maps[s], it // stages)
+            yield ("wait", carry[s], it // stages)
+            yield ("read", f"{name}.carry{s}", it)
+            for v in range(w):
+                yield ("read", f"{name}.map{s}.{v}", it)
+            yield ("read", f"{name}.rows{s}", it)
+            yield ("arrive", empty[s], it)
+
+        it = 0
+        yield from map_tile(0)
+        while meta[it] is not None:
+            yield from map_tile(it + 1)
+            yield from results(it)
+            it += 1
+
+    for g in [copy(), carries()] + [consumer(w) for w in range(WARPS)]:
+        sim.agent(g)
+
+
 def _chain(n, group, backwards_in_group=False):
     tiles = []
     for i in range(n):
@@ -143,6 +230,23 @@ def test_scan_blocks_wait_only_for_what_comes(n, group, blocks):
         for k in range(blocks):
             scan_block(sim, f"b{k}", _chain(n, group), 2 + seed % 2)
     assert _found(make) == []
+
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 4])
+@pytest.mark.parametrize("n,group", [(1, 4), (2, 1), (7, 3), (12, 4), (9, 1), (24, 8)])
+def test_scan_blocks_a_map_ahead(n, group, blocks):
+    def make(sim, seed):
+        for k in range(blocks):
+            scan_block_ahead(sim, f"b{k}", _chain(n, group))
+    assert _found(make) == []
+
+
+def test_scan_a_map_ahead_wants_a_stage_of_its_own():
+    """In one stage, the map would wait for the results before it, and they come after the map."""
+    def make(sim, seed):
+        scan_block_ahead(sim, "b", _chain(4, 2), stages=1)
+    assert all("deadlock" in m.lower() for m in _found(make, 5)) and len(_found(make, 5)) == 5
 
 
 def test_scan_rejects_a_group_dealt_out_backwards():
