@@ -12,11 +12,16 @@
 // Five streams forward and eight backward are read or written once each, with some 20 operations a
 // value: HBM bounds both.  (As separate steps the norm, the gate, the addition and the next norm
 // would move twelve.)  A row belongs to R threads, which keep it in registers over both of its
-// sums.  Rows of 1 KB and more are copied ahead by cp.async.bulk into a ring in shared memory,
-// whose bytes on their way do not depend on registers; shorter rows share a warp, and the next
-// ones are loaded into registers ahead.  Blocks are persistent: weights and the weights' gradients
-// of a thread's columns stay in its registers.  A block leaves one row of those gradients, a second
-// kernel adds them in ascending order: no atomics, the same bits on every run.
+// sums.  Rows are copied ahead by cp.async.bulk into a ring in shared memory, whose bytes on their way
+// do not depend on registers; short rows share a warp.  Blocks are persistent: weights and the weights'
+// gradients of a thread's columns stay in its registers.  A block leaves one row of those gradients, a
+// second kernel adds them in ascending order: no atomics, the same bits on every run.
+//
+// bf16, 65,536 rows of 2,048 channels with everything: forward 216 us (92 % of the copy's rate), backward 325 (97 %);
+// 1,048,560 heads of 128 with norm and gate 132 (90 %) and 212 (93 %); fp32, 32,768 x 2,048: 222 (89 %) and 349 (91 %).
+// Far from it are 8,192 channels backward (bf16 48 %, fp32 67 %: one stage of a 1,024-thread block is all
+// that shared memory holds beside the weights' sums) and bf16 rows that are not whole vectors, which
+// instructions bound (see RAGGED).  One row of 2,048: 2.2 us on the device.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -44,7 +49,7 @@ struct Fwd {
     void *h, *n;
     float *r1, *r2;
     int32_t *error;
-    int64_t C;
+    int64_t C, whole_end, whole_rows;   // values in whole vectors of a tensor, and the rows that end before that
     int32_t D, act;
     float scale, eps;
 };
@@ -55,21 +60,18 @@ struct Bwd {
     void *dy, *dgate, *dres;
     float *part;                    // [groups][2 D]: of w1, of w2
     int32_t *error;
-    int64_t C;
+    int64_t C, whole_end, whole_rows;
     int32_t D, act;
     float scale;
 };
 
-// A thread's values of one vector: pairs, or a single one.
+// A thread's values of one vector, in pairs.
 template <int VEC> struct Vals {
-    using E = typename std::conditional<VEC == 1, float, Two>::type;
-    static constexpr int n = VEC == 1 ? 1 : VEC / 2;
+    using E = Two;
+    static constexpr int n = VEC / 2;
     E e[n];
 };
-template <int VEC> __device__ __forceinline__ typename Vals<VEC>::E all(float c) {
-    if constexpr (VEC == 1) return c;
-    else return make_float2(c, c);
-}
+template <int VEC> __device__ __forceinline__ typename Vals<VEC>::E all(float c) { return make_float2(c, c); }
 template <typename T, int VEC> __device__ __forceinline__ void open(const Raw<T, VEC> &r, Vals<VEC> &v) {
     if constexpr (sizeof(T) == 2 && VEC == 8) {
         const uint32_t *u = &r.u.x;
@@ -79,8 +81,87 @@ template <typename T, int VEC> __device__ __forceinline__ void open(const Raw<T,
         unpack(r, reinterpret_cast<float *>(v.e));
     }
 }
-template <typename T, int VEC> __device__ __forceinline__ void put(void *p, int64_t i, const Vals<VEC> &v) {
-    st<T, VEC>(p, i, reinterpret_cast<const float *>(v.e));
+
+// Rows that are not whole vectors (RAGGED) begin anywhere: they are copied with what shares their first
+// and last 16 bytes, and a thread's "vector" is four words (one fp32 value or two of bf16) that lie R
+// words apart.  A bf16 row that begins in the middle of a word has a first one that is half its own, and any
+// row may have such a last one: the other half is taken as zero and not written.  (With everything,
+// forward and backward: bf16 65,536 x 2,001 275 and 580 us, 131,072 x 1,001 302 and 580, 250,000 x 500 289 and 615,
+// 1,000,000 x 131 479 and 903; fp32 32,768 x 2,001 231 and 358.  One value per thread at a time instead, straight from
+// memory: 485 and 922, 736 and 1,391, 1,179 and 2,269, 713 and 1,013, 254 and 496.  Whole vectors, what is not the row's
+// own masked out at the edges: 296 and 608, 365 and 567, 327 and 678, 773 and 1,400, 284 and 401.)
+template <typename T> constexpr int kWord = 4 / sizeof(T);                        // values of a word
+template <typename T, int VEC, int R, bool RAGGED> __device__ __forceinline__ int32_t col_of(int j, int t, int into) {
+    return RAGGED ? j * VEC * R + t * kWord<T> - into : (j * R + t) * VEC;
+}
+template <typename T, int R, bool RAGGED> __device__ __forceinline__ int32_t value_of(int i) {   // a vector's i-th value, behind its first
+    return RAGGED ? i / kWord<T> * R * kWord<T> + i % kWord<T> : i;
+}
+// Pairs of a vector that any of the R threads has something in; shape_of gives a row as few threads and
+// values as it takes, so that a thread's first half is always its own (SURE).
+template <typename T, int VEC, int R> __device__ __forceinline__ int pairs_of(int j, int32_t D) {
+    return min(max((D + kWord<T> - 1 - j * VEC * R + 2 * R - 1) / (2 * R), 0), VEC / 2);
+}
+template <int VEC, int R, int NV, bool RAGGED> __device__ __forceinline__ constexpr bool sure(int j, int i) {
+    return !RAGGED || (R > 8 && (j * VEC + 2 * i + 2) * 2 <= NV * VEC);
+}
+// at: the place of the row's first value; pairs: those of the vector
+template <typename T, int VEC, int R, int NV, bool RAGGED> __device__ __forceinline__ void put(void *p, int64_t at, int j, int32_t col, int32_t D, int pairs, const Vals<VEC> &v) {
+    if constexpr (RAGGED) {
+        Raw<T, VEC> r;
+        pack(r, reinterpret_cast<const float *>(v.e));
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(&r.u);
+        uint32_t *words = reinterpret_cast<uint32_t *>(static_cast<T *>(p) + at + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = k * kWord<T> / 2;
+            if (!sure<VEC, R, NV, true>(j, i) && i >= pairs) break;
+            const int32_t c = col + k * R * kWord<T>;
+            if constexpr (sizeof(T) == 4) {
+                if (sure<VEC, R, NV, true>(j, i) || c < D) words[k * R] = u[k];
+            } else {
+                const bool first = j == 0 && k == 0 && c < 0;
+                if (!first && (sure<VEC, R, NV, true>(j, i) || c + 1 < D)) words[k * R] = u[k];
+                if (j == 0 && k == 0 && first) reinterpret_cast<uint16_t *>(words)[1] = static_cast<uint16_t>(u[k] >> 16);
+                if (!sure<VEC, R, NV, true>(j, i) && !first && c + 1 == D) reinterpret_cast<uint16_t *>(words)[2 * k * R] = static_cast<uint16_t>(u[k]);
+            }
+        }
+    } else {
+        st<T, VEC>(p, at + col, reinterpret_cast<const float *>(v.e));
+    }
+}
+// Of a tensor whose size is not a whole vector, the last values are not among what was copied: `in`, from memory.
+template <typename T, int VEC, int R, int NV, bool RAGGED> __device__ __forceinline__ Raw<T, VEC> take(const T *buf, const T *in, bool last, int j, int32_t col, int32_t D, int pairs) {
+    if constexpr (RAGGED) {
+        Raw<T, VEC> r;
+        uint32_t *u = reinterpret_cast<uint32_t *>(&r.u);
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(buf + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = k * kWord<T> / 2;
+            const int32_t c = col + k * R * kWord<T>;
+            if (sure<VEC, R, NV, true>(j, i)) {
+                u[k] = words[k * R];
+            } else {
+                if (i >= pairs) break;
+                if (c < D) u[k] = words[k * R];
+                if (sizeof(T) == 2 && c + 1 >= D) u[k] &= 0xffffu;
+            }
+        }
+        if (sizeof(T) == 2 && j == 0 && col < 0) u[0] &= 0xffff0000u;
+        if (last) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int32_t c = col + value_of<T, R, true>(i);
+                if (c >= 0 && c < D && c > D - VEC) reinterpret_cast<T *>(u)[i] = in[c];
+            }
+        }
+        return r;
+    } else {
+        return ld<T, VEC>(buf, col);
+    }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -114,20 +195,22 @@ template <typename T, typename E> __device__ __forceinline__ E sigmoid(E z, E &o
     }
 }
 // A gate's value, and its slope.
-template <typename T, int VEC> __device__ __forceinline__ void open_gate(Vals<VEC> &z, int act) {
+template <typename T, int VEC, int R, int NV, bool RAGGED> __device__ __forceinline__ void open_gate(Vals<VEC> &z, int act, int j, int pairs) {
     if (act == HARTS_GATE_LINEAR) return;
     const bool silu = act == HARTS_GATE_SILU;
 #pragma unroll
     for (int i = 0; i < Vals<VEC>::n; ++i) {
+        if (!sure<VEC, R, NV, RAGGED>(j, i) && i >= pairs) break;
         typename Vals<VEC>::E rest;
         const auto q = sigmoid<T>(z.e[i], rest);
         z.e[i] = silu ? mul(z.e[i], q) : q;
     }
 }
-template <typename T, int VEC> __device__ __forceinline__ void open_gate(Vals<VEC> &z, Vals<VEC> &slope, int act) {
+template <typename T, int VEC, int R, int NV, bool RAGGED> __device__ __forceinline__ void open_gate(Vals<VEC> &z, Vals<VEC> &slope, int act, int j, int pairs) {
     const bool silu = act == HARTS_GATE_SILU;
 #pragma unroll
     for (int i = 0; i < Vals<VEC>::n; ++i) {
+        if (!sure<VEC, R, NV, RAGGED>(j, i) && i >= pairs) break;
         typename Vals<VEC>::E rest;
         const auto q = sigmoid<T>(z.e[i], rest);
         slope.e[i] = mul(q, silu ? fma(z.e[i], rest, all<VEC>(1.f)) : rest);
@@ -138,24 +221,38 @@ template <typename T, int VEC> __device__ __forceinline__ void open_gate(Vals<VE
 // The R threads of a row, or the warp that several rows share, are a team: it takes its rows, or
 // twice as many where they are short, at a time, which lie one behind another in memory, and has them copied ahead into a ring of
 // its own, without a look at other teams.
-template <int R, int VALUES> struct Team {
+template <int R, int VALUES, bool RAGGED> struct Team {
     static constexpr int threads = R < 32 ? 32 : R, side = threads / R;        // rows side by side
-    static constexpr int batch = R <= 32 && VALUES <= 8 ? 2 : 1, rows = side * batch, count = block_of(R) / threads;
+    static constexpr int batch = R <= (RAGGED ? 16 : 32) && VALUES <= 8 ? 2 : 1, rows = side * batch, count = block_of(R) / threads;
 };
+
+// Bytes of a team's rows of one tensor in a stage.
+template <typename T, bool RAGGED> __host__ __device__ __forceinline__ uint32_t room_of(int rows, int32_t D) {
+    return RAGGED ? (static_cast<uint32_t>(rows) * D * sizeof(T) + 30) / 16 * 16 : static_cast<uint32_t>(rows) * D * sizeof(T);
+}
 
 // The N tensors' rows on their way, one tensor behind another.  The team's first thread fetches; a
 // wait that runs out is reported once and never waited for again, and the block goes on with what
 // its shared memory holds, so that its barriers stay matched.
-template <typename T, int N, bool ONCE> struct Ahead {
+template <typename T, int N, bool ONCE, bool RAGGED> struct Ahead {
     uint8_t *mem;
     uint64_t *full;
     int *fail;
     uint32_t tensor, stage;         // bytes of a stage and of one tensor in it
     int stages, s;
     uint32_t phase;
-    __device__ __forceinline__ void fetch(const void *const (&in)[N], int64_t row, int rows, int64_t C, int32_t D, int slot) {
+    // rows from `row` on, whose first value is `first`
+    __device__ __forceinline__ void fetch(const void *const (&in)[N], int64_t row, int64_t first, int rows, int64_t C, int64_t whole_end, int32_t D, int slot) {
         if (row >= C) return;
-        const uint32_t bytes = static_cast<uint32_t>(C - row < rows ? C - row : rows) * D * sizeof(T);
+        const uint32_t values = static_cast<uint32_t>(C - row < rows ? C - row : rows) * D;
+        uint32_t bytes = values * sizeof(T);
+        if (RAGGED) {                                           // from the vector that the first row begins in to the end of the last one's
+            constexpr int64_t kMask = 16 / sizeof(T) - 1;
+            const int64_t end = min((first + values + kMask) & ~kMask, whole_end);
+            first &= ~kMask;
+            bytes = static_cast<uint32_t>(end - first) * sizeof(T);
+            if (bytes == 0) { tc::mbar_expect_tx(&full[slot], 0); return; }
+        }
         uint8_t *dst = mem + slot * stage;
         uint32_t total = 0;
 #pragma unroll
@@ -164,8 +261,8 @@ template <typename T, int N, bool ONCE> struct Ahead {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (!in[i]) continue;
-            if (ONCE) bulk_load_once(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
-            else bulk_load(dst, static_cast<const T *>(in[i]) + row * D, bytes, &full[slot]);
+            if (ONCE) bulk_load_once(dst, static_cast<const T *>(in[i]) + first, bytes, &full[slot]);
+            else bulk_load(dst, static_cast<const T *>(in[i]) + first, bytes, &full[slot]);
             dst += tensor;
         }
     }
@@ -185,16 +282,28 @@ template <typename T, int N, bool ONCE> struct Ahead {
 
 // Weights of a thread's columns: in its registers, from shared memory, or from where they are.
 enum Place { kRegs, kShared, kMemory };
-template <int NV, int VEC, int PLACE> struct Weights {
+template <typename T, int NV, int VEC, int R, int PLACE, bool RAGGED> struct Weights {
     Vals<VEC> kept[PLACE == kRegs ? NV : 1];
     const float *from;
-    __device__ __forceinline__ void take(const float *w, float *sh, int R, int t, int32_t D) {
+    int32_t width;
+    __device__ __forceinline__ void one(const float *w, int32_t col, Vals<VEC> &v) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int32_t c = col + value_of<T, R, true>(i);
+            reinterpret_cast<float *>(v.e)[i] = c >= 0 && c < width ? __ldg(w + c) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void take(const float *w, float *sh, int t, int into, int32_t D) {
+        width = D;
         from = PLACE == kShared ? sh : w;
         if (!w) return;
         if constexpr (PLACE == kRegs) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if ((j * R + t) * VEC < D) ld_w<VEC>(w, (j * R + t) * VEC, *reinterpret_cast<float (*)[VEC]>(kept[j].e));
+            for (int j = 0; j < NV; ++j) {
+                const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
+                if (RAGGED) one(w, col, kept[j]);
+                else if (col < D) ld_w<VEC>(w, col, *reinterpret_cast<float (*)[VEC]>(kept[j].e));
+            }
         } else if constexpr (PLACE == kShared) {
             for (int32_t c = threadIdx.x; c < D; c += blockDim.x) sh[c] = w[c];
         }
@@ -202,6 +311,7 @@ template <int NV, int VEC, int PLACE> struct Weights {
     __device__ __forceinline__ Vals<VEC> get(int j, int32_t col) const {
         Vals<VEC> v;
         if constexpr (PLACE == kRegs) v = kept[j];
+        else if constexpr (RAGGED) one(from, col, v);
         else
 #pragma unroll
         for (int i = 0; i < Vals<VEC>::n; i += 2)            // vectors hold four values, or eight
@@ -211,22 +321,20 @@ template <int NV, int VEC, int PLACE> struct Weights {
 };
 
 // Blocks of an SM that registers are shared out for: by the values that a thread keeps.
-constexpr int fwd_blocks(int R, int values, bool ring) { return ring ? std::max(1, (values <= 8 ? 768 : 512) / block_of(R)) : 1; }
-constexpr int bwd_blocks(int R, bool ring) { return ring ? std::max(1, 512 / block_of(R)) : 1; }
+constexpr int fwd_blocks(int R, int values) { return std::max(1, (values <= 8 ? 768 : 512) / block_of(R)); }
+constexpr int bwd_blocks(int R) { return std::max(1, 512 / block_of(R)); }
 
 // What there is beside y: known where it is what surrounds a block, with a gate or without, or a
 // head's gated norm, and looked up otherwise.
 enum Kind { kAny, kBlock, kHead, kUngated };
 
-// RING: rows come through shared memory; otherwise (rows that are not whole vectors) the next one
-// is loaded into registers ahead.
-template <typename T, int VEC, int R, int NV, bool RING, int PLACE, int KIND>
-__global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) block_norm_fwd_kernel(const Fwd p, int stages) {
-    using M = Team<R, NV * VEC>;
-    constexpr int kBatch = RING ? M::batch : 1, kTeamRows = M::side * kBatch;
+template <typename T, int VEC, int R, int NV, int PLACE, int KIND, bool RAGGED>
+__global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC)) block_norm_fwd_kernel(const Fwd p, int stages) {
+    using M = Team<R, NV * VEC, RAGGED>;
+    constexpr int kBatch = M::batch, kTeamRows = M::side * kBatch;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float sm[2][2][rows_of(R)][R < 32 ? 1 : R / 32];
-    __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
+    __shared__ uint64_t full[M::count][kMaxStages];
     __shared__ int s_fail;
     constexpr bool block = KIND == kBlock || KIND == kUngated;
     const bool post = KIND != kAny || p.w1, gated = KIND == kBlock || KIND == kHead || (KIND == kAny && p.in[1]);
@@ -236,65 +344,56 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
     const int32_t D = p.D;
     const int64_t step = static_cast<int64_t>(gridDim.x) * M::count * kTeamRows;
     int64_t row0 = (static_cast<int64_t>(blockIdx.x) * M::count + team) * kTeamRows;
+    int64_t first = row0 * D;                                   // of row0's values
+    const int64_t stride = step * D;
     const float inv_d = 1.f / static_cast<float>(D);
     Raw<T, VEC> a[3][NV];
-    [[maybe_unused]] Ahead<T, 3, (R > 32)> ahead;
+    [[maybe_unused]] Ahead<T, 3, (R > 32), RAGGED> ahead;
     float *sh = reinterpret_cast<float *>(ring);
-    Weights<NV, VEC, PLACE> w1, w2;
-    w1.take(p.w1, sh, R, t, D);
-    w2.take(p.w2, sh + D, R, t, D);
-    auto load = [&](int64_t r) {                                // without a ring: a row's values into registers
+    int pairs[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col < D && r < p.C) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) if (there(i)) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
-            }
-        }
-    };
-    if constexpr (RING) {
-        ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
-        ahead.stage = ahead.tensor * (1 + gated + added);
-        ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
-        ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
-        if (threadIdx.x == 0) s_fail = 0;
-        if (tt == 0) {
-            for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
-            tc::fence_mbar_init();
-            for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, kTeamRows, p.C, D, s);
-        }
-    } else {
-        load(row0 + tt / R);
+    for (int j = 0; j < NV; ++j) pairs[j] = RAGGED ? pairs_of<T, VEC, R>(j, D) : VEC / 2;
+    // values by which the thread's rows begin into a word: the same for all, they are an even number apart
+    const int into = RAGGED ? static_cast<int>(row0 + tt / R) & D & (kWord<T> - 1) : 0;
+    Weights<T, NV, VEC, R, PLACE, RAGGED> w1, w2;
+    w1.take(p.w1, sh, t, into, D);
+    w2.take(p.w2, sh + D, t, into, D);
+    ahead.tensor = room_of<T, RAGGED>(kTeamRows, D);
+    ahead.stage = ahead.tensor * (1 + gated + added);
+    ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+    ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
+    if (threadIdx.x == 0) s_fail = 0;
+    if (tt == 0) {
+        for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
+        tc::fence_mbar_init();
+        for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, first + s * stride, kTeamRows, p.C, p.whole_end, D, s);
     }
     __syncthreads();
-    for (int slot = 0; row0 < p.C; row0 += step) {
-        if constexpr (RING) ahead.wait(p.error);
+    for (int slot = 0; row0 < p.C; row0 += step, first += stride) {
+        ahead.wait(p.error);
 #pragma unroll 1
         for (int batch = 0; batch < kBatch; ++batch, slot ^= 1) {
             const int in_stage = batch * M::side + tt / R;
             const int64_t row = row0 + in_stage;
             const bool on = row < p.C;
-            if constexpr (RING) {
-                const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D;
+            const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D + (RAGGED ? static_cast<int>(first) & (VEC - 1) : 0);
+            const int64_t at = first + in_stage * D;
+            const bool last = RAGGED && on && row >= p.whole_rows;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    if (!there(i)) continue;
+            for (int i = 0; i < 3; ++i) {
+                if (!there(i)) continue;
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        const int32_t col = (j * R + t) * VEC;
-                        if (col < D) a[i][j] = ld<T, VEC>(buf, col);
-                    }
-                    buf += ahead.tensor / sizeof(T);
+                for (int j = 0; j < NV; ++j) {
+                    const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
+                    if (col < D) a[i][j] = take<T, VEC, R, NV, RAGGED>(buf, static_cast<const T *>(p.in[i]) + at, last, j, col, D, pairs[j]);
                 }
+                buf += ahead.tensor / sizeof(T);
             }
             // behind a sum's barrier, or the warp's own, the stage is free
             auto free_stage = [&] {
-                if constexpr (RING) {
-                    if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, kTeamRows, p.C, D, ahead.s);
-                }
+                if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, first + stages * stride, kTeamRows, p.C, p.whole_end, D, ahead.s);
             };
-            if constexpr (RING && R <= 32) {
+            if constexpr (R <= 32) {
                 __syncwarp();
                 free_stage();
             }
@@ -304,7 +403,7 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 res[j] = a[2][j];
-                if ((j * R + t) * VEC >= D) continue;
+                if (col_of<T, VEC, R, RAGGED>(j, t, into) >= D) continue;
                 open(a[0][j], v[j]);
                 if (post) {
 #pragma unroll
@@ -312,21 +411,20 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
                 }
                 if (gated) {
                     open(a[1][j], g[j]);
-                    open_gate<T, VEC>(g[j], p.act);
+                    open_gate<T, VEC, R, NV, RAGGED>(g[j], p.act, j, pairs[j]);
                 }
             }
             float factor = p.scale;
             if (post) {
                 const float r1 = __frsqrt_rn(fmaf(row_sum<R>(total(s), sm[slot][0][sub]), inv_d, p.eps));
                 factor *= r1;
-                if constexpr (!RING) load(row + step);
-                else if constexpr (R > 32) free_stage();
+                if constexpr (R > 32) free_stage();
                 if (t == 0 && p.r1 && on) p.r1[row] = r1;
             }
             s = all<VEC>(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int32_t col = (j * R + t) * VEC;
+                const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
                 if (col >= D) continue;
                 if (post) {
                     const Vals<VEC> w = w1.get(j, col);
@@ -350,39 +448,38 @@ __global__ void __launch_bounds__(block_of(R), fwd_blocks(R, NV * VEC, RING)) bl
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) s = fma(v[j].e[i], v[j].e[i], s);
                 }
-                if (on) put<T, VEC>(p.h, row * D + col, v[j]);
+                if (on) put<T, VEC, R, NV, RAGGED>(p.h, at, j, col, D, pairs[j], v[j]);
             }
             if (pre) {
                 const float r2 = __frsqrt_rn(fmaf(row_sum<R>(total(s), sm[slot][1][sub]), inv_d, p.eps));
                 if (!post) {
-                    if constexpr (!RING) load(row + step);
-                    else if constexpr (R > 32) free_stage();
+                    if constexpr (R > 32) free_stage();
                 }
                 if (t == 0 && p.r2 && on) p.r2[row] = r2;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const int32_t col = (j * R + t) * VEC;
+                    const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
                     if (col >= D) continue;
                     const Vals<VEC> w = w2.get(j, col);
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) v[j].e[i] = mul(mul(v[j].e[i], all<VEC>(r2)), w.e[i]);
-                    if (on) put<T, VEC>(p.n, row * D + col, v[j]);
+                    if (on) put<T, VEC, R, NV, RAGGED>(p.n, at, j, col, D, pairs[j], v[j]);
                 }
             }
         }
-        if constexpr (RING) ahead.next();
+        ahead.next();
     }
-    if constexpr (RING) if (tt == 0) ahead.drain();
+    if (tt == 0) ahead.drain();
 }
 
-template <typename T, int VEC, int R, int NV, bool RING, int PLACE, int KIND>
-__global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_bwd_kernel(const Bwd p, int stages) {
-    using M = Team<R, NV * VEC>;
+template <typename T, int VEC, int R, int NV, int PLACE, int KIND, bool RAGGED>
+__global__ void __launch_bounds__(block_of(R), bwd_blocks(R)) block_norm_bwd_kernel(const Bwd p, int stages) {
+    using M = Team<R, NV * VEC, RAGGED>;
     constexpr int kRows = rows_of(R);
-    constexpr int kBatch = RING ? M::batch : 1, kTeamRows = M::side * kBatch;
+    constexpr int kBatch = M::batch, kTeamRows = M::side * kBatch;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float sm[2][2][kRows][R < 32 ? 1 : R / 32];
-    __shared__ uint64_t full[RING ? M::count : 1][RING ? kMaxStages : 1];
+    __shared__ uint64_t full[M::count][kMaxStages];
     __shared__ int s_fail;
     constexpr bool block = KIND == kBlock || KIND == kUngated;
     const bool post = KIND != kAny || p.w1, gated = KIND == kBlock || KIND == kHead || (KIND == kAny && p.in[1]);
@@ -392,14 +489,21 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
     const int32_t D = p.D;
     const int64_t step = static_cast<int64_t>(gridDim.x) * M::count * kTeamRows;
     int64_t row0 = (static_cast<int64_t>(blockIdx.x) * M::count + team) * kTeamRows;
+    int64_t first = row0 * D;                                   // of row0's values
+    const int64_t stride = step * D;
     const float inv_d = 1.f / static_cast<float>(D);
     let_next_start();
     Raw<T, VEC> a[5][NV];
-    [[maybe_unused]] Ahead<T, 5, false> ahead;
+    [[maybe_unused]] Ahead<T, 5, false, RAGGED> ahead;
     float *sh = reinterpret_cast<float *>(ring);
-    Weights<NV, VEC, PLACE> w1, w2;
-    w1.take(p.w1, sh, R, t, D);
-    w2.take(p.w2, sh + D, R, t, D);
+    int pairs[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) pairs[j] = RAGGED ? pairs_of<T, VEC, R>(j, D) : VEC / 2;
+    // values by which the thread's rows begin into a word: the same for all, they are an even number apart
+    const int into = RAGGED ? static_cast<int>(row0 + tt / R) & D & (kWord<T> - 1) : 0;
+    Weights<T, NV, VEC, R, PLACE, RAGGED> w1, w2;
+    w1.take(p.w1, sh, t, into, D);
+    w2.take(p.w2, sh + D, t, into, D);
     // the weights' gradients of a thread's columns: registers, but shared memory where 64 of them
     // are all that a thread has (then the weights stay where they are)
     constexpr bool kSums = PLACE == kMemory;
@@ -413,22 +517,21 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
         for (int32_t c = threadIdx.x; c < 2 * D; c += blockDim.x) sh[c] = 0.f;
     auto add_dw = [&](Vals<VEC> *dw, int which, int j, int32_t col, const Vals<VEC> &a, const Vals<VEC> &b) {
         if constexpr (kSums) {
-            auto *at = reinterpret_cast<typename Vals<VEC>::E *>(sh + which * D + col);
+            float *at = sh + which * D + col;
 #pragma unroll
-            for (int i = 0; i < Vals<VEC>::n; ++i) at[i] = fma(a.e[i], b.e[i], at[i]);
+            for (int i = 0; i < Vals<VEC>::n; ++i) {
+                if constexpr (RAGGED) {
+                    const int32_t c = value_of<T, R, true>(2 * i), d = value_of<T, R, true>(2 * i + 1);
+                    if (col + c >= 0 && col + c < D) at[c] = fmaf(a.e[i].x, b.e[i].x, at[c]);
+                    if (col + d < D) at[d] = fmaf(a.e[i].y, b.e[i].y, at[d]);
+                } else {
+                    Two *pair = reinterpret_cast<Two *>(at) + i;
+                    *pair = fma(a.e[i], b.e[i], *pair);
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < Vals<VEC>::n; ++i) dw[j].e[i] = fma(a.e[i], b.e[i], dw[j].e[i]);
-        }
-    };
-    auto load = [&](int64_t r) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
-            if (col < D && r < p.C) {
-#pragma unroll
-                for (int i = 0; i < 5; ++i) if (there(i)) a[i][j] = ld<T, VEC>(p.in[i], r * D + col);
-            }
         }
     };
     float next1 = 0.f, next2 = 0.f;
@@ -437,24 +540,20 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
         if (post) next1 = __ldg(p.r1 + r);
         if (pre) next2 = __ldg(p.r2 + r);
     };
-    if constexpr (RING) {
-        ahead.tensor = static_cast<uint32_t>(kTeamRows) * D * sizeof(T);
-        ahead.stage = ahead.tensor * (1 + gated + 2 * pre + along);
-        ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
-        ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
-        if (threadIdx.x == 0) s_fail = 0;
-        if (tt == 0) {
-            for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
-            tc::fence_mbar_init();
-            for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, kTeamRows, p.C, D, s);
-        }
-    } else {
-        load(row0 + tt / R);
+    ahead.tensor = room_of<T, RAGGED>(kTeamRows, D);
+    ahead.stage = ahead.tensor * (1 + gated + 2 * pre + along);
+    ahead.mem = ring + (PLACE == kRegs ? 0 : (2 * D * sizeof(float) + 127) / 128 * 128) + static_cast<size_t>(team) * stages * ahead.stage;
+    ahead.full = full[team]; ahead.fail = &s_fail; ahead.stages = stages; ahead.s = 0; ahead.phase = 0;
+    if (threadIdx.x == 0) s_fail = 0;
+    if (tt == 0) {
+        for (int s = 0; s < stages; ++s) tc::mbar_init(&ahead.full[s], 1);
+        tc::fence_mbar_init();
+        for (int s = 0; s < stages; ++s) ahead.fetch(p.in, row0 + s * step, first + s * stride, kTeamRows, p.C, p.whole_end, D, s);
     }
     load_roots(row0 + tt / R);
     __syncthreads();
-    for (int slot = 0; row0 < p.C; row0 += step) {
-        if constexpr (RING) ahead.wait(p.error);
+    for (int slot = 0; row0 < p.C; row0 += step, first += stride) {
+        ahead.wait(p.error);
 #pragma unroll 1
         for (int batch = 0; batch < kBatch; ++batch, slot ^= 1) {
             const int in_stage = batch * M::side + tt / R;
@@ -462,25 +561,23 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             const bool on = row < p.C;
             const float r1 = next1, r2 = next2;
             load_roots(batch < kBatch - 1 ? row + M::side : row0 + step + tt / R);
-            if constexpr (RING) {
-                const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D;
+            const T *buf = reinterpret_cast<const T *>(ring + (ahead.mem - ring) + ahead.s * ahead.stage) + in_stage * D + (RAGGED ? static_cast<int>(first) & (VEC - 1) : 0);
+            const int64_t at = first + in_stage * D;
+            const bool last = RAGGED && on && row >= p.whole_rows;
 #pragma unroll
-                for (int i = 0; i < 5; ++i) {
-                    if (!there(i)) continue;
+            for (int i = 0; i < 5; ++i) {
+                if (!there(i)) continue;
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        const int32_t col = (j * R + t) * VEC;
-                        if (col < D) a[i][j] = ld<T, VEC>(buf, col);
-                    }
-                    buf += ahead.tensor / sizeof(T);
+                for (int j = 0; j < NV; ++j) {
+                    const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
+                    if (col < D) a[i][j] = take<T, VEC, R, NV, RAGGED>(buf, static_cast<const T *>(p.in[i]) + at, last, j, col, D, pairs[j]);
                 }
+                buf += ahead.tensor / sizeof(T);
             }
             auto free_stage = [&] {
-                if constexpr (RING) {
-                    if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, kTeamRows, p.C, D, ahead.s);
-                }
+                if (tt == 0 && batch == kBatch - 1) ahead.fetch(p.in, row0 + stages * step, first + stages * stride, kTeamRows, p.C, p.whole_end, D, ahead.s);
             };
-            if constexpr (RING && R <= 32) {
+            if constexpr (R <= 32) {
                 __syncwarp();
                 free_stage();
                 if (!on) continue;                              // rows of a warp do not wait for each other from here on
@@ -492,7 +589,7 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             for (int j = 0; j < NV; ++j) {
                 y[j] = a[0][j];
                 g[j] = a[1][j];
-                const int32_t col = (j * R + t) * VEC;
+                const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
                 if (col >= D) continue;
                 if (along) {
                     open(a[4][j], d[j]);
@@ -516,8 +613,7 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             }
             if (pre) {
                 const float m = row_sum<R>(total(s), sm[slot][0][sub]) * inv_d * -r2;
-                if constexpr (!RING) load(row + step);
-                else if constexpr (R > 32) free_stage();
+                if constexpr (R > 32) free_stage();
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -528,9 +624,9 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             s = all<VEC>(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int32_t col = (j * R + t) * VEC;
+                const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
                 if (col >= D) continue;
-                if (p.dres && on) put<T, VEC>(p.dres, row * D + col, d[j]);
+                if (p.dres && on) put<T, VEC, R, NV, RAGGED>(p.dres, at, j, col, D, pairs[j], d[j]);
                 Vals<VEC> w;
                 if (post) w = w1.get(j, col);
                 open(y[j], n[j]);
@@ -549,13 +645,13 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
                     }
                     if (p.act != HARTS_GATE_LINEAR) {
                         Vals<VEC> slope;
-                        open_gate<T, VEC>(z, slope, p.act);
+                        open_gate<T, VEC, R, NV, RAGGED>(z, slope, p.act, j, pairs[j]);
 #pragma unroll
                         for (int i = 0; i < Vals<VEC>::n; ++i) out.e[i] = mul(out.e[i], slope.e[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = mul(d[j].e[i], z.e[i]);
-                    if (p.dgate && on) put<T, VEC>(p.dgate, row * D + col, out);
+                    if (p.dgate && on) put<T, VEC, R, NV, RAGGED>(p.dgate, at, j, col, D, pairs[j], out);
                 }
                 if (post) {
                     add_dw(dw1, 0, j, col, d[j], n[j]);
@@ -570,24 +666,23 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
             if (post) {
                 m = -row_sum<R>(total(s), sm[slot][1][sub]) * inv_d;
                 if (!pre) {
-                    if constexpr (!RING) load(row + step);
-                    else if constexpr (R > 32) free_stage();
+                    if constexpr (R > 32) free_stage();
                 }
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int32_t col = (j * R + t) * VEC;
+                const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
                 if (col >= D) continue;
                 if (post) {
 #pragma unroll
                     for (int i = 0; i < Vals<VEC>::n; ++i) d[j].e[i] = mul(all<VEC>(r1), fma(n[j].e[i], all<VEC>(m), d[j].e[i]));
                 }
-                if (on) put<T, VEC>(p.dy, row * D + col, d[j]);
+                if (on) put<T, VEC, R, NV, RAGGED>(p.dy, at, j, col, D, pairs[j], d[j]);
             }
         }
-        if constexpr (RING) ahead.next();
+        ahead.next();
     }
-    if constexpr (RING) if (tt == 0) ahead.drain();
+    if (tt == 0) ahead.drain();
     // the rows of a block leave one sum of either weight, added in ascending order
     __shared__ float all[kRows > 1 ? kRows : 1][kRows > 1 ? R * NV * VEC : 1];
     for (int which = 0; which < 2; ++which) {
@@ -596,13 +691,15 @@ __global__ void __launch_bounds__(block_of(R), bwd_blocks(R, RING)) block_norm_b
         if constexpr (kRows > 1) __syncthreads();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int32_t col = (j * R + t) * VEC;
+            const int32_t col = col_of<T, VEC, R, RAGGED>(j, t, into);
             if (col >= D) continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float v = kSums ? sh[which * D + col + i] : reinterpret_cast<const float *>(which ? dw2[kSums ? 0 : j].e : dw1[kSums ? 0 : j].e)[i];
-                if constexpr (kRows > 1) all[sub][col + i] = v;
-                else part[col + i] = v;
+                const int32_t at = col + value_of<T, R, RAGGED>(i);
+                if (RAGGED && (at < 0 || at >= D)) continue;
+                const float v = kSums ? sh[which * D + at] : reinterpret_cast<const float *>(which ? dw2[kSums ? 0 : j].e : dw1[kSums ? 0 : j].e)[i];
+                if constexpr (kRows > 1) all[sub][at] = v;
+                else part[at] = v;
             }
         }
         if constexpr (kRows > 1) {
@@ -641,20 +738,22 @@ __global__ void __launch_bounds__(1024) block_norm_dw_kernel(const Dw p) {
     }
 }
 
-// Threads of a row and values that each of them keeps.  Rows that are not whole vectors move single
-// values.
-struct Shape { int vec, r, values; };
+// Threads of a row and values that each of them keeps.
+struct Shape { int vec, r, values; bool ragged; };
 Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     const int full = dtype == HARTS_BF16 ? 8 : 4;
-    Shape s{D % full == 0 ? full : 1, 8, 8};
-    if (s.vec == 1) {
-        s.r = D <= 256 ? 32 : D <= 2048 ? 256 : 1024;
-        return s;
-    }
+    Shape s{full, 8, 8, D % full != 0};
+    if (s.ragged && full == 8) ++D;                      // a row's words, where it begins in the middle of one
     while (s.r < 16 && s.r * 8 < D) s.r *= 2;
     if (s.r * 8 < D && !backward) s.values = 16;
     while (s.r * s.values < D) s.r *= 2;
     return s;
+}
+
+template <typename P> void set_whole(P &p, int32_t dtype) {
+    const int vec = dtype == HARTS_BF16 ? 8 : 4;
+    p.whole_end = p.C * p.D / vec * vec;
+    p.whole_rows = p.whole_end / p.D;
 }
 
 // Most blocks that are resident at a time, whatever the kernel's registers.
@@ -664,44 +763,41 @@ int64_t blocks_of(const Shape &s, int64_t C) {
 
 // Resident blocks of a persistent kernel, and the rows that each of them has on its way: `budget`
 // bytes an SM.
-template <typename T, int R, int VT, bool RING, int PLACE, typename K, typename P>
+template <typename T, int R, int VT, int PLACE, bool RAGGED, typename K, typename P>
 cudaError_t launch_rows(K *kernel, const P &p, int tensors, size_t most, std::atomic<uint64_t> &allowed, std::atomic<int> &regs_fit, int64_t *groups, cudaStream_t st) {
     constexpr size_t kSmem = size_t(200) * 1024;
-    using M = Team<R, VT>;
+    using M = Team<R, VT, RAGGED>;
     int stages = 1, n = regs_fit.load(std::memory_order_relaxed);
     if (n == 0) {                                        // blocks that registers leave room for
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block_of(R), 0) != cudaSuccess || n < 1) n = 1;
         regs_fit.store(n, std::memory_order_relaxed);
     }
     size_t smem = 0;
-    if (RING) {
-        const size_t weights = PLACE == kRegs ? 0 : (2 * size_t(p.D) * sizeof(float) + 127) / 128 * 128;
-        const size_t stage = size_t(p.D) * sizeof(T) * tensors * M::rows * M::count;
-        while (n > 1 && n * (weights + 2 * stage) > kSmem) --n;
-        stages = static_cast<int>(std::min<size_t>(most, std::max<size_t>(1, (kSmem / n - std::min(weights, kSmem / n)) / stage)));
-        smem = weights + stages * stage;
-        const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and weights: 224 KB
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t rows = rows_of(R), grid = std::min<int64_t>((p.C + rows - 1) / rows, int64_t(sm_count()) * n);
+    const size_t weights = PLACE == kRegs ? 0 : (2 * size_t(p.D) * sizeof(float) + 127) / 128 * 128;
+    const size_t stage = size_t(room_of<T, RAGGED>(M::rows, p.D)) * tensors * M::count;
+    while (n > 1 && n * (weights + 2 * stage) > kSmem) --n;
+    stages = static_cast<int>(std::min<size_t>(most, std::max<size_t>(1, (kSmem / n - std::min(weights, kSmem / n)) / stage)));
+    smem = weights + stages * stage;
+    const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and weights: 224 KB
+    if (e != cudaSuccess) return e;
+    // an even number of blocks, so that a thread's rows are an even number apart
+    const int64_t rows = rows_of(R), grid = std::min<int64_t>((p.C + rows - 1) / rows, std::max(int64_t(sm_count()) * n / 2 * 2, int64_t(1)));
     *groups = grid;
     return launch(kernel, grid, block_of(R), smem, 1, false, st, p, stages);
 }
 
-template <typename T, int VEC, int R, int VT, int KIND>
+template <typename T, int VEC, int R, int VT, int KIND, bool RAGGED>
 cudaError_t launch_kind(const Fwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     static std::atomic<int> fit{0};
-    constexpr bool ring = VEC > 1;
-    return launch_rows<T, R, VT, ring, kRegs>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, ring, kRegs, KIND>, p, tensors, R <= 32 && VT > 8 ? 1 : kMaxStages, allowed, fit, groups, st);
+    return launch_rows<T, R, VT, kRegs, RAGGED>(block_norm_fwd_kernel<T, VEC, R, VT / VEC, kRegs, KIND, RAGGED>, p, tensors, R <= 32 && VT > 8 ? 1 : kMaxStages, allowed, fit, groups, st);
 }
-template <typename T, int VEC, int R, int VT, int KIND>
+template <typename T, int VEC, int R, int VT, int KIND, bool RAGGED>
 cudaError_t launch_kind(const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     static std::atomic<int> fit{0};
-    constexpr bool ring = VEC > 1;
-    constexpr int place = !ring ? kRegs : R < 1024 ? kShared : kMemory;
-    return launch_rows<T, R, VT, ring, place>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, ring, place, KIND>, p, tensors, kMaxStages, allowed, fit, groups, st);
+    constexpr int place = RAGGED && R < 1024 ? kRegs : R < 1024 ? kShared : kMemory;
+    return launch_rows<T, R, VT, place, RAGGED>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, place, KIND, RAGGED>, p, tensors, kMaxStages, allowed, fit, groups, st);
 }
 Kind kind_of(const Fwd &p) {
     if (!p.w1 || (p.w2 == nullptr) != (p.in[2] == nullptr)) return kAny;
@@ -712,28 +808,24 @@ Kind kind_of(const Bwd &p) {
     return p.w2 ? (p.in[1] ? kBlock : kUngated) : p.in[1] ? kHead : kAny;
 }
 template <typename T, int VEC, int R, int VT, typename P>
-cudaError_t launch_one(const P &p, int tensors, int64_t *groups, cudaStream_t st) {
-    if constexpr (VEC > 1) {
-        const Kind k = kind_of(p);
-        if (k == kBlock) return launch_kind<T, VEC, R, VT, kBlock>(p, tensors, groups, st);
-        if (k == kHead) return launch_kind<T, VEC, R, VT, kHead>(p, tensors, groups, st);
-        if (k == kUngated) return launch_kind<T, VEC, R, VT, kUngated>(p, tensors, groups, st);
-    }
-    return launch_kind<T, VEC, R, VT, kAny>(p, tensors, groups, st);
+cudaError_t launch_one(const P &p, bool ragged, int tensors, int64_t *groups, cudaStream_t st) {
+    const Kind k = kind_of(p);
+    if (k == kBlock) return ragged ? launch_kind<T, VEC, R, VT, kBlock, true>(p, tensors, groups, st) : launch_kind<T, VEC, R, VT, kBlock, false>(p, tensors, groups, st);
+    if (k == kHead) return ragged ? launch_kind<T, VEC, R, VT, kHead, true>(p, tensors, groups, st) : launch_kind<T, VEC, R, VT, kHead, false>(p, tensors, groups, st);
+    if (k == kUngated) return ragged ? launch_kind<T, VEC, R, VT, kUngated, true>(p, tensors, groups, st) : launch_kind<T, VEC, R, VT, kUngated, false>(p, tensors, groups, st);
+    return ragged ? launch_kind<T, VEC, R, VT, kAny, true>(p, tensors, groups, st) : launch_kind<T, VEC, R, VT, kAny, false>(p, tensors, groups, st);
 }
 
 // The instances that shape_of names.
-#define HARTS_CASE(V, R, VT) if (s.vec == V && s.r == R && s.values == VT) return launch_one<T, V, R, VT>(p, tensors, groups, st);
+#define HARTS_CASE(V, R, VT) if (s.vec == V && s.r == R && s.values == VT) return launch_one<T, V, R, VT>(p, s.ragged, tensors, groups, st);
 template <typename T, int VEC> cudaError_t run(const Shape &s, const Fwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     HARTS_CASE(VEC, 8, 8) HARTS_CASE(VEC, 16, 8) HARTS_CASE(VEC, 16, 16) HARTS_CASE(VEC, 32, 16) HARTS_CASE(VEC, 64, 16)
     HARTS_CASE(VEC, 128, 16) HARTS_CASE(VEC, 256, 16) HARTS_CASE(VEC, 512, 16)
-    HARTS_CASE(1, 32, 8) HARTS_CASE(1, 256, 8) HARTS_CASE(1, 1024, 8)
     return cudaErrorInvalidValue;
 }
 template <typename T, int VEC> cudaError_t run(const Shape &s, const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     HARTS_CASE(VEC, 8, 8) HARTS_CASE(VEC, 16, 8) HARTS_CASE(VEC, 32, 8) HARTS_CASE(VEC, 64, 8)
     HARTS_CASE(VEC, 128, 8) HARTS_CASE(VEC, 256, 8) HARTS_CASE(VEC, 512, 8) HARTS_CASE(VEC, 1024, 8)
-    HARTS_CASE(1, 32, 8) HARTS_CASE(1, 256, 8) HARTS_CASE(1, 1024, 8)
     return cudaErrorInvalidValue;
 }
 #undef HARTS_CASE
@@ -787,6 +879,7 @@ int harts_block_norm_fwd(const harts_block_norm_args *a, harts_stream_t stream) 
     p.w1 = a->post_weight; p.w2 = a->pre_weight;
     p.h = a->h; p.n = a->n; p.r1 = a->rstd_post; p.r2 = a->rstd_pre;
     p.C = a->C; p.D = a->D; p.act = a->gate_act; p.scale = a->scale; p.eps = a->eps;
+    set_whole(p, a->dtype);
     p.error = a->error ? a->error : own_error_word();
     if (!p.error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     int64_t groups = 0;
@@ -841,6 +934,7 @@ int harts_block_norm_bwd(const harts_block_norm_bwd_args *b, harts_stream_t stre
     p.dy = b->dy; p.dgate = b->dgate; p.dres = b->dresidual;
     p.part = static_cast<float *>(b->workspace);
     p.C = a->C; p.D = a->D; p.act = a->gate_act; p.scale = a->scale;
+    set_whole(p, a->dtype);
     p.error = a->error ? a->error : own_error_word();
     if (!p.error) { set_error("the library's error word is not to be had"); return HARTS_ECUDA; }
     int tensors = 0;

@@ -150,6 +150,43 @@ def test_in_place(form, D):
     assert got["dy"] is y and got["dresidual"] is dh
 
 
+
+# rows that begin inside a vector: up to its last value, over more rows than are resident, shorter than a
+# vector, as wide as whole vectors of such rows may be, and one wider
+RAGGED = [(1, 3), (11, 5), (50_003, 3), (5, 65), (40_001, 67), (20_000, 100), (9001, 250), (5000, 129), (3001, 513), (2501, 1025),
+          (901, 2047), (400, 4095), (333, 4089), (40, 8185), (3, 8186), (6, 8189)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("form", ["all", "heads", "bare"])
+@pytest.mark.parametrize("C,D", RAGGED)
+def test_rows_that_are_not_whole_vectors(C, D, form, dtype):
+    c = Case(C, D, dtype, form)
+    c.check_backward(*c.check_forward())
+
+
+@pytest.mark.parametrize("C,D", [(3000, 1003), (30_000, 61), (700, 4001)])
+def test_neighbours_of_rows_that_begin_inside_a_vector(C, D):
+    """Nothing of a row reaches the next, which shares its first or last 16 bytes; in place neither."""
+    c = Case(C, D, "bf16", "all")
+    h, n, r1, r2 = c.forward()
+    d = c.backward(h, r1, r2)
+    res, y = c.res.clone(), c.y.clone()
+    got = block_norm_fwd(y, residual=res, eps=EPS, **c.kw(), h=res, n=y)
+    assert got[0] is res and torch.equal(res, h) and torch.equal(y, n)
+    rows = torch.arange(C, device="cuda")
+    bad, good = rows % 3 == 1, rows % 3 != 1
+    odd = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").bfloat16()
+    for t in (c.y, c.gate, c.res, c.dn, c.dh):
+        t[bad] = odd[torch.randint(0, 3, (D,), device="cuda")]
+    h2, n2, s1, s2 = c.forward()
+    h[bad] = float("nan")
+    d2 = c.backward(h, r1, r2)
+    assert torch.equal(h2[good], h[good]) and torch.equal(n2[good], n[good]) and torch.equal(s1[good], r1[good]) and torch.equal(s2[good], r2[good])
+    for k in ("dy", "dresidual", "dgate"):
+        assert torch.equal(d2[k][good], d[k][good])
+
+
 def test_gate_far_out_and_rows_of_nothing():
     c = Case(4, 512, "fp32", "all")
     c.gate[0] = 90.0

@@ -8,7 +8,7 @@ from tests.test_tail_sources import _arguments, _source
 
 # What a caller hands in and no kernel of the call writes.  (w0, w1: rows of the weight; bias + col: the
 # bias; w + col: a norm's weight, through rows.cuh.)
-INPUTS = {"block_norm.cu": {"p.r1", "p.r2"}, "rows.cuh": {"w"},
+INPUTS = {"block_norm.cu": {"p.r1", "p.r2", "w"}, "rows.cuh": {"w"},
           "linear.cu": {"bias", "w0", "w1", "p.x", "p.ep.bias", "p.dy", "p.z"}}
 
 
