@@ -38,6 +38,10 @@ constexpr int kWarps = 8, kWarpRows = kScanRows / kWarps;      // consumers
 constexpr int kThreads = 32 * (kWarps + 2);                    // and a warp each for carries and copies
 constexpr int kAtOnce = 8;                                     // maps that are fetched at a time
 constexpr int kBox = 32;                                       // rows of one copy
+// Rows of a tile for a warp: sixteen, and none for the last warps of a short tile; but as many for each (EVEN) where
+// a warp also fetches its rows' x itself.  (The mix form's gradients, 65,536 rows of 2,048 channels: 768 segments 430 us to
+// 378, 361 335 to 314; elsewhere a short tile only gains more joins: forward, 1,024 segments of 64 rows 153 to 172.)
+template <bool EVEN> __device__ __forceinline__ int rows_each(int rows) { return EVEN ? (rows + kWarps - 1) / kWarps : kWarpRows; }
 constexpr uint32_t kTileBytes = kScanRows * 128;               // of one tensor
 constexpr uint32_t kEmpty = 0xffffffffu;                       // not published yet
 
@@ -370,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
             if (!warp_wait(&full[s], (it / R::stages) & 1, &s_fail)) return -1;
             const int rows = meta[s].t.rows;
             if (rows == 0) return 0;
-            const int mine = min(max(rows - warp * kWarpRows, 0), kWarpRows);
-            const uint8_t *src = sm + s * R::stage_bytes + warp * kWarpRows * 128 + lane * 4;
+            const int from = warp * rows_each<BWD && MIX>(rows), mine = min(max(rows - from, 0), rows_each<BWD && MIX>(rows));
+            const uint8_t *src = sm + s * R::stage_bytes + from * 128 + lane * 4;
             const int64_t ch = meta[s].col + lane * CH;
             if (BWD && warp == 0 && ch < p.D) {                // state before the tile's first row
                 const int32_t pr = meta[s].t.pred_row;
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
                 else if (p.h0) before = L::load(p.h0 + static_cast<int64_t>(-1 - pr) * p.D + ch);
             }
             if constexpr (BWD && MIX) {
-                const T *xp = static_cast<const T *>(p.x_in) + static_cast<int64_t>(meta[s].t.row0 + warp * kWarpRows) * p.D + ch;
+                const T *xp = static_cast<const T *>(p.x_in) + static_cast<int64_t>(meta[s].t.row0 + from) * p.D + ch;
 #pragma unroll
                 for (int i = 0; i < kWarpRows; ++i)
                     xr[i] = i < mine && ch < p.D ? __ldcs(reinterpret_cast<const uint32_t *>(xp + static_cast<int64_t>(i) * p.D)) : 0u;
@@ -431,13 +435,13 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
         auto results = [&](uint32_t it, const V (&d)[kWarpRows], [[maybe_unused]] V before, [[maybe_unused]] const uint32_t *xr) -> bool {
             const int s = it % R::stages;
             if (!warp_wait(&maps_full[s], (it / R::stages) & 1, &s_fail) || !warp_wait(&carry_full[s], (it / R::stages) & 1, &s_fail)) return false;
-            const int rows = meta[s].t.rows, mine = min(max(rows - warp * kWarpRows, 0), kWarpRows);
-            const uint8_t *src = sm + s * R::stage_bytes + warp * kWarpRows * 128 + lane * 4;
+            const int rows = meta[s].t.rows, from = warp * rows_each<BWD && MIX>(rows), mine = min(max(rows - from, 0), rows_each<BWD && MIX>(rows));
+            const uint8_t *src = sm + s * R::stage_bytes + from * 128 + lane * 4;
             const int64_t ch = meta[s].col + lane * CH;
             V v = s_carry[s][lane];
             for (int k = BWD ? kWarps - 1 : 0; k != warp; k += BWD ? -1 : 1) v = fma(s_a[s][k][lane], v, s_b[s][k][lane]);
             if (ch < p.D) {
-                const int64_t at = static_cast<int64_t>(meta[s].t.row0 + warp * kWarpRows) * p.D + ch;
+                const int64_t at = static_cast<int64_t>(meta[s].t.row0 + from) * p.D + ch;
                 T *out0 = static_cast<T *>(p.out0) + at;
                 [[maybe_unused]] T *out1 = static_cast<T *>(p.out1) + at;
                 auto row = [&](int i) {
@@ -463,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
                     for (int k = 0; k < kWarpRows; ++k)
                         if ((BWD ? kWarpRows - 1 - k : k) < mine) row(BWD ? kWarpRows - 1 - k : k);
                 }
-                if (!BWD && p.final_state && meta[s].t.seq_end >= 0 && meta[s].t.at == meta[s].t.count - 1 && mine > 0 &&
-                    rows - warp * kWarpRows <= kWarpRows)
+                if (!BWD && p.final_state && meta[s].t.seq_end >= 0 && meta[s].t.at == meta[s].t.count - 1 && mine > 0 && from + mine == rows)
                     L::store(p.final_state + static_cast<int64_t>(meta[s].t.seq_end) * p.D + ch, v);
             }
             __syncwarp();
