@@ -37,13 +37,16 @@ using namespace two;
 
 constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K step (one 128-byte swizzle row), tile columns
 constexpr uint32_t kABytes = kTM * kTK * 2;
-constexpr uint32_t kSlots = 4, kSlotBytes = kTM * 128;          // 128 rows x 128 bytes of output on their way out
+constexpr uint32_t kSlots = 4, kSlotBytes = kTM * 64;           // 128 rows x 64 bytes of output on their way out
 constexpr int kThreads = 448, kEpiWarp0 = 4, kStoreWarp0 = 12;  // eight epilogue warps: two for each 32 TMEM lanes
 constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr int kDotRows = 2;                         // most rows that are done by dot products
 
+// As many stages as fit beside small slots: copies are some 2,500 cycles on their way while results go out, five steps
+// of a pair.  (8,192 x 2,048 x 8,192, cycles, plain / gelu and z: six stages and slots of 8 KB 259 K / 276 K, five and
+// slots of 16 KB 271 K / 311 K, four 305 K / 339 K; 229 K are the products alone.)
 template <int G> struct Ring {
-    static constexpr uint32_t stages = G == 2 ? 5 : 3;
+    static constexpr uint32_t stages = G == 2 ? 6 : 4;
     static constexpr uint32_t stage_bytes = kABytes + kTN / G * kTK * 2;
     static constexpr uint32_t smem = stages * stage_bytes + kSlots * kSlotBytes + 1024;
     static_assert(smem <= 227 * 1024 - 512, "shared memory of an SM");
@@ -180,22 +183,18 @@ template <int ACT> __device__ __forceinline__ Two slope_of(Two z) {
 }
 __device__ __forceinline__ Two open(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// Eight columns from `col` of one row (the residual's at `res`): z with its bias, and y.  Columns
-// come in eights.
+// Eight columns of one row, with their bias and residual: z and y.  Columns come in eights.
 struct Eight { Two v[4]; };
-template <int ACT> __device__ __forceinline__ void finish8(const float *bias, const uint4 *res, int32_t col, Eight &z, Eight &y) {
-    if (bias) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(bias + col)), b = __ldg(reinterpret_cast<const float4 *>(bias + col) + 1);
-        z.v[0] = add(z.v[0], make_float2(a.x, a.y)); z.v[1] = add(z.v[1], make_float2(a.z, a.w));
-        z.v[2] = add(z.v[2], make_float2(b.x, b.y)); z.v[3] = add(z.v[3], make_float2(b.z, b.w));
-    }
+struct Bias8 { float4 a, b; };
+__device__ __forceinline__ Bias8 bias_of(const float *bias, int32_t col) {
+    return {__ldg(reinterpret_cast<const float4 *>(bias + col)), __ldg(reinterpret_cast<const float4 *>(bias + col) + 1)};
+}
+template <int ACT> __device__ __forceinline__ void finish8(const Bias8 &b, const uint4 &res, Eight &z, Eight &y) {
+    z.v[0] = add(z.v[0], make_float2(b.a.x, b.a.y)); z.v[1] = add(z.v[1], make_float2(b.a.z, b.a.w));
+    z.v[2] = add(z.v[2], make_float2(b.b.x, b.b.y)); z.v[3] = add(z.v[3], make_float2(b.b.z, b.b.w));
+    const uint32_t *u = &res.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y.v[i] = act_of<ACT>(z.v[i]);
-    if (res) {
-        const uint32_t *u = &res->x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y.v[i] = add(y.v[i], open(u[i]));
-    }
+    for (int i = 0; i < 4; ++i) y.v[i] = add(act_of<ACT>(z.v[i]), open(u[i]));
 }
 __device__ __forceinline__ uint4 pack8(const Eight &e) {
     return make_uint4(tc::pack_bf16(e.v[0].x, e.v[0].y), tc::pack_bf16(e.v[1].x, e.v[1].y), tc::pack_bf16(e.v[2].x, e.v[2].y), tc::pack_bf16(e.v[3].x, e.v[3].y));
@@ -319,11 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
             }
         }
     } else if (warp >= kEpiWarp0 && warp < kStoreWarp0) {
-        // 128 bytes of columns at a time, taken in turn by the two warps of 32 TMEM lanes; each of
+        // 64 bytes of columns at a time, taken in turn by the two warps of 32 TMEM lanes; each of
         // the two has two of the slots, z before y where both go out
         const int lg = (warp - kEpiWarp0) & 3, half = (warp - kEpiWarp0) >> 2;
         const uint32_t lane_off = static_cast<uint32_t>(lg * 32) << 16;
-        uint8_t *out = sm + kStages * kStageBytes + lg * 4096;  // this warp's rows of a slot
+        uint8_t *out = sm + kStages * kStageBytes + lg * 2048 + lane * 64;  // this lane's row of a slot
+        const int swizzle = (lane >> 1) & 3;
         const uint32_t released = G == 2 ? leader_addr(&bars[B::acc_empty]) : 0;
         uint32_t tile = 0, groups = 0, q_out = 0;
         TileId t;
@@ -355,58 +355,57 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
             }
             if (!warp_wait(&bars[B::acc_full + buf], (tile >> 1) & 1, &s_fail)) break;
             tc::fence_after_sync();
-            const int step = !FWD && q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
+            const int step = !FWD && q.out_f32 ? 16 : 32, end = min(q.n, q.cols - n0);
             for (int c = 0; c < end; c += step, ++groups) {
                 if ((groups & 1) != static_cast<uint32_t>(half)) continue;
-                uint32_t slot;
-                if (!slot_for(slot)) { ok = false; break; }
-                uint8_t *dst = out + slot * kSlotBytes;
+                // The values first, then a slot for them: what the unit before it left there is on its way out
+                // meanwhile.  A row's four 16 bytes are swizzled by its number in pairs.
+                auto leave = [&](const uint4 (&w)[4]) {
+                    uint32_t slot;
+                    if (!slot_for(slot)) return false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(out + slot * kSlotBytes + ((j ^ swizzle) << 4)) = w[j];
+                    send(slot);
+                    return true;
+                };
                 if (!FWD && q.out_f32) {
+                    float v[16];
+                    tc::tmem_ld16(acc + c, v);
+                    ok = leave(reinterpret_cast<const uint4(&)[4]>(v));
+                } else {
+                    const int32_t col = n0 + c;
+                    uint4 r[4] = {};
+                    Bias8 b[4] = {};
+                    if constexpr (FWD) {                        // on their way together, and ahead of the accumulator
+                        if (p.ep.res && row < q.rows) {
+                            const __nv_bfloat16 *res = p.ep.res + static_cast<int64_t>(row) * q.cols;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const uint4 *>(res + min(col + 8 * j, q.cols - 8));
+                        }
+                        if (p.ep.bias) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) b[j] = bias_of(p.ep.bias, min(col + 8 * j, q.cols - 8));
+                        }
+                    }
                     float v[32];
                     tc::tmem_ld32(acc + c, v);
+                    uint4 zs[4], ys[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4 *>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else if constexpr (FWD) {
-                    uint8_t *z_dst = dst;
-                    const uint32_t z_slot = slot;
-                    if (p.keep) {
-                        if (!slot_for(slot)) { ok = false; break; }
-                        dst = out + slot * kSlotBytes;
-                    }
-                    // 32 columns at a time: what is unrolled is fetched anew by every launch
-#pragma unroll 1
-                    for (int h = 0; h < 64; h += 32) {
-                        const int32_t col = n0 + c + h;
-                        const __nv_bfloat16 *res = p.ep.res ? p.ep.res + static_cast<int64_t>(row) * q.cols + col : nullptr;
-                        uint4 r[4];
+                    for (int j = 0; j < 4; ++j) {
+                        Eight z, y;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            r[j] = make_uint4(0, 0, 0, 0);
-                            if (res && row < q.rows && col + 8 * j < q.cols) r[j] = *reinterpret_cast<const uint4 *>(res + 8 * j);
-                        }
-                        float v[32];
-                        tc::tmem_ld32(acc + c + h, v);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (col + 8 * j >= q.cols) break;
-                            Eight z, y;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) z.v[i] = make_float2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-                            finish8<FWD ? ACT : 0>(p.ep.bias, p.ep.res ? &r[j] : nullptr, col + 8 * j, z, y);
-                            const uint32_t chunk = lane * 128 + (((h / 8 + j) ^ (lane & 7)) << 4);
-                            if (p.keep) *reinterpret_cast<uint4 *>(z_dst + chunk) = pack8(z);
-                            *reinterpret_cast<uint4 *>(dst + chunk) = pack8(y);
+                        for (int i = 0; i < 4; ++i) z.v[i] = make_float2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                        if constexpr (FWD) {
+                            finish8<ACT>(b[j], r[j], z, y);
+                            zs[j] = pack8(z);
+                            ys[j] = pack8(y);
+                        } else {
+                            ys[j] = pack8(z);
                         }
                     }
-                    if (p.keep) send(z_slot);
-                } else {
-                    float v[64];
-                    tc::tmem_ld32x2(acc + c, reinterpret_cast<float(&)[32]>(v[0]), acc + c + 32, reinterpret_cast<float(&)[32]>(v[32]));
-                    store_row(dst, lane, v);
+                    ok = (!FWD || !p.keep || leave(zs)) && leave(ys);
                 }
-                send(slot);
+                if (!ok) break;
             }
             tc::fence_before_sync();                    // the accumulator has been read
             __syncwarp();
@@ -415,8 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
             }
         }
     } else if (warp >= kStoreWarp0) {
-        // Two threads send the slots of a half each, with all but the last of their stores read: a store
-        // takes its thread a few hundred cycles, which the warps that fill the slots need not wait for.
+        // Two threads send the slots of a half each: a store takes its thread a few hundred cycles, which the
+        // warps that fill the slots need not wait for.  A slot is given back behind the next store; z's and y's
+        // together (one behind the other keeps the next z waiting: 276 K cycles to 291 K for 8,192 x 2,048 x 8,192 with gelu).
         if (lane == 0) {
             const uint32_t mine = warp - kStoreWarp0;
             uint32_t groups = 0, q_out = 0;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
             for (uint32_t n = 0; ok && tile_at(p, n, worker, workers, t); ++n) {
                 const Prod &q = p.prod[t.which];
                 const int32_t n0 = t.nt * q.n, y = (t.mt * G + rank) * kTM;
-                const int step = !FWD && q.out_f32 ? 32 : 64, end = min(q.n, q.cols - n0);
+                const int step = !FWD && q.out_f32 ? 16 : 32, end = min(q.n, q.cols - n0);
                 for (int c = 0; ok && c < end; c += step, ++groups) {
                     if ((groups & 1) != mine) continue;
                     for (int k = FWD && p.keep ? 0 : 1; k < 2; ++k) {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
                         if (y < q.rows) store_3d(k == 0 ? &q.keep : &q.out, n0 + c, y, t.split, src, false);
                         tc::bulk_commit();
                         ++q_out;
-                        if (FWD && p.keep) {            // z's slot waits for y's: both are given back at once
+                        if (FWD && p.keep) {            // z's and y's given back at once
                             if (k == 0) continue;
                             tc::bulk_wait_read();
                             arrive(&bars[B::out_free + mine]);
@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(128) linear_join_kernel(const Join p) {
     }
     uint4 r = make_uint4(0, 0, 0, 0);
     if (p.ep.res) r = *reinterpret_cast<const uint4 *>(p.ep.res + at);
-    finish8<ACT>(p.ep.bias, p.ep.res ? &r : nullptr, static_cast<int32_t>(at % o.cols), z, y);
+    Bias8 b{};
+    if (p.ep.bias) b = bias_of(p.ep.bias, static_cast<int32_t>(at % o.cols));
+    finish8<ACT>(b, r, z, y);
     if (o.z) *reinterpret_cast<uint4 *>(o.z + at) = pack8(z);
     *reinterpret_cast<uint4 *>(o.y + at) = pack8(y);
 }
@@ -631,7 +633,7 @@ struct Cut { int G; int32_t n, splits, k_per; };
 // Blocks that share a tile, its width and the pieces of the sum, by the time of the busiest worker:
 // a step of 64 takes two cycles a column, no less than its copies and barriers (430 - 450), and in
 // single blocks 1.2 as long, as each reads its columns alone; a tile's ends cost about three steps.
-// Columns leave in 64s, and an operand read by columns comes in 64s per block.
+// An operand read by columns comes in 64s per block.
 // Pieces cost their fp32 sums, written and read again at some 3,500 bytes a cycle, a launch, and the caller a
 // workspace.
 Cut cut_of(int64_t M, int64_t N, int32_t kb, bool by_columns, int32_t outputs, int groups = 2) {
@@ -673,16 +675,16 @@ bool map_cols(CUtensorMap *m, CUtensorMap *edge, const void *base, int64_t rows,
     return encode_bf16(m, base, 3, dims, strides, box);
 }
 
-// [layers][rows][cols], written in boxes of 128 bytes x 128 rows.
+// [layers][rows][cols], written in boxes of 64 bytes x 128 rows.
 bool map_out(CUtensorMap *m, void *base, int64_t layers, int64_t rows, int64_t cols, bool f32) {
     const cuuint64_t e = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(layers)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * e, static_cast<cuuint64_t>(cols) * e * rows};
-    const cuuint32_t box[3] = {f32 ? 32u : 64u, kTM, 1};
+    const cuuint32_t box[3] = {f32 ? 16u : 32u, kTM, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     auto fn = encode_tiled();
     return fn && fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides,
-                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -2,7 +2,7 @@
 tests/_barrier_model.py: under every schedule no deadlock, no wait that returns on another phase, no
 buffer read before it is written or after it is overwritten.  What the kernels did while they were
 built, and must not do again, is rejected: tiles dealt out with a group's later ones first, a tile's own map
-kept back until the others' are there, z's slot given back before y's is asked for."""
+kept back until the others' are there, slots for z and y asked for before either is filled."""
 import pytest
 
 from tests._barrier_model import Sim, Violation
@@ -269,28 +269,29 @@ def test_scan_maps_do_not_wait_for_one_another():
         assert (("map", 1) in sim.there) == published
 
 
-def output_slots(sim, keep, units, eager_y=True):
-    """The two halves' epilogue warps (one stands for four) and their storing threads."""
+def output_slots(sim, keep, units, both_first=False, together=True):
+    """The two halves' epilogue warps (one stands for four) and their storing threads: every unit leaves
+    z, where it is kept, and y in the half's two slots in turn.  together: both are given back behind y,
+    otherwise each behind the next store."""
     full = [sim.bar(f"full{i}") for i in range(4)]
     free = [sim.bar(f"free{i}") for i in range(4)]
 
     def epilogue(half):
         q = 0
-
-        def slot():
-            return half + 2 * (q & 1), q >> 1
         for u in range(half, units, 2):
-            out = []
+            asked = []
             for k in (0, 1) if keep else (1,):
-                s, use = slot()
+                s, use = half + 2 * (q & 1), q >> 1
                 q += 1
                 if use > 0:
                     yield ("wait", free[s], use - 1)
-                out.append((s, use))
-            for k, (s, use) in enumerate(out):
-                yield ("write", f"slot{s}", (u, len(out) - 1 - k))
-            for s, use in out:
-                yield ("arrive", full[s], use)
+                asked.append((s, use, k))
+                if both_first and k == 0:
+                    continue
+                for s, use, k in asked:
+                    yield ("write", f"slot{s}", (u, k))
+                    yield ("arrive", full[s], use)
+                asked = []
 
     def store(half):
         q = 0
@@ -299,9 +300,9 @@ def output_slots(sim, keep, units, eager_y=True):
             for k in (0, 1) if keep else (1,):
                 s, use = half + 2 * (q & 1), q >> 1
                 yield ("wait", full[s], use)
-                yield ("read", f"slot{s}", (u, 1 - k if keep else 0))
+                yield ("read", f"slot{s}", (u, k))
                 q += 1
-                if keep and eager_y:
+                if keep and together:
                     if k == 1:
                         yield ("arrive", free[half], use)
                         yield ("arrive", free[half + 2], use)
@@ -315,17 +316,19 @@ def output_slots(sim, keep, units, eager_y=True):
 
 
 @pytest.mark.parametrize("units", [1, 2, 3, 8, 13])
+@pytest.mark.parametrize("together", [False, True])
 @pytest.mark.parametrize("keep", [False, True])
-def test_output_slots(keep, units):
+def test_output_slots(keep, together, units):
     for seed in range(60):
         sim = Sim(seed)
-        output_slots(sim, keep, units)
+        output_slots(sim, keep, units, together=together)
         sim.run()
 
 
-def test_output_slots_reject_z_held_back_by_the_last_y():
+def test_output_slots_reject_both_asked_for_before_either_is_filled():
+    """Where a slot is given back behind the next store, y's comes free only behind the z that follows it."""
     with pytest.raises(Violation, match="(?i)deadlock"):
         for seed in range(20):
             sim = Sim(seed)
-            output_slots(sim, True, 8, eager_y=False)
+            output_slots(sim, True, 8, both_first=True, together=False)
             sim.run()
