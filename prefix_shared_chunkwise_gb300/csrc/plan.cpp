@@ -538,7 +538,7 @@ void build_image(harts_plan &P) {
     }
     I.scan_alone = alone;
     I.scan_longest = *std::max_element(behind.begin(), behind.end());
-    for (int cut = 0; cut < 2; ++cut) {
+    for (int cut = 0; cut < kScanCuts; ++cut) {
         const int group = kScanGroups[cut];
         std::vector<ScanTile> tiles;
         std::vector<int32_t> gfirst(n + 1, 0), depth, height, snext;

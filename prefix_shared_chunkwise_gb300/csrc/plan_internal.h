@@ -12,10 +12,10 @@ namespace harts {
 constexpr int kConvMaxW = 8;       // widest short convolution the plan tables serve
 constexpr int kAttnTile = 128;     // query / key rows per branch-attention tile
 constexpr int kScanRows = 128;     // rows per tile of the gated scan
-// Most tiles of one segment whose carries are joined side by side, in a plan's two cuts: few where
+// Most tiles of one segment whose carries are joined side by side, in a plan's three cuts: few where
 // the tiles of many channels take turns (a tile looks at those before it in its group), many where a
 // chain of carries is all there is, or where a tile's own work is long (backward).
-constexpr int kScanGroups[2] = {16, 32};
+constexpr int kScanCuts = 3, kScanGroups[kScanCuts] = {8, 16, 32};
 constexpr int64_t kAttnMaxRows = int64_t(1) << 27;   // largest ancestor-row table built
 
 // A tile of the gated scan: up to kScanRows rows of one segment.  Up to kScanGroups[k] consecutive
@@ -68,8 +68,8 @@ struct PlanDev {
     const int32_t *attn_kq;        // (sequence, query tile, f): f own rows of the key's sequence visible, -1 causal
     int32_t n_qt, n_kt;
     // gated scan: one record per tile, predecessors first (forward) and successors first (backward)
-    const struct ScanTile *scan_fwd[2], *scan_bwd[2];   // [n_scan], by kScanGroups
-    const int32_t *scan_next[2];   // groups that follow a segment's last group: ScanTile::next_begin ..
+    const struct ScanTile *scan_fwd[kScanCuts], *scan_bwd[kScanCuts];   // [n_scan], by kScanGroups
+    const int32_t *scan_next[kScanCuts];   // groups that follow a segment's last group: ScanTile::next_begin ..
     int32_t n_rounds, n_seq, n_states, n_roots, n_fold, chunk, n_seg;
     uint32_t flags;                // harts_plan_calls flags (HARTS_PLAN_NOREPLAY: slots inside chunks)
     int64_t R, n_chunks, C;
@@ -84,8 +84,8 @@ struct PlanImage {
         off_fold_rows, off_fold_ptr, off_fold_occ, off_chunk_seq, off_row_seg, off_seg_row0,
         off_seg_len, off_conv_ctx, off_conv_sptr, off_conv_succ, off_attn_rptr, off_attn_runs,
         off_attn_mptr, off_attn_mask, off_attn_hp, off_attn_qt, off_attn_kt, off_attn_kptr, off_attn_kq,
-        off_scan_fwd[2], off_scan_bwd[2], off_scan_next[2];
-    int32_t n_qt, n_kt, n_scan, n_scan_groups[2], scan_alone;   // scan_alone: no tile follows another one
+        off_scan_fwd[kScanCuts], off_scan_bwd[kScanCuts], off_scan_next[kScanCuts];
+    int32_t n_qt, n_kt, n_scan, n_scan_groups[kScanCuts], scan_alone;   // scan_alone: no tile follows another one
     int64_t scan_longest;          // rows of the longest trajectory
 };
 

@@ -12,8 +12,8 @@
 // planner cuts segments into tiles of 128 rows (a fork lies at a tile's end); a block takes a
 // tile of 128 bytes of channels: eight warps of 16 rows each compose their rows' map, a ninth
 // joins the eight and forms the carry, from the maps that the tiles before it in its group published
-// (16 or 32 tiles of a segment, which need not wait for one another) and the state that the group before
-// left, both fetched while the rows are still on their way: a chain waits once for 2,048 or 4,096 rows,
+// (8 to 32 tiles of a segment, which need not wait for one another) and the state that the group before
+// left, both fetched while the rows are still on their way: a chain waits once for 1,024 to 4,096 rows,
 // about 1 us.  The order in which maps are joined is fixed by position: no atomics on values, the same
 // bits on every run.  What is published carries its own validity: the workspace starts as all ones, a NaN
 // that no published value has.  Tiles are taken in an order that has predecessors first, by a ticket
@@ -21,8 +21,8 @@
 // the same.
 //
 // bf16: 65,536 rows of 2,048 channels in 361 segments, add form: 141 us (84 % of the copy's rate), gradients 234 (84 %);
-// mix form's gradients 314 (76 %).  One trajectory of 131,071 rows, 1,024 channels, mix form with states: 190 us
-// (62 %), bound by the chain of its groups.  512 segments of 128 rows: 139 (85 %); 4,096 of 16: 558 (21 %), where a
+// mix form's gradients 314 (76 %).  One trajectory of 131,071 rows, 1,024 channels, mix form with states: 180 us
+// (66 %), bound by the chain of its groups.  512 segments of 128 rows: 139 (85 %); 4,096 of 16: 558 (21 %), where a
 // tile's fixed time, 1.9 us a block, is all.  48 single rows: 1.4 us on the device.
 #include <algorithm>
 #include <cstring>
@@ -197,14 +197,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f)
 // before it in the block, whose carry may be long in coming: on long trajectories all blocks would
 // otherwise compose and then wait together.  That takes the registers of two tiles' decays, so a third
 // block's, and does nothing for tiles that need not wait: the forward takes it where the longest trajectory has
-// kAheadRows rows.  (bf16, mix form: one of 131,072 rows of 1,024 channels 192 us, 339 without; 4 of
+// kAheadRows rows.  (bf16, mix form, groups of 16: one of 131,072 rows of 1,024 channels 192 us, 339 without; 4 of
 // 16,384 rows of 2,048 channels 170 and 202, 8 of 8,192 rows 168 and 177, 16 of 4,200 rows 172 and 169,
 // 16 chains of 40 segments of 200 rows 215 and 197.)
 constexpr int64_t kAheadRows = 8192;
-// Up to so many tiles across, the chain of carries is all there is, and the longer groups are
-// taken forward too.  (131,072 rows, bf16, mix: 64 channels 35 us, 54 in groups of 16; 128: 49 and 72; 256:
-// 79 and 76; 1,024: 221 and 192.  Backward, 1,024 channels: 345 and 394.)
-constexpr int32_t kNarrow = 2;
+// Groups of 8 tiles are the forward's where more than eight tiles lie side by side; up to eight are too few to fill
+// the chip with small groups, and up to two leave the chain of carries as all there is.  (131,072 rows, bf16, mix, in
+// groups of 8 / 16 / 32: 1,024 channels 180 us / 192 / 221, 512 127 / 111 / 137, 256 110 / 76 / 79, 128 97 / 72 / 49, 64
+// 90 / 54 / 35.  Backward, 1,024 channels: 406 / 394 / 345.)
 template <bool BWD, bool AHEAD> struct Ring {
     static constexpr int tensors = BWD ? 3 : 2, stages = AHEAD ? 3 : 2, blocks = BWD || AHEAD ? 2 : 3;
     static constexpr uint32_t stage_bytes = tensors * kTileBytes;
@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
                 }
             }
             if (AHEAD && __shfl_sync(0xffffffffu, last, 0) && meta[s].t.at < meta[s].t.count - 1) {
+                __syncwarp();                                  // the other warps' maps, which the first lane has seen
                 A = L::all(1.f), B = L::all(0.f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
@@ -534,7 +535,7 @@ Space space_of(const harts_plan *P, int32_t D, int32_t dtype) {
     Space s{};
     if (P->image.scan_alone) return s;
     s.inc = 256;
-    s.agg = s.inc + align256(4 * width * std::max(P->image.n_scan_groups[0], P->image.n_scan_groups[1]));
+    s.agg = s.inc + align256(4 * width * P->image.n_scan_groups[0]);      // the cut with most groups
     s.total = s.agg + align256(8 * width * P->image.n_scan);
     return s;
 }
@@ -626,7 +627,7 @@ ScanParams params_of(const harts_plan *P, const harts_scan_fwd_args *a, bool bac
     const Space s = space_of(P, a->channels, a->dtype);
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.cols = ceil_div(a->channels, wide_of(a->dtype));
-    const int cut = backward || p.cols <= kNarrow;
+    const int cut = backward || p.cols <= 2 ? 2 : p.cols <= 8;
     p.tiles = backward ? P->view.scan_bwd[cut] : P->view.scan_fwd[cut];
     p.next = P->view.scan_next[cut];
     p.h0 = a->h0;

@@ -209,7 +209,7 @@ def _tiles(parent, seg_len, rows=128):
 
 
 def test_workspace_holds_every_tile_and_group():
-    """fp32 states of every group of 16 tiles (its longer groups are fewer) and pairs of every tile of 128 rows, 64 bf16 or 32 fp32 channels wide."""
+    """fp32 states of every group of 8 tiles (longer groups are fewer) and pairs of every tile of 128 rows, 64 bf16 or 32 fp32 channels wide."""
     from prefix_shared_chunkwise_gb300.api import Plan
     r = np.random.default_rng(3)
     for _ in range(20):
@@ -218,7 +218,7 @@ def test_workspace_holds_every_tile_and_group():
         length = [int(v) for v in r.integers(1, 9000, n)]
         pl = Plan(parent, length, 64)
         tiles = len(_tiles(parent, length))
-        groups = sum((v + 2047) // 2048 for v in length)
+        groups = sum((v + 1023) // 1024 for v in length)
         up = lambda b: (b + 255) // 256 * 256
         for D, dtype, width in ((64, 1, 64), (72, 1, 128), (72, 0, 96), (1000, 0, 1024)):
             assert L.lib().harts_scan_workspace_bytes(pl.handle, D, dtype) == 256 + up(4 * width * groups) + up(8 * width * tiles)
