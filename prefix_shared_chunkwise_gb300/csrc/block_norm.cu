@@ -19,9 +19,8 @@
 //
 // bf16, 65,536 rows of 2,048 channels with everything: forward 216 us (92 % of the copy's rate), backward 325 (97 %);
 // 1,048,560 heads of 128 with norm and gate 132 (90 %) and 212 (93 %); fp32, 32,768 x 2,048: 222 (89 %) and 349 (91 %).
-// Far from it are 8,192 channels backward (bf16 48 %, fp32 67 %: one stage of a 1,024-thread block is all
-// that shared memory holds beside the weights' sums) and bf16 rows that are not whole vectors, which
-// instructions bound (see RAGGED).  One row of 2,048: 2.2 us on the device.
+// Far from it are 8,192 channels backward (bf16 71 %, fp32 65 %: one row of a block at a time, on its way and in work)
+// and bf16 rows that are not whole vectors, which instructions bound (see RAGGED).  One row of 2,048: 2.2 us on the device.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -40,7 +39,7 @@ namespace {
 using namespace rows;
 using namespace two;
 
-constexpr int kMaxDim = 8192;       // 1024 threads x 8 values
+constexpr int kMaxDim = 8192;       // 512 threads x 16 values
 constexpr int kMaxStages = 2;       // rows copied ahead
 
 struct Fwd {
@@ -738,7 +737,10 @@ __global__ void __launch_bounds__(1024) block_norm_dw_kernel(const Dw p) {
     }
 }
 
-// Threads of a row and values that each of them keeps.
+// Threads of a row and values that each of them keeps.  The backward's rows above 4,096 channels have 16 values
+// a thread, their sums in shared memory and the weights where they are, which is L1 beside one stage (bf16, 16,384 x
+// 8,192: 443 us; two stages, which leave L1 no room, 491; 1,024 threads with eight values, 64 registers each,
+// 655.  fp32, 8,192 x 8,192: 490, 473 and 480; 12,000 x 5,120 426, 436 and 470).
 struct Shape { int vec, r, values; bool ragged; };
 Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     const int full = dtype == HARTS_BF16 ? 8 : 4;
@@ -746,6 +748,7 @@ Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     if (s.ragged && full == 8) ++D;                      // a row's words, where it begins in the middle of one
     while (s.r < 16 && s.r * 8 < D) s.r *= 2;
     if (s.r * 8 < D && !backward) s.values = 16;
+    if (D > 4096) s.values = 16;
     while (s.r * s.values < D) s.r *= 2;
     return s;
 }
@@ -778,7 +781,7 @@ cudaError_t launch_rows(K *kernel, const P &p, int tensors, size_t most, std::at
     while (n > 1 && n * (weights + 2 * stage) > kSmem) --n;
     stages = static_cast<int>(std::min<size_t>(most, std::max<size_t>(1, (kSmem / n - std::min(weights, kSmem / n)) / stage)));
     smem = weights + stages * stage;
-    const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and weights: 224 KB
+    const cudaError_t e = allow_smem(kernel, R >= 512 ? 226 * 1024 : kSmem, allowed);     // one stage of 8,192 fp32 values and sums: 224 KB
     if (e != cudaSuccess) return e;
     // an even number of blocks, so that a thread's rows are an even number apart
     const int64_t rows = rows_of(R), grid = std::min<int64_t>((p.C + rows - 1) / rows, std::max(int64_t(sm_count()) * n / 2 * 2, int64_t(1)));
@@ -796,7 +799,7 @@ template <typename T, int VEC, int R, int VT, int KIND, bool RAGGED>
 cudaError_t launch_kind(const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     static std::atomic<int> fit{0};
-    constexpr int place = RAGGED && R < 1024 ? kRegs : R < 1024 ? kShared : kMemory;
+    constexpr int place = VT > 8 ? kMemory : RAGGED ? kRegs : kShared;
     return launch_rows<T, R, VT, place, RAGGED>(block_norm_bwd_kernel<T, VEC, R, VT / VEC, place, KIND, RAGGED>, p, tensors, kMaxStages, allowed, fit, groups, st);
 }
 Kind kind_of(const Fwd &p) {
@@ -825,7 +828,7 @@ template <typename T, int VEC> cudaError_t run(const Shape &s, const Fwd &p, int
 }
 template <typename T, int VEC> cudaError_t run(const Shape &s, const Bwd &p, int tensors, int64_t *groups, cudaStream_t st) {
     HARTS_CASE(VEC, 8, 8) HARTS_CASE(VEC, 16, 8) HARTS_CASE(VEC, 32, 8) HARTS_CASE(VEC, 64, 8)
-    HARTS_CASE(VEC, 128, 8) HARTS_CASE(VEC, 256, 8) HARTS_CASE(VEC, 512, 8) HARTS_CASE(VEC, 1024, 8)
+    HARTS_CASE(VEC, 128, 8) HARTS_CASE(VEC, 256, 8) HARTS_CASE(VEC, 512, 8) HARTS_CASE(VEC, 512, 16)
     return cudaErrorInvalidValue;
 }
 #undef HARTS_CASE

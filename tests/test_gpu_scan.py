@@ -53,6 +53,11 @@ def _np(t):
     return t.double().cpu().numpy()
 
 
+def plan_bytes(plan, D):
+    from prefix_shared_chunkwise_gb300 import _lib as L
+    return L.lib().harts_scan_workspace_bytes(plan.handle, D, L.HARTS_BF16)
+
+
 class Case:
     def __init__(self, forest, D, dtype, form, state, seed=0, **plan):
         self.parent, self.len = forest
@@ -285,3 +290,33 @@ def test_slow_decays_over_a_long_trajectory():
     a = np.exp(lg)
     age = a / -np.expm1(lg) - n * np.exp(n * lg) / -np.expm1(n * lg)        # of a term, by its share of the sum
     assert np.all(np.abs(_np(h) - ref) <= (2.0 ** -8 + 1.7 * U * (age + 1)) * ref)
+
+
+def test_long_trajectories_captured_and_two_at_once():
+    """Blocks of two calls wait for their own call's blocks only."""
+    c = [Case(LONG["forks"], 264, "bf16", "mix", True, seed=s) for s in (1, 2)]
+    plan = c[0].plan
+    want = [x.forward() for x in c]
+    back = [x.backward(h) for x, (h, _) in zip(c, want)]
+    ws = [torch.empty(plan_bytes(plan, 264), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, got = [], []
+    for x, w, st in zip(c, ws, streams):
+        h, final = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+        dx, dg, dh0 = torch.empty_like(h), torch.empty_like(h), torch.empty_like(x.h0)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            scan_fwd(plan, x.x, x.g, form="mix", h0=x.h0, final_state=final, h=h, workspace=w)
+            scan_bwd(plan, x.x, x.g, h, x.dh, form="mix", h0=x.h0, d_final=x.dfinal, dx=dx, dg=dg, dh0=dh0, workspace=w)
+        graphs.append(graph)
+        got.append((h, final, dx, dg, dh0))
+    for _ in range(4):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert plan.device_error() == 0
+    for g, w, b in zip(got, want, back):
+        for a, e in zip(g, (*w, *b)):
+            assert torch.equal(a, e)
