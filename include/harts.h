@@ -687,7 +687,7 @@ typedef struct {
     const void *weight;      /* device [N][K] */
     const float *bias;       /* device [N] fp32, or NULL; not used by the backward */
     const void *residual;    /* device [C][N], or NULL; not used by the backward (its gradient is d_y) */
-    void *y;                 /* device [C][N] output; may be residual; not used by the backward */
+    void *y;                 /* device [C][N] output; y or z may be residual; not used by the backward */
     void *z;                 /* device [C][N]: output of the forward, or NULL; read by the backward where there
                                 is an activation */
     int32_t *error;          /* device [1]: set to 3 if a bounded wait ran out; cleared by the caller.

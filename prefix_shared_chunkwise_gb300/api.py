@@ -845,7 +845,7 @@ def linear_fwd(x, weight, bias=None, residual=None, *, activation="none", keep_z
     """harts_linear_fwd: y = act(x weight^T + bias) + residual, in one pass.  x [C, K], weight [N, K],
     residual [C, N] bf16, bias [N] fp32; K and N multiples of 8; activation "none", "silu" or "gelu" (by the
     normal distribution).  Returns (y [C, N] bf16, z): z is x weight^T + bias in bf16 with keep_z=True (what
-    linear_bwd wants where there is an activation), else None.  y may be given as residual.  error: as
+    linear_bwd wants where there is an activation), else None.  y or z may be given as residual.  error: as
     linear_logprob_fwd's."""
     import torch
     C, K, N = _linear_sizes(x, weight, activation, error)

@@ -547,10 +547,9 @@ __global__ void __launch_bounds__(256) linear_dot_kernel(const DotParams p) {
     const int32_t col = n0 + (lane & 1);
     const int64_t at = static_cast<int64_t>(lane >> 1) * p.N + col;
     if (p.ep.bias) mine += __ldg(p.ep.bias + col);
+    const float res = p.ep.res ? __bfloat162float(p.ep.res[at]) : 0.f;      // before z, which may be written over it
     if (p.z) p.z[at] = __float2bfloat16_rn(mine);
-    float y = act_of<ACT>(both(mine)).x;
-    if (p.ep.res) y += __bfloat162float(p.ep.res[at]);
-    p.y[at] = __float2bfloat16_rn(y);
+    p.y[at] = __float2bfloat16_rn(act_of<ACT>(both(mine)).x + res);
 }
 
 // ---- dz and the bias gradient -----------------------------------------------------------
