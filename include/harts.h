@@ -700,8 +700,8 @@ typedef struct {
  * may be NULL then), and for invalid arguments. */
 size_t harts_linear_fwd_workspace_bytes(int64_t C, int32_t K, int32_t N);
 
-/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, activation, y or z over x or one
- * another), HARTS_EUNSUPPORTED (dtype other than bf16, K or N not a multiple of 8), HARTS_EOVERFLOW (more
+/* Forward.  Errors: HARTS_EINVAL (NULL / misaligned pointers, sizes, activation, y or z over x, weight, bias
+ * or one another), HARTS_EUNSUPPORTED (dtype other than bf16, K or N not a multiple of 8), HARTS_EOVERFLOW (more
  * than 2^24 tiles), HARTS_ESMALLBUF (workspace), HARTS_ECUDA. */
 int harts_linear_fwd(const harts_linear_args *args, harts_stream_t stream);
 

@@ -817,7 +817,9 @@ int harts_linear_fwd(const harts_linear_args *a, harts_stream_t stream) {
     if (a->C == 0) { set_error(""); return HARTS_OK; }
     if (!a->y) { set_error("NULL y"); return HARTS_EINVAL; }
     if (a->y == a->z) { set_error("y and z are one buffer"); return HARTS_EINVAL; }
-    if (a->y == a->x || a->z == a->x) { set_error("y and z may not be x"); return HARTS_EINVAL; }
+    const void *const in_use[] = {a->x, a->weight, a->bias};
+    for (const void *q : in_use)
+        if (a->y == q || (a->z && a->z == q)) { set_error("y and z may not be x, weight or bias"); return HARTS_EINVAL; }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const Epilogue ep{a->bias, static_cast<const __nv_bfloat16 *>(a->residual)};
     const int32_t C = static_cast<int32_t>(a->C);
