@@ -98,8 +98,9 @@ template <> struct Lane<float> {
 };
 
 // e^g for g <= 0, as one number that gives both a and 1 - a with few roundings.  2^y = 2^n 2^f with
-// |f| <= 1/2 and the series of e^(f ln 2) to its seventh power (the next term is 5e-9); below
-// 2^-126.5, zero.  Memories of a thousand rows multiply a thousand decays: an approximate
+// |f| <= 1/2, y = g log2 e with the factor in two terms (one alone is 2e-8 off, which g = -88 makes 20 u of
+// a, u = 2^-24), and the series of e^(f ln 2) to its seventh power (the next term is 5e-9); below
+// 2^-126.5, zero.  a is within 1.9 u of itself, 1 - a within 2.6 u.  Memories of a thousand rows multiply a thousand decays: an approximate
 // exponential's 2^-22 would be 2e-4 of the state.  kExact keeps a.  kRest keeps 1 - a, which the
 // rounding of an a near 1 would take most digits of: 2^n (1 + t) with t the series gives it as
 // (1 - 2^n) - 2^n t, rounded once; a is then 1 - (1 - a), off by 2^-25 at most.  kBoth, for the mix
@@ -121,7 +122,7 @@ template <int KIND, typename T> __device__ __forceinline__ typename Lane<T>::V d
     });
     const auto z = fma(g, L::all(1.4426950408889634f), L::all(12582912.f));        // its low bits are n
     const auto n = fma(z, L::all(-1.f), L::all(12582912.f));                       // -n
-    const auto f = fma(g, L::all(1.4426950408889634f), n);
+    const auto f = fma(g, L::all(1.9259629911e-8f), fma(g, L::all(1.4426950408889634f), n));
     constexpr float sign = KIND == kExact ? 1.f : -1.f;
     auto q = L::all(sign * 1.5252733804e-5f);
     q = fma(q, f, L::all(sign * 1.5403530394e-4f));

@@ -1,0 +1,51 @@
+"""harts_scan_fwd / _bwd at the ends of their ranges.  u = 2^-24."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from prefix_shared_chunkwise_gb300.api import Plan, scan_bwd, scan_fwd
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from prefix_shared_chunkwise_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_decays_from_the_smallest_to_the_largest(rows):
+    """What a decay and its complement are themselves: h = a (x = 0, h0 = 1), h = 1 - a (x = 1, h0 = 0), dx = (1 - a)
+    dh and dg = a dh (h0 = 1, x = 0), in roots of one row (a decoding step's kernel) and of two (the tiles').
+    f = g log2 e - n has two roundings of at most 2^-26, 0.35 u of a in all; t = 2^f - 1 is off by f's share
+    and five half steps of the last terms of its series, less than 3 u of |t| <= 0.42; a = scale (1 + t) rounds once more: 0.35 +
+    1.3 + 0.5 < 2.5 u.  1 - a is t itself near a = 1: 3.5 u with f's two roundings relative to f.  The mix form's forward
+    has a from 1 - a, 2^-25 + 3.5 u of 1 - a off; results below fp32's normal range count as 2^-126."""
+    B, D = 64, 512
+    g = -torch.logspace(-7, np.log10(87.0), B * D, dtype=torch.float64).float().view(B, 1, D)
+    g = torch.cat([g, torch.full((B, rows - 1, D), -1.0)], dim=1).reshape(B * rows, D).cuda()
+    plan = Plan([-1] * B, [rows] * B, 64).upload()
+    first = torch.arange(B, device="cuda") * rows
+    g64 = g[first].double().cpu().numpy()
+    a, rest = np.exp(g64), -np.expm1(g64)
+    one, zero, h0 = torch.ones_like(g), torch.zeros_like(g), torch.ones(B, D, device="cuda")
+    got = lambda t: t[first].double().cpu().numpy()
+    tiny = 2.0 ** -126
+    h = scan_fwd(plan, zero, g, h0=h0)
+    assert np.all(np.abs(got(h) - a) <= 2.5 * U * a + tiny)
+    assert np.all(np.abs(got(scan_fwd(plan, one, g, form="mix")) - rest) <= 3.5 * U * rest)
+    assert np.all(np.abs(got(scan_fwd(plan, zero, g, form="mix", h0=h0)) - a) <= 2.0 ** -25 + 3.5 * U * rest + U * a)
+    dh = torch.zeros_like(g)
+    dh[first] = 1.0
+    for form in ("add", "mix"):
+        dx, dg = scan_bwd(plan, zero, g, h, dh, form=form, h0=h0)
+        assert np.all(np.abs(got(dx) - (rest if form == "mix" else 1.0)) <= (3.5 * U * rest if form == "mix" else 0.0))
+        assert np.all(np.abs(got(dg) - a) <= 2.5 * U * a + U * a + tiny)
+    torch.cuda.synchronize()
+    assert plan.device_error() == 0
