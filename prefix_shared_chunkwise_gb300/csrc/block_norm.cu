@@ -174,13 +174,14 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 // sigmoid(z) and sigmoid(-z).  For bf16 streams, where instructions are what the kernels are short
-// of, by e^-z, which ends at 2^126: a gate below e^-87 counts as e^-87.  For fp32 by e^-|z|, which
-// neither overflows nor is lost in a 1.
+// of, by e^-z, which ends at 2^127: the reciprocal of that is below fp32's normal range, zero, so that
+// gates below -87.3 count as none at all (the other factor, of no use beside a zero, is zero there too).  For
+// fp32 by e^-|z|, which neither overflows nor is lost in a 1.
 template <typename T, typename E> __device__ __forceinline__ E sigmoid(E z, E &other) {
     if constexpr (sizeof(T) == 2) {
         const E e = each(z, [](float v) {
             float a;
-            asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(v * -1.44269504f), "f"(126.f));
+            asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(v * -1.44269504f), "f"(127.f));
             return ex2(a);
         });
         const E q = each(e, [](float v) { return rcp(1.f + v); });
