@@ -173,11 +173,9 @@ int harts_plan_upload(harts_plan *P, void *dev_buf, size_t bytes, harts_stream_t
     v.attn_mask = w + I.off_attn_mask; v.attn_hp = w + I.off_attn_hp; v.attn_qt = w + I.off_attn_qt;
     v.attn_kt = w + I.off_attn_kt; v.attn_kptr = w + I.off_attn_kptr; v.attn_kq = w + I.off_attn_kq;
     v.n_qt = I.n_qt; v.n_kt = I.n_kt;
-    for (int k = 0; k < kScanCuts; ++k) {
-        v.scan_fwd[k] = reinterpret_cast<const ScanTile *>(w + I.off_scan_fwd[k]);
-        v.scan_bwd[k] = reinterpret_cast<const ScanTile *>(w + I.off_scan_bwd[k]);
-        v.scan_next[k] = w + I.off_scan_next[k];
-    }
+    v.scan_fwd = reinterpret_cast<const ScanTile *>(w + I.off_scan_fwd);
+    v.scan_bwd = reinterpret_cast<const ScanTile *>(w + I.off_scan_bwd);
+    v.scan_next = w + I.off_scan_next;
     v.n_rounds = P->info.n_rounds; v.n_seq = P->info.n_seq; v.n_states = P->info.n_states;
     v.n_roots = P->info.n_roots; v.n_fold = P->info.n_fold_rows; v.chunk = P->info.chunk;
     v.R = P->info.R; v.n_chunks = P->info.n_chunks; v.C = P->info.C; v.flags = P->info.flags;

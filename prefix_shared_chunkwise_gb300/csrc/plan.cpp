@@ -526,73 +526,75 @@ void build_image(harts_plan &P) {
     put(I.off_attn_kq, kq.data(), kq.size());
 
     // ---- gated scan -------------------------------------------------------------------
-    // Tiles of kScanRows rows of one segment, so that a fork always lies at a tile's end, in
-    // groups of `group` tiles.  Forward by the number of groups before a tile, backward by the most
-    // groups behind it: what a tile waits for (in its group: the tiles on the way to it) comes
-    // before it in either order.
-    std::vector<int64_t> behind(n, 0);                  // rows from the root to a segment's end
+    // Tiles of kScanRows rows of one segment, so that a fork always lies at a tile's end.  Forward by the number
+    // of groups of kScanLeast tiles before a tile, backward by the most groups behind it, then by its place in the
+    // group (from the end, backward), then by index: what a tile waits for (in its group: the tiles on the way to
+    // it) comes before it in either order, and so it does in larger groups, whose tiles wait for tiles of
+    // the same trajectory.  Of groups that may run side by side, the first tiles of all come before the second
+    // ones: by then what the tiles of a group publish for the next is long there.  Both orders are found by counting.
+    constexpr int32_t kLeast = kScanLeast;
+    std::vector<int32_t> first_tile(n + 1, 0), slot(n + 1, 0), before(n, 0), behind(n, 0);   // groups before and behind a segment
     bool alone = true;
+    int32_t deepest = 0, highest = 0;
+    I.scan_longest = 0;
     for (int32_t v = 0; v < n; ++v) {
-        alone = alone && P.parent[v] < 0 && P.seg_len[v] <= kScanRows;
-        behind[v] = P.seg_len[v] + (P.parent[v] < 0 ? 0 : behind[P.parent[v]]);
+        const int32_t u = P.parent[v], count = static_cast<int32_t>((P.seg_len[v] + kScanRows - 1) / kScanRows), groups = (count + kLeast - 1) / kLeast;
+        first_tile[v + 1] = first_tile[v] + count;
+        slot[v + 1] = slot[v] + groups;
+        if (u >= 0) before[v] = before[u] + slot[u + 1] - slot[u];
+        deepest = std::max(deepest, before[v] + groups);
+        alone = alone && u < 0 && count == 1;
+        I.scan_longest = std::max(I.scan_longest, P.seg_pos[v] + P.seg_len[v]);
+    }
+    for (int32_t v = n; v-- > 0;) {
+        const int32_t u = P.parent[v], height = behind[v] + slot[v + 1] - slot[v];
+        highest = std::max(highest, height);
+        if (u >= 0) behind[u] = std::max(behind[u], height);
     }
     I.scan_alone = alone;
-    I.scan_longest = *std::max_element(behind.begin(), behind.end());
-    for (int cut = 0; cut < kScanCuts; ++cut) {
-        const int group = kScanGroups[cut];
-        std::vector<ScanTile> tiles;
-        std::vector<int32_t> gfirst(n + 1, 0), depth, height, snext;
-        for (int32_t v = 0; v < n; ++v)
-            gfirst[v + 1] = gfirst[v] + static_cast<int32_t>((P.seg_len[v] + kScanRows * group - 1) / (kScanRows * group));
-        const int32_t n_groups = gfirst[n];
-        depth.assign(n_groups, 0);
-        height.assign(n_groups, 0);
-        for (int32_t v = 0, root_no = 0; v < n; ++v) {
-            const int32_t u = P.parent[v], root_id = u < 0 ? root_no++ : 0;
-            const int64_t count = (P.seg_len[v] + kScanRows - 1) / kScanRows;
-            for (int64_t t = 0; t < count; ++t) {
-                ScanTile s{};
-                s.tile = static_cast<int32_t>(tiles.size());
-                s.row0 = static_cast<int32_t>(P.seg_offset[v] + t * kScanRows);
-                s.rows = static_cast<int32_t>(std::min<int64_t>(kScanRows, P.seg_len[v] - t * kScanRows));
-                s.at = static_cast<int32_t>(t % group);
-                s.group = gfirst[v] + static_cast<int32_t>(t / group);
-                s.count = static_cast<int32_t>(std::min<int64_t>(group, count - (t - s.at)));
-                const int32_t outer = u < 0 ? -1 - root_id : 0;
-                s.pred = t >= group ? s.group - 1 : u < 0 ? outer : gfirst[u + 1] - 1;
-                s.pred_row = t > 0 ? s.row0 - 1 : u < 0 ? outer : static_cast<int32_t>(P.seg_offset[u] + P.seg_len[u] - 1);
-                const bool last = s.group == gfirst[v + 1] - 1;
-                s.seq_end = last && P.seg_ctop[v] < 0 ? P.seg_seq[v] : -1;
-                s.next_begin = static_cast<int32_t>(snext.size());
-                s.next_count = last ? kptr[v + 1] - kptr[v] : 1;
-                if (s.pred >= 0) depth[s.group] = depth[s.pred] + 1;
-                if (s.at == s.count - 1) {
-                    if (last) for (int32_t j = kptr[v]; j < kptr[v + 1]; ++j) snext.push_back(gfirst[kids[j]]);
-                    else snext.push_back(s.group + 1);
-                }
-                tiles.push_back(s);
+    I.n_scan = first_tile[n];
+    I.n_scan_slots = slot[n];
+    std::vector<int32_t> at_fwd(static_cast<size_t>(deepest) * kLeast + 1, 0), at_bwd(static_cast<size_t>(highest) * kLeast + 1, 0);
+    auto each_tile = [&](auto &&f) {                    // tile, place, segment, its key in either order
+        for (int32_t v = 0; v < n; ++v) {
+            const int32_t count = first_tile[v + 1] - first_tile[v], groups = slot[v + 1] - slot[v];
+            for (int32_t t = 0; t < count; ++t) {
+                const int32_t g = t / kLeast, end = std::min(count, (g + 1) * kLeast);
+                f(first_tile[v] + t, t, v, static_cast<int64_t>(before[v] + g) * kLeast + t % kLeast,
+                  static_cast<int64_t>(behind[v] + groups - 1 - g) * kLeast + end - 1 - t);
             }
         }
-        for (size_t t = tiles.size(); t-- > 0;)         // a group comes after its predecessor here too
-            if (tiles[t].pred >= 0) height[tiles[t].pred] = std::max(height[tiles[t].pred], height[tiles[t].group] + 1);
-        constexpr size_t kWords = sizeof(ScanTile) / sizeof(int32_t);
-        I.n_scan = static_cast<int32_t>(tiles.size());
-        I.n_scan_groups[cut] = n_groups;
-        put(I.off_scan_next[cut], snext.data(), snext.size());
-        // Of groups that may run side by side, the first tiles of all come before the second ones: by
-        // then what the tiles of a group publish for the next is long there.
-        std::sort(tiles.begin(), tiles.end(), [&](const ScanTile &a, const ScanTile &b) {
-            if (depth[a.group] != depth[b.group]) return depth[a.group] < depth[b.group];
-            return a.at != b.at ? a.at < b.at : a.tile < b.tile;
-        });
-        put(I.off_scan_fwd[cut], reinterpret_cast<const int32_t *>(tiles.data()), tiles.size() * kWords);
-        std::sort(tiles.begin(), tiles.end(), [&](const ScanTile &a, const ScanTile &b) {
-            if (height[a.group] != height[b.group]) return height[a.group] < height[b.group];
-            const int32_t u = a.count - a.at, v = b.count - b.at;
-            return u != v ? u < v : a.tile < b.tile;
-        });
-        put(I.off_scan_bwd[cut], reinterpret_cast<const int32_t *>(tiles.data()), tiles.size() * kWords);
-    }
+    };
+    each_tile([&](int32_t, int32_t, int32_t, int64_t f, int64_t b) { ++at_fwd[f + 1]; ++at_bwd[b + 1]; });
+    for (size_t i = 1; i < at_fwd.size(); ++i) at_fwd[i] += at_fwd[i - 1];
+    for (size_t i = 1; i < at_bwd.size(); ++i) at_bwd[i] += at_bwd[i - 1];
+    constexpr size_t kWords = sizeof(ScanTile) / sizeof(int32_t);
+    std::vector<int32_t> next(kids.size()), root_no(n, 0);
+    for (size_t j = 0; j < kids.size(); ++j) next[j] = slot[kids[j]];
+    for (int32_t v = 0, r = 0; v < n; ++v) if (P.parent[v] < 0) root_no[v] = r++;
+    put(I.off_scan_next, next.data(), next.size());
+    put(I.off_scan_fwd, nullptr, 0);
+    w.resize(w.size() + kWords * I.n_scan);
+    put(I.off_scan_bwd, nullptr, 0);
+    w.resize(w.size() + kWords * I.n_scan);
+    each_tile([&](int32_t tile, int32_t t, int32_t v, int64_t f, int64_t b) {
+        const int32_t u = P.parent[v], outer = -1 - root_no[v];
+        ScanTile s;
+        s.tile = tile;
+        s.row0 = static_cast<int32_t>(P.seg_offset[v]) + t * kScanRows;
+        s.rows = static_cast<int32_t>(std::min<int64_t>(kScanRows, P.seg_len[v] - int64_t(t) * kScanRows));
+        s.at = t;
+        s.count = first_tile[v + 1] - first_tile[v];
+        s.slot = slot[v];
+        s.pred_count = u < 0 ? 0 : first_tile[u + 1] - first_tile[u];
+        s.pred_slot = u < 0 ? outer : slot[u];
+        s.pred_row = t > 0 ? s.row0 - 1 : u < 0 ? outer : static_cast<int32_t>(P.seg_offset[u] + P.seg_len[u] - 1);
+        s.seq_end = P.seg_ctop[v] < 0 ? P.seg_seq[v] : -1;
+        s.next_begin = kptr[v];
+        s.next_count = kptr[v + 1] - kptr[v];
+        std::memcpy(&w[I.off_scan_fwd + kWords * at_fwd[f]++], &s, sizeof(s));
+        std::memcpy(&w[I.off_scan_bwd + kWords * at_bwd[b]++], &s, sizeof(s));
+    });
     while (w.size() % 64) w.push_back(0);
 }
 

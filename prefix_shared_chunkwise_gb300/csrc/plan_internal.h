@@ -12,21 +12,48 @@ namespace harts {
 constexpr int kConvMaxW = 8;       // widest short convolution the plan tables serve
 constexpr int kAttnTile = 128;     // query / key rows per branch-attention tile
 constexpr int kScanRows = 128;     // rows per tile of the gated scan
-// Most tiles of one segment whose carries are joined side by side, in a plan's three cuts: few where
-// the tiles of many channels take turns (a tile looks at those before it in its group), many where a
-// chain of carries is all there is, or where a tile's own work is long (backward).
-constexpr int kScanCuts = 3, kScanGroups[kScanCuts] = {8, 16, 32};
+// Most tiles of one segment whose carries are joined side by side: few where the tiles of many channels
+// take turns (a tile looks at those before it in its group), many where a chain of carries is all there
+// is, or where a tile's own work is long (backward).
+constexpr int kScanGroups[] = {8, 16, 32}, kScanLeast = 8;
 constexpr int64_t kAttnMaxRows = int64_t(1) << 27;   // largest ancestor-row table built
 
-// A tile of the gated scan: up to kScanRows rows of one segment.  Up to kScanGroups[k] consecutive
-// tiles of a segment form a group; a group's predecessor is the one before it in its segment, or
-// the last one of the parent segment.
+// A tile of the gated scan: up to kScanRows rows of one segment.  The tables know no groups: a segment has a
+// slot for a state behind each of its kScanLeast tiles, and larger groups, multiples of that, use the first
+// slot that lies in them.
 struct ScanTile {
-    int32_t tile, row0, rows, at;             // index, first row, rows, place in its group
-    int32_t group, count, pred, pred_row;     // tiles of the group; predecessor group and the row before row0, or -1 - root
-    int32_t seq_end, next_begin, next_count;  // sequence that ends with the group (or -1); groups that follow it
-    int32_t pad;
+    int32_t tile, row0, rows, at;             // index, first row, rows, place in its segment
+    int32_t count, slot;                      // tiles and first slot of the segment
+    int32_t pred_count, pred_slot;            // of the parent; pred_slot is -1 - root where there is none
+    int32_t pred_row, seq_end;                // row before row0, or -1 - root; sequence that ends with the segment, or -1
+    int32_t next_begin, next_count;           // first slots of the segments that follow: scan_next[next_begin ..]
 };
+
+// The same among groups of `group` tiles: the group's predecessor is the one before it in its segment, or
+// the last one of the parent segment.
+struct ScanPlace {
+    int32_t tile, row0, rows, at;             // at: place in its group
+    int32_t slot, count, pred, pred_row;      // the group's slot and tiles; predecessor's slot, or -1 - root
+    int32_t seq_end, next_begin, next_count;  // next_begin < 0: the one group that follows has slot -1 - next_begin
+};
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline ScanPlace scan_place(const ScanTile &t, int32_t group) {      // group: a power of two
+    ScanPlace p;
+    p.tile = t.tile; p.row0 = t.row0; p.rows = t.rows; p.pred_row = t.pred_row;
+    p.at = t.at & (group - 1);
+    const int32_t first = t.at - p.at, left = t.count - first;
+    p.slot = t.slot + first / kScanLeast;
+    p.count = left < group ? left : group;
+    p.pred = first > 0 ? p.slot - group / kScanLeast
+                       : t.pred_slot < 0 ? t.pred_slot : t.pred_slot + ((t.pred_count - 1) & -group) / kScanLeast;
+    const bool last = left <= group;
+    p.seq_end = last ? t.seq_end : -1;
+    p.next_begin = last ? t.next_begin : -1 - (p.slot + group / kScanLeast);
+    p.next_count = last ? t.next_count : 1;
+    return p;
+}
 
 struct PlanDev {
     int32_t *err;                // [4] device error word: code, info, info, info
@@ -68,8 +95,8 @@ struct PlanDev {
     const int32_t *attn_kq;        // (sequence, query tile, f): f own rows of the key's sequence visible, -1 causal
     int32_t n_qt, n_kt;
     // gated scan: one record per tile, predecessors first (forward) and successors first (backward)
-    const struct ScanTile *scan_fwd[kScanCuts], *scan_bwd[kScanCuts];   // [n_scan], by kScanGroups
-    const int32_t *scan_next[kScanCuts];   // groups that follow a segment's last group: ScanTile::next_begin ..
+    const struct ScanTile *scan_fwd, *scan_bwd;   // [n_scan]
+    const int32_t *scan_next;              // ScanTile::next_begin ..
     int32_t n_rounds, n_seq, n_states, n_roots, n_fold, chunk, n_seg;
     uint32_t flags;                // harts_plan_calls flags (HARTS_PLAN_NOREPLAY: slots inside chunks)
     int64_t R, n_chunks, C;
@@ -84,8 +111,8 @@ struct PlanImage {
         off_fold_rows, off_fold_ptr, off_fold_occ, off_chunk_seq, off_row_seg, off_seg_row0,
         off_seg_len, off_conv_ctx, off_conv_sptr, off_conv_succ, off_attn_rptr, off_attn_runs,
         off_attn_mptr, off_attn_mask, off_attn_hp, off_attn_qt, off_attn_kt, off_attn_kptr, off_attn_kq,
-        off_scan_fwd[kScanCuts], off_scan_bwd[kScanCuts], off_scan_next[kScanCuts];
-    int32_t n_qt, n_kt, n_scan, n_scan_groups[kScanCuts], scan_alone;   // scan_alone: no tile follows another one
+        off_scan_fwd, off_scan_bwd, off_scan_next;
+    int32_t n_qt, n_kt, n_scan, n_scan_slots, scan_alone;   // scan_alone: no tile follows another one
     int64_t scan_longest;          // rows of the longest trajectory
 };
 

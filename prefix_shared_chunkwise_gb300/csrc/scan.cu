@@ -59,10 +59,10 @@ struct ScanParams {
     void *out0, *out1;              // forward h; backward dx, dg
     float *final_state, *dh0;
     uint32_t *ticket;               // nullptr: tiles that wait for nothing are dealt out in turn
-    float *inc;                     // [groups][width] state behind a group (backward: before it)
+    float *inc;                     // [slots][width] state behind a group (backward: before it)
     float2 *agg;                    // [tiles][width] a tile's map
     int32_t *error;
-    int32_t D, width, cols;         // channels, rounded up to tiles', tiles across
+    int32_t D, width, cols, group;  // channels, rounded up to tiles', tiles across; most tiles of a group
     uint32_t total;
 };
 
@@ -212,7 +212,7 @@ template <bool BWD, bool AHEAD> struct Ring {
     static constexpr uint32_t smem = stages * stage_bytes + 128;
 };
 
-struct Meta { ScanTile t; int32_t col; };                      // rows 0: the end
+struct Meta { ScanPlace t; int32_t col; };                      // rows 0: the end
 
 template <typename T, bool BWD, bool MIX, int KIND, bool AHEAD>
 __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kernel(const __grid_constant__ ScanParams p) {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
             const int s = it % R::stages;
             Meta m{};
             if (idx < p.total) {
-                m.t = p.tiles[idx / p.cols];
+                m.t = scan_place(p.tiles[idx / p.cols], p.group);
                 m.col = static_cast<int32_t>(idx % p.cols) * kWide;
                 if (p.ticket) drawn = draw();
             }
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
                 V state = L::all(0.f);
                 bool there = false;
                 if (left > 0) {
-                    const int64_t g = BWD ? p.next[m.t.next_begin + m.t.next_count - left] : m.t.pred;
+                    const int64_t g = !BWD ? m.t.pred : m.t.next_begin < 0 ? -1 - m.t.next_begin : p.next[m.t.next_begin + m.t.next_count - left];
                     if constexpr (CH == 2) state = look(reinterpret_cast<const float2 *>(p.inc + g * p.width + ch));
                     else state = look(p.inc + g * p.width + ch);
                 }
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BWD, AHEAD>::blocks) scan_kerne
             if (!mapped || !carried) break;
             v = fma(A, v, B);
             if (BWD ? m.t.at == 0 && m.t.pred >= 0 : m.t.at == m.t.count - 1 && m.t.next_count > 0)
-                publish(p.inc + static_cast<int64_t>(m.t.group) * p.width + ch, v);
+                publish(p.inc + static_cast<int64_t>(m.t.slot) * p.width + ch, v);
             else if (BWD && m.t.at == 0 && p.dh0 && inside)
                 L::store(p.dh0 + static_cast<int64_t>(-1 - m.t.pred) * p.D + ch, v);
             __syncwarp();
@@ -536,7 +536,7 @@ Space space_of(const harts_plan *P, int32_t D, int32_t dtype) {
     Space s{};
     if (P->image.scan_alone) return s;
     s.inc = 256;
-    s.agg = s.inc + align256(4 * width * P->image.n_scan_groups[0]);      // the cut with most groups
+    s.agg = s.inc + align256(4 * width * P->image.n_scan_slots);
     s.total = s.agg + align256(8 * width * P->image.n_scan);
     return s;
 }
@@ -628,9 +628,9 @@ ScanParams params_of(const harts_plan *P, const harts_scan_fwd_args *a, bool bac
     const Space s = space_of(P, a->channels, a->dtype);
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.cols = ceil_div(a->channels, wide_of(a->dtype));
-    const int cut = backward || p.cols <= 2 ? 2 : p.cols <= 8;
-    p.tiles = backward ? P->view.scan_bwd[cut] : P->view.scan_fwd[cut];
-    p.next = P->view.scan_next[cut];
+    p.group = kScanGroups[backward || p.cols <= 2 ? 2 : p.cols <= 8];
+    p.tiles = backward ? P->view.scan_bwd : P->view.scan_fwd;
+    p.next = P->view.scan_next;
     p.h0 = a->h0;
     if (!P->image.scan_alone) {
         p.ticket = reinterpret_cast<uint32_t *>(ws);
