@@ -32,6 +32,7 @@
 #include "launch_util.h"
 #include "tc_primitives.cuh"
 #include "tensor_map.h"
+#include "tile_order.h"
 #include "tile_pairs.cuh"
 #include "two.cuh"
 
@@ -45,7 +46,6 @@ constexpr int kTM = 128, kTK = 64, kTN = 256;       // a block's tile rows, K st
 constexpr uint32_t kABytes = kTM * kTK * 2;
 constexpr uint32_t kSlots = 4, kSlotBytes = kTM * 64;           // 128 rows x 64 bytes of output on their way out
 constexpr int kThreads = 448, kEpiWarp0 = 4, kStoreWarp0 = 12;  // eight epilogue warps: two for each 32 TMEM lanes
-constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr int kDotRows = 2;                         // most rows that are done by dot products
 
 // As many stages as fit beside small slots: copies are some 2,500 cycles on their way while results go out, five steps
@@ -90,49 +90,6 @@ struct Params {
     Epilogue ep;
     int32_t keep;                   // z goes out too
 };
-
-struct TileId { int which, mt, nt, split; };
-
-// The n-th tile of worker `w` of `workers` (blocks or pairs): those of the first product go round,
-// then the second's, the workers that got one tile less of the first taking `extra` of them before the others
-// join in.
-__device__ __forceinline__ bool tile_at(const Params &p, uint32_t n, uint32_t w, uint32_t workers, TileId &t) {
-    uint32_t idx = w + n * workers;
-    t.which = 0;
-    if (idx >= p.prod[0].items) {
-        if (p.n_prod < 2) return false;
-        t.which = 1;
-        const uint32_t few = workers - p.over;
-        uint32_t m = n - p.each0 - (w < p.over ? 1 : 0);
-        if (p.over == 0) {
-            idx = w + m * workers;
-        } else if (w >= p.over && m < p.extra) {
-            idx = (w - p.over) + m * few;
-        } else {
-            if (w >= p.over) m -= p.extra;
-            idx = few * p.extra + w + m * workers;
-        }
-        if (idx >= p.prod[1].items) return false;
-    }
-    const Prod &q = p.prod[t.which];
-    t.split = 0;
-    if (q.splits > 1) {
-        t.split = static_cast<int>(idx / q.per_split);
-        idx -= t.split * q.per_split;
-    }
-    const uint32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
-    uint32_t base = 0, len = fast;
-    if (fast > kGroup) {
-        const uint32_t g = idx / (kGroup * slow);
-        idx -= g * kGroup * slow;
-        base = g * kGroup;
-        len = min(static_cast<uint32_t>(kGroup), fast - base);
-    }
-    const uint32_t s = idx / len, f = base + idx - s * len;
-    t.mt = q.fast_n ? s : f;
-    t.nt = q.fast_n ? f : s;
-    return true;
-}
 
 // ---- activations ------------------------------------------------------------------------
 
@@ -714,22 +671,7 @@ cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(linear_tile_kernel<ACT, G>, Ring<G>::smem, done);
     if (e != cudaSuccess) return e;
-    int64_t items = 0;
-    for (int i = 0; i < p.n_prod; ++i) {
-        Prod &q = p.prod[i];
-        q.per_split = static_cast<uint32_t>(q.m_tiles) * q.n_tiles;
-        q.items = q.per_split * q.splits;
-        items += q.items;
-    }
-    const uint32_t workers = static_cast<uint32_t>(std::min<int64_t>(items, sm_count() / G));
-    p.each0 = p.prod[0].items / workers;
-    p.over = p.prod[0].items % workers;
-    p.extra = 0;
-    if (p.n_prod == 2 && p.over) {
-        // a tile costs its K steps and about three more for its ends
-        const uint32_t a = p.prod[0].k_per + 3, b = p.prod[1].k_per + 3;
-        p.extra = std::min((a + b / 2) / b, p.prod[1].items / (workers - p.over));
-    }
+    const uint32_t workers = share_tiles(p, sm_count() / G);
     return launch(linear_tile_kernel<ACT, G>, int64_t(workers) * G, kThreads, Ring<G>::smem, G, behind, st, p);
 }
 template <int ACT> cudaError_t launch_tiles(Params &p, int G, bool behind, cudaStream_t st) {

@@ -36,6 +36,7 @@
 #include "launch_util.h"
 #include "tc_primitives.cuh"
 #include "tensor_map.h"
+#include "tile_order.h"
 #include "tile_pairs.cuh"
 
 namespace harts {
@@ -49,7 +50,6 @@ constexpr uint32_t kABytes = kTM * kTK * 2;
 constexpr uint32_t kSlotBytes = kTM * 128;           // 128 rows x 128 bytes of the output on their way out
 
 constexpr int kThreads = 448, kEpiWarp0 = 4, kStoreWarp0 = 12;    // eight epilogue warps: two for each 32 TMEM lanes
-constexpr int kGroup = 16;                          // tiles along the fast side that run together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kFwd = 0, kDz = 1, kGrad = 2 };
@@ -102,51 +102,6 @@ struct Params {
     int32_t v0;                     // dz: first vocabulary entry of the piece
     int32_t twin;                   // dz: rows 32 .. 63 hold what rounding takes from rows 0 .. 31
 };
-
-struct TileId { int which, mt, nt, split; };
-
-// The n-th tile of worker `w` of `workers` (blocks or pairs).  Tiles of the first product go
-// round the workers; those of the second follow, the workers that got one tile less of the
-// first taking `extra` of them before the others join in.  32-bit arithmetic: the threads that
-// feed the tensor cores come through here between two tiles.
-__device__ __forceinline__ bool tile_at(const Params &p, uint32_t n, uint32_t w, uint32_t workers, TileId &t) {
-    uint32_t idx = w + n * workers;
-    t.which = 0;
-    if (idx >= p.prod[0].items) {
-        if (p.n_prod < 2) return false;
-        t.which = 1;
-        const uint32_t few = workers - p.over;                       // workers with a tile less, if any
-        uint32_t m = n - p.each0 - (w < p.over ? 1 : 0);
-        if (p.over == 0) {
-            idx = w + m * workers;
-        } else if (w >= p.over && m < p.extra) {
-            idx = (w - p.over) + m * few;
-        } else {
-            if (w >= p.over) m -= p.extra;
-            idx = few * p.extra + w + m * workers;
-        }
-        if (idx >= p.prod[1].items) return false;
-    }
-    const Prod &q = p.prod[t.which];
-    t.split = 0;
-    if (q.splits > 1) {
-        t.split = static_cast<int>(idx / q.per_split);
-        idx -= t.split * q.per_split;
-    }
-    // groups of `group` tiles along the fast side run against every tile of the other
-    const uint32_t fast = q.fast_n ? q.n_tiles : q.m_tiles, slow = q.fast_n ? q.m_tiles : q.n_tiles;
-    uint32_t base = 0, len = fast;
-    if (fast > kGroup) {
-        const uint32_t g = idx / (kGroup * slow);
-        idx -= g * kGroup * slow;
-        base = g * kGroup;
-        len = min(static_cast<uint32_t>(kGroup), fast - base);
-    }
-    const uint32_t s = idx / len, f = base + idx - s * len;
-    t.mt = q.fast_n ? s : f;
-    t.nt = q.fast_n ? f : s;
-    return true;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -1064,22 +1019,7 @@ cudaError_t launch_group(Params &p, bool behind, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(head_tile_kernel<MODE, G>, Ring<MODE, G>::smem, done);
     if (e != cudaSuccess) return e;
-    int64_t items = 0;
-    for (int i = 0; i < p.n_prod; ++i) {
-        Prod &q = p.prod[i];
-        q.per_split = static_cast<uint32_t>(q.m_tiles) * q.n_tiles;
-        q.items = q.per_split * q.splits;
-        items += q.items;
-    }
-    const uint32_t workers = static_cast<uint32_t>(std::min<int64_t>(items, sm_count() / G));
-    p.each0 = p.prod[0].items / workers;
-    p.over = p.prod[0].items % workers;
-    p.extra = 0;
-    if (p.n_prod == 2 && p.over) {
-        // a tile costs its K steps and about three more for its ends
-        const uint32_t a = p.prod[0].k_per + 3, b = p.prod[1].k_per + 3;
-        p.extra = std::min((a + b / 2) / b, p.prod[1].items / (workers - p.over));
-    }
+    const uint32_t workers = share_tiles(p, sm_count() / G);
     return launch(head_tile_kernel<MODE, G>, int64_t(workers) * G, kThreads, Ring<MODE, G>::smem, G, behind, st, p);
 }
 template <int MODE>
