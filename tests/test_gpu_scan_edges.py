@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from prefix_shared_chunkwise_gb300.api import Plan, scan_bwd, scan_fwd
+from tests.test_gpu_scan import FORESTS, LONG, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,19 @@ def test_decays_from_the_smallest_to_the_largest(rows):
         assert np.all(np.abs(got(dg) - a) <= 2.5 * U * a + U * a + tiny)
     torch.cuda.synchronize()
     assert plan.device_error() == 0
+
+
+@pytest.mark.parametrize("form,state", [("add", False), ("mix", True), ("add", True)])
+@pytest.mark.parametrize("forest", ["groups", "group-ends", "trees", "forks"])
+def test_groups_of_eight_tiles(forest, form, state):
+    """More than 512 bf16 channels, whose forward joins eight tiles' maps at most, against the oracle."""
+    c = Case({**FORESTS, **LONG}[forest], 1000, "bf16", form, state, seed=2)
+    c.check_backward(c.check_forward())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("children", [64, 513])
+def test_many_branches_of_one_segment(children, dtype):
+    """The gradient behind a wide fork is a sum over all its branches, by ascending segment."""
+    c = Case(([-1] + [0] * children, [300] + [1 + (11 * i) % 40 for i in range(children)]), 72, dtype, "mix", True, seed=3)
+    c.check_backward(c.check_forward())
