@@ -66,3 +66,23 @@ def test_many_branches_of_one_segment(children, dtype):
     """The gradient behind a wide fork is a sum over all its branches, by ascending segment."""
     c = Case(([-1] + [0] * children, [300] + [1 + (11 * i) % 40 for i in range(children)]), 72, dtype, "mix", True, seed=3)
     c.check_backward(c.check_forward())
+
+
+@pytest.mark.parametrize("forest", ["steps", "trees"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_states_and_their_gradients_one_without_the_other(forest, dtype):
+    """No h0 is an h0 of zeros, no d_final a d_final of zeros, and what is not asked for changes nothing else."""
+    c = Case(FORESTS[forest], 72, dtype, "mix", True, seed=4)
+    c.h0.zero_()
+    c.dfinal.zero_()
+    h, final = c.forward()
+    assert torch.equal(scan_fwd(c.plan, c.x, c.g, form="mix"), h)
+    got = torch.full_like(final, 7.0)
+    scan_fwd(c.plan, c.x, c.g, form="mix", final_state=got)
+    assert torch.equal(got, final)
+    dx, dg, dh0 = c.backward(h)
+    for kw in ({}, {"h0": c.h0}, {"d_final": c.dfinal}):
+        got = torch.full_like(dh0, 7.0)
+        out = scan_bwd(c.plan, c.x, c.g, h, c.dh, form="mix", dh0=got, **kw)
+        assert torch.equal(out[0], dx) and torch.equal(out[1], dg) and torch.equal(got, dh0)
+        assert all(torch.equal(a, b) for a, b in zip(scan_bwd(c.plan, c.x, c.g, h, c.dh, form="mix", **kw), (dx, dg)))
