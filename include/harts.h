@@ -351,10 +351,14 @@ int harts_conv_bwd(const harts_plan *plan, const harts_conv_bwd_args *args, hart
  * (its segment's, or its parent's last one; the root's initial state at a trajectory's start):
  *   a = e^g,  h[r] = a h[before r] + x[r]            (HARTS_SCAN_ADD)
  *             h[r] = a h[before r] + (1 - a) x[r]    (HARTS_SCAN_MIX)
- * g is the natural-log decay, as KDA's: g <= 0, -inf starts afresh.  States, and what the long
- * products of decays are made of, are fp32.  All plan modes work; results do not depend on the
- * rounds, and their bits do not depend on timing.  A forest whose segments are roots of one row each is a
- * decoding step: h0 holds the states before, final_state those behind.
+ * g is the natural-log decay, as KDA's: g <= 0, -inf starts afresh.  A positive g is not looked for, and
+ * its results are not defined.  States, and what the long products of decays are made of, are fp32.
+ * All plan modes work; results do not depend on the rounds, and their bits do not depend on timing.
+ * Decays are within two half steps of fp32, but for one case: in bf16's add form, where no trajectory of the
+ * plan has more than 4,096 rows and no fp32 state (final_state, dh0) is asked for, they are the hardware's
+ * exponential, 2^-22 off.  There, asking for a state or adding a long tree to the forest can change the last bit of
+ * the other results.  A forest whose segments are roots of one row each is a decoding step: h0 holds the
+ * states before, final_state those behind.
  * What is not finite reaches the rows behind it on its trajectories (backward: before it), and no others.
  */
 #define HARTS_SCAN_ADD 0

@@ -681,7 +681,7 @@ def _scan_args(plan, x, g, h, h0, final_state, form, workspace):
 def scan_fwd(plan: Plan, x, g, *, form="add", h0=None, h=None, final_state=None, workspace=None, stream=None):
     """harts_scan_fwd: the gated recurrence h = e^g h_before + x ("add") or e^g h_before + (1 - e^g) x
     ("mix") per channel over the compact rows, each from the row before it on its trajectory.
-    x, g: [C, D] bf16 or fp32, D a multiple of 8, g <= 0.  h0: [n_roots, D] fp32 states before the roots, or None.
+    x, g: [C, D] bf16 or fp32, D a multiple of 8, g <= 0 (a positive g is not looked for).  h0: [n_roots, D] fp32 states before the roots, or None.
     final_state: [n_seq, D] fp32, receives the state after each sequence.  Returns h like x."""
     import torch
     if h is None:

@@ -13,8 +13,10 @@
 // value: HBM bounds both.  (As separate steps the norm, the gate, the addition and the next norm
 // would move twelve.)  A row belongs to R threads, which keep it in registers over both of its
 // sums.  Rows are copied ahead by cp.async.bulk into a ring in shared memory, whose bytes on their way
-// do not depend on registers; short rows share a warp.  Blocks are persistent: weights and the weights'
-// gradients of a thread's columns stay in its registers.  A block leaves one row of those gradients, a
+// do not depend on registers; short rows share a warp.  Blocks are persistent.  Forward, the weights of a thread's
+// columns stay in its registers.  Backward, their gradients do, beside weights in shared memory (in registers too
+// where rows are not whole vectors); above 4,096 channels the gradients are in shared memory and the weights are read
+// where they are, through L1.  A block leaves one row of those gradients, a
 // second kernel adds them in ascending order: no atomics, the same bits on every run.
 //
 // bf16, 65,536 rows of 2,048 channels with everything: forward 216 us (92 % of the copy's rate), backward 325 (97 %);
@@ -176,7 +178,8 @@ __device__ __forceinline__ float rcp(float x) {
 // sigmoid(z) and sigmoid(-z).  For bf16 streams, where instructions are what the kernels are short
 // of, by e^-z, which ends at 2^127: the reciprocal of that is below fp32's normal range, zero, so that
 // gates below -87.3 count as none at all (the other factor, of no use beside a zero, is zero there too).  For
-// fp32 by e^-|z|, which neither overflows nor is lost in a 1.
+// fp32 by e^-|z|, which neither overflows nor is lost in a 1; __expf leaves it off by some (2 + |z|) u of itself, less
+// than 2^-18 of a gate's value wherever that is not below 2^-60 (expf: heads of 128 141 us -> 148, gradients 224 -> 234).
 template <typename T, typename E> __device__ __forceinline__ E sigmoid(E z, E &other) {
     if constexpr (sizeof(T) == 2) {
         const E e = each(z, [](float v) {
@@ -739,9 +742,11 @@ __global__ void __launch_bounds__(1024) block_norm_dw_kernel(const Dw p) {
 }
 
 // Threads of a row and values that each of them keeps.  The backward's rows above 4,096 channels have 16 values
-// a thread, their sums in shared memory and the weights where they are, which is L1 beside one stage (bf16, 16,384 x
-// 8,192: 443 us; two stages, which leave L1 no room, 491; 1,024 threads with eight values, 64 registers each,
-// 655.  fp32, 8,192 x 8,192: 490, 473 and 480; 12,000 x 5,120 426, 436 and 470).
+// a thread, their sums in shared memory and the weights where they are.  Where shared memory holds them (launch_rows),
+// two stages are on their way: with everything up to 7,314 channels in bf16 and 4,266 in fp32, without a gate up to
+// 8,192 in bf16; wider rows have one, and more of L1 for the weights.  (bf16, 16,384 x 8,192 with everything: one stage 443
+// us, two by leaving L1 no room 491, 1,024 threads with eight values, 64 registers each, 655.  fp32, 8,192 x
+// 8,192, one stage: 471 - 497.  Two stages, bf16: 24,576 x 5,120 507, 20,000 x 6,144 459.)
 struct Shape { int vec, r, values; bool ragged; };
 Shape shape_of(int32_t dtype, int32_t D, bool backward) {
     const int full = dtype == HARTS_BF16 ? 8 : 4;

@@ -21,9 +21,12 @@
 // the same.
 //
 // bf16: 65,536 rows of 2,048 channels in 361 segments, add form: 141 us (84 % of the copy's rate), gradients 234 (84 %);
-// mix form's gradients 314 (76 %).  One trajectory of 131,071 rows, 1,024 channels, mix form with states: 180 us
-// (66 %), bound by the chain of its groups.  512 segments of 128 rows: 139 (85 %); 4,096 of 16: 558 (21 %), where a
-// tile's fixed time, 1.9 us a block, is all.  48 single rows: 1.4 us on the device.
+// mix form's gradients 314 (76 %).  fp32, 1,024 channels: 137 (86 %) and 226 (88 %).  One trajectory of 131,071 rows, 1,024
+// channels, mix form with states: 182 us (65 %), bound by the chain of its groups, each of which waits for the finished
+// state of the one before; gradients 421 (56 %).  512 segments of 128 rows: 140 (84 %); 4,096 of 16: 563 (21 %), where a
+// tile's fixed time, 1.9 us a block, is all.  48 single rows: 1.4 us on the device.  Gradients behind a wide fork are far
+// from either bound: the fork's last group adds its branches' states one after another, each fetched behind
+// the one before, in every tile of it (512 branches of 120 rows off 4,096: 1,150 us, forward 145).
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -109,7 +112,8 @@ template <> struct Lane<float> {
 // rounds to 2^-9, in the add form, where no trajectory has more than kFastRows rows: so many decays
 // are off by 2^-10 at most.  (A microbatch of 361 segments, 65,536 rows of 2,048 channels: 141 us, 168 with
 // the series.  Slow decays over 131,072 rows: off by up to 2^-7.3 with it, with the series by the 2^-8 of
-// the result's rounding.)
+// the result's rounding.)  So the bits of h are those of one kernel or the other, by what else is asked for and by the
+// longest trajectory of the forest.
 constexpr int64_t kFastRows = 4096;
 enum Kind { kFast, kExact, kRest, kBoth };
 template <int KIND, typename T> __device__ __forceinline__ typename Lane<T>::V decay(typename Lane<T>::V g) {
@@ -200,12 +204,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *f)
 // block's, and does nothing for tiles that need not wait: the forward takes it where the longest trajectory has
 // kAheadRows rows.  (bf16, mix form, groups of 16: one of 131,072 rows of 1,024 channels 192 us, 339 without; 4 of
 // 16,384 rows of 2,048 channels 170 and 202, 8 of 8,192 rows 168 and 177, 16 of 4,200 rows 172 and 169,
-// 16 chains of 40 segments of 200 rows 215 and 197.)
+// 16 chains of 40 segments of 200 rows 215 and 197; before the decay's argument had its second term.)
 constexpr int64_t kAheadRows = 8192;
 // Groups of 8 tiles are the forward's where more than eight tiles lie side by side; up to eight are too few to fill
 // the chip with small groups, and up to two leave the chain of carries as all there is.  (131,072 rows, bf16, mix, in
 // groups of 8 / 16 / 32: 1,024 channels 180 us / 192 / 221, 512 127 / 111 / 137, 256 110 / 76 / 79, 128 97 / 72 / 49, 64
-// 90 / 54 / 35.  Backward, 1,024 channels: 406 / 394 / 345.)
+// 90 / 54 / 35.  Backward, add form, 1,024 channels: 406 / 394 / 345, now 359 with the decay's second term.)
 template <bool BWD, bool AHEAD> struct Ring {
     static constexpr int tensors = BWD ? 3 : 2, stages = AHEAD ? 3 : 2, blocks = BWD || AHEAD ? 2 : 3;
     static constexpr uint32_t stage_bytes = tensors * kTileBytes;
